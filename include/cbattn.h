@@ -14,7 +14,8 @@
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Element type of q, k_new, v_new, caches and out is bf16 (IEEE bfloat16,
- *    passed as void*).  Accumulation is fp32.
+ *    passed as void*); the caches of the _fp8 calls are described with them.
+ *    Accumulation is fp32.
  *  - "device" pointers must point to memory of the current CUDA device; "host"
  *    pointers to ordinary (or pinned) host memory.
  *  - `stream` is a cudaStream_t (NULL = legacy default stream).  Every GPU entry
@@ -215,6 +216,73 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
                                         void* out, float scale, int n_q_heads, int n_kv_heads, int head_dim,
                                         int block_size, int window, void* workspace, size_t workspace_bytes,
                                         void* stream);
+
+/* ---------------------------------------------------------------- 8-bit cache
+ * The same step over a cache of half the bytes: K and V rows are quantised as
+ * they are appended and read back inside the attention.  The pages have no
+ * counterpart; decode attention reads every stored byte once per token, so the
+ * cache's bytes are its time and bound how many requests a pool holds.
+ *
+ * Format.  A row x (one token, one KV head, head_dim values) is stored as e4m3
+ * values and one exponent byte b = e + 127:
+ *     e = the least integer >= -126 with max|x| <= 448 * 2^e
+ *     value = round(x * 2^-e) to e4m3, to nearest, ties to even
+ * and stands for value * 2^e (within a relative 2^-4 of each x not below
+ * 2^(e-6), within 2^(e-10) of the smaller ones).  A row that holds a NaN or an infinity
+ * is stored as zeros with b = 255 and stands for NaNs: an attention that
+ * reaches it gives NaN for the query heads of that KV head, and for no other.
+ *  k_cache, v_cache  device, e4m3 [num_blocks][n_kv_heads][block_size][head_dim]
+ *  k_exps, v_exps    device, uint8 [num_blocks][n_kv_heads][block_size]
+ * all four 16-byte aligned.  Rows that were never written may hold anything;
+ * rows that an attention reads hold what cb_kv_append_fp8 or cb_copy_blocks_fp8
+ * stored (or the same format: no e4m3 NaN among the values).
+ * Shapes, sizes, errors, ownership and streams are those of the calls without
+ * _fp8; num_blocks * n_kv_heads * block_size < 2^31 - block_size.
+ *
+ * cb_kv_append_fp8: cb_kv_append into this cache.  The slots of one call that
+ * are not negative are distinct. */
+int cb_kv_append_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, int n_tokens, void* k_cache,
+                     void* v_cache, void* k_exps, void* v_exps, int num_blocks, int n_kv_heads, int head_dim,
+                     int block_size, void* stream);
+
+/* Stored rows read back as bf16 (to move a request to a bf16 cache or to the
+ * host): for every i with slot_mapping[i] >= 0 and every KV head g,
+ *     k_out[i][g][:] = what the cache holds for that slot and head
+ * and the same for v.  Exact, but for values under 2^-126, which bf16 rounds.
+ * A negative slot leaves row i as it was; a slot >= num_blocks * block_size
+ * does too and sets the device error word (CB_EDEVICE).
+ *  k_out, v_out   device, bf16 [n_rows][n_kv_heads][head_dim], 16-byte aligned */
+int cb_kv_gather_fp8(const int64_t* slot_mapping, int n_rows, const void* k_cache, const void* v_cache,
+                     const void* k_exps, const void* v_exps, int num_blocks, void* k_out, void* v_out, int n_kv_heads,
+                     int head_dim, int block_size, void* stream);
+
+/* cb_copy_blocks for this cache: values and exponents, bit-exact. */
+int cb_copy_blocks_fp8(const int32_t* pairs, int n_pairs, void* k_cache, void* v_cache, void* k_exps, void* v_exps,
+                       int num_blocks, int n_kv_heads, int head_dim, int block_size, void* stream);
+
+/* cb_paged_attention_window over this cache (window 0: none): q and out bf16,
+ * the softmax and the sums in fp32.  Rows of out that belong to no request are
+ * left as they were. */
+int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,
+                           const int32_t* block_tables, int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len,
+                           int max_kv_len, const void* k_cache, const void* v_cache, const void* k_exps,
+                           const void* v_exps, int num_blocks, void* out, float scale, int n_q_heads, int n_kv_heads,
+                           int head_dim, int block_size, int window, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Bytes of workspace that the attention calls need for these sizes (0 on
+ * invalid sizes).  Pure host function. */
+size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
+                                             int n_kv_heads, int head_dim, int block_size);
+
+/* cb_kv_append_fp8 of the step's new rows, then cb_paged_attention_fp8, on
+ * `stream`. */
+int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,
+                                     const int32_t* cu_q_lens, const int32_t* ctx_lens, const int32_t* block_tables,
+                                     int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len, int max_kv_len,
+                                     void* k_cache, void* v_cache, void* k_exps, void* v_exps, int num_blocks, void* out,
+                                     float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                     int window, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------- no-allocation variant
  * The pages have no counterpart: this exists for callers that cannot allocate

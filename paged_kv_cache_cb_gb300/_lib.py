@@ -38,6 +38,16 @@ SIGNATURES = [
     ("cb_kv_append_paged_attention_window", _c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                                      _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_float, _c_int,
                                                      _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    ("cb_kv_append_fp8", _c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    ("cb_kv_gather_fp8", _c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
+    ("cb_copy_blocks_fp8", _c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    ("cb_paged_attention_fp8", _c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                                        _vp, _c_int, _vp, _c_float, _c_int, _c_int, _c_int, _c_int, _c_int, _vp,
+                                        _c_size, _vp]),
+    ("cb_paged_attention_fp8_workspace_size", _c_size, [_c_int] * 8),
+    ("cb_kv_append_paged_attention_fp8", _c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                                                  _c_int, _vp, _vp, _vp, _vp, _c_int, _vp, _c_float, _c_int, _c_int,
+                                                  _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
     ("cb_paged_attention_noalloc", _c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
                                             _c_int, _vp, _c_float, _c_int, _c_int, _c_int, _c_int, _vp]),
     ("cb_last_error", _c_int, [_vp]),
@@ -260,6 +270,126 @@ def _append_attention(name, window, k_new, v_new, slot_mapping, q, cu_q_lens, ct
     rc = getattr(lib(), name)(pk, pv, ps, pq, pcu, pctx, pbt, block_tables.shape[1], n_reqs, n_tok, int(max_q_len),
                               int(max_kv_len), ck, cv, nb, po, float(scale), hq, hk, a, bs, *w, pw,
                               workspace.numel(), _stream(stream))
+    _check(name, rc)
+
+
+# ---------------------------------------------------------------- 8-bit cache
+def _fp8_cache(k_cache, v_cache, k_exps, v_exps):
+    """Pointers of an 8-bit cache (e4m3 [num_blocks, Hkv, bs, A] and uint8
+    exponents [num_blocks, Hkv, bs]) and its shape."""
+    torch = _t()
+    f8, u8 = torch.float8_e4m3fn, torch.uint8
+    ptrs = (_dev(k_cache, f8, "k_cache", 4), _dev(v_cache, f8, "v_cache", 4), _dev(k_exps, u8, "k_exps", 3),
+            _dev(v_exps, u8, "v_exps", 3))
+    shape = k_cache.shape
+    if v_cache.shape != shape or k_exps.shape != shape[:3] or v_exps.shape != shape[:3]:
+        raise ValueError("cache shape mismatch")
+    return ptrs, shape
+
+
+def _one_device(*tensors):
+    """Raw device pointers are launched on the current device: every tensor lives there."""
+    dev = _t().cuda.current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current device ({dev}), got one on {t.get_device()}")
+
+
+def cb_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exps, stream=None):
+    """k_new, v_new: bf16 [n_tokens, Hkv, A]; slot_mapping: int64 [n_tokens];
+    k_cache, v_cache: float8_e4m3fn [num_blocks, Hkv, block_size, A] and k_exps,
+    v_exps: uint8 [num_blocks, Hkv, block_size], written in place: each row's
+    values and its power-of-two exponent (include/cbattn.h, 8-bit cache)."""
+    torch = _t()
+    bf = torch.bfloat16
+    pk = _dev(k_new, bf, "k_new", 3)
+    pv = _dev(v_new, bf, "v_new", 3)
+    ps = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
+    n = k_new.shape[0]
+    if k_new.shape != (n, hk, a) or v_new.shape != k_new.shape or slot_mapping.shape[0] != n:
+        raise ValueError("shape mismatch")
+    _one_device(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exps)
+    _check("cb_kv_append_fp8", lib().cb_kv_append_fp8(pk, pv, ps, n, *cache, nb, hk, a, bs, _stream(stream)))
+
+
+def cb_kv_gather_fp8(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_out, stream=None):
+    """The rows stored at slot_mapping (int64 [n_rows], negative: the output row is
+    left as it was) read back into k_out, v_out: bf16 [n_rows, Hkv, A]."""
+    torch = _t()
+    bf = torch.bfloat16
+    ps = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
+    pk = _dev(k_out, bf, "k_out", 3)
+    pv = _dev(v_out, bf, "v_out", 3)
+    n = slot_mapping.shape[0]
+    if k_out.shape != (n, hk, a) or v_out.shape != k_out.shape:
+        raise ValueError("shape mismatch")
+    _one_device(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_out)
+    _check("cb_kv_gather_fp8", lib().cb_kv_gather_fp8(ps, n, *cache, nb, pk, pv, hk, a, bs, _stream(stream)))
+
+
+def cb_copy_blocks_fp8(pairs, k_cache, v_cache, k_exps, v_exps, stream=None):
+    """cb_copy_blocks of an 8-bit cache: values and exponents of block dst become
+    those of block src for every (src, dst) of pairs, int32 [n, 2]."""
+    pp = _dev(pairs, _t().int32, "pairs", 2)
+    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
+    if pairs.shape[1] != 2:
+        raise ValueError("shape mismatch")
+    _one_device(pairs, k_cache, v_cache, k_exps, v_exps)
+    _check("cb_copy_blocks_fp8", lib().cb_copy_blocks_fp8(pp, pairs.shape[0], *cache, nb, hk, a, bs, _stream(stream)))
+
+
+def cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim,
+                                          block_size):
+    return int(lib().cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads,
+                                                           n_kv_heads, head_dim, block_size))
+
+
+def cb_paged_attention_fp8(q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, scale,
+                           workspace, max_q_len, max_kv_len, window=0, stream=None):
+    """cb_paged_attention_window over an 8-bit cache (window 0: none).  q, out:
+    bf16 [n_tokens, Hq, A]; workspace: uint8 CUDA tensor of at least
+    cb_paged_attention_fp8_workspace_size bytes; the cache as for cb_kv_append_fp8."""
+    _attention_fp8("cb_paged_attention_fp8", None, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps,
+                   v_exps, out, scale, workspace, max_q_len, max_kv_len, window, stream)
+
+
+def cb_kv_append_paged_attention_fp8(k_new, v_new, slot_mapping, q, cu_q_lens, ctx_lens, block_tables, k_cache,
+                                     v_cache, k_exps, v_exps, out, scale, workspace, max_q_len, max_kv_len, window=0,
+                                     stream=None):
+    """cb_kv_append_fp8 of the step's new rows, then cb_paged_attention_fp8, as one
+    call; k_new, v_new: bf16 [n_tokens, Hkv, A] with n_tokens = q's."""
+    _attention_fp8("cb_kv_append_paged_attention_fp8", (k_new, v_new, slot_mapping), q, cu_q_lens, ctx_lens,
+                   block_tables, k_cache, v_cache, k_exps, v_exps, out, scale, workspace, max_q_len, max_kv_len,
+                   window, stream)
+
+
+def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, scale,
+                   workspace, max_q_len, max_kv_len, window, stream):
+    torch = _t()
+    bf, i32 = torch.bfloat16, torch.int32
+    ptrs = [_dev(q, bf, "q", 3), _dev(cu_q_lens, i32, "cu_q_lens", 1), _dev(ctx_lens, i32, "ctx_lens", 1),
+            _dev(block_tables, i32, "block_tables", 2)]
+    po = _dev(out, bf, "out", 3)
+    pw = _dev(workspace, torch.uint8, "workspace", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
+    n_tok, hq, a2 = q.shape
+    n_reqs = ctx_lens.shape[0]
+    if out.shape != q.shape or cu_q_lens.shape[0] != n_reqs + 1 or block_tables.shape[0] != n_reqs:
+        raise ValueError("shape mismatch")
+    if a2 != a:
+        raise ValueError("cache shape mismatch")
+    if new is not None:
+        k_new, v_new, slots = new
+        ptrs = [_dev(k_new, bf, "k_new", 3), _dev(v_new, bf, "v_new", 3),
+                _dev(slots, torch.int64, "slot_mapping", 1)] + ptrs
+        if k_new.shape != (n_tok, hk, a) or v_new.shape != k_new.shape or slots.shape[0] != n_tok:
+            raise ValueError("new rows must be [n_tokens, Hkv, A] with one slot per token")
+        _one_device(k_new, v_new, slots)
+    _one_device(q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, workspace)
+    rc = getattr(lib(), name)(*ptrs, block_tables.shape[1], n_reqs, n_tok, int(max_q_len), int(max_kv_len), *cache, nb,
+                              po, float(scale), hq, hk, a, bs, int(window), pw, workspace.shape[0], _stream(stream))
     _check(name, rc)
 
 

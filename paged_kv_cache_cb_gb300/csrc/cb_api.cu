@@ -242,6 +242,14 @@ bool shape_ok(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
 
 }  // namespace
 
+namespace cb {
+unsigned int* stream_error_word(cudaStream_t stream, int* rc) { return launch_err(stream, rc); }
+void set_last_launches(int n) { g_last_launches = n; }
+bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
+  return shape_ok(n_q_heads, n_kv_heads, head_dim, block_size);
+}
+}  // namespace cb
+
 extern "C" {
 
 int cb_kv_append(const void* k_new, const void* v_new, const int64_t* slot_mapping, int n_tokens, void* k_cache,

@@ -1,0 +1,176 @@
+// Entry points of the 8-bit KV cache (include/cbattn.h): argument checks and
+// dispatch.  Host code only.
+#include "../../include/cbattn.h"
+#include "cb_internal.h"
+
+using namespace cb;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The cache arguments shared by every entry point; false: CB_EINVAL.
+bool cache_of(Fp8Cache* c, const void* k, const void* v, const void* ke, const void* ve, int num_blocks, int n_kv_heads,
+              int head_dim, int block_size) {
+  if (num_blocks <= 0 || n_kv_heads <= 0 || (head_dim != 64 && head_dim != 128) || block_size != kBlockSize) return false;
+  if ((long long)num_blocks * n_kv_heads * kBlockSize >= (1LL << 31) - kBlockSize) return false;
+  if (!k || !v || !ke || !ve || !aligned16(k) || !aligned16(v) || !aligned16(ke) || !aligned16(ve)) return false;
+  c->k = static_cast<uint8_t*>(const_cast<void*>(k));
+  c->v = static_cast<uint8_t*>(const_cast<void*>(v));
+  c->k_exps = static_cast<uint8_t*>(const_cast<void*>(ke));
+  c->v_exps = static_cast<uint8_t*>(const_cast<void*>(ve));
+  c->num_blocks = num_blocks;
+  c->n_kv_heads = n_kv_heads;
+  c->head_dim = head_dim;
+  return true;
+}
+
+struct NewRows {
+  const void* k;
+  const void* v;
+  const int64_t* slots;
+};
+
+int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,
+             const int32_t* block_tables, int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len,
+             int max_kv_len, const void* k_cache, const void* v_cache, const void* k_exps, const void* v_exps,
+             int num_blocks, void* out, float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+             int window, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!supported_shape(n_q_heads, n_kv_heads, head_dim, block_size) || window < 0) return CB_EINVAL;
+  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
+      max_blocks_per_seq < 1 || num_blocks <= 0 || !(scale > 0.f) || max_q_len > max_kv_len)
+    return CB_EINVAL;
+  if (n_reqs == 0 || n_tokens == 0) {
+    set_last_launches(0);
+    return CB_OK;
+  }
+  Fp8Step s{};
+  if (!cache_of(&s.cache, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+    return CB_EINVAL;
+  if (!q || !cu_q_lens || !ctx_lens || !block_tables || !out || !workspace) return CB_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return CB_EINVAL;
+  if (app && (!app->k || !app->v || !app->slots || !aligned16(app->k) || !aligned16(app->v))) return CB_EINVAL;
+  if (workspace_bytes < cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads,
+                                                              n_kv_heads, head_dim, block_size))
+    return CB_EWORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int rc = CB_OK;
+  s.err = stream_error_word(st, &rc);
+  if (!s.err) return rc;
+  s.q = static_cast<const uint16_t*>(q);
+  s.cu_q_lens = cu_q_lens;
+  s.ctx_lens = ctx_lens;
+  s.block_tables = block_tables;
+  s.out = static_cast<uint16_t*>(out);
+  s.max_blocks_per_seq = max_blocks_per_seq;
+  s.n_reqs = n_reqs;
+  s.n_tokens = n_tokens;
+  s.max_q_len = max_q_len;
+  s.max_kv_len = max_kv_len;
+  s.n_q_heads = n_q_heads;
+  s.window = window;
+  s.scale_log2 = scale * 1.4426950408889634f;
+  if (app && launch_append_fp8(app->k, app->v, app->slots, n_tokens, s.cache, s.err, st) != cudaSuccess)
+    return CB_ECUDA;
+  int launches = 0;
+  if (launch_attention_fp8(s, st, &launches) != cudaSuccess) return CB_ECUDA;
+  set_last_launches(launches + (app ? 1 : 0));
+  return CB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cb_kv_append_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, int n_tokens, void* k_cache,
+                     void* v_cache, void* k_exps, void* v_exps, int num_blocks, int n_kv_heads, int head_dim,
+                     int block_size, void* stream) {
+  Fp8Cache c;
+  if (n_tokens < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+    return CB_EINVAL;
+  if (n_tokens == 0) {
+    set_last_launches(0);
+    return CB_OK;
+  }
+  if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new)) return CB_EINVAL;
+  int rc = CB_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned int* err = stream_error_word(st, &rc);
+  if (!err) return rc;
+  if (launch_append_fp8(k_new, v_new, slot_mapping, n_tokens, c, err, st) != cudaSuccess) return CB_ECUDA;
+  set_last_launches(1);
+  return CB_OK;
+}
+
+int cb_kv_gather_fp8(const int64_t* slot_mapping, int n_rows, const void* k_cache, const void* v_cache,
+                     const void* k_exps, const void* v_exps, int num_blocks, void* k_out, void* v_out, int n_kv_heads,
+                     int head_dim, int block_size, void* stream) {
+  Fp8Cache c;
+  if (n_rows < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+    return CB_EINVAL;
+  if (n_rows == 0) {
+    set_last_launches(0);
+    return CB_OK;
+  }
+  if (!k_out || !v_out || !slot_mapping || !aligned16(k_out) || !aligned16(v_out)) return CB_EINVAL;
+  int rc = CB_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned int* err = stream_error_word(st, &rc);
+  if (!err) return rc;
+  if (launch_gather_fp8(slot_mapping, n_rows, c, k_out, v_out, err, st) != cudaSuccess) return CB_ECUDA;
+  set_last_launches(1);
+  return CB_OK;
+}
+
+int cb_copy_blocks_fp8(const int32_t* pairs, int n_pairs, void* k_cache, void* v_cache, void* k_exps, void* v_exps,
+                       int num_blocks, int n_kv_heads, int head_dim, int block_size, void* stream) {
+  Fp8Cache c;
+  if (n_pairs < 0 || n_pairs > 65535 ||
+      !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+    return CB_EINVAL;
+  if (n_pairs == 0) {
+    set_last_launches(0);
+    return CB_OK;
+  }
+  if (!pairs) return CB_EINVAL;
+  int rc = CB_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned int* err = stream_error_word(st, &rc);
+  if (!err) return rc;
+  if (launch_copy_blocks_fp8(pairs, n_pairs, c, err, st) != cudaSuccess) return CB_ECUDA;
+  set_last_launches(1);
+  return CB_OK;
+}
+
+size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
+                                             int n_kv_heads, int head_dim, int block_size) {
+  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
+      !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
+    return 0;
+  return 256;
+}
+
+int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,
+                           const int32_t* block_tables, int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len,
+                           int max_kv_len, const void* k_cache, const void* v_cache, const void* k_exps,
+                           const void* v_exps, int num_blocks, void* out, float scale, int n_q_heads, int n_kv_heads,
+                           int head_dim, int block_size, int window, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return step_fp8(nullptr, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
+                  max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
+                  head_dim, block_size, window, workspace, workspace_bytes, stream);
+}
+
+int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,
+                                     const int32_t* cu_q_lens, const int32_t* ctx_lens, const int32_t* block_tables,
+                                     int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len, int max_kv_len,
+                                     void* k_cache, void* v_cache, void* k_exps, void* v_exps, int num_blocks, void* out,
+                                     float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
+                                     int window, void* workspace, size_t workspace_bytes, void* stream) {
+  const NewRows app{k_new, v_new, slot_mapping};
+  return step_fp8(&app, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
+                  max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
+                  head_dim, block_size, window, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

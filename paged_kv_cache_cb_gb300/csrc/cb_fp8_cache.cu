@@ -1,0 +1,178 @@
+// The 8-bit KV cache's data movement: append with quantisation, read-back and
+// block copies (format: cb_fp8.cuh).
+#include <algorithm>
+
+#include "cb_fp8.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// 8 bf16 (16 bytes) of a row, its largest |bits| over LANES consecutive lanes.
+template <int LANES>
+__device__ __forceinline__ uint32_t row_amax(const uint4& x) {
+  uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+#pragma unroll
+  for (int o = LANES / 2; o >= 1; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// 8 bf16 -> 8 e4m3 under the row's exponent byte.
+__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t b) {
+  if (b == kExpNan) return make_uint2(0u, 0u);
+  const float f = exp_inverse(b);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = pack_e4m3(bf16lo(w[i]) * f, bf16hi(w[i]) * f);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// 8 e4m3 -> 8 bf16 under the row's exponent byte.
+__device__ __forceinline__ uint4 restore8(const uint2& x, uint32_t b) {
+  const float f = exp_scale(b);
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    e4m3_to_f32((i < 2 ? x.x : x.y) >> (16 * (i & 1)), lo, hi);
+    o[i] = pack_bf16(lo * f, hi * f);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Token t's rows of K and V: LANES = A / 8 lanes hold one row of each, 8 values
+// per lane, so a row's largest magnitude is a shuffle reduction and a warp's
+// loads and stores are whole 256-byte and 128-byte rows.
+template <int LANES>
+__global__ void __launch_bounds__(kThreads) append_fp8_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
+                                                              const int64_t* __restrict__ slots, int64_t pieces,
+                                                              uint2* __restrict__ k_cache, uint2* __restrict__ v_cache,
+                                                              uint8_t* __restrict__ k_exps, uint8_t* __restrict__ v_exps,
+                                                              int64_t n_slots, int n_kv_heads, unsigned int* err) {
+  // rows are whole groups of lanes and pieces % LANES == 0: a group is in or out as one
+  for (int64_t i0 = blockIdx.x * (int64_t)kThreads; i0 < pieces; i0 += (int64_t)gridDim.x * kThreads) {
+    const int64_t i = i0 + threadIdx.x;
+    const bool in = i < pieces;
+    const int64_t row = i / LANES, t = row / n_kv_heads;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 k = in ? __ldg(k_new + i) : zero, v = in ? __ldg(v_new + i) : zero;
+    int64_t slot = in ? __ldg(slots + t) : -1;
+    const uint32_t kb = row_exp(row_amax<LANES>(k)), vb = row_exp(row_amax<LANES>(v));
+    if (slot >= n_slots) {
+      set_error(err, CB_DEVERR_BADSLOT);
+      slot = -1;
+    }
+    if (slot < 0) continue;
+    const int64_t dst = ((slot / kBlockSize) * n_kv_heads + (row - t * n_kv_heads)) * kBlockSize + slot % kBlockSize;
+    const int c = threadIdx.x % LANES;
+    k_cache[dst * LANES + c] = quantise8(k, kb);
+    v_cache[dst * LANES + c] = quantise8(v, vb);
+    if (c == 0) {
+      k_exps[dst] = (uint8_t)kb;
+      v_exps[dst] = (uint8_t)vb;
+    }
+  }
+}
+
+template <int LANES>
+__global__ void __launch_bounds__(kThreads) gather_fp8_kernel(const int64_t* __restrict__ slots, int64_t pieces,
+                                                              const uint2* __restrict__ k_cache,
+                                                              const uint2* __restrict__ v_cache,
+                                                              const uint8_t* __restrict__ k_exps,
+                                                              const uint8_t* __restrict__ v_exps, uint4* __restrict__ k_out,
+                                                              uint4* __restrict__ v_out, int64_t n_slots, int n_kv_heads,
+                                                              unsigned int* err) {
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / LANES, t = row / n_kv_heads;
+    const int64_t slot = __ldg(slots + t);
+    if (slot < 0) continue;
+    if (slot >= n_slots) {
+      set_error(err, CB_DEVERR_BADSLOT);
+      continue;
+    }
+    const int64_t src = ((slot / kBlockSize) * n_kv_heads + (row - t * n_kv_heads)) * kBlockSize + slot % kBlockSize;
+    const int c = (int)(i % LANES);
+    const uint2 k = __ldg(k_cache + src * LANES + c), v = __ldg(v_cache + src * LANES + c);
+    const uint32_t kb = __ldg(k_exps + src), vb = __ldg(v_exps + src);
+    k_out[i] = restore8(k, kb);
+    v_out[i] = restore8(v, vb);
+  }
+}
+
+// Block dst of both caches and of their exponents becomes block src; grid.y =
+// pair.  A block is `pieces` 16-byte pieces of values and n_kv_heads of
+// exponents.
+__global__ void __launch_bounds__(kThreads) copy_blocks_fp8_kernel(const int32_t* __restrict__ pairs, uint4* k_cache, uint4* v_cache,
+                                                                   uint4* k_exps, uint4* v_exps, int num_blocks,
+                                                                   int64_t pieces, int n_kv_heads, unsigned int* err) {
+  const int src = __ldg(pairs + 2 * blockIdx.y), dst = __ldg(pairs + 2 * blockIdx.y + 1);
+  if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_error(err, CB_DEVERR_BADBLOCK);
+    return;
+  }
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < pieces + n_kv_heads;
+       i += (int64_t)gridDim.x * kThreads) {
+    const bool e = i >= pieces;
+    const int64_t n = e ? n_kv_heads : pieces, at = e ? i - pieces : i;
+    uint4* kc = e ? k_exps : k_cache;
+    uint4* vc = e ? v_exps : v_cache;
+    const uint4 k = kc[src * n + at], v = vc[src * n + at];
+    kc[dst * n + at] = k;
+    vc[dst * n + at] = v;
+  }
+}
+
+unsigned grid_for(int64_t pieces) { return (unsigned)std::min<int64_t>((pieces + kThreads - 1) / kThreads, 1 << 20); }
+
+}  // namespace
+
+cudaError_t launch_append_fp8(const void* k_new, const void* v_new, const int64_t* slots, int n_tokens, const Fp8Cache& c,
+                              unsigned int* err, cudaStream_t stream) {
+  const int lanes = c.head_dim / 8;
+  const int64_t pieces = (int64_t)n_tokens * c.n_kv_heads * lanes;
+  if (pieces == 0) return cudaSuccess;
+#define CB_APPEND(L_)                                                                                                  \
+  append_fp8_kernel<L_><<<grid_for(pieces), kThreads, 0, stream>>>(                                                    \
+      static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slots, pieces,                               \
+      reinterpret_cast<uint2*>(c.k), reinterpret_cast<uint2*>(c.v), c.k_exps, c.v_exps, (int64_t)c.num_blocks * kBlockSize, \
+      c.n_kv_heads, err)
+  if (lanes == 16)
+    CB_APPEND(16);
+  else
+    CB_APPEND(8);
+#undef CB_APPEND
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_fp8(const int64_t* slots, int n_rows, const Fp8Cache& c, void* k_out, void* v_out,
+                              unsigned int* err, cudaStream_t stream) {
+  const int lanes = c.head_dim / 8;
+  const int64_t pieces = (int64_t)n_rows * c.n_kv_heads * lanes;
+  if (pieces == 0) return cudaSuccess;
+#define CB_GATHER(L_)                                                                                              \
+  gather_fp8_kernel<L_><<<grid_for(pieces), kThreads, 0, stream>>>(                                                \
+      slots, pieces, reinterpret_cast<const uint2*>(c.k), reinterpret_cast<const uint2*>(c.v), c.k_exps, c.v_exps, \
+      static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), (int64_t)c.num_blocks * kBlockSize, c.n_kv_heads, err)
+  if (lanes == 16)
+    CB_GATHER(16);
+  else
+    CB_GATHER(8);
+#undef CB_GATHER
+  return cudaGetLastError();
+}
+
+cudaError_t launch_copy_blocks_fp8(const int32_t* pairs, int n_pairs, const Fp8Cache& c, unsigned int* err,
+                                   cudaStream_t stream) {
+  if (n_pairs == 0) return cudaSuccess;
+  const int64_t pieces = (int64_t)c.n_kv_heads * c.head_dim;        // 16 tokens x head_dim bytes per head
+  const int ctas = (int)std::min<int64_t>(8, (pieces + c.n_kv_heads + kThreads - 1) / kThreads);
+  copy_blocks_fp8_kernel<<<dim3(ctas, n_pairs), kThreads, 0, stream>>>(
+      pairs, reinterpret_cast<uint4*>(c.k), reinterpret_cast<uint4*>(c.v), reinterpret_cast<uint4*>(c.k_exps),
+      reinterpret_cast<uint4*>(c.v_exps), c.num_blocks, pieces, c.n_kv_heads, err);
+  return cudaGetLastError();
+}
+
+}  // namespace cb

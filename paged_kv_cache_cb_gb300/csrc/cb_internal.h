@@ -115,4 +115,41 @@ cudaError_t launch_copy_blocks(const int32_t* pairs, int n_pairs, void* k_cache,
                                int n_kv_heads, int head_dim, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_hbm_copy(void* dst, const void* src, size_t bytes, int n_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 8-bit cache
+// K and V as e4m3 values [num_blocks][Hkv][16][A] with one exponent byte per row
+// [num_blocks][Hkv][16] (cb_fp8.cuh).
+struct Fp8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_exps;
+  uint8_t* v_exps;
+  int num_blocks, n_kv_heads, head_dim;
+};
+// A step's attention over it.
+struct Fp8Step {
+  const uint16_t* q;            // bf16 [n_tokens][Hq][A]
+  const int32_t* cu_q_lens;     // [n_reqs + 1]
+  const int32_t* ctx_lens;      // [n_reqs]
+  const int32_t* block_tables;  // [n_reqs][max_blocks_per_seq]
+  uint16_t* out;                // bf16 [n_tokens][Hq][A]
+  Fp8Cache cache;
+  int max_blocks_per_seq, n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads;
+  int window;                   // 0: none
+  float scale_log2;             // scale * log2(e)
+  unsigned int* err;            // the launching stream's error word
+};
+cudaError_t launch_append_fp8(const void* k_new, const void* v_new, const int64_t* slots, int n_tokens, const Fp8Cache& c,
+                              unsigned int* err, cudaStream_t stream);
+cudaError_t launch_gather_fp8(const int64_t* slots, int n_rows, const Fp8Cache& c, void* k_out, void* v_out,
+                              unsigned int* err, cudaStream_t stream);
+cudaError_t launch_copy_blocks_fp8(const int32_t* pairs, int n_pairs, const Fp8Cache& c, unsigned int* err,
+                                   cudaStream_t stream);
+// Attention of the step's requests; `launches` receives the kernels enqueued.
+cudaError_t launch_attention_fp8(const Fp8Step& s, cudaStream_t stream, int* launches);
+
+// Library state that the entry points of other files use (cb_api.cu).
+unsigned int* stream_error_word(cudaStream_t stream, int* rc);   // nullptr: return *rc
+void set_last_launches(int n);
+bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size);
+
 }  // namespace cb
