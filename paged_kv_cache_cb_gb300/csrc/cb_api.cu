@@ -245,6 +245,23 @@ bool shape_ok(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
 namespace cb {
 unsigned int* stream_error_word(cudaStream_t stream, int* rc) { return launch_err(stream, rc); }
 void set_last_launches(int n) { g_last_launches = n; }
+bool device_sms(int* n) {
+  DeviceInfo di;
+  if (!device_info(&di)) return false;
+  *n = di.n_sms;
+  return true;
+}
+bool encode_byte_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)row_bytes, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+  const cuuint32_t box[2] = {(cuuint32_t)row_bytes, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
   return shape_ok(n_q_heads, n_kv_heads, head_dim, block_size);
 }

@@ -1,5 +1,7 @@
 // Entry points of the 8-bit KV cache (include/cbattn.h): argument checks and
 // dispatch.  Host code only.
+#include <algorithm>
+
 #include "../../include/cbattn.h"
 #include "cb_internal.h"
 
@@ -47,12 +49,18 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   Fp8Step s{};
   if (!cache_of(&s.cache, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
     return CB_EINVAL;
+  // the kernels count tiles of the step in 32 bits
+  const long long blocks = std::min<long long>(max_blocks_per_seq, ((long long)max_kv_len + kBlockSize - 1) / kBlockSize);
+  if (blocks * n_reqs * n_kv_heads >= 1LL << 31) return CB_EINVAL;
   if (!q || !cu_q_lens || !ctx_lens || !block_tables || !out || !workspace) return CB_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return CB_EINVAL;
   if (app && (!app->k || !app->v || !app->slots || !aligned16(app->k) || !aligned16(app->v))) return CB_EINVAL;
   if (workspace_bytes < cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads,
                                                               n_kv_heads, head_dim, block_size))
     return CB_EWORKSPACE;
+  int sms = 0;
+  if (!device_sms(&sms)) return CB_ECUDA;
+  sms = sms < kMaxDecodeGrid ? sms : kMaxDecodeGrid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int rc = CB_OK;
   s.err = stream_error_word(st, &rc);
@@ -72,9 +80,17 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   s.scale_log2 = scale * 1.4426950408889634f;
   if (app && launch_append_fp8(app->k, app->v, app->slots, n_tokens, s.cache, s.err, st) != cudaSuccess)
     return CB_ECUDA;
-  int launches = 0;
-  if (launch_attention_fp8(s, st, &launches) != cudaSuccess) return CB_ECUDA;
-  set_last_launches(launches + (app ? 1 : 0));
+  int launches = app ? 1 : 0;
+  const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
+  if (tiles) {
+    if (launch_decode_fp8(s, fp8_partials(workspace), sms, st) != cudaSuccess) return CB_ECUDA;
+    launches += 2;
+  }
+  if (max_q_len > 1 || !tiles) {
+    if (launch_attention_fp8_simple(s, !tiles, st) != cudaSuccess) return CB_ECUDA;
+    ++launches;
+  }
+  set_last_launches(launches);
   return CB_OK;
 }
 
@@ -147,7 +163,7 @@ size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q
   if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
       !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
-  return 256;
+  return fp8_partials_bytes(head_dim);
 }
 
 int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,

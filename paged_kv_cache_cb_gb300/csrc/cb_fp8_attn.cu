@@ -12,7 +12,7 @@ constexpr int kWarps = 4;
 // visible keys in turn, lane = A / 32 dimensions, running max and sum per head
 // in base 2; the four warps' (m, l, o) are joined in shared memory.
 template <int A, int GS>
-__global__ void __launch_bounds__(32 * kWarps) attention_fp8_simple(const Fp8Step P, int group) {
+__global__ void __launch_bounds__(32 * kWarps) attention_fp8_simple(const Fp8Step P, int group, bool singles) {
   constexpr int D = A / 32;
   __shared__ float sm[kWarps][GS], sl[kWarps][GS], so[kWarps][GS][A];
   const int t = blockIdx.x, g = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(32 * kWarps) attention_fp8_simple(const Fp8Ste
       hi = mid - 1;
   }
   const int r = lo, q0 = __ldg(P.cu_q_lens + r), q_len = __ldg(P.cu_q_lens + r + 1) - q0, ctx = __ldg(P.ctx_lens + r);
+  if (q_len == 1 && !singles) return;
   if (ctx < 0 || q0 < 0 || t - q0 >= q_len || q_len > P.max_q_len || (long long)ctx + q_len > P.max_kv_len ||
       ((long long)ctx + q_len + kBlockSize - 1) / kBlockSize > P.max_blocks_per_seq) {
     if (threadIdx.x == 0) set_error(P.err, CB_DEVERR_BADLEN);
@@ -100,13 +101,12 @@ __global__ void __launch_bounds__(32 * kWarps) attention_fp8_simple(const Fp8Ste
 
 }  // namespace
 
-cudaError_t launch_attention_fp8(const Fp8Step& s, cudaStream_t stream, int* launches) {
+cudaError_t launch_attention_fp8_simple(const Fp8Step& s, bool singles, cudaStream_t stream) {
   const int group = s.n_q_heads / s.cache.n_kv_heads;
-  *launches = 1;
 #define CB_SIMPLE(A_, GS_)                                                                                       \
   if (s.cache.head_dim == A_ && (group == GS_ || (GS_ == 8 && group > 8))) {                                     \
     attention_fp8_simple<A_, GS_>                                                                                \
-        <<<dim3(s.n_tokens, s.cache.n_kv_heads, group / GS_), 32 * kWarps, 0, stream>>>(s, group);               \
+        <<<dim3(s.n_tokens, s.cache.n_kv_heads, group / GS_), 32 * kWarps, 0, stream>>>(s, group, singles);      \
     return cudaGetLastError();                                                                                   \
   }
   CB_SIMPLE(128, 1)

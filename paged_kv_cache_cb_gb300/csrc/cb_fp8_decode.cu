@@ -1,0 +1,984 @@
+// Single-token attention over the 8-bit KV cache (format: cb_fp8.cuh) on the
+// tensor cores, without converting the cache.
+//
+// Mathematics.  For a request's query head h with keys j (values k_j 2^ek_j,
+// v_j 2^ev_j, k_j and v_j e4m3):
+//     x_j = scale log2(e) 2^(eq + ek_j) (q . k_j)          p_j = 2^(x_j - m)
+//     o   = sum_j 2^(x_j + ev_j - M) v_j                   l   = sum_j p_j
+//     out = o 2^(M - m) / l
+// with the running maxima m of x_j and M of x_j + ev_j.  The rows' powers of two
+// never touch the matrices: 2^ek_j is a factor of row j's scores, 2^ev_j goes
+// into row j's weight.  Two maxima, because the weights' dynamic range is what
+// the 8-bit operand has to hold, whatever the value rows' sizes; p is kept in
+// fp32 for l alone.
+// Both matrix products take e4m3 K and V straight from the cache
+// (tcgen05.mma kind::f8f6f4, fp32 accumulation).  Their other operands are split
+// into 8-bit terms whose products add up:
+//   q    two e4m3 terms (each 4 significant bits, so 8: exactly bf16's) of
+//        q 2^-eq, the row's largest value in [128, 256): values down to 2^-15 of
+//        the largest are exact, smaller ones are off by 2^-18 of it at most;
+//   w    three e5m2 terms of the weight 2^12 w, w in (0, 2^3]: the weight is
+//        rounded to 11 bits (half), the first two terms are its top 3 bits and
+//        the next 3, the third rounds the rest to 3 bits: within 2^-9 of w (bf16
+//        rounds within 2^-8) and 2^-29 of the largest.
+// Using the 8-bit products instead of converting K and V to bf16 halves what
+// passes through shared memory, the second limit after HBM (at the copy rate each
+// SM takes 23 bytes of cache a cycle; converted tiles would add a read and twice
+// that in writes and operand reads, over its 128 bytes a cycle).
+//
+// Tiles.  In the cache layout [block][KV head][16 tokens][A], HG heads of one
+// block are 16 HG contiguous rows.  A tile is 128 rows: 8 / HG blocks of HG
+// heads (HG = 8, 4, 2 or 1, the largest that divides the KV heads), so 8 slots
+// of 16 rows, slot j = (block j / HG, head j % HG).
+//     S[row, (term, slot, g)] = K_tile . q^T      one MMA per 32 dimensions, N = 16 G
+//     O^T[dim, (slot, term, g)] += V^T . w^T      one MMA per 2 slots (32 rows)
+// A row needs only its own slot's columns of S.  Each slot keeps its own maxima
+// and its own columns of O, so softmax never crosses a half-warp; the slots of a
+// head are joined at the end of a sequence.  Head dimension 64: V^T has 64 rows,
+// its descriptor repeats them (leading offset 0) to M = 128.
+//
+// Work.  A sequence is a (request, group of HG heads).  All sequences' tiles,
+// laid end to end, are cut into one equal range per CTA (one CTA per SM).  A
+// sequence cut at a range's end leaves (m, l, o) per piece, and a second small
+// kernel joins the pieces by log-sum-exp: no counters, no grid barrier, nothing
+// to initialise, and the same bits every time.
+//
+// Warps: 0-3 and 4-7 softmax groups, which take the segments (a range's parts of
+// sequences) in turn, so that one group's segment start (query terms) and end
+// (output) overlap the other's tiles; 8 K loads, 9 V loads (TMA through the block
+// table), 10 issues S, 11 issues O.  Thread = tile row, then output dimension.
+// Every wait is bounded.
+#include <algorithm>
+
+#include "cb_decode_item.cuh"
+#include "cb_fp8.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMinTiles = 2;        // tiles per CTA below which a step uses fewer CTAs
+constexpr float kWeightBits = 12.f; // weights are stored times 2^12 (e5m2: up to 2^15.8, down to 2^-16)
+constexpr float kLazyP = 8.f;       // the running maxima follow only beyond these (base 2)
+constexpr float kLazyW = 3.f;
+constexpr int kMaxHeads = 64;       // query heads of a tile
+
+template <int A, int G>
+struct Cfg {
+  static constexpr int C = 8 * G;                            // columns: slot x group member
+  static constexpr int NS = 2 * C;                           // S columns (two query terms)
+  static constexpr int SS = G <= 2 ? 8 : (G == 4 ? 16 : 24); // w rows per slot (three terms x G, padded)
+  static constexpr int NO = 8 * SS;                          // O columns
+  static constexpr int SB = G == 8 ? 2 : 4;                  // S buffers
+  static constexpr int OB = G == 8 ? 1 : 2;                  // O buffers
+  static constexpr int KS = A == 128 ? 4 : 6, VS = KS;       // K and V stages
+  static constexpr int PB = 4;                               // w buffers
+  static constexpr int ES = 8;                               // exponent stages
+  static constexpr int kTile = 128 * A;                      // bytes
+  static constexpr int kCols = SB * NS + OB * NO;
+  static constexpr int kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
+  static_assert(kCols <= 512, "tensor memory");
+};
+
+template <int A, int G>
+struct alignas(1024) Smem {
+  using X = Cfg<A, G>;
+  uint8_t k[X::KS][X::kTile];
+  uint8_t v[X::VS][X::kTile];
+  uint8_t q[2][16 * G * A];          // per group: rows (term, slot, g) of A bytes, swizzled like K
+  uint8_t p[X::PB][256 * X::SS];     // w: [2 slots][2 SS rows][32 bytes], 8-row x 16-byte core matrices
+  uint8_t ex[X::ES][2][128];         // exponent bytes of the tile's K and V rows
+  float cf[2][X::C];                 // per group: scale log2(e) 2^eq per column
+  float alpha[2][2][X::C];           // factors of O when M moves
+  float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // a segment's l, m, M, then l, m per head and the slots' factors
+  uint64_t k_full[X::KS], k_empty[X::KS], v_full[X::VS], v_empty[X::VS];
+  uint64_t e_full[X::ES], e_empty[X::ES], s_full[X::SB], s_empty[X::SB], p_full[X::PB], pv_done[X::PB];
+  uint64_t q_full[2], o_full[X::OB], o_free[X::OB], turn[2], drain[2];
+  int scan[16];
+  uint32_t tmem;
+  volatile int abort;
+  int u0, u1, total, eff;            // this CTA's range of tiles; all tiles; CTAs with a range
+};
+
+// Plan arrays after Smem: pre[n + 1] tiles before request r (one head group), kv[n] keys, tok[n] query row.
+struct Plan {
+  const int *pre, *kv, *tok;
+};
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// D(tmem) (+)= A(smem) B(smem), 8-bit floating point operands, fp32 accumulation.
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: formats 0 = e4m3, 1 = e5m2; fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_fmt, int b_fmt, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Shared-memory matrix descriptor; layout 0: no swizzle, 2: 128-byte, 4: 64-byte swizzle.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, int layout) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 |
+         (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
+}
+// Untiled bulk copy (16-byte aligned on both sides, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(static_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+// N (2, 4, 8, 16) consecutive fp32 columns of this thread's TMEM lane (no wait).
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+  uint32_t r[N];
+  if constexpr (N == 2)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr));
+  if constexpr (N == 4)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+  if constexpr (N == 8)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Bounded wait with the same outcome in all 32 lanes.
+template <class S>
+__device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  if (!ok) {
+    set_error(P.err, CB_DEVERR_TIMEOUT);
+    sm.abort = 1;
+  }
+  return ok;
+}
+
+// ---------------------------------------------------------------- work
+// A segment: tiles [t0, t0 + nt) of the `tiles` tiles of sequence (r, hg).
+struct Seg {
+  int r, hg, t0, nt, tiles, kv, tok, fb;   // fb: the first block its window reaches
+};
+struct SegIter {
+  Plan plan;
+  int u, u1, nhg, r, window;
+  __device__ SegIter(const Plan& pl, int u0, int u1_, int nhg_, int n, int window_)
+      : plan(pl), u(u0), u1(u1_), nhg(nhg_), window(window_) {
+    int lo = 0, hi = n - 1;            // the last request whose tiles start at or before u0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.pre[mid] * nhg <= u0)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    r = lo;
+  }
+  __device__ bool next(Seg& s) {
+    if (u >= u1) return false;
+    while (plan.pre[r + 1] * nhg <= u) ++r;
+    s.r = r;
+    s.tiles = plan.pre[r + 1] - plan.pre[r];
+    const int off = u - plan.pre[r] * nhg;
+    s.hg = off / s.tiles;
+    s.t0 = off - s.hg * s.tiles;
+    s.nt = min(s.tiles - s.t0, u1 - u);
+    s.kv = plan.kv[r];
+    s.tok = plan.tok[r];
+    s.fb = window_first_block(s.kv, window);
+    u += s.nt;
+    return true;
+  }
+};
+
+// Tiles of one head group of request r if it has one new token; 0 otherwise.
+__device__ __forceinline__ int request_tiles(const Fp8Step& P, int r, int bpt, int* kv, int* tok) {
+  const int q0 = __ldg(P.cu_q_lens + r), q1 = __ldg(P.cu_q_lens + r + 1), ctx = __ldg(P.ctx_lens + r);
+  *kv = 0;
+  *tok = 0;
+  const long long n = (long long)q1 - q0;
+  if (q0 >= 0 && q1 <= P.n_tokens && (n == 0 || (n > 1 && P.max_q_len > 1))) return 0;
+  const long long keys = (long long)ctx + 1, nblk = (keys + kBlockSize - 1) / kBlockSize;
+  if (n != 1 || ctx < 0 || q0 < 0 || q1 > P.n_tokens || keys > P.max_kv_len || nblk > P.max_blocks_per_seq) {
+    set_error(P.err, CB_DEVERR_BADLEN);
+    return 0;
+  }
+  *kv = (int)keys;
+  *tok = q0;
+  return ((int)nblk - window_first_block(keys, P.window) + bpt - 1) / bpt;
+}
+
+// The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
+__device__ __forceinline__ int cta_of(int u, int total, int eff) {
+  return (int)((((long long)u + 1) * eff - 1) / total);
+}
+
+// All threads; ends with __syncthreads().
+template <int A, int G>
+__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, int* pre, int* kv, int* tok, int hg_heads) {
+  const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, nw = kThreads / 32;
+  const int bpt = 8 / hg_heads, nhg = P.cache.n_kv_heads / hg_heads;
+  const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
+  int own = 0;
+  for (int r = lo; r < hi; ++r) {
+    const int t = request_tiles(P, r, bpt, kv + r, tok + r);
+    pre[r] = t;
+    own += t;
+  }
+  int incl = own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += x;
+  }
+  if (lane == 31) S.scan[wid] = incl;
+  __syncthreads();
+  int total = 0, run = incl - own;
+  for (int w = 0; w < nw; ++w) {
+    total += S.scan[w];
+    run += w < wid ? S.scan[w] : 0;
+  }
+  for (int r = lo; r < hi; ++r) {
+    const int t = pre[r];
+    pre[r] = run;
+    run += t;
+  }
+  if (tid == 0) {
+    pre[n] = total;
+    total *= nhg;
+    const int eff = max(1, min((int)gridDim.x, (total + kMinTiles - 1) / kMinTiles));
+    const int b = blockIdx.x;
+    S.total = total;
+    S.eff = eff;
+    S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
+    S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
+  }
+  __syncthreads();
+  if (tid == 0) {                     // the sequence that starts in this range and goes on after it
+    Fp8Rec rec = {0, 0, 0, 0};
+    if (S.u1 > S.u0) {
+      SegIter last({pre, kv, tok}, S.u1 - 1, S.u1, nhg, n, P.window);
+      Seg s;
+      last.next(s);
+      const int start = pre[s.r] * nhg + s.hg * s.tiles, end = start + s.tiles;
+      if (start >= S.u0 && end > S.u1) rec = {s.r, s.hg, cta_of(end - 1, S.total, S.eff) - (int)blockIdx.x + 1, 0};
+    }
+    W.rec[blockIdx.x] = rec;
+  }
+}
+
+// ---------------------------------------------------------------- loads (warps 8, 9)
+// A segment's block-table entries, 32 at a time (a lane each), the next 32 (or
+// the next segment's first) on their way while these are used.
+struct Table {
+  int cur, nxt;
+  __device__ static int entry(const Fp8Step& P, const Seg& s, int bpt, int chunk) {
+    const int b = s.fb + s.t0 * bpt + chunk * 32 + (int)(threadIdx.x & 31);
+    const int end = (s.kv + kBlockSize - 1) / kBlockSize;
+    // entries past the segment belong to another CTA or to nobody: not read
+    if (b >= end || b >= s.fb + (s.t0 + s.nt) * bpt) return -2;
+    const int e = __ldg(P.block_tables + (size_t)s.r * P.max_blocks_per_seq + b);
+    return e < 0 || e >= P.cache.num_blocks ? -1 : e;
+  }
+};
+
+// K: also the tiles' exponents.  V: values only.
+template <int A, int G, bool IS_K>
+__device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>& S, const Plan& plan, int hg_heads) {
+  using X = Cfg<A, G>;
+  constexpr int NST = IS_K ? X::KS : X::VS;
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, Hkv = P.cache.n_kv_heads, bpt = 8 / hg_heads, nhg = Hkv / hg_heads;
+  const int rows_total = P.cache.num_blocks * Hkv * kBlockSize, box = hg_heads * kBlockSize;
+  uint64_t* full = IS_K ? S.k_full : S.v_full;
+  uint64_t* empty = IS_K ? S.k_empty : S.v_empty;
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  Seg s, nx;
+  uint32_t n = 0;
+  bool ok = true;
+  bool more = it.next(s);
+  int nxt = more ? Table::entry(P, s, bpt, 0) : -2;
+  while (more && ok) {
+    const bool again = it.next(nx);
+    const int per = 32 / bpt;                        // tiles per 32 entries
+    int cur = -2;
+    for (int j = 0; j < s.nt && ok; ++j, ++n) {
+      if (j % per == 0) {
+        cur = nxt;
+        if (IS_K && cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);   // its rows load as zeros
+        nxt = j + per < s.nt ? Table::entry(P, s, bpt, j / per + 1) : (again ? Table::entry(P, nx, bpt, 0) : -2);
+      }
+      const int e = __shfl_sync(FULL, cur, (j % per) * bpt + (lane & (bpt - 1)));
+      const int row = e >= 0 ? (e * Hkv + s.hg * hg_heads) * kBlockSize : rows_total;   // past the extent: zeros
+      const int st = n % NST;
+      ok = wwait(P, S, &empty[st], ((n / NST) & 1) ^ 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[st], X::kTile);
+      __syncwarp();
+      if (lane < bpt) tma_load_2d((IS_K ? S.k[st] : S.v[st]) + lane * box * A, map, 0, row, &full[st]);
+      if constexpr (IS_K) {
+        const int es = n % X::ES;
+        ok = wwait(P, S, &S.e_empty[es], ((n / X::ES) & 1) ^ 1);
+        if (!ok) {
+          ++n;
+          break;
+        }
+        const unsigned have = __ballot_sync(FULL, lane < bpt && e >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&S.e_full[es], 2u * box * __popc(have));
+        __syncwarp();
+        if (lane < bpt && e >= 0) {
+          bulk_load(&S.ex[es][0][lane * box], P.cache.k_exps + row, box, &S.e_full[es]);
+          bulk_load(&S.ex[es][1][lane * box], P.cache.v_exps + row, box, &S.e_full[es]);
+        }
+      }
+    }
+    s = nx;
+    more = again;
+  }
+  if (!ok) {
+    // let the copies already issued land before the CTA exits
+    for (uint32_t i = n > (uint32_t)NST ? n - NST : 0; i < n; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, 20000000ull);
+    if constexpr (IS_K)
+      for (uint32_t i = n > (uint32_t)X::ES ? n - X::ES : 0; i < n; ++i)
+        mbar_wait(&S.e_full[i % X::ES], (i / X::ES) & 1, 20000000ull);
+  }
+}
+
+// ---------------------------------------------------------------- MMA issue (warps 10, 11)
+template <int A, int G>
+__device__ void issue_s(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int nhg) {
+  using X = Cfg<A, G>;
+  constexpr uint32_t kIdesc = idesc_f8(128, X::NS, 0, 0, 0, 0);
+  constexpr int kLayout = A == 128 ? 2 : 4;
+  const uint64_t kd = smem_desc(smem_u32(S.k[0]), 16, 8 * A, kLayout), qd = smem_desc(smem_u32(S.q[0]), 16, 8 * A, kLayout);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  Seg s;
+  uint32_t n = 0;
+  bool ok = true;
+  for (int i = 0; ok && it.next(s); ++i) {
+    ok = wwait(P, S, &S.q_full[i & 1], (i >> 1) & 1);
+    for (int j = 0; j < s.nt && ok; ++j, ++n) {
+      const int st = n % X::KS, sb = n % X::SB;
+      ok = wwait(P, S, &S.s_empty[sb], ((n / X::SB) & 1) ^ 1) && wwait(P, S, &S.k_full[st], (n / X::KS) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t a = kd + (uint32_t)(st * (X::kTile >> 4)), b = qd + (uint32_t)((i & 1) * ((16 * G * A) >> 4));
+      if (elect_one()) {
+#pragma unroll
+        for (int d = 0; d < A / 32; ++d) mma_f8(S.tmem + sb * X::NS, a + d * 2, b + d * 2, kIdesc, d > 0);
+        tc_commit(&S.k_empty[st]);
+        tc_commit(&S.s_full[sb]);
+      }
+      __syncwarp();
+    }
+  }
+  if (!ok) S.abort = 1;
+  if (elect_one()) tc_commit(&S.drain[0]);
+  __syncwarp();
+  mbar_wait(&S.drain[0], 0, 20000000ull);
+}
+
+template <int A, int G>
+__device__ void issue_pv(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int nhg) {
+  using X = Cfg<A, G>;
+  constexpr uint32_t kIdesc = idesc_f8(128, 2 * X::SS, 0, 1, 1, 0);   // V^T: e4m3, MN-major; w: e5m2, K-major
+  constexpr int kLayout = A == 128 ? 2 : 4;
+  const uint64_t vd = smem_desc(smem_u32(S.v[0]), 0, 8 * A, kLayout), pd = smem_desc(smem_u32(S.p[0]), 128, 256, 0);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  Seg s;
+  uint32_t n = 0;
+  bool ok = true;
+  for (int i = 0; ok && it.next(s); ++i) {
+    const int ob = i % X::OB;
+    ok = wwait(P, S, &S.o_free[ob], ((i / X::OB) & 1) ^ 1);
+    for (int j = 0; j < s.nt && ok; ++j, ++n) {
+      const int st = n % X::VS, pb = n % X::PB;
+      ok = wwait(P, S, &S.v_full[st], (n / X::VS) & 1) && wwait(P, S, &S.p_full[pb], (n / X::PB) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t a = vd + (uint32_t)(st * (X::kTile >> 4)), b = pd + (uint32_t)(pb * ((256 * X::SS) >> 4));
+      const uint32_t d = S.tmem + X::SB * X::NS + ob * X::NO;
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_f8(d + ks * 2 * X::SS, a + ((ks * 32 * A) >> 4), b + ((ks * 64 * X::SS) >> 4), kIdesc, j > 0);
+        tc_commit(&S.v_empty[st]);
+        tc_commit(&S.pv_done[pb]);
+        // a barrier of its own: pv_done may run through the other group's tiles before this one looks
+        if (j == s.nt - 1) tc_commit(&S.o_full[ob]);
+      }
+      __syncwarp();
+    }
+  }
+  if (!ok) S.abort = 1;
+  if (elect_one()) tc_commit(&S.drain[1]);
+  __syncwarp();
+  mbar_wait(&S.drain[1], 0, 20000000ull);
+}
+
+// ---------------------------------------------------------------- softmax groups (warps 0-3, 4-7)
+// Query terms of the segment's heads into q[grp], and the columns' factors.
+template <int A, int G>
+__device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int grp, int hg_heads) {
+  constexpr int D = A / 32;                  // values per lane
+  constexpr int B = 8;                       // heads in flight
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int heads = hg_heads * G, bpt = 8 / hg_heads;
+  const uint16_t* src = P.q + ((size_t)s.tok * P.n_q_heads + (size_t)s.hg * heads) * A + lane * D;
+  for (int h0 = warp; h0 < heads; h0 += 4 * B) {
+    uint32_t w[B][D / 2];
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      const int h = h0 + 4 * u;
+#pragma unroll
+      for (int d = 0; d < D / 2; ++d)
+        w[u][d] = h < heads ? *reinterpret_cast<const uint32_t*>(src + (size_t)h * A + 2 * d) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < B; ++u) {
+      const int h = h0 + 4 * u;
+      if (h >= heads) break;                 // the same in every lane
+      uint32_t m = w[u][0] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int d = 1; d < D / 2; ++d) m = __vmaxu2(m, w[u][d] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      m = __reduce_max_sync(0xffffffffu, m);
+      // the row's power of two: largest value in [128, 256); not finite: zeros and a NaN factor
+      const bool bad = m >= 0x7F80u;
+      const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);
+      const float f = bad ? 0.f : exp_inverse(eb);
+      uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+      for (int d = 0; d < D / 2; ++d) {
+        const float y0 = bad ? 0.f : bf16lo(w[u][d]) * f, y1 = bad ? 0.f : bf16hi(w[u][d]) * f;
+        const uint32_t a = pack_e4m3(y0, y1);
+        float z0, z1;
+        e4m3_to_f32(a, z0, z1);
+        c0 |= a << (16 * d);
+        c1 |= pack_e4m3(y0 - z0, y1 - z1) << (16 * d);
+      }
+      const int hh = h / G, g = h - hh * G;
+      for (int bi = 0; bi < bpt; ++bi) {
+        const int col = (bi * hg_heads + hh) * G + g;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int row = t * Cfg<A, G>::C + col;
+          if constexpr (A == 128) {
+            *reinterpret_cast<uint32_t*>(&S.q[grp][row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4]) = t ? c1 : c0;
+          } else {
+            *reinterpret_cast<uint16_t*>(&S.q[grp][row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2]) =
+                (uint16_t)(t ? c1 : c0);
+          }
+        }
+        if (lane == 0) S.cf[grp][col] = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+      }
+    }
+  }
+}
+
+// Output dimension d of every head of the segment: the slots of a head joined,
+// o 2^(M - m) / l, written as the output or as this piece's part of it with m
+// and l.  2^(M - m) comes as two factors: for the smallest and the largest
+// exponents of value rows it is outside fp32's normal range.
+template <int A, int G>
+__device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, const Seg& s, int grp, uint32_t o_tmem,
+                          int hg_heads, bool whole, int slot_out) {
+  using X = Cfg<A, G>;
+  const int t = threadIdx.x & 127, warp = t >> 5, bpt = 8 / hg_heads, heads = hg_heads * G;
+  if (A == 64 && warp >= 2) return;          // rows 64 .. 127 repeat 0 .. 63
+  const uint32_t base = o_tmem + ((uint32_t)(warp * 32) << 16);
+  for (int hh = 0; hh < hg_heads; ++hh) {
+    float acc[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) acc[g] = 0.f;
+    for (int bi = 0; bi < bpt; ++bi) {
+      const int slot = bi * hg_heads + hh;
+      float o[X::SS];
+      const uint32_t at = base + slot * X::SS;
+      if constexpr (X::SS == 24) {
+        tmem_ld<16>(at, o);
+        tmem_ld<8>(at + 16, o + 16);
+      } else {
+        tmem_ld<X::SS>(at, o);
+      }
+      tmem_wait_ld();
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float f = S.sw[grp][slot * G + g];
+        acc[g] += ((o[g] + o[G + g] + o[2 * G + g]) * f) * (f * (1.f / S.sl[grp][hh * G + g]));
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int h = hh * G + g;
+      const float l = S.sl[grp][h];
+      if (whole) {
+        P.out[((size_t)s.tok * P.n_q_heads + (size_t)s.hg * heads + h) * A + t] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(acc[g]));
+      } else {
+        const size_t at = (size_t)slot_out * kMaxHeads + h;
+        W.acc[at * A + t] = acc[g];
+        if (t == 0) *reinterpret_cast<float2*>(W.ml + at * 2) = make_float2(S.sm[grp][h], l);
+      }
+    }
+  }
+}
+
+template <int A, int G>
+__device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, const Plan& plan, int grp, int hg_heads) {
+  using X = Cfg<A, G>;
+  const unsigned FULL = 0xffffffffu;
+  const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31, bar_id = 1 + grp;
+  const int slot = tid >> 4, tok = tid & 15, bpt = 8 / hg_heads, nhg = P.cache.n_kv_heads / hg_heads;
+  const int bi = slot / hg_heads;
+  const bool upper = lane & 16;
+  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  Seg s;
+  uint32_t n = 0;                            // tiles before this segment
+  for (int i = 0; it.next(s); ++i) {
+    if ((i & 1) != grp) {
+      n += s.nt;
+      continue;
+    }
+    load_query<A, G>(P, S, s, grp, hg_heads);
+    fence_proxy_async_smem();
+    named_bar(bar_id, 128);                  // cf
+    mbar_arrive(&S.q_full[grp]);
+    float f[G], m[G], M[G], l[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      f[g] = S.cf[grp][slot * G + g];
+      m[g] = M[g] = kNegInf;
+      l[g] = 0.f;
+    }
+    const uint32_t o_tmem = S.tmem + X::SB * X::NS + (i % X::OB) * X::NO;
+    const int first_key = P.window > 0 ? max(0, s.kv - P.window) : 0;
+    // The other group has read its last scores: the rings' phases that this one waits for next are then
+    // one ahead of the last completed ones (a parity cannot tell phases two apart).
+    bool fail = i > 0 && !wwait(P, S, &S.turn[grp], ((i - 1) >> 1) & 1), stop = false;
+    for (int j = 0; j < s.nt; ++j, ++n) {
+      const int sb = n % X::SB, es = n % X::ES, pb = n % X::PB;
+      const int pos = (s.fb + (s.t0 + j) * bpt + bi) * kBlockSize + tok;
+      const bool valid = pos < s.kv && pos >= first_key;
+      fail |= !wwait(P, S, &S.e_full[es], (n / X::ES) & 1);
+      const uint32_t kb = S.ex[es][0][tid], vb = S.ex[es][1][tid];
+      fail |= !wwait(P, S, &S.s_full[sb], (n / X::SB) & 1);
+      tc_fence_after();
+      float s0[2 * G], s1[2 * G];
+      const uint32_t at = S.tmem + lane_base + sb * X::NS + 2 * warp * G;
+      tmem_ld<2 * G>(at, s0);
+      tmem_ld<2 * G>(at + X::C, s1);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.s_empty[sb]);
+        mbar_arrive(&S.e_empty[es]);
+        if (j == s.nt - 1) mbar_arrive(&S.turn[grp ^ 1]);
+      }
+      const float fk = exp_scale(kb), ev = vb == kExpNan ? __uint_as_float(0x7FC00000u) : (float)((int)vb - 127);
+      float x[G];
+      bool grow = false;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        x[g] = valid ? (upper ? s0[G + g] + s1[G + g] : s0[g] + s1[g]) * (f[g] * fk) : kNegInf;
+        grow |= x[g] > m[g] + kLazyP || x[g] + ev > M[g] + kLazyW;
+      }
+      bool need = false;
+      if (__any_sync(FULL, grow)) {
+        // the slot's exact maxima; the references move where they would be exceeded
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float mx = x[g], tx = x[g] + ev;
+#pragma unroll
+          for (int off = 8; off > 0; off >>= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+            tx = fmaxf(tx, __shfl_xor_sync(FULL, tx, off));
+          }
+          if (mx > m[g] + kLazyP) {
+            l[g] *= ex2(m[g] - mx);
+            m[g] = mx;
+          }
+          float a = 1.f;
+          if (tx > M[g] + kLazyW) {
+            a = ex2(M[g] - tx);
+            M[g] = tx;
+            need = true;
+          }
+          if (tok == 0) S.alpha[grp][n & 1][slot * G + g] = a;
+        }
+      } else if (tok < G) {
+        S.alpha[grp][n & 1][slot * G + tok] = 1.f;
+      }
+      if (named_bar_or(bar_id, 128, (need && j > 0) || fail || S.abort)) {
+        if (named_bar_or(bar_id, 128, fail || S.abort)) {
+          stop = true;
+          break;
+        }
+        // O times the factors, once the products before this tile have landed
+        fail |= !wwait(P, S, &S.pv_done[(n - 1) % X::PB], ((n - 1) / X::PB) & 1);
+        tc_fence_after();
+        if (!fail) {
+#pragma unroll 1
+          for (int sl = 0; sl < 8; ++sl) {
+            const uint32_t oc = o_tmem + lane_base + sl * X::SS;
+#pragma unroll
+            for (int c = 0; c < X::SS / 8; ++c) {
+              float o[8];
+              tmem_ld8(oc + 8 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 8; ++u) o[u] *= S.alpha[grp][n & 1][sl * G + (8 * c + u) % G];
+              tmem_st8(oc + 8 * c, o);
+            }
+          }
+          tmem_wait_st();
+        }
+      }
+      // weights: three e5m2 terms; p for the sum
+      uint32_t b0[(G + 1) / 2], b1[(G + 1) / 2], b2[(G + 1) / 2];
+#pragma unroll
+      for (int g = 0; g < G; g += 2) {
+        float w[2] = {0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 2 && g + u < G; ++u) {
+          if (valid) {
+            l[g + u] += ex2(x[g + u] - m[g + u]);
+            w[u] = ex2(x[g + u] + ev - M[g + u] + kWeightBits);
+          }
+        }
+        uint32_t h, r1, r2;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(w[1]), "f"(w[0]));
+        b0[g / 2] = h & 0xFF00FF00u;                // e5m2 is the top byte of a half: its first 3 bits
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(h), "r"(b0[g / 2]));
+        b1[g / 2] = r1 & 0xFF00FF00u;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r2) : "r"(r1), "r"(b1[g / 2]));
+        uint16_t c;
+        asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(r2));
+        b2[g / 2] = c;
+      }
+      // the buffer is free once the products of tile n - PB have landed
+      fail |= !wwait(P, S, &S.pv_done[pb], ((n / X::PB) & 1) ^ 1);
+      uint8_t* pp = S.p[pb] + (slot >> 1) * (64 * X::SS) + (slot & 1) * 128 + tok;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int sh = (g & 1) ? 24 : 8, sh2 = (g & 1) ? 8 : 0;
+#pragma unroll
+        for (int t = 0; t < 3; ++t) {
+          const int row = (slot & 1) * X::SS + t * G + g;
+          pp[(row >> 3) * 256 + (row & 7) * 16] =
+              (uint8_t)(t == 0 ? b0[g / 2] >> sh : t == 1 ? b1[g / 2] >> sh : b2[g / 2] >> sh2);
+        }
+      }
+      // rows that the request does not have hold whatever the cache had: 0 * NaN must not reach O
+      if (!valid) {
+        const int st = n % X::VS;
+        if (mbar_wait(&S.v_full[st], (n / X::VS) & 1)) {
+#pragma unroll
+          for (int c = 0; c < A / 16; ++c) *reinterpret_cast<uint4*>(&S.v[st][tid * A + c * 16]) = make_uint4(0, 0, 0, 0);
+        } else {
+          set_error(P.err, CB_DEVERR_TIMEOUT);
+          S.abort = 1;
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[pb]);
+    }
+    if (stop) break;
+    // the segment's sums; then the heads' and the slots' factors
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) l[g] += __shfl_xor_sync(FULL, l[g], off);
+      if (tok == 0) {
+        S.sl[grp][slot * G + g] = l[g];
+        S.sm[grp][slot * G + g] = m[g];
+        S.sw[grp][slot * G + g] = M[g];
+      }
+    }
+    fail |= !wwait(P, S, &S.o_full[i % X::OB], (i / X::OB) & 1);
+    if (named_bar_or(bar_id, 128, fail || S.abort)) break;
+    tc_fence_after();
+    float hm = kNegInf, hl = 0.f, hw = 0.f;
+    if (tid < X::C) {
+      const int head = (tid / G) % hg_heads, g = tid % G;
+      for (int b = 0; b < bpt; ++b) hm = fmaxf(hm, S.sm[grp][(b * hg_heads + head) * G + g]);
+      for (int b = 0; b < bpt; ++b) {
+        const int c = (b * hg_heads + head) * G + g;
+        if (S.sm[grp][c] != kNegInf) hl += S.sl[grp][c] * ex2(S.sm[grp][c] - hm);
+        // a slot without keys adds nothing; one whose sum is NaN passes it on
+        else if (S.sl[grp][c] != 0.f) hl += S.sl[grp][c];
+      }
+      hw = S.sw[grp][tid] == kNegInf ? (S.sl[grp][tid] != 0.f ? 1.f : 0.f) : ex2(0.5f * (S.sw[grp][tid] - kWeightBits - hm));
+    }
+    named_bar(bar_id, 128);
+    if (tid < X::C) {
+      S.sw[grp][tid] = hw;
+      if (tid < hg_heads * G) {
+        S.sl[grp][tid] = hl;
+        S.sm[grp][tid] = hm;
+      }
+    }
+    named_bar(bar_id, 128);
+    // a range's first segment that began before it is piece 2b, any other one that is cut piece 2b + 1
+    write_out<A, G>(P, W, S, s, grp, o_tmem, hg_heads, s.nt == s.tiles, 2 * (int)blockIdx.x + (s.t0 > 0 ? 0 : 1));
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.o_free[i % X::OB]);
+  }
+}
+
+template <int A, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_fp8_kernel(const Fp8Step P, const Fp8Partials W, const int hg_heads, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+  using X = Cfg<A, G>;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<A, G>& S = *reinterpret_cast<Smem<A, G>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* pre = reinterpret_cast<int*>(&S + 1);
+  int *kv = pre + P.n_reqs + 1, *tok = kv + P.n_reqs;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < X::KS; ++i) {
+      mbar_init(&S.k_full[i], 1);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 1);
+      mbar_init(&S.v_empty[i], 1);
+    }
+    for (int i = 0; i < X::ES; ++i) {
+      mbar_init(&S.e_full[i], 1);
+      mbar_init(&S.e_empty[i], 4);
+    }
+    for (int i = 0; i < X::SB; ++i) {
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.s_empty[i], 4);
+    }
+    for (int i = 0; i < X::PB; ++i) {
+      mbar_init(&S.p_full[i], 4);
+      mbar_init(&S.pv_done[i], 1);
+    }
+    for (int i = 0; i < X::OB; ++i) {
+      mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.o_free[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.q_full[i], 128);
+      mbar_init(&S.turn[i], 4);
+      mbar_init(&S.drain[i], 1);
+    }
+    S.abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+  }
+  if (warp == 10) {
+    tmem_alloc(&S.tmem, X::kTmem);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  for (int i = threadIdx.x; i < (int)sizeof(S.p) / 16; i += kThreads)
+    reinterpret_cast<uint4*>(S.p)[i] = make_uint4(0, 0, 0, 0);       // the other slot's rows and the padding stay zero
+  fence_proxy_async_smem();
+  make_plan<A, G>(P, W, S, pre, kv, tok, hg_heads);
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Plan plan{pre, kv, tok};
+  const int nhg = P.cache.n_kv_heads / hg_heads;
+  if (warp < 8)
+    softmax_group<A, G>(P, W, S, plan, warp >> 2, hg_heads);
+  else if (warp == 8)
+    load_tiles<A, G, true>(P, &kmap, S, plan, hg_heads);
+  else if (warp == 9)
+    load_tiles<A, G, false>(P, &vmap, S, plan, hg_heads);
+  else if (warp == 10)
+    issue_s<A, G>(P, S, plan, nhg);
+  else
+    issue_pv<A, G>(P, S, plan, nhg);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 10) {
+    tc_fence_after();
+    tmem_dealloc(S.tmem, X::kTmem);
+  }
+}
+
+// ---------------------------------------------------------------- joining the pieces
+// For every sequence cut between CTAs and every query head of it: M = max m_i,
+// W_i = 2^(m_i - M) l_i, out = sum W_i o_i / sum W_i, in the pieces' order.
+// A warp takes a (sequence, head), lane = A / 32 dimensions; where there are
+// fewer of those than CTAs, a CTA does, its warps taking the pieces in turn.
+constexpr int kJoinThreads = 256;
+template <int A>
+__global__ void __launch_bounds__(kJoinThreads) join_fp8_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int hg_heads) {
+  constexpr int D = A / 32, NW = kJoinThreads / 32;
+  __shared__ int owner[kMaxDecodeGrid];
+  __shared__ int n_owner;
+  __shared__ float red[NW][A];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = hg_heads * (P.n_q_heads / P.cache.n_kv_heads);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    int n = 0;
+    for (int b0 = 0; b0 < ctas; b0 += 32) {
+      const int b = b0 + lane;
+      const bool has = b < ctas && W.rec[b].n > 1;
+      const unsigned mask = __ballot_sync(0xffffffffu, has);
+      if (has) owner[n + __popc(mask & ((1u << lane) - 1))] = b;
+      n += __popc(mask);
+    }
+    if (lane == 0) n_owner = n;
+  }
+  __syncthreads();
+  const int tasks = n_owner * heads;
+  const bool by_cta = tasks <= (int)gridDim.x;
+  const int step = by_cta ? NW : 1, first = by_cta ? warp : 0;
+  for (int task = by_cta ? blockIdx.x : blockIdx.x * NW + warp; task < tasks; task += by_cta ? gridDim.x : gridDim.x * NW) {
+    const int b = owner[task / heads], h = task % heads;
+    const Fp8Rec rec = W.rec[b];
+    auto piece = [&](int i) { return (size_t)(i == 0 ? 2 * b + 1 : 2 * (b + i)) * kMaxHeads + h; };
+    float M = kNegInf, L = 0.f;
+    for (int i = lane; i < rec.n; i += 32) M = fmaxf(M, W.ml[piece(i) * 2]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int i = lane; i < rec.n; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(i) * 2);
+      L += ml.x == kNegInf ? ml.y : ex2(ml.x - M) * ml.y;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    float o[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] = 0.f;
+    for (int i0 = first; i0 < rec.n; i0 += 8 * step) {
+      float y[8][D], w[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * step;
+        w[u] = 0.f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) y[u][d] = 0.f;
+        if (i < rec.n) {
+          const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(i) * 2);
+          const float* src = W.acc + piece(i) * A + lane * D;
+          w[u] = ml.x == kNegInf ? ml.y : ex2(ml.x - M) * ml.y;      // -inf: a piece of NaNs only
+          if constexpr (D == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            y[u][0] = v.x, y[u][1] = v.y, y[u][2] = v.z, y[u][3] = v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            y[u][0] = v.x, y[u][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] += w[u] * y[u][d];
+    }
+    if (by_cta) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) red[warp][lane * D + d] = o[d];
+      __syncthreads();
+      if (warp == 0) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          o[d] = 0.f;
+          for (int w = 0; w < NW; ++w) o[d] += red[w][lane * D + d];
+        }
+      }
+    }
+    if (!by_cta || warp == 0) {
+      const int t = __ldg(P.cu_q_lens + rec.r);
+      uint16_t* dst = P.out + ((size_t)t * P.n_q_heads + (size_t)rec.hg * heads + h) * A + lane * D;
+#pragma unroll
+      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d] / L, o[d + 1] / L);
+    }
+    if (by_cta) __syncthreads();
+  }
+}
+
+template <int A, int G>
+size_t smem_bytes(int n_reqs) {
+  return 1024 + sizeof(Smem<A, G>) + (size_t)(3 * n_reqs + 1) * 4;
+}
+constexpr int kSmemLimit = 232448;
+static_assert(sizeof(Smem<128, 8>) + 1024 + (3 * kMaxReqs + 1) * 4 <= kSmemLimit, "shared memory");
+static_assert(sizeof(Smem<128, 4>) + 1024 + (3 * kMaxReqs + 1) * 4 <= kSmemLimit, "shared memory");
+
+template <int A, int G>
+cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
+  int hg = 8;
+  while (s.cache.n_kv_heads % hg) hg >>= 1;
+  CUtensorMap km, vm;
+  const long long rows = (long long)s.cache.num_blocks * s.cache.n_kv_heads * kBlockSize;
+  if (!encode_byte_rows(&km, s.cache.k, rows, A, hg * kBlockSize) || !encode_byte_rows(&vm, s.cache.v, rows, A, hg * kBlockSize))
+    return cudaErrorInvalidValue;
+  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(decode_fp8_kernel<A, G>), kSmemLimit);
+  if (e != cudaSuccess) return e;
+  decode_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A, G>(s.n_reqs), stream>>>(s, w, hg, km, vm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(4 * grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its CTAs are placed while the last pieces are written
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_fp8_kernel<A>, s, w, grid, hg);
+}
+
+}  // namespace
+
+bool fp8_decode_shape(int head_dim, int group) { return (head_dim == 64 || head_dim == 128) && group <= 8; }
+
+size_t fp8_partials_bytes(int head_dim) {
+  return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * kMaxHeads * (2 + head_dim) * 4;
+}
+Fp8Partials fp8_partials(void* workspace) {
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  Fp8Partials w;
+  w.rec = reinterpret_cast<Fp8Rec*>(p);
+  w.ml = reinterpret_cast<float*>(p + sizeof(Fp8Rec) * kMaxDecodeGrid);
+  w.acc = w.ml + (size_t)2 * kMaxDecodeGrid * kMaxHeads * 2;
+  return w;
+}
+
+cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
+  const int a = s.cache.head_dim, g = s.n_q_heads / s.cache.n_kv_heads;
+#define CB_CASE(A_, G_) \
+  if (a == A_ && g == G_) return launch_t<A_, G_>(s, w, grid, stream);
+  CB_CASE(128, 1)
+  CB_CASE(128, 2)
+  CB_CASE(128, 4)
+  CB_CASE(128, 8)
+  CB_CASE(64, 1)
+  CB_CASE(64, 2)
+  CB_CASE(64, 4)
+  CB_CASE(64, 8)
+#undef CB_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace cb

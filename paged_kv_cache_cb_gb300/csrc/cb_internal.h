@@ -144,12 +144,32 @@ cudaError_t launch_gather_fp8(const int64_t* slots, int n_rows, const Fp8Cache& 
                               unsigned int* err, cudaStream_t stream);
 cudaError_t launch_copy_blocks_fp8(const int32_t* pairs, int n_pairs, const Fp8Cache& c, unsigned int* err,
                                    cudaStream_t stream);
-// Attention of the step's requests; `launches` receives the kernels enqueued.
-cudaError_t launch_attention_fp8(const Fp8Step& s, cudaStream_t stream, int* launches);
+// A piece of one sequence's softmax: which CTA's range it starts in, and how
+// many CTAs' ranges it reaches (n = 0: no sequence starts there and goes on).
+struct Fp8Rec {
+  int r, hg, n, pad;
+};
+// Workspace of the single-token attention: per CTA two partial results (its
+// first and its last piece), [64 heads][A] values and [64][2] (max, sum).
+struct Fp8Partials {
+  Fp8Rec* rec;                  // [kMaxDecodeGrid]
+  float* ml;                    // [2 * kMaxDecodeGrid][64][2]
+  float* acc;                   // [2 * kMaxDecodeGrid][64][A]
+};
+size_t fp8_partials_bytes(int head_dim);
+Fp8Partials fp8_partials(void* workspace);
+bool fp8_decode_shape(int head_dim, int group);
+// The requests with one new token, on `grid` CTAs (at most one per SM), and the join of their pieces.
+cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream);
+// The other requests (all of them with singles = true).
+cudaError_t launch_attention_fp8_simple(const Fp8Step& s, bool singles, cudaStream_t stream);
 
 // Library state that the entry points of other files use (cb_api.cu).
 unsigned int* stream_error_word(cudaStream_t stream, int* rc);   // nullptr: return *rc
 void set_last_launches(int n);
+bool device_sms(int* n);
+// Tensor map of a matrix of `rows` rows of row_bytes bytes (64 or 128, one swizzle span), boxes of box_rows whole rows.
+bool encode_byte_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows);
 bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size);
 
 }  // namespace cb
