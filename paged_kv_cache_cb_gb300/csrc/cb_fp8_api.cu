@@ -11,6 +11,8 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
+
 // The cache arguments shared by every entry point; false: CB_EINVAL.
 bool cache_of(Fp8Cache* c, const void* k, const void* v, const void* ke, const void* ve, int num_blocks, int n_kv_heads,
               int head_dim, int block_size) {
@@ -87,8 +89,9 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
     launches += 2;
   }
   if (max_q_len > 1 || !tiles) {
-    if (launch_attention_fp8_simple(s, !tiles, st) != cudaSuccess) return CB_ECUDA;
-    ++launches;
+    uint8_t* ws = static_cast<uint8_t*>(workspace) + (tiles ? align_up(fp8_partials_bytes(head_dim)) : 0);
+    if (launch_chunk_fp8(s, fp8_chunk_partials(ws), tiles ? 2 : 1, sms, st) != cudaSuccess) return CB_ECUDA;
+    launches += 2;
   }
   set_last_launches(launches);
   return CB_OK;
@@ -163,7 +166,9 @@ size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q
   if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
       !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
-  return fp8_partials_bytes(head_dim);
+  const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
+  return (tiles ? align_up(fp8_partials_bytes(head_dim)) : 0) +
+         (max_q_len > 1 || !tiles ? fp8_chunk_partials_bytes(head_dim) : 0);
 }
 
 int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,

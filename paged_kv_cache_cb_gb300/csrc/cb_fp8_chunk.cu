@@ -1,0 +1,840 @@
+// Attention of several new tokens per request over the 8-bit KV cache (format:
+// cb_fp8.cuh) on the tensor cores.
+//
+// Mathematics.  For a row (token at position p, query head h) with visible keys
+// j <= p (and j > p - W under a window):
+//     x_j = scale log2(e) q . K_j,   p_j = 2^(x_j - m),   out = sum p_j V_j / sum p_j
+// with m a running maximum that moves only when a score passes it by 8.  K_j and
+// V_j are the cache's rows as bf16, which is exact (the rows' scales are powers of
+// two), so the two products are bf16 x bf16 with fp32 sums; p_j is rounded to bf16
+// for the second one (2^-8 relative, the type of the cache's own 16-bit form),
+// the sum of p_j is taken before that rounding.
+// Here K and V are converted (the single-token kernel multiplies the 8-bit values
+// as they are): every tile serves 256 query rows, so the conversion is one
+// operation in 256, while the 8-bit products would need two terms of q and three
+// of p each, more tensor work than the bf16 products.
+//
+// Tiles.  An item is (request, KV head, 2 TOK tokens), TOK = 128 / G: two query
+// tiles of 128 rows (row i = token i / G, head i % G) that share the keys, in
+// tiles of 128.  Tensor memory: S_A | P_A, S_B | P_B (P over the first half of its
+// own S), O_A, O_B.  The tensor pipe alternates PV_A(j-1) S_A(j), PV_B(j-1)
+// S_B(j): one query tile's softmax runs under the other's products.  P is handed
+// over in two halves of 64 keys, so the products start while the second half is
+// computed.  An item of at most TOK tokens has one query tile.
+//
+// Work.  All items' key tiles, laid end to end, are cut into one equal range per
+// CTA (one CTA per SM); an item cut at a range's end leaves (m, l, o) per piece
+// and a second kernel joins them.  Where whole items, dealt to the CTAs in turn,
+// end sooner than the cut ranges and their joining, they stay whole.
+//
+// Warps: 0-3 and 4-7 softmax of tiles A and B (thread = row; the row's 128
+// scores stay in registers, one read of tensor memory), 8-11 convert K and V from
+// global memory (loads a step ahead in registers) to bf16 in shared memory, 12
+// issues the products, 13 loads Q.  Every wait is bounded.
+#include <algorithm>
+
+#include "cb_decode_item.cuh"
+#include "cb_fp8.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRows = 256;             // rows of an item (two query tiles)
+constexpr int kMinTiles = 4;           // key tiles per CTA below which a step uses fewer CTAs
+constexpr int kCutTiles = 7;           // what cutting items costs, in key tiles' time (partial results and their joining)
+constexpr int kSmemLimit = 232448;
+
+template <int A>
+struct alignas(1024) Smem {
+  static constexpr int H = A / 64;     // 64-dimension halves of 128-byte rows
+  uint8_t q[2][H][128][128];
+  uint8_t k[2][H][128][128];
+  uint8_t v[2][H][128][128];
+  uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain;
+  uint32_t v_nan[2][4];                // rows of the V stage that stand for NaNs (stored as zeros)
+  long long scan[16], tiles, u0, u1;
+  int iscan[16], items, longest, whole, eff;
+  uint32_t tmem;
+  volatile int abort;
+};
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+template <class S>
+__device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  if (!ok) {
+    set_error(P.err, CB_DEVERR_TIMEOUT);
+    sm.abort = 1;
+  }
+  return ok;
+}
+
+// ---------------------------------------------------------------- work
+// Key tiles [first, end) of the `pair`-th 2 TOK tokens of a request.
+__device__ __forceinline__ int pair_first(int ctx, int pair, int tok2, int window) {
+  return window > 0 ? max(0, ctx + pair * tok2 - window + 1) / kTileN : 0;
+}
+__device__ __forceinline__ int pair_end(int ctx, int q_len, int pair, int tok2) {
+  return (int)(((long long)ctx + min((long long)q_len, (pair + 1LL) * tok2) + kTileN - 1) / kTileN);
+}
+
+// (q0, q_len, ctx) of request r if it is one of this kernel's; q_len 0 otherwise.
+__device__ __forceinline__ int3 request(const Fp8Step& P, int r, int min_q, bool report) {
+  const int q0 = __ldg(P.cu_q_lens + r), q1 = __ldg(P.cu_q_lens + r + 1), ctx = __ldg(P.ctx_lens + r);
+  const long long n = (long long)q1 - q0, kv = (long long)ctx + n;
+  if (q0 >= 0 && q1 <= P.n_tokens && n >= 0 && n < min_q) return make_int3(0, 0, 0);
+  if (n < 0 || ctx < 0 || q0 < 0 || q1 > P.n_tokens || n > P.max_q_len || kv > P.max_kv_len ||
+      (kv + kBlockSize - 1) / kBlockSize > P.max_blocks_per_seq) {
+    if (report) set_error(P.err, CB_DEVERR_BADLEN);
+    return make_int3(0, 0, 0);
+  }
+  return make_int3(q0, (int)n, ctx);
+}
+
+// An item, and the piece [a, b) of its key tiles [first, end).
+struct Item {
+  int r, g, pair, q0, q_len, ctx, tok_lo, tok_hi, first, end, a, b, sides;
+};
+
+// The CTA's pieces in order.  Items of a request: pairs from the last (most
+// keys) down, KV heads inside.
+template <int TOK>
+struct ItemIter {
+  const Fp8Step& P;
+  const long long* tpre;               // tiles before request r
+  const int* ipre;                     // items before request r
+  int min_q, whole, step, index, n_items;   // whole items: index, index + step, ...
+  long long u, u1;                     // cut ranges
+  int3 rq;
+  int r, pair, g, j0;                  // the next piece's place (cut ranges)
+  bool fresh = true;
+  template <class S>
+  __device__ ItemIter(const Fp8Step& p, const S& s, const long long* tp, const int* ip, int mq)
+      : P(p), tpre(tp), ipre(ip), min_q(mq), whole(s.whole), step(s.eff), index(blockIdx.x), n_items(s.items), u(s.u0), u1(s.u1) {}
+  template <class T>
+  __device__ int find(const T* pre, T x) const {
+    int lo = 0, hi = P.n_reqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+  __device__ void fill(Item& I) const {
+    I.r = r;
+    I.g = g;
+    I.pair = pair;
+    I.q0 = rq.x;
+    I.q_len = rq.y;
+    I.ctx = rq.z;
+    I.tok_lo = pair * 2 * TOK;
+    I.tok_hi = min(rq.y, I.tok_lo + 2 * TOK);
+    I.sides = I.tok_hi - I.tok_lo > TOK ? 2 : 1;
+    I.first = pair_first(rq.z, pair, 2 * TOK, P.window);
+    I.end = pair_end(rq.z, rq.y, pair, 2 * TOK);
+  }
+  __device__ bool next(Item& I) {
+    const int Hkv = P.cache.n_kv_heads;
+    if (whole) {
+      if (index >= n_items) return false;
+      r = find(ipre, index);
+      rq = request(P, r, min_q, false);
+      const int rem = index - ipre[r], pairs = (rq.y + 2 * TOK - 1) / (2 * TOK);
+      pair = pairs - 1 - rem / Hkv;
+      g = rem % Hkv;
+      fill(I);
+      I.a = I.first;
+      I.b = I.end;
+      index += step;
+      return true;
+    }
+    if (u >= u1) return false;
+    if (fresh) {
+      fresh = false;
+      r = find(tpre, u);
+      rq = request(P, r, min_q, false);
+      long long off = u - tpre[r];
+      for (pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1; pair > 0; --pair) {
+        const long long t = (long long)(pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window)) * Hkv;
+        if (off < t) break;
+        off -= t;
+      }
+      const int t = pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window);
+      g = (int)(off / t);
+      j0 = (int)(off % t);
+    }
+    fill(I);
+    I.a = I.first + j0;
+    I.b = (int)min((long long)I.end, I.a + (u1 - u));
+    u += I.b - I.a;
+    j0 = 0;
+    if (++g == Hkv) {
+      g = 0;
+      if (--pair < 0 && u < u1) {
+        do {
+          ++r;
+        } while (tpre[r + 1] <= u);
+        rq = request(P, r, min_q, false);
+        pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1;
+      }
+    }
+    return true;
+  }
+};
+
+// The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
+__device__ __forceinline__ int cta_of(long long u, long long total, int eff) { return (int)(((u + 1) * eff - 1) / total); }
+
+// All threads; ends with __syncthreads().
+template <int A, int TOK>
+__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, long long* tpre, int* ipre, int min_q) {
+  const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, Hkv = P.cache.n_kv_heads;
+  if (tid == 0) S.longest = 0;
+  for (int r = tid; r < n; r += kThreads) {
+    const int3 q = request(P, r, min_q, blockIdx.x == 0);
+    ipre[r] = (q.y + 2 * TOK - 1) / (2 * TOK);         // its pairs
+    tpre[r] = ((long long)q.z << 32) | (unsigned)q.y;  // its lengths
+  }
+  __syncthreads();
+  for (int r = wid; r < n; r += kThreads / 32) {       // a warp per request with pairs
+    const int pairs = ipre[r];
+    if (pairs == 0) {
+      if (lane == 0) tpre[r] = 0;
+      continue;
+    }
+    const int ctx = (int)(tpre[r] >> 32), q_len = (int)(tpre[r] & 0xFFFFFFFF);
+    long long t = 0;
+    int mx = 0;
+    for (int p = lane; p < pairs; p += 32) {
+      const int x = pair_end(ctx, q_len, p, 2 * TOK) - pair_first(ctx, p, 2 * TOK, P.window);
+      t += x;
+      mx = max(mx, x);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    __syncwarp();
+    if (lane == 0) {
+      tpre[r] = t * Hkv;
+      ipre[r] = pairs * Hkv;
+      atomicMax(&S.longest, mx);
+    }
+  }
+  __syncthreads();
+  // exclusive prefix sums of both
+  const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
+  long long t_own = 0;
+  int i_own = 0;
+  for (int r = lo; r < hi; ++r) {
+    t_own += tpre[r];
+    i_own += ipre[r];
+  }
+  long long t_incl = t_own;
+  int i_incl = i_own;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, t_incl, off);
+    const int y = __shfl_up_sync(0xffffffffu, i_incl, off);
+    if (lane >= off) {
+      t_incl += x;
+      i_incl += y;
+    }
+  }
+  if (lane == 31) {
+    S.scan[wid] = t_incl;
+    S.iscan[wid] = i_incl;
+  }
+  __syncthreads();
+  long long total = 0, t_run = t_incl - t_own;
+  int items = 0, i_run = i_incl - i_own;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    total += S.scan[w];
+    items += S.iscan[w];
+    if (w < wid) {
+      t_run += S.scan[w];
+      i_run += S.iscan[w];
+    }
+  }
+  for (int r = lo; r < hi; ++r) {
+    const long long t = tpre[r];
+    const int i = ipre[r];
+    tpre[r] = t_run;
+    ipre[r] = i_run;
+    t_run += t;
+    i_run += i;
+  }
+  if (tid == 0) {
+    tpre[n] = total;
+    ipre[n] = items;
+    const int grid = gridDim.x, b = blockIdx.x;
+    const int eff = (int)max(1LL, min((long long)grid, (total + kMinTiles - 1) / kMinTiles));
+    S.tiles = total;
+    S.items = items;
+    S.whole = (long long)((items + grid - 1) / grid) * S.longest <= (total + grid - 1) / grid + kCutTiles;
+    S.eff = S.whole ? grid : eff;
+    S.u0 = b < eff ? total * b / eff : total;
+    S.u1 = b < eff ? total * (b + 1) / eff : total;
+  }
+  __syncthreads();
+  if (tid == 0) {                      // the item that starts in this range and goes on after it
+    Fp8Rec rec = {0, 0, 0, 0};
+    if (!S.whole && S.u1 > S.u0 && S.u1 < S.tiles) {
+      ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+      it.u = S.u1 - 1;
+      Item I;
+      it.next(I);
+      const long long start = S.u1 - 1 - (I.a - I.first);
+      const long long end = start + (I.end - I.first);
+      if (start >= S.u0 && end > S.u1)
+        rec = {I.r, I.g, cta_of(end - 1, S.tiles, S.eff) - (int)blockIdx.x + 1, I.pair};
+    }
+    W.rec[blockIdx.x] = rec;
+  }
+}
+
+// ---------------------------------------------------------------- conversion (warps 8-11)
+// 16 e4m3 -> 16 bf16 times 2^e.  Each byte is sign-extended to 16 bits and moved
+// up by 4: sign, zeros, the 4 exponent and 3 fraction bits in bf16's places, a
+// bf16 2^-120 times too small (also for e4m3's subnormals, which become bf16's);
+// one multiplication by 2^(120 + e) is exact.  Bytes b > 134 (e > 7) need a second.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t permute(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
+  return r;
+}
+__device__ __forceinline__ void widen16(const uint4& x, uint32_t b, uint32_t (&o)[8]) {
+  const uint32_t f1 = (min(b, 134u) + 120u) << 7, m1 = f1 | (f1 << 16);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // bytes 0, 1 (then 2, 3) as two sign-extended halves: selector bit 3 repeats a byte's sign
+    const uint32_t lo = permute<0x9180>(w[i]), hi = permute<0xB3A2>(w[i]);
+    o[2 * i] = mul_bf16x2((lo << 4) & 0x87F087F0u, m1);
+    o[2 * i + 1] = mul_bf16x2((hi << 4) & 0x87F087F0u, m1);
+  }
+  if (b > 134u) {
+    const uint32_t f2 = b == kExpNan ? 0x7FC0u : (b - 134u + 127u) << 7, m2 = f2 | (f2 << 16);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], m2);
+  }
+}
+
+// A tile's rows on their way: this lane's 16-byte pieces, and the exponent of
+// row 32 warp + lane.
+template <int A>
+struct Flight {
+  static constexpr int N = A / 16;     // pieces per lane: 32 rows x A bytes per warp
+  uint4 x[N];
+  uint32_t e;
+};
+
+template <int A, int TOK>
+__device__ void convert(const Fp8Step& P, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
+  constexpr int N = Flight<A>::N, LR = A / 16, RP = 32 / LR;   // lanes per row, rows per piece step
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, Hkv = P.cache.n_kv_heads;
+  const int col = lane % LR, rsub = lane / LR;
+  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+  Item I;
+  uint32_t n = 0;
+  while (it.next(I)) {
+    const int kv_hi = I.ctx + I.tok_hi, nblk = (kv_hi + kBlockSize - 1) / kBlockSize;
+    const int key_lo = P.window > 0 ? max(0, I.ctx + I.tok_lo - P.window + 1) : 0, blk_lo = key_lo / kBlockSize;
+    // lane 2 t + i: entry of block 2 warp + i of tile base + t; 16 tiles at a time, the next 16 on their way
+    auto entry = [&](int base) {
+      const int blk = (base + (lane >> 1)) * 8 + 2 * warp + (lane & 1);
+      if (blk < blk_lo || blk >= nblk || base + (lane >> 1) >= I.b) return -2;
+      const int e = __ldg(P.block_tables + (size_t)I.r * P.max_blocks_per_seq + blk);
+      return e < 0 || e >= P.cache.num_blocks ? -1 : e;
+    };
+    int cur = entry(I.a), nxt = entry(I.a + 16);
+    if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);    // its rows count as zeros
+    auto load = [&](Flight<A>& f, const uint8_t* cache, const uint8_t* exps, int t) {
+      const int b0 = __shfl_sync(FULL, cur, 2 * t), b1 = __shfl_sync(FULL, cur, 2 * t + 1);
+      const int eb = lane < 16 ? b0 : b1;
+      f.e = eb >= 0 ? __ldg(exps + ((size_t)eb * Hkv + I.g) * kBlockSize + (lane & 15)) : 1u;
+#pragma unroll
+      for (int p = 0; p < N; ++p) {
+        const int row = p * RP + rsub, b = row < 16 ? b0 : b1;
+        f.x[p] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + (((size_t)b * Hkv + I.g) * kBlockSize + (row & 15)) * A) + col)
+                        : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto store = [&](const Flight<A>& f, uint8_t (*dst)[128][128], int key0, bool is_v, uint32_t st) {
+      if (is_v) {
+        // rows that no row of the item sees, and rows of NaNs: zeros (0 * NaN must not reach O); the
+        // latter are told to the softmax, which gives NaN to the rows that see them
+        const int key = key0 + 32 * warp + lane;
+        const unsigned bad = __ballot_sync(FULL, f.e == kExpNan && key >= key_lo && key < kv_hi);
+        if (lane == 0) S.v_nan[st][warp] = bad;
+      }
+#pragma unroll
+      for (int p = 0; p < N; ++p) {
+        const int row = p * RP + rsub, r = 32 * warp + row;
+        const uint32_t e = __shfl_sync(FULL, f.e, row);
+        uint32_t o[8];
+        widen16(f.x[p], e, o);
+        if (is_v && (e == kExpNan || key0 + r < key_lo || key0 + r >= kv_hi)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = 0;
+        }
+        // 16 dimensions: two 16-byte chunks of the half's 128-byte row; lanes of the second half store them
+        // in the other order (the halves share banks)
+        const int c = (col & 3) * 2, half = A == 128 ? col >> 2 : 0, sw = half;
+        uint8_t* d = &dst[half][r][0];
+        const uint4 x0 = make_uint4(o[0], o[1], o[2], o[3]), x1 = make_uint4(o[4], o[5], o[6], o[7]);
+        *reinterpret_cast<uint4*>(d + (((c + sw) ^ (r & 7)) << 4)) = sw ? x1 : x0;
+        *reinterpret_cast<uint4*>(d + (((c + 1 - sw) ^ (r & 7)) << 4)) = sw ? x0 : x1;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    Flight<A> fk, fv;
+    load(fk, P.cache.k, P.cache.k_exps, 0);
+    bool ok = true;
+    for (int j = I.a; j < I.b; ++j, ++n) {
+      const int t = (j - I.a) & 15;
+      const uint32_t st = n & 1, ph = (n >> 1) & 1;
+      load(fv, P.cache.v, P.cache.v_exps, t);
+      ok = wwait(P, S, &S.k_empty[st], ph ^ 1);
+      if (!ok) break;
+      store(fk, S.k[st], j * kTileN, false, st);
+      if (lane == 0) mbar_arrive(&S.k_full[st]);
+      if (j + 1 < I.b) {
+        if (t == 15) {
+          cur = nxt;
+          nxt = entry(j + 17);
+          if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);
+        }
+        load(fk, P.cache.k, P.cache.k_exps, (t + 1) & 15);
+      }
+      ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
+      if (!ok) break;
+      store(fv, S.v[st], j * kTileN, true, st);
+      if (lane == 0) mbar_arrive(&S.v_full[st]);
+    }
+    if (!ok) break;
+  }
+}
+
+// ---------------------------------------------------------------- Q (warp 13)
+template <int A, int G>
+__device__ void load_q(const Fp8Step& P, const CUtensorMap* qmap, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
+  constexpr int TOK = kTileM / G, H = A / 64;
+  const int lane = threadIdx.x & 31;
+  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+  Item I;
+  uint32_t n = 0;
+  bool ok = true;
+  for (; it.next(I); ++n) {
+    ok = wwait(P, S, &S.q_empty, (n & 1) ^ 1);
+    if (!ok) break;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&S.q_full, I.sides * H * 128 * 128);
+      for (int side = 0; side < I.sides; ++side)
+        for (int h = 0; h < H; ++h)
+          tma_load_3d(&S.q[side][h][0][0], qmap, h * 64, I.g * G, I.q0 + I.tok_lo + side * TOK, &S.q_full);
+    }
+    __syncwarp();
+  }
+  if (!ok && n > 0) mbar_wait(&S.q_full, (n - 1) & 1, 20000000ull);   // its last copy lands before the CTA exits
+}
+
+// ---------------------------------------------------------------- products (warp 12)
+template <int A, int TOK>
+__device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescO = idesc_bf16_f32(128, A, 1);
+  constexpr uint32_t kHalf = 128 * 128, kTile = (A / 64) * kHalf;
+  const uint64_t qd = smem_desc_sw128(smem_u32(S.q), 16, 1024), kd = smem_desc_sw128(smem_u32(S.k), 16, 1024);
+  const uint64_t vd = smem_desc_sw128(smem_u32(S.v), kHalf, 1024);
+  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+  Item I;
+  uint32_t n = 0, np[2] = {0, 0};      // key tiles before this item; products with P issued per side
+  uint32_t ni[2] = {0, 0};             // items per side
+  bool ok = true;
+  for (uint32_t i = 0; ok && it.next(I); ++i) {
+    ok = wwait(P, S, &S.q_full, i & 1);
+    const int len = I.b - I.a;
+    for (int j = 0; j <= len && ok; ++j) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        if (side >= I.sides || !ok) break;
+        const uint32_t s_t = S.tmem + side * 128, o_t = S.tmem + 256 + side * A;
+        if (j > 0) {                   // O += P V of the tile before
+          const uint32_t t = n + j - 1, st = t & 1;
+          ok = wwait(P, S, &S.v_full[st], (t >> 1) & 1);
+          if (ok && j == 1) ok = wwait(P, S, &S.o_free[side], (ni[side] & 1) ^ 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wwait(P, S, &S.p_full[side][h], np[side] & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                tc_mma_f16_ts(o_t, s_t + ks * 8, vd + (uint32_t)((st * kTile + ks * 16 * 128) >> 4), kIdescO, (j > 1 || ks > 0) ? 1u : 0u);
+              if (h == 1) {
+                if (side == I.sides - 1) tc_commit(&S.v_empty[st]);
+                if (j == len) tc_commit(&S.o_full[side]);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ++np[side];
+        }
+        if (j < len) {                 // S of this one
+          const uint32_t t = n + j, st = t & 1;
+          ok = wwait(P, S, &S.k_full[st], (t >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < A / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+              tc_mma_f16(s_t, qd + (uint32_t)((side * kTile + off) >> 4), kd + (uint32_t)((st * kTile + off) >> 4), kIdescS, ks > 0);
+            }
+            tc_commit(&S.s_full[side]);
+            if (side == I.sides - 1) {
+              tc_commit(&S.k_empty[st]);
+              if (j == len - 1) tc_commit(&S.q_empty);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    n += len;
+    ++ni[0];
+    if (I.sides == 2) ++ni[1];
+  }
+  if (!ok) S.abort = 1;
+  if (elect_one()) tc_commit(&S.drain);
+  __syncwarp();
+  mbar_wait(&S.drain, 0, 20000000ull);
+}
+
+// ---------------------------------------------------------------- softmax (warps 0-3, 4-7)
+template <int A, int G>
+__device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, const long long* tpre, const int* ipre, int min_q, int side) {
+  constexpr int TOK = kTileM / G;
+  const unsigned FULL = 0xffffffffu;
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
+  const uint32_t s_t = S.tmem + lane_base + side * 128, o_t = S.tmem + lane_base + 256 + side * A;
+  const float sl2 = P.scale_log2;
+  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+  Item I;
+  uint32_t n = 0, ns = 0, ni = 0;      // key tiles of all items, of this side's items; this side's items
+  while (it.next(I)) {
+    if (side >= I.sides) {
+      n += I.b - I.a;
+      continue;
+    }
+    const int ti = I.tok_lo + side * TOK + row / G;
+    const int pos = I.ctx + min(ti, I.tok_hi - 1);           // the last key this row sees
+    const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
+    const unsigned span = (unsigned)(pos - lo);              // key k is visible iff (unsigned)(k - lo) <= span
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    for (int j = I.a; j < I.b; ++j, ++n, ++ns) {
+      ok = wwait(P, S, &S.s_full[side], ns & 1);             // also: O holds every product before this tile
+      if (!ok) break;
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, reinterpret_cast<float (&)[32]>(s[32 * c]));
+      tmem_wait_ld();
+      const int key0 = j * kTileN;
+      const bool edge = key0 + kTileN - 1 > pos || key0 < lo;
+      if (__any_sync(FULL, edge)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if ((unsigned)(key0 + k - lo) > span) s[k] = kNegInf;
+      }
+      float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+      for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
+      const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * sl2;
+      const bool need = mt > m + 8.f;
+      float alpha = 1.f;
+      if (need) {
+        alpha = ex2(m - mt);
+        m = mt;
+      }
+      if (j > I.a && __any_sync(FULL, need)) {
+#pragma unroll 1
+        for (int c = 0; c < A / 8; ++c) {
+          float o[8];
+          tmem_ld8(o_t + c * 8, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) o[k] *= alpha;
+          tmem_st8(o_t + c * 8, o);
+        }
+      }
+      l *= alpha;
+      const float mr = m == kNegInf ? 0.f : m;               // a row that has seen no key yet: every p is 0
+      const uint64_t sl2x2 = f2(sl2, sl2), nm2 = f2(-mr, -mr);
+      uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float t0, t1;
+          f2split(ffma2(f2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), sl2x2, nm2), t0, t1);
+          t0 = ex2(t0);
+          t1 = ex2(t1);
+          sum[k & 1] = fadd2(sum[k & 1], f2(t0, t1));
+          pk[k] = pack_bf16(t0, t1);
+        }
+        // value rows of NaNs (stored as zeros): NaN weights for the rows that see them
+        if (h == 0) {
+          const uint32_t st = n & 1;
+          if (!wwait(P, S, &S.v_full[st], (n >> 1) & 1)) ok = false;
+        }
+        const uint32_t b0 = S.v_nan[n & 1][2 * h], b1 = S.v_nan[n & 1][2 * h + 1];
+        if (b0 | b1) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t b = (k < 16 ? b0 : b1) >> (2 * (k & 15));
+            if ((b & 1) && (unsigned)(key0 + 64 * h + 2 * k - lo) <= span) pk[k] = (pk[k] & 0xFFFF0000u) | 0x7FC0u;
+            if ((b & 2) && (unsigned)(key0 + 64 * h + 2 * k + 1 - lo) <= span) pk[k] = (pk[k] & 0xFFFFu) | 0x7FC00000u;
+          }
+        }
+        tmem_st32u(s_t + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[side][h]);
+      }
+      float r0, r1, r2, r3;
+      f2split(sum[0], r0, r1);
+      f2split(sum[1], r2, r3);
+      l += (r0 + r1) + (r2 + r3);
+      if (!ok) break;
+    }
+    ok = ok && wwait(P, S, &S.o_full[side], ni & 1);
+    if (!ok) {
+      S.abort = 1;
+      break;
+    }
+    tc_fence_after();
+    const bool cut = I.a > I.first || I.b < I.end;
+    const float inv = 1.f / l;
+    uint16_t* dst = P.out + ((size_t)(I.q0 + ti) * P.n_q_heads + (size_t)I.g * G + row % G) * A;
+    // a range's first piece that began before it is 2b, any other one that is cut 2b + 1
+    const size_t pr = ((size_t)2 * blockIdx.x + (I.a > I.first ? 0 : 1)) * kRows + side * kTileM + row;
+    if (cut) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(m, l);
+#pragma unroll 1
+    for (int c = 0; c < A / 32; ++c) {
+      float o[32];
+      tmem_ld32(o_t + 32 * c, o);
+      tmem_wait_ld();
+      if (cut) {
+        float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      } else if (ti < I.tok_hi) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) =
+              make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                         pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.o_free[side]);
+    ++ni;
+  }
+}
+
+template <int A, int G>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_fp8_kernel(const Fp8Step P, const Fp8Partials W, const int min_q, const __grid_constant__ CUtensorMap qmap) {
+  constexpr int TOK = kTileM / G;
+  extern __shared__ uint8_t smem_raw[];
+  Smem<A>& S = *reinterpret_cast<Smem<A>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  long long* tpre = reinterpret_cast<long long*>(&S + 1);
+  int* ipre = reinterpret_cast<int*>(tpre + P.n_reqs + 1);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.v_full[i], 4);
+      mbar_init(&S.v_empty[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
+      mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.o_free[i], 4);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&qmap);
+  }
+  if (warp == 12) {
+    tmem_alloc(&S.tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  make_plan<A, TOK>(P, W, S, tpre, ipre, min_q);
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // registers of the four warpgroups: 2 x 184 + 88 + 56 = 4 x 128, what the launch holds
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    softmax<A, G>(P, W, S, tpre, ipre, min_q, warp >> 2);
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    convert<A, TOK>(P, S, tpre, ipre, min_q);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 12) issue<A, TOK>(P, S, tpre, ipre, min_q);
+    if (warp == 13) load_q<A, G>(P, &qmap, S, tpre, ipre, min_q);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(S.tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- joining the pieces
+// For every row of every item cut between CTAs: M = max m_i, out = sum 2^(m_i -
+// M) o_i / sum 2^(m_i - M) l_i, in the pieces' order.  A CTA takes 32 rows of an
+// item, a warp 4 of them, lane = A / 32 dimensions.
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+template <int A>
+__global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int group) {
+  constexpr int D = A / 32;
+  __shared__ int owner[kMaxDecodeGrid];
+  __shared__ int n_owner;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = kTileM / group;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    int n = 0;
+    for (int b0 = 0; b0 < ctas; b0 += 32) {
+      const int b = b0 + lane;
+      const bool has = b < ctas && W.rec[b].n > 1;
+      const unsigned mask = __ballot_sync(0xffffffffu, has);
+      if (has) owner[n + __popc(mask & ((1u << lane) - 1))] = b;
+      n += __popc(mask);
+    }
+    if (lane == 0) n_owner = n;
+  }
+  __syncthreads();
+  for (int task = blockIdx.x; task < n_owner * (kRows / kJoinRows); task += gridDim.x) {
+    const int b = owner[task / (kRows / kJoinRows)];
+    const Fp8Rec rec = W.rec[b];
+    const int q0 = __ldg(P.cu_q_lens + rec.r), q_len = __ldg(P.cu_q_lens + rec.r + 1) - q0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (task % (kRows / kJoinRows)) * kJoinRows + warp * 4 + i;
+      const int ti = rec.pad * 2 * tok + row / group;          // rows of tile B follow tile A's: its tokens do too
+      if (ti >= q_len) continue;
+      auto piece = [&](int k) { return (size_t)(k == 0 ? 2 * b + 1 : 2 * (b + k)) * kRows + row; };
+      float M = kNegInf;
+      for (int k = 0; k < rec.n; ++k) M = fmaxf(M, W.ml[piece(k) * 2]);
+      float L = 0.f, o[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[d] = 0.f;
+      for (int k = 0; k < rec.n; ++k) {
+        const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(k) * 2);
+        const float w = ml.x == kNegInf ? (ml.y != 0.f ? 1.f : 0.f) : ex2(ml.x - M);   // -inf: no key seen, or NaNs only
+        L += w * ml.y;
+        const float* src = W.acc + piece(k) * A + lane * D;
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] += w * src[d];
+      }
+      uint16_t* dst = P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D;
+#pragma unroll
+      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d] / L, o[d + 1] / L);
+    }
+  }
+}
+
+template <int A>
+size_t smem_bytes(int n_reqs) {
+  return 1024 + sizeof(Smem<A>) + (size_t)(n_reqs + 1) * 12;
+}
+static_assert(sizeof(Smem<128>) + 1024 + (kMaxReqs + 1) * 12 <= kSmemLimit, "shared memory");
+
+template <int A, int G>
+cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream) {
+  CUtensorMap qm;
+  if (!encode_query_tiles(&qm, s.q, s.n_tokens, s.n_q_heads, A, G, kTileM / G)) return cudaErrorInvalidValue;
+  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(chunk_fp8_kernel<A, G>), kSmemLimit);
+  if (e != cudaSuccess) return e;
+  chunk_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, min_q, qm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(4 * grid);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_chunk_kernel<A>, s, w, grid, G);
+}
+
+}  // namespace
+
+size_t fp8_chunk_partials_bytes(int head_dim) {
+  return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * kRows * (2 + head_dim) * 4;
+}
+Fp8Partials fp8_chunk_partials(void* workspace) {
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  Fp8Partials w;
+  w.rec = reinterpret_cast<Fp8Rec*>(p);
+  w.ml = reinterpret_cast<float*>(p + sizeof(Fp8Rec) * kMaxDecodeGrid);
+  w.acc = w.ml + (size_t)2 * kMaxDecodeGrid * kRows * 2;
+  return w;
+}
+
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream) {
+  const int a = s.cache.head_dim, g = s.n_q_heads / s.cache.n_kv_heads;
+#define CB_CASE(A_, G_) \
+  if (a == A_ && g == G_) return launch_t<A_, G_>(s, w, min_q, grid, stream);
+  CB_CASE(128, 1)
+  CB_CASE(128, 2)
+  CB_CASE(128, 4)
+  CB_CASE(128, 8)
+  CB_CASE(128, 16)
+  CB_CASE(128, 32)
+  CB_CASE(64, 1)
+  CB_CASE(64, 2)
+  CB_CASE(64, 4)
+  CB_CASE(64, 8)
+#undef CB_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace cb

@@ -147,7 +147,7 @@ cudaError_t launch_copy_blocks_fp8(const int32_t* pairs, int n_pairs, const Fp8C
 // A piece of one sequence's softmax: which CTA's range it starts in, and how
 // many CTAs' ranges it reaches (n = 0: no sequence starts there and goes on).
 struct Fp8Rec {
-  int r, hg, n, pad;
+  int r, hg, n, pad;            // pad: the chunk kernel's pair of query tiles (hg: its KV head)
 };
 // Workspace of the single-token attention: per CTA two partial results (its
 // first and its last piece), [64 heads][A] values and [64][2] (max, sum).
@@ -161,8 +161,11 @@ Fp8Partials fp8_partials(void* workspace);
 bool fp8_decode_shape(int head_dim, int group);
 // The requests with one new token, on `grid` CTAs (at most one per SM), and the join of their pieces.
 cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream);
-// The other requests (all of them with singles = true).
-cudaError_t launch_attention_fp8_simple(const Fp8Step& s, bool singles, cudaStream_t stream);
+// The requests with at least min_q new tokens, and the join of their pieces.  Partial
+// results: as above, per CTA two times [256 rows][A] values and [256][2] (max, sum).
+size_t fp8_chunk_partials_bytes(int head_dim);
+Fp8Partials fp8_chunk_partials(void* workspace);
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream);
 
 // Library state that the entry points of other files use (cb_api.cu).
 unsigned int* stream_error_word(cudaStream_t stream, int* rc);   // nullptr: return *rc
@@ -170,6 +173,9 @@ void set_last_launches(int n);
 bool device_sms(int* n);
 // Tensor map of a matrix of `rows` rows of row_bytes bytes (64 or 128, one swizzle span), boxes of box_rows whole rows.
 bool encode_byte_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows);
+// Tensor map of q [n_tokens][Hq][A], boxes of 64 columns x box_heads heads x box_tokens tokens.
+bool encode_query_tiles(CUtensorMap* m, const void* q, int n_tokens, int n_q_heads, int head_dim, int box_heads,
+                        int box_tokens);
 bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size);
 
 }  // namespace cb

@@ -257,6 +257,41 @@ def test_a_row_of_nans_reaches_its_own_head_only(hq, hk, a, which, q_len):
 
 
 @pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (32, 1, 128)])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_a_row_of_nans_is_seen_from_its_position_on(hq, hk, a, which):
+    """A bad row among the chunk's own tokens: the tokens before it do not see it,
+    nor do those for which it has left the window."""
+    s = Step([(200, 90)], hq, hk, a, seed=23, window=64)
+    clean = s.run()
+    p, g = 90 + 70, hk - 1
+    blk, off = s.tables[0, p // BS], p % BS
+    (s.k_codes if which == "k" else s.v_codes)[blk, g, off] = 0
+    (s.k_exps if which == "k" else s.v_exps)[blk, g, off] = 255
+    out = s.run()
+    G = hq // hk
+    hit = torch.zeros(200, hq, dtype=torch.bool)
+    hit[70:70 + 64, g * G:(g + 1) * G] = True
+    assert out.cpu()[hit].isnan().all()
+    assert torch.equal(out.cpu()[~hit], clean.cpu()[~hit])
+
+
+@pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (64, 8, 128), (32, 2, 128), (32, 1, 128)])
+@pytest.mark.parametrize("q_len", [1, 50])
+def test_every_code(hq, hk, a, q_len):
+    """All 254 finite e4m3 codes, subnormals and zeros of both signs among them,
+    over rows of exponents on both sides of the conversion's two ranges."""
+    s = Step([(q_len, 250), (q_len, 31)], hq, hk, a, seed=22, qscale=0.05)
+    rng = np.random.default_rng(1)
+    finite = np.array([c for c in range(256) if c & 127 != 127], np.uint8)
+    for r, (q, c) in enumerate(s.reqs):
+        for p in range(q + c):
+            at = (s.tables[r, p // BS], slice(None), p % BS)
+            s.k_codes[at], s.v_codes[at] = rng.choice(finite, (hk, a)), rng.choice(finite, (hk, a))
+            s.v_exps[at] = rng.integers(130, 140, hk)
+    check(s.run(), *s.reference(), "every code")
+
+
+@pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (32, 1, 128)])
 @pytest.mark.parametrize("q_len", [1, 3])
 def test_nan_in_q_stays_in_its_head(hq, hk, a, q_len):
     s = Step([(q_len, 90)], hq, hk, a, seed=14)
