@@ -251,10 +251,6 @@ bool device_sms(int* n) {
   *n = di.n_sms;
   return true;
 }
-bool encode_query_tiles(CUtensorMap* m, const void* q, int n_tokens, int n_q_heads, int head_dim, int box_heads,
-                        int box_tokens) {
-  return encode_q_map(m, q, n_tokens, n_q_heads, head_dim, box_heads, box_tokens);
-}
 bool encode_byte_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows) {
   auto fn = encode_fn();
   if (!fn) return false;

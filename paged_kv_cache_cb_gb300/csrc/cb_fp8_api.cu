@@ -53,7 +53,10 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
     return CB_EINVAL;
   // the kernels count tiles of the step in 32 bits
   const long long blocks = std::min<long long>(max_blocks_per_seq, ((long long)max_kv_len + kBlockSize - 1) / kBlockSize);
-  if (blocks * n_reqs * n_kv_heads >= 1LL << 31) return CB_EINVAL;
+  const long long tok = kTileM / (n_q_heads / n_kv_heads), items = n_tokens / (2 * tok) + n_reqs;
+  if (blocks * n_reqs * n_kv_heads >= 1LL << 31 ||
+      items * (((long long)max_kv_len + kTileN - 1) / kTileN) * n_kv_heads >= 1LL << 31)
+    return CB_EINVAL;
   if (!q || !cu_q_lens || !ctx_lens || !block_tables || !out || !workspace) return CB_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return CB_EINVAL;
   if (app && (!app->k || !app->v || !app->slots || !aligned16(app->k) || !aligned16(app->v))) return CB_EINVAL;

@@ -2,17 +2,18 @@
 // cb_fp8.cuh) on the tensor cores.
 //
 // Mathematics.  For a row (token at position p, query head h) with visible keys
-// j <= p (and j > p - W under a window):
-//     x_j = scale log2(e) q . K_j,   p_j = 2^(x_j - m),   out = sum p_j V_j / sum p_j
-// with m a running maximum that moves only when a score passes it by 8.  K_j and
-// V_j are the cache's rows as bf16, which is exact (the rows' scales are powers of
-// two), so the two products are bf16 x bf16 with fp32 sums; p_j is rounded to bf16
-// for the second one (2^-8 relative, the type of the cache's own 16-bit form),
-// the sum of p_j is taken before that rounding.
-// Here K and V are converted (the single-token kernel multiplies the 8-bit values
-// as they are): every tile serves 256 query rows, so the conversion is one
-// operation in 256, while the 8-bit products would need two terms of q and three
-// of p each, more tensor work than the bf16 products.
+// j <= p (and j > p - W under a window), keys k_j 2^ek_j and values v_j 2^ev_j:
+//     x_j = scale log2(e) 2^eq 2^ek_j (q . k_j),  p_j = 2^(x_j - m),  out = sum p_j V_j / sum p_j
+// with m a running maximum that moves only when a score passes it by 8.
+//   S = q k^T takes e4m3 K from the cache as it is; q 2^-eq is two e4m3 terms
+//   whose products add up (4 significant bits each: bf16's 8; values down to
+//   2^-15 of the row's largest exactly, smaller ones within 2^-18 of it).
+//   O = p V takes V as bf16, converted exactly (the rows' scales are powers of
+//   two), and p rounded to bf16 (2^-8 relative, the type of the 16-bit cache);
+//   the sum of p is taken before that rounding.
+// The two S terms cost as much tensor time as one bf16 product and leave K
+// unconverted; p in 8-bit terms would cost three, and the softmax's time for
+// making them.
 //
 // Tiles.  An item is (request, KV head, 2 TOK tokens), TOK = 128 / G: two query
 // tiles of 128 rows (row i = token i / G, head i % G) that share the keys, in
@@ -28,9 +29,10 @@
 // end sooner than the cut ranges and their joining, they stay whole.
 //
 // Warps: 0-3 and 4-7 softmax of tiles A and B (thread = row; the row's 128
-// scores stay in registers, one read of tensor memory), 8-11 convert K and V from
-// global memory (loads a step ahead in registers) to bf16 in shared memory, 12
-// issues the products, 13 loads Q.  Every wait is bounded.
+// scores stay in registers, one read of tensor memory; also the query's terms and
+// the output), 8-11 convert V from a staged copy, in short loops (the warps'
+// code shares one instruction cache), 12 issues the products, 13 loads K, V and
+// the exponents, 14 walks the work and publishes it.  Every wait is bounded.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -46,26 +48,31 @@ constexpr int kMinTiles = 4;           // key tiles per CTA below which a step u
 constexpr int kCutTiles = 7;           // what cutting items costs, in key tiles' time (partial results and their joining)
 constexpr int kSmemLimit = 232448;
 
+// An item, and the piece [a, b) of its key tiles [first, end); b = a: no more items.
+struct Item {
+  int r, g, pair, q0, q_len, ctx, tok_lo, tok_hi, first, end, a, b, sides, pad[3];
+};
+constexpr int kItems = 4;              // published ahead
+constexpr int kReaders = 14;           // warps that read them
+
 template <int A>
 struct alignas(1024) Smem {
   static constexpr int H = A / 64;     // 64-dimension halves of 128-byte rows
-  uint8_t q[2][H][128][128];
-  uint8_t k[2][H][128][128];
-  uint8_t v[2][H][128][128];
-  uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain;
-  uint32_t v_nan[2][4];                // rows of the V stage that stand for NaNs (stored as zeros)
-  long long scan[16], tiles, u0, u1;
-  int iscan[16], items, longest, whole, eff;
+  uint8_t q[2][2][128 * A];            // [query tile][term]: e4m3 rows of A bytes
+  uint8_t k[2][128 * A];               // e4m3 as in the cache
+  uint8_t vr[2][128 * A];              // V as in the cache, no swizzle
+  uint8_t v[2][H][128][128];           // V in bf16
+  float fk[4][128];                    // 2^ek of the tile's keys
+  uint32_t v_nan[4][4];                // keys whose V stands for NaNs (stored as zeros)
+  uint8_t ex[2][2][128];               // the tile's exponent bytes, K and V
+  uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, item_full[kItems], item_empty[kItems];
+  Item item[kItems];
+  int scan[16], iscan[16], tiles, u0, u1, items, longest, whole, eff;
   uint32_t tmem;
   volatile int abort;
 };
 
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
 template <class S>
 __device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
   const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
@@ -98,28 +105,22 @@ __device__ __forceinline__ int3 request(const Fp8Step& P, int r, int min_q, bool
   return make_int3(q0, (int)n, ctx);
 }
 
-// An item, and the piece [a, b) of its key tiles [first, end).
-struct Item {
-  int r, g, pair, q0, q_len, ctx, tok_lo, tok_hi, first, end, a, b, sides;
-};
-
 // The CTA's pieces in order.  Items of a request: pairs from the last (most
 // keys) down, KV heads inside.
 template <int TOK>
 struct ItemIter {
   const Fp8Step& P;
-  const long long* tpre;               // tiles before request r
+  const int* tpre;                     // tiles before request r
   const int* ipre;                     // items before request r
   int min_q, whole, step, index, n_items;   // whole items: index, index + step, ...
-  long long u, u1;                     // cut ranges
+  int u, u1;                           // cut ranges
   int3 rq;
   int r, pair, g, j0;                  // the next piece's place (cut ranges)
   bool fresh = true;
   template <class S>
-  __device__ ItemIter(const Fp8Step& p, const S& s, const long long* tp, const int* ip, int mq)
+  __device__ ItemIter(const Fp8Step& p, const S& s, const int* tp, const int* ip, int mq)
       : P(p), tpre(tp), ipre(ip), min_q(mq), whole(s.whole), step(s.eff), index(blockIdx.x), n_items(s.items), u(s.u0), u1(s.u1) {}
-  template <class T>
-  __device__ int find(const T* pre, T x) const {
+  __device__ int find(const int* pre, int x) const {
     int lo = 0, hi = P.n_reqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -163,19 +164,19 @@ struct ItemIter {
       fresh = false;
       r = find(tpre, u);
       rq = request(P, r, min_q, false);
-      long long off = u - tpre[r];
+      int off = u - tpre[r];
       for (pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1; pair > 0; --pair) {
-        const long long t = (long long)(pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window)) * Hkv;
+        const int t = (pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window)) * Hkv;
         if (off < t) break;
         off -= t;
       }
       const int t = pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window);
-      g = (int)(off / t);
-      j0 = (int)(off % t);
+      g = off / t;
+      j0 = off % t;
     }
     fill(I);
     I.a = I.first + j0;
-    I.b = (int)min((long long)I.end, I.a + (u1 - u));
+    I.b = min(I.end, I.a + (u1 - u));
     u += I.b - I.a;
     j0 = 0;
     if (++g == Hkv) {
@@ -193,28 +194,25 @@ struct ItemIter {
 };
 
 // The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
-__device__ __forceinline__ int cta_of(long long u, long long total, int eff) { return (int)(((u + 1) * eff - 1) / total); }
+__device__ __forceinline__ int cta_of(int u, int total, int eff) {
+  return (int)((((long long)u + 1) * eff - 1) / total);
+}
 
 // All threads; ends with __syncthreads().
 template <int A, int TOK>
-__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, long long* tpre, int* ipre, int min_q) {
+__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int* tpre, int* ipre, int min_q) {
   const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, Hkv = P.cache.n_kv_heads;
   if (tid == 0) S.longest = 0;
   for (int r = tid; r < n; r += kThreads) {
     const int3 q = request(P, r, min_q, blockIdx.x == 0);
-    ipre[r] = (q.y + 2 * TOK - 1) / (2 * TOK);         // its pairs
-    tpre[r] = ((long long)q.z << 32) | (unsigned)q.y;  // its lengths
+    ipre[r] = q.y;
+    tpre[r] = q.z;
   }
   __syncthreads();
   for (int r = wid; r < n; r += kThreads / 32) {       // a warp per request with pairs
-    const int pairs = ipre[r];
-    if (pairs == 0) {
-      if (lane == 0) tpre[r] = 0;
-      continue;
-    }
-    const int ctx = (int)(tpre[r] >> 32), q_len = (int)(tpre[r] & 0xFFFFFFFF);
-    long long t = 0;
-    int mx = 0;
+    const int q_len = ipre[r], ctx = tpre[r], pairs = (q_len + 2 * TOK - 1) / (2 * TOK);
+    if (pairs == 0) continue;                          // both are 0
+    int t = 0, mx = 0;
     for (int p = lane; p < pairs; p += 32) {
       const int x = pair_end(ctx, q_len, p, 2 * TOK) - pair_first(ctx, p, 2 * TOK, P.window);
       t += x;
@@ -233,18 +231,15 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
   __syncthreads();
   // exclusive prefix sums of both
   const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
-  long long t_own = 0;
-  int i_own = 0;
+  int t_own = 0, i_own = 0;
   for (int r = lo; r < hi; ++r) {
     t_own += tpre[r];
     i_own += ipre[r];
   }
-  long long t_incl = t_own;
-  int i_incl = i_own;
+  int t_incl = t_own, i_incl = i_own;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, t_incl, off);
-    const int y = __shfl_up_sync(0xffffffffu, i_incl, off);
+    const int x = __shfl_up_sync(0xffffffffu, t_incl, off), y = __shfl_up_sync(0xffffffffu, i_incl, off);
     if (lane >= off) {
       t_incl += x;
       i_incl += y;
@@ -255,8 +250,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
     S.iscan[wid] = i_incl;
   }
   __syncthreads();
-  long long total = 0, t_run = t_incl - t_own;
-  int items = 0, i_run = i_incl - i_own;
+  int total = 0, t_run = t_incl - t_own, items = 0, i_run = i_incl - i_own;
   for (int w = 0; w < kThreads / 32; ++w) {
     total += S.scan[w];
     items += S.iscan[w];
@@ -266,8 +260,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
     }
   }
   for (int r = lo; r < hi; ++r) {
-    const long long t = tpre[r];
-    const int i = ipre[r];
+    const int t = tpre[r], i = ipre[r];
     tpre[r] = t_run;
     ipre[r] = i_run;
     t_run += t;
@@ -277,13 +270,13 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
     tpre[n] = total;
     ipre[n] = items;
     const int grid = gridDim.x, b = blockIdx.x;
-    const int eff = (int)max(1LL, min((long long)grid, (total + kMinTiles - 1) / kMinTiles));
+    const int eff = max(1, min(grid, (total + kMinTiles - 1) / kMinTiles));
     S.tiles = total;
     S.items = items;
     S.whole = (long long)((items + grid - 1) / grid) * S.longest <= (total + grid - 1) / grid + kCutTiles;
     S.eff = S.whole ? grid : eff;
-    S.u0 = b < eff ? total * b / eff : total;
-    S.u1 = b < eff ? total * (b + 1) / eff : total;
+    S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
+    S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
   }
   __syncthreads();
   if (tid == 0) {                      // the item that starts in this range and goes on after it
@@ -293,8 +286,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
       it.u = S.u1 - 1;
       Item I;
       it.next(I);
-      const long long start = S.u1 - 1 - (I.a - I.first);
-      const long long end = start + (I.end - I.first);
+      const int start = S.u1 - 1 - (I.a - I.first), end = start + (I.end - I.first);
       if (start >= S.u0 && end > S.u1)
         rec = {I.r, I.g, cta_of(end - 1, S.tiles, S.eff) - (int)blockIdx.x + 1, I.pair};
     }
@@ -302,7 +294,105 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, lo
   }
 }
 
-// ---------------------------------------------------------------- conversion (warps 8-11)
+// ---------------------------------------------------------------- items (warp 14)
+// One warp walks the CTA's pieces and publishes them: the others need no
+// registers for the walk.
+template <int A, int TOK>
+__device__ void publish(const Fp8Step& P, Smem<A>& S, const int* tpre, const int* ipre, int min_q) {
+  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+  Item I;
+  for (uint32_t i = 0;; ++i) {
+    const bool more = it.next(I);
+    if (!wwait(P, S, &S.item_empty[i % kItems], ((i / kItems) & 1) ^ 1)) break;
+    if ((threadIdx.x & 31) == 0) {
+      if (!more) I.a = I.b = 0;
+      S.item[i % kItems] = I;
+      mbar_arrive(&S.item_full[i % kItems]);
+    }
+    __syncwarp();
+    if (!more) break;
+  }
+}
+// A warp's walk over the published items.
+template <class SM>
+struct Items {
+  uint32_t i = 0;
+  __device__ const Item* next(const Fp8Step& P, SM& S) {
+    if (!wwait(P, S, &S.item_full[i % kItems], (i / kItems) & 1)) return nullptr;
+    const Item* I = &S.item[i % kItems];
+    return I->b > I->a ? I : nullptr;
+  }
+  __device__ void done(SM& S) {        // the whole warp has read what it needs of it
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.item_empty[i % kItems]);
+    ++i;
+  }
+};
+
+// ---------------------------------------------------------------- loads (warp 13)
+// K into the swizzled operand layout, V and the exponent bytes as they are.
+template <int A>
+__device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S) {
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, Hkv = P.cache.n_kv_heads, rows_total = P.cache.num_blocks * Hkv * kBlockSize;
+  Items<Smem<A>> items;
+  uint32_t n = 0;
+  bool ok = true;
+  while (ok) {
+    const Item* item = items.next(P, S);
+    if (!item) break;
+    const int r = item->r, g = item->g, a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi;
+    const int key_lo = P.window > 0 ? max(0, item->ctx + item->tok_lo - P.window + 1) : 0;
+    items.done(S);
+    const int nblk = (kv_hi + kBlockSize - 1) / kBlockSize, blk_lo = key_lo / kBlockSize;
+    // lane 8 t + i: entry of block i of tile base + t; 4 tiles at a time, the next 4 on their way.  Blocks
+    // that no row of the item sees are not read: they may have been released.
+    auto entry = [&](int base) {
+      const int blk = base * 8 + lane;
+      if (blk < blk_lo || blk >= nblk || base + (lane >> 3) >= b) return -2;
+      const int e = __ldg(P.block_tables + (size_t)r * P.max_blocks_per_seq + blk);
+      return e < 0 || e >= P.cache.num_blocks ? -1 : e;
+    };
+    int cur = -2, nxt = entry(a);
+    for (int j = a; j < b && ok; ++j, ++n) {
+      const int t = (j - a) & 3;
+      if (t == 0) {
+        cur = nxt;
+        nxt = entry(j + 4);
+        if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);   // its rows count as zeros
+      }
+      const int e = __shfl_sync(FULL, cur, t * 8 + (lane & 7));
+      const bool have = lane < 8 && e >= 0;
+      const int row = e >= 0 ? (e * Hkv + g) * kBlockSize : rows_total;    // past the extent: zeros
+      const unsigned blocks = __popc(__ballot_sync(FULL, have));
+      const uint32_t st = n & 1, ph = ((n >> 1) & 1) ^ 1;
+      ok = wwait(P, S, &S.k_empty[st], ph);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&S.k_full[st], 128 * A);
+      __syncwarp();
+      if (lane < 8) tma_load_2d(&S.k[st][lane * kBlockSize * A], kmap, 0, row, &S.k_full[st]);
+      ok = wwait(P, S, &S.vr_empty[st], ph);
+      if (!ok) {
+        ++n;
+        break;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&S.vr_full[st], blocks * (kBlockSize * A + 2 * kBlockSize));
+      __syncwarp();
+      if (have) {
+        bulk_load(&S.vr[st][lane * kBlockSize * A], P.cache.v + (size_t)row * A, kBlockSize * A, &S.vr_full[st]);
+        bulk_load(&S.ex[st][0][lane * kBlockSize], P.cache.k_exps + row, kBlockSize, &S.vr_full[st]);
+        bulk_load(&S.ex[st][1][lane * kBlockSize], P.cache.v_exps + row, kBlockSize, &S.vr_full[st]);
+      }
+    }
+  }
+  if (!ok)                             // copies already issued land before the CTA exits
+    for (uint32_t i = n > 2u ? n - 2 : 0; i < n; ++i) {
+      mbar_wait(&S.k_full[i & 1], (i >> 1) & 1, 20000000ull);
+      mbar_wait(&S.vr_full[i & 1], (i >> 1) & 1, 20000000ull);
+    }
+}
+
+// ---------------------------------------------------------------- conversion of V (warps 8-11)
 // 16 e4m3 -> 16 bf16 times 2^e.  Each byte is sign-extended to 16 bits and moved
 // up by 4: sign, zeros, the 4 exponent and 3 fraction bits in bf16's places, a
 // bf16 2^-120 times too small (also for e4m3's subnormals, which become bf16's);
@@ -318,163 +408,102 @@ __device__ __forceinline__ uint32_t permute(uint32_t x) {
   asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
   return r;
 }
-__device__ __forceinline__ void widen16(const uint4& x, uint32_t b, uint32_t (&o)[8]) {
-  const uint32_t f1 = (min(b, 134u) + 120u) << 7, m1 = f1 | (f1 << 16);
+__device__ __forceinline__ void widen16(const uint4& x, uint32_t f, uint32_t (&o)[8]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // bytes 0, 1 (then 2, 3) as two sign-extended halves: selector bit 3 repeats a byte's sign
-    const uint32_t lo = permute<0x9180>(w[i]), hi = permute<0xB3A2>(w[i]);
-    o[2 * i] = mul_bf16x2((lo << 4) & 0x87F087F0u, m1);
-    o[2 * i + 1] = mul_bf16x2((hi << 4) & 0x87F087F0u, m1);
-  }
-  if (b > 134u) {
-    const uint32_t f2 = b == kExpNan ? 0x7FC0u : (b - 134u + 127u) << 7, m2 = f2 | (f2 << 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], m2);
+    o[2 * i] = mul_bf16x2((permute<0x9180>(w[i]) << 4) & 0x87F087F0u, f);
+    o[2 * i + 1] = mul_bf16x2((permute<0xB3A2>(w[i]) << 4) & 0x87F087F0u, f);
   }
 }
+// The factor of exponent byte b as a pair of bf16 (up to 2^7 of it: see above), and what is left of it.
+__device__ __forceinline__ uint32_t factor1(uint32_t b) { return ((min(b, 134u) + 120u) << 7) * 0x10001u; }
+__device__ __forceinline__ uint32_t factor2(uint32_t b) { return ((max(b, 134u) - 134u + 127u) << 7) * 0x10001u; }
 
-// A tile's rows on their way: this lane's 16-byte pieces, and the exponent of
-// row 32 warp + lane.
 template <int A>
-struct Flight {
-  static constexpr int N = A / 16;     // pieces per lane: 32 rows x A bytes per warp
-  uint4 x[N];
-  uint32_t e;
-};
-
-template <int A, int TOK>
-__device__ void convert(const Fp8Step& P, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
-  constexpr int N = Flight<A>::N, LR = A / 16, RP = 32 / LR;   // lanes per row, rows per piece step
+__device__ void convert(const Fp8Step& P, Smem<A>& S) {
+  constexpr int LR = A / 16, RP = 32 / LR, N = 32 / RP;   // lanes per row, rows per step, steps
   const unsigned FULL = 0xffffffffu;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, Hkv = P.cache.n_kv_heads;
-  const int col = lane % LR, rsub = lane / LR;
-  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
-  Item I;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const int col = lane % LR, rsub = lane / LR, key_l = 32 * warp + lane;
+  // 16 dimensions: two 16-byte chunks of the half's 128-byte row; lanes of the second half store them in
+  // the other order (the halves share banks)
+  const int c = (col & 3) * 2, sw = A == 128 ? col >> 2 : 0;
+  Items<Smem<A>> items;
   uint32_t n = 0;
-  while (it.next(I)) {
-    const int kv_hi = I.ctx + I.tok_hi, nblk = (kv_hi + kBlockSize - 1) / kBlockSize;
-    const int key_lo = P.window > 0 ? max(0, I.ctx + I.tok_lo - P.window + 1) : 0, blk_lo = key_lo / kBlockSize;
-    // lane 2 t + i: entry of block 2 warp + i of tile base + t; 16 tiles at a time, the next 16 on their way
-    auto entry = [&](int base) {
-      const int blk = (base + (lane >> 1)) * 8 + 2 * warp + (lane & 1);
-      if (blk < blk_lo || blk >= nblk || base + (lane >> 1) >= I.b) return -2;
-      const int e = __ldg(P.block_tables + (size_t)I.r * P.max_blocks_per_seq + blk);
-      return e < 0 || e >= P.cache.num_blocks ? -1 : e;
-    };
-    int cur = entry(I.a), nxt = entry(I.a + 16);
-    if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);    // its rows count as zeros
-    auto load = [&](Flight<A>& f, const uint8_t* cache, const uint8_t* exps, int t) {
-      const int b0 = __shfl_sync(FULL, cur, 2 * t), b1 = __shfl_sync(FULL, cur, 2 * t + 1);
-      const int eb = lane < 16 ? b0 : b1;
-      f.e = eb >= 0 ? __ldg(exps + ((size_t)eb * Hkv + I.g) * kBlockSize + (lane & 15)) : 1u;
-#pragma unroll
+  bool ok = true;
+  while (ok) {
+    const Item* item = items.next(P, S);
+    if (!item) break;
+    const int a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi;
+    const int key_lo = P.window > 0 ? max(0, item->ctx + item->tok_lo - P.window + 1) : 0;
+    items.done(S);
+    for (int j = a; j < b; ++j, ++n) {
+      const uint32_t st = n & 1, ph = (n >> 1) & 1;
+      ok = wwait(P, S, &S.vr_full[st], ph);
+      if (!ok) break;
+      // this lane's key: its factors.  Values that no row of the item sees, and rows of NaNs, become zeros
+      // (0 * NaN must not reach O); the latter are told to the softmax, for the rows that see them.
+      const uint32_t kb = S.ex[st][0][key_l], vb = S.ex[st][1][key_l];
+      const int key = j * kTileN + key_l;
+      const bool seen = key >= key_lo && key < kv_hi, nan = vb == kExpNan;
+      S.fk[n & 3][key_l] = exp_scale(kb);
+      const unsigned bad = __ballot_sync(FULL, nan && seen);
+      if (lane == 0) S.v_nan[n & 3][warp] = bad;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.fk_full[n & 3]);
+      const uint32_t f1 = seen && !nan ? factor1(vb) : 0u;
+      const bool large = __any_sync(FULL, seen && !nan && vb > 134u);
+      ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
+      if (!ok) break;
+      const uint8_t* src = &S.vr[st][32 * warp * A + lane * 16];
+      uint8_t* dst = &S.v[st][sw][32 * warp + rsub][0];
+#pragma unroll 2
       for (int p = 0; p < N; ++p) {
-        const int row = p * RP + rsub, b = row < 16 ? b0 : b1;
-        f.x[p] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + (((size_t)b * Hkv + I.g) * kBlockSize + (row & 15)) * A) + col)
-                        : make_uint4(0, 0, 0, 0);
-      }
-    };
-    auto store = [&](const Flight<A>& f, uint8_t (*dst)[128][128], int key0, bool is_v, uint32_t st) {
-      if (is_v) {
-        // rows that no row of the item sees, and rows of NaNs: zeros (0 * NaN must not reach O); the
-        // latter are told to the softmax, which gives NaN to the rows that see them
-        const int key = key0 + 32 * warp + lane;
-        const unsigned bad = __ballot_sync(FULL, f.e == kExpNan && key >= key_lo && key < kv_hi);
-        if (lane == 0) S.v_nan[st][warp] = bad;
-      }
-#pragma unroll
-      for (int p = 0; p < N; ++p) {
-        const int row = p * RP + rsub, r = 32 * warp + row;
-        const uint32_t e = __shfl_sync(FULL, f.e, row);
+        const int row = p * RP + rsub;
         uint32_t o[8];
-        widen16(f.x[p], e, o);
-        if (is_v && (e == kExpNan || key0 + r < key_lo || key0 + r >= kv_hi)) {
+        widen16(*reinterpret_cast<const uint4*>(src + p * 512), __shfl_sync(FULL, f1, row), o);
+        if (large) {
+          const uint32_t f2 = factor2(__shfl_sync(FULL, vb, row));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = 0;
+          for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], f2);
         }
-        // 16 dimensions: two 16-byte chunks of the half's 128-byte row; lanes of the second half store them
-        // in the other order (the halves share banks)
-        const int c = (col & 3) * 2, half = A == 128 ? col >> 2 : 0, sw = half;
-        uint8_t* d = &dst[half][r][0];
         const uint4 x0 = make_uint4(o[0], o[1], o[2], o[3]), x1 = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint4*>(d + (((c + sw) ^ (r & 7)) << 4)) = sw ? x1 : x0;
-        *reinterpret_cast<uint4*>(d + (((c + 1 - sw) ^ (r & 7)) << 4)) = sw ? x0 : x1;
+        *reinterpret_cast<uint4*>(dst + p * RP * 128 + (((c + sw) ^ (row & 7)) << 4)) = sw ? x1 : x0;
+        *reinterpret_cast<uint4*>(dst + p * RP * 128 + (((c + 1 - sw) ^ (row & 7)) << 4)) = sw ? x0 : x1;
       }
       fence_proxy_async_smem();
       __syncwarp();
-    };
-    Flight<A> fk, fv;
-    load(fk, P.cache.k, P.cache.k_exps, 0);
-    bool ok = true;
-    for (int j = I.a; j < I.b; ++j, ++n) {
-      const int t = (j - I.a) & 15;
-      const uint32_t st = n & 1, ph = (n >> 1) & 1;
-      load(fv, P.cache.v, P.cache.v_exps, t);
-      ok = wwait(P, S, &S.k_empty[st], ph ^ 1);
-      if (!ok) break;
-      store(fk, S.k[st], j * kTileN, false, st);
-      if (lane == 0) mbar_arrive(&S.k_full[st]);
-      if (j + 1 < I.b) {
-        if (t == 15) {
-          cur = nxt;
-          nxt = entry(j + 17);
-          if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);
-        }
-        load(fk, P.cache.k, P.cache.k_exps, (t + 1) & 15);
+      if (lane == 0) {
+        mbar_arrive(&S.v_full[st]);
+        mbar_arrive(&S.vr_empty[st]);
       }
-      ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
-      if (!ok) break;
-      store(fv, S.v[st], j * kTileN, true, st);
-      if (lane == 0) mbar_arrive(&S.v_full[st]);
     }
-    if (!ok) break;
   }
-}
-
-// ---------------------------------------------------------------- Q (warp 13)
-template <int A, int G>
-__device__ void load_q(const Fp8Step& P, const CUtensorMap* qmap, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
-  constexpr int TOK = kTileM / G, H = A / 64;
-  const int lane = threadIdx.x & 31;
-  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
-  Item I;
-  uint32_t n = 0;
-  bool ok = true;
-  for (; it.next(I); ++n) {
-    ok = wwait(P, S, &S.q_empty, (n & 1) ^ 1);
-    if (!ok) break;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&S.q_full, I.sides * H * 128 * 128);
-      for (int side = 0; side < I.sides; ++side)
-        for (int h = 0; h < H; ++h)
-          tma_load_3d(&S.q[side][h][0][0], qmap, h * 64, I.g * G, I.q0 + I.tok_lo + side * TOK, &S.q_full);
-    }
-    __syncwarp();
-  }
-  if (!ok && n > 0) mbar_wait(&S.q_full, (n - 1) & 1, 20000000ull);   // its last copy lands before the CTA exits
 }
 
 // ---------------------------------------------------------------- products (warp 12)
-template <int A, int TOK>
-__device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const int* ipre, int min_q) {
-  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescO = idesc_bf16_f32(128, A, 1);
+template <int A>
+__device__ void issue(const Fp8Step& P, Smem<A>& S) {
+  constexpr uint32_t kIdescS = idesc_f8(128, 128, 0, 0, 0, 0), kIdescO = idesc_bf16_f32(128, A, 1);
   constexpr uint32_t kHalf = 128 * 128, kTile = (A / 64) * kHalf;
-  const uint64_t qd = smem_desc_sw128(smem_u32(S.q), 16, 1024), kd = smem_desc_sw128(smem_u32(S.k), 16, 1024);
+  constexpr int kLayout = A == 128 ? 2 : 4;
+  const uint64_t qd = smem_desc(smem_u32(S.q), 16, 8 * A, kLayout), kd = smem_desc(smem_u32(S.k), 16, 8 * A, kLayout);
   const uint64_t vd = smem_desc_sw128(smem_u32(S.v), kHalf, 1024);
-  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
-  Item I;
+  Items<Smem<A>> items;
   uint32_t n = 0, np[2] = {0, 0};      // key tiles before this item; products with P issued per side
   uint32_t ni[2] = {0, 0};             // items per side
   bool ok = true;
-  for (uint32_t i = 0; ok && it.next(I); ++i) {
-    ok = wwait(P, S, &S.q_full, i & 1);
-    const int len = I.b - I.a;
+  while (ok) {
+    const Item* item = items.next(P, S);
+    if (!item) break;
+    const int len = item->b - item->a, sides = item->sides;
+    items.done(S);
     for (int j = 0; j <= len && ok; ++j) {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
-        if (side >= I.sides || !ok) break;
+        if (side >= sides || !ok) break;
         const uint32_t s_t = S.tmem + side * 128, o_t = S.tmem + 256 + side * A;
         if (j > 0) {                   // O += P V of the tile before
           const uint32_t t = n + j - 1, st = t & 1;
@@ -490,7 +519,7 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const
               for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
                 tc_mma_f16_ts(o_t, s_t + ks * 8, vd + (uint32_t)((st * kTile + ks * 16 * 128) >> 4), kIdescO, (j > 1 || ks > 0) ? 1u : 0u);
               if (h == 1) {
-                if (side == I.sides - 1) tc_commit(&S.v_empty[st]);
+                if (side == sides - 1) tc_commit(&S.v_empty[st]);
                 if (j == len) tc_commit(&S.o_full[side]);
               }
             }
@@ -501,20 +530,19 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const
         }
         if (j < len) {                 // S of this one
           const uint32_t t = n + j, st = t & 1;
-          ok = wwait(P, S, &S.k_full[st], (t >> 1) & 1);
+          if (j == 0) ok = wwait(P, S, &S.q_full[side], ni[side] & 1);
+          ok = ok && wwait(P, S, &S.k_full[st], (t >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < A / 16; ++ks) {
-              const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
-              tc_mma_f16(s_t, qd + (uint32_t)((side * kTile + off) >> 4), kd + (uint32_t)((st * kTile + off) >> 4), kIdescS, ks > 0);
-            }
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int d = 0; d < A / 32; ++d)
+                mma_f8(s_t, qd + (uint32_t)((((side * 2 + term) * 128 * A) >> 4) + 2 * d), kd + (uint32_t)(((st * 128 * A) >> 4) + 2 * d),
+                       kIdescS, term > 0 || d > 0);
             tc_commit(&S.s_full[side]);
-            if (side == I.sides - 1) {
-              tc_commit(&S.k_empty[st]);
-              if (j == len - 1) tc_commit(&S.q_empty);
-            }
+            if (side == sides - 1) tc_commit(&S.k_empty[st]);
           }
           __syncwarp();
         }
@@ -522,7 +550,7 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const
     }
     n += len;
     ++ni[0];
-    if (I.sides == 2) ++ni[1];
+    if (sides == 2) ++ni[1];
   }
   if (!ok) S.abort = 1;
   if (elect_one()) tc_commit(&S.drain);
@@ -531,54 +559,116 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S, const long long* tpre, const
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-3, 4-7)
+// This thread's query row as two e4m3 terms; returns its factor scale log2(e)
+// 2^eq (NaN for a row that is not finite, whose terms are zeros).
+template <int A>
+__device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid) {
+  const uint4* src = reinterpret_cast<const uint4*>(P.q + ((size_t)tok * P.n_q_heads + head) * A);
+  uint4 x[A / 8];
+#pragma unroll
+  for (int i = 0; i < A / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < A / 8; ++i)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+  m = max(m & 0xFFFFu, m >> 16);
+  const bool bad = m >= 0x7F80u;
+  const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
+  const float f = exp_inverse(bad ? 1u : eb);
+#pragma unroll
+  for (int c = 0; c < A / 16; ++c) {
+    const uint32_t w[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w, x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+    uint32_t t0[4], t1[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y0 = bad ? 0.f : bf16lo(w[i]) * f, y1 = bad ? 0.f : bf16hi(w[i]) * f;
+      const uint32_t hi = pack_e4m3(y0, y1);
+      float z0, z1;
+      e4m3_to_f32(hi, z0, z1);
+      const uint32_t lo = pack_e4m3(y0 - z0, y1 - z1);
+      t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
+      t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
+    }
+    const int at = row * A + ((A == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+    *reinterpret_cast<uint4*>(&S.q[side][0][at]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+    *reinterpret_cast<uint4*>(&S.q[side][1][at]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+  }
+  fence_proxy_async_smem();
+  mbar_arrive(&S.q_full[side]);
+  return bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+}
+
 template <int A, int G>
-__device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, const long long* tpre, const int* ipre, int min_q, int side) {
+__device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int side) {
   constexpr int TOK = kTileM / G;
   const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
   const uint32_t s_t = S.tmem + lane_base + side * 128, o_t = S.tmem + lane_base + 256 + side * A;
-  const float sl2 = P.scale_log2;
-  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
-  Item I;
+  Items<Smem<A>> items;
   uint32_t n = 0, ns = 0, ni = 0;      // key tiles of all items, of this side's items; this side's items
-  while (it.next(I)) {
-    if (side >= I.sides) {
-      n += I.b - I.a;
-      continue;
+  const Item* item = nullptr;
+  // the next item that has this side, its query rows made ready
+  auto next_item = [&](float& fq) {
+    while ((item = items.next(P, S)) != nullptr) {
+      if (side < item->sides) {
+        const int ti = item->tok_lo + side * TOK + row / G;
+        fq = make_query<A>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi);
+        return;
+      }
+      n += item->b - item->a;
+      items.done(S);
     }
-    const int ti = I.tok_lo + side * TOK + row / G;
-    const int pos = I.ctx + min(ti, I.tok_hi - 1);           // the last key this row sees
+  };
+  float fq = 0.f;
+  next_item(fq);
+  while (item) {
+    const int ti = item->tok_lo + side * TOK + row / G, tok_hi = item->tok_hi, a0 = item->a, b0 = item->b;
+    const int pos = item->ctx + min(ti, tok_hi - 1);         // the last key this row sees
     const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
     const unsigned span = (unsigned)(pos - lo);              // key k is visible iff (unsigned)(k - lo) <= span
+    const bool began = a0 > item->first, cut = began || b0 < item->end;
+    uint16_t* dst = P.out + ((size_t)(item->q0 + ti) * P.n_q_heads + (size_t)item->g * G + row % G) * A;
+    items.done(S);
     float m = kNegInf, l = 0.f;
     bool ok = true;
-    for (int j = I.a; j < I.b; ++j, ++n, ++ns) {
-      ok = wwait(P, S, &S.s_full[side], ns & 1);             // also: O holds every product before this tile
+    for (int j = a0; j < b0; ++j, ++n, ++ns) {
+      ok = wwait(P, S, &S.fk_full[n & 3], (n >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);   // O holds all products before
       if (!ok) break;
       tc_fence_after();
       float s[128];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, reinterpret_cast<float (&)[32]>(s[32 * c]));
       tmem_wait_ld();
-      const int key0 = j * kTileN;
-      const bool edge = key0 + kTileN - 1 > pos || key0 < lo;
-      if (__any_sync(FULL, edge)) {
+      const float4* fk = reinterpret_cast<const float4*>(S.fk[n & 3]);
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
+      for (int k = 0; k < 32; ++k) {
+        const float4 f = fk[k];
+        f2split(fmul2(f2(s[4 * k], s[4 * k + 1]), f2(f.x, f.y)), s[4 * k], s[4 * k + 1]);
+        f2split(fmul2(f2(s[4 * k + 2], s[4 * k + 3]), f2(f.z, f.w)), s[4 * k + 2], s[4 * k + 3]);
+      }
+      const int key0 = j * kTileN;
+      const uint4 vn = *reinterpret_cast<const uint4*>(S.v_nan[n & 3]);
+      if (__any_sync(FULL, key0 + kTileN - 1 > pos || key0 < lo || (vn.x | vn.y | vn.z | vn.w) != 0)) {
+        // keys out of sight; visible ones whose value row is NaNs
+#pragma unroll
+        for (int k = 0; k < 128; ++k) {
+          const uint32_t w = k < 32 ? vn.x : k < 64 ? vn.y : k < 96 ? vn.z : vn.w;
+          if ((w >> (k & 31)) & 1) s[k] = __uint_as_float(0x7FC00000u);
           if ((unsigned)(key0 + k - lo) > span) s[k] = kNegInf;
+        }
       }
       float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
       for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
-      const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * sl2;
+      const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * fq;
       const bool need = mt > m + 8.f;
       float alpha = 1.f;
       if (need) {
         alpha = ex2(m - mt);
         m = mt;
       }
-      if (j > I.a && __any_sync(FULL, need)) {
+      if (j > a0 && __any_sync(FULL, need)) {
 #pragma unroll 1
         for (int c = 0; c < A / 8; ++c) {
           float o[8];
@@ -591,7 +681,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, cons
       }
       l *= alpha;
       const float mr = m == kNegInf ? 0.f : m;               // a row that has seen no key yet: every p is 0
-      const uint64_t sl2x2 = f2(sl2, sl2), nm2 = f2(-mr, -mr);
+      const uint64_t fq2 = f2(fq, fq), nm2 = f2(-mr, -mr);
       uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -599,25 +689,11 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, cons
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           float t0, t1;
-          f2split(ffma2(f2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), sl2x2, nm2), t0, t1);
+          f2split(ffma2(f2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), fq2, nm2), t0, t1);
           t0 = ex2(t0);
           t1 = ex2(t1);
           sum[k & 1] = fadd2(sum[k & 1], f2(t0, t1));
           pk[k] = pack_bf16(t0, t1);
-        }
-        // value rows of NaNs (stored as zeros): NaN weights for the rows that see them
-        if (h == 0) {
-          const uint32_t st = n & 1;
-          if (!wwait(P, S, &S.v_full[st], (n >> 1) & 1)) ok = false;
-        }
-        const uint32_t b0 = S.v_nan[n & 1][2 * h], b1 = S.v_nan[n & 1][2 * h + 1];
-        if (b0 | b1) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const uint32_t b = (k < 16 ? b0 : b1) >> (2 * (k & 15));
-            if ((b & 1) && (unsigned)(key0 + 64 * h + 2 * k - lo) <= span) pk[k] = (pk[k] & 0xFFFF0000u) | 0x7FC0u;
-            if ((b & 2) && (unsigned)(key0 + 64 * h + 2 * k + 1 - lo) <= span) pk[k] = (pk[k] & 0xFFFFu) | 0x7FC00000u;
-          }
         }
         tmem_st32u(s_t + 32 * h, pk);
         tmem_wait_st();
@@ -629,19 +705,18 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, cons
       f2split(sum[0], r0, r1);
       f2split(sum[1], r2, r3);
       l += (r0 + r1) + (r2 + r3);
-      if (!ok) break;
     }
-    ok = ok && wwait(P, S, &S.o_full[side], ni & 1);
     if (!ok) {
       S.abort = 1;
       break;
     }
+    // the next item's query first: its first scores are computed during this one's output
+    next_item(fq);
+    if (!wwait(P, S, &S.o_full[side], ni & 1)) break;
     tc_fence_after();
-    const bool cut = I.a > I.first || I.b < I.end;
     const float inv = 1.f / l;
-    uint16_t* dst = P.out + ((size_t)(I.q0 + ti) * P.n_q_heads + (size_t)I.g * G + row % G) * A;
     // a range's first piece that began before it is 2b, any other one that is cut 2b + 1
-    const size_t pr = ((size_t)2 * blockIdx.x + (I.a > I.first ? 0 : 1)) * kRows + side * kTileM + row;
+    const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows + side * kTileM + row;
     if (cut) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(m, l);
 #pragma unroll 1
     for (int c = 0; c < A / 32; ++c) {
@@ -652,7 +727,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, cons
         float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
 #pragma unroll
         for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      } else if (ti < I.tok_hi) {
+      } else if (ti < tok_hi) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           *reinterpret_cast<uint4*>(dst + 32 * c + 8 * k) =
@@ -669,19 +744,20 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, cons
 
 template <int A, int G>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_fp8_kernel(const Fp8Step P, const Fp8Partials W, const int min_q, const __grid_constant__ CUtensorMap qmap) {
+    chunk_fp8_kernel(const Fp8Step P, const Fp8Partials W, const int min_q, const __grid_constant__ CUtensorMap kmap) {
   constexpr int TOK = kTileM / G;
   extern __shared__ uint8_t smem_raw[];
   Smem<A>& S = *reinterpret_cast<Smem<A>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  long long* tpre = reinterpret_cast<long long*>(&S + 1);
-  int* ipre = reinterpret_cast<int*>(tpre + P.n_reqs + 1);
+  int* tpre = reinterpret_cast<int*>(&S + 1);
+  int* ipre = tpre + P.n_reqs + 1;
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
-    mbar_init(&S.q_full, 1);
-    mbar_init(&S.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&S.k_full[i], 4);
+      mbar_init(&S.q_full[i], 128);
+      mbar_init(&S.k_full[i], 1);
       mbar_init(&S.k_empty[i], 1);
+      mbar_init(&S.vr_full[i], 1);
+      mbar_init(&S.vr_empty[i], 4);
       mbar_init(&S.v_full[i], 4);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
@@ -690,10 +766,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_free[i], 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.fk_full[i], 4);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&S.item_full[i], 1);
+      mbar_init(&S.item_empty[i], kReaders);
+    }
     mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
-    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
   }
   if (warp == 12) {
     tmem_alloc(&S.tmem, 512);
@@ -704,17 +785,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // registers of the four warpgroups: 2 x 184 + 88 + 56 = 4 x 128, what the launch holds
+  // registers of the four warpgroups: 2 x 176 + 72 + 88 = 4 x 128, what the launch holds
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-    softmax<A, G>(P, W, S, tpre, ipre, min_q, warp >> 2);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    softmax<A, G>(P, W, S, warp >> 2);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    convert<A, TOK>(P, S, tpre, ipre, min_q);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    convert<A>(P, S);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 12) issue<A, TOK>(P, S, tpre, ipre, min_q);
-    if (warp == 13) load_q<A, G>(P, &qmap, S, tpre, ipre, min_q);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 12) issue<A>(P, S);
+    if (warp == 13) load_tiles<A>(P, &kmap, S);
+    if (warp == 14) publish<A, TOK>(P, S, tpre, ipre, min_q);
   }
   tc_fence_before();
   __syncthreads();
@@ -780,17 +862,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step 
 
 template <int A>
 size_t smem_bytes(int n_reqs) {
-  return 1024 + sizeof(Smem<A>) + (size_t)(n_reqs + 1) * 12;
+  return 1024 + sizeof(Smem<A>) + (size_t)(n_reqs + 1) * 8;
 }
-static_assert(sizeof(Smem<128>) + 1024 + (kMaxReqs + 1) * 12 <= kSmemLimit, "shared memory");
+static_assert(sizeof(Smem<128>) + 1024 + (kMaxReqs + 1) * 8 <= kSmemLimit, "shared memory");
 
 template <int A, int G>
 cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream) {
-  CUtensorMap qm;
-  if (!encode_query_tiles(&qm, s.q, s.n_tokens, s.n_q_heads, A, G, kTileM / G)) return cudaErrorInvalidValue;
+  CUtensorMap km;
+  const long long rows = (long long)s.cache.num_blocks * s.cache.n_kv_heads * kBlockSize;
+  if (!encode_byte_rows(&km, s.cache.k, rows, A, kBlockSize)) return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(chunk_fp8_kernel<A, G>), kSmemLimit);
   if (e != cudaSuccess) return e;
-  chunk_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, min_q, qm);
+  chunk_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, min_q, km);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};

@@ -173,9 +173,6 @@ void set_last_launches(int n);
 bool device_sms(int* n);
 // Tensor map of a matrix of `rows` rows of row_bytes bytes (64 or 128, one swizzle span), boxes of box_rows whole rows.
 bool encode_byte_rows(CUtensorMap* m, const void* base, long long rows, int row_bytes, int box_rows);
-// Tensor map of q [n_tokens][Hq][A], boxes of 64 columns x box_heads heads x box_tokens tokens.
-bool encode_query_tiles(CUtensorMap* m, const void* q, int n_tokens, int n_q_heads, int head_dim, int box_heads,
-                        int box_tokens);
 bool supported_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size);
 
 }  // namespace cb
