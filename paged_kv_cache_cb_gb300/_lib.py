@@ -274,25 +274,69 @@ def _append_attention(name, window, k_new, v_new, slot_mapping, q, cu_q_lens, ct
 
 
 # ---------------------------------------------------------------- 8-bit cache
-def _fp8_cache(k_cache, v_cache, k_exps, v_exps):
+# These calls take a few microseconds on the GPU at their smallest, so their
+# checks read each tensor's attributes once and keep torch's objects at hand.
+class _Torch:
+    """torch's dtypes, and the current device and stream, without its wrappers."""
+
+    def __init__(self):
+        torch = _t()
+        self.bf16, self.fp8, self.u8 = torch.bfloat16, torch.float8_e4m3fn, torch.uint8
+        self.i32, self.i64 = torch.int32, torch.int64
+        c = torch._C
+        self.device = getattr(c, "_cuda_getDevice", None) or torch.cuda.current_device
+        raw = getattr(c, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_TC = None
+
+
+def _tc():
+    global _TC
+    if _TC is None:
+        _TC = _Torch()
+    return _TC
+
+
+def _on(dev, t, dtype, name, ndim):
+    """Raw pointer of a contiguous tensor of the current device ``dev`` (raw
+    pointers are launched there)."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, ndim)                     # says what is wrong, but for the device
+    raise ValueError(f"{name} must be on the current device ({dev}), got {t.get_device()}")
+
+
+def _current_device(c, t):
+    """The current device; a tensor on the host is refused before CUDA is asked."""
+    try:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+    except AttributeError:
+        raise ValueError("tensors must be CUDA tensors") from None
+    return c.device()
+
+
+def _raw_stream(c, dev, stream):
+    return c.stream(dev) if stream is None else _stream(stream)
+
+
+def _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps):
     """Pointers of an 8-bit cache (e4m3 [num_blocks, Hkv, bs, A] and uint8
     exponents [num_blocks, Hkv, bs]) and its shape."""
-    torch = _t()
-    f8, u8 = torch.float8_e4m3fn, torch.uint8
-    ptrs = (_dev(k_cache, f8, "k_cache", 4), _dev(v_cache, f8, "v_cache", 4), _dev(k_exps, u8, "k_exps", 3),
-            _dev(v_exps, u8, "v_exps", 3))
+    ptrs = (_on(dev, k_cache, c.fp8, "k_cache", 4), _on(dev, v_cache, c.fp8, "v_cache", 4),
+            _on(dev, k_exps, c.u8, "k_exps", 3), _on(dev, v_exps, c.u8, "v_exps", 3))
     shape = k_cache.shape
-    if v_cache.shape != shape or k_exps.shape != shape[:3] or v_exps.shape != shape[:3]:
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("cache shape mismatch")
+    rows = shape[:3]
+    if k_exps.shape != rows or v_exps.shape != rows:
         raise ValueError("cache shape mismatch")
     return ptrs, shape
-
-
-def _one_device(*tensors):
-    """Raw device pointers are launched on the current device: every tensor lives there."""
-    dev = _t().cuda.current_device()
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"tensors must be on the current device ({dev}), got one on {t.get_device()}")
 
 
 def cb_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exps, stream=None):
@@ -300,44 +344,46 @@ def cb_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exp
     k_cache, v_cache: float8_e4m3fn [num_blocks, Hkv, block_size, A] and k_exps,
     v_exps: uint8 [num_blocks, Hkv, block_size], written in place: each row's
     values and its power-of-two exponent (include/cbattn.h, 8-bit cache)."""
-    torch = _t()
-    bf = torch.bfloat16
-    pk = _dev(k_new, bf, "k_new", 3)
-    pv = _dev(v_new, bf, "v_new", 3)
-    ps = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
-    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
-    n = k_new.shape[0]
-    if k_new.shape != (n, hk, a) or v_new.shape != k_new.shape or slot_mapping.shape[0] != n:
+    c = _tc()
+    dev = _current_device(c, k_new)
+    pk = _on(dev, k_new, c.bf16, "k_new", 3)
+    pv = _on(dev, v_new, c.bf16, "v_new", 3)
+    ps = _on(dev, slot_mapping, c.i64, "slot_mapping", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
+    shape = k_new.shape
+    n = shape[0]
+    if shape != (n, hk, a) or v_new.shape != shape or slot_mapping.shape != (n,):
         raise ValueError("shape mismatch")
-    _one_device(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exps)
-    _check("cb_kv_append_fp8", lib().cb_kv_append_fp8(pk, pv, ps, n, *cache, nb, hk, a, bs, _stream(stream)))
+    _check("cb_kv_append_fp8", lib().cb_kv_append_fp8(pk, pv, ps, n, *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
 def cb_kv_gather_fp8(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_out, stream=None):
     """The rows stored at slot_mapping (int64 [n_rows], negative: the output row is
     left as it was) read back into k_out, v_out: bf16 [n_rows, Hkv, A]."""
-    torch = _t()
-    bf = torch.bfloat16
-    ps = _dev(slot_mapping, torch.int64, "slot_mapping", 1)
-    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
-    pk = _dev(k_out, bf, "k_out", 3)
-    pv = _dev(v_out, bf, "v_out", 3)
+    c = _tc()
+    dev = _current_device(c, slot_mapping)
+    ps = _on(dev, slot_mapping, c.i64, "slot_mapping", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
+    pk = _on(dev, k_out, c.bf16, "k_out", 3)
+    pv = _on(dev, v_out, c.bf16, "v_out", 3)
     n = slot_mapping.shape[0]
-    if k_out.shape != (n, hk, a) or v_out.shape != k_out.shape:
+    shape = k_out.shape
+    if shape != (n, hk, a) or v_out.shape != shape or slot_mapping.dim() != 1:
         raise ValueError("shape mismatch")
-    _one_device(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_out)
-    _check("cb_kv_gather_fp8", lib().cb_kv_gather_fp8(ps, n, *cache, nb, pk, pv, hk, a, bs, _stream(stream)))
+    _check("cb_kv_gather_fp8", lib().cb_kv_gather_fp8(ps, n, *cache, nb, pk, pv, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
 def cb_copy_blocks_fp8(pairs, k_cache, v_cache, k_exps, v_exps, stream=None):
     """cb_copy_blocks of an 8-bit cache: values and exponents of block dst become
     those of block src for every (src, dst) of pairs, int32 [n, 2]."""
-    pp = _dev(pairs, _t().int32, "pairs", 2)
-    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
-    if pairs.shape[1] != 2:
+    c = _tc()
+    dev = _current_device(c, pairs)
+    pp = _on(dev, pairs, c.i32, "pairs", 2)
+    cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
+    n = pairs.shape[0]
+    if pairs.shape != (n, 2):
         raise ValueError("shape mismatch")
-    _one_device(pairs, k_cache, v_cache, k_exps, v_exps)
-    _check("cb_copy_blocks_fp8", lib().cb_copy_blocks_fp8(pp, pairs.shape[0], *cache, nb, hk, a, bs, _stream(stream)))
+    _check("cb_copy_blocks_fp8", lib().cb_copy_blocks_fp8(pp, n, *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
 def cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim,
@@ -367,30 +413,35 @@ def cb_kv_append_paged_attention_fp8(k_new, v_new, slot_mapping, q, cu_q_lens, c
 
 def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, scale,
                    workspace, max_q_len, max_kv_len, window, stream):
-    torch = _t()
-    bf, i32 = torch.bfloat16, torch.int32
-    ptrs = [_dev(q, bf, "q", 3), _dev(cu_q_lens, i32, "cu_q_lens", 1), _dev(ctx_lens, i32, "ctx_lens", 1),
-            _dev(block_tables, i32, "block_tables", 2)]
-    po = _dev(out, bf, "out", 3)
-    pw = _dev(workspace, torch.uint8, "workspace", 1)
-    cache, (nb, hk, bs, a) = _fp8_cache(k_cache, v_cache, k_exps, v_exps)
-    n_tok, hq, a2 = q.shape
+    c = _tc()
+    dev = _current_device(c, q)
+    pq = _on(dev, q, c.bf16, "q", 3)
+    pcu = _on(dev, cu_q_lens, c.i32, "cu_q_lens", 1)
+    pctx = _on(dev, ctx_lens, c.i32, "ctx_lens", 1)
+    pbt = _on(dev, block_tables, c.i32, "block_tables", 2)
+    po = _on(dev, out, c.bf16, "out", 3)
+    pw = _on(dev, workspace, c.u8, "workspace", 1)
+    cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
+    shape, tables = q.shape, block_tables.shape
     n_reqs = ctx_lens.shape[0]
-    if out.shape != q.shape or cu_q_lens.shape[0] != n_reqs + 1 or block_tables.shape[0] != n_reqs:
+    if (len(shape) != 3 or out.shape != shape or ctx_lens.dim() != 1 or cu_q_lens.shape != (n_reqs + 1,)
+            or len(tables) != 2 or tables[0] != n_reqs or workspace.dim() != 1):
         raise ValueError("shape mismatch")
+    n_tok, hq, a2 = shape
     if a2 != a:
         raise ValueError("cache shape mismatch")
+    args = (pq, pcu, pctx, pbt, tables[1], n_reqs, n_tok, int(max_q_len), int(max_kv_len), *cache, nb, po, float(scale),
+            hq, hk, a, bs, int(window), pw, workspace.shape[0], _raw_stream(c, dev, stream))
     if new is not None:
         k_new, v_new, slots = new
-        ptrs = [_dev(k_new, bf, "k_new", 3), _dev(v_new, bf, "v_new", 3),
-                _dev(slots, torch.int64, "slot_mapping", 1)] + ptrs
-        if k_new.shape != (n_tok, hk, a) or v_new.shape != k_new.shape or slots.shape[0] != n_tok:
+        pk = _on(dev, k_new, c.bf16, "k_new", 3)
+        pv = _on(dev, v_new, c.bf16, "v_new", 3)
+        ps = _on(dev, slots, c.i64, "slot_mapping", 1)
+        if k_new.shape != (n_tok, hk, a) or v_new.shape != (n_tok, hk, a) or slots.shape != (n_tok,):
             raise ValueError("new rows must be [n_tokens, Hkv, A] with one slot per token")
-        _one_device(k_new, v_new, slots)
-    _one_device(q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, workspace)
-    rc = getattr(lib(), name)(*ptrs, block_tables.shape[1], n_reqs, n_tok, int(max_q_len), int(max_kv_len), *cache, nb,
-                              po, float(scale), hq, hk, a, bs, int(window), pw, workspace.shape[0], _stream(stream))
-    _check(name, rc)
+        _check(name, lib().cb_kv_append_paged_attention_fp8(pk, pv, ps, *args))
+        return
+    _check(name, lib().cb_paged_attention_fp8(*args))
 
 
 CB_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024

@@ -445,33 +445,32 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       if (!ok) break;
       // this lane's key: its factors.  Values that no row of the item sees, and rows of NaNs, become zeros
       // (0 * NaN must not reach O); the latter are told to the softmax, for the rows that see them.
-      const uint32_t kb = S.ex[st][0][key_l], vb = S.ex[st][1][key_l];
+      const uint32_t kb = lds8(smem_u32(&S.ex[st][0][key_l])), vb = lds8(smem_u32(&S.ex[st][1][key_l]));
       const int key = j * kTileN + key_l;
       const bool seen = key >= key_lo && key < kv_hi, nan = vb == kExpNan;
-      S.fk[n & 3][key_l] = exp_scale(kb);
+      sts32(smem_u32(&S.fk[n & 3][key_l]), __float_as_uint(exp_scale(kb)));
       const unsigned bad = __ballot_sync(FULL, nan && seen);
-      if (lane == 0) S.v_nan[n & 3][warp] = bad;
+      if (lane == 0) sts32(smem_u32(&S.v_nan[n & 3][warp]), bad);
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.fk_full[n & 3]);
       const uint32_t f1 = seen && !nan ? factor1(vb) : 0u;
       const bool large = __any_sync(FULL, seen && !nan && vb > 134u);
       ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
       if (!ok) break;
-      const uint8_t* src = &S.vr[st][32 * warp * A + lane * 16];
-      uint8_t* dst = &S.v[st][sw][32 * warp + rsub][0];
+      const uint32_t src = smem_u32(&S.vr[st][32 * warp * A + lane * 16]), dst = smem_u32(&S.v[st][sw][32 * warp + rsub][0]);
 #pragma unroll 2
       for (int p = 0; p < N; ++p) {
         const int row = p * RP + rsub;
         uint32_t o[8];
-        widen16(*reinterpret_cast<const uint4*>(src + p * 512), __shfl_sync(FULL, f1, row), o);
+        widen16(lds128(src + p * 512), __shfl_sync(FULL, f1, row), o);
         if (large) {
           const uint32_t f2 = factor2(__shfl_sync(FULL, vb, row));
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], f2);
         }
         const uint4 x0 = make_uint4(o[0], o[1], o[2], o[3]), x1 = make_uint4(o[4], o[5], o[6], o[7]);
-        *reinterpret_cast<uint4*>(dst + p * RP * 128 + (((c + sw) ^ (row & 7)) << 4)) = sw ? x1 : x0;
-        *reinterpret_cast<uint4*>(dst + p * RP * 128 + (((c + 1 - sw) ^ (row & 7)) << 4)) = sw ? x0 : x1;
+        sts128(dst + p * RP * 128 + (((c + sw) ^ (row & 7)) << 4), sw ? x1 : x0);
+        sts128(dst + p * RP * 128 + (((c + 1 - sw) ^ (row & 7)) << 4), sw ? x0 : x1);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -633,7 +632,10 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int j = a0; j < b0; ++j, ++n, ++ns) {
-      ok = wwait(P, S, &S.fk_full[n & 3], (n >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);   // O holds all products before
+      // The factors' barrier comes first: it is usually complete by now.  For a piece's first tile it may be
+      // several phases behind until S is done (the V of the tile before is then converted).
+      ok = j > a0 || wwait(P, S, &S.s_full[side], ns & 1);
+      ok = ok && wwait(P, S, &S.fk_full[n & 3], (n >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);   // O holds all products before
       if (!ok) break;
       tc_fence_after();
       float s[128];

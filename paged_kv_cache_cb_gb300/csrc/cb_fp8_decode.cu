@@ -94,7 +94,7 @@ struct alignas(1024) Smem {
   float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // a segment's l, m, M, then l, m per head and the slots' factors
   uint64_t k_full[X::KS], k_empty[X::KS], v_full[X::VS], v_empty[X::VS];
   uint64_t e_full[X::ES], e_empty[X::ES], s_full[X::SB], s_empty[X::SB], p_full[X::PB], pv_done[X::PB];
-  uint64_t q_full[2], o_full[X::OB], o_free[X::OB], turn[2], drain[2];
+  uint64_t q_full[2], o_full[2], o_free[X::OB], turn[2], drain[2];
   int scan[16];
   uint32_t tmem;
   volatile int abort;
@@ -390,8 +390,8 @@ __device__ void issue_pv(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int 
           mma_f8(d + ks * 2 * X::SS, a + ((ks * 32 * A) >> 4), b + ((ks * 64 * X::SS) >> 4), kIdesc, j > 0);
         tc_commit(&S.v_empty[st]);
         tc_commit(&S.pv_done[pb]);
-        // a barrier of its own: pv_done may run through the other group's tiles before this one looks
-        if (j == s.nt - 1) tc_commit(&S.o_full[ob]);
+        // a barrier per group: pv_done (or one per O buffer) may be phases away when this group looks
+        if (j == s.nt - 1) tc_commit(&S.o_full[i & 1]);
       }
       __syncwarp();
     }
@@ -548,7 +548,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       const int pos = (s.fb + (s.t0 + j) * bpt + bi) * kBlockSize + tok;
       const bool valid = pos < s.kv && pos >= first_key;
       fail |= !wwait(P, S, &S.e_full[es], (n / X::ES) & 1);
-      const uint32_t kb = S.ex[es][0][tid], vb = S.ex[es][1][tid];
+      const uint32_t kb = lds8(smem_u32(&S.ex[es][0][tid])), vb = lds8(smem_u32(&S.ex[es][1][tid]));
       fail |= !wwait(P, S, &S.s_full[sb], (n / X::SB) & 1);
       tc_fence_after();
       float s0[2 * G], s1[2 * G];
@@ -592,10 +592,10 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
             M[g] = tx;
             need = true;
           }
-          if (tok == 0) S.alpha[grp][n & 1][slot * G + g] = a;
+          if (tok == 0) sts32(smem_u32(&S.alpha[grp][n & 1][slot * G + g]), __float_as_uint(a));
         }
       } else if (tok < G) {
-        S.alpha[grp][n & 1][slot * G + tok] = 1.f;
+        sts32(smem_u32(&S.alpha[grp][n & 1][slot * G + tok]), __float_as_uint(1.f));
       }
       if (named_bar_or(bar_id, 128, (need && j > 0) || fail || S.abort)) {
         if (named_bar_or(bar_id, 128, fail || S.abort)) {
@@ -646,15 +646,14 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       }
       // the buffer is free once the products of tile n - PB have landed
       fail |= !wwait(P, S, &S.pv_done[pb], ((n / X::PB) & 1) ^ 1);
-      uint8_t* pp = S.p[pb] + (slot >> 1) * (64 * X::SS) + (slot & 1) * 128 + tok;
+      const uint32_t pp = smem_u32(S.p[pb]) + (slot >> 1) * (64 * X::SS) + (slot & 1) * 128 + tok;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         const int sh = (g & 1) ? 24 : 8, sh2 = (g & 1) ? 8 : 0;
 #pragma unroll
         for (int t = 0; t < 3; ++t) {
           const int row = (slot & 1) * X::SS + t * G + g;
-          pp[(row >> 3) * 256 + (row & 7) * 16] =
-              (uint8_t)(t == 0 ? b0[g / 2] >> sh : t == 1 ? b1[g / 2] >> sh : b2[g / 2] >> sh2);
+          sts8(pp + (row >> 3) * 256 + (row & 7) * 16, t == 0 ? b0[g / 2] >> sh : t == 1 ? b1[g / 2] >> sh : b2[g / 2] >> sh2);
         }
       }
       // rows that the request does not have hold whatever the cache had: 0 * NaN must not reach O
@@ -662,7 +661,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
         const int st = n % X::VS;
         if (mbar_wait(&S.v_full[st], (n / X::VS) & 1)) {
 #pragma unroll
-          for (int c = 0; c < A / 16; ++c) *reinterpret_cast<uint4*>(&S.v[st][tid * A + c * 16]) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < A / 16; ++c) sts128(smem_u32(&S.v[st][tid * A + c * 16]), make_uint4(0, 0, 0, 0));
         } else {
           set_error(P.err, CB_DEVERR_TIMEOUT);
           S.abort = 1;
@@ -685,7 +684,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
         S.sw[grp][slot * G + g] = M[g];
       }
     }
-    fail |= !wwait(P, S, &S.o_full[i % X::OB], (i / X::OB) & 1);
+    fail |= !wwait(P, S, &S.o_full[grp], (i >> 1) & 1);
     if (named_bar_or(bar_id, 128, fail || S.abort)) break;
     tc_fence_after();
     float hm = kNegInf, hl = 0.f, hw = 0.f;
@@ -746,13 +745,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.pv_done[i], 1);
     }
-    for (int i = 0; i < X::OB; ++i) {
-      mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.o_free[i], 4);
-    }
+    for (int i = 0; i < X::OB; ++i) mbar_init(&S.o_free[i], 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.q_full[i], 128);
       mbar_init(&S.turn[i], 4);
+      mbar_init(&S.o_full[i], 1);
       mbar_init(&S.drain[i], 1);
     }
     S.abort = 0;

@@ -203,7 +203,8 @@ def _calls(L, f):
 ])
 def test_binding_refuses_wrong_tensors(bad, calls, monkeypatch):
     L = _lib()
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    tc = L._tc()
+    monkeypatch.setattr(tc, "device", lambda: 0)
     monkeypatch.setattr(torch, "Tensor", (torch.Tensor, _Fake))
     for name in calls.split():
         with pytest.raises(ValueError):

@@ -194,11 +194,30 @@ def test_one_long_request_is_split(hq, hk, a):
     check(s.run(), *s.reference(), "one long request")
 
 
-@pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (32, 1, 128)])
-def test_many_requests(hq, hk, a):
+@pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (64, 8, 128), (32, 2, 128), (32, 1, 128)])
+@pytest.mark.parametrize("most", [40, 130])
+def test_many_requests(hq, hk, a, most):
+    """Several short sequences per CTA, run repeatedly: the same bits each time."""
     rng = np.random.default_rng(7)
-    s = Step([(1, int(c)) for c in rng.integers(0, 130, 300)], hq, hk, a, seed=8)
-    check(s.run(), *s.reference(), "many requests")
+    s = Step([(1, int(c)) for c in rng.integers(0, most, 300)], hq, hk, a, seed=8)
+    cache, meta, ws = s.cache(), s.meta(), s.workspace()
+    out = s.run(cache=cache, meta=meta, workspace=ws)
+    check(out, *s.reference(), "many requests")
+    for _ in range(20):
+        assert torch.equal(s.run(cache=cache, meta=meta, workspace=ws), out)
+
+
+@pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (8, 8, 64), (32, 1, 128)])
+def test_many_chunks_of_one_and_two_query_tiles(hq, hk, a):
+    """Short and long chunks mixed, several items per CTA, run repeatedly."""
+    rng = np.random.default_rng(9)
+    reqs = [(int(q), int(c)) for q, c in zip(rng.choice([2, 7, 40, 70], 150), rng.integers(0, 300, 150))]
+    s = Step(reqs, hq, hk, a, seed=9)
+    cache, meta, ws = s.cache(), s.meta(), s.workspace()
+    out = s.run(cache=cache, meta=meta, workspace=ws)
+    check(out, *s.reference(), "many chunks")
+    for _ in range(20):
+        assert torch.equal(s.run(cache=cache, meta=meta, workspace=ws), out)
 
 
 @pytest.mark.parametrize("hq,hk,a", [(32, 8, 128), (16, 16, 64), (64, 8, 128), (32, 2, 128), (32, 1, 128)])
