@@ -59,6 +59,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ float lds32f(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint16_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
@@ -68,6 +73,9 @@ __device__ __forceinline__ void sts128(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void sts32(uint32_t a, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
+}
 __device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
 }
@@ -103,6 +111,89 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                    smem_u32(dst)),
                "l"(static_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+
+// ---------------------------------------------------------------- joining pieces
+// A sequence cut between CTAs leaves per piece and row the maximum m and sum l of
+// its weights and its output o (already over l); the joined row is
+//     sum_i W_i o_i / sum_i W_i,   W_i = 2^(m_i - M) l_i,  M = max m_i,
+// in the pieces' order.  m = -inf: no key seen (l = 0), or NaNs only (l is one).
+constexpr int kJoinLoads = (kMaxDecodeGrid + 31) / 32;   // pieces per lane
+// The CTAs whose records start such a sequence, into owner[]; their number.  One warp.
+__device__ __forceinline__ int join_owners(const Fp8Partials& W, int ctas, int* owner) {
+  const int lane = threadIdx.x & 31;
+  int n[kJoinLoads], found = 0;
+#pragma unroll
+  for (int k = 0; k < kJoinLoads; ++k) n[k] = lane + 32 * k < ctas ? W.rec[lane + 32 * k].n : 0;
+#pragma unroll
+  for (int k = 0; k < kJoinLoads; ++k) {
+    const unsigned mask = __ballot_sync(0xffffffffu, n[k] > 1);
+    if (n[k] > 1) owner[found + __popc(mask & ((1u << lane) - 1))] = lane + 32 * k;
+    found += __popc(mask);
+  }
+  return found;
+}
+// This warp's share (pieces first, first + step, ...) of the joined row `row` of
+// the n pieces that start in CTA b; `rows` rows per partial result.  Lane = A / 32
+// dimensions; eight pieces' loads in flight.
+template <int A>
+__device__ __forceinline__ void join_row(const Fp8Partials& W, int rows, int b, int n, int row, int first, int step, float (&o)[A / 32]) {
+  constexpr int D = A / 32;
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  auto piece = [&](int i) { return (size_t)(i == 0 ? 2 * b + 1 : 2 * (b + i)) * rows + row; };
+  float m[kJoinLoads], w[kJoinLoads], M = -__int_as_float(0x7f800000), L = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinLoads; ++k) {
+    const int i = lane + 32 * k;
+    const float2 ml = i < n ? *reinterpret_cast<const float2*>(W.ml + piece(i) * 2) : make_float2(-__int_as_float(0x7f800000), 0.f);
+    m[k] = ml.x;
+    w[k] = ml.y;
+    M = fmaxf(M, ml.x);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, off));
+#pragma unroll
+  for (int k = 0; k < kJoinLoads; ++k) {
+    if (m[k] != -__int_as_float(0x7f800000)) w[k] *= ex2(m[k] - M);
+    L += w[k];
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(FULL, L, off);
+#pragma unroll
+  for (int d = 0; d < D; ++d) o[d] = 0.f;
+  for (int i0 = first; i0 < n; i0 += 8 * step) {
+    float y[8][D];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * step;
+      const float* src = W.acc + piece(i) * A + lane * D;
+#pragma unroll
+      for (int d = 0; d < D; ++d) y[u][d] = 0.f;
+      if (i < n) {
+        if constexpr (D == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          y[u][0] = v.x, y[u][1] = v.y, y[u][2] = v.z, y[u][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          y[u][0] = v.x, y[u][1] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * step;                       // the same in every lane
+      if (i >= n) break;
+      float f = w[0];
+#pragma unroll
+      for (int k = 1; k < kJoinLoads; ++k) f = (i >> 5) == k ? w[k] : f;
+      f = __shfl_sync(FULL, f, i & 31);
+#pragma unroll
+      for (int d = 0; d < D; ++d) o[d] += f * y[u][d];
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d) o[d] /= L;
 }
 
 }  // namespace cb

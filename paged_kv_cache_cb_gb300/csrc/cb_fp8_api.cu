@@ -11,8 +11,6 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
-
 // The cache arguments shared by every entry point; false: CB_EINVAL.
 bool cache_of(Fp8Cache* c, const void* k, const void* v, const void* ke, const void* ve, int num_blocks, int n_kv_heads,
               int head_dim, int block_size) {
@@ -86,14 +84,14 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   if (app && launch_append_fp8(app->k, app->v, app->slots, n_tokens, s.cache, s.err, st) != cudaSuccess)
     return CB_ECUDA;
   int launches = app ? 1 : 0;
+  // the single tokens, then the chunks (ordered on the stream: both may use the same workspace)
   const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
-  if (tiles) {
-    if (launch_decode_fp8(s, fp8_partials(workspace), sms, st) != cudaSuccess) return CB_ECUDA;
-    launches += 2;
-  }
-  if (max_q_len > 1 || !tiles) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace) + (tiles ? align_up(fp8_partials_bytes(head_dim)) : 0);
-    if (launch_chunk_fp8(s, fp8_chunk_partials(ws), tiles ? 2 : 1, sms, st) != cudaSuccess) return CB_ECUDA;
+  const Fp8Partials parts = fp8_chunk_partials(workspace);
+  if ((tiles ? launch_decode_fp8(s, fp8_partials(workspace), sms, st) : launch_chunk_fp8(s, parts, true, sms, st)) != cudaSuccess)
+    return CB_ECUDA;
+  launches += 2;
+  if (max_q_len > 1) {
+    if (launch_chunk_fp8(s, parts, false, sms, st) != cudaSuccess) return CB_ECUDA;
     launches += 2;
   }
   set_last_launches(launches);
@@ -170,8 +168,7 @@ size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q
       !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
   const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
-  return (tiles ? align_up(fp8_partials_bytes(head_dim)) : 0) +
-         (max_q_len > 1 || !tiles ? fp8_chunk_partials_bytes(head_dim) : 0);
+  return std::max(tiles ? fp8_partials_bytes(head_dim) : 0, max_q_len > 1 || !tiles ? fp8_chunk_partials_bytes(head_dim) : 0);
 }
 
 int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,

@@ -66,7 +66,7 @@ struct alignas(1024) Smem {
   uint32_t v_nan[4][4];                // keys whose V stands for NaNs (stored as zeros)
   uint8_t ex[2][2][128];               // the tile's exponent bytes, K and V
   uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], drain, item_full[kItems], item_empty[kItems];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], q_free, x_full, x_empty, drain, item_full[kItems], item_empty[kItems];
   Item item[kItems];
   int scan[16], iscan[16], tiles, u0, u1, items, longest, whole, eff;
   uint32_t tmem;
@@ -92,11 +92,13 @@ __device__ __forceinline__ int pair_end(int ctx, int q_len, int pair, int tok2) 
   return (int)(((long long)ctx + min((long long)q_len, (pair + 1LL) * tok2) + kTileN - 1) / kTileN);
 }
 
-// (q0, q_len, ctx) of request r if it is one of this kernel's; q_len 0 otherwise.
-__device__ __forceinline__ int3 request(const Fp8Step& P, int r, int min_q, bool report) {
+// (q0, q_len, ctx) of request r if it is one of this kernel's (ONE: with one new
+// token, else with several); q_len 0 otherwise.
+template <bool ONE>
+__device__ __forceinline__ int3 request(const Fp8Step& P, int r, bool report) {
   const int q0 = __ldg(P.cu_q_lens + r), q1 = __ldg(P.cu_q_lens + r + 1), ctx = __ldg(P.ctx_lens + r);
   const long long n = (long long)q1 - q0, kv = (long long)ctx + n;
-  if (q0 >= 0 && q1 <= P.n_tokens && n >= 0 && n < min_q) return make_int3(0, 0, 0);
+  if (q0 >= 0 && q1 <= P.n_tokens && n >= 0 && (ONE ? n == 0 || (n > 1 && P.max_q_len > 1) : n < 2)) return make_int3(0, 0, 0);
   if (n < 0 || ctx < 0 || q0 < 0 || q1 > P.n_tokens || n > P.max_q_len || kv > P.max_kv_len ||
       (kv + kBlockSize - 1) / kBlockSize > P.max_blocks_per_seq) {
     if (report) set_error(P.err, CB_DEVERR_BADLEN);
@@ -107,19 +109,19 @@ __device__ __forceinline__ int3 request(const Fp8Step& P, int r, int min_q, bool
 
 // The CTA's pieces in order.  Items of a request: pairs from the last (most
 // keys) down, KV heads inside.
-template <int TOK>
+template <int TOK, bool ONE>
 struct ItemIter {
   const Fp8Step& P;
   const int* tpre;                     // tiles before request r
   const int* ipre;                     // items before request r
-  int min_q, whole, step, index, n_items;   // whole items: index, index + step, ...
+  int whole, step, index, n_items;   // whole items: index, index + step, ...
   int u, u1;                           // cut ranges
   int3 rq;
   int r, pair, g, j0;                  // the next piece's place (cut ranges)
   bool fresh = true;
   template <class S>
-  __device__ ItemIter(const Fp8Step& p, const S& s, const int* tp, const int* ip, int mq)
-      : P(p), tpre(tp), ipre(ip), min_q(mq), whole(s.whole), step(s.eff), index(blockIdx.x), n_items(s.items), u(s.u0), u1(s.u1) {}
+  __device__ ItemIter(const Fp8Step& p, const S& s, const int* tp, const int* ip)
+      : P(p), tpre(tp), ipre(ip), whole(s.whole), step(s.eff), index(blockIdx.x), n_items(s.items), u(s.u0), u1(s.u1) {}
   __device__ int find(const int* pre, int x) const {
     int lo = 0, hi = P.n_reqs - 1;
     while (lo < hi) {
@@ -149,7 +151,7 @@ struct ItemIter {
     if (whole) {
       if (index >= n_items) return false;
       r = find(ipre, index);
-      rq = request(P, r, min_q, false);
+      rq = request<ONE>(P, r, false);
       const int rem = index - ipre[r], pairs = (rq.y + 2 * TOK - 1) / (2 * TOK);
       pair = pairs - 1 - rem / Hkv;
       g = rem % Hkv;
@@ -163,7 +165,7 @@ struct ItemIter {
     if (fresh) {
       fresh = false;
       r = find(tpre, u);
-      rq = request(P, r, min_q, false);
+      rq = request<ONE>(P, r, false);
       int off = u - tpre[r];
       for (pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1; pair > 0; --pair) {
         const int t = (pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window)) * Hkv;
@@ -185,7 +187,7 @@ struct ItemIter {
         do {
           ++r;
         } while (tpre[r + 1] <= u);
-        rq = request(P, r, min_q, false);
+        rq = request<ONE>(P, r, false);
         pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1;
       }
     }
@@ -199,12 +201,12 @@ __device__ __forceinline__ int cta_of(int u, int total, int eff) {
 }
 
 // All threads; ends with __syncthreads().
-template <int A, int TOK>
-__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int* tpre, int* ipre, int min_q) {
+template <int A, int TOK, bool ONE>
+__device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int* tpre, int* ipre) {
   const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, Hkv = P.cache.n_kv_heads;
   if (tid == 0) S.longest = 0;
   for (int r = tid; r < n; r += kThreads) {
-    const int3 q = request(P, r, min_q, blockIdx.x == 0);
+    const int3 q = request<ONE>(P, r, blockIdx.x == 0);
     ipre[r] = q.y;
     tpre[r] = q.z;
   }
@@ -282,7 +284,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
   if (tid == 0) {                      // the item that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
     if (!S.whole && S.u1 > S.u0 && S.u1 < S.tiles) {
-      ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+      ItemIter<TOK, ONE> it(P, S, tpre, ipre);
       it.u = S.u1 - 1;
       Item I;
       it.next(I);
@@ -297,9 +299,9 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
 // ---------------------------------------------------------------- items (warp 14)
 // One warp walks the CTA's pieces and publishes them: the others need no
 // registers for the walk.
-template <int A, int TOK>
-__device__ void publish(const Fp8Step& P, Smem<A>& S, const int* tpre, const int* ipre, int min_q) {
-  ItemIter<TOK> it(P, S, tpre, ipre, min_q);
+template <int A, int TOK, bool ONE>
+__device__ void publish(const Fp8Step& P, Smem<A>& S, const int* tpre, const int* ipre) {
+  ItemIter<TOK, ONE> it(P, S, tpre, ipre);
   Item I;
   for (uint32_t i = 0;; ++i) {
     const bool more = it.next(I);
@@ -560,7 +562,8 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S) {
 // ---------------------------------------------------------------- softmax (warps 0-3, 4-7)
 // This thread's query row as two e4m3 terms; returns its factor scale log2(e)
 // 2^eq (NaN for a row that is not finite, whose terms are zeros).
-template <int A>
+// WRITE false: the factor only.
+template <int A, bool WRITE>
 __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid) {
   const uint4* src = reinterpret_cast<const uint4*>(P.q + ((size_t)tok * P.n_q_heads + head) * A);
   uint4 x[A / 8];
@@ -573,6 +576,8 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
   m = max(m & 0xFFFFu, m >> 16);
   const bool bad = m >= 0x7F80u;
   const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
+  const float factor = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+  if constexpr (!WRITE) return factor;
   const float f = exp_inverse(bad ? 1u : eb);
 #pragma unroll
   for (int c = 0; c < A / 16; ++c) {
@@ -594,7 +599,86 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
   }
   fence_proxy_async_smem();
   mbar_arrive(&S.q_full[side]);
-  return bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+  return factor;
+}
+
+// One key tile (number n; this query tile's S in s_t, its O in o_t) of this
+// thread's row: its weights into tensor memory, m and l brought up to date.
+// fq: the row's factor; it sees the keys lo .. pos.  fresh: O holds nothing yet.
+template <int A>
+__device__ __forceinline__ void softmax_tile(Smem<A>& S, uint32_t s_t, uint32_t o_t, int side, uint32_t n, int key0, bool fresh, float fq,
+                                             int lo, int pos, float& m, float& l) {
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const unsigned span = (unsigned)(pos - lo);                // key k is visible iff (unsigned)(k - lo) <= span
+  float s[128];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, reinterpret_cast<float (&)[32]>(s[32 * c]));
+  tmem_wait_ld();
+  const float4* fk = reinterpret_cast<const float4*>(S.fk[n & 3]);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float4 f = fk[k];
+    f2split(fmul2(f2(s[4 * k], s[4 * k + 1]), f2(f.x, f.y)), s[4 * k], s[4 * k + 1]);
+    f2split(fmul2(f2(s[4 * k + 2], s[4 * k + 3]), f2(f.z, f.w)), s[4 * k + 2], s[4 * k + 3]);
+  }
+  const uint4 vn = *reinterpret_cast<const uint4*>(S.v_nan[n & 3]);
+  if (__any_sync(FULL, key0 + kTileN - 1 > pos || key0 < lo || (vn.x | vn.y | vn.z | vn.w) != 0)) {
+    // keys out of sight; visible ones whose value row is NaNs
+#pragma unroll
+    for (int k = 0; k < 128; ++k) {
+      const uint32_t w = k < 32 ? vn.x : k < 64 ? vn.y : k < 96 ? vn.z : vn.w;
+      if ((w >> (k & 31)) & 1) s[k] = __uint_as_float(0x7FC00000u);
+      if ((unsigned)(key0 + k - lo) > span) s[k] = kNegInf;
+    }
+  }
+  float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+#pragma unroll
+  for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
+  const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * fq;
+  const bool need = mt > m + 8.f;
+  float alpha = 1.f;
+  if (need) {
+    alpha = ex2(m - mt);
+    m = mt;
+  }
+  if (!fresh && __any_sync(FULL, need)) {
+#pragma unroll 1
+    for (int c = 0; c < A / 8; ++c) {
+      float o[8];
+      tmem_ld8(o_t + c * 8, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] *= alpha;
+      tmem_st8(o_t + c * 8, o);
+    }
+  }
+  l *= alpha;
+  const float mr = m == kNegInf ? 0.f : m;               // a row that has seen no key yet: every p is 0
+  const uint64_t fq2 = f2(fq, fq), nm2 = f2(-mr, -mr);
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      float t0, t1;
+      f2split(ffma2(f2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), fq2, nm2), t0, t1);
+      t0 = ex2(t0);
+      t1 = ex2(t1);
+      sum[k & 1] = fadd2(sum[k & 1], f2(t0, t1));
+      pk[k] = pack_bf16(t0, t1);
+    }
+    tmem_st32u(s_t + 32 * h, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.p_full[side][h]);
+  }
+  float r0, r1, r2, r3;
+  f2split(sum[0], r0, r1);
+  f2split(sum[1], r2, r3);
+  l += (r0 + r1) + (r2 + r3);
 }
 
 template <int A, int G>
@@ -612,7 +696,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     while ((item = items.next(P, S)) != nullptr) {
       if (side < item->sides) {
         const int ti = item->tok_lo + side * TOK + row / G;
-        fq = make_query<A>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi);
+        fq = make_query<A, true>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi);
         return;
       }
       n += item->b - item->a;
@@ -625,7 +709,6 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     const int ti = item->tok_lo + side * TOK + row / G, tok_hi = item->tok_hi, a0 = item->a, b0 = item->b;
     const int pos = item->ctx + min(ti, tok_hi - 1);         // the last key this row sees
     const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
-    const unsigned span = (unsigned)(pos - lo);              // key k is visible iff (unsigned)(k - lo) <= span
     const bool began = a0 > item->first, cut = began || b0 < item->end;
     uint16_t* dst = P.out + ((size_t)(item->q0 + ti) * P.n_q_heads + (size_t)item->g * G + row % G) * A;
     items.done(S);
@@ -638,75 +721,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
       ok = ok && wwait(P, S, &S.fk_full[n & 3], (n >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);   // O holds all products before
       if (!ok) break;
       tc_fence_after();
-      float s[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_t + 32 * c, reinterpret_cast<float (&)[32]>(s[32 * c]));
-      tmem_wait_ld();
-      const float4* fk = reinterpret_cast<const float4*>(S.fk[n & 3]);
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float4 f = fk[k];
-        f2split(fmul2(f2(s[4 * k], s[4 * k + 1]), f2(f.x, f.y)), s[4 * k], s[4 * k + 1]);
-        f2split(fmul2(f2(s[4 * k + 2], s[4 * k + 3]), f2(f.z, f.w)), s[4 * k + 2], s[4 * k + 3]);
-      }
-      const int key0 = j * kTileN;
-      const uint4 vn = *reinterpret_cast<const uint4*>(S.v_nan[n & 3]);
-      if (__any_sync(FULL, key0 + kTileN - 1 > pos || key0 < lo || (vn.x | vn.y | vn.z | vn.w) != 0)) {
-        // keys out of sight; visible ones whose value row is NaNs
-#pragma unroll
-        for (int k = 0; k < 128; ++k) {
-          const uint32_t w = k < 32 ? vn.x : k < 64 ? vn.y : k < 96 ? vn.z : vn.w;
-          if ((w >> (k & 31)) & 1) s[k] = __uint_as_float(0x7FC00000u);
-          if ((unsigned)(key0 + k - lo) > span) s[k] = kNegInf;
-        }
-      }
-      float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-#pragma unroll
-      for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
-      const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * fq;
-      const bool need = mt > m + 8.f;
-      float alpha = 1.f;
-      if (need) {
-        alpha = ex2(m - mt);
-        m = mt;
-      }
-      if (j > a0 && __any_sync(FULL, need)) {
-#pragma unroll 1
-        for (int c = 0; c < A / 8; ++c) {
-          float o[8];
-          tmem_ld8(o_t + c * 8, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] *= alpha;
-          tmem_st8(o_t + c * 8, o);
-        }
-      }
-      l *= alpha;
-      const float mr = m == kNegInf ? 0.f : m;               // a row that has seen no key yet: every p is 0
-      const uint64_t fq2 = f2(fq, fq), nm2 = f2(-mr, -mr);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float t0, t1;
-          f2split(ffma2(f2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), fq2, nm2), t0, t1);
-          t0 = ex2(t0);
-          t1 = ex2(t1);
-          sum[k & 1] = fadd2(sum[k & 1], f2(t0, t1));
-          pk[k] = pack_bf16(t0, t1);
-        }
-        tmem_st32u(s_t + 32 * h, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[side][h]);
-      }
-      float r0, r1, r2, r3;
-      f2split(sum[0], r0, r1);
-      f2split(sum[1], r2, r3);
-      l += (r0 + r1) + (r2 + r3);
+      softmax_tile<A>(S, s_t, o_t, side, n, j * kTileN, j == a0, fq, lo, pos, m, l);
     }
     if (!ok) {
       S.abort = 1;
@@ -716,7 +731,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     next_item(fq);
     if (!wwait(P, S, &S.o_full[side], ni & 1)) break;
     tc_fence_after();
-    const float inv = 1.f / l;
+    const float inv = l != 0.f ? 1.f / l : 0.f;              // 0: a piece in which the row saw no key
     // a range's first piece that began before it is 2b, any other one that is cut 2b + 1
     const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows + side * kTileM + row;
     if (cut) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(m, l);
@@ -728,7 +743,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
       if (cut) {
         float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
       } else if (ti < tok_hi) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -744,9 +759,205 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
   }
 }
 
+// ---------------------------------------------------------------- single tokens (groups of 16 and 32 heads)
+// A step's requests with one new token: an item is (request, KV head), its G
+// rows are the first of a query tile.  Both tiles of tensor memory take the same
+// rows, A the even key tiles and B the odd ones, so that one's softmax runs under
+// the other's products as with two query tiles; at the end B hands (m, l, O) to A
+// through shared memory (Q's second tile, not used here).  Only one warp of each
+// side has rows.
+template <int A>
+__device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
+  constexpr uint32_t kIdescS = idesc_f8(128, 128, 0, 0, 0, 0), kIdescO = idesc_bf16_f32(128, A, 1);
+  constexpr uint32_t kHalf = 128 * 128, kTile = (A / 64) * kHalf;
+  constexpr int kLayout = A == 128 ? 2 : 4;
+  const uint64_t qd = smem_desc(smem_u32(S.q), 16, 8 * A, kLayout), kd = smem_desc(smem_u32(S.k), 16, 8 * A, kLayout);
+  const uint64_t vd = smem_desc_sw128(smem_u32(S.v), kHalf, 1024);
+  Items<Smem<A>> items;
+  uint32_t n = 0, i = 0;               // key tiles and items before this one
+  uint32_t np[2] = {0, 0}, nb = 0;     // products with P issued per side; items in which B has tiles
+  bool ok = true;
+  while (ok) {
+    const Item* item = items.next(P, S);
+    if (!item) break;
+    const int len = item->b - item->a;
+    items.done(S);
+    for (int t0 = 0; t0 < len + 2 && ok; t0 += 2) {
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int t = t0 + side;
+        const uint32_t s_t = S.tmem + side * 128, o_t = S.tmem + 256 + side * A;
+        const uint32_t st = (n + t) & 1;                     // the stage of tile t and of tile t - 2
+        if (t >= 2 && t - 2 < len) {   // O += P V of this side's tile before
+          ok = ok && wwait(P, S, &S.v_full[st], ((n + t - 2) >> 1) & 1);
+          if (t < 4) ok = ok && wwait(P, S, &S.o_free[side], ((side ? nb : i) & 1) ^ 1);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wwait(P, S, &S.p_full[side][h], np[side] & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                tc_mma_f16_ts(o_t, s_t + ks * 8, vd + (uint32_t)((st * kTile + ks * 16 * 128) >> 4), kIdescO, (t >= 4 || ks > 0) ? 1u : 0u);
+              if (h == 1) {
+                tc_commit(&S.v_empty[st]);
+                if (t >= len) tc_commit(&S.o_full[side]);
+              }
+            }
+            __syncwarp();
+          }
+          ++np[side];
+        }
+        if (t < len) {
+          if (t == 0) ok = ok && wwait(P, S, &S.q_full[0], i & 1);
+          ok = ok && wwait(P, S, &S.k_full[st], ((n + t) >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int d = 0; d < A / 32; ++d)
+                mma_f8(s_t, qd + (uint32_t)(((term * 128 * A) >> 4) + 2 * d), kd + (uint32_t)(((st * 128 * A) >> 4) + 2 * d), kIdescS,
+                       term > 0 || d > 0);
+            tc_commit(&S.s_full[side]);
+            tc_commit(&S.k_empty[st]);
+            if (t == len - 1) tc_commit(&S.q_free);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+    n += len;
+    ++i;
+    if (len > 1) ++nb;
+  }
+  if (!ok) S.abort = 1;
+  if (elect_one()) tc_commit(&S.drain);
+  __syncwarp();
+  mbar_wait(&S.drain, 0, 20000000ull);
+}
+
 template <int A, int G>
+__device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int side) {
+  static_assert(G <= 32 && 32 * (A + 4) * 4 + 256 <= (int)sizeof(S.q[1]), "B's rows fit in Q's second tile");
+  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const bool works = row < 32;
+  const uint32_t s_t = S.tmem + side * 128, o_t = S.tmem + 256 + side * A;   // warps 0 and 4: lanes 0 .. 31
+  const uint32_t x_row = smem_u32(S.q[1]) + lane * (A + 4) * 4, x_ml = smem_u32(S.q[1]) + 32 * (A + 4) * 4 + lane * 8;
+  Items<Smem<A>> items;
+  uint32_t n = 0, ns = 0, nt = 0;      // key tiles of all items; this side's; items in which this side has tiles
+  for (uint32_t i = 0;; ++i) {
+    const Item* item = items.next(P, S);
+    if (!item) break;
+    const int a0 = item->a, b0 = item->b, pos = item->ctx, head = item->g * G + row;
+    const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
+    const bool began = a0 > item->first, cut = began || b0 < item->end;
+    const size_t at = ((size_t)item->q0 * P.n_q_heads + head) * A;
+    bool ok = true;
+    float fq = 0.f;
+    if (side == 0) {
+      ok = i == 0 || wwait(P, S, &S.q_free, (i - 1) & 1);    // every S of the item before is done
+      if (ok) fq = make_query<A, true>(P, S, 0, row, item->q0, head, row < G);
+    } else if (works) {
+      fq = make_query<A, false>(P, S, 0, row, item->q0, head, row < G);
+    }
+    items.done(S);
+    if (!ok) break;
+    if (works) {
+      float m = kNegInf, l = 0.f;
+      const bool any = a0 + side < b0;
+      for (int j = a0 + side; j < b0; j += 2, ++ns) {
+        const uint32_t nj = n + (j - a0);
+        ok = j > a0 + side || wwait(P, S, &S.s_full[side], ns & 1);
+        ok = ok && wwait(P, S, &S.fk_full[nj & 3], (nj >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);
+        if (!ok) break;
+        tc_fence_after();
+        softmax_tile<A>(S, s_t, o_t, side, nj, j * kTileN, j == a0 + side, fq, lo, pos, m, l);
+      }
+      if (any) {
+        ok = ok && wwait(P, S, &S.o_full[side], nt & 1);
+        ++nt;
+      }
+      if (!ok) {
+        S.abort = 1;
+        break;
+      }
+      tc_fence_after();
+      if (side == 1) {
+        if (!wwait(P, S, &S.x_empty, (i & 1) ^ 1)) break;
+        if (any) {
+#pragma unroll 1
+          for (int c = 0; c < A / 32; ++c) {
+            float o[32];
+            tmem_ld32(o_t + 32 * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              sts128(x_row + 128 * c + 16 * k, make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                                          __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
+          }
+        }
+        sts32(x_ml, __float_as_uint(m));
+        sts32(x_ml + 4, __float_as_uint(l));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.x_full);
+          if (any) mbar_arrive(&S.o_free[1]);
+        }
+      } else {
+        if (!wwait(P, S, &S.x_full, i & 1)) break;
+        const float mb = lds32f(x_ml), lb = lds32f(x_ml + 4);
+        const bool with_b = b0 - a0 > 1;
+        // -inf: no key seen, or NaNs only (then l is one)
+        const float mm = fmaxf(m, mb);
+        const float fa = m == kNegInf ? (l != 0.f ? 1.f : 0.f) : ex2(m - mm), fb = mb == kNegInf ? (lb != 0.f ? 1.f : 0.f) : ex2(mb - mm);
+        const float ls = fa * l + fb * lb, inv = 1.f / ls;
+        const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows + row;
+        if (cut && row < G) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(mm, ls);
+#pragma unroll 1
+        for (int c = 0; c < A / 32; ++c) {
+          float o[32];
+          tmem_ld32(o_t + 32 * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint4 x = with_b ? lds128(x_row + 128 * c + 16 * k) : make_uint4(0, 0, 0, 0);
+            o[4 * k] = (o[4 * k] * fa + __uint_as_float(x.x) * fb) * inv;
+            o[4 * k + 1] = (o[4 * k + 1] * fa + __uint_as_float(x.y) * fb) * inv;
+            o[4 * k + 2] = (o[4 * k + 2] * fa + __uint_as_float(x.z) * fb) * inv;
+            o[4 * k + 3] = (o[4 * k + 3] * fa + __uint_as_float(x.w) * fb) * inv;
+          }
+          if (cut && row < G) {
+            float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else if (row < G) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(P.out + at + 32 * c + 8 * k) =
+                  make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
+                             pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.x_empty);
+          mbar_arrive(&S.o_free[0]);
+        }
+      }
+    }
+    n += b0 - a0;
+  }
+}
+
+template <int A, int G, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_fp8_kernel(const Fp8Step P, const Fp8Partials W, const int min_q, const __grid_constant__ CUtensorMap kmap) {
+    chunk_fp8_kernel(const Fp8Step P, const Fp8Partials W, const __grid_constant__ CUtensorMap kmap) {
   constexpr int TOK = kTileM / G;
   extern __shared__ uint8_t smem_raw[];
   Smem<A>& S = *reinterpret_cast<Smem<A>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -763,11 +974,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.v_full[i], 4);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i][0], 4);
-      mbar_init(&S.p_full[i][1], 4);
+      mbar_init(&S.p_full[i][0], ONE ? 1 : 4);
+      mbar_init(&S.p_full[i][1], ONE ? 1 : 4);
       mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.o_free[i], 4);
+      mbar_init(&S.o_free[i], ONE ? 1 : 4);
     }
+    mbar_init(&S.q_free, 1);
+    mbar_init(&S.x_full, 1);
+    mbar_init(&S.x_empty, 1);
     for (int i = 0; i < 4; ++i) mbar_init(&S.fk_full[i], 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&S.item_full[i], 1);
@@ -783,22 +997,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  make_plan<A, TOK>(P, W, S, tpre, ipre, min_q);
+  make_plan<A, TOK, ONE>(P, W, S, tpre, ipre);
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // registers of the four warpgroups: 2 x 176 + 72 + 88 = 4 x 128, what the launch holds
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    softmax<A, G>(P, W, S, warp >> 2);
+    if constexpr (ONE)
+      softmax_one<A, G>(P, W, S, warp >> 2);
+    else
+      softmax<A, G>(P, W, S, warp >> 2);
   } else if (warp < 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     convert<A>(P, S);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp == 12) issue<A>(P, S);
+    if (warp == 12) {
+      if constexpr (ONE)
+        issue_one<A>(P, S);
+      else
+        issue<A>(P, S);
+    }
     if (warp == 13) load_tiles<A>(P, &kmap, S);
-    if (warp == 14) publish<A, TOK>(P, S, tpre, ipre, min_q);
+    if (warp == 14) publish<A, TOK, ONE>(P, S, tpre, ipre);
   }
   tc_fence_before();
   __syncthreads();
@@ -809,10 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining the pieces
-// For every row of every item cut between CTAs: M = max m_i, out = sum 2^(m_i -
-// M) o_i / sum 2^(m_i - M) l_i, in the pieces' order.  A CTA takes 32 rows of an
-// item, a warp 4 of them, lane = A / 32 dimensions.
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+// A CTA takes 8 rows of an item at a time, a warp per row.
+constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;
 template <int A>
 __global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int group) {
   constexpr int D = A / 32;
@@ -821,14 +1041,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = kTileM / group;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
-    int n = 0;
-    for (int b0 = 0; b0 < ctas; b0 += 32) {
-      const int b = b0 + lane;
-      const bool has = b < ctas && W.rec[b].n > 1;
-      const unsigned mask = __ballot_sync(0xffffffffu, has);
-      if (has) owner[n + __popc(mask & ((1u << lane) - 1))] = b;
-      n += __popc(mask);
-    }
+    const int n = join_owners(W, ctas, owner);
     if (lane == 0) n_owner = n;
   }
   __syncthreads();
@@ -836,29 +1049,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step 
     const int b = owner[task / (kRows / kJoinRows)];
     const Fp8Rec rec = W.rec[b];
     const int q0 = __ldg(P.cu_q_lens + rec.r), q_len = __ldg(P.cu_q_lens + rec.r + 1) - q0;
+    const int row = (task % (kRows / kJoinRows)) * kJoinRows + warp;
+    const int ti = rec.pad * 2 * tok + row / group;            // rows of tile B follow tile A's: its tokens do too
+    if (ti >= q_len) continue;
+    float o[D];
+    join_row<A>(W, kRows, b, rec.n, row, 0, 1, o);
+    uint16_t* dst = P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = (task % (kRows / kJoinRows)) * kJoinRows + warp * 4 + i;
-      const int ti = rec.pad * 2 * tok + row / group;          // rows of tile B follow tile A's: its tokens do too
-      if (ti >= q_len) continue;
-      auto piece = [&](int k) { return (size_t)(k == 0 ? 2 * b + 1 : 2 * (b + k)) * kRows + row; };
-      float M = kNegInf;
-      for (int k = 0; k < rec.n; ++k) M = fmaxf(M, W.ml[piece(k) * 2]);
-      float L = 0.f, o[D];
-#pragma unroll
-      for (int d = 0; d < D; ++d) o[d] = 0.f;
-      for (int k = 0; k < rec.n; ++k) {
-        const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(k) * 2);
-        const float w = ml.x == kNegInf ? (ml.y != 0.f ? 1.f : 0.f) : ex2(ml.x - M);   // -inf: no key seen, or NaNs only
-        L += w * ml.y;
-        const float* src = W.acc + piece(k) * A + lane * D;
-#pragma unroll
-        for (int d = 0; d < D; ++d) o[d] += w * src[d];
-      }
-      uint16_t* dst = P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D;
-#pragma unroll
-      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d] / L, o[d + 1] / L);
-    }
+    for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d], o[d + 1]);
   }
 }
 
@@ -868,14 +1066,14 @@ size_t smem_bytes(int n_reqs) {
 }
 static_assert(sizeof(Smem<128>) + 1024 + (kMaxReqs + 1) * 8 <= kSmemLimit, "shared memory");
 
-template <int A, int G>
-cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream) {
+template <int A, int G, bool ONE>
+cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
   CUtensorMap km;
   const long long rows = (long long)s.cache.num_blocks * s.cache.n_kv_heads * kBlockSize;
   if (!encode_byte_rows(&km, s.cache.k, rows, A, kBlockSize)) return cudaErrorInvalidValue;
-  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(chunk_fp8_kernel<A, G>), kSmemLimit);
+  cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(chunk_fp8_kernel<A, G, ONE>), kSmemLimit);
   if (e != cudaSuccess) return e;
-  chunk_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, min_q, km);
+  chunk_fp8_kernel<A, G, ONE><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, km);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -904,20 +1102,22 @@ Fp8Partials fp8_chunk_partials(void* workspace) {
   return w;
 }
 
-cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream) {
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, cudaStream_t stream) {
   const int a = s.cache.head_dim, g = s.n_q_heads / s.cache.n_kv_heads;
-#define CB_CASE(A_, G_) \
-  if (a == A_ && g == G_) return launch_t<A_, G_>(s, w, min_q, grid, stream);
-  CB_CASE(128, 1)
-  CB_CASE(128, 2)
-  CB_CASE(128, 4)
-  CB_CASE(128, 8)
-  CB_CASE(128, 16)
-  CB_CASE(128, 32)
-  CB_CASE(64, 1)
-  CB_CASE(64, 2)
-  CB_CASE(64, 4)
-  CB_CASE(64, 8)
+#define CB_CASE(A_, G_, ONE_) \
+  if (a == A_ && g == G_ && single == ONE_) return launch_t<A_, G_, ONE_>(s, w, grid, stream);
+  CB_CASE(128, 1, false)
+  CB_CASE(128, 2, false)
+  CB_CASE(128, 4, false)
+  CB_CASE(128, 8, false)
+  CB_CASE(128, 16, false)
+  CB_CASE(128, 16, true)
+  CB_CASE(128, 32, false)
+  CB_CASE(128, 32, true)
+  CB_CASE(64, 1, false)
+  CB_CASE(64, 2, false)
+  CB_CASE(64, 4, false)
+  CB_CASE(64, 8, false)
 #undef CB_CASE
   return cudaErrorInvalidValue;
 }

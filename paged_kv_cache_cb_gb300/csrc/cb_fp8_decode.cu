@@ -92,6 +92,7 @@ struct alignas(1024) Smem {
   float cf[2][X::C];                 // per group: scale log2(e) 2^eq per column
   float alpha[2][2][X::C];           // factors of O when M moves
   float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // a segment's l, m, M, then l, m per head and the slots' factors
+  float si[2][X::C];                 // 1 / l per head
   uint64_t k_full[X::KS], k_empty[X::KS], v_full[X::VS], v_empty[X::VS];
   uint64_t e_full[X::ES], e_empty[X::ES], s_full[X::SB], s_empty[X::SB], p_full[X::PB], pv_done[X::PB];
   uint64_t q_full[2], o_full[2], o_free[X::OB], turn[2], drain[2];
@@ -410,6 +411,7 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int gr
   constexpr int B = 8;                       // heads in flight
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int heads = hg_heads * G, bpt = 8 / hg_heads;
+  const uint32_t q_at = smem_u32(S.q[grp]);
   const uint16_t* src = P.q + ((size_t)s.tok * P.n_q_heads + (size_t)s.hg * heads) * A + lane * D;
   for (int h0 = warp; h0 < heads; h0 += 4 * B) {
     uint32_t w[B][D / 2];
@@ -450,10 +452,9 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int gr
         for (int t = 0; t < 2; ++t) {
           const int row = t * Cfg<A, G>::C + col;
           if constexpr (A == 128) {
-            *reinterpret_cast<uint32_t*>(&S.q[grp][row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4]) = t ? c1 : c0;
+            sts32(q_at + row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4, t ? c1 : c0);
           } else {
-            *reinterpret_cast<uint16_t*>(&S.q[grp][row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2]) =
-                (uint16_t)(t ? c1 : c0);
+            sts16(q_at + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2, t ? c1 : c0);
           }
         }
         if (lane == 0) S.cf[grp][col] = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
@@ -472,11 +473,14 @@ __device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
   using X = Cfg<A, G>;
   const int t = threadIdx.x & 127, warp = t >> 5, bpt = 8 / hg_heads, heads = hg_heads * G;
   if (A == 64 && warp >= 2) return;          // rows 64 .. 127 repeat 0 .. 63
-  const uint32_t base = o_tmem + ((uint32_t)(warp * 32) << 16);
+  const uint32_t base = o_tmem + ((uint32_t)(warp * 32) << 16), sw = smem_u32(S.sw[grp]);
   for (int hh = 0; hh < hg_heads; ++hh) {
-    float acc[G];
+    float acc[G], inv[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) acc[g] = 0.f;
+    for (int g = 0; g < G; ++g) {
+      acc[g] = 0.f;
+      inv[g] = lds32f(smem_u32(&S.si[grp][hh * G + g]));
+    }
     for (int bi = 0; bi < bpt; ++bi) {
       const int slot = bi * hg_heads + hh;
       float o[X::SS];
@@ -490,21 +494,20 @@ __device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
       tmem_wait_ld();
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float f = S.sw[grp][slot * G + g];
-        acc[g] += ((o[g] + o[G + g] + o[2 * G + g]) * f) * (f * (1.f / S.sl[grp][hh * G + g]));
+        const float f = lds32f(sw + (slot * G + g) * 4);
+        acc[g] += ((o[g] + o[G + g] + o[2 * G + g]) * f) * (f * inv[g]);
       }
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int h = hh * G + g;
-      const float l = S.sl[grp][h];
       if (whole) {
         P.out[((size_t)s.tok * P.n_q_heads + (size_t)s.hg * heads + h) * A + t] =
             __bfloat16_as_ushort(__float2bfloat16_rn(acc[g]));
       } else {
         const size_t at = (size_t)slot_out * kMaxHeads + h;
         W.acc[at * A + t] = acc[g];
-        if (t == 0) *reinterpret_cast<float2*>(W.ml + at * 2) = make_float2(S.sm[grp][h], l);
+        if (t == 0) *reinterpret_cast<float2*>(W.ml + at * 2) = make_float2(S.sm[grp][h], S.sl[grp][h]);
       }
     }
   }
@@ -704,6 +707,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       S.sw[grp][tid] = hw;
       if (tid < hg_heads * G) {
         S.sl[grp][tid] = hl;
+        S.si[grp][tid] = 1.f / hl;
         S.sm[grp][tid] = hm;
       }
     }
@@ -790,10 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining the pieces
-// For every sequence cut between CTAs and every query head of it: M = max m_i,
-// W_i = 2^(m_i - M) l_i, out = sum W_i o_i / sum W_i, in the pieces' order.
-// A warp takes a (sequence, head), lane = A / 32 dimensions; where there are
-// fewer of those than CTAs, a CTA does, its warps taking the pieces in turn.
+// A warp takes a (sequence, head); where there are fewer of those than CTAs, a CTA
+// does, its warps taking the pieces in turn.
 constexpr int kJoinThreads = 256;
 template <int A>
 __global__ void __launch_bounds__(kJoinThreads) join_fp8_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int hg_heads) {
@@ -804,63 +806,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_fp8_kernel(const Fp8Step P,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = hg_heads * (P.n_q_heads / P.cache.n_kv_heads);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
-    int n = 0;
-    for (int b0 = 0; b0 < ctas; b0 += 32) {
-      const int b = b0 + lane;
-      const bool has = b < ctas && W.rec[b].n > 1;
-      const unsigned mask = __ballot_sync(0xffffffffu, has);
-      if (has) owner[n + __popc(mask & ((1u << lane) - 1))] = b;
-      n += __popc(mask);
-    }
+    const int n = join_owners(W, ctas, owner);
     if (lane == 0) n_owner = n;
   }
   __syncthreads();
   const int tasks = n_owner * heads;
   const bool by_cta = tasks <= (int)gridDim.x;
-  const int step = by_cta ? NW : 1, first = by_cta ? warp : 0;
   for (int task = by_cta ? blockIdx.x : blockIdx.x * NW + warp; task < tasks; task += by_cta ? gridDim.x : gridDim.x * NW) {
     const int b = owner[task / heads], h = task % heads;
     const Fp8Rec rec = W.rec[b];
-    auto piece = [&](int i) { return (size_t)(i == 0 ? 2 * b + 1 : 2 * (b + i)) * kMaxHeads + h; };
-    float M = kNegInf, L = 0.f;
-    for (int i = lane; i < rec.n; i += 32) M = fmaxf(M, W.ml[piece(i) * 2]);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    for (int i = lane; i < rec.n; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(i) * 2);
-      L += ml.x == kNegInf ? ml.y : ex2(ml.x - M) * ml.y;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    const int t = __ldg(P.cu_q_lens + rec.r);
     float o[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) o[d] = 0.f;
-    for (int i0 = first; i0 < rec.n; i0 += 8 * step) {
-      float y[8][D], w[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int i = i0 + u * step;
-        w[u] = 0.f;
-#pragma unroll
-        for (int d = 0; d < D; ++d) y[u][d] = 0.f;
-        if (i < rec.n) {
-          const float2 ml = *reinterpret_cast<const float2*>(W.ml + piece(i) * 2);
-          const float* src = W.acc + piece(i) * A + lane * D;
-          w[u] = ml.x == kNegInf ? ml.y : ex2(ml.x - M) * ml.y;      // -inf: a piece of NaNs only
-          if constexpr (D == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            y[u][0] = v.x, y[u][1] = v.y, y[u][2] = v.z, y[u][3] = v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            y[u][0] = v.x, y[u][1] = v.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-#pragma unroll
-        for (int d = 0; d < D; ++d) o[d] += w[u] * y[u][d];
-    }
+    join_row<A>(W, kMaxHeads, b, rec.n, h, by_cta ? warp : 0, by_cta ? NW : 1, o);
     if (by_cta) {
 #pragma unroll
       for (int d = 0; d < D; ++d) red[warp][lane * D + d] = o[d];
@@ -874,10 +831,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_fp8_kernel(const Fp8Step P,
       }
     }
     if (!by_cta || warp == 0) {
-      const int t = __ldg(P.cu_q_lens + rec.r);
       uint16_t* dst = P.out + ((size_t)t * P.n_q_heads + (size_t)rec.hg * heads + h) * A + lane * D;
 #pragma unroll
-      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d] / L, o[d + 1] / L);
+      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d], o[d + 1]);
     }
     if (by_cta) __syncthreads();
   }

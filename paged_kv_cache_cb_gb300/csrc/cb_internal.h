@@ -161,11 +161,12 @@ Fp8Partials fp8_partials(void* workspace);
 bool fp8_decode_shape(int head_dim, int group);
 // The requests with one new token, on `grid` CTAs (at most one per SM), and the join of their pieces.
 cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream);
-// The requests with at least min_q new tokens, and the join of their pieces.  Partial
-// results: as above, per CTA two times [256 rows][A] values and [256][2] (max, sum).
+// The requests with several new tokens, or (single) those with one where
+// launch_decode_fp8 has no kernel, and the join of their pieces.  Partial results:
+// as above, per CTA two times [256 rows][A] values and [256][2] (max, sum).
 size_t fp8_chunk_partials_bytes(int head_dim);
 Fp8Partials fp8_chunk_partials(void* workspace);
-cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, int min_q, int grid, cudaStream_t stream);
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, cudaStream_t stream);
 
 // Library state that the entry points of other files use (cb_api.cu).
 unsigned int* stream_error_word(cudaStream_t stream, int* rc);   // nullptr: return *rc
