@@ -53,7 +53,7 @@ struct Item {
   int r, g, pair, q0, q_len, ctx, tok_lo, tok_hi, first, end, a, b, sides, pad[3];
 };
 constexpr int kItems = 4;              // published ahead
-constexpr int kReaders = 14;           // warps that read them
+constexpr int kReaders = 14;              // warps that read them
 
 template <int A>
 struct alignas(1024) Smem {
@@ -66,7 +66,7 @@ struct alignas(1024) Smem {
   uint32_t v_nan[4][4];                // keys whose V stands for NaNs (stored as zeros)
   uint8_t ex[2][2][128];               // the tile's exponent bytes, K and V
   uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], q_free, x_full, x_empty, drain, item_full[kItems], item_empty[kItems];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], q_free, x_bar, drain, item_full[kItems], item_empty[kItems];
   Item item[kItems];
   int scan[16], iscan[16], tiles, u0, u1, items, longest, whole, eff;
   uint32_t tmem;
@@ -378,15 +378,15 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
         ++n;
         break;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&S.vr_full[st], blocks * (kBlockSize * A + 2 * kBlockSize));
+      if (lane == 0) mbar_arrive_expect_tx(&S.vr_full[st], blocks * kBlockSize * A);
       __syncwarp();
-      if (have) {
-        bulk_load(&S.vr[st][lane * kBlockSize * A], P.cache.v + (size_t)row * A, kBlockSize * A, &S.vr_full[st]);
-        bulk_load(&S.ex[st][0][lane * kBlockSize], P.cache.k_exps + row, kBlockSize, &S.vr_full[st]);
-        bulk_load(&S.ex[st][1][lane * kBlockSize], P.cache.v_exps + row, kBlockSize, &S.vr_full[st]);
-      }
+      if (have) bulk_load(&S.vr[st][lane * kBlockSize * A], P.cache.v + (size_t)row * A, kBlockSize * A, &S.vr_full[st]);
+      // the exponents: lanes 0 .. 7 K's, 8 .. 15 V's
+      if (lane < 16 && e >= 0) cp_async16(&S.ex[st][lane >> 3][(lane & 7) * kBlockSize], (lane < 8 ? P.cache.k_exps : P.cache.v_exps) + row);
+      cp_async_arrive(&S.vr_full[st]);
     }
   }
+  cp_async_wait_all();
   if (!ok)                             // copies already issued land before the CTA exits
     for (uint32_t i = n > 2u ? n - 2 : 0; i < n; ++i) {
       mbar_wait(&S.k_full[i & 1], (i >> 1) & 1, 20000000ull);
@@ -593,9 +593,9 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
       t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
       t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
     }
-    const int at = row * A + ((A == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-    *reinterpret_cast<uint4*>(&S.q[side][0][at]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-    *reinterpret_cast<uint4*>(&S.q[side][1][at]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    const uint32_t at = smem_u32(S.q[side]) + row * A + ((A == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+    sts128(at, make_uint4(t0[0], t0[1], t0[2], t0[3]));
+    sts128(at + 128 * A, make_uint4(t1[0], t1[1], t1[2], t1[3]));
   }
   fence_proxy_async_smem();
   mbar_arrive(&S.q_full[side]);
@@ -760,12 +760,13 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
 }
 
 // ---------------------------------------------------------------- single tokens (groups of 16 and 32 heads)
-// A step's requests with one new token: an item is (request, KV head), its G
-// rows are the first of a query tile.  Both tiles of tensor memory take the same
-// rows, A the even key tiles and B the odd ones, so that one's softmax runs under
-// the other's products as with two query tiles; at the end B hands (m, l, O) to A
-// through shared memory (Q's second tile, not used here).  Only one warp of each
-// side has rows.
+// A step's requests with one new token: an item is (request, KV head) with G rows.
+// A query tile holds them four times, at rows 0, 32, 64 and 96, and warp w's copy
+// takes the tile's keys 32 w .. 32 w + 31 only (its weights of the others are zeros),
+// so that the four warps of a tile share its softmax.  Both tiles of tensor memory
+// take the same rows, A the even key tiles and B the odd ones, and one's softmax
+// runs under the other's products.  At the end of an item the eight copies' (m, l,
+// O) are joined through shared memory (Q's second tile, not used here).
 template <int A>
 __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
   constexpr uint32_t kIdescS = idesc_f8(128, 128, 0, 0, 0, 0), kIdescO = idesc_bf16_f32(128, A, 1);
@@ -791,22 +792,17 @@ __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
         if (t >= 2 && t - 2 < len) {   // O += P V of this side's tile before
           ok = ok && wwait(P, S, &S.v_full[st], ((n + t - 2) >> 1) & 1);
           if (t < 4) ok = ok && wwait(P, S, &S.o_free[side], ((side ? nb : i) & 1) ^ 1);
+          ok = ok && wwait(P, S, &S.p_full[side][0], np[side] & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && wwait(P, S, &S.p_full[side][h], np[side] & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                tc_mma_f16_ts(o_t, s_t + ks * 8, vd + (uint32_t)((st * kTile + ks * 16 * 128) >> 4), kIdescO, (t >= 4 || ks > 0) ? 1u : 0u);
-              if (h == 1) {
-                tc_commit(&S.v_empty[st]);
-                if (t >= len) tc_commit(&S.o_full[side]);
-              }
-            }
-            __syncwarp();
+            for (int ks = 0; ks < 8; ++ks)
+              tc_mma_f16_ts(o_t, s_t + ks * 8, vd + (uint32_t)((st * kTile + ks * 16 * 128) >> 4), kIdescO, (t >= 4 || ks > 0) ? 1u : 0u);
+            tc_commit(&S.v_empty[st]);
+            if (t >= len) tc_commit(&S.o_full[side]);
           }
+          __syncwarp();
           ++np[side];
         }
         if (t < len) {
@@ -840,117 +836,183 @@ __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
   mbar_wait(&S.drain, 0, 20000000ull);
 }
 
+// Bounded meeting of the eight softmax warps (phase: counted by the caller).
+template <class SM>
+__device__ __forceinline__ bool meet(const Fp8Step& P, SM& S, uint32_t& phase) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&S.x_bar);
+  return wwait(P, S, &S.x_bar, phase++ & 1);
+}
+
 template <int A, int G>
 __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int side) {
-  static_assert(G <= 32 && 32 * (A + 4) * 4 + 256 <= (int)sizeof(S.q[1]), "B's rows fit in Q's second tile");
-  const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
-  const bool works = row < 32;
-  const uint32_t s_t = S.tmem + side * 128, o_t = S.tmem + 256 + side * A;   // warps 0 and 4: lanes 0 .. 31
-  const uint32_t x_row = smem_u32(S.q[1]) + lane * (A + 4) * 4, x_ml = smem_u32(S.q[1]) + 32 * (A + 4) * 4 + lane * 8;
+  static_assert(G <= 32 && 8 * 32 * 32 * 4 <= (int)sizeof(S.q[1]), "a quarter of the copies' O fits in Q's second tile");
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, copy = 4 * side + w;
+  const uint32_t lanes = (uint32_t)(32 * w) << 16;
+  const uint32_t s_t = S.tmem + lanes + side * 128, o_t = S.tmem + lanes + 256 + side * A, xs = smem_u32(S.q[1]);
   Items<Smem<A>> items;
-  uint32_t n = 0, ns = 0, nt = 0;      // key tiles of all items; this side's; items in which this side has tiles
+  uint32_t n = 0, ns = 0, nt = 0, phase = 0;   // key tiles of all items; this side's; items in which this side has tiles
   for (uint32_t i = 0;; ++i) {
     const Item* item = items.next(P, S);
     if (!item) break;
-    const int a0 = item->a, b0 = item->b, pos = item->ctx, head = item->g * G + row;
+    const int a0 = item->a, b0 = item->b, pos = item->ctx, g = item->g;
     const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
+    const unsigned span = (unsigned)(pos - lo);                // key k is visible iff (unsigned)(k - lo) <= span
     const bool began = a0 > item->first, cut = began || b0 < item->end;
-    const size_t at = ((size_t)item->q0 * P.n_q_heads + head) * A;
+    const int tok = item->q0, head = g * G + lane;
     bool ok = true;
     float fq = 0.f;
     if (side == 0) {
-      ok = i == 0 || wwait(P, S, &S.q_free, (i - 1) & 1);    // every S of the item before is done
-      if (ok) fq = make_query<A, true>(P, S, 0, row, item->q0, head, row < G);
-    } else if (works) {
-      fq = make_query<A, false>(P, S, 0, row, item->q0, head, row < G);
+      ok = i == 0 || wwait(P, S, &S.q_free, (i - 1) & 1);      // every S of the item before is done
+      if (ok) fq = make_query<A, true>(P, S, 0, 32 * w + lane, tok, head, lane < G);
+    } else {
+      fq = make_query<A, false>(P, S, 0, 0, tok, head, lane < G);
     }
     items.done(S);
     if (!ok) break;
-    if (works) {
-      float m = kNegInf, l = 0.f;
-      const bool any = a0 + side < b0;
-      for (int j = a0 + side; j < b0; j += 2, ++ns) {
-        const uint32_t nj = n + (j - a0);
-        ok = j > a0 + side || wwait(P, S, &S.s_full[side], ns & 1);
-        ok = ok && wwait(P, S, &S.fk_full[nj & 3], (nj >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);
-        if (!ok) break;
-        tc_fence_after();
-        softmax_tile<A>(S, s_t, o_t, side, nj, j * kTileN, j == a0 + side, fq, lo, pos, m, l);
-      }
-      if (any) {
-        ok = ok && wwait(P, S, &S.o_full[side], nt & 1);
-        ++nt;
-      }
-      if (!ok) {
-        S.abort = 1;
-        break;
-      }
+    float m = kNegInf, l = 0.f;
+    const bool any = a0 + side < b0;
+    for (int j = a0 + side; j < b0; j += 2, ++ns) {
+      const uint32_t nj = n + (j - a0);
+      // (the factors' barrier: see softmax())
+      ok = j > a0 + side || wwait(P, S, &S.s_full[side], ns & 1);
+      ok = ok && wwait(P, S, &S.fk_full[nj & 3], (nj >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);
+      if (!ok) break;
       tc_fence_after();
-      if (side == 1) {
-        if (!wwait(P, S, &S.x_empty, (i & 1) ^ 1)) break;
-        if (any) {
-#pragma unroll 1
-          for (int c = 0; c < A / 32; ++c) {
-            float o[32];
-            tmem_ld32(o_t + 32 * c, o);
-            tmem_wait_ld();
+      float s[32];
+      tmem_ld32(s_t + 32 * w, s);
+      const uint32_t fk = smem_u32(&S.fk[nj & 3][32 * w]);
+      const uint32_t vn = __float_as_uint(lds32f(smem_u32(&S.v_nan[nj & 3][w])));
+      const int key = j * kTileN + 32 * w;
+      tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              sts128(x_row + 128 * c + 16 * k, make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
-                                                          __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
-          }
+      for (int k = 0; k < 8; ++k) {
+        const uint4 f = lds128(fk + 16 * k);
+        f2split(fmul2(f2(s[4 * k], s[4 * k + 1]), f2(__uint_as_float(f.x), __uint_as_float(f.y))), s[4 * k], s[4 * k + 1]);
+        f2split(fmul2(f2(s[4 * k + 2], s[4 * k + 3]), f2(__uint_as_float(f.z), __uint_as_float(f.w))), s[4 * k + 2], s[4 * k + 3]);
+      }
+      if (key + 31 > pos || key < lo || vn != 0) {             // the same in every lane
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          if ((vn >> k) & 1) s[k] = __uint_as_float(0x7FC00000u);
+          if ((unsigned)(key + k - lo) > span) s[k] = kNegInf;
         }
-        sts32(x_ml, __float_as_uint(m));
-        sts32(x_ml + 4, __float_as_uint(l));
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.x_full);
-          if (any) mbar_arrive(&S.o_free[1]);
-        }
-      } else {
-        if (!wwait(P, S, &S.x_full, i & 1)) break;
-        const float mb = lds32f(x_ml), lb = lds32f(x_ml + 4);
-        const bool with_b = b0 - a0 > 1;
-        // -inf: no key seen, or NaNs only (then l is one)
-        const float mm = fmaxf(m, mb);
-        const float fa = m == kNegInf ? (l != 0.f ? 1.f : 0.f) : ex2(m - mm), fb = mb == kNegInf ? (lb != 0.f ? 1.f : 0.f) : ex2(mb - mm);
-        const float ls = fa * l + fb * lb, inv = 1.f / ls;
-        const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows + row;
-        if (cut && row < G) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(mm, ls);
+      }
+      float a[2] = {kNegInf, kNegInf};
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) a[(k >> 1) & 1] = max3(a[(k >> 1) & 1], s[k], s[k + 1]);
+      const float mt = fmaxf(a[0], a[1]) * fq;
+      const bool need = mt > m + 8.f;
+      float alpha = 1.f;
+      if (need) {
+        alpha = ex2(m - mt);
+        m = mt;
+      }
+      if (j > a0 + side && __any_sync(FULL, need)) {
 #pragma unroll 1
-        for (int c = 0; c < A / 32; ++c) {
-          float o[32];
-          tmem_ld32(o_t + 32 * c, o);
+        for (int c = 0; c < A / 8; ++c) {
+          float o[8];
+          tmem_ld8(o_t + c * 8, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint4 x = with_b ? lds128(x_row + 128 * c + 16 * k) : make_uint4(0, 0, 0, 0);
-            o[4 * k] = (o[4 * k] * fa + __uint_as_float(x.x) * fb) * inv;
-            o[4 * k + 1] = (o[4 * k + 1] * fa + __uint_as_float(x.y) * fb) * inv;
-            o[4 * k + 2] = (o[4 * k + 2] * fa + __uint_as_float(x.z) * fb) * inv;
-            o[4 * k + 3] = (o[4 * k + 3] * fa + __uint_as_float(x.w) * fb) * inv;
-          }
-          if (cut && row < G) {
-            float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else if (row < G) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              *reinterpret_cast<uint4*>(P.out + at + 32 * c + 8 * k) =
-                  make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                             pack_bf16(o[8 * k + 4], o[8 * k + 5]), pack_bf16(o[8 * k + 6], o[8 * k + 7]));
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.x_empty);
-          mbar_arrive(&S.o_free[0]);
+          for (int k = 0; k < 8; ++k) o[k] *= alpha;
+          tmem_st8(o_t + c * 8, o);
         }
       }
+      const float mr = m == kNegInf ? 0.f : m;                 // no key seen yet: every weight is 0
+      const uint64_t fq2 = f2(fq, fq), nm2 = f2(-mr, -mr);
+      uint64_t sum[2] = {0ull, 0ull};
+      uint32_t pk[16], zero[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        float t0, t1;
+        f2split(ffma2(f2(s[2 * k], s[2 * k + 1]), fq2, nm2), t0, t1);
+        t0 = ex2(t0);
+        t1 = ex2(t1);
+        sum[k & 1] = fadd2(sum[k & 1], f2(t0, t1));
+        pk[k] = pack_bf16(t0, t1);
+        zero[k] = 0u;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q == w)
+          tmem_st16u(s_t + 16 * q, pk);
+        else
+          tmem_st16u(s_t + 16 * q, zero);
+      }
+      float r0, r1, r2, r3;
+      f2split(sum[0], r0, r1);
+      f2split(sum[1], r2, r3);
+      l = l * alpha + ((r0 + r1) + (r2 + r3));
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[side][0]);
     }
+    if (any) {
+      ok = ok && wwait(P, S, &S.o_full[side], nt & 1);
+      ++nt;
+    }
+    if (!ok) {
+      S.abort = 1;
+      break;
+    }
+    tc_fence_after();
+    // the copies' maxima and sums, then their O a quarter of the dimensions at a time
+    sts32(xs + (copy * 32 + lane) * 8, __float_as_uint(m));
+    sts32(xs + (copy * 32 + lane) * 8 + 4, __float_as_uint(l));
+    if (!meet(P, S, phase)) break;
+    float mm = kNegInf, ls = 0.f;
+    for (int c = 0; c < 8; ++c) mm = fmaxf(mm, lds32f(xs + (c * 32 + lane) * 8));
+    for (int c = 0; c < 8; ++c) {
+      const float mc = lds32f(xs + (c * 32 + lane) * 8), lc = lds32f(xs + (c * 32 + lane) * 8 + 4);
+      ls += mc == kNegInf ? lc : ex2(mc - mm) * lc;            // -inf: no key seen, or NaNs only (then lc is one)
+    }
+    const float f = (m == kNegInf ? (l != 0.f ? 1.f : 0.f) : ex2(m - mm)) / ls;
+    const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows;
+    if (cut && copy == 0 && lane < G) *reinterpret_cast<float2*>(W.ml + (pr + lane) * 2) = make_float2(mm, ls);
+#pragma unroll 1
+    for (int c = 0; c < A / 32 && ok; ++c) {
+      float o[32];
+      if (any) {
+        tmem_ld32(o_t + 32 * c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      }
+      ok = meet(P, S, phase);                                  // what was there has been read
+      // row `lane` of this copy: 32 values, their 16-byte chunks in an order that spreads the banks
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        sts128(xs + (copy * 32 + lane) * 128 + ((k ^ (lane & 7)) << 4),
+               make_uint4(__float_as_uint(o[4 * k] * f), __float_as_uint(o[4 * k + 1] * f), __float_as_uint(o[4 * k + 2] * f),
+                          __float_as_uint(o[4 * k + 3] * f)));
+      ok = ok && meet(P, S, phase);
+      // 256 threads: row r, dimensions 4 k .. 4 k + 3
+      const int r = threadIdx.x >> 3, k = threadIdx.x & 7;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const uint4 x = lds128(xs + (q * 32 + r) * 128 + ((k ^ (r & 7)) << 4));
+        y[0] += __uint_as_float(x.x);
+        y[1] += __uint_as_float(x.y);
+        y[2] += __uint_as_float(x.z);
+        y[3] += __uint_as_float(x.w);
+      }
+      if (ok && r < G) {
+        if (cut)
+          *reinterpret_cast<float4*>(W.acc + (pr + r) * A + 32 * c + 4 * k) = make_float4(y[0], y[1], y[2], y[3]);
+        else
+          *reinterpret_cast<uint2*>(P.out + ((size_t)tok * P.n_q_heads + (size_t)g * G + r) * A + 32 * c + 4 * k) =
+              make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      }
+    }
+    if (!ok) break;
+    tc_fence_before();
+    if (!meet(P, S, phase)) break;                             // the exchange is free for the next item
+    if (lane == 0 && any) mbar_arrive(&S.o_free[side]);
     n += b0 - a0;
   }
 }
@@ -969,19 +1031,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.q_full[i], 128);
       mbar_init(&S.k_full[i], 1);
       mbar_init(&S.k_empty[i], 1);
-      mbar_init(&S.vr_full[i], 1);
+      mbar_init(&S.vr_full[i], 1 + 32);   // the values' copies; each lane's of the exponents
       mbar_init(&S.vr_empty[i], 4);
       mbar_init(&S.v_full[i], 4);
       mbar_init(&S.v_empty[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i][0], ONE ? 1 : 4);
-      mbar_init(&S.p_full[i][1], ONE ? 1 : 4);
+      mbar_init(&S.p_full[i][0], 4);
+      mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.o_free[i], ONE ? 1 : 4);
+      mbar_init(&S.o_free[i], 4);
     }
     mbar_init(&S.q_free, 1);
-    mbar_init(&S.x_full, 1);
-    mbar_init(&S.x_empty, 1);
+    mbar_init(&S.x_bar, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&S.fk_full[i], 4);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&S.item_full[i], 1);

@@ -310,24 +310,22 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
           ++n;
           break;
         }
-        const unsigned have = __ballot_sync(FULL, lane < bpt && e >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(&S.e_full[es], 2u * box * __popc(have));
-        __syncwarp();
-        if (lane < bpt && e >= 0) {
-          bulk_load(&S.ex[es][0][lane * box], P.cache.k_exps + row, box, &S.e_full[es]);
-          bulk_load(&S.ex[es][1][lane * box], P.cache.v_exps + row, box, &S.e_full[es]);
-        }
+        // exponents, 16 pieces of 16 bytes: lanes 0 .. 7 K's, 8 .. 15 V's, in the tile's order of rows
+        const int piece = lane & 7, pe = __shfl_sync(FULL, e, piece / hg_heads);
+        if (lane < 16 && pe >= 0)
+          cp_async16(&S.ex[es][lane >> 3][piece * kBlockSize],
+                     (lane < 8 ? P.cache.k_exps : P.cache.v_exps) +
+                         ((size_t)pe * Hkv + s.hg * hg_heads + piece % hg_heads) * kBlockSize);
+        cp_async_arrive(&S.e_full[es]);
       }
     }
     s = nx;
     more = again;
   }
+  if constexpr (IS_K) cp_async_wait_all();
   if (!ok) {
     // let the copies already issued land before the CTA exits
     for (uint32_t i = n > (uint32_t)NST ? n - NST : 0; i < n; ++i) mbar_wait(&full[i % NST], (i / NST) & 1, 20000000ull);
-    if constexpr (IS_K)
-      for (uint32_t i = n > (uint32_t)X::ES ? n - X::ES : 0; i < n; ++i)
-        mbar_wait(&S.e_full[i % X::ES], (i / X::ES) & 1, 20000000ull);
   }
 }
 
@@ -738,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.v_empty[i], 1);
     }
     for (int i = 0; i < X::ES; ++i) {
-      mbar_init(&S.e_full[i], 1);
+      mbar_init(&S.e_full[i], 32);
       mbar_init(&S.e_empty[i], 4);
     }
     for (int i = 0; i < X::SB; ++i) {
