@@ -53,7 +53,7 @@ struct Item {
   int r, g, pair, q0, q_len, ctx, tok_lo, tok_hi, first, end, a, b, sides, pad[3];
 };
 constexpr int kItems = 4;              // published ahead
-constexpr int kReaders = 14;              // warps that read them
+constexpr int kReaders = 15;           // warps that read them
 
 template <int A>
 struct alignas(1024) Smem {
@@ -63,6 +63,7 @@ struct alignas(1024) Smem {
   uint8_t vr[2][128 * A];              // V as in the cache, no swizzle
   uint8_t v[2][H][128][128];           // V in bf16
   float fk[4][128];                    // 2^ek of the tile's keys
+  float fq[4][32];                     // single tokens: the rows' factors, of four items
   uint32_t v_nan[4][4];                // keys whose V stands for NaNs (stored as zeros)
   uint8_t ex[2][2][128];               // the tile's exponent bytes, K and V
   uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
@@ -331,10 +332,11 @@ struct Items {
   }
 };
 
-// ---------------------------------------------------------------- loads (warp 13)
-// K into the swizzled operand layout, V and the exponent bytes as they are.
+// ---------------------------------------------------------------- loads (warps 13 and 15)
+// One warp brings K into the swizzled operand layout, the other (load_v) V and
+// the exponent bytes as they are: neither waits for the other's buffers.
 template <int A>
-__device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S) {
+__device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S, bool load_v) {
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, Hkv = P.cache.n_kv_heads, rows_total = P.cache.num_blocks * Hkv * kBlockSize;
   Items<Smem<A>> items;
@@ -361,22 +363,20 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
       if (t == 0) {
         cur = nxt;
         nxt = entry(j + 4);
-        if (cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);   // its rows count as zeros
+        if (cur == -1 && !load_v) set_error(P.err, CB_DEVERR_BADBLOCK);   // its rows count as zeros
       }
       const int e = __shfl_sync(FULL, cur, t * 8 + (lane & 7));
       const bool have = lane < 8 && e >= 0;
       const int row = e >= 0 ? (e * Hkv + g) * kBlockSize : rows_total;    // past the extent: zeros
       const unsigned blocks = __popc(__ballot_sync(FULL, have));
       const uint32_t st = n & 1, ph = ((n >> 1) & 1) ^ 1;
-      ok = wwait(P, S, &S.k_empty[st], ph);
+      ok = wwait(P, S, load_v ? &S.vr_empty[st] : &S.k_empty[st], ph);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&S.k_full[st], 128 * A);
-      __syncwarp();
-      if (lane < 8) tma_load_2d(&S.k[st][lane * kBlockSize * A], kmap, 0, row, &S.k_full[st]);
-      ok = wwait(P, S, &S.vr_empty[st], ph);
-      if (!ok) {
-        ++n;
-        break;
+      if (!load_v) {
+        if (lane == 0) mbar_arrive_expect_tx(&S.k_full[st], 128 * A);
+        __syncwarp();
+        if (lane < 8) tma_load_2d(&S.k[st][lane * kBlockSize * A], kmap, 0, row, &S.k_full[st]);
+        continue;
       }
       if (lane == 0) mbar_arrive_expect_tx(&S.vr_full[st], blocks * kBlockSize * A);
       __syncwarp();
@@ -388,10 +388,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
   }
   cp_async_wait_all();
   if (!ok)                             // copies already issued land before the CTA exits
-    for (uint32_t i = n > 2u ? n - 2 : 0; i < n; ++i) {
-      mbar_wait(&S.k_full[i & 1], (i >> 1) & 1, 20000000ull);
-      mbar_wait(&S.vr_full[i & 1], (i >> 1) & 1, 20000000ull);
-    }
+    for (uint32_t i = n > 2u ? n - 2 : 0; i < n; ++i) mbar_wait(load_v ? &S.vr_full[i & 1] : &S.k_full[i & 1], (i >> 1) & 1, 20000000ull);
 }
 
 // ---------------------------------------------------------------- conversion of V (warps 8-11)
@@ -423,7 +420,51 @@ __device__ __forceinline__ void widen16(const uint4& x, uint32_t f, uint32_t (&o
 __device__ __forceinline__ uint32_t factor1(uint32_t b) { return ((min(b, 134u) + 120u) << 7) * 0x10001u; }
 __device__ __forceinline__ uint32_t factor2(uint32_t b) { return ((max(b, 134u) - 134u + 127u) << 7) * 0x10001u; }
 
-template <int A>
+// This thread's query row as two e4m3 terms; returns its factor scale log2(e)
+// 2^eq (NaN for a row that is not finite, whose terms are zeros).
+// ready(): called between the loads and the first store; false: nothing is stored.
+template <int A, class F>
+__device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid, F ready) {
+  const uint4* src = reinterpret_cast<const uint4*>(P.q + ((size_t)tok * P.n_q_heads + head) * A);
+  uint4 x[A / 8];
+#pragma unroll
+  for (int i = 0; i < A / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < A / 8; ++i)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
+  m = max(m & 0xFFFFu, m >> 16);
+  const bool bad = m >= 0x7F80u;
+  const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
+  const float factor = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+  if (!ready()) return factor;
+  const float f = exp_inverse(bad ? 1u : eb);
+#pragma unroll
+  for (int c = 0; c < A / 16; ++c) {
+    const uint32_t w[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w, x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
+    uint32_t t0[4], t1[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y0 = bad ? 0.f : bf16lo(w[i]) * f, y1 = bad ? 0.f : bf16hi(w[i]) * f;
+      const uint32_t hi = pack_e4m3(y0, y1);
+      float z0, z1;
+      e4m3_to_f32(hi, z0, z1);
+      const uint32_t lo = pack_e4m3(y0 - z0, y1 - z1);
+      t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
+      t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
+    }
+    const uint32_t at = smem_u32(S.q[side]) + row * A + ((A == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
+    sts128(at, make_uint4(t0[0], t0[1], t0[2], t0[3]));
+    sts128(at + 128 * A, make_uint4(t1[0], t1[1], t1[2], t1[3]));
+  }
+  fence_proxy_async_smem();
+  mbar_arrive(&S.q_full[side]);
+  return factor;
+}
+
+// ONE: also the query rows of each single-token item, while the softmax is still
+// at the item before.
+template <int A, int G, bool ONE>
 __device__ void convert(const Fp8Step& P, Smem<A>& S) {
   constexpr int LR = A / 16, RP = 32 / LR, N = 32 / RP;   // lanes per row, rows per step, steps
   const unsigned FULL = 0xffffffffu;
@@ -438,9 +479,17 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
   while (ok) {
     const Item* item = items.next(P, S);
     if (!item) break;
-    const int a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi;
+    const int a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi, tok = item->q0, head = item->g * G + lane;
     const int key_lo = P.window > 0 ? max(0, item->ctx + item->tok_lo - P.window + 1) : 0;
+    const uint32_t it = items.i;
     items.done(S);
+    if constexpr (ONE) {
+      // (every tile of the item before is converted: nothing that its S waits for waits for this warp)
+      const float fq = make_query<A>(P, S, 0, 32 * warp + lane, tok, head, lane < G,
+                                     [&] { return ok = it == 0 || wwait(P, S, &S.q_free, (it - 1) & 1); });
+      if (!ok) break;
+      if (warp == 0) sts32(smem_u32(&S.fq[it & 3][lane]), __float_as_uint(fq));
+    }
     for (int j = a; j < b; ++j, ++n) {
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
       ok = wwait(P, S, &S.vr_full[st], ph);
@@ -560,48 +609,6 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S) {
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-3, 4-7)
-// This thread's query row as two e4m3 terms; returns its factor scale log2(e)
-// 2^eq (NaN for a row that is not finite, whose terms are zeros).
-// WRITE false: the factor only.
-template <int A, bool WRITE>
-__device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid) {
-  const uint4* src = reinterpret_cast<const uint4*>(P.q + ((size_t)tok * P.n_q_heads + head) * A);
-  uint4 x[A / 8];
-#pragma unroll
-  for (int i = 0; i < A / 8; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < A / 8; ++i)
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
-  m = max(m & 0xFFFFu, m >> 16);
-  const bool bad = m >= 0x7F80u;
-  const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
-  const float factor = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
-  if constexpr (!WRITE) return factor;
-  const float f = exp_inverse(bad ? 1u : eb);
-#pragma unroll
-  for (int c = 0; c < A / 16; ++c) {
-    const uint32_t w[8] = {x[2 * c].x, x[2 * c].y, x[2 * c].z, x[2 * c].w, x[2 * c + 1].x, x[2 * c + 1].y, x[2 * c + 1].z, x[2 * c + 1].w};
-    uint32_t t0[4], t1[4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float y0 = bad ? 0.f : bf16lo(w[i]) * f, y1 = bad ? 0.f : bf16hi(w[i]) * f;
-      const uint32_t hi = pack_e4m3(y0, y1);
-      float z0, z1;
-      e4m3_to_f32(hi, z0, z1);
-      const uint32_t lo = pack_e4m3(y0 - z0, y1 - z1);
-      t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
-      t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
-    }
-    const uint32_t at = smem_u32(S.q[side]) + row * A + ((A == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-    sts128(at, make_uint4(t0[0], t0[1], t0[2], t0[3]));
-    sts128(at + 128 * A, make_uint4(t1[0], t1[1], t1[2], t1[3]));
-  }
-  fence_proxy_async_smem();
-  mbar_arrive(&S.q_full[side]);
-  return factor;
-}
-
 // One key tile (number n; this query tile's S in s_t, its O in o_t) of this
 // thread's row: its weights into tensor memory, m and l brought up to date.
 // fq: the row's factor; it sees the keys lo .. pos.  fresh: O holds nothing yet.
@@ -696,7 +703,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     while ((item = items.next(P, S)) != nullptr) {
       if (side < item->sides) {
         const int ti = item->tok_lo + side * TOK + row / G;
-        fq = make_query<A, true>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi);
+        fq = make_query<A>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi, [] { return true; });
         return;
       }
       n += item->b - item->a;
@@ -860,17 +867,10 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
     const unsigned span = (unsigned)(pos - lo);                // key k is visible iff (unsigned)(k - lo) <= span
     const bool began = a0 > item->first, cut = began || b0 < item->end;
-    const int tok = item->q0, head = g * G + lane;
+    const int tok = item->q0;
     bool ok = true;
     float fq = 0.f;
-    if (side == 0) {
-      ok = i == 0 || wwait(P, S, &S.q_free, (i - 1) & 1);      // every S of the item before is done
-      if (ok) fq = make_query<A, true>(P, S, 0, 32 * w + lane, tok, head, lane < G);
-    } else {
-      fq = make_query<A, false>(P, S, 0, 0, tok, head, lane < G);
-    }
     items.done(S);
-    if (!ok) break;
     float m = kNegInf, l = 0.f;
     const bool any = a0 + side < b0;
     for (int j = a0 + side; j < b0; j += 2, ++ns) {
@@ -884,6 +884,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
       tmem_ld32(s_t + 32 * w, s);
       const uint32_t fk = smem_u32(&S.fk[nj & 3][32 * w]);
       const uint32_t vn = __float_as_uint(lds32f(smem_u32(&S.v_nan[nj & 3][w])));
+      if (j == a0 + side) fq = lds32f(smem_u32(&S.fq[i & 3][lane]));   // written before the first tile's factors
       const int key = j * kTileN + 32 * w;
       tmem_wait_ld();
 #pragma unroll
@@ -1062,25 +1063,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // registers of the four warpgroups: 2 x 176 + 72 + 88 = 4 x 128, what the launch holds
+  // registers of the four warpgroups: 2 x 176 + 72 + 88 = 4 x 128, what the launch holds (single tokens: 128 each)
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    if constexpr (!ONE) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     if constexpr (ONE)
       softmax_one<A, G>(P, W, S, warp >> 2);
     else
       softmax<A, G>(P, W, S, warp >> 2);
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    convert<A>(P, S);
+    if constexpr (!ONE) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    convert<A, G, ONE>(P, S);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (!ONE) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 12) {
       if constexpr (ONE)
         issue_one<A>(P, S);
       else
         issue<A>(P, S);
     }
-    if (warp == 13) load_tiles<A>(P, &kmap, S);
+    if (warp == 13 || warp == 15) load_tiles<A>(P, &kmap, S, warp == 15);
     if (warp == 14) publish<A, TOK, ONE>(P, S, tpre, ipre);
   }
   tc_fence_before();
