@@ -43,13 +43,41 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
   return r;
 }
-// Two e4m3 (low 16 bits of w) -> two floats; exact.
-__device__ __forceinline__ void e4m3_to_f32(uint32_t w, float& lo, float& hi) {
-  const uint32_t h = e4m3_to_f16x2(w);
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(h));
+// What two floats have left after the e4m3 in w's low 16 bits, as two e4m3.  The
+// subtraction takes the halves as they are: conversions run at a fraction of the
+// arithmetic's rate.
+__device__ __forceinline__ uint32_t pack_rest(uint32_t w, float lo, float hi) {
+  asm("{\n\t.reg .f16 a, b, n;\n\tmov.b32 {a, b}, %2;\n\tmov.b16 n, 0xBC00;\n\tfma.rn.f32.f16 %0, a, n, %0;\n\tfma.rn.f32.f16 %1, b, n, %1;\n\t}"
+      : "+f"(lo), "+f"(hi)
+      : "r"(e4m3_to_f16x2(w)));
+  return pack_e4m3(lo, hi);
 }
+
+// e4m3 -> bf16 times 2^e.  Each byte is sign-extended to 16 bits and moved
+// up by 4: sign, zeros, the 4 exponent and 3 fraction bits in bf16's places, a
+// bf16 2^-120 times too small (also for e4m3's subnormals, which become bf16's);
+// one multiplication by 2^(120 + e) is exact.  Bytes b > 134 (e > 7) need a second.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int SEL>
+__device__ __forceinline__ uint32_t permute(uint32_t x) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
+  return r;
+}
+__device__ __forceinline__ void widen8(uint32_t lo, uint32_t hi, uint32_t f, uint32_t* o) {
+  // bytes 0, 1 (then 2, 3) as two sign-extended halves: selector bit 3 repeats a byte's sign
+  o[0] = mul_bf16x2((permute<0x9180>(lo) << 4) & 0x87F087F0u, f);
+  o[1] = mul_bf16x2((permute<0xB3A2>(lo) << 4) & 0x87F087F0u, f);
+  o[2] = mul_bf16x2((permute<0x9180>(hi) << 4) & 0x87F087F0u, f);
+  o[3] = mul_bf16x2((permute<0xB3A2>(hi) << 4) & 0x87F087F0u, f);
+}
+// The factor of exponent byte b as a pair of bf16 (up to 2^7 of it: see above), and what is left of it.
+__device__ __forceinline__ uint32_t factor1(uint32_t b) { return ((min(b, 134u) + 120u) << 7) * 0x10001u; }
+__device__ __forceinline__ uint32_t factor2(uint32_t b) { return ((max(b, 134u) - 134u + 127u) << 7) * 0x10001u; }
 
 // ---------------------------------------------------------------- shared memory
 // Shared-memory accesses by address: through a generic pointer whose space the

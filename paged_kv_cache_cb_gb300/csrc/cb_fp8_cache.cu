@@ -8,7 +8,7 @@ namespace cb {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kPieces = 2;
 
 // 8 bf16 (16 bytes) of a row, its largest |bits| over LANES consecutive lanes.
 template <int LANES>
@@ -30,49 +30,66 @@ __device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t b) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// 8 e4m3 -> 8 bf16 under the row's exponent byte.
+// 8 e4m3 -> 8 bf16 under the row's exponent byte; exact.
 __device__ __forceinline__ uint4 restore8(const uint2& x, uint32_t b) {
-  const float f = exp_scale(b);
   uint32_t o[4];
+  widen8(x.x, x.y, factor1(b), o);
+  if (b > 134u) {
+    const uint32_t f2 = factor2(b), nan = b == kExpNan ? 0x7FC07FC0u : 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float lo, hi;
-    e4m3_to_f32((i < 2 ? x.x : x.y) >> (16 * (i & 1)), lo, hi);
-    o[i] = pack_bf16(lo * f, hi * f);
+    for (int i = 0; i < 4; ++i) o[i] = nan ? nan : mul_bf16x2(o[i], f2);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Where a token's row of a KV head stands in the cache.
+__device__ __forceinline__ int64_t cache_row(int64_t slot, uint32_t head, uint32_t n_kv_heads) {
+  const uint64_t s = (uint64_t)slot;
+  return (int64_t)((s / kBlockSize * n_kv_heads + head) * kBlockSize + s % kBlockSize);
+}
+
 // Token t's rows of K and V: LANES = A / 8 lanes hold one row of each, 8 values
 // per lane, so a row's largest magnitude is a shuffle reduction and a warp's
-// loads and stores are whole 256-byte and 128-byte rows.
+// loads and stores are whole 256-byte and 128-byte rows.  A thread has kPieces
+// pieces on their way at once.  Rows are counted in 32 bits (2^32 of the smallest
+// are 512 GiB of bf16).
 template <int LANES>
 __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                                                               const int64_t* __restrict__ slots, int64_t pieces,
                                                               uint2* __restrict__ k_cache, uint2* __restrict__ v_cache,
                                                               uint8_t* __restrict__ k_exps, uint8_t* __restrict__ v_exps,
-                                                              int64_t n_slots, int n_kv_heads, unsigned int* err) {
+                                                              int64_t n_slots, uint32_t n_kv_heads, unsigned int* err) {
   // rows are whole groups of lanes and pieces % LANES == 0: a group is in or out as one
-  for (int64_t i0 = blockIdx.x * (int64_t)kThreads; i0 < pieces; i0 += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = i0 + threadIdx.x;
-    const bool in = i < pieces;
-    const int64_t row = i / LANES, t = row / n_kv_heads;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 k = in ? __ldg(k_new + i) : zero, v = in ? __ldg(v_new + i) : zero;
-    int64_t slot = in ? __ldg(slots + t) : -1;
-    const uint32_t kb = row_exp(row_amax<LANES>(k)), vb = row_exp(row_amax<LANES>(v));
-    if (slot >= n_slots) {
-      set_error(err, CB_DEVERR_BADSLOT);
-      slot = -1;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads * kPieces; i0 < pieces; i0 += (int64_t)gridDim.x * kThreads * kPieces) {
+    uint4 k[kPieces], v[kPieces];
+    int64_t slot[kPieces];
+    uint32_t head[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int64_t i = i0 + u * kThreads + threadIdx.x;
+      const bool in = i < pieces;
+      const uint32_t row = (uint32_t)(i / LANES), t = row / n_kv_heads;
+      head[u] = row - t * n_kv_heads;
+      k[u] = in ? __ldg(k_new + i) : make_uint4(0u, 0u, 0u, 0u);
+      v[u] = in ? __ldg(v_new + i) : make_uint4(0u, 0u, 0u, 0u);
+      slot[u] = in ? __ldg(slots + t) : -1;
     }
-    if (slot < 0) continue;
-    const int64_t dst = ((slot / kBlockSize) * n_kv_heads + (row - t * n_kv_heads)) * kBlockSize + slot % kBlockSize;
-    const int c = threadIdx.x % LANES;
-    k_cache[dst * LANES + c] = quantise8(k, kb);
-    v_cache[dst * LANES + c] = quantise8(v, vb);
-    if (c == 0) {
-      k_exps[dst] = (uint8_t)kb;
-      v_exps[dst] = (uint8_t)vb;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const uint32_t kb = row_exp(row_amax<LANES>(k[u])), vb = row_exp(row_amax<LANES>(v[u]));
+      if (slot[u] >= n_slots) {
+        set_error(err, CB_DEVERR_BADSLOT);
+        slot[u] = -1;
+      }
+      if (slot[u] < 0) continue;
+      const int64_t dst = cache_row(slot[u], head[u], n_kv_heads);
+      const int c = threadIdx.x % LANES;
+      k_cache[dst * LANES + c] = quantise8(k[u], kb);
+      v_cache[dst * LANES + c] = quantise8(v[u], vb);
+      if (c == 0) {
+        k_exps[dst] = (uint8_t)kb;
+        v_exps[dst] = (uint8_t)vb;
+      }
     }
   }
 }
@@ -83,22 +100,36 @@ __global__ void __launch_bounds__(kThreads) gather_fp8_kernel(const int64_t* __r
                                                               const uint2* __restrict__ v_cache,
                                                               const uint8_t* __restrict__ k_exps,
                                                               const uint8_t* __restrict__ v_exps, uint4* __restrict__ k_out,
-                                                              uint4* __restrict__ v_out, int64_t n_slots, int n_kv_heads,
+                                                              uint4* __restrict__ v_out, int64_t n_slots, uint32_t n_kv_heads,
                                                               unsigned int* err) {
-  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / LANES, t = row / n_kv_heads;
-    const int64_t slot = __ldg(slots + t);
-    if (slot < 0) continue;
-    if (slot >= n_slots) {
-      set_error(err, CB_DEVERR_BADSLOT);
-      continue;
+  for (int64_t i0 = (int64_t)blockIdx.x * kThreads * kPieces; i0 < pieces; i0 += (int64_t)gridDim.x * kThreads * kPieces) {
+    int64_t src[kPieces];
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int64_t i = i0 + u * kThreads + threadIdx.x;
+      const uint32_t row = (uint32_t)(i / LANES), t = row / n_kv_heads;
+      const int64_t slot = i < pieces ? __ldg(slots + t) : -1;
+      if (slot >= n_slots) set_error(err, CB_DEVERR_BADSLOT);
+      src[u] = slot < 0 || slot >= n_slots ? -1 : cache_row(slot, row - t * n_kv_heads, n_kv_heads);
     }
-    const int64_t src = ((slot / kBlockSize) * n_kv_heads + (row - t * n_kv_heads)) * kBlockSize + slot % kBlockSize;
-    const int c = (int)(i % LANES);
-    const uint2 k = __ldg(k_cache + src * LANES + c), v = __ldg(v_cache + src * LANES + c);
-    const uint32_t kb = __ldg(k_exps + src), vb = __ldg(v_exps + src);
-    k_out[i] = restore8(k, kb);
-    v_out[i] = restore8(v, vb);
+    uint2 k[kPieces], v[kPieces];
+    uint32_t kb[kPieces], vb[kPieces];
+    const int c = threadIdx.x % LANES;
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      const int64_t at = max(src[u], (int64_t)0);            // a row that exists, where there is nothing to read
+      k[u] = __ldg(k_cache + at * LANES + c);
+      v[u] = __ldg(v_cache + at * LANES + c);
+      kb[u] = __ldg(k_exps + at);
+      vb[u] = __ldg(v_exps + at);
+    }
+#pragma unroll
+    for (int u = 0; u < kPieces; ++u) {
+      if (src[u] < 0) continue;
+      const int64_t i = i0 + u * kThreads + threadIdx.x;
+      k_out[i] = restore8(k[u], kb[u]);
+      v_out[i] = restore8(v[u], vb[u]);
+    }
   }
 }
 
@@ -135,7 +166,7 @@ cudaError_t launch_append_fp8(const void* k_new, const void* v_new, const int64_
   const int64_t pieces = (int64_t)n_tokens * c.n_kv_heads * lanes;
   if (pieces == 0) return cudaSuccess;
 #define CB_APPEND(L_)                                                                                                  \
-  append_fp8_kernel<L_><<<grid_for(pieces), kThreads, 0, stream>>>(                                                    \
+  append_fp8_kernel<L_><<<grid_for((pieces + kPieces - 1) / kPieces), kThreads, 0, stream>>>(                        \
       static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new), slots, pieces,                               \
       reinterpret_cast<uint2*>(c.k), reinterpret_cast<uint2*>(c.v), c.k_exps, c.v_exps, (int64_t)c.num_blocks * kBlockSize, \
       c.n_kv_heads, err)
@@ -153,7 +184,7 @@ cudaError_t launch_gather_fp8(const int64_t* slots, int n_rows, const Fp8Cache& 
   const int64_t pieces = (int64_t)n_rows * c.n_kv_heads * lanes;
   if (pieces == 0) return cudaSuccess;
 #define CB_GATHER(L_)                                                                                              \
-  gather_fp8_kernel<L_><<<grid_for(pieces), kThreads, 0, stream>>>(                                                \
+  gather_fp8_kernel<L_><<<grid_for((pieces + kPieces - 1) / kPieces), kThreads, 0, stream>>>(                    \
       slots, pieces, reinterpret_cast<const uint2*>(c.k), reinterpret_cast<const uint2*>(c.v), c.k_exps, c.v_exps, \
       static_cast<uint4*>(k_out), static_cast<uint4*>(v_out), (int64_t)c.num_blocks * kBlockSize, c.n_kv_heads, err)
   if (lanes == 16)

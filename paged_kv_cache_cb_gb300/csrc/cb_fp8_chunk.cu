@@ -392,34 +392,6 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
 }
 
 // ---------------------------------------------------------------- conversion of V (warps 8-11)
-// 16 e4m3 -> 16 bf16 times 2^e.  Each byte is sign-extended to 16 bits and moved
-// up by 4: sign, zeros, the 4 exponent and 3 fraction bits in bf16's places, a
-// bf16 2^-120 times too small (also for e4m3's subnormals, which become bf16's);
-// one multiplication by 2^(120 + e) is exact.  Bytes b > 134 (e > 7) need a second.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-template <int SEL>
-__device__ __forceinline__ uint32_t permute(uint32_t x) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(r) : "r"(x), "n"(SEL));
-  return r;
-}
-__device__ __forceinline__ void widen16(const uint4& x, uint32_t f, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // bytes 0, 1 (then 2, 3) as two sign-extended halves: selector bit 3 repeats a byte's sign
-    o[2 * i] = mul_bf16x2((permute<0x9180>(w[i]) << 4) & 0x87F087F0u, f);
-    o[2 * i + 1] = mul_bf16x2((permute<0xB3A2>(w[i]) << 4) & 0x87F087F0u, f);
-  }
-}
-// The factor of exponent byte b as a pair of bf16 (up to 2^7 of it: see above), and what is left of it.
-__device__ __forceinline__ uint32_t factor1(uint32_t b) { return ((min(b, 134u) + 120u) << 7) * 0x10001u; }
-__device__ __forceinline__ uint32_t factor2(uint32_t b) { return ((max(b, 134u) - 134u + 127u) << 7) * 0x10001u; }
-
 // This thread's query row as two e4m3 terms; returns its factor scale log2(e)
 // 2^eq (NaN for a row that is not finite, whose terms are zeros).
 // ready(): called between the loads and the first store; false: nothing is stored.
@@ -447,9 +419,7 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
     for (int i = 0; i < 8; ++i) {
       const float y0 = bad ? 0.f : bf16lo(w[i]) * f, y1 = bad ? 0.f : bf16hi(w[i]) * f;
       const uint32_t hi = pack_e4m3(y0, y1);
-      float z0, z1;
-      e4m3_to_f32(hi, z0, z1);
-      const uint32_t lo = pack_e4m3(y0 - z0, y1 - z1);
+      const uint32_t lo = pack_rest(hi, y0, y1);
       t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
       t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
     }
@@ -513,7 +483,10 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       for (int p = 0; p < N; ++p) {
         const int row = p * RP + rsub;
         uint32_t o[8];
-        widen16(lds128(src + p * 512), __shfl_sync(FULL, f1, row), o);
+        const uint4 x = lds128(src + p * 512);
+        const uint32_t f = __shfl_sync(FULL, f1, row);
+        widen8(x.x, x.y, f, o);
+        widen8(x.z, x.w, f, o + 4);
         if (large) {
           const uint32_t f2 = factor2(__shfl_sync(FULL, vb, row));
 #pragma unroll

@@ -438,10 +438,8 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int gr
       for (int d = 0; d < D / 2; ++d) {
         const float y0 = bad ? 0.f : bf16lo(w[u][d]) * f, y1 = bad ? 0.f : bf16hi(w[u][d]) * f;
         const uint32_t a = pack_e4m3(y0, y1);
-        float z0, z1;
-        e4m3_to_f32(a, z0, z1);
         c0 |= a << (16 * d);
-        c1 |= pack_e4m3(y0 - z0, y1 - z1) << (16 * d);
+        c1 |= pack_rest(a, y0, y1) << (16 * d);
       }
       const int hh = h / G, g = h - hh * G;
       for (int bi = 0; bi < bpt; ++bi) {
