@@ -235,4 +235,24 @@ __device__ __forceinline__ void join_row(const Fp8Partials& W, int rows, int b, 
   for (int d = 0; d < D; ++d) o[d] /= L;
 }
 
+// A kernel launch.  chained: the kernel may be placed while the kernel before it on
+// the stream, one of the same call, still runs.  Until its griddepcontrol.wait it
+// reads only what no kernel of the call writes (the requests' lengths) and writes
+// nothing to global memory but error flags.  The first kernel of a call is not
+// chained: what stands before it on the stream may write those lengths.
+template <class... T, class... U>
+cudaError_t launch_after(bool chained, void (*kernel)(T...), int grid, int threads, size_t smem, cudaStream_t stream, const U&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace cb

@@ -33,6 +33,9 @@ struct NewRows {
   const int64_t* slots;
 };
 
+// The single tokens' part of a step's workspace; the chunks' follows.
+size_t single_bytes(int head_dim) { return (fp8_partials_bytes(kSingleRows, head_dim) + 255) / 256 * 256; }
+
 int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,
              const int32_t* block_tables, int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len,
              int max_kv_len, const void* k_cache, const void* v_cache, const void* k_exps, const void* v_exps,
@@ -84,16 +87,17 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   if (app && launch_append_fp8(app->k, app->v, app->slots, n_tokens, s.cache, s.err, st) != cudaSuccess)
     return CB_ECUDA;
   int launches = app ? 1 : 0;
-  // the single tokens, then the chunks (ordered on the stream: both may use the same workspace)
-  const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
-  const Fp8Partials parts = fp8_chunk_partials(workspace);
-  if ((tiles ? launch_decode_fp8(s, fp8_partials(workspace), sms, st) : launch_chunk_fp8(s, parts, true, sms, st)) != cudaSuccess)
+  // the single tokens, the chunks, then what both have cut into pieces
+  const int group = n_q_heads / n_kv_heads;
+  const bool tiles = fp8_decode_shape(head_dim, group), many = max_q_len > 1;
+  const Fp8Partials singles = fp8_partials(workspace, kSingleRows);
+  const Fp8Partials chunks = fp8_partials(static_cast<uint8_t*>(workspace) + single_bytes(head_dim), kChunkRows);
+  if ((tiles ? launch_decode_fp8(s, singles, sms, app != nullptr, st)
+             : launch_chunk_fp8(s, singles, true, sms, app != nullptr, st)) != cudaSuccess ||
+      (many && launch_chunk_fp8(s, chunks, false, sms, true, st) != cudaSuccess) ||
+      launch_join_fp8(s, singles, tiles ? fp8_head_group(n_kv_heads) * group : group, many ? &chunks : nullptr, sms, st) != cudaSuccess)
     return CB_ECUDA;
-  launches += 2;
-  if (max_q_len > 1) {
-    if (launch_chunk_fp8(s, parts, false, sms, st) != cudaSuccess) return CB_ECUDA;
-    launches += 2;
-  }
+  launches += many ? 3 : 2;
   set_last_launches(launches);
   return CB_OK;
 }
@@ -167,8 +171,7 @@ size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q
   if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
       !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
-  const bool tiles = fp8_decode_shape(head_dim, n_q_heads / n_kv_heads);
-  return std::max(tiles ? fp8_partials_bytes(head_dim) : 0, max_q_len > 1 || !tiles ? fp8_chunk_partials_bytes(head_dim) : 0);
+  return single_bytes(head_dim) + (max_q_len > 1 ? fp8_partials_bytes(kChunkRows, head_dim) : 0);
 }
 
 int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,

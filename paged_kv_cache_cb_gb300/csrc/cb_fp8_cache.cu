@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(const uint4* __res
                                                               uint2* __restrict__ k_cache, uint2* __restrict__ v_cache,
                                                               uint8_t* __restrict__ k_exps, uint8_t* __restrict__ v_exps,
                                                               int64_t n_slots, uint32_t n_kv_heads, unsigned int* err) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // of a step's attention: it waits for this grid's end
   // rows are whole groups of lanes and pieces % LANES == 0: a group is in or out as one
   for (int64_t i0 = (int64_t)blockIdx.x * kThreads * kPieces; i0 < pieces; i0 += (int64_t)gridDim.x * kThreads * kPieces) {
     uint4 k[kPieces], v[kPieces];

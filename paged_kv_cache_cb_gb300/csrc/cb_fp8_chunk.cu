@@ -43,7 +43,7 @@ namespace cb {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRows = 256;             // rows of an item (two query tiles)
+constexpr int kRows = kChunkRows;      // rows of an item (two query tiles)
 constexpr int kMinTiles = 4;           // key tiles per CTA below which a step uses fewer CTAs
 constexpr int kCutTiles = 7;           // what cutting items costs, in key tiles' time (partial results and their joining)
 constexpr int kSmemLimit = 232448;
@@ -281,6 +281,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
     S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
   }
+  if constexpr (ONE) asm volatile("griddepcontrol.wait;" ::: "memory");   // so far only the requests' lengths were read (launch_after)
   __syncthreads();
   if (tid == 0) {                      // the item that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
@@ -944,7 +945,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
       ls += mc == kNegInf ? lc : ex2(mc - mm) * lc;            // -inf: no key seen, or NaNs only (then lc is one)
     }
     const float f = (m == kNegInf ? (l != 0.f ? 1.f : 0.f) : ex2(m - mm)) / ls;
-    const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows;
+    const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kSingleRows;
     if (cut && copy == 0 && lane < G) *reinterpret_cast<float2*>(W.ml + (pr + lane) * 2) = make_float2(mm, ls);
 #pragma unroll 1
     for (int c = 0; c < A / 32 && ok; ++c) {
@@ -1063,36 +1064,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(S.tmem, 512);
   }
-}
-
-// ---------------------------------------------------------------- joining the pieces
-// A CTA takes 8 rows of an item at a time, a warp per row.
-constexpr int kJoinThreads = 256, kJoinRows = kJoinThreads / 32;
-template <int A>
-__global__ void __launch_bounds__(kJoinThreads) join_chunk_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int group) {
-  constexpr int D = A / 32;
-  __shared__ int owner[kMaxDecodeGrid];
-  __shared__ int n_owner;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tok = kTileM / group;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 0) {
-    const int n = join_owners(W, ctas, owner);
-    if (lane == 0) n_owner = n;
-  }
-  __syncthreads();
-  for (int task = blockIdx.x; task < n_owner * (kRows / kJoinRows); task += gridDim.x) {
-    const int b = owner[task / (kRows / kJoinRows)];
-    const Fp8Rec rec = W.rec[b];
-    const int q0 = __ldg(P.cu_q_lens + rec.r), q_len = __ldg(P.cu_q_lens + rec.r + 1) - q0;
-    const int row = (task % (kRows / kJoinRows)) * kJoinRows + warp;
-    const int ti = rec.pad * 2 * tok + row / group;            // rows of tile B follow tile A's: its tokens do too
-    if (ti >= q_len) continue;
-    float o[D];
-    join_row<A>(W, kRows, b, rec.n, row, 0, 1, o);
-    uint16_t* dst = P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D;
-#pragma unroll
-    for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d], o[d + 1]);
-  }
+  // Chunks do not wait for the single tokens' kernel: its CTAs let this one start only after the appended rows
+  // stood in the cache, and the two write different rows and workspaces.  This grid ends after that one does, so
+  // that the joining kernel has both.
+  if constexpr (!ONE) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int A>
@@ -1102,45 +1077,21 @@ size_t smem_bytes(int n_reqs) {
 static_assert(sizeof(Smem<128>) + 1024 + (kMaxReqs + 1) * 8 <= kSmemLimit, "shared memory");
 
 template <int A, int G, bool ONE>
-cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
+cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, bool chained, cudaStream_t stream) {
   CUtensorMap km;
   const long long rows = (long long)s.cache.num_blocks * s.cache.n_kv_heads * kBlockSize;
   if (!encode_byte_rows(&km, s.cache.k, rows, A, kBlockSize)) return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(chunk_fp8_kernel<A, G, ONE>), kSmemLimit);
   if (e != cudaSuccess) return e;
-  chunk_fp8_kernel<A, G, ONE><<<grid, kThreads, smem_bytes<A>(s.n_reqs), stream>>>(s, w, km);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(4 * grid);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_chunk_kernel<A>, s, w, grid, G);
+  return launch_after(chained, chunk_fp8_kernel<A, G, ONE>, grid, kThreads, smem_bytes<A>(s.n_reqs), stream, s, w, km);
 }
 
 }  // namespace
 
-size_t fp8_chunk_partials_bytes(int head_dim) {
-  return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * kRows * (2 + head_dim) * 4;
-}
-Fp8Partials fp8_chunk_partials(void* workspace) {
-  uint8_t* p = static_cast<uint8_t*>(workspace);
-  Fp8Partials w;
-  w.rec = reinterpret_cast<Fp8Rec*>(p);
-  w.ml = reinterpret_cast<float*>(p + sizeof(Fp8Rec) * kMaxDecodeGrid);
-  w.acc = w.ml + (size_t)2 * kMaxDecodeGrid * kRows * 2;
-  return w;
-}
-
-cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, cudaStream_t stream) {
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, bool chained, cudaStream_t stream) {
   const int a = s.cache.head_dim, g = s.n_q_heads / s.cache.n_kv_heads;
 #define CB_CASE(A_, G_, ONE_) \
-  if (a == A_ && g == G_ && single == ONE_) return launch_t<A_, G_, ONE_>(s, w, grid, stream);
+  if (a == A_ && g == G_ && single == ONE_) return launch_t<A_, G_, ONE_>(s, w, grid, chained, stream);
   CB_CASE(128, 1, false)
   CB_CASE(128, 2, false)
   CB_CASE(128, 4, false)

@@ -62,7 +62,7 @@ constexpr int kMinTiles = 2;        // tiles per CTA below which a step uses few
 constexpr float kWeightBits = 12.f; // weights are stored times 2^12 (e5m2: up to 2^15.8, down to 2^-16)
 constexpr float kLazyP = 8.f;       // the running maxima follow only beyond these (base 2)
 constexpr float kLazyW = 3.f;
-constexpr int kMaxHeads = 64;       // query heads of a tile
+constexpr int kMaxHeads = kSingleRows;   // query heads of a tile
 
 template <int A, int G>
 struct Cfg {
@@ -240,6 +240,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
     S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
     S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // so far only the requests' lengths were read (launch_after)
   __syncthreads();
   if (tid == 0) {                     // the sequence that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
@@ -789,52 +790,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// ---------------------------------------------------------------- joining the pieces
-// A warp takes a (sequence, head); where there are fewer of those than CTAs, a CTA
-// does, its warps taking the pieces in turn.
-constexpr int kJoinThreads = 256;
-template <int A>
-__global__ void __launch_bounds__(kJoinThreads) join_fp8_kernel(const Fp8Step P, const Fp8Partials W, int ctas, int hg_heads) {
-  constexpr int D = A / 32, NW = kJoinThreads / 32;
-  __shared__ int owner[kMaxDecodeGrid];
-  __shared__ int n_owner;
-  __shared__ float red[NW][A];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, heads = hg_heads * (P.n_q_heads / P.cache.n_kv_heads);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (warp == 0) {
-    const int n = join_owners(W, ctas, owner);
-    if (lane == 0) n_owner = n;
-  }
-  __syncthreads();
-  const int tasks = n_owner * heads;
-  const bool by_cta = tasks <= (int)gridDim.x;
-  for (int task = by_cta ? blockIdx.x : blockIdx.x * NW + warp; task < tasks; task += by_cta ? gridDim.x : gridDim.x * NW) {
-    const int b = owner[task / heads], h = task % heads;
-    const Fp8Rec rec = W.rec[b];
-    const int t = __ldg(P.cu_q_lens + rec.r);
-    float o[D];
-    join_row<A>(W, kMaxHeads, b, rec.n, h, by_cta ? warp : 0, by_cta ? NW : 1, o);
-    if (by_cta) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) red[warp][lane * D + d] = o[d];
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          o[d] = 0.f;
-          for (int w = 0; w < NW; ++w) o[d] += red[w][lane * D + d];
-        }
-      }
-    }
-    if (!by_cta || warp == 0) {
-      uint16_t* dst = P.out + ((size_t)t * P.n_q_heads + (size_t)rec.hg * heads + h) * A + lane * D;
-#pragma unroll
-      for (int d = 0; d < D; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d], o[d + 1]);
-    }
-    if (by_cta) __syncthreads();
-  }
-}
-
 template <int A, int G>
 size_t smem_bytes(int n_reqs) {
   return 1024 + sizeof(Smem<A, G>) + (size_t)(3 * n_reqs + 1) * 4;
@@ -844,50 +799,31 @@ static_assert(sizeof(Smem<128, 8>) + 1024 + (3 * kMaxReqs + 1) * 4 <= kSmemLimit
 static_assert(sizeof(Smem<128, 4>) + 1024 + (3 * kMaxReqs + 1) * 4 <= kSmemLimit, "shared memory");
 
 template <int A, int G>
-cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
-  int hg = 8;
-  while (s.cache.n_kv_heads % hg) hg >>= 1;
+cudaError_t launch_t(const Fp8Step& s, const Fp8Partials& w, int grid, bool chained, cudaStream_t stream) {
+  const int hg = fp8_head_group(s.cache.n_kv_heads);
   CUtensorMap km, vm;
   const long long rows = (long long)s.cache.num_blocks * s.cache.n_kv_heads * kBlockSize;
   if (!encode_byte_rows(&km, s.cache.k, rows, A, hg * kBlockSize) || !encode_byte_rows(&vm, s.cache.v, rows, A, hg * kBlockSize))
     return cudaErrorInvalidValue;
   cudaError_t e = opt_in_smem(reinterpret_cast<const void*>(decode_fp8_kernel<A, G>), kSmemLimit);
   if (e != cudaSuccess) return e;
-  decode_fp8_kernel<A, G><<<grid, kThreads, smem_bytes<A, G>(s.n_reqs), stream>>>(s, w, hg, km, vm);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(4 * grid);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // its CTAs are placed while the last pieces are written
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_fp8_kernel<A>, s, w, grid, hg);
+  return launch_after(chained, decode_fp8_kernel<A, G>, grid, kThreads, smem_bytes<A, G>(s.n_reqs), stream, s, w, hg, km, vm);
 }
 
 }  // namespace
 
 bool fp8_decode_shape(int head_dim, int group) { return (head_dim == 64 || head_dim == 128) && group <= 8; }
 
-size_t fp8_partials_bytes(int head_dim) {
-  return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * kMaxHeads * (2 + head_dim) * 4;
-}
-Fp8Partials fp8_partials(void* workspace) {
-  uint8_t* p = static_cast<uint8_t*>(workspace);
-  Fp8Partials w;
-  w.rec = reinterpret_cast<Fp8Rec*>(p);
-  w.ml = reinterpret_cast<float*>(p + sizeof(Fp8Rec) * kMaxDecodeGrid);
-  w.acc = w.ml + (size_t)2 * kMaxDecodeGrid * kMaxHeads * 2;
-  return w;
+int fp8_head_group(int n_kv_heads) {
+  int hg = 8;
+  while (n_kv_heads % hg) hg >>= 1;
+  return hg;
 }
 
-cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream) {
+cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, bool chained, cudaStream_t stream) {
   const int a = s.cache.head_dim, g = s.n_q_heads / s.cache.n_kv_heads;
 #define CB_CASE(A_, G_) \
-  if (a == A_ && g == G_) return launch_t<A_, G_>(s, w, grid, stream);
+  if (a == A_ && g == G_) return launch_t<A_, G_>(s, w, grid, chained, stream);
   CB_CASE(128, 1)
   CB_CASE(128, 2)
   CB_CASE(128, 4)

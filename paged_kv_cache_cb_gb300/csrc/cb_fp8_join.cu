@@ -1,0 +1,88 @@
+// Joining the pieces that attention over the 8-bit cache has cut sequences into:
+//     M = max m_i,  out = sum 2^(m_i - M) l_i o_i / sum 2^(m_i - M) l_i
+// over the pieces' (m_i, l_i, o_i), o_i divided by l_i already.  One kernel for the
+// single tokens' pieces and the chunks': its first CTAs take the former.  Its CTAs
+// are placed while the last pieces are written.
+#include "cb_fp8.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kJoinThreads = 256, kWarps = kJoinThreads / 32;
+
+template <int A>
+__device__ __forceinline__ void store_row(uint16_t* dst, const float (&o)[A / 32]) {
+#pragma unroll
+  for (int d = 0; d < A / 32; d += 2) *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16(o[d], o[d + 1]);
+}
+
+// n_singles: the CTAs of the single tokens; the others take the chunks.
+template <int A>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_fp8_kernel(const Fp8Step P, const Fp8Partials singles, const Fp8Partials chunks, int ctas, int n_singles, int heads) {
+  constexpr int D = A / 32;
+  __shared__ int owner[kMaxDecodeGrid];
+  __shared__ int n_owner;
+  __shared__ float red[kWarps][A];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool single = (int)blockIdx.x < n_singles;
+  const Fp8Partials& W = single ? singles : chunks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 0) {
+    const int n = join_owners(W, ctas, owner);
+    if (lane == 0) n_owner = n;
+  }
+  __syncthreads();
+  float o[D];
+  if (single) {
+    // A warp takes a (sequence, head); where there are fewer of those than CTAs, a CTA does, its warps taking
+    // the pieces in turn.
+    const int tasks = n_owner * heads;
+    const bool by_cta = tasks <= n_singles;
+    for (int task = by_cta ? blockIdx.x : blockIdx.x * kWarps + warp; task < tasks; task += by_cta ? n_singles : n_singles * kWarps) {
+      const int b = owner[task / heads], h = task % heads;
+      const Fp8Rec rec = W.rec[b];
+      const int t = __ldg(P.cu_q_lens + rec.r);
+      join_row<A>(W, kSingleRows, b, rec.n, h, by_cta ? warp : 0, by_cta ? kWarps : 1, o);
+      if (by_cta) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) red[warp][lane * D + d] = o[d];
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int d = 0; d < D; ++d) {
+            o[d] = 0.f;
+            for (int w = 0; w < kWarps; ++w) o[d] += red[w][lane * D + d];
+          }
+        }
+      }
+      if (!by_cta || warp == 0) store_row<A>(P.out + ((size_t)t * P.n_q_heads + (size_t)rec.hg * heads + h) * A + lane * D, o);
+      if (by_cta) __syncthreads();
+    }
+    return;
+  }
+  // kWarps rows of a chunk's item at a time, a warp per row
+  const int group = P.n_q_heads / P.cache.n_kv_heads, tok = kTileM / group;
+  for (int task = blockIdx.x - n_singles; task < n_owner * (kChunkRows / kWarps); task += gridDim.x - n_singles) {
+    const int b = owner[task / (kChunkRows / kWarps)];
+    const Fp8Rec rec = W.rec[b];
+    const int q0 = __ldg(P.cu_q_lens + rec.r), q_len = __ldg(P.cu_q_lens + rec.r + 1) - q0;
+    const int row = (task % (kChunkRows / kWarps)) * kWarps + warp;
+    const int ti = rec.pad * 2 * tok + row / group;            // rows of tile B follow tile A's: its tokens do too
+    if (ti >= q_len) continue;
+    join_row<A>(W, kChunkRows, b, rec.n, row, 0, 1, o);
+    store_row<A>(P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D, o);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_join_fp8(const Fp8Step& s, const Fp8Partials& singles, int heads, const Fp8Partials* chunks, int grid, cudaStream_t stream) {
+  const int n = 4 * grid, ctas = chunks ? 2 * n : n;
+  return s.cache.head_dim == 128
+             ? launch_after(true, join_fp8_kernel<128>, ctas, kJoinThreads, 0, stream, s, singles, chunks ? *chunks : singles, grid, n, heads)
+             : launch_after(true, join_fp8_kernel<64>, ctas, kJoinThreads, 0, stream, s, singles, chunks ? *chunks : singles, grid, n, heads);
+}
+
+}  // namespace cb

@@ -149,24 +149,35 @@ cudaError_t launch_copy_blocks_fp8(const int32_t* pairs, int n_pairs, const Fp8C
 struct Fp8Rec {
   int r, hg, n, pad;            // pad: the chunk kernel's pair of query tiles (hg: its KV head)
 };
-// Workspace of the single-token attention: per CTA two partial results (its
-// first and its last piece), [64 heads][A] values and [64][2] (max, sum).
+// Partial results of attention: per CTA two (its first and its last piece), `rows`
+// rows of A values and of (max, sum) each.
 struct Fp8Partials {
   Fp8Rec* rec;                  // [kMaxDecodeGrid]
-  float* ml;                    // [2 * kMaxDecodeGrid][64][2]
-  float* acc;                   // [2 * kMaxDecodeGrid][64][A]
+  float* ml;                    // [2 * kMaxDecodeGrid][rows][2]
+  float* acc;                   // [2 * kMaxDecodeGrid][rows][A]
 };
-size_t fp8_partials_bytes(int head_dim);
-Fp8Partials fp8_partials(void* workspace);
+constexpr int kSingleRows = 64, kChunkRows = 256;   // of the single tokens' pieces, of the chunks'
+inline size_t fp8_partials_bytes(int rows, int head_dim) {
+  return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * rows * (2 + head_dim) * 4;
+}
+inline Fp8Partials fp8_partials(void* workspace, int rows) {
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  Fp8Partials w;
+  w.rec = reinterpret_cast<Fp8Rec*>(p);
+  w.ml = reinterpret_cast<float*>(p + sizeof(Fp8Rec) * kMaxDecodeGrid);
+  w.acc = w.ml + (size_t)2 * kMaxDecodeGrid * rows * 2;
+  return w;
+}
 bool fp8_decode_shape(int head_dim, int group);
-// The requests with one new token, on `grid` CTAs (at most one per SM), and the join of their pieces.
-cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, cudaStream_t stream);
+int fp8_head_group(int n_kv_heads);              // KV heads of a tile of launch_decode_fp8
+// The requests with one new token, on `grid` CTAs (at most one per SM).
+cudaError_t launch_decode_fp8(const Fp8Step& s, const Fp8Partials& w, int grid, bool chained, cudaStream_t stream);
 // The requests with several new tokens, or (single) those with one where
-// launch_decode_fp8 has no kernel, and the join of their pieces.  Partial results:
-// as above, per CTA two times [256 rows][A] values and [256][2] (max, sum).
-size_t fp8_chunk_partials_bytes(int head_dim);
-Fp8Partials fp8_chunk_partials(void* workspace);
-cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, cudaStream_t stream);
+// launch_decode_fp8 has no kernel.  The former are launched after one of the latter.
+cudaError_t launch_chunk_fp8(const Fp8Step& s, const Fp8Partials& w, bool single, int grid, bool chained, cudaStream_t stream);
+// Joins the pieces of both (chunks null: of the single tokens only); heads: query
+// heads of a single token's piece.
+cudaError_t launch_join_fp8(const Fp8Step& s, const Fp8Partials& singles, int heads, const Fp8Partials* chunks, int grid, cudaStream_t stream);
 
 // Library state that the entry points of other files use (cb_api.cu).
 unsigned int* stream_error_word(cudaStream_t stream, int* rc);   // nullptr: return *rc
