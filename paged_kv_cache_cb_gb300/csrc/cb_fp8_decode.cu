@@ -57,7 +57,7 @@ namespace cb {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kMinTiles = 2;        // tiles per CTA below which a step uses fewer CTAs
 constexpr float kWeightBits = 12.f; // weights are stored times 2^12 (e5m2: up to 2^15.8, down to 2^-16)
 constexpr float kLazyP = 8.f;       // the running maxima follow only beyond these (base 2)
@@ -70,13 +70,12 @@ struct Cfg {
   static constexpr int NS = 2 * C;                           // S columns (two query terms)
   static constexpr int SS = G <= 2 ? 8 : (G == 4 ? 16 : 24); // w rows per slot (three terms x G, padded)
   static constexpr int NO = 8 * SS;                          // O columns
-  static constexpr int SB = G == 8 ? 2 : 4;                  // S buffers
-  static constexpr int OB = G == 8 ? 1 : 2;                  // O buffers
+  static constexpr int SB = G == 8 ? 1 : 4, NB = SB == 1 ? 2 : SB;   // S buffers, and their barriers (see issue_s)
   static constexpr int KS = A == 128 ? 4 : 6, VS = KS;       // K and V stages
   static constexpr int PB = 4;                               // w buffers
   static constexpr int ES = 8;                               // exponent stages
   static constexpr int kTile = 128 * A;                      // bytes
-  static constexpr int kCols = SB * NS + OB * NO;
+  static constexpr int kCols = SB * NS + 2 * NO;
   static constexpr int kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= 512, "tensor memory");
 };
@@ -86,16 +85,17 @@ struct alignas(1024) Smem {
   using X = Cfg<A, G>;
   uint8_t k[X::KS][X::kTile];
   uint8_t v[X::VS][X::kTile];
-  uint8_t q[2][16 * G * A];          // per group: rows (term, slot, g) of A bytes, swizzled like K
+  uint8_t q[2][16 * G * A];          // of two segments: rows (term, slot, g) of A bytes, swizzled like K
   uint8_t p[X::PB][256 * X::SS];     // w: [2 slots][2 SS rows][32 bytes], 8-row x 16-byte core matrices
   uint8_t ex[X::ES][2][128];         // exponent bytes of the tile's K and V rows
-  float cf[2][X::C];                 // per group: scale log2(e) 2^eq per column
-  float alpha[2][2][X::C];           // factors of O when M moves
-  float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // a segment's l, m, M, then l, m per head and the slots' factors
-  float si[2][X::C];                 // 1 / l per head
+  float cf[2][X::C];                 // of two segments: scale log2(e) 2^eq per column
+  float alpha[2][2][X::C];           // per group: factors of O when M moves
+  float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // per group: a segment's l, m, M
+  float of[2][X::C];                 // per group: the slots' factors of O
+  float hl[2][X::C], hm[2][X::C], hi[2][X::C];   // l, m, 1 / l per head (each group its own copy)
   uint64_t k_full[X::KS], k_empty[X::KS], v_full[X::VS], v_empty[X::VS];
-  uint64_t e_full[X::ES], e_empty[X::ES], s_full[X::SB], s_empty[X::SB], p_full[X::PB], pv_done[X::PB];
-  uint64_t q_full[2], o_full[2], o_free[X::OB], turn[2], drain[2];
+  uint64_t e_full[X::ES], e_empty[X::ES], s_full[X::NB], s_empty[X::NB], p_full[X::PB], pv_done[X::PB];
+  uint64_t q_full[2], q_free[2], o_full, o_free, drain[2];
   int scan[16];
   uint32_t tmem;
   volatile int abort;
@@ -344,8 +344,12 @@ __device__ void issue_s(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int n
   for (int i = 0; ok && it.next(s); ++i) {
     ok = wwait(P, S, &S.q_full[i & 1], (i >> 1) & 1);
     for (int j = 0; j < s.nt && ok; ++j, ++n) {
+      // a single buffer has two barriers all the same: a group looks at every second tile, and a parity cannot
+      // tell phases two apart
       const int st = n % X::KS, sb = n % X::SB;
-      ok = wwait(P, S, &S.s_empty[sb], ((n / X::SB) & 1) ^ 1) && wwait(P, S, &S.k_full[st], (n / X::KS) & 1);
+      const uint32_t was = n - X::SB;                          // the tile before in this buffer
+      ok = (n < (uint32_t)X::SB || wwait(P, S, &S.s_empty[was % X::NB], (was / X::NB) & 1)) &&
+           wwait(P, S, &S.k_full[st], (n / X::KS) & 1);
       if (!ok) break;
       tc_fence_after();
       const uint64_t a = kd + (uint32_t)(st * (X::kTile >> 4)), b = qd + (uint32_t)((i & 1) * ((16 * G * A) >> 4));
@@ -353,7 +357,8 @@ __device__ void issue_s(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int n
 #pragma unroll
         for (int d = 0; d < A / 32; ++d) mma_f8(S.tmem + sb * X::NS, a + d * 2, b + d * 2, kIdesc, d > 0);
         tc_commit(&S.k_empty[st]);
-        tc_commit(&S.s_full[sb]);
+        tc_commit(&S.s_full[n % X::NB]);
+        if (j == s.nt - 1) tc_commit(&S.q_free[i & 1]);
       }
       __syncwarp();
     }
@@ -375,23 +380,21 @@ __device__ void issue_pv(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int 
   uint32_t n = 0;
   bool ok = true;
   for (int i = 0; ok && it.next(s); ++i) {
-    const int ob = i % X::OB;
-    ok = wwait(P, S, &S.o_free[ob], ((i / X::OB) & 1) ^ 1);
+    ok = wwait(P, S, &S.o_free, (i & 1) ^ 1);
     for (int j = 0; j < s.nt && ok; ++j, ++n) {
       const int st = n % X::VS, pb = n % X::PB;
       ok = wwait(P, S, &S.v_full[st], (n / X::VS) & 1) && wwait(P, S, &S.p_full[pb], (n / X::PB) & 1);
       if (!ok) break;
       tc_fence_after();
       const uint64_t a = vd + (uint32_t)(st * (X::kTile >> 4)), b = pd + (uint32_t)(pb * ((256 * X::SS) >> 4));
-      const uint32_t d = S.tmem + X::SB * X::NS + ob * X::NO;
+      const uint32_t d = S.tmem + X::SB * X::NS + (n & 1) * X::NO;
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          mma_f8(d + ks * 2 * X::SS, a + ((ks * 32 * A) >> 4), b + ((ks * 64 * X::SS) >> 4), kIdesc, j > 0);
+          mma_f8(d + ks * 2 * X::SS, a + ((ks * 32 * A) >> 4), b + ((ks * 64 * X::SS) >> 4), kIdesc, j > 1);
         tc_commit(&S.v_empty[st]);
         tc_commit(&S.pv_done[pb]);
-        // a barrier per group: pv_done (or one per O buffer) may be phases away when this group looks
-        if (j == s.nt - 1) tc_commit(&S.o_full[i & 1]);
+        if (j == s.nt - 1) tc_commit(&S.o_full);
       }
       __syncwarp();
     }
@@ -402,15 +405,15 @@ __device__ void issue_pv(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int 
   mbar_wait(&S.drain[1], 0, 20000000ull);
 }
 
-// ---------------------------------------------------------------- softmax groups (warps 0-3, 4-7)
-// Query terms of the segment's heads into q[grp], and the columns' factors.
+// ---------------------------------------------------------------- queries (warps 12-15)
+// Query terms of the segment's heads into q[buf], and the columns' factors.
 template <int A, int G>
-__device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int grp, int hg_heads) {
+__device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int buf, int hg_heads) {
   constexpr int D = A / 32;                  // values per lane
   constexpr int B = 8;                       // heads in flight
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const int heads = hg_heads * G, bpt = 8 / hg_heads;
-  const uint32_t q_at = smem_u32(S.q[grp]);
+  const uint32_t q_at = smem_u32(S.q[buf]);
   const uint16_t* src = P.q + ((size_t)s.tok * P.n_q_heads + (size_t)s.hg * heads) * A + lane * D;
   for (int h0 = warp; h0 < heads; h0 += 4 * B) {
     uint32_t w[B][D / 2];
@@ -454,34 +457,50 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int gr
             sts16(q_at + row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2, t ? c1 : c0);
           }
         }
-        if (lane == 0) S.cf[grp][col] = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
+        if (lane == 0) S.cf[buf][col] = bad ? __uint_as_float(0x7FC00000u) : P.scale_log2 * __uint_as_float(eb << 23);
       }
     }
   }
 }
 
-// Output dimension d of every head of the segment: the slots of a head joined,
-// o 2^(M - m) / l, written as the output or as this piece's part of it with m
-// and l.  2^(M - m) comes as two factors: for the smallest and the largest
-// exponents of value rows it is outside fp32's normal range.
+// The queries of the segments, two ahead of the softmax at most.
 template <int A, int G>
-__device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, const Seg& s, int grp, uint32_t o_tmem,
+__device__ void queries(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int hg_heads) {
+  SegIter it(plan, S.u0, S.u1, P.cache.n_kv_heads / hg_heads, P.n_reqs, P.window);
+  Seg s;
+  for (int i = 0; it.next(s); ++i) {
+    if (!wwait(P, S, &S.q_free[i & 1], ((i >> 1) & 1) ^ 1)) break;
+    load_query<A, G>(P, S, s, i & 1, hg_heads);
+    fence_proxy_async_smem();
+    mbar_arrive(&S.q_full[i & 1]);
+  }
+}
+
+// ---------------------------------------------------------------- softmax groups (warps 0-3, 4-7)
+// Output dimension d of this group's heads of the segment (every second): the
+// slots of a head joined over both groups' O, o 2^(M - m) / l, written as the output
+// or as this piece's part of it with m and l.  2^(M - m) comes as two factors: for
+// the smallest and the largest exponents of value rows it is outside fp32's normal
+// range.  obs: bit b: O buffer b holds products.
+template <int A, int G>
+__device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, const Seg& s, int grp, uint32_t obs,
                           int hg_heads, bool whole, int slot_out) {
   using X = Cfg<A, G>;
   const int t = threadIdx.x & 127, warp = t >> 5, bpt = 8 / hg_heads, heads = hg_heads * G;
   if (A == 64 && warp >= 2) return;          // rows 64 .. 127 repeat 0 .. 63
-  const uint32_t base = o_tmem + ((uint32_t)(warp * 32) << 16), sw = smem_u32(S.sw[grp]);
-  for (int hh = 0; hh < hg_heads; ++hh) {
+  const uint32_t base = S.tmem + X::SB * X::NS + ((uint32_t)(warp * 32) << 16);
+  for (int hh = grp; hh < hg_heads; hh += 2) {
     float acc[G], inv[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       acc[g] = 0.f;
-      inv[g] = lds32f(smem_u32(&S.si[grp][hh * G + g]));
+      inv[g] = lds32f(smem_u32(&S.hi[grp][hh * G + g]));
     }
-    for (int bi = 0; bi < bpt; ++bi) {
-      const int slot = bi * hg_heads + hh;
+    for (int k = 0; k < 2 * bpt; ++k) {
+      const int ob = k & 1, slot = (k >> 1) * hg_heads + hh;
+      if (!((obs >> ob) & 1)) continue;
       float o[X::SS];
-      const uint32_t at = base + slot * X::SS;
+      const uint32_t at = base + ob * X::NO + slot * X::SS, of = smem_u32(&S.of[ob][slot * G]);
       if constexpr (X::SS == 24) {
         tmem_ld<16>(at, o);
         tmem_ld<8>(at + 16, o + 16);
@@ -491,7 +510,7 @@ __device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
       tmem_wait_ld();
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        const float f = lds32f(sw + (slot * G + g) * 4);
+        const float f = lds32f(of + g * 4);
         acc[g] += ((o[g] + o[G + g] + o[2 * G + g]) * f) * (f * inv[g]);
       }
     }
@@ -504,7 +523,7 @@ __device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
       } else {
         const size_t at = (size_t)slot_out * kMaxHeads + h;
         W.acc[at * A + t] = acc[g];
-        if (t == 0) *reinterpret_cast<float2*>(W.ml + at * 2) = make_float2(S.sm[grp][h], S.sl[grp][h]);
+        if (t == 0) *reinterpret_cast<float2*>(W.ml + at * 2) = make_float2(S.hm[grp][h], S.hl[grp][h]);
       }
     }
   }
@@ -521,35 +540,29 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
   SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
   Seg s;
-  uint32_t n = 0;                            // tiles before this segment
-  for (int i = 0; it.next(s); ++i) {
-    if ((i & 1) != grp) {
-      n += s.nt;
-      continue;
-    }
-    load_query<A, G>(P, S, s, grp, hg_heads);
-    fence_proxy_async_smem();
-    named_bar(bar_id, 128);                  // cf
-    mbar_arrive(&S.q_full[grp]);
+  uint32_t n0 = 0;                           // tiles before this segment
+  const uint32_t o_tmem = S.tmem + X::SB * X::NS + grp * X::NO;
+  for (int i = 0; it.next(s); ++i, n0 += s.nt) {
+    bool fail = !wwait(P, S, &S.q_full[i & 1], (i >> 1) & 1);
     float f[G], m[G], M[G], l[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      f[g] = S.cf[grp][slot * G + g];
+      f[g] = S.cf[i & 1][slot * G + g];
       m[g] = M[g] = kNegInf;
       l[g] = 0.f;
     }
-    const uint32_t o_tmem = S.tmem + X::SB * X::NS + (i % X::OB) * X::NO;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_free[i & 1]);
     const int first_key = P.window > 0 ? max(0, s.kv - P.window) : 0;
-    // The other group has read its last scores: the rings' phases that this one waits for next are then
-    // one ahead of the last completed ones (a parity cannot tell phases two apart).
-    bool fail = i > 0 && !wwait(P, S, &S.turn[grp], ((i - 1) >> 1) & 1), stop = false;
-    for (int j = 0; j < s.nt; ++j, ++n) {
+    const int j0 = (n0 ^ grp) & 1;           // this group's first tile of the segment
+    for (int j = j0; j < s.nt; j += 2) {
+      const uint32_t n = n0 + j;
       const int sb = n % X::SB, es = n % X::ES, pb = n % X::PB;
       const int pos = (s.fb + (s.t0 + j) * bpt + bi) * kBlockSize + tok;
       const bool valid = pos < s.kv && pos >= first_key;
       fail |= !wwait(P, S, &S.e_full[es], (n / X::ES) & 1);
       const uint32_t kb = lds8(smem_u32(&S.ex[es][0][tid])), vb = lds8(smem_u32(&S.ex[es][1][tid]));
-      fail |= !wwait(P, S, &S.s_full[sb], (n / X::SB) & 1);
+      fail |= !wwait(P, S, &S.s_full[n % X::NB], (n / X::NB) & 1);
       tc_fence_after();
       float s0[2 * G], s1[2 * G];
       const uint32_t at = S.tmem + lane_base + sb * X::NS + 2 * warp * G;
@@ -559,9 +572,8 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&S.s_empty[sb]);
+        mbar_arrive(&S.s_empty[n % X::NB]);
         mbar_arrive(&S.e_empty[es]);
-        if (j == s.nt - 1) mbar_arrive(&S.turn[grp ^ 1]);
       }
       const float fk = exp_scale(kb), ev = vb == kExpNan ? __uint_as_float(0x7FC00000u) : (float)((int)vb - 127);
       float x[G];
@@ -592,18 +604,18 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
             M[g] = tx;
             need = true;
           }
-          if (tok == 0) sts32(smem_u32(&S.alpha[grp][n & 1][slot * G + g]), __float_as_uint(a));
+          if (tok == 0) sts32(smem_u32(&S.alpha[grp][(n >> 1) & 1][slot * G + g]), __float_as_uint(a));
         }
       } else if (tok < G) {
-        sts32(smem_u32(&S.alpha[grp][n & 1][slot * G + tok]), __float_as_uint(1.f));
+        sts32(smem_u32(&S.alpha[grp][(n >> 1) & 1][slot * G + tok]), __float_as_uint(1.f));
       }
-      if (named_bar_or(bar_id, 128, (need && j > 0) || fail || S.abort)) {
+      if (named_bar_or(bar_id, 128, (need && j > 1) || fail || S.abort)) {
         if (named_bar_or(bar_id, 128, fail || S.abort)) {
-          stop = true;
+          fail = true;
           break;
         }
-        // O times the factors, once the products before this tile have landed
-        fail |= !wwait(P, S, &S.pv_done[(n - 1) % X::PB], ((n - 1) / X::PB) & 1);
+        // O times the factors, once the products of this group's tile before have landed
+        fail |= !wwait(P, S, &S.pv_done[(n - 2) % X::PB], ((n - 2) / X::PB) & 1);
         tc_fence_after();
         if (!fail) {
 #pragma unroll 1
@@ -615,7 +627,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
               tmem_ld8(oc + 8 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int u = 0; u < 8; ++u) o[u] *= S.alpha[grp][n & 1][sl * G + (8 * c + u) % G];
+              for (int u = 0; u < 8; ++u) o[u] *= S.alpha[grp][(n >> 1) & 1][sl * G + (8 * c + u) % G];
               tmem_st8(oc + 8 * c, o);
             }
           }
@@ -672,8 +684,8 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[pb]);
     }
-    if (stop) break;
-    // the segment's sums; then the heads' and the slots' factors
+    // the segment's sums; then the heads' and the slots' factors, over both groups.  A group that gave up comes
+    // here too: the other one waits for it.
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
@@ -684,36 +696,34 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
         S.sw[grp][slot * G + g] = M[g];
       }
     }
-    fail |= !wwait(P, S, &S.o_full[grp], (i >> 1) & 1);
-    if (named_bar_or(bar_id, 128, fail || S.abort)) break;
+    if (!fail) fail = !wwait(P, S, &S.o_full, i & 1);
+    if (named_bar_or(3, 256, fail || S.abort)) break;
     tc_fence_after();
-    float hm = kNegInf, hl = 0.f, hw = 0.f;
     if (tid < X::C) {
       const int head = (tid / G) % hg_heads, g = tid % G;
-      for (int b = 0; b < bpt; ++b) hm = fmaxf(hm, S.sm[grp][(b * hg_heads + head) * G + g]);
-      for (int b = 0; b < bpt; ++b) {
-        const int c = (b * hg_heads + head) * G + g;
-        if (S.sm[grp][c] != kNegInf) hl += S.sl[grp][c] * ex2(S.sm[grp][c] - hm);
+      float hm = kNegInf, hl = 0.f;
+      for (int b = 0; b < 2 * bpt; ++b) hm = fmaxf(hm, S.sm[b & 1][((b >> 1) * hg_heads + head) * G + g]);
+      for (int b = 0; b < 2 * bpt; ++b) {
+        const float sl = S.sl[b & 1][((b >> 1) * hg_heads + head) * G + g], sm = S.sm[b & 1][((b >> 1) * hg_heads + head) * G + g];
         // a slot without keys adds nothing; one whose sum is NaN passes it on
-        else if (S.sl[grp][c] != 0.f) hl += S.sl[grp][c];
+        if (sm != kNegInf)
+          hl += sl * ex2(sm - hm);
+        else if (sl != 0.f)
+          hl += sl;
       }
-      hw = S.sw[grp][tid] == kNegInf ? (S.sl[grp][tid] != 0.f ? 1.f : 0.f) : ex2(0.5f * (S.sw[grp][tid] - kWeightBits - hm));
-    }
-    named_bar(bar_id, 128);
-    if (tid < X::C) {
-      S.sw[grp][tid] = hw;
+      S.of[grp][tid] = S.sw[grp][tid] == kNegInf ? (S.sl[grp][tid] != 0.f ? 1.f : 0.f) : ex2(0.5f * (S.sw[grp][tid] - kWeightBits - hm));
       if (tid < hg_heads * G) {
-        S.sl[grp][tid] = hl;
-        S.si[grp][tid] = 1.f / hl;
-        S.sm[grp][tid] = hm;
+        S.hl[grp][tid] = hl;
+        S.hi[grp][tid] = 1.f / hl;
+        S.hm[grp][tid] = hm;
       }
     }
-    named_bar(bar_id, 128);
+    named_bar(3, 256);
     // a range's first segment that began before it is piece 2b, any other one that is cut piece 2b + 1
-    write_out<A, G>(P, W, S, s, grp, o_tmem, hg_heads, s.nt == s.tiles, 2 * (int)blockIdx.x + (s.t0 > 0 ? 0 : 1));
+    write_out<A, G>(P, W, S, s, grp, s.nt > 1 ? 3u : 1u << (n0 & 1), hg_heads, s.nt == s.tiles, 2 * (int)blockIdx.x + (s.t0 > 0 ? 0 : 1));
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.o_free[i % X::OB]);
+    if (lane == 0) mbar_arrive(&S.o_free);
   }
 }
 
@@ -738,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.e_full[i], 32);
       mbar_init(&S.e_empty[i], 4);
     }
-    for (int i = 0; i < X::SB; ++i) {
+    for (int i = 0; i < X::NB; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.s_empty[i], 4);
     }
@@ -746,11 +756,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i], 4);
       mbar_init(&S.pv_done[i], 1);
     }
-    for (int i = 0; i < X::OB; ++i) mbar_init(&S.o_free[i], 4);
+    mbar_init(&S.o_full, 1);
+    mbar_init(&S.o_free, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.q_full[i], 128);
-      mbar_init(&S.turn[i], 4);
-      mbar_init(&S.o_full[i], 1);
+      mbar_init(&S.q_free[i], 1 + 8);   // its products are done; the softmax warps have its factors
       mbar_init(&S.drain[i], 1);
     }
     S.abort = 0;
@@ -780,6 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     load_tiles<A, G, false>(P, &vmap, S, plan, hg_heads);
   else if (warp == 10)
     issue_s<A, G>(P, S, plan, nhg);
+  else if (warp >= 12)
+    queries<A, G>(P, S, plan, hg_heads);
   else
     issue_pv<A, G>(P, S, plan, nhg);
   tc_fence_before();
