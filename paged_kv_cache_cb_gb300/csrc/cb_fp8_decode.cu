@@ -88,7 +88,7 @@ struct alignas(1024) Smem {
   uint8_t q[2][16 * G * A];          // of two segments: rows (term, slot, g) of A bytes, swizzled like K
   uint8_t p[X::PB][256 * X::SS];     // w: [2 slots][2 SS rows][32 bytes], 8-row x 16-byte core matrices
   uint8_t ex[X::ES][2][128];         // exponent bytes of the tile's K and V rows
-  float cf[2][X::C];                 // of two segments: scale log2(e) 2^eq per column
+  alignas(16) float cf[2][X::C];                 // of two segments: scale log2(e) 2^eq per column
   float alpha[2][2][X::C];           // per group: factors of O when M moves
   float sl[2][X::C], sm[2][X::C], sw[2][X::C];   // per group: a segment's l, m, M
   float of[2][X::C];                 // per group: the slots' factors of O
@@ -107,6 +107,20 @@ struct Plan {
   const int *pre, *kv, *tok;
 };
 
+// N consecutive floats of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_n(uint32_t a, float* v) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 x = lds128(a + 4 * i);
+      v[i] = __uint_as_float(x.x), v[i + 1] = __uint_as_float(x.y), v[i + 2] = __uint_as_float(x.z), v[i + 3] = __uint_as_float(x.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lds32f(a + 4 * i);
+  }
+}
 // N (2, 4, 8, 16) consecutive fp32 columns of this thread's TMEM lane (no wait).
 template <int N>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
@@ -492,26 +506,28 @@ __device__ void write_out(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
   for (int hh = grp; hh < hg_heads; hh += 2) {
     float acc[G], inv[G];
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      acc[g] = 0.f;
-      inv[g] = lds32f(smem_u32(&S.hi[grp][hh * G + g]));
-    }
-    for (int k = 0; k < 2 * bpt; ++k) {
-      const int ob = k & 1, slot = (k >> 1) * hg_heads + hh;
-      if (!((obs >> ob) & 1)) continue;
-      float o[X::SS];
-      const uint32_t at = base + ob * X::NO + slot * X::SS, of = smem_u32(&S.of[ob][slot * G]);
-      if constexpr (X::SS == 24) {
-        tmem_ld<16>(at, o);
-        tmem_ld<8>(at + 16, o + 16);
-      } else {
-        tmem_ld<X::SS>(at, o);
+    for (int g = 0; g < G; ++g) acc[g] = 0.f;
+    lds_n<G>(smem_u32(&S.hi[grp][hh * G]), inv);
+    for (int bi = 0; bi < bpt; ++bi) {
+      const int slot = bi * hg_heads + hh;
+      float o[2][X::SS], f[2][G];
+#pragma unroll
+      for (int ob = 0; ob < 2; ++ob) {
+        const uint32_t at = base + ob * X::NO + slot * X::SS;
+        if constexpr (X::SS == 24) {
+          tmem_ld<16>(at, o[ob]);
+          tmem_ld<8>(at + 16, o[ob] + 16);
+        } else {
+          tmem_ld<X::SS>(at, o[ob]);
+        }
+        lds_n<G>(smem_u32(&S.of[ob][slot * G]), f[ob]);
       }
       tmem_wait_ld();
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float f = lds32f(of + g * 4);
-        acc[g] += ((o[g] + o[G + g] + o[2 * G + g]) * f) * (f * inv[g]);
+      for (int ob = 0; ob < 2; ++ob) {
+        if (!((obs >> ob) & 1)) continue;      // whatever the buffer holds
+#pragma unroll
+        for (int g = 0; g < G; ++g) acc[g] += ((o[ob][g] + o[ob][G + g] + o[ob][2 * G + g]) * f[ob][g]) * (f[ob][g] * inv[g]);
       }
     }
 #pragma unroll
