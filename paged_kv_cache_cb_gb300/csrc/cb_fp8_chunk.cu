@@ -714,17 +714,19 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     tc_fence_after();
     const float inv = l != 0.f ? 1.f / l : 0.f;              // 0: a piece in which the row saw no key
     // a range's first piece that began before it is 2b, any other one that is cut 2b + 1
-    const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kRows + side * kTileM + row;
-    if (cut) *reinterpret_cast<float2*>(W.ml + pr * 2) = make_float2(m, l);
+    const size_t piece = (size_t)2 * blockIdx.x + (began ? 0 : 1);
+    const int prow = side * kTileM + row;
+    if (cut) *reinterpret_cast<float2*>(W.ml + (piece * kRows + prow) * 2) = make_float2(m, l);
 #pragma unroll 1
     for (int c = 0; c < A / 32; ++c) {
       float o[32];
       tmem_ld32(o_t + 32 * c, o);
       tmem_wait_ld();
       if (cut) {
-        float4* d = reinterpret_cast<float4*>(W.acc + pr * A + 32 * c);
+        // 4 dimensions of all rows together: a warp's store is 512 bytes in a row
+        float4* d = reinterpret_cast<float4*>(W.acc) + (piece * (A / 4) + 8 * c) * kRows + prow;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
+        for (int k = 0; k < 8; ++k) d[k * kRows] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv, o[4 * k + 3] * inv);
       } else if (ti < tok_hi) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)

@@ -62,17 +62,40 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
     return;
   }
-  // kWarps rows of a chunk's item at a time, a warp per row
+  // 32 rows of a chunk's item at a time: a lane per row, A / 8 dimensions per warp
+  constexpr int V = A / 32;                  // float4 columns per warp
   const int group = P.n_q_heads / P.cache.n_kv_heads, tok = kTileM / group;
-  for (int task = blockIdx.x - n_singles; task < n_owner * (kChunkRows / kWarps); task += gridDim.x - n_singles) {
-    const int b = owner[task / (kChunkRows / kWarps)];
+  for (int task = blockIdx.x - n_singles; task < n_owner * (kChunkRows / 32); task += gridDim.x - n_singles) {
+    const int b = owner[task / (kChunkRows / 32)];
     const Fp8Rec rec = W.rec[b];
+    const int row = (task % (kChunkRows / 32)) * 32 + lane, n = rec.n;
+    auto piece = [&](int i) { return (size_t)(i == 0 ? 2 * b + 1 : 2 * (b + i)); };
+    auto ml = [&](int i) { return *reinterpret_cast<const float2*>(W.ml + (piece(i) * kChunkRows + row) * 2); };
+    float M = -__int_as_float(0x7f800000), L = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) M = fmaxf(M, ml(i).x);
+    float4 y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float2 x = ml(i);
+      const float f = x.x == -__int_as_float(0x7f800000) ? x.y : x.y * ex2(x.x - M);
+      L += f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float4 a = reinterpret_cast<const float4*>(W.acc)[(piece(i) * (A / 4) + warp * V + v) * kChunkRows + row];
+        y[v].x += f * a.x, y[v].y += f * a.y, y[v].z += f * a.z, y[v].w += f * a.w;
+      }
+    }
     const int q0 = __ldg(P.cu_q_lens + rec.r), q_len = __ldg(P.cu_q_lens + rec.r + 1) - q0;
-    const int row = (task % (kChunkRows / kWarps)) * kWarps + warp;
     const int ti = rec.pad * 2 * tok + row / group;            // rows of tile B follow tile A's: its tokens do too
     if (ti >= q_len) continue;
-    join_row<A>(W, kChunkRows, b, rec.n, row, 0, 1, o);
-    store_row<A>(P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + lane * D, o);
+    uint16_t* dst = P.out + ((size_t)(q0 + ti) * P.n_q_heads + (size_t)rec.hg * group + row % group) * A + warp * (A / 8);
+#pragma unroll
+    for (int v = 0; v < V; v += 2)
+      *reinterpret_cast<uint4*>(dst + 4 * v) = make_uint4(pack_bf16(y[v].x / L, y[v].y / L), pack_bf16(y[v].z / L, y[v].w / L),
+                                                          pack_bf16(y[v + 1].x / L, y[v + 1].y / L), pack_bf16(y[v + 1].z / L, y[v + 1].w / L));
   }
 }
 

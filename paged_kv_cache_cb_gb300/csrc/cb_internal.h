@@ -150,11 +150,12 @@ struct Fp8Rec {
   int r, hg, n, pad;            // pad: the chunk kernel's pair of query tiles (hg: its KV head)
 };
 // Partial results of attention: per CTA two (its first and its last piece), `rows`
-// rows of A values and of (max, sum) each.
+// rows of A values and of (max, sum) each.  The values of the single tokens' pieces
+// stand row by row, the chunks' [A / 4][rows][4].
 struct Fp8Partials {
   Fp8Rec* rec;                  // [kMaxDecodeGrid]
   float* ml;                    // [2 * kMaxDecodeGrid][rows][2]
-  float* acc;                   // [2 * kMaxDecodeGrid][rows][A]
+  float* acc;                   // [2 * kMaxDecodeGrid][rows * A]
 };
 constexpr int kSingleRows = 64, kChunkRows = 256;   // of the single tokens' pieces, of the chunks'
 inline size_t fp8_partials_bytes(int rows, int head_dim) {
