@@ -27,6 +27,8 @@ Modules:
                   masks, the per-request step and the explicit ragged form.
     paged      -- slot mapping from block tables, the append loop, the gather of a
                   request's contiguous K/V from a paged pool.
+    fp8        -- the 8-bit cache's row format: e4m3 codes and one exponent byte, and
+                  the values they stand for.
     sizes      -- KV-cache byte formulas, chunk counts, padding counts.
     scheduler  -- FCFS iteration-level scheduler with a block allocator and
                   recompute preemption (host metadata only).

@@ -25,14 +25,23 @@
 //
 // Work.  All items' key tiles, laid end to end, are cut into one equal range per
 // CTA (one CTA per SM); an item cut at a range's end leaves (m, l, o) per piece
-// and a second kernel joins them.  Where whole items, dealt to the CTAs in turn,
-// end sooner than the cut ranges and their joining, they stay whole.
+// and a second kernel (cb_fp8_join.cu) joins them.  Where whole items, dealt to the
+// CTAs in turn, end sooner than the cut ranges and their joining, they stay whole.
 //
 // Warps: 0-3 and 4-7 softmax of tiles A and B (thread = row; the row's 128
 // scores stay in registers, one read of tensor memory; also the query's terms and
 // the output), 8-11 convert V from a staged copy, in short loops (the warps'
-// code shares one instruction cache), 12 issues the products, 13 loads K, V and
+// code shares one instruction cache), 12 issues the products, 13 loads K, 15 V and
 // the exponents, 14 walks the work and publishes it.  Every wait is bounded.
+//
+// Bound by the tensor pipe and the softmax in turn: 2048 new tokens after 30720
+// keys (32 heads on 8) take 916 us, 1.16 PFLOP/s, 0.61 of cuBLAS's bf16 rate; one
+// thread issues the products, every wait of its warp between them is idle time of
+// the pipe (a second issuing warp was slower), and an item's start and end cost
+// about 8 us.  Single tokens (below): 256 requests of 32 heads on 1 KV head (1024
+// to 16384 keys, 539 MB) take 169 us, 3.2 TB/s, 0.47 of a copy's rate: a key tile
+// of 32 KB passes shared memory 5.5 times (loaded, read and written again as bf16
+// V, read by the products, the query's terms with them), over 1400 cycles of it.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -44,8 +53,11 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kRows = kChunkRows;      // rows of an item (two query tiles)
-constexpr int kMinTiles = 4;           // key tiles per CTA below which a step uses fewer CTAs
-constexpr int kCutTiles = 7;           // what cutting items costs, in key tiles' time (partial results and their joining)
+// What cutting items costs, in key tiles' time (2 us): the pieces' queries and
+// partial results, their joining.  813 new tokens under a window of 1000: whole
+// items (10 tiles) 51 us, cut ones (6.5) 63 us; 1024 after 1024 and 2048 keys, next
+// to 48 single tokens: whole (20) 140 us, cut (12.2) 156 us.
+constexpr int kCutTiles = 10;
 constexpr int kSmemLimit = 232448;
 
 // An item, and the piece [a, b) of its key tiles [first, end); b = a: no more items.
@@ -272,8 +284,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
   if (tid == 0) {
     tpre[n] = total;
     ipre[n] = items;
-    const int grid = gridDim.x, b = blockIdx.x;
-    const int eff = max(1, min(grid, (total + kMinTiles - 1) / kMinTiles));
+    const int grid = gridDim.x, b = blockIdx.x, eff = max(1, min(grid, total));
     S.tiles = total;
     S.items = items;
     S.whole = (long long)((items + grid - 1) / grid) * S.longest <= (total + grid - 1) / grid + kCutTiles;
@@ -746,10 +757,12 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
 // A step's requests with one new token: an item is (request, KV head) with G rows.
 // A query tile holds them four times, at rows 0, 32, 64 and 96, and warp w's copy
 // takes the tile's keys 32 w .. 32 w + 31 only (its weights of the others are zeros),
-// so that the four warps of a tile share its softmax.  Both tiles of tensor memory
-// take the same rows, A the even key tiles and B the odd ones, and one's softmax
-// runs under the other's products.  At the end of an item the eight copies' (m, l,
-// O) are joined through shared memory (Q's second tile, not used here).
+// so that the four warps of a tile share its softmax (one warp per tile: 220 us
+// instead of 199 for 256 requests).  Both tiles of tensor memory take the same rows,
+// A the even key tiles and B the odd ones, and one's softmax runs under the other's
+// products.  At the end of an item the eight copies' (m, l, O) are joined through
+// shared memory (Q's second tile, not used here).  The warps that convert V write
+// the next item's query rows as soon as this one's last S is done (199 -> 179 us).
 template <int A>
 __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
   constexpr uint32_t kIdescS = idesc_f8(128, 128, 0, 0, 0, 0), kIdescO = idesc_bf16_f32(128, A, 1);

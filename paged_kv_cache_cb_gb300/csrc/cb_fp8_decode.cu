@@ -40,14 +40,25 @@
 // Work.  A sequence is a (request, group of HG heads).  All sequences' tiles,
 // laid end to end, are cut into one equal range per CTA (one CTA per SM).  A
 // sequence cut at a range's end leaves (m, l, o) per piece, and a second small
-// kernel joins the pieces by log-sum-exp: no counters, no grid barrier, nothing
-// to initialise, and the same bits every time.
+// kernel (cb_fp8_join.cu) joins the pieces by log-sum-exp: no counters, no grid
+// barrier, nothing to initialise, and the same bits every time.
 //
-// Warps: 0-3 and 4-7 softmax groups, which take the segments (a range's parts of
-// sequences) in turn, so that one group's segment start (query terms) and end
-// (output) overlap the other's tiles; 8 K loads, 9 V loads (TMA through the block
-// table), 10 issues S, 11 issues O.  Thread = tile row, then output dimension.
-// Every wait is bounded.
+// Warps: 0-3 and 4-7 softmax groups, which share a range's parts of sequences
+// (segments) tile by tile: every second tile each, with its own maxima, sums and O
+// in tensor memory, joined at the segment's end.  A tile's chain (scores, maxima,
+// weights, one barrier of the group for a move of O) is mostly waiting, so two
+// tiles at a time take little more than one: with a segment per group in turn, 48
+// decodes took 104 us instead of 90.  8 K loads, 9 V loads (TMA through the block
+// table; the exponents by per-thread copies: a TMA copy of 16 bytes takes the unit
+// as long as one of 2 KB), 10 issues S, 11 issues O, 12-15 make the next segments'
+// query terms ready.  Thread = tile row, then output dimension.  Every wait is
+// bounded.
+//
+// Bound by HBM where a KV head has one query head: 64 decodes of 32 heads (512 to
+// 4096 keys, 1.30 GB) in 199 us, 6.5 TB/s, 0.96 of a copy's rate.  With four, a
+// tile's softmax is four times the work: 48 decodes (256 to 8192 keys, 461 MB) in 90
+// us, 5.1 TB/s, 0.75; a segment's end adds 4.5 us to its CTA.  Two sequences of 4900
+// keys: 25 us, of which 12 in this kernel's pieces of 4 tiles.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -58,7 +69,6 @@ namespace cb {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kMinTiles = 2;        // tiles per CTA below which a step uses fewer CTAs
 constexpr float kWeightBits = 12.f; // weights are stored times 2^12 (e5m2: up to 2^15.8, down to 2^-16)
 constexpr float kLazyP = 8.f;       // the running maxima follow only beyond these (base 2)
 constexpr float kLazyW = 3.f;
@@ -247,7 +257,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
   if (tid == 0) {
     pre[n] = total;
     total *= nhg;
-    const int eff = max(1, min((int)gridDim.x, (total + kMinTiles - 1) / kMinTiles));
+    const int eff = max(1, min((int)gridDim.x, total));   // a tile per CTA at least: 4 x 250 keys 18 us, with two tiles 21
     const int b = blockIdx.x;
     S.total = total;
     S.eff = eff;

@@ -110,6 +110,10 @@ def test_attention_arguments():
         assert call(*args(wsb=16)) == -3
     for bad in ((None, D, D), (D, ODD, D), (D, D, None)):
         assert L.cb_kv_append_paged_attention_fp8(*bad, *args()) == -1
+    # key tiles that 32 bits cannot count: of the single tokens, of the chunks
+    big = dict(hq=8, hk=8, nr=1024, nt=1024, mkv=1 << 22, maxb=1 << 18)
+    assert f(*args(mq=1, **big)) == -1 and f(*args(mq=1, **{**big, "maxb": 1 << 17}, wsb=16)) == -3
+    assert f(*args(mq=1 << 20, **{**big, "maxb": 1 << 17, "nt": 1 << 27})) == -1
 
 
 def test_workspace_size():

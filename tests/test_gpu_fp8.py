@@ -1,11 +1,15 @@
 """The 8-bit KV cache on the GPU: append and read-back bit for bit against the
 float64 definition, attention against the fp64 oracle over the stored values."""
+import math
+
 import numpy as np
 import pytest
 import torch
 
+import workloads as wl
 from fp8_util import BS, Step, check
 from gpu_util import L
+from oracle import attention as oa
 from oracle import fp8 as of8
 
 pytestmark = pytest.mark.gpu
@@ -500,3 +504,61 @@ def test_two_graphs_replayed_at_once():
         torch.cuda.synchronize()
         for m in made:
             assert torch.equal(m[1], m[2])
+
+
+# ------------------------------------------------------------------ a serving loop
+@pytest.mark.parametrize("hq,hk,a,prefix,seed", [(32, 8, 128, 20, 0), (32, 1, 128, 37, 1), (4, 4, 64, 23, 3)])
+def test_scheduled_trace_with_shared_prefixes(hq, hk, a, prefix, seed):
+    """The scheduler's trace, prefixes shared through the block tables: each step's
+    block copies, then its append and attention as one call.  Every request's output
+    is that of its own quantised keys in fp64, and a finished step's rows read back
+    are theirs."""
+    lib = L()
+    tr = wl.with_prefixes(wl.small_trace(seed, num_blocks=28), 3, prefix, seed=seed)
+    max_len = max(p + o for _, p, o, _, _ in tr.requests)
+    rng = np.random.default_rng(seed)
+    bf = lambda *n: torch.from_numpy(rng.standard_normal(n)).to(torch.bfloat16)  # noqa: E731
+    # contents 0 .. 2: the groups' prefixes; then a request's own rows
+    K, V = bf(3 + len(tr.requests), max_len, hk, a), bf(3 + len(tr.requests), max_len, hk, a)
+    Q = bf(len(tr.requests), max_len, hq, a)
+    K8, V8 = (of8.values(*of8.quantise(x.double().numpy())) for x in (K, V))
+    content = lambda r, p: tr.requests[r][3] if tr.requests[r][3] >= 0 and p < tr.requests[r][4] else 3 + r  # noqa: E731
+    maxblk = max(-(-(p + o - 1) // BS) for _, p, o, _, _ in tr.requests)
+    sched = lib.Scheduler(tr.num_blocks, BS, tr.token_budget, tr.token_budget, wl.free_order(tr.num_blocks, tr.seed), maxblk)
+    for t in tr.requests:
+        sched.add_request(*t)
+    cache = [torch.full((tr.num_blocks, hk, BS, a), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+             for _ in range(2)] + [torch.full((tr.num_blocks, hk, BS), 254, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scale = 1.0 / math.sqrt(a)
+    ws = torch.empty(lib.cb_paged_attention_fp8_workspace_size(tr.token_budget, tr.token_budget, tr.token_budget, max_len, hq, hk,
+                                                               a, BS), dtype=torch.uint8, device="cuda")
+    copies = 0
+    while not sched.done():
+        m = sched.step()
+        pairs = sched.step_copies()
+        if len(pairs):
+            lib.cb_copy_blocks_fp8(torch.from_numpy(pairs).cuda(), *cache)
+            copies += len(pairs)
+        b = len(m["req_ids"])
+        if b == 0:
+            continue
+        rows = [(int(r), p) for r, c, n in zip(m["req_ids"], m["ctx_lens"], m["q_lens"]) for p in range(c, c + n)]
+        k_new, v_new = (torch.stack([x[content(r, p), p] for r, p in rows]).cuda() for x in (K, V))
+        q = torch.stack([Q[r, p] for r, p in rows]).cuda()
+        out = torch.full_like(q, float("nan"))
+        q_lens, ctx = m["q_lens"].astype(np.int32), m["ctx_lens"].astype(np.int32)
+        slots = torch.from_numpy(m["slot_mapping"][:len(rows)]).cuda()
+        lib.cb_kv_append_paged_attention_fp8(
+            k_new, v_new, slots, q, torch.from_numpy(m["cu_q_lens"][:b + 1].astype(np.int32)).cuda(), torch.from_numpy(ctx).cuda(),
+            torch.from_numpy(np.ascontiguousarray(m["block_tables"][:b])).cuda(), *cache, out, scale, ws, int(q_lens.max()),
+            int((q_lens + ctx).max()))
+        assert lib.cb_last_error() == 0
+        ks, vs = ([np.stack([x[content(int(r), p), p] for p in range(c + n)]) for r, c, n in zip(m["req_ids"], ctx, q_lens)]
+                  for x in (K8, V8))
+        f = lambda v: oa.attention_step(q.double().cpu().numpy(), q_lens.tolist(), ctx.tolist(), ks, v, scale, hq, hk)  # noqa: E731
+        check(out, f(vs), f([np.abs(v) for v in vs]), "step")
+        back = [torch.empty_like(k_new), torch.empty_like(v_new)]
+        lib.cb_kv_gather_fp8(slots, *cache, *back)
+        for got, x in zip(back, (K8, V8)):
+            assert np.array_equal(got.double().cpu().numpy(), np.stack([x[content(r, p), p] for r, p in rows]))
+    assert copies > 0
