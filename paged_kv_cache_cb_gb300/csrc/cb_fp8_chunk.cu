@@ -676,7 +676,6 @@ __device__ __forceinline__ void softmax_tile(Smem<A>& S, uint32_t s_t, uint32_t 
 template <int A, int G>
 __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int side) {
   constexpr int TOK = kTileM / G;
-  const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lane_base = (uint32_t)(row & ~31) << 16;
   const uint32_t s_t = S.tmem + lane_base + side * 128, o_t = S.tmem + lane_base + 256 + side * A;
@@ -842,13 +841,13 @@ __device__ __forceinline__ bool meet(const Fp8Step& P, SM& S, uint32_t& phase) {
 
 template <int A, int G>
 __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int side) {
-  static_assert(G <= 32 && 8 * 32 * 32 * 4 <= (int)sizeof(S.q[1]), "a quarter of the copies' O fits in Q's second tile");
+  static_assert(G <= 32 && 8 * 32 * 32 * 4 <= (int)sizeof(S.q[1]), "32 dimensions of each side's copies fit in Q's second tile");
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & 3, copy = 4 * side + w;
   const uint32_t lanes = (uint32_t)(32 * w) << 16;
   const uint32_t s_t = S.tmem + lanes + side * 128, o_t = S.tmem + lanes + 256 + side * A, xs = smem_u32(S.q[1]);
   Items<Smem<A>> items;
-  uint32_t n = 0, ns = 0, nt = 0, phase = 0;   // key tiles of all items; this side's; items in which this side has tiles
+  uint32_t n = 0, ns = 0, nb = 0, phase = 0;   // key tiles of all items; this side's; items in which B has tiles
   for (uint32_t i = 0;; ++i) {
     const Item* item = items.next(P, S);
     if (!item) break;
@@ -861,7 +860,6 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     float fq = 0.f;
     items.done(S);
     float m = kNegInf, l = 0.f;
-    const bool any = a0 + side < b0;
     for (int j = a0 + side; j < b0; j += 2, ++ns) {
       const uint32_t nj = n + (j - a0);
       // (the factors' barrier: see softmax())
@@ -940,69 +938,84 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[side][0]);
     }
-    if (any) {
-      ok = ok && wwait(P, S, &S.o_full[side], nt & 1);
-      ++nt;
-    }
+    const bool both = a0 + 1 < b0;                             // B has tiles
+    ok = ok && wwait(P, S, &S.o_full[0], i & 1) && (!both || wwait(P, S, &S.o_full[1], nb & 1));
     if (!ok) {
       S.abort = 1;
       break;
     }
     tc_fence_after();
-    // the copies' maxima and sums, then their O a quarter of the dimensions at a time
+    // the copies' maxima and sums; then O, half of the dimensions per side, 32 of them at a time: a warp adds both
+    // tiles' rows, then four warps' copies are added through shared memory
     sts32(xs + (copy * 32 + lane) * 8, __float_as_uint(m));
     sts32(xs + (copy * 32 + lane) * 8 + 4, __float_as_uint(l));
     if (!meet(P, S, phase)) break;
-    float mm = kNegInf, ls = 0.f;
+    float mm = kNegInf, ls = 0.f, f[2];
     for (int c = 0; c < 8; ++c) mm = fmaxf(mm, lds32f(xs + (c * 32 + lane) * 8));
+    // -inf: no key seen, or NaNs only (then the sum is one)
+    auto weight = [&](int c, float& lc) {
+      const float mc = lds32f(xs + (c * 32 + lane) * 8);
+      lc = lds32f(xs + (c * 32 + lane) * 8 + 4);
+      return mc == kNegInf ? (lc != 0.f ? 1.f : 0.f) : ex2(mc - mm);
+    };
     for (int c = 0; c < 8; ++c) {
-      const float mc = lds32f(xs + (c * 32 + lane) * 8), lc = lds32f(xs + (c * 32 + lane) * 8 + 4);
-      ls += mc == kNegInf ? lc : ex2(mc - mm) * lc;            // -inf: no key seen, or NaNs only (then lc is one)
+      float lc;
+      const float wc = weight(c, lc);
+      ls += wc * lc;
+      if ((c & 3) == w) f[c >> 2] = wc;
     }
-    const float f = (m == kNegInf ? (l != 0.f ? 1.f : 0.f) : ex2(m - mm)) / ls;
+    f[0] /= ls;
+    f[1] /= ls;
     const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kSingleRows;
     if (cut && copy == 0 && lane < G) *reinterpret_cast<float2*>(W.ml + (pr + lane) * 2) = make_float2(mm, ls);
+    const uint32_t o_a = S.tmem + lanes + 256, xh = xs + side * (128 * 128);
 #pragma unroll 1
-    for (int c = 0; c < A / 32 && ok; ++c) {
-      float o[32];
-      if (any) {
-        tmem_ld32(o_t + 32 * c, o);
-        tmem_wait_ld();
-      } else {
+    for (int c = 0; c < A / 64 && ok; ++c) {
+      const int d0 = (A / 2) * side + 32 * c;                  // this side's dimensions
+      float o[32], ob[32];
+      tmem_ld32(o_a + d0, o);
+      if (both) tmem_ld32(o_a + A + d0, ob);
+      tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-      }
+      for (int k = 0; k < 32; ++k) o[k] = both ? o[k] * f[0] + ob[k] * f[1] : o[k] * f[0];
       ok = meet(P, S, phase);                                  // what was there has been read
       // row `lane` of this copy: 32 values, their 16-byte chunks in an order that spreads the banks
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        sts128(xs + (copy * 32 + lane) * 128 + ((k ^ (lane & 7)) << 4),
-               make_uint4(__float_as_uint(o[4 * k] * f), __float_as_uint(o[4 * k + 1] * f), __float_as_uint(o[4 * k + 2] * f),
-                          __float_as_uint(o[4 * k + 3] * f)));
+        sts128(xh + (w * 32 + lane) * 128 + ((k ^ (lane & 7)) << 4),
+               make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3])));
       ok = ok && meet(P, S, phase);
-      // 256 threads: row r, dimensions 4 k .. 4 k + 3
-      const int r = threadIdx.x >> 3, k = threadIdx.x & 7;
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      // this side's 128 threads: rows r and r + 16, dimensions 4 k .. 4 k + 3
+      const int k = threadIdx.x & 7;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const uint4 x = lds128(xs + (q * 32 + r) * 128 + ((k ^ (r & 7)) << 4));
-        y[0] += __uint_as_float(x.x);
-        y[1] += __uint_as_float(x.y);
-        y[2] += __uint_as_float(x.z);
-        y[3] += __uint_as_float(x.w);
-      }
-      if (ok && r < G) {
-        if (cut)
-          *reinterpret_cast<float4*>(W.acc + (pr + r) * A + 32 * c + 4 * k) = make_float4(y[0], y[1], y[2], y[3]);
-        else
-          *reinterpret_cast<uint2*>(P.out + ((size_t)tok * P.n_q_heads + (size_t)g * G + r) * A + 32 * c + 4 * k) =
-              make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+      for (int h = 0; h < 2; ++h) {
+        const int r = 16 * h + ((threadIdx.x & 127) >> 3);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 x = lds128(xh + (q * 32 + r) * 128 + ((k ^ (r & 7)) << 4));
+          y[0] += __uint_as_float(x.x);
+          y[1] += __uint_as_float(x.y);
+          y[2] += __uint_as_float(x.z);
+          y[3] += __uint_as_float(x.w);
+        }
+        if (ok && r < G) {
+          if (cut)
+            *reinterpret_cast<float4*>(W.acc + (pr + r) * A + d0 + 4 * k) = make_float4(y[0], y[1], y[2], y[3]);
+          else
+            *reinterpret_cast<uint2*>(P.out + ((size_t)tok * P.n_q_heads + (size_t)g * G + r) * A + d0 + 4 * k) =
+                make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        }
       }
     }
     if (!ok) break;
     tc_fence_before();
     if (!meet(P, S, phase)) break;                             // the exchange is free for the next item
-    if (lane == 0 && any) mbar_arrive(&S.o_free[side]);
+    if (lane == 0) {
+      mbar_arrive(&S.o_free[0]);
+      if (both) mbar_arrive(&S.o_free[1]);
+    }
+    nb += both;
     n += b0 - a0;
   }
 }
@@ -1029,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.p_full[i][0], 4);
       mbar_init(&S.p_full[i][1], 4);
       mbar_init(&S.o_full[i], 1);
-      mbar_init(&S.o_free[i], 4);
+      mbar_init(&S.o_free[i], ONE ? 8 : 4);
     }
     mbar_init(&S.q_free, 1);
     mbar_init(&S.x_bar, 8);
