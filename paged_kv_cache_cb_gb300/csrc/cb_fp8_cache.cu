@@ -1,5 +1,9 @@
 // The 8-bit KV cache's data movement: append with quantisation, read-back and
 // block copies (format: cb_fp8.cuh).
+//
+// One pass each, bound by HBM: 65,536 new tokens (8 KV heads of 128, 404 MB) in 70
+// us, 5.8 TB/s, 0.85 of a copy's rate; 32,768 rows read back (202 MB) in 35 us, 5.8
+// TB/s, 0.86.  A step's few tokens take the launch, 3.5 us of GPU time.
 #include <algorithm>
 
 #include "cb_fp8.cuh"
@@ -8,7 +12,8 @@ namespace cb {
 
 namespace {
 
-constexpr int kThreads = 256, kPieces = 2;
+constexpr int kThreads = 256;
+constexpr int kPieces = 2;             // per thread, in flight (append, read-back: 1 73, 40 us; 2 70, 36; 4 69, 38)
 
 // 8 bf16 (16 bytes) of a row, its largest |bits| over LANES consecutive lanes.
 template <int LANES>

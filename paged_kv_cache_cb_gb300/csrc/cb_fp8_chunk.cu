@@ -35,13 +35,13 @@
 // the exponents, 14 walks the work and publishes it.  Every wait is bounded.
 //
 // Bound by the tensor pipe and the softmax in turn: 2048 new tokens after 30720
-// keys (32 heads on 8) take 916 us, 1.16 PFLOP/s, 0.61 of cuBLAS's bf16 rate; one
+// keys (32 heads on 8) take 905 us, 1.18 PFLOP/s, 0.61 of cuBLAS's bf16 rate; one
 // thread issues the products, every wait of its warp between them is idle time of
 // the pipe (a second issuing warp was slower), and an item's start and end cost
 // about 8 us.  Single tokens (below): 256 requests of 32 heads on 1 KV head (1024
-// to 16384 keys, 539 MB) take 169 us, 3.2 TB/s, 0.47 of a copy's rate: a key tile
-// of 32 KB passes shared memory 5.5 times (loaded, read and written again as bf16
-// V, read by the products, the query's terms with them), over 1400 cycles of it.
+// to 16384 keys, 539 MB) take 162 us, 3.3 TB/s, 0.49 of a copy's rate: a tile's
+// conversion (1500 cycles of a warp, which shares the memory's bandwidth with the
+// products' operands) is the longest part of its chain, HBM's share 1400.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"

@@ -56,9 +56,9 @@
 //
 // Bound by HBM where a KV head has one query head: 64 decodes of 32 heads (512 to
 // 4096 keys, 1.30 GB) in 199 us, 6.5 TB/s, 0.96 of a copy's rate.  With four, a
-// tile's softmax is four times the work: 48 decodes (256 to 8192 keys, 461 MB) in 90
-// us, 5.1 TB/s, 0.75; a segment's end adds 4.5 us to its CTA.  Two sequences of 4900
-// keys: 25 us, of which 12 in this kernel's pieces of 4 tiles.
+// tile's softmax is four times the work: 48 decodes (256 to 8192 keys, 461 MB) in 89
+// us, 5.2 TB/s, 0.77; a segment's end adds 4.5 us to its CTA.  Two sequences of 4900
+// keys: 25 us, of which 12 in this kernel, 4 tiles per CTA.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
