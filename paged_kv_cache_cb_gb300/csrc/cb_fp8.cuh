@@ -158,16 +158,23 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 //     sum_i W_i o_i / sum_i W_i,   W_i = 2^(m_i - M) l_i,  M = max m_i,
 // in the pieces' order.  m = -inf: no key seen (l = 0), or NaNs only (l is one).
 constexpr int kJoinLoads = (kMaxDecodeGrid + 31) / 32;   // pieces per lane
-// The CTAs whose records start such a sequence, into owner[]; their number.  One warp.
-__device__ __forceinline__ int join_owners(const Fp8Partials& W, int ctas, int* owner) {
+// The CTAs whose records start such a sequence and those records, into owner[] and
+// rec[]; their number.  One warp.
+__device__ __forceinline__ int join_owners(const Fp8Partials& W, int ctas, int* owner, Fp8Rec* rec) {
   const int lane = threadIdx.x & 31;
-  int n[kJoinLoads], found = 0;
+  int4 x[kJoinLoads];
+  int found = 0;
 #pragma unroll
-  for (int k = 0; k < kJoinLoads; ++k) n[k] = lane + 32 * k < ctas ? W.rec[lane + 32 * k].n : 0;
+  for (int k = 0; k < kJoinLoads; ++k)
+    x[k] = lane + 32 * k < ctas ? reinterpret_cast<const int4*>(W.rec)[lane + 32 * k] : make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int k = 0; k < kJoinLoads; ++k) {
-    const unsigned mask = __ballot_sync(0xffffffffu, n[k] > 1);
-    if (n[k] > 1) owner[found + __popc(mask & ((1u << lane) - 1))] = lane + 32 * k;
+    const unsigned mask = __ballot_sync(0xffffffffu, x[k].z > 1);
+    if (x[k].z > 1) {
+      const int at = found + __popc(mask & ((1u << lane) - 1));
+      owner[at] = lane + 32 * k;
+      rec[at] = {x[k].x, x[k].y, x[k].z, x[k].w};
+    }
     found += __popc(mask);
   }
   return found;

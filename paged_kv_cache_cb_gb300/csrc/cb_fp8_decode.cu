@@ -37,8 +37,12 @@
 // head are joined at the end of a sequence.  Head dimension 64: V^T has 64 rows,
 // its descriptor repeats them (leading offset 0) to M = 128.
 //
-// Work.  A sequence is a (request, group of HG heads).  All sequences' tiles,
-// laid end to end, are cut into one equal range per CTA (one CTA per SM).  A
+// Work.  A sequence is a (request, group of HG heads).  All sequences' tiles, each
+// sequence's behind kLead empty places, laid end to end, are cut into one equal
+// range per CTA (one CTA per SM).  The empty places stand for what a sequence's end
+// costs its CTA (4.5 us; without them and with: 2 sequences 26.0 and 23.3 us, 48 90.7
+// and 87.1, 200 of 50-1000 keys 74 and 62.6; 100 of 50-600 keys on 32 KV heads 66 and
+// 58.4, with one place 63.4).  A
 // sequence cut at a range's end leaves (m, l, o) per piece, and a second small
 // kernel (cb_fp8_join.cu) joins the pieces by log-sum-exp: no counters, no grid
 // barrier, nothing to initialise, and the same bits every time.
@@ -48,7 +52,7 @@
 // in tensor memory, joined at the segment's end.  A tile's chain (scores, maxima,
 // weights, one barrier of the group for a move of O) is mostly waiting, so two
 // tiles at a time take little more than one: with a segment per group in turn, 48
-// decodes took 104 us instead of 90.  8 K loads, 9 V loads (TMA through the block
+// decodes took 104 us instead of 90 (both without the empty places).  8 K loads, 9 V loads (TMA through the block
 // table; the exponents by per-thread copies: a TMA copy of 16 bytes takes the unit
 // as long as one of 2 KB), 10 issues S, 11 issues O, 12-15 make the next segments'
 // query terms ready.  Thread = tile row, then output dimension.  Every wait is
@@ -56,9 +60,9 @@
 //
 // Bound by HBM where a KV head has one query head: 64 decodes of 32 heads (512 to
 // 4096 keys, 1.30 GB) in 199 us, 6.5 TB/s, 0.96 of a copy's rate.  With four, a
-// tile's softmax is four times the work: 48 decodes (256 to 8192 keys, 461 MB) in 89
-// us, 5.2 TB/s, 0.77; a segment's end adds 4.5 us to its CTA.  Two sequences of 4900
-// keys: 25 us, of which 12 in this kernel, 4 tiles per CTA.
+// tile's softmax is four times the work: 48 decodes (256 to 8192 keys, 461 MB) in 86
+// us, 5.4 TB/s, 0.79; a segment's end adds 4.5 us to its CTA.  Two sequences of 4900
+// keys: 23 us, of which 12 in this kernel, 4 tiles per CTA.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -85,6 +89,7 @@ struct Cfg {
   static constexpr int PB = 4;                               // w buffers
   static constexpr int ES = 8;                               // exponent stages
   static constexpr int kTile = 128 * A;                      // bytes
+  static constexpr int kLead = G >= 4 ? 6 : 3;               // what a segment's end costs, in tiles (see Work above)
   static constexpr int kCols = SB * NS + 2 * NO;
   static constexpr int kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= 512, "tensor memory");
@@ -112,7 +117,7 @@ struct alignas(1024) Smem {
   int u0, u1, total, eff;            // this CTA's range of tiles; all tiles; CTAs with a range
 };
 
-// Plan arrays after Smem: pre[n + 1] tiles before request r (one head group), kv[n] keys, tok[n] query row.
+// Plan arrays after Smem: pre[n + 1] places before request r (one head group), kv[n] keys, tok[n] query row.
 struct Plan {
   const int *pre, *kv, *tok;
 };
@@ -172,9 +177,9 @@ struct Seg {
 };
 struct SegIter {
   Plan plan;
-  int u, u1, nhg, r, window;
-  __device__ SegIter(const Plan& pl, int u0, int u1_, int nhg_, int n, int window_)
-      : plan(pl), u(u0), u1(u1_), nhg(nhg_), window(window_) {
+  int u, u1, nhg, r, window, lead;
+  __device__ SegIter(const Plan& pl, int u0, int u1_, int nhg_, int n, int window_, int lead_)
+      : plan(pl), u(u0), u1(u1_), nhg(nhg_), window(window_), lead(lead_) {
     int lo = 0, hi = n - 1;            // the last request whose tiles start at or before u0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -185,20 +190,31 @@ struct SegIter {
     }
     r = lo;
   }
-  __device__ bool next(Seg& s) {
-    if (u >= u1) return false;
+  // The sequence of place u: its first place and its size.
+  __device__ void locate(int& start, int& size, int& hg) {
     while (plan.pre[r + 1] * nhg <= u) ++r;
-    s.r = r;
-    s.tiles = plan.pre[r + 1] - plan.pre[r];
+    size = plan.pre[r + 1] - plan.pre[r];
     const int off = u - plan.pre[r] * nhg;
-    s.hg = off / s.tiles;
-    s.t0 = off - s.hg * s.tiles;
-    s.nt = min(s.tiles - s.t0, u1 - u);
-    s.kv = plan.kv[r];
-    s.tok = plan.tok[r];
-    s.fb = window_first_block(s.kv, window);
-    u += s.nt;
-    return true;
+    hg = off / size;
+    start = u - (off - hg * size);
+  }
+  __device__ bool next(Seg& s) {
+    while (u < u1) {
+      int start, size;
+      locate(start, size, s.hg);
+      const int first = start + lead, end = min(start + size, u1), from = max(u, first);
+      u = end;
+      if (end <= from) continue;       // nothing but the lead
+      s.r = r;
+      s.tiles = size - lead;
+      s.t0 = from - first;
+      s.nt = end - from;
+      s.kv = plan.kv[r];
+      s.tok = plan.tok[r];
+      s.fb = window_first_block(s.kv, window);
+      return true;
+    }
+    return false;
   }
 };
 
@@ -232,7 +248,8 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
   const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
   int own = 0;
   for (int r = lo; r < hi; ++r) {
-    const int t = request_tiles(P, r, bpt, kv + r, tok + r);
+    int t = request_tiles(P, r, bpt, kv + r, tok + r);
+    if (t > 0) t += Cfg<A, G>::kLead;
     pre[r] = t;
     own += t;
   }
@@ -269,11 +286,11 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
   if (tid == 0) {                     // the sequence that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
     if (S.u1 > S.u0) {
-      SegIter last({pre, kv, tok}, S.u1 - 1, S.u1, nhg, n, P.window);
-      Seg s;
-      last.next(s);
-      const int start = pre[s.r] * nhg + s.hg * s.tiles, end = start + s.tiles;
-      if (start >= S.u0 && end > S.u1) rec = {s.r, s.hg, cta_of(end - 1, S.total, S.eff) - (int)blockIdx.x + 1, 0};
+      SegIter last({pre, kv, tok}, S.u1 - 1, S.u1, nhg, n, P.window, Cfg<A, G>::kLead);
+      int start, size, hg;
+      last.locate(start, size, hg);
+      const int first = start + Cfg<A, G>::kLead, end = start + size;
+      if (first >= S.u0 && first < S.u1 && end > S.u1) rec = {last.r, hg, cta_of(end - 1, S.total, S.eff) - (int)blockIdx.x + 1, 0};
     }
     W.rec[blockIdx.x] = rec;
   }
@@ -304,7 +321,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
   const int rows_total = P.cache.num_blocks * Hkv * kBlockSize, box = hg_heads * kBlockSize;
   uint64_t* full = IS_K ? S.k_full : S.v_full;
   uint64_t* empty = IS_K ? S.k_empty : S.v_empty;
-  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window, X::kLead);
   Seg s, nx;
   uint32_t n = 0;
   bool ok = true;
@@ -361,7 +378,7 @@ __device__ void issue_s(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int n
   constexpr uint32_t kIdesc = idesc_f8(128, X::NS, 0, 0, 0, 0);
   constexpr int kLayout = A == 128 ? 2 : 4;
   const uint64_t kd = smem_desc(smem_u32(S.k[0]), 16, 8 * A, kLayout), qd = smem_desc(smem_u32(S.q[0]), 16, 8 * A, kLayout);
-  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window, X::kLead);
   Seg s;
   uint32_t n = 0;
   bool ok = true;
@@ -399,7 +416,7 @@ __device__ void issue_pv(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int 
   constexpr uint32_t kIdesc = idesc_f8(128, 2 * X::SS, 0, 1, 1, 0);   // V^T: e4m3, MN-major; w: e5m2, K-major
   constexpr int kLayout = A == 128 ? 2 : 4;
   const uint64_t vd = smem_desc(smem_u32(S.v[0]), 0, 8 * A, kLayout), pd = smem_desc(smem_u32(S.p[0]), 128, 256, 0);
-  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window, X::kLead);
   Seg s;
   uint32_t n = 0;
   bool ok = true;
@@ -490,7 +507,7 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int bu
 // The queries of the segments, two ahead of the softmax at most.
 template <int A, int G>
 __device__ void queries(const Fp8Step& P, Smem<A, G>& S, const Plan& plan, int hg_heads) {
-  SegIter it(plan, S.u0, S.u1, P.cache.n_kv_heads / hg_heads, P.n_reqs, P.window);
+  SegIter it(plan, S.u0, S.u1, P.cache.n_kv_heads / hg_heads, P.n_reqs, P.window, Cfg<A, G>::kLead);
   Seg s;
   for (int i = 0; it.next(s); ++i) {
     if (!wwait(P, S, &S.q_free[i & 1], ((i >> 1) & 1) ^ 1)) break;
@@ -564,7 +581,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
   const int bi = slot / hg_heads;
   const bool upper = lane & 16;
   const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window);
+  SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window, X::kLead);
   Seg s;
   uint32_t n0 = 0;                           // tiles before this segment
   const uint32_t o_tmem = S.tmem + X::SB * X::NS + grp * X::NO;

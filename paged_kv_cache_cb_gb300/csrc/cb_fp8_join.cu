@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     join_fp8_kernel(const Fp8Step P, const Fp8Partials singles, const Fp8Partials chunks, int ctas, int n_singles, int heads) {
   constexpr int D = A / 32;
   __shared__ int owner[kMaxDecodeGrid];
+  __shared__ Fp8Rec recs[kMaxDecodeGrid];
   __shared__ int n_owner;
   __shared__ float red[kWarps][A];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -30,7 +31,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const Fp8Partials& W = single ? singles : chunks;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (warp == 0) {
-    const int n = join_owners(W, ctas, owner);
+    const int n = join_owners(W, ctas, owner, recs);
     if (lane == 0) n_owner = n;
   }
   __syncthreads();
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kJoinThreads)
     const bool by_cta = tasks <= n_singles;
     for (int task = by_cta ? blockIdx.x : blockIdx.x * kWarps + warp; task < tasks; task += by_cta ? n_singles : n_singles * kWarps) {
       const int b = owner[task / heads], h = task % heads;
-      const Fp8Rec rec = W.rec[b];
+      const Fp8Rec rec = recs[task / heads];
       const int t = __ldg(P.cu_q_lens + rec.r);
       join_row<A>(W, kSingleRows, b, rec.n, h, by_cta ? warp : 0, by_cta ? kWarps : 1, o);
       if (by_cta) {
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int group = P.n_q_heads / P.cache.n_kv_heads, tok = kTileM / group;
   for (int task = blockIdx.x - n_singles; task < n_owner * (kChunkRows / 32); task += gridDim.x - n_singles) {
     const int b = owner[task / (kChunkRows / 32)];
-    const Fp8Rec rec = W.rec[b];
+    const Fp8Rec rec = recs[task / (kChunkRows / 32)];
     const int row = (task % (kChunkRows / 32)) * 32 + lane, n = rec.n;
     auto piece = [&](int i) { return (size_t)(i == 0 ? 2 * b + 1 : 2 * (b + i)); };
     auto ml = [&](int i) { return *reinterpret_cast<const float2*>(W.ml + (piece(i) * kChunkRows + row) * 2); };
