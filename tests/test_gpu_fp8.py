@@ -562,3 +562,40 @@ def test_scheduled_trace_with_shared_prefixes(hq, hk, a, prefix, seed):
         for got, x in zip(back, (K8, V8)):
             assert np.array_equal(got.double().cpu().numpy(), np.stack([x[content(r, p), p] for r, p in rows]))
     assert copies > 0
+
+
+# ------------------------------------------------------------------ the largest sizes
+def test_blocks_far_into_a_large_cache():
+    """Blocks past 4 GiB of each cache: the bits of the same step in a small one."""
+    lib = L()
+    s = Step([(1, 37), (1, 900), (20, 300), (300, 5)], 32, 8, 128, seed=77)
+    n, small, meta = 300_000, s.cache(), s.meta()
+    off = n - s.nb
+    big = [torch.empty((n,) + c.shape[1:], dtype=c.dtype, device="cuda") for c in small]
+    for b, c in zip(big, small):
+        b.view(torch.uint8)[off:] = c.view(torch.uint8)
+    far = meta[:3] + (torch.where(meta[3] >= 0, meta[3] + off, meta[3]),)
+    assert torch.equal(s.run(cache=small, meta=meta), s.run(cache=big, meta=far))
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(40, 8, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2))
+    slots = torch.randperm(s.nb * BS, generator=g)[:40].cuda()
+    pairs = torch.tensor([[1, 0], [3, 2]], dtype=torch.int32, device="cuda")
+    outs = []
+    for cache, d in ((small, 0), (big, off)):
+        lib.cb_kv_append_fp8(k, v, slots + d * BS, *cache)
+        lib.cb_copy_blocks_fp8(pairs + d, *cache)
+        out = [torch.zeros_like(k), torch.zeros_like(v)]
+        lib.cb_kv_gather_fp8(slots + d * BS, *cache, *out)
+        assert lib.cb_last_error() == 0
+        outs.append([c.view(torch.uint8)[d:] for c in cache] + [o.view(torch.int16) for o in out])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("hq,hk,a", [(8, 1, 128), (32, 2, 128), (4, 4, 64)])
+def test_the_most_requests(hq, hk, a):
+    """As many requests as a step may have, of one and of several tokens, some
+    with none."""
+    reqs = [((1, 1, 0, 1, 2, 1, 1)[i % 7], i % 23) for i in range(2048)]
+    s = Step(reqs, hq, hk, a, seed=8)
+    check(s.run(), *s.reference(), "2048 requests")
