@@ -242,6 +242,14 @@ __device__ __forceinline__ void join_row(const Fp8Partials& W, int rows, int b, 
   for (int d = 0; d < D; ++d) o[d] /= L;
 }
 
+// The warp's arrival that gives back a buffer of shared memory whose values it has
+// loaded.  v: of all of the lane's loaded values.  Which lane arrives depends on
+// them: an arrival that merely followed the loads was seen to let the next copy
+// overwrite the buffer before they had read it.
+__device__ __forceinline__ void arrive_after(uint64_t* bar, uint32_t v) {
+  if ((threadIdx.x & 31) == (__ballot_sync(0xffffffffu, v != 0u) & 1u)) mbar_arrive(bar);
+}
+
 // A kernel launch.  chained: the kernel may be placed while the kernel before it on
 // the stream, one of the same call, still runs.  Until its griddepcontrol.wait it
 // reads only what no kernel of the call writes (the requests' lengths) and writes

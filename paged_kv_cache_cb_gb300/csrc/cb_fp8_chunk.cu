@@ -39,9 +39,9 @@
 // thread issues the products, every wait of its warp between them is idle time of
 // the pipe (a second issuing warp was slower), and an item's start and end cost
 // about 8 us.  Single tokens (below): 256 requests of 32 heads on 1 KV head (1024
-// to 16384 keys, 539 MB) take 162 us, 3.3 TB/s, 0.49 of a copy's rate: a tile's
-// conversion (1500 cycles of a warp, which shares the memory's bandwidth with the
-// products' operands) is the longest part of its chain, HBM's share 1400.
+// to 16384 keys, 539 MB) take 156 us, 3.5 TB/s, 0.51 of a copy's rate: a tile's
+// conversion, whose shared-memory accesses compete with the products' operands, is
+// the longest part of its chain.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -337,9 +337,8 @@ struct Items {
     const Item* I = &S.item[i % kItems];
     return I->b > I->a ? I : nullptr;
   }
-  __device__ void done(SM& S) {        // the whole warp has read what it needs of it
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&S.item_empty[i % kItems]);
+  __device__ void done(SM& S, int v) { // the whole warp has read what it needs of it: v, from all of that
+    arrive_after(&S.item_empty[i % kItems], (uint32_t)v);
     ++i;
   }
 };
@@ -359,7 +358,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
     if (!item) break;
     const int r = item->r, g = item->g, a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi;
     const int key_lo = P.window > 0 ? max(0, item->ctx + item->tok_lo - P.window + 1) : 0;
-    items.done(S);
+    items.done(S, r ^ g ^ a ^ b ^ kv_hi ^ key_lo);
     const int nblk = (kv_hi + kBlockSize - 1) / kBlockSize, blk_lo = key_lo / kBlockSize;
     // lane 8 t + i: entry of block i of tile base + t; 4 tiles at a time, the next 4 on their way.  Blocks
     // that no row of the item sees are not read: they may have been released.
@@ -464,7 +463,7 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
     const int a = item->a, b = item->b, kv_hi = item->ctx + item->tok_hi, tok = item->q0, head = item->g * G + lane;
     const int key_lo = P.window > 0 ? max(0, item->ctx + item->tok_lo - P.window + 1) : 0;
     const uint32_t it = items.i;
-    items.done(S);
+    items.done(S, a ^ b ^ kv_hi ^ key_lo ^ tok ^ head);
     if constexpr (ONE) {
       // (every tile of the item before is converted: nothing that its S waits for waits for this warp)
       const float fq = make_query<A>(P, S, 0, 32 * warp + lane, tok, head, lane < G,
@@ -488,14 +487,10 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       if (lane == 0) mbar_arrive(&S.fk_full[n & 3]);
       const uint32_t f1 = seen && !nan ? factor1(vb) : 0u;
       const bool large = __any_sync(FULL, seen && !nan && vb > 134u);
-      ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
-      if (!ok) break;
       const uint32_t src = smem_u32(&S.vr[st][32 * warp * A + lane * 16]), dst = smem_u32(&S.v[st][sw][32 * warp + rsub][0]);
-#pragma unroll 2
-      for (int p = 0; p < N; ++p) {
+      auto put = [&](int p, const uint4& x) {
         const int row = p * RP + rsub;
         uint32_t o[8];
-        const uint4 x = lds128(src + p * 512);
         const uint32_t f = __shfl_sync(FULL, f1, row);
         widen8(x.x, x.y, f, o);
         widen8(x.z, x.w, f, o + 4);
@@ -507,12 +502,32 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
         const uint4 x0 = make_uint4(o[0], o[1], o[2], o[3]), x1 = make_uint4(o[4], o[5], o[6], o[7]);
         sts128(dst + p * RP * 128 + (((c + sw) ^ (row & 7)) << 4), sw ? x1 : x0);
         sts128(dst + p * RP * 128 + (((c + 1 - sw) ^ (row & 7)) << 4), sw ? x0 : x1);
+      };
+      if constexpr (ONE) {
+        // The conversion is the longest part of a tile's chain here and registers are free: the staged tile is
+        // read at once and its buffer given back before the stores (165 -> 156 us for 256 MQA decodes).
+        uint4 x[N];
+#pragma unroll
+        for (int p = 0; p < N; ++p) x[p] = lds128(src + p * 512);
+        uint32_t all = 0;
+#pragma unroll
+        for (int p = 0; p < N; ++p) all ^= x[p].x ^ x[p].y ^ x[p].z ^ x[p].w;
+        arrive_after(&S.vr_empty[st], all ^ kb ^ vb);
+        ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
+        if (!ok) break;
+#pragma unroll
+        for (int p = 0; p < N; ++p) put(p, x[p]);
+      } else {
+        ok = wwait(P, S, &S.v_empty[st], ph ^ 1);
+        if (!ok) break;
+#pragma unroll 2
+        for (int p = 0; p < N; ++p) put(p, lds128(src + p * 512));
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&S.v_full[st]);
-        mbar_arrive(&S.vr_empty[st]);
+        if constexpr (!ONE) mbar_arrive(&S.vr_empty[st]);
       }
     }
   }
@@ -534,7 +549,7 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S) {
     const Item* item = items.next(P, S);
     if (!item) break;
     const int len = item->b - item->a, sides = item->sides;
-    items.done(S);
+    items.done(S, len ^ sides);
     for (int j = 0; j <= len && ok; ++j) {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
@@ -691,7 +706,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
         return;
       }
       n += item->b - item->a;
-      items.done(S);
+      items.done(S, n);
     }
   };
   float fq = 0.f;
@@ -702,7 +717,7 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
     const int lo = P.window > 0 ? max(0, pos - P.window + 1) : 0;
     const bool began = a0 > item->first, cut = began || b0 < item->end;
     uint16_t* dst = P.out + ((size_t)(item->q0 + ti) * P.n_q_heads + (size_t)item->g * G + row % G) * A;
-    items.done(S);
+    items.done(S, tok_hi ^ a0 ^ b0 ^ pos ^ lo ^ ti ^ (int)cut ^ (int)(uintptr_t)dst);
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int j = a0; j < b0; ++j, ++n, ++ns) {
@@ -777,7 +792,7 @@ __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
     const Item* item = items.next(P, S);
     if (!item) break;
     const int len = item->b - item->a;
-    items.done(S);
+    items.done(S, len);
     for (int t0 = 0; t0 < len + 2 && ok; t0 += 2) {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
@@ -831,11 +846,12 @@ __device__ void issue_one(const Fp8Step& P, Smem<A>& S) {
   mbar_wait(&S.drain, 0, 20000000ull);
 }
 
-// Bounded meeting of the eight softmax warps (phase: counted by the caller).
+// Bounded meeting of the eight softmax warps (phase: counted by the caller; v: of
+// the values loaded from what is overwritten after it).
 template <class SM>
-__device__ __forceinline__ bool meet(const Fp8Step& P, SM& S, uint32_t& phase) {
+__device__ __forceinline__ bool meet(const Fp8Step& P, SM& S, uint32_t& phase, float v = 0.f) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&S.x_bar);
+  arrive_after(&S.x_bar, __float_as_uint(v));
   return wwait(P, S, &S.x_bar, phase++ & 1);
 }
 
@@ -858,7 +874,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     const int tok = item->q0;
     bool ok = true;
     float fq = 0.f;
-    items.done(S);
+    items.done(S, a0 ^ b0 ^ pos ^ g ^ tok ^ (int)cut);
     float m = kNegInf, l = 0.f;
     for (int j = a0 + side; j < b0; j += 2, ++ns) {
       const uint32_t nj = n + (j - a0);
@@ -966,6 +982,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     }
     f[0] /= ls;
     f[1] /= ls;
+    float read = f[0] + f[1];
     const size_t pr = ((size_t)2 * blockIdx.x + (began ? 0 : 1)) * kSingleRows;
     if (cut && copy == 0 && lane < G) *reinterpret_cast<float2*>(W.ml + (pr + lane) * 2) = make_float2(mm, ls);
     const uint32_t o_a = S.tmem + lanes + 256, xh = xs + side * (128 * 128);
@@ -978,7 +995,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
       tmem_wait_ld();
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = both ? o[k] * f[0] + ob[k] * f[1] : o[k] * f[0];
-      ok = meet(P, S, phase);                                  // what was there has been read
+      ok = meet(P, S, phase, read);                            // what was there has been read
       // row `lane` of this copy: 32 values, their 16-byte chunks in an order that spreads the banks
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -999,6 +1016,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
           y[2] += __uint_as_float(x.z);
           y[3] += __uint_as_float(x.w);
         }
+        read = h == 0 ? y[0] + y[1] + y[2] + y[3] : read + (y[0] + y[1] + y[2] + y[3]);
         if (ok && r < G) {
           if (cut)
             *reinterpret_cast<float4*>(W.acc + (pr + r) * A + d0 + 4 * k) = make_float4(y[0], y[1], y[2], y[3]);
@@ -1010,7 +1028,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     }
     if (!ok) break;
     tc_fence_before();
-    if (!meet(P, S, phase)) break;                             // the exchange is free for the next item
+    if (!meet(P, S, phase, read)) break;                       // the exchange is free for the next item
     if (lane == 0) {
       mbar_arrive(&S.o_free[0]);
       if (both) mbar_arrive(&S.o_free[1]);

@@ -594,8 +594,10 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       m[g] = M[g] = kNegInf;
       l[g] = 0.f;
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.q_free[i & 1]);
+    uint32_t read = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) read ^= __float_as_uint(f[g]);
+    arrive_after(&S.q_free[i & 1], read);
     const int first_key = P.window > 0 ? max(0, s.kv - P.window) : 0;
     const int j0 = (n0 ^ grp) & 1;           // this group's first tile of the segment
     for (int j = j0; j < s.nt; j += 2) {
@@ -616,7 +618,6 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&S.s_empty[n % X::NB]);
-        mbar_arrive(&S.e_empty[es]);
       }
       const float fk = exp_scale(kb), ev = vb == kExpNan ? __uint_as_float(0x7FC00000u) : (float)((int)vb - 127);
       float x[G];
@@ -725,7 +726,10 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.p_full[pb]);
+      if (lane == 0) {
+        mbar_arrive(&S.p_full[pb]);
+        mbar_arrive(&S.e_empty[es]);         // its exponents are in the weights
+      }
     }
     // the segment's sums; then the heads' and the slots' factors, over both groups.  A group that gave up comes
     // here too: the other one waits for it.
