@@ -39,7 +39,7 @@
 // thread issues the products, every wait of its warp between them is idle time of
 // the pipe (a second issuing warp was slower), and an item's start and end cost
 // about 8 us.  Single tokens (below): 256 requests of 32 heads on 1 KV head (1024
-// to 16384 keys, 539 MB) take 156 us, 3.5 TB/s, 0.51 of a copy's rate: a tile's
+// to 16384 keys, 539 MB) take 157 us, 3.4 TB/s, 0.51 of a copy's rate: a tile's
 // conversion, whose shared-memory accesses compete with the products' operands, is
 // the longest part of its chain.
 #include <algorithm>
