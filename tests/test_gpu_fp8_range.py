@@ -1,0 +1,50 @@
+"""Attention over the 8-bit cache at the ends of its number range: keys and
+queries of the largest and smallest sizes, and query rows of a wide spread."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_util import BS, Step, check
+from gpu_util import L
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(4, 4, 64), (32, 32, 128), (16, 8, 128), (32, 8, 128), (64, 8, 128), (32, 2, 128), (32, 1, 128)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    L().lib()
+
+
+def _every_row(s):
+    """(block, slice, offset) of every stored row of every request."""
+    for r, (q, c) in enumerate(s.reqs):
+        for p in range(q + c):
+            yield s.tables[r, p // BS], slice(None), p % BS
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("kexp", [(245, 248), (232, 240), (90, 93), (5, 8), (1, 3)])
+@pytest.mark.parametrize("q_len", [1, 3, 40])
+def test_keys_of_any_size_with_moderate_scores(hq, hk, a, kexp, q_len):
+    """Keys around 2^120 and around 2^-120, queries as much the other way: the
+    scores are those of normal rows (the bound's rounding errors are too: every
+    factor is a power of two, the queries' subnormals are in the oracle's inputs)."""
+    mid = (kexp[0] + kexp[1] - 1) / 2
+    s = Step([(q_len, 300), (q_len, 15)], hq, hk, a, seed=61, kexp=kexp, qscale=2.0 ** (121 - mid))
+    check(s.run(), *s.reference(), "keys of any size")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_keys_of_all_sizes_side_by_side(hq, hk, a, q_len):
+    """Most keys so small that they score 0, some normal ones among them, one tile
+    of small ones only."""
+    s = Step([(q_len, 500)], hq, hk, a, seed=62)
+    rng = np.random.default_rng(3)
+    for i, at in enumerate(_every_row(s)):
+        s.k_exps[at] = rng.choice([1, 2, 40, 80]) if 128 <= i < 256 or i % 3 else 121
+    check(s.run(), *s.reference(), "keys of all sizes")
