@@ -449,9 +449,10 @@ __device__ uint32_t make_query(const Fp8Step& P, Smem<A>& S, int side, int row, 
   return eb;
 }
 // The factor scale log2(e) 2^eq 2^E of a query row's exponent byte rb and that of the
-// keys: NaN for a row of NaNs, else finite (the power of two saturates).
+// keys: NaN for a row of NaNs, else finite and not 0 (keys out of sight are -inf times it).
 __device__ __forceinline__ float score_factor(const Fp8Step& P, uint32_t rb, uint32_t ke) {
-  const float f = fminf(P.scale_log2 * __uint_as_float((uint32_t)min(max((int)(rb + ke) - 127, 1), 254) << 23), 3.4028235e38f);
+  const float x = P.scale_log2 * __uint_as_float((uint32_t)min(max((int)(rb + ke) - 127, 1), 254) << 23);
+  const float f = fminf(fmaxf(x, 1.17549435e-38f), 3.4028235e38f);
   return rb == kExpNan ? __uint_as_float(0x7FC00000u) : f;
 }
 

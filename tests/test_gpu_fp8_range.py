@@ -48,3 +48,13 @@ def test_keys_of_all_sizes_side_by_side(hq, hk, a, q_len):
     for i, at in enumerate(_every_row(s)):
         s.k_exps[at] = rng.choice([1, 2, 40, 80]) if 128 <= i < 256 or i % 3 else 121
     check(s.run(), *s.reference(), "keys of all sizes")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_query_of_zeros_under_a_small_scale(hq, hk, a, q_len):
+    """Every score is 0, whatever the scale; the keys out of sight stay out."""
+    s = Step([(q_len, 77)], hq, hk, a, seed=64)
+    s.q[:, ::2] = 0
+    s.scale = 1e-12
+    check(s.run(), *s.reference(), "small scale")
