@@ -159,6 +159,13 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
+// The largest finite number for an infinity, a NaN for a NaN: the factors' product may
+// pass fp32's range where the score they multiply is 0.
+__device__ __forceinline__ float finite(float f) {
+  float r;
+  asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(f));
+  return r;
+}
 // Bounded wait with the same outcome in all 32 lanes.
 template <class S>
 __device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
@@ -624,7 +631,7 @@ __device__ void softmax_group(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>
       bool grow = false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        x[g] = valid ? (upper ? s0[G + g] + s1[G + g] : s0[g] + s1[g]) * (f[g] * fk) : kNegInf;
+        x[g] = valid ? (upper ? s0[G + g] + s1[G + g] : s0[g] + s1[g]) * finite(f[g] * fk) : kNegInf;
         grow |= x[g] > m[g] + kLazyP || x[g] + ev > M[g] + kLazyW;
       }
       bool need = false;

@@ -58,3 +58,17 @@ def test_query_of_zeros_under_a_small_scale(hq, hk, a, q_len):
     s.q[:, ::2] = 0
     s.scale = 1e-12
     check(s.run(), *s.reference(), "small scale")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_large_rows_at_right_angles(hq, hk, a, q_len):
+    """Queries and keys of 2^100 in different channels: every score is 0."""
+    s = Step([(q_len, 200)], hq, hk, a, seed=63)
+    s.q.zero_()
+    s.q[..., 0] = 2.0 ** 100
+    for at in _every_row(s):
+        s.k_codes[at] = 0
+        s.k_codes[at][:, 1] = 0x7E
+        s.k_exps[at] = 220
+    check(s.run(), *s.reference(), "right angles")
