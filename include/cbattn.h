@@ -242,6 +242,17 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  * and n_kv_heads; for several new tokens each, max_kv_len / 128 for every
  * 256 n_kv_heads / n_q_heads of them) is refused with CB_EINVAL.
  *
+ * Precision.  Scores, softmax statistics and sums are fp32.  What has fewer bits:
+ *  - a query row (token, query head) enters as two e4m3 terms times a power of two:
+ *    each value exactly from 2^-9 of the row's largest magnitude on, the smaller
+ *    ones within 2^-17 of that magnitude.  Next to a value more than 2^17 times
+ *    theirs the others count as zeros, also where the keys hold 0 in its channel;
+ *  - a weight is within 2^-8 of itself (bf16); with one new token and at most 8
+ *    query heads per KV head within 2^-9 + 2^-11, and 2^-29 of the largest.
+ * With several new tokens, or 16 or 32 query heads per KV head, values of v are
+ * summed under weights of up to 2^8 before the division: a token that sees n keys
+ * has a finite result for |v| < 2^119 / n.
+ *
  * cb_kv_append_fp8: cb_kv_append into this cache.  The slots of one call that
  * are not negative are distinct. */
 int cb_kv_append_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, int n_tokens, void* k_cache,

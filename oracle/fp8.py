@@ -18,6 +18,14 @@ def row_exponent(largest):
     raise ValueError("not a bf16 magnitude")
 
 
+def _nearest(y):
+    """Codes of the e4m3 values nearest to y >= 0, ties to the even code."""
+    hi = np.clip(np.searchsorted(VALUES, y), 0, 126)
+    lo = np.maximum(hi - 1, 0)
+    up, down = VALUES[hi] - y, y - VALUES[lo]
+    return np.where(up < down, hi, np.where(down < up, lo, np.where(hi % 2 == 0, hi, lo)))
+
+
 def quantise(x):
     """x float64 [..., A] -> (codes uint8 [..., A], exponent bytes uint8 [...])."""
     x = np.asarray(x, np.float64)
@@ -29,11 +37,7 @@ def quantise(x):
             exps[i] = 255
             continue
         e = row_exponent(np.abs(row).max())
-        y = np.abs(row) * 2.0 ** -e
-        hi = np.clip(np.searchsorted(VALUES, y), 0, 126)
-        lo = np.maximum(hi - 1, 0)
-        up, down = VALUES[hi] - y, y - VALUES[lo]
-        code = np.where(up < down, hi, np.where(down < up, lo, np.where(hi % 2 == 0, hi, lo)))
+        code = _nearest(np.abs(row) * 2.0 ** -e)
         codes[i] = code | np.where(np.signbit(row), 128, 0)
         exps[i] = e + 127
     return codes.reshape(x.shape), exps.reshape(x.shape[:-1])
@@ -47,3 +51,16 @@ def values(codes, exps):
     v = np.where(c & 128, -1.0, 1.0) * VALUES[c & 127]
     e = np.asarray(exps).astype(np.int64)
     return np.where((e == 255)[..., None], np.nan, v * np.exp2((e - 127).astype(np.float64))[..., None])
+
+
+def as_queried(q):
+    """What attention takes finite query rows [..., A] (bf16 values) as: two e4m3
+    terms, each nearest, of the row times the power of two that brings its largest
+    magnitude into [128, 256) (at most 2^126)."""
+    q = np.asarray(q, np.float64)
+    largest = np.abs(q).max(-1, keepdims=True)
+    shift = np.minimum(8 - np.frexp(largest)[1], 126)
+    y = np.where(largest > 0, q * np.exp2(shift.astype(np.float64)), 0.0)
+    hi = np.sign(y) * VALUES[_nearest(np.abs(y))]
+    rest = y - hi
+    return (hi + np.sign(rest) * VALUES[_nearest(np.abs(rest))]) * np.exp2(-shift.astype(np.float64))

@@ -7,7 +7,7 @@
 // with m a running maximum that moves only when a score passes it by 8.
 //   S = q k^T takes e4m3 K from the cache as it is; q 2^-eq is two e4m3 terms
 //   whose products add up (4 significant bits each: bf16's 8; values down to
-//   2^-15 of the row's largest exactly, smaller ones within 2^-18 of it).
+//   2^-9 of the row's largest exactly, smaller ones within 2^-17 of it).
 //   S is up to 2^24 and ek up to 120, so S 2^ek alone may pass fp32's range where
 //   x does not.  Of a tile's keys the largest exponent E is taken out: S is
 //   multiplied by 2^(ek - E) <= 1, the row's factor by 2^E.  What underflows is a

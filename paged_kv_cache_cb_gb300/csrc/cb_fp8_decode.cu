@@ -15,12 +15,13 @@
 // (tcgen05.mma kind::f8f6f4, fp32 accumulation).  Their other operands are split
 // into 8-bit terms whose products add up:
 //   q    two e4m3 terms (each 4 significant bits, so 8: exactly bf16's) of
-//        q 2^-eq, the row's largest value in [128, 256): values down to 2^-15 of
-//        the largest are exact, smaller ones are off by 2^-18 of it at most;
+//        q 2^-eq, the row's largest value in [128, 256): values down to 2^-9 of
+//        the largest are exact, smaller ones are off by 2^-17 of it at most (half
+//        of e4m3's least step, 2^-9, beside 128);
 //   w    three e5m2 terms of the weight 2^12 w, w in (0, 2^3]: the weight is
 //        rounded to 11 bits (half), the first two terms are its top 3 bits and
-//        the next 3, the third rounds the rest to 3 bits: within 2^-9 of w (bf16
-//        rounds within 2^-8) and 2^-29 of the largest.
+//        the next 3, the third rounds the rest to 3 bits: within 2^-9 + 2^-11 of w
+//        (bf16 rounds within 2^-8) and 2^-29 of the largest.
 // Using the 8-bit products instead of converting K and V to bf16 halves what
 // passes through shared memory, the second limit after HBM (at the copy rate each
 // SM takes 23 bytes of cache a cycle; converted tiles would add a read and twice

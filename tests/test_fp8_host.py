@@ -213,3 +213,18 @@ def test_binding_refuses_wrong_tensors(bad, calls, monkeypatch):
     for name in calls.split():
         with pytest.raises(ValueError):
             _calls(L, _fakes(**bad))[name]()
+
+
+# ------------------------------------------------------------------ what a query row enters as
+def test_query_rows_are_two_terms_within_the_documented_limit():
+    """Every value within 2^-17 of its row's largest; exact from 2^-9 of it on."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(400, 128, generator=g) * torch.exp(4 * torch.randn(400, 128, generator=g))
+    x = (x * 2.0 ** torch.randint(-60, 60, (400, 1), generator=g)).to(torch.bfloat16).double().numpy()
+    big = np.abs(x).max(-1, keepdims=True)
+    y = of8.as_queried(x)
+    assert (np.abs(y - x) <= 2.0 ** -17 * big).all()
+    kept = np.abs(x) >= 2.0 ** -9 * big
+    assert np.array_equal(y[kept], x[kept])
+    assert not np.array_equal(y, x)
+    assert np.array_equal(of8.as_queried(np.zeros((2, 64))), np.zeros((2, 64)))

@@ -6,6 +6,8 @@ import torch
 
 from fp8_util import BS, Step, check
 from gpu_util import L
+from oracle import attention as oa
+from oracle import fp8 as of8
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +74,38 @@ def test_large_rows_at_right_angles(hq, hk, a, q_len):
         s.k_codes[at][:, 1] = 0x7E
         s.k_exps[at] = 220
     check(s.run(), *s.reference(), "right angles")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("ratio", [2.0 ** 9, 2.0 ** 13, 2.0 ** 17])
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_query_rows_of_a_wide_spread(hq, hk, a, ratio, q_len):
+    """A query value many times the others, over keys that are 0 in its channel, so
+    that the others alone decide the scores.  They enter as the documented two
+    terms, and the weights follow from those within the usual bound."""
+    s = Step([(q_len, 150), (q_len, 31)], hq, hk, a, seed=65)
+    s.q[..., 5] = ratio
+    for at in _every_row(s):
+        s.k_codes[at][:, 5] = 0
+    q = of8.as_queried(s.q.double().numpy())
+    assert (np.abs(q - s.q.double().numpy()) <= 2.0 ** -17 * ratio).all()
+    ks, vs = zip(*[s.rows(r) for r in range(len(s.reqs))])
+    f = lambda v: oa.attention_step(q, s.q_lens, s.ctx, ks, v, s.scale, hq, hk)  # noqa: E731
+    check(s.run(), f(vs), f([np.abs(v) for v in vs]), "wide spread")
+
+
+@pytest.mark.parametrize("hq,hk,a", [x for x in SHAPES if x[0] // x[1] <= 8])
+def test_single_tokens_weights_have_more_bits_than_bf16(hq, hk, a):
+    """Two to nine keys whose values cancel in pairs, so that neither averaging nor
+    the output's rounding hides the weights' error: at most 2^-11 (a half's
+    rounding) and 2^-9 (its lowest five bits rounded to three) of each, and 2^-11
+    of its exponent (a score's terms sum to about 20 in magnitude: 20 log2 e 128
+    2^-24 < 2^-12, and as much for 2^x and the sums)."""
+    s = Step([(1, 1 + 2 * (i % 5)) for i in range(60)], hq, hk, a, seed=66)
+    for r, (q, c) in enumerate(s.reqs):
+        for p in range(1, q + c, 2):
+            at, one = ((s.tables[r, i // BS], slice(None), i % BS) for i in (p, p - 1))
+            s.v_codes[at], s.v_exps[at] = s.v_codes[one] ^ 128, s.v_exps[one]
+    ref, mag = s.reference()
+    err = np.abs(s.run().double().cpu().numpy() - ref)
+    assert (err <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -9 + 2 * 2.0 ** -11) * mag).all()
