@@ -148,9 +148,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // 16-byte asynchronous copy by this thread, outside the bulk-copy unit (which takes
 // about as long for 16 bytes as for 2 KB), and the arrival on `bar` once this
 // thread's copies have landed (counted among the barrier's expected arrivals).
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-               "l"(static_cast<uint64_t>(__cvta_generic_to_global(src)))
+// !have: zeros; src is not read then.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool have) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+               "l"(static_cast<uint64_t>(__cvta_generic_to_global(src))), "r"(have ? 16 : 0)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {

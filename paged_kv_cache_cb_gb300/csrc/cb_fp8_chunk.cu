@@ -399,8 +399,9 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
       if (lane == 0) mbar_arrive_expect_tx(&S.vr_full[st], blocks * kBlockSize * A);
       __syncwarp();
       if (have) bulk_load(&S.vr[st][lane * kBlockSize * A], P.cache.v + (size_t)row * A, kBlockSize * A, &S.vr_full[st]);
-      // the exponents: lanes 0 .. 7 K's, 8 .. 15 V's
-      if (lane < 16 && e >= 0) cp_async16(&S.ex[st][lane >> 3][(lane & 7) * kBlockSize], (lane < 8 ? P.cache.k_exps : P.cache.v_exps) + row);
+      // the exponents: lanes 0 .. 7 K's, 8 .. 15 V's; zeros, which no stored row has, where there is no block
+      if (lane < 16)
+        cp_async16(&S.ex[st][lane >> 3][(lane & 7) * kBlockSize], (lane < 8 ? P.cache.k_exps : P.cache.v_exps) + (e >= 0 ? row : 0), e >= 0);
       cp_async_arrive(&S.vr_full[st]);
     }
   }
@@ -489,7 +490,8 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       ok = wwait(P, S, &S.vr_full[st], ph);
       if (!ok) break;
       // this lane's key: its factors.  Values that no row of the item sees, and rows of NaNs, become zeros
-      // (0 * NaN must not reach O); the latter are told to the softmax, for the rows that see them.
+      // (0 * NaN must not reach O); the latter are told to the softmax, for the rows that see them.  So do those
+      // of a bad block id (exponent byte 0), whose rows were not copied.
       const uint32_t kb = lds8(smem_u32(&S.ex[st][0][key_l])), vb = lds8(smem_u32(&S.ex[st][1][key_l]));
       const int key = j * kTileN + key_l;
       const bool seen = key >= key_lo && key < kv_hi, nan = vb == kExpNan;
@@ -514,7 +516,7 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.fk_full[n & 3]);
-      const uint32_t f1 = seen && !nan ? factor1(vb) : 0u;
+      const uint32_t f1 = seen && !nan && vb != 0u ? factor1(vb) : 0u;
       const bool large = __any_sync(FULL, seen && !nan && vb > 134u);
       const uint32_t src = smem_u32(&S.vr[st][32 * warp * A + lane * 16]), dst = smem_u32(&S.v[st][sw][32 * warp + rsub][0]);
       auto put = [&](int p, const uint4& x) {

@@ -360,12 +360,13 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
           ++n;
           break;
         }
-        // exponents, 16 pieces of 16 bytes: lanes 0 .. 7 K's, 8 .. 15 V's, in the tile's order of rows
+        // exponents, 16 pieces of 16 bytes: lanes 0 .. 7 K's, 8 .. 15 V's, in the tile's order of rows (zeros
+        // where there is no block: what the stage held before must not reach the scores)
         const int piece = lane & 7, pe = __shfl_sync(FULL, e, piece / hg_heads);
-        if (lane < 16 && pe >= 0)
+        if (lane < 16)
           cp_async16(&S.ex[es][lane >> 3][piece * kBlockSize],
                      (lane < 8 ? P.cache.k_exps : P.cache.v_exps) +
-                         ((size_t)pe * Hkv + s.hg * hg_heads + piece % hg_heads) * kBlockSize);
+                         ((size_t)max(pe, 0) * Hkv + s.hg * hg_heads + piece % hg_heads) * kBlockSize, pe >= 0);
         cp_async_arrive(&S.e_full[es]);
       }
     }
