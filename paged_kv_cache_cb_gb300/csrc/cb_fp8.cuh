@@ -256,11 +256,32 @@ __device__ __forceinline__ void arrive_after(uint64_t* bar, uint32_t v) {
   if ((threadIdx.x & 31) == (__ballot_sync(0xffffffffu, v != 0u) & 1u)) mbar_arrive(bar);
 }
 
+// ---------------------------------------------------------------- the kernels of a call
+// Chunks run next to the single tokens' kernel, so they cannot wait for its end, and
+// the rows they read were appended by the kernel before it.  That kernel, once its own
+// griddepcontrol.wait has made those rows visible to it, releases the call's ticket;
+// a chunk CTA that acquires the ticket has them too.  One that does not find it there
+// waits for the end of the kernel before, which has them as well: nothing spins, and
+// nothing rests on when the kernels start.  The joining kernel clears the word, so that
+// a recorded call finds its own ticket only after its own release.  One thread each,
+// before the CTA's barrier in front of its first loads; the loading warps then fence,
+// because the rows were stored through another proxy than they load them by.
+__device__ __forceinline__ void signal_ready(const Fp8Step& P) {
+  if (P.ready) asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(P.ready), "l"(P.ticket) : "memory");
+}
+__device__ __forceinline__ void await_ready(const Fp8Step& P) {
+  unsigned long long t;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(t) : "l"(P.ready) : "memory");
+  if (t != P.ticket) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // A kernel launch.  chained: the kernel may be placed while the kernel before it on
-// the stream, one of the same call, still runs.  Until its griddepcontrol.wait it
-// reads only what no kernel of the call writes (the requests' lengths) and writes
-// nothing to global memory but error flags.  The first kernel of a call is not
-// chained: what stands before it on the stream may write those lengths.
+// the stream, one of the same call, still runs.  Until its griddepcontrol.wait (the
+// chunks': await_ready) it reads only what no kernel of the call writes, the requests'
+// lengths, and writes nothing to global memory but error flags.  The chunks' kernel
+// then writes its rows of out and its part of the workspace, which the single tokens'
+// kernel does not touch.  The first kernel of a call is not chained: what stands before
+// it on the stream may write those lengths.
 template <class... T, class... U>
 cudaError_t launch_after(bool chained, void (*kernel)(T...), int grid, int threads, size_t smem, cudaStream_t stream, const U&... args) {
   cudaLaunchConfig_t cfg{};

@@ -1,6 +1,7 @@
 // Entry points of the 8-bit KV cache (include/cbattn.h): argument checks and
 // dispatch.  Host code only.
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/cbattn.h"
 #include "cb_internal.h"
@@ -33,8 +34,17 @@ struct NewRows {
   const int64_t* slots;
 };
 
-// The single tokens' part of a step's workspace; the chunks' follows.
-size_t single_bytes(int head_dim) { return (fp8_partials_bytes(kSingleRows, head_dim) + 255) / 256 * 256; }
+// A step's workspace: the single tokens' part, the chunks', the ready word.
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+size_t single_bytes(int head_dim) { return round_up(fp8_partials_bytes(kSingleRows, head_dim)); }
+size_t ready_at(int head_dim) { return single_bytes(head_dim) + round_up(fp8_partials_bytes(kChunkRows, head_dim)); }
+
+// A number that no other call of the process has (a recorded call keeps its own; its
+// last kernel clears the word).
+unsigned long long next_ticket() {
+  static std::atomic<unsigned long long> n{0x6b1d3f5a00000001ull};
+  return n.fetch_add(1, std::memory_order_relaxed);
+}
 
 int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,
              const int32_t* block_tables, int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len,
@@ -84,6 +94,10 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   s.n_q_heads = n_q_heads;
   s.window = window;
   s.scale_log2 = scale * 1.4426950408889634f;
+  if (max_q_len > 1) {
+    s.ready = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + ready_at(head_dim));
+    s.ticket = next_ticket();
+  }
   if (app && launch_append_fp8(app->k, app->v, app->slots, n_tokens, s.cache, s.err, st) != cudaSuccess)
     return CB_ECUDA;
   int launches = app ? 1 : 0;
@@ -171,7 +185,7 @@ size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q
   if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 1 ||
       !supported_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
-  return single_bytes(head_dim) + (max_q_len > 1 ? fp8_partials_bytes(kChunkRows, head_dim) : 0);
+  return max_q_len > 1 ? ready_at(head_dim) + 16 : single_bytes(head_dim);
 }
 
 int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_t* ctx_lens,

@@ -224,6 +224,8 @@ __device__ __forceinline__ int cta_of(int u, int total, int eff) {
 template <int A, int TOK, bool ONE>
 __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int* tpre, int* ipre) {
   const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, Hkv = P.cache.n_kv_heads;
+  if constexpr (!ONE)
+    if (tid == kThreads - 1) await_ready(P);           // in front of the barriers below, and those of the loads
   if (tid == 0) S.longest = 0;
   for (int r = tid; r < n; r += kThreads) {
     const int3 q = request<ONE>(P, r, blockIdx.x == 0);
@@ -299,7 +301,10 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
     S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
   }
-  if constexpr (ONE) asm volatile("griddepcontrol.wait;" ::: "memory");   // so far only the requests' lengths were read (launch_after)
+  if constexpr (ONE) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // so far only the requests' lengths were read (launch_after)
+    if (tid == 0 && blockIdx.x == 0) signal_ready(P);
+  }
   __syncthreads();
   if (tid == 0) {                      // the item that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
@@ -357,6 +362,7 @@ template <int A>
 __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S, bool load_v) {
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31, Hkv = P.cache.n_kv_heads, rows_total = P.cache.num_blocks * Hkv * kBlockSize;
+  fence_proxy_async_global();           // the rows were appended by ordinary stores
   Items<Smem<A>> items;
   uint32_t n = 0;
   bool ok = true;
@@ -1144,9 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(S.tmem, 512);
   }
-  // Chunks do not wait for the single tokens' kernel: its CTAs let this one start only after the appended rows
-  // stood in the cache, and the two write different rows and workspaces.  This grid ends after that one does, so
-  // that the joining kernel has both.
+  // This grid ends after the single tokens' does, so that the joining kernel has both.
   if constexpr (!ONE) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 

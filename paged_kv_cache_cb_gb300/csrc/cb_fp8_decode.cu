@@ -290,6 +290,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
     S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");   // so far only the requests' lengths were read (launch_after)
+  if (tid == 0 && blockIdx.x == 0) signal_ready(P);
   __syncthreads();
   if (tid == 0) {                     // the sequence that starts in this range and goes on after it
     Fp8Rec rec = {0, 0, 0, 0};
@@ -329,6 +330,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
   const int rows_total = P.cache.num_blocks * Hkv * kBlockSize, box = hg_heads * kBlockSize;
   uint64_t* full = IS_K ? S.k_full : S.v_full;
   uint64_t* empty = IS_K ? S.k_empty : S.v_empty;
+  fence_proxy_async_global();           // the rows were appended by ordinary stores
   SegIter it(plan, S.u0, S.u1, nhg, P.n_reqs, P.window, X::kLead);
   Seg s, nx;
   uint32_t n = 0;

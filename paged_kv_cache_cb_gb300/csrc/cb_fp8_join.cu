@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const bool single = (int)blockIdx.x < n_singles;
   const Fp8Partials& W = single ? singles : chunks;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (P.ready && blockIdx.x == 0 && threadIdx.x == 0) *P.ready = 0ull;   // the call is over (signal_ready)
   if (warp == 0) {
     const int n = join_owners(W, ctas, owner, recs);
     if (lane == 0) n_owner = n;

@@ -137,6 +137,8 @@ struct Fp8Step {
   int window;                   // 0: none
   float scale_log2;             // scale * log2(e)
   unsigned int* err;            // the launching stream's error word
+  unsigned long long* ready;    // the workspace's last word, and what stands there once the appended rows
+  unsigned long long ticket;    // may be read (signal_ready); null without chunks
 };
 cudaError_t launch_append_fp8(const void* k_new, const void* v_new, const int64_t* slots, int n_tokens, const Fp8Cache& c,
                               unsigned int* err, cudaStream_t stream);
