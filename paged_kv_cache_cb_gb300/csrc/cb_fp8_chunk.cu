@@ -88,7 +88,7 @@ struct alignas(1024) Smem {
   uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], q_free, x_bar, drain, item_full[kItems], item_empty[kItems];
   Item item[kItems];
-  int scan[16], iscan[16], tiles, u0, u1, items, longest, whole, eff;
+  int scan[16], iscan[16], tiles, u0, u1, items, longest, high, whole, eff;
   uint32_t tmem;
   volatile int abort;
 };
@@ -226,7 +226,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
   const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, Hkv = P.cache.n_kv_heads;
   if constexpr (!ONE)
     if (tid == kThreads - 1) await_ready(P);           // in front of the barriers below, and those of the loads
-  if (tid == 0) S.longest = 0;
+  if (tid == 0) S.longest = S.high = 0;
   for (int r = tid; r < n; r += kThreads) {
     const int3 q = request<ONE>(P, r, blockIdx.x == 0);
     ipre[r] = q.y;
@@ -250,6 +250,7 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
       tpre[r] = t * Hkv;
       ipre[r] = pairs * Hkv;
       atomicMax(&S.longest, mx);
+      atomicAdd(&S.high, (t * Hkv) >> 12);
     }
   }
   __syncthreads();
@@ -291,6 +292,13 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     i_run += i;
   }
   if (tid == 0) {
+    // Query lengths that increase count every token once, and the host has seen to it that their tiles fit 32 bits.
+    // Others may count a token in many requests.  `high` sums each request's tiles without their lowest 12 bits,
+    // which come to 2^23 at most: below 2^19 of it the sum of all is under 2^31 + 2^23, and shows by its sign.
+    if (S.high >= 1 << 19 || total < 0) {
+      set_error(P.err, CB_DEVERR_BADLEN);
+      total = items = 0;                               // no work
+    }
     tpre[n] = total;
     ipre[n] = items;
     const int grid = gridDim.x, b = blockIdx.x, eff = max(1, min(grid, total));

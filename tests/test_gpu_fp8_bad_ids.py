@@ -41,3 +41,23 @@ def test_rows_of_a_bad_block_count_as_zeros(hq, hk, a, q_len, ctx):
         n.run(cache=n.cache())
         out = s.run(cache=cache, meta=(q, cu, ctxs, torch.from_numpy(bad).cuda()), status=lib.CB_EDEVICE)
         assert torch.equal(out, want)
+
+
+def test_lengths_that_count_tokens_many_times():
+    """cu_q_lens that jumps back and forth: 33 requests of all 65,536 tokens at
+    2^20 keys each would be more key tiles than 32 bits count.  Nothing is read or
+    written; the error is reported, and the next call runs as ever."""
+    lib = L()
+    n, hq, ctx = 65536, 32, 1 << 20
+    tables = torch.zeros(66, (ctx + n) // 16, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n] * 33 + [0], dtype=torch.int32, device="cuda")
+    ctxs = torch.full((66,), ctx, dtype=torch.int32, device="cuda")
+    s = Step([(3, 20), (1, 64)], hq, 1, 128, seed=25)
+    cache = s.cache()
+    q = torch.zeros(n, hq, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 3.0)
+    ws = torch.empty(lib.cb_paged_attention_fp8_workspace_size(66, n, n, ctx + n, hq, 1, 128, 16), dtype=torch.uint8, device="cuda")
+    lib.cb_paged_attention_fp8(q, cu, ctxs, tables, *cache, out, 0.1, ws, n, ctx + n)
+    assert lib.cb_last_error() == lib.CB_EDEVICE
+    assert (out == 3.0).all()
+    check(s.run(cache=cache), *s.reference(), "the next call")
