@@ -239,7 +239,7 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  * The rows of a block id out of range count as zeros (the call is reported all
  * the same).  Shapes, sizes, errors, ownership and streams are those of the calls
  * without _fp8; num_blocks * n_kv_heads * block_size < 2^31 - block_size.  A step whose
- * key tiles could reach 2^31 (max_blocks_per_seq or max_kv_len / 16, times n_reqs
+ * key tiles could reach 2^31 (7 + max_blocks_per_seq or max_kv_len / 16, times n_reqs
  * and n_kv_heads; for several new tokens each, max_kv_len / 128 for every
  * 256 n_kv_heads / n_q_heads of them) is refused with CB_EINVAL.  Query lengths on
  * the device that decrease are reported; where the tokens they count several times

@@ -228,3 +228,12 @@ def test_query_rows_are_two_terms_within_the_documented_limit():
     assert np.array_equal(y[kept], x[kept])
     assert not np.array_equal(y, x)
     assert np.array_equal(of8.as_queried(np.zeros((2, 64))), np.zeros((2, 64)))
+
+
+def test_places_that_32_bits_cannot_count():
+    """Short requests of very many KV heads: each takes some empty places beside its tiles."""
+    L = _lib().lib()
+    call = lambda hk, nr: L.cb_paged_attention_fp8(D, D, D, D, 1, nr, nr, 1, 16, D, D, D, D, 1, D, 0.1, hk, hk, 128, 16, 0, D, 16,  # noqa: E731
+                                                   None)
+    assert call((1 << 18) + 1, 2048) == -1
+    assert call((1 << 16) + 1, 2048) == -3             # too small a workspace: the sizes were taken
