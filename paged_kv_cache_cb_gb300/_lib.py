@@ -351,10 +351,9 @@ def cb_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_exps, v_exp
     ps = _on(dev, slot_mapping, c.i64, "slot_mapping", 1)
     cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
     shape = k_new.shape
-    n = shape[0]
-    if shape != (n, hk, a) or v_new.shape != shape or slot_mapping.shape != (n,):
+    if len(shape) != 3 or shape[1:] != (hk, a) or v_new.shape != shape or slot_mapping.shape != shape[:1]:
         raise ValueError("shape mismatch")
-    _check("cb_kv_append_fp8", lib().cb_kv_append_fp8(pk, pv, ps, n, *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
+    _check("cb_kv_append_fp8", lib().cb_kv_append_fp8(pk, pv, ps, shape[0], *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
 def cb_kv_gather_fp8(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_out, stream=None):
@@ -366,10 +365,10 @@ def cb_kv_gather_fp8(slot_mapping, k_cache, v_cache, k_exps, v_exps, k_out, v_ou
     cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
     pk = _on(dev, k_out, c.bf16, "k_out", 3)
     pv = _on(dev, v_out, c.bf16, "v_out", 3)
-    n = slot_mapping.shape[0]
     shape = k_out.shape
-    if shape != (n, hk, a) or v_out.shape != shape or slot_mapping.dim() != 1:
+    if slot_mapping.dim() != 1 or shape != (*slot_mapping.shape, hk, a) or v_out.shape != shape:
         raise ValueError("shape mismatch")
+    n = shape[0]
     _check("cb_kv_gather_fp8", lib().cb_kv_gather_fp8(ps, n, *cache, nb, pk, pv, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
@@ -380,10 +379,9 @@ def cb_copy_blocks_fp8(pairs, k_cache, v_cache, k_exps, v_exps, stream=None):
     dev = _current_device(c, pairs)
     pp = _on(dev, pairs, c.i32, "pairs", 2)
     cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
-    n = pairs.shape[0]
-    if pairs.shape != (n, 2):
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("shape mismatch")
-    _check("cb_copy_blocks_fp8", lib().cb_copy_blocks_fp8(pp, n, *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
+    _check("cb_copy_blocks_fp8", lib().cb_copy_blocks_fp8(pp, pairs.shape[0], *cache, nb, hk, a, bs, _raw_stream(c, dev, stream)))
 
 
 def cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim,
@@ -423,9 +421,10 @@ def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_c
     pw = _on(dev, workspace, c.u8, "workspace", 1)
     cache, (nb, hk, bs, a) = _fp8_cache(c, dev, k_cache, v_cache, k_exps, v_exps)
     shape, tables = q.shape, block_tables.shape
+    if len(shape) != 3 or out.shape != shape or ctx_lens.dim() != 1 or len(tables) != 2 or workspace.dim() != 1:
+        raise ValueError("shape mismatch")
     n_reqs = ctx_lens.shape[0]
-    if (len(shape) != 3 or out.shape != shape or ctx_lens.dim() != 1 or cu_q_lens.shape != (n_reqs + 1,)
-            or len(tables) != 2 or tables[0] != n_reqs or workspace.dim() != 1):
+    if cu_q_lens.shape != (n_reqs + 1,) or tables[0] != n_reqs:
         raise ValueError("shape mismatch")
     n_tok, hq, a2 = shape
     if a2 != a:

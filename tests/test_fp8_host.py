@@ -237,3 +237,20 @@ def test_places_that_32_bits_cannot_count():
                                                    None)
     assert call((1 << 18) + 1, 2048) == -1
     assert call((1 << 16) + 1, 2048) == -3             # too small a workspace: the sizes were taken
+
+
+@pytest.mark.parametrize("name,calls", [("kn", "append one"), ("vn", "append gather one"), ("sl", "append gather one"), ("k", "append gather attention one"),
+                                        ("ke", "append gather attention one"), ("q", "attention one"), ("cu", "attention one"),
+                                        ("ctx", "attention one"), ("bt", "attention one"), ("out", "attention one"), ("ws", "attention one"),
+                                        ("pairs", "copy")])
+def test_binding_refuses_tensors_without_dimensions(name, calls, monkeypatch):
+    L = _lib()
+    monkeypatch.setattr(L._tc(), "device", lambda: 0)
+    monkeypatch.setattr(torch, "Tensor", (torch.Tensor, _Fake))
+    f = _fakes(pairs=_Fake(torch.int32, 1, 2))
+    for shape in [(), (3,) * 5]:
+        f = dict(f, **{name: _Fake(f[name].dtype, *shape)})
+        made = dict(_calls(L, f), copy=lambda: L.cb_copy_blocks_fp8(f["pairs"], f["k"], f["v"], f["ke"], f["ve"], stream=1))
+        for call in calls.split():
+            with pytest.raises(ValueError):
+                made[call]()
