@@ -321,6 +321,12 @@ def _current_device(c, t):
     return c.device()
 
 
+def _fit_int(*sizes):
+    """Refuses what a C int cannot hold (ctypes would pass the low 32 bits)."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes must fit a C int, got {sizes}")
+
+
 def _raw_stream(c, dev, stream):
     return c.stream(dev) if stream is None else _stream(stream)
 
@@ -386,8 +392,9 @@ def cb_copy_blocks_fp8(pairs, k_cache, v_cache, k_exps, v_exps, stream=None):
 
 def cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim,
                                           block_size):
-    return int(lib().cb_paged_attention_fp8_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads,
-                                                           n_kv_heads, head_dim, block_size))
+    sizes = (n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, block_size)
+    _fit_int(*sizes)
+    return int(lib().cb_paged_attention_fp8_workspace_size(*sizes))
 
 
 def cb_paged_attention_fp8(q, cu_q_lens, ctx_lens, block_tables, k_cache, v_cache, k_exps, v_exps, out, scale,
@@ -429,8 +436,10 @@ def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_c
     n_tok, hq, a2 = shape
     if a2 != a:
         raise ValueError("cache shape mismatch")
-    args = (pq, pcu, pctx, pbt, tables[1], n_reqs, n_tok, int(max_q_len), int(max_kv_len), *cache, nb, po, float(scale),
-            hq, hk, a, bs, int(window), pw, workspace.shape[0], _raw_stream(c, dev, stream))
+    max_q_len, max_kv_len, window = int(max_q_len), int(max_kv_len), int(window)
+    _fit_int(max_q_len, max_kv_len, window)
+    args = (pq, pcu, pctx, pbt, tables[1], n_reqs, n_tok, max_q_len, max_kv_len, *cache, nb, po, float(scale),
+            hq, hk, a, bs, window, pw, workspace.shape[0], _raw_stream(c, dev, stream))
     if new is not None:
         k_new, v_new, slots = new
         pk = _on(dev, k_new, c.bf16, "k_new", 3)

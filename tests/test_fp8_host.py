@@ -254,3 +254,27 @@ def test_binding_refuses_tensors_without_dimensions(name, calls, monkeypatch):
         for call in calls.split():
             with pytest.raises(ValueError):
                 made[call]()
+
+
+@pytest.mark.parametrize("sizes", [(3 + (1 << 32), 8, 0), (3, 8 + (1 << 32), 0), (3, 8, 5 + (1 << 32)), (3, 8, 1 << 32), (3, 8, 1 << 31)])
+def test_binding_refuses_sizes_beyond_32_bits(sizes, monkeypatch):
+    """A window of 2^32 + 5 is not one of 5."""
+    L = _lib()
+    monkeypatch.setattr(L._tc(), "device", lambda: 0)
+    monkeypatch.setattr(torch, "Tensor", (torch.Tensor, _Fake))
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(L, "lib", Lib)
+    f = _fakes()
+    step = (f["q"], f["cu"], f["ctx"], f["bt"], f["k"], f["v"], f["ke"], f["ve"], f["out"], 0.1, f["ws"])
+    L.cb_paged_attention_fp8(*step, 3, 8, 0, stream=1)
+    with pytest.raises(ValueError):
+        L.cb_paged_attention_fp8(*step, *sizes, stream=1)
+    with pytest.raises(ValueError):
+        L.cb_kv_append_paged_attention_fp8(f["kn"], f["vn"], f["sl"], *step, *sizes, stream=1)
+    if sizes[2] == 0:
+        with pytest.raises(ValueError):
+            L.cb_paged_attention_fp8_workspace_size(1, 3, sizes[0], sizes[1], 4, 2, 64, 16)
