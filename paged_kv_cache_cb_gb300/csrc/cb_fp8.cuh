@@ -158,6 +158,22 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// ---------------------------------------------------------------- what both attention kernels use
+// Bounded wait with the same outcome in all 32 lanes.
+template <class S>
+__device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  if (!ok) {
+    set_error(P.err, CB_DEVERR_TIMEOUT);
+    sm.abort = 1;
+  }
+  return ok;
+}
+// The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
+__device__ __forceinline__ int cta_of(int u, int total, int eff) {
+  return (int)((((long long)u + 1) * eff - 1) / total);
+}
+
 // ---------------------------------------------------------------- joining pieces
 // A sequence cut between CTAs leaves per piece and row the maximum m and sum l of
 // its weights and its output o (already over l); the joined row is

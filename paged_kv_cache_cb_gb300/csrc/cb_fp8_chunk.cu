@@ -93,16 +93,6 @@ struct alignas(1024) Smem {
   volatile int abort;
 };
 
-template <class S>
-__device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-  if (!ok) {
-    set_error(P.err, CB_DEVERR_TIMEOUT);
-    sm.abort = 1;
-  }
-  return ok;
-}
-
 // ---------------------------------------------------------------- work
 // Key tiles [first, end) of the `pair`-th 2 TOK tokens of a request.
 __device__ __forceinline__ int pair_first(int ctx, int pair, int tok2, int window) {
@@ -214,11 +204,6 @@ struct ItemIter {
     return true;
   }
 };
-
-// The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
-__device__ __forceinline__ int cta_of(int u, int total, int eff) {
-  return (int)((((long long)u + 1) * eff - 1) / total);
-}
 
 // All threads; ends with __syncthreads().
 template <int A, int TOK, bool ONE>

@@ -167,16 +167,6 @@ __device__ __forceinline__ float finite(float f) {
   asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(f));
   return r;
 }
-// Bounded wait with the same outcome in all 32 lanes.
-template <class S>
-__device__ __forceinline__ bool wwait(const Fp8Step& P, S& sm, uint64_t* bar, uint32_t parity) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
-  if (!ok) {
-    set_error(P.err, CB_DEVERR_TIMEOUT);
-    sm.abort = 1;
-  }
-  return ok;
-}
 
 // ---------------------------------------------------------------- work
 // A segment: tiles [t0, t0 + nt) of the `tiles` tiles of sequence (r, hg).
@@ -243,11 +233,6 @@ __device__ __forceinline__ int request_tiles(const Fp8Step& P, int r, int bpt, i
   return ((int)nblk - window_first_block(keys, P.window) + bpt - 1) / bpt;
 }
 
-// The CTA whose range holds tile u (ranges [total b / eff, total (b + 1) / eff)).
-__device__ __forceinline__ int cta_of(int u, int total, int eff) {
-  return (int)((((long long)u + 1) * eff - 1) / total);
-}
-
 // All threads; ends with __syncthreads().
 template <int A, int G>
 __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S, int* pre, int* kv, int* tok, int hg_heads) {
@@ -308,17 +293,14 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A, G>& S,
 // ---------------------------------------------------------------- loads (warps 8, 9)
 // A segment's block-table entries, 32 at a time (a lane each), the next 32 (or
 // the next segment's first) on their way while these are used.
-struct Table {
-  int cur, nxt;
-  __device__ static int entry(const Fp8Step& P, const Seg& s, int bpt, int chunk) {
-    const int b = s.fb + s.t0 * bpt + chunk * 32 + (int)(threadIdx.x & 31);
-    const int end = (s.kv + kBlockSize - 1) / kBlockSize;
-    // entries past the segment belong to another CTA or to nobody: not read
-    if (b >= end || b >= s.fb + (s.t0 + s.nt) * bpt) return -2;
-    const int e = __ldg(P.block_tables + (size_t)s.r * P.max_blocks_per_seq + b);
-    return e < 0 || e >= P.cache.num_blocks ? -1 : e;
-  }
-};
+__device__ __forceinline__ int table_entry(const Fp8Step& P, const Seg& s, int bpt, int chunk) {
+  const int b = s.fb + s.t0 * bpt + chunk * 32 + (int)(threadIdx.x & 31);
+  const int end = (s.kv + kBlockSize - 1) / kBlockSize;
+  // entries past the segment belong to another CTA or to nobody: not read
+  if (b >= end || b >= s.fb + (s.t0 + s.nt) * bpt) return -2;
+  const int e = __ldg(P.block_tables + (size_t)s.r * P.max_blocks_per_seq + b);
+  return e < 0 || e >= P.cache.num_blocks ? -1 : e;
+}
 
 // K: also the tiles' exponents.  V: values only.
 template <int A, int G, bool IS_K>
@@ -336,7 +318,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
   uint32_t n = 0;
   bool ok = true;
   bool more = it.next(s);
-  int nxt = more ? Table::entry(P, s, bpt, 0) : -2;
+  int nxt = more ? table_entry(P, s, bpt, 0) : -2;
   while (more && ok) {
     const bool again = it.next(nx);
     const int per = 32 / bpt;                        // tiles per 32 entries
@@ -345,7 +327,7 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* map, Smem<A, G>&
       if (j % per == 0) {
         cur = nxt;
         if (IS_K && cur == -1) set_error(P.err, CB_DEVERR_BADBLOCK);   // its rows load as zeros
-        nxt = j + per < s.nt ? Table::entry(P, s, bpt, j / per + 1) : (again ? Table::entry(P, nx, bpt, 0) : -2);
+        nxt = j + per < s.nt ? table_entry(P, s, bpt, j / per + 1) : (again ? table_entry(P, nx, bpt, 0) : -2);
       }
       const int e = __shfl_sync(FULL, cur, (j % per) * bpt + (lane & (bpt - 1)));
       const int row = e >= 0 ? (e * Hkv + s.hg * hg_heads) * kBlockSize : rows_total;   // past the extent: zeros
