@@ -28,6 +28,16 @@ bool cache_of(Fp8Cache* c, const void* k, const void* v, const void* ke, const v
   return true;
 }
 
+// No C++ exception (an allocation or a lock of the library's host state) leaves an entry point.
+template <class F>
+int guarded(F call) {
+  try {
+    return call();
+  } catch (...) {
+    return CB_ECUDA;
+  }
+}
+
 struct NewRows {
   const void* k;
   const void* v;
@@ -123,61 +133,67 @@ extern "C" {
 int cb_kv_append_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, int n_tokens, void* k_cache,
                      void* v_cache, void* k_exps, void* v_exps, int num_blocks, int n_kv_heads, int head_dim,
                      int block_size, void* stream) {
-  Fp8Cache c;
-  if (n_tokens < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
-    return CB_EINVAL;
-  if (n_tokens == 0) {
-    set_last_launches(0);
+  return guarded([&]() -> int {
+    Fp8Cache c;
+    if (n_tokens < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+      return CB_EINVAL;
+    if (n_tokens == 0) {
+      set_last_launches(0);
+      return CB_OK;
+    }
+    if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new)) return CB_EINVAL;
+    int rc = CB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned int* err = stream_error_word(st, &rc);
+    if (!err) return rc;
+    if (launch_append_fp8(k_new, v_new, slot_mapping, n_tokens, c, err, st) != cudaSuccess) return CB_ECUDA;
+    set_last_launches(1);
     return CB_OK;
-  }
-  if (!k_new || !v_new || !slot_mapping || !aligned16(k_new) || !aligned16(v_new)) return CB_EINVAL;
-  int rc = CB_OK;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int* err = stream_error_word(st, &rc);
-  if (!err) return rc;
-  if (launch_append_fp8(k_new, v_new, slot_mapping, n_tokens, c, err, st) != cudaSuccess) return CB_ECUDA;
-  set_last_launches(1);
-  return CB_OK;
+  });
 }
 
 int cb_kv_gather_fp8(const int64_t* slot_mapping, int n_rows, const void* k_cache, const void* v_cache,
                      const void* k_exps, const void* v_exps, int num_blocks, void* k_out, void* v_out, int n_kv_heads,
                      int head_dim, int block_size, void* stream) {
-  Fp8Cache c;
-  if (n_rows < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
-    return CB_EINVAL;
-  if (n_rows == 0) {
-    set_last_launches(0);
+  return guarded([&]() -> int {
+    Fp8Cache c;
+    if (n_rows < 0 || !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+      return CB_EINVAL;
+    if (n_rows == 0) {
+      set_last_launches(0);
+      return CB_OK;
+    }
+    if (!k_out || !v_out || !slot_mapping || !aligned16(k_out) || !aligned16(v_out)) return CB_EINVAL;
+    int rc = CB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned int* err = stream_error_word(st, &rc);
+    if (!err) return rc;
+    if (launch_gather_fp8(slot_mapping, n_rows, c, k_out, v_out, err, st) != cudaSuccess) return CB_ECUDA;
+    set_last_launches(1);
     return CB_OK;
-  }
-  if (!k_out || !v_out || !slot_mapping || !aligned16(k_out) || !aligned16(v_out)) return CB_EINVAL;
-  int rc = CB_OK;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int* err = stream_error_word(st, &rc);
-  if (!err) return rc;
-  if (launch_gather_fp8(slot_mapping, n_rows, c, k_out, v_out, err, st) != cudaSuccess) return CB_ECUDA;
-  set_last_launches(1);
-  return CB_OK;
+  });
 }
 
 int cb_copy_blocks_fp8(const int32_t* pairs, int n_pairs, void* k_cache, void* v_cache, void* k_exps, void* v_exps,
                        int num_blocks, int n_kv_heads, int head_dim, int block_size, void* stream) {
-  Fp8Cache c;
-  if (n_pairs < 0 || n_pairs > 65535 ||
-      !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
-    return CB_EINVAL;
-  if (n_pairs == 0) {
-    set_last_launches(0);
+  return guarded([&]() -> int {
+    Fp8Cache c;
+    if (n_pairs < 0 || n_pairs > 65535 ||
+        !cache_of(&c, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
+      return CB_EINVAL;
+    if (n_pairs == 0) {
+      set_last_launches(0);
+      return CB_OK;
+    }
+    if (!pairs) return CB_EINVAL;
+    int rc = CB_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    unsigned int* err = stream_error_word(st, &rc);
+    if (!err) return rc;
+    if (launch_copy_blocks_fp8(pairs, n_pairs, c, err, st) != cudaSuccess) return CB_ECUDA;
+    set_last_launches(1);
     return CB_OK;
-  }
-  if (!pairs) return CB_EINVAL;
-  int rc = CB_OK;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  unsigned int* err = stream_error_word(st, &rc);
-  if (!err) return rc;
-  if (launch_copy_blocks_fp8(pairs, n_pairs, c, err, st) != cudaSuccess) return CB_ECUDA;
-  set_last_launches(1);
-  return CB_OK;
+  });
 }
 
 size_t cb_paged_attention_fp8_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
@@ -194,9 +210,11 @@ int cb_paged_attention_fp8(const void* q, const int32_t* cu_q_lens, const int32_
                            const void* v_exps, int num_blocks, void* out, float scale, int n_q_heads, int n_kv_heads,
                            int head_dim, int block_size, int window, void* workspace, size_t workspace_bytes,
                            void* stream) {
-  return step_fp8(nullptr, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
-                  max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
-                  head_dim, block_size, window, workspace, workspace_bytes, stream);
+  return guarded([&]() -> int {
+    return step_fp8(nullptr, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
+                    max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
+                    head_dim, block_size, window, workspace, workspace_bytes, stream);
+  });
 }
 
 int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const int64_t* slot_mapping, const void* q,
@@ -205,10 +223,12 @@ int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const
                                      void* k_cache, void* v_cache, void* k_exps, void* v_exps, int num_blocks, void* out,
                                      float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
                                      int window, void* workspace, size_t workspace_bytes, void* stream) {
-  const NewRows app{k_new, v_new, slot_mapping};
-  return step_fp8(&app, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
-                  max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
-                  head_dim, block_size, window, workspace, workspace_bytes, stream);
+  return guarded([&]() -> int {
+    const NewRows app{k_new, v_new, slot_mapping};
+    return step_fp8(&app, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
+                    max_kv_len, k_cache, v_cache, k_exps, v_exps, num_blocks, out, scale, n_q_heads, n_kv_heads,
+                    head_dim, block_size, window, workspace, workspace_bytes, stream);
+  });
 }
 
 }  // extern "C"
