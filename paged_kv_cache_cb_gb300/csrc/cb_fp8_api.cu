@@ -72,11 +72,11 @@ int step_fp8(const NewRows* app, const void* q, const int32_t* cu_q_lens, const 
   Fp8Step s{};
   if (!cache_of(&s.cache, k_cache, v_cache, k_exps, v_exps, num_blocks, n_kv_heads, head_dim, block_size))
     return CB_EINVAL;
-  // the kernels count tiles of the step in 32 bits, the single tokens' with up to 6 empty places a request
+  // the kernels count tiles of the step in 32 bits, with the empty places before them (single tokens: up to 6)
   const long long blocks = std::min<long long>(max_blocks_per_seq, ((long long)max_kv_len + kBlockSize - 1) / kBlockSize);
   const long long tok = kTileM / (n_q_heads / n_kv_heads), items = n_tokens / (2 * tok) + n_reqs;
   if ((blocks + 7) * n_reqs * n_kv_heads >= 1LL << 31 ||
-      items * (((long long)max_kv_len + kTileN - 1) / kTileN) * n_kv_heads >= 1LL << 31)
+      items * (((long long)max_kv_len + kTileN - 1) / kTileN + kChunkLead) * n_kv_heads >= 1LL << 31)
     return CB_EINVAL;
   if (!q || !cu_q_lens || !ctx_lens || !block_tables || !out || !workspace) return CB_EINVAL;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace)) return CB_EINVAL;

@@ -29,10 +29,11 @@
 // over in two halves of 64 keys, so the products start while the second half is
 // computed.  An item of at most TOK tokens has one query tile.
 //
-// Work.  All items' key tiles, laid end to end, are cut into one equal range per
-// CTA (one CTA per SM); an item cut at a range's end leaves (m, l, o) per piece
-// and a second kernel (cb_fp8_join.cu) joins them.  Where whole items, dealt to the
-// CTAs in turn, end sooner than the cut ranges and their joining, they stay whole.
+// Work.  All items' key tiles, each item's behind a few empty places for its start and
+// end, laid end to end, are cut into one equal range per CTA (one CTA per SM); an item
+// cut at a range's end leaves (m, l, o) per piece and a second kernel
+// (cb_fp8_join.cu) joins them.  Where whole items, dealt to the CTAs in turn, end
+// sooner than the cut ranges and their joining, they stay whole.
 //
 // Warps: 0-3 and 4-7 softmax of tiles A and B (thread = row; the row's 128
 // scores stay in registers, one read of tensor memory; also the query's terms and
@@ -59,11 +60,19 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kRows = kChunkRows;      // rows of an item (two query tiles)
-// What cutting items costs, in key tiles' time (2 us): the pieces' queries and
-// partial results, their joining.  813 new tokens under a window of 1000: whole
-// items (10 tiles) 51 us, cut ones (6.5) 63 us; 1024 after 1024 and 2048 keys, next
-// to 48 single tokens: whole (20) 140 us, cut (12.2) 156 us.
-constexpr int kCutTiles = 10;
+// The cut (see Work above), in key tiles' time (2 us; single tokens 1.4).  An item's
+// start and end (its queries, first scores and output) are kLead empty places: cut by
+// tiles alone, a range of short items takes as many starts and ends.  With 0, 2, 4 and
+// 6 of them 2048 tokens without stored keys, cut, took 180, 99, 89 and 88 us, 8192 of
+// them 1037, 730, 604 and 579, 512 after 4096 keys 76, 73, 71 and 72; 256 single tokens
+// of 32 heads on 1 with 0, 2 and 4 of them 164, 161 and 162.
+// kJoinTiles is how much sooner the cut ranges must end than whole items: 512 tokens
+// after 2048 keys (10 tiles sooner) take 67 us whole and 56 cut, 2048 after 2048 (12)
+// 147 and 142, but 2048 without stored keys of 64 heads on 8 (9) 127 and 143, next to
+// 48 single tokens 235 and 257; at 5 to 8 either may be 3 us shorter.
+template <bool ONE>
+constexpr int kLead = ONE ? 2 : kChunkLead;
+constexpr int kJoinTiles = 9;
 constexpr int kSmemLimit = 232448;
 
 // An item, and the piece [a, b) of its key tiles [first, end); b = a: no more items.
@@ -121,13 +130,14 @@ __device__ __forceinline__ int3 request(const Fp8Step& P, int r, bool report) {
 // keys) down, KV heads inside.
 template <int TOK, bool ONE>
 struct ItemIter {
+  static constexpr int LEAD = kLead<ONE>;
   const Fp8Step& P;
-  const int* tpre;                     // tiles before request r
+  const int* tpre;                     // places before request r
   const int* ipre;                     // items before request r
   int whole, step, index, n_items;   // whole items: index, index + step, ...
   int u, u1;                           // cut ranges
   int3 rq;
-  int r, pair, g, j0;                  // the next piece's place (cut ranges)
+  int r, pair, g, j0;                  // the next item, the place within it where the range goes on (cut ranges)
   bool fresh = true;
   template <class S>
   __device__ ItemIter(const Fp8Step& p, const S& s, const int* tp, const int* ip)
@@ -171,37 +181,43 @@ struct ItemIter {
       index += step;
       return true;
     }
-    if (u >= u1) return false;
-    if (fresh) {
+    while (u < u1) {
+      if (fresh) locate();
       fresh = false;
-      r = find(tpre, u);
-      rq = request<ONE>(P, r, false);
-      int off = u - tpre[r];
-      for (pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1; pair > 0; --pair) {
-        const int t = (pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window)) * Hkv;
-        if (off < t) break;
-        off -= t;
+      fill(I);
+      const int last = min(places(), j0 + (u1 - u));           // its places j0 .. last - 1 are in the range
+      I.a = I.first + max(j0, LEAD) - LEAD;
+      I.b = I.first + last - LEAD;
+      u += last - j0;
+      j0 = 0;
+      if (++g == Hkv) {
+        g = 0;
+        if (--pair < 0 && u < u1) {
+          do {
+            ++r;
+          } while (tpre[r + 1] <= u);
+          rq = request<ONE>(P, r, false);
+          pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1;
+        }
       }
-      const int t = pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window);
-      g = off / t;
-      j0 = off % t;
+      if (I.b > I.a) return true;                              // not only empty places
     }
-    fill(I);
-    I.a = I.first + j0;
-    I.b = min(I.end, I.a + (u1 - u));
-    u += I.b - I.a;
-    j0 = 0;
-    if (++g == Hkv) {
-      g = 0;
-      if (--pair < 0 && u < u1) {
-        do {
-          ++r;
-        } while (tpre[r + 1] <= u);
-        rq = request<ONE>(P, r, false);
-        pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1;
-      }
+    return false;
+  }
+  // Places of an item of the pair.
+  __device__ int places() const { return LEAD + pair_end(rq.z, rq.y, pair, 2 * TOK) - pair_first(rq.z, pair, 2 * TOK, P.window); }
+  // The item of place u.
+  __device__ void locate() {
+    r = find(tpre, u);
+    rq = request<ONE>(P, r, false);
+    int off = u - tpre[r];
+    for (pair = (rq.y + 2 * TOK - 1) / (2 * TOK) - 1; pair > 0; --pair) {
+      const int t = places() * P.cache.n_kv_heads;
+      if (off < t) break;
+      off -= t;
     }
-    return true;
+    g = off / places();
+    j0 = off % places();
   }
 };
 
@@ -232,24 +248,28 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     mx = __reduce_max_sync(0xffffffffu, mx);
     __syncwarp();
     if (lane == 0) {
-      tpre[r] = t * Hkv;
+      t = (t + pairs * kLead<ONE>) * Hkv;
+      tpre[r] = t;
       ipre[r] = pairs * Hkv;
       atomicMax(&S.longest, mx);
-      atomicAdd(&S.high, (t * Hkv) >> 12);
+      atomicAdd(&S.high, t >> 12);
     }
   }
   __syncthreads();
   // exclusive prefix sums of both
   const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
-  int t_own = 0, i_own = 0;
+  unsigned t_own = 0;
+  int i_own = 0;
   for (int r = lo; r < hi; ++r) {
     t_own += tpre[r];
     i_own += ipre[r];
   }
-  int t_incl = t_own, i_incl = i_own;
+  unsigned t_incl = t_own;
+  int i_incl = i_own;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, t_incl, off), y = __shfl_up_sync(0xffffffffu, i_incl, off);
+    const unsigned x = __shfl_up_sync(0xffffffffu, t_incl, off);
+    const int y = __shfl_up_sync(0xffffffffu, i_incl, off);
     if (lane >= off) {
       t_incl += x;
       i_incl += y;
@@ -260,9 +280,10 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     S.iscan[wid] = i_incl;
   }
   __syncthreads();
-  int total = 0, t_run = t_incl - t_own, items = 0, i_run = i_incl - i_own;
+  unsigned all = 0, t_run = t_incl - t_own;
+  int items = 0, i_run = i_incl - i_own;
   for (int w = 0; w < kThreads / 32; ++w) {
-    total += S.scan[w];
+    all += S.scan[w];
     items += S.iscan[w];
     if (w < wid) {
       t_run += S.scan[w];
@@ -271,15 +292,16 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
   }
   for (int r = lo; r < hi; ++r) {
     const int t = tpre[r], i = ipre[r];
-    tpre[r] = t_run;
+    tpre[r] = (int)t_run;
     ipre[r] = i_run;
     t_run += t;
     i_run += i;
   }
   if (tid == 0) {
-    // Query lengths that increase count every token once, and the host has seen to it that their tiles fit 32 bits.
-    // Others may count a token in many requests.  `high` sums each request's tiles without their lowest 12 bits,
-    // which come to 2^23 at most: below 2^19 of it the sum of all is under 2^31 + 2^23, and shows by its sign.
+    // Query lengths that increase count every token once, and the host has seen to it that their places fit 32 bits.
+    // Others may count a token in many requests.  `high` sums each request's places without their lowest 12 bits,
+    // which come to 2^23 at most: below 2^19 of it the sum of all is under 2^31 + 2^23, and shows by its top bit.
+    int total = (int)all;
     if (S.high >= 1 << 19 || total < 0) {
       set_error(P.err, CB_DEVERR_BADLEN);
       total = items = 0;                               // no work
@@ -289,7 +311,9 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     const int grid = gridDim.x, b = blockIdx.x, eff = max(1, min(grid, total));
     S.tiles = total;
     S.items = items;
-    S.whole = (long long)((items + grid - 1) / grid) * S.longest <= (total + grid - 1) / grid + kCutTiles;
+    // whole items, dealt in turn: the first CTA's, the longest and mean ones; cut ones: an even share, joined
+    const long long more = (items + grid - 1) / grid - 1;
+    S.whole = items == 0 || S.longest + more * (total / items) <= (total + grid - 1) / grid + kJoinTiles;
     S.eff = S.whole ? grid : eff;
     S.u0 = b < eff ? (int)((long long)total * b / eff) : total;
     S.u1 = b < eff ? (int)((long long)total * (b + 1) / eff) : total;
@@ -304,11 +328,10 @@ __device__ void make_plan(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, in
     if (!S.whole && S.u1 > S.u0 && S.u1 < S.tiles) {
       ItemIter<TOK, ONE> it(P, S, tpre, ipre);
       it.u = S.u1 - 1;
-      Item I;
-      it.next(I);
-      const int start = S.u1 - 1 - (I.a - I.first), end = start + (I.end - I.first);
-      if (start >= S.u0 && end > S.u1)
-        rec = {I.r, I.g, cta_of(end - 1, S.tiles, S.eff) - (int)blockIdx.x + 1, I.pair};
+      it.locate();
+      const int start = it.u - it.j0, first = start + kLead<ONE>, end = start + it.places();
+      if (first >= S.u0 && first < S.u1 && end > S.u1)
+        rec = {it.r, it.g, cta_of(end - 1, S.tiles, S.eff) - (int)blockIdx.x + 1, it.pair};
     }
     W.rec[blockIdx.x] = rec;
   }

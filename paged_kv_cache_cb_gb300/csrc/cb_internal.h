@@ -159,6 +159,7 @@ struct Fp8Partials {
   float* ml;                    // [2 * kMaxDecodeGrid][rows][2]
   float* acc;                   // [2 * kMaxDecodeGrid][rows * A]
 };
+constexpr int kChunkLead = 4;   // empty places in front of an item of several tokens
 constexpr int kSingleRows = 64, kChunkRows = 256;   // of the single tokens' pieces, of the chunks'
 inline size_t fp8_partials_bytes(int rows, int head_dim) {
   return sizeof(Fp8Rec) * kMaxDecodeGrid + (size_t)2 * kMaxDecodeGrid * rows * (2 + head_dim) * 4;
