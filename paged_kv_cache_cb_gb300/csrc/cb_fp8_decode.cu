@@ -43,21 +43,23 @@
 // range per CTA (one CTA per SM).  The empty places stand for what a sequence's end
 // costs its CTA (4.5 us; without them and with: 2 sequences 26.0 and 23.3 us, 48 90.7
 // and 87.1, 200 of 50-1000 keys 74 and 62.6; 100 of 50-600 keys on 32 KV heads 66 and
-// 58.4, with one place 63.4).  A
-// sequence cut at a range's end leaves (m, l, o) per piece, and a second small
-// kernel (cb_fp8_join.cu) joins the pieces by log-sum-exp: no counters, no grid
-// barrier, nothing to initialise, and the same bits every time.
+// 58.4, with one place 63.4.  With 0, 3, 6 and 9: groups of 2, 48 sequences 81.0, 81.0,
+// 79.4 and 79.9, 100 short ones 31.1, 28.8, 28.0 and 28.8; groups of 8, 125, 120, 117.4
+// and 118, and 52.2, 46.9, 47.7 and 48.1; 8 heads on 1 KV head 36.7, 34.3, 35.9 and
+// 36.5, and 24.2, 23.9, 23.8 and 23.3).  A sequence cut at a range's end leaves
+// (m, l, o) per piece, and a second small kernel (cb_fp8_join.cu) joins the pieces by
+// log-sum-exp: no counters, no grid barrier, and the same bits every time.
 //
 // Warps: 0-3 and 4-7 softmax groups, which share a range's parts of sequences
 // (segments) tile by tile: every second tile each, with its own maxima, sums and O
 // in tensor memory, joined at the segment's end.  A tile's chain (scores, maxima,
 // weights, one barrier of the group for a move of O) is mostly waiting, so two
 // tiles at a time take little more than one: with a segment per group in turn, 48
-// decodes took 104 us instead of 90 (both without the empty places).  8 K loads, 9 V loads (TMA through the block
-// table; the exponents by per-thread copies: a TMA copy of 16 bytes takes the unit
-// as long as one of 2 KB), 10 issues S, 11 issues O, 12-15 make the next segments'
-// query terms ready.  Thread = tile row, then output dimension.  Every wait is
-// bounded.
+// decodes took 104 us instead of 90 (both without the empty places).  8 K loads, 9 V
+// loads (TMA through the block table; the exponents by per-thread copies: a TMA copy
+// of 16 bytes takes the unit as long as one of 2 KB), 10 issues S, 11 issues O, 12-15
+// make the next segments' query terms ready.  Thread = tile row, then output
+// dimension.  Every wait is bounded.
 //
 // Bound by HBM where a KV head has one query head: 64 decodes of 32 heads (512 to
 // 4096 keys, 1.30 GB) in 199 us, 6.5 TB/s, 0.96 of a copy's rate.  With four, a
@@ -90,7 +92,7 @@ struct Cfg {
   static constexpr int PB = 4;                               // w buffers
   static constexpr int ES = 8;                               // exponent stages
   static constexpr int kTile = 128 * A;                      // bytes
-  static constexpr int kLead = G >= 4 ? 6 : 3;               // what a segment's end costs, in tiles (see Work above)
+  static constexpr int kLead = G >= 2 ? 6 : 3;               // what a segment's end costs, in tiles (see Work above)
   static constexpr int kCols = SB * NS + 2 * NO;
   static constexpr int kTmem = kCols <= 128 ? 128 : (kCols <= 256 ? 256 : 512);
   static_assert(kCols <= 512, "tensor memory");
