@@ -9,11 +9,11 @@
 //   whose products add up (4 significant bits each: bf16's 8; values down to
 //   2^-9 of the row's largest exactly, smaller ones within 2^-17 of it).
 //   S is up to 2^24 and ek up to 120, so S 2^ek alone may pass fp32's range where
-//   x does not.  Of a tile's keys the largest exponent E is taken out: S is
-//   multiplied by 2^(ek - E) <= 1, the row's factor by 2^E.  What underflows is a
-//   key 2^126 times smaller than another of the tile, whose score is 0 next to that
-//   one's.  (With an E for every 32 keys the softmax has four factors to hold: 2048
-//   tokens after 30720 keys took 942 us instead of 905.)
+//   x does not.  What a tile's largest ek has beyond 100 is its E (0 almost always):
+//   S is multiplied by 2^(ek - E), the row's factor by 2^E.  No key falls out at the
+//   other end: ek - E is -146 at least, a subnormal.  (With an E for every 32 keys
+//   the softmax has four factors to hold: 2048 tokens after 30720 keys took 942 us
+//   instead of 905.)
 //   O = p V takes V as bf16, converted exactly (the rows' scales are powers of
 //   two), and p rounded to bf16 (2^-8 relative, the type of the 16-bit cache);
 //   the sum of p is taken before that rounding.
@@ -517,7 +517,7 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       const uint32_t kb = lds8(smem_u32(&S.ex[st][0][key_l])), vb = lds8(smem_u32(&S.ex[st][1][key_l]));
       const int key = j * kTileN + key_l;
       const bool seen = key >= key_lo && key < kv_hi, nan = vb == kExpNan;
-      uint32_t ke = 1;                                         // E + 127 of the keys that are seen
+      uint32_t ke = 1;                                         // the largest exponent byte of the keys that are seen
       if constexpr (ONE) {
         if (seen && kb != kExpNan) ke = kb;
       } else {                                                 // each warp for itself: lane l takes keys 4 l .. 4 l + 3 of the tile
@@ -529,8 +529,9 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
           if (k >= key_lo && k < kv_hi && b != kExpNan) ke = max(ke, b);
         }
       }
-      ke = __reduce_max_sync(FULL, ke);
-      sts32(smem_u32(&S.fk[n & 3][key_l]), kb == kExpNan ? 0x7FC00000u : (uint32_t)max((int)(kb - ke) + 127, 0) << 23);
+      ke = max(__reduce_max_sync(FULL, ke), 227u) - 100u;
+      const int d = (int)(kb + 127u) - (int)ke;                // ek - E + 127
+      sts32(smem_u32(&S.fk[n & 3][key_l]), kb == kExpNan ? 0x7FC00000u : d > 0 ? (uint32_t)d << 23 : 0x400000u >> min(-d, 31));
       const unsigned bad = __ballot_sync(FULL, nan && seen);
       if (lane == 0) {
         sts32(smem_u32(&S.v_nan[n & 3][warp]), bad);

@@ -53,6 +53,25 @@ def test_keys_of_all_sizes_side_by_side(hq, hk, a, q_len):
 
 
 @pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("kexp,large", [(87, 220), (87, 247), (10, 230), (121, 247), (1, 126)])
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_a_large_key_does_not_hide_small_ones(hq, hk, a, kexp, large, q_len):
+    """Keys up to 2^240 times the others, at right angles to the queries; with several
+    tokens also one that only the last token, whose query is 0, sees."""
+    s = Step([(q_len, 300)], hq, hk, a, seed=67, kexp=(kexp, kexp + 2), qscale=2.0 ** (121 - kexp))
+    s.q[..., 1] = 0
+    for p in (3, 140, 290) + ((319,) if q_len > 1 else ()):
+        at = s.tables[0, p // BS], slice(None), p % BS
+        s.k_exps[at] = large
+        if p < 319:
+            s.k_codes[at] = 0
+            s.k_codes[at][:, 1] = 0x7E
+    if q_len > 1:
+        s.q[-1] = 0
+    check(s.run(), *s.reference(), "a large key")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
 @pytest.mark.parametrize("q_len", [1, 3])
 def test_query_of_zeros_under_a_small_scale(hq, hk, a, q_len):
     """Every score is 0, whatever the scale; the keys out of sight stay out."""
