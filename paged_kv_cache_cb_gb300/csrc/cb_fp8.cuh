@@ -31,6 +31,14 @@ __device__ __forceinline__ float exp_scale(uint32_t b) {
 }
 __device__ __forceinline__ float exp_inverse(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
+// The largest finite number for an infinity, a NaN for a NaN: the factors' product may
+// pass fp32's range where the score they multiply is 0.
+__device__ __forceinline__ float finite(float f) {
+  float r;
+  asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(f));
+  return r;
+}
+
 // Two floats -> two e4m3 in the low 16 bits (first one lowest), rounded to nearest even.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   uint16_t r;

@@ -90,8 +90,8 @@ struct alignas(1024) Smem {
   uint8_t vr[2][128 * A];              // V as in the cache, no swizzle
   uint8_t v[2][H][128][128];           // V in bf16
   float fk[4][128];                    // 2^(ek - E) of the tile's keys
-  uint32_t ke[4][4];                   // E + 127, by the warp that wrote them (single tokens: of its 32 keys)
-  uint32_t rb[4][32];                  // single tokens: the rows' exponent bytes, of four items
+  float fe[4][4];                      // 2^E, by the warp that wrote them (single tokens: of its 32 keys)
+  float fq[4][32];                     // single tokens: the rows' factors, of four items
   uint32_t v_nan[4][4];                // keys whose V stands for NaNs (stored as zeros)
   uint8_t ex[2][2][128];               // the tile's exponent bytes, K and V
   uint64_t q_full[2], k_full[2], k_empty[2], vr_full[2], vr_empty[2], fk_full[4], v_full[2], v_empty[2];
@@ -433,11 +433,12 @@ __device__ void load_tiles(const Fp8Step& P, const CUtensorMap* kmap, Smem<A>& S
 }
 
 // ---------------------------------------------------------------- conversion of V (warps 8-11)
-// This thread's query row as two e4m3 terms; returns eq + 127 (kExpNan for a row
-// that is not finite, whose terms are zeros).
+// This thread's query row as two e4m3 terms; returns its factor scale log2(e)
+// 2^eq: finite and not 0 (keys out of sight are -inf times it), but NaN for a row that
+// is not finite, whose terms are zeros.
 // ready(): called between the loads and the first store; false: nothing is stored.
 template <int A, class F>
-__device__ uint32_t make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid, F ready) {
+__device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int tok, int head, bool valid, F ready) {
   const uint4* src = reinterpret_cast<const uint4*>(P.q + ((size_t)tok * P.n_q_heads + head) * A);
   uint4 x[A / 8];
 #pragma unroll
@@ -448,8 +449,9 @@ __device__ uint32_t make_query(const Fp8Step& P, Smem<A>& S, int side, int row, 
     m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
   m = max(m & 0xFFFFu, m >> 16);
   const bool bad = m >= 0x7F80u;
-  const uint32_t eb = bad ? kExpNan : (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
-  if (!ready()) return eb;
+  const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
+  const float factor = bad ? __uint_as_float(0x7FC00000u) : finite(fmaxf(P.scale_log2 * __uint_as_float(eb << 23), 1.4e-45f));
+  if (!ready()) return factor;
   const float f = exp_inverse(bad ? 1u : eb);
 #pragma unroll
   for (int c = 0; c < A / 16; ++c) {
@@ -469,14 +471,7 @@ __device__ uint32_t make_query(const Fp8Step& P, Smem<A>& S, int side, int row, 
   }
   fence_proxy_async_smem();
   mbar_arrive(&S.q_full[side]);
-  return eb;
-}
-// The factor scale log2(e) 2^eq 2^E of a query row's exponent byte rb and that of the
-// keys: NaN for a row of NaNs, else finite and not 0 (keys out of sight are -inf times it).
-__device__ __forceinline__ float score_factor(const Fp8Step& P, uint32_t rb, uint32_t ke) {
-  const float x = P.scale_log2 * __uint_as_float((uint32_t)min(max((int)(rb + ke) - 127, 1), 254) << 23);
-  const float f = fminf(fmaxf(x, 1.17549435e-38f), 3.4028235e38f);
-  return rb == kExpNan ? __uint_as_float(0x7FC00000u) : f;
+  return factor;
 }
 
 // ONE: also the query rows of each single-token item, while the softmax is still
@@ -502,10 +497,10 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
     items.done(S, a ^ b ^ kv_hi ^ key_lo ^ tok ^ head);
     if constexpr (ONE) {
       // (every tile of the item before is converted: nothing that its S waits for waits for this warp)
-      const uint32_t rb = make_query<A>(P, S, 0, 32 * warp + lane, tok, head, lane < G,
-                                        [&] { return ok = it == 0 || wwait(P, S, &S.q_free, (it - 1) & 1); });
+      const float fq = make_query<A>(P, S, 0, 32 * warp + lane, tok, head, lane < G,
+                                     [&] { return ok = it == 0 || wwait(P, S, &S.q_free, (it - 1) & 1); });
       if (!ok) break;
-      if (warp == 0) sts32(smem_u32(&S.rb[it & 3][lane]), rb);
+      if (warp == 0) sts32(smem_u32(&S.fq[it & 3][lane]), __float_as_uint(fq));
     }
     for (int j = a; j < b; ++j, ++n) {
       const uint32_t st = n & 1, ph = (n >> 1) & 1;
@@ -535,7 +530,7 @@ __device__ void convert(const Fp8Step& P, Smem<A>& S) {
       const unsigned bad = __ballot_sync(FULL, nan && seen);
       if (lane == 0) {
         sts32(smem_u32(&S.v_nan[n & 3][warp]), bad);
-        sts32(smem_u32(&S.ke[n & 3][warp]), ke);
+        sts32(smem_u32(&S.fe[n & 3][warp]), ke << 23);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.fk_full[n & 3]);
@@ -665,10 +660,10 @@ __device__ void issue(const Fp8Step& P, Smem<A>& S) {
 // ---------------------------------------------------------------- softmax (warps 0-3, 4-7)
 // One key tile (number n; this query tile's S in s_t, its O in o_t) of this
 // thread's row: its weights into tensor memory, m and l brought up to date.
-// rb: the row's exponent byte; it sees the keys lo .. pos.  fresh: O holds nothing yet.
+// fr: the row's factor; it sees the keys lo .. pos.  fresh: O holds nothing yet.
 template <int A>
-__device__ __forceinline__ void softmax_tile(const Fp8Step& P, Smem<A>& S, uint32_t s_t, uint32_t o_t, int side, uint32_t n, int key0,
-                                             bool fresh, uint32_t rb, int lo, int pos, float& m, float& l) {
+__device__ __forceinline__ void softmax_tile(Smem<A>& S, uint32_t s_t, uint32_t o_t, int side, uint32_t n, int key0, bool fresh, float fr,
+                                             int lo, int pos, float& m, float& l) {
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const unsigned span = (unsigned)(pos - lo);                // key k is visible iff (unsigned)(k - lo) <= span
@@ -696,7 +691,7 @@ __device__ __forceinline__ void softmax_tile(const Fp8Step& P, Smem<A>& S, uint3
   float a[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
 #pragma unroll
   for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
-  const float fq = score_factor(P, rb, S.ke[n & 3][0]);
+  const float fq = finite(fr * S.fe[n & 3][0]);
   const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * fq;
   const bool need = mt > m + 8.f;
   float alpha = 1.f;
@@ -753,19 +748,19 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
   uint32_t n = 0, ns = 0, ni = 0;      // key tiles of all items, of this side's items; this side's items
   const Item* item = nullptr;
   // the next item that has this side, its query rows made ready
-  auto next_item = [&](uint32_t& rb) {
+  auto next_item = [&](float& fr) {
     while ((item = items.next(P, S)) != nullptr) {
       if (side < item->sides) {
         const int ti = item->tok_lo + side * TOK + row / G;
-        rb = make_query<A>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi, [] { return true; });
+        fr = make_query<A>(P, S, side, row, item->q0 + ti, item->g * G + row % G, ti < item->tok_hi, [] { return true; });
         return;
       }
       n += item->b - item->a;
       items.done(S, n);
     }
   };
-  uint32_t rb = 0;
-  next_item(rb);
+  float fr = 0.f;
+  next_item(fr);
   while (item) {
     const int ti = item->tok_lo + side * TOK + row / G, tok_hi = item->tok_hi, a0 = item->a, b0 = item->b;
     const int pos = item->ctx + min(ti, tok_hi - 1);         // the last key this row sees
@@ -782,14 +777,14 @@ __device__ void softmax(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, int 
       ok = ok && wwait(P, S, &S.fk_full[n & 3], (n >> 2) & 1) && wwait(P, S, &S.s_full[side], ns & 1);   // O holds all products before
       if (!ok) break;
       tc_fence_after();
-      softmax_tile<A>(P, S, s_t, o_t, side, n, j * kTileN, j == a0, rb, lo, pos, m, l);
+      softmax_tile<A>(S, s_t, o_t, side, n, j * kTileN, j == a0, fr, lo, pos, m, l);
     }
     if (!ok) {
       S.abort = 1;
       break;
     }
     // the next item's query first: its first scores are computed during this one's output
-    next_item(rb);
+    next_item(fr);
     if (!wwait(P, S, &S.o_full[side], ni & 1)) break;
     tc_fence_after();
     const float inv = l != 0.f ? 1.f / l : 0.f;              // 0: a piece in which the row saw no key
@@ -928,7 +923,7 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
     const bool began = a0 > item->first, cut = began || b0 < item->end;
     const int tok = item->q0;
     bool ok = true;
-    uint32_t rb = 0;
+    float fr = 0.f;
     items.done(S, a0 ^ b0 ^ pos ^ g ^ tok ^ (int)cut);
     float m = kNegInf, l = 0.f;
     for (int j = a0 + side; j < b0; j += 2, ++ns) {
@@ -942,9 +937,9 @@ __device__ void softmax_one(const Fp8Step& P, const Fp8Partials& W, Smem<A>& S, 
       tmem_ld32(s_t + 32 * w, s);
       const uint32_t fk = smem_u32(&S.fk[nj & 3][32 * w]);
       const uint32_t vn = lds32(smem_u32(&S.v_nan[nj & 3][w]));
-      const uint32_t ke = lds32(smem_u32(&S.ke[nj & 3][w]));
-      if (j == a0 + side) rb = lds32(smem_u32(&S.rb[i & 3][lane]));   // written before the first tile's factors
-      const float fq = score_factor(P, rb, ke);
+      const float fe = lds32f(smem_u32(&S.fe[nj & 3][w]));
+      if (j == a0 + side) fr = lds32f(smem_u32(&S.fq[i & 3][lane]));   // written before the first tile's factors
+      const float fq = finite(fr * fe);
       const int key = j * kTileN + 32 * w;
       tmem_wait_ld();
 #pragma unroll

@@ -162,13 +162,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
-// The largest finite number for an infinity, a NaN for a NaN: the factors' product may
-// pass fp32's range where the score they multiply is 0.
-__device__ __forceinline__ float finite(float f) {
-  float r;
-  asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(r) : "f"(f));
-  return r;
-}
 
 // ---------------------------------------------------------------- work
 // A segment: tiles [t0, t0 + nt) of the `tiles` tiles of sequence (r, hg).

@@ -72,6 +72,21 @@ def test_a_large_key_does_not_hide_small_ones(hq, hk, a, kexp, large, q_len):
 
 
 @pytest.mark.parametrize("hq,hk,a", SHAPES)
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_the_smallest_queries_keep_their_scale(hq, hk, a, q_len):
+    """Rows of 2^-119 in line with keys of 2^108, on either side: small scores, but
+    not nothing, from a factor below the normal numbers."""
+    s = Step([(q_len, 300)], hq, hk, a, seed=68)
+    s.q[:] = 2.0 ** -119
+    for i, at in enumerate(_every_row(s)):
+        s.k_codes[at], s.k_exps[at] = 0x7E if i % 2 else 0xFE, 227
+        s.v_codes[at] = (s.v_codes[at] & 127) | (0 if i % 2 else 128)
+    ref, mag = s.reference()
+    assert np.abs(ref).max() > 0.01 * mag.max()
+    check(s.run(), ref, mag, "small queries")
+
+
+@pytest.mark.parametrize("hq,hk,a", SHAPES)
 @pytest.mark.parametrize("q_len", [1, 3])
 def test_query_of_zeros_under_a_small_scale(hq, hk, a, q_len):
     """Every score is 0, whatever the scale; the keys out of sight stay out."""
