@@ -1,9 +1,10 @@
 // The 8-bit KV cache's data movement: append with quantisation, read-back and
 // block copies (format: cb_fp8.cuh).
 //
-// One pass each, bound by HBM: 65,536 new tokens (8 KV heads of 128, 404 MB) in 70
-// us, 5.8 TB/s, 0.85 of a copy's rate; 32,768 rows read back (202 MB) in 35 us, 5.8
-// TB/s, 0.86.  A step's few tokens take the launch, 3.5 us of GPU time.
+// One pass each, bound by HBM: 65,536 new tokens (8 KV heads of 128, 404 MB) in 68.5
+// us, 5.9 TB/s, 0.87 of a copy's rate; 32,768 rows read back (202 MB) in 34.8 us, 5.8
+// TB/s, 0.86; 16,384 blocks of 8 heads copied (1.08 GB) in 171 us, 0.93, 4096 of 32
+// heads in 160, 1.00.  A step's few tokens take the launch, 3.5 us of GPU time.
 #include <algorithm>
 
 #include "cb_fp8.cuh"

@@ -41,14 +41,14 @@
 // code shares one instruction cache), 12 issues the products, 13 loads K, 15 V and
 // the exponents, 14 walks the work and publishes it.  Every wait is bounded.
 //
-// Bound by the tensor pipe and the softmax in turn: 2048 new tokens after 30720
-// keys (32 heads on 8) take 905 us, 1.18 PFLOP/s, 0.61 of cuBLAS's bf16 rate; one
-// thread issues the products, every wait of its warp between them is idle time of
-// the pipe (a second issuing warp was slower), and an item's start and end cost
-// about 8 us.  Single tokens (below): 256 requests of 32 heads on 1 KV head (1024
-// to 16384 keys, 539 MB) take 157 us, 3.4 TB/s, 0.51 of a copy's rate: a tile's
-// conversion, whose shared-memory accesses compete with the products' operands, is
-// the longest part of its chain.
+// Bound by a tile's chain, not by a unit: 2048 new tokens after 30720 keys (32 heads
+// on 8) take 915 us, 1.16 PFLOP/s, 0.61 of cuBLAS's bf16 rate, with the tensor pipe
+// active half of the time; S of a query tile overwrites the columns of its P, so its
+// softmax, PV and S follow one another and only the other query tile's hide them.  An
+// item's start and end cost about 8 us.  Single tokens (below): 256 requests of 32
+// heads on 1 KV head (1024 to 16384 keys, 539 MB) take 159 us, 3.4 TB/s, 0.50 of a
+// copy's rate: a tile's conversion, whose shared-memory accesses compete with the
+// products' operands, is the longest part of its chain.
 #include <algorithm>
 
 #include "cb_decode_item.cuh"
@@ -64,7 +64,7 @@ constexpr int kRows = kChunkRows;      // rows of an item (two query tiles)
 // start and end (its queries, first scores and output) are kLead empty places: cut by
 // tiles alone, a range of short items takes as many starts and ends.  With 0, 2, 4 and
 // 6 of them 2048 tokens without stored keys, cut, took 180, 99, 89 and 88 us, 8192 of
-// them 1037, 730, 604 and 579, 512 after 4096 keys 76, 73, 71 and 72; 256 single tokens
+// them 1037, 730, 604 and 579 (592 whole), 512 after 4096 keys 76, 73, 71 and 72; 256 single tokens
 // of 32 heads on 1 with 0, 2 and 4 of them 164, 161 and 162.
 // kJoinTiles is how much sooner the cut ranges must end than whole items: 512 tokens
 // after 2048 keys (10 tiles sooner) take 67 us whole and 56 cut, 2048 after 2048 (12)
