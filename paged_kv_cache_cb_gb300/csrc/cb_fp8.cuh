@@ -61,6 +61,15 @@ __device__ __forceinline__ uint32_t pack_rest(uint32_t w, float lo, float hi) {
   return pack_e4m3(lo, hi);
 }
 
+// A query row of largest |bits| amax as two e4m3 terms of q 2^-e: the exponent byte e +
+// 127 that brings its largest value into [128, 256), and the terms of two values (lo: of
+// what hi leaves of them).  Rows that are not finite are the caller's.
+__device__ __forceinline__ uint32_t query_exp(uint32_t amax) { return (uint32_t)max(1, (int)(amax >> 7) - 7); }
+__device__ __forceinline__ void query_terms(float y0, float y1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_e4m3(y0, y1);
+  lo = pack_rest(hi, y0, y1);
+}
+
 // e4m3 -> bf16 times 2^e.  Each byte is sign-extended to 16 bits and moved
 // up by 4: sign, zeros, the 4 exponent and 3 fraction bits in bf16's places, a
 // bf16 2^-120 times too small (also for e4m3's subnormals, which become bf16's);

@@ -449,7 +449,7 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
     m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu), __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
   m = max(m & 0xFFFFu, m >> 16);
   const bool bad = m >= 0x7F80u;
-  const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);   // largest value in [128, 256)
+  const uint32_t eb = query_exp(m);
   const float factor = bad ? __uint_as_float(0x7FC00000u) : finite(fmaxf(P.scale_log2 * __uint_as_float(eb << 23), 1.4e-45f));
   if (!ready()) return factor;
   const float f = exp_inverse(bad ? 1u : eb);
@@ -460,8 +460,8 @@ __device__ float make_query(const Fp8Step& P, Smem<A>& S, int side, int row, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float y0 = bad ? 0.f : bf16lo(w[i]) * f, y1 = bad ? 0.f : bf16hi(w[i]) * f;
-      const uint32_t hi = pack_e4m3(y0, y1);
-      const uint32_t lo = pack_rest(hi, y0, y1);
+      uint32_t hi, lo;
+      query_terms(y0, y1, hi, lo);
       t0[i / 2] = (i & 1) ? t0[i / 2] | (hi << 16) : hi;
       t1[i / 2] = (i & 1) ? t1[i / 2] | (lo << 16) : lo;
     }

@@ -462,17 +462,18 @@ __device__ void load_query(const Fp8Step& P, Smem<A, G>& S, const Seg& s, int bu
       for (int d = 1; d < D / 2; ++d) m = __vmaxu2(m, w[u][d] & 0x7FFF7FFFu);
       m = max(m & 0xFFFFu, m >> 16);
       m = __reduce_max_sync(0xffffffffu, m);
-      // the row's power of two: largest value in [128, 256); not finite: zeros and a NaN factor
+      // not finite: zeros and a NaN factor
       const bool bad = m >= 0x7F80u;
-      const uint32_t eb = (uint32_t)max(1, (int)(m >> 7) - 7);
+      const uint32_t eb = query_exp(m);
       const float f = bad ? 0.f : exp_inverse(eb);
       uint32_t c0 = 0, c1 = 0;
 #pragma unroll
       for (int d = 0; d < D / 2; ++d) {
         const float y0 = bad ? 0.f : bf16lo(w[u][d]) * f, y1 = bad ? 0.f : bf16hi(w[u][d]) * f;
-        const uint32_t a = pack_e4m3(y0, y1);
-        c0 |= a << (16 * d);
-        c1 |= pack_rest(a, y0, y1) << (16 * d);
+        uint32_t hi, lo;
+        query_terms(y0, y1, hi, lo);
+        c0 |= hi << (16 * d);
+        c1 |= lo << (16 * d);
       }
       const int hh = h / G, g = h - hh * G;
       for (int bi = 0; bi < bpt; ++bi) {
