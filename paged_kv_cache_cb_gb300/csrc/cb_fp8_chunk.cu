@@ -64,12 +64,14 @@ constexpr int kRows = kChunkRows;      // rows of an item (two query tiles)
 // start and end (its queries, first scores and output) are kLead empty places: cut by
 // tiles alone, a range of short items takes as many starts and ends.  With 0, 2, 4 and
 // 6 of them 2048 tokens without stored keys, cut, took 180, 99, 89 and 88 us, 8192 of
-// them 1037, 730, 604 and 579 (592 whole), 512 after 4096 keys 76, 73, 71 and 72; 256 single tokens
-// of 32 heads on 1 with 0, 2 and 4 of them 164, 161 and 162.
+// them 1037, 730, 604 and 579 (592 whole), 512 after 4096 keys 76, 73, 71 and 72; 256
+// single tokens of 32 heads on 1 with 0, 2 and 4 of them 164, 161 and 162.
 // kJoinTiles is how much sooner the cut ranges must end than whole items: 512 tokens
 // after 2048 keys (10 tiles sooner) take 67 us whole and 56 cut, 2048 after 2048 (12)
 // 147 and 142, but 2048 without stored keys of 64 heads on 8 (9) 127 and 143, next to
-// 48 single tokens 235 and 257; at 5 to 8 either may be 3 us shorter.
+// 48 single tokens 235 and 257.  At 5 to 8 either may be shorter: next to 48 single
+// tokens 512 after 1024 and 2048, 64 heads on 8 (6) 205 and 225, 256 after 1000 (7) 128
+// and 121.
 template <bool ONE>
 constexpr int kLead = ONE ? 2 : kChunkLead;
 constexpr int kJoinTiles = 9;
