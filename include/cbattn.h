@@ -68,6 +68,7 @@ extern "C" {
 #define CB_ESTATE (-6)     /* scheduler: bad request id / state, or capacity exceeded */
 
 #define CB_MAX_REQS 2048
+#define CB_MAX_CACHE_BUFFERS 8
 
 /* ---------------------------------------------------------------- KV append
  * [CB] Chunked prefill ("store the KV states") and [SM] PagedAttention (new
@@ -301,6 +302,95 @@ int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const
                                      float scale, int n_q_heads, int n_kv_heads, int head_dim, int block_size,
                                      int window, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- block pool on the device
+ * The pages' scheduler takes and frees blocks on the host ([SM] PagedAttention:
+ * a block is taken only when the request's last block is full; [KVB] 思想:
+ * sequences share blocks through their block tables, as in beam search).  Which
+ * beam goes on from which, or how many drafted tokens stand, is known on the
+ * device first; these calls do the same work there, so that a decoding loop
+ * needs no synchronisation and can be recorded as a graph.
+ *
+ * State, all device int32 and the caller's (4-byte aligned):
+ *  block_tables [n_rows][max_blocks_per_seq]; row r holds its first
+ *             ceil(lens[r] / block_size) entries.  Entries < 0 among them name
+ *             no block (a rolling window let go of it)
+ *  lens       [n_rows] stored tokens, 0 .. max_blocks_per_seq * block_size
+ *  refs       [num_blocks] holders of each block: the table entries that name
+ *             it, and whoever else holds it (a kept prefix: the caller adds 1
+ *             for it).  0: free
+ * Free blocks are taken from the lowest id on, in row order: the result of a
+ * call depends on nothing else.  n_rows <= CB_MAX_REQS, block_size 16, fewer than
+ * 2^31 table entries; n_rows 0 does nothing (cb_compact_blocks still compacts).
+ * workspace: device, cb_block_ops_workspace_size(...) bytes, 16-byte aligned, no
+ * initialisation; calls that may overlap need their own.  The arguments do not
+ * overlap in memory.
+ * Errors: CB_EINVAL, CB_EWORKSPACE, CB_ECUDA; found by the kernels, and
+ * reported by cb_last_error: CB_EDEVICE for lengths and block ids out of range
+ * (lengths count as the nearest one in range, ids name no block), CB_ESTATE for
+ * a pool without a free block that a row needs. */
+size_t cb_block_ops_workspace_size(int n_rows, int max_blocks_per_seq, int num_blocks, int block_size);
+
+/* Fork, reorder, cut and free rows: every row j becomes the first keep_lens[j]
+ * tokens of what row parents[j] was before the call (beam search: its beam's
+ * parent; parents[j] = j: the row itself).
+ *  parents    device, int32 [n_rows]; < 0 frees row j (length 0); >= n_rows does
+ *             too and is reported
+ *  keep_lens  device, int32 [n_rows], or NULL; < 0, or more than the parent
+ *             holds: all of it
+ *  pairs      device, int32 [n_rows][2], written: the block copies (src, dst)
+ *             that the rows need, (-1, -1) for a row that needs none -- run
+ *             cb_copy_blocks_layers on them before the next append
+ * Whole blocks are shared.  A partial last block is not: of the rows that end in
+ * it the lowest keeps it, if nothing else holds it; each of the others gets a
+ * free block and a copy.  With no free block left, a row ends at its last whole
+ * block (lens says so; CB_ESTATE).  Entries that a row no longer uses become -1. */
+int cb_fork_blocks(const int32_t* parents, const int32_t* keep_lens, int32_t* block_tables, int max_blocks_per_seq,
+                   int n_rows, int32_t* lens, int32_t* refs, int num_blocks, int block_size, int32_t* pairs,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* Room for new tokens, and the step's metadata: row i stores cu_q_lens[i + 1] -
+ * cu_q_lens[i] tokens more (the device counterpart of the scheduler's allocation
+ * and of cb_build_slot_mapping).
+ *  cu_q_lens  device, int32 [n_rows + 1], as for cb_paged_attention
+ *  ctx_lens   device, int32 [n_rows], written: the lengths before the call
+ *  slot_mapping device, int64 [n_tokens], written: token t's slot; -1 for the
+ *             tokens from cu_q_lens[n_rows] on (a padded batch)
+ * lens grows.  A row gets all the blocks that it needs or none: once the rows
+ * before it and itself need more than are free, its length stays, its tokens'
+ * slots are -1 and the call is reported (CB_ESTATE); rows that need no new block
+ * grow all the same.  A row that would outgrow its table, or whose lengths are
+ * out of range, stays too (CB_EDEVICE).  The last, partial block of a row is
+ * written by no other row (as cb_fork_blocks leaves it). */
+int cb_grow_blocks(const int32_t* cu_q_lens, int32_t* block_tables, int max_blocks_per_seq, int n_rows, int32_t* lens,
+                   int32_t* refs, int num_blocks, int block_size, int32_t* ctx_lens, int64_t* slot_mapping,
+                   int n_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Live blocks (refs > 0) move to the pool's lowest ids: with L of them, the k-th
+ * lowest of those from id L on moves to the k-th lowest free id below L.
+ *  block_map  device, int32 [num_blocks], written: each block's id after the call,
+ *             -1 for a free one (for tables that the call does not see)
+ *  pairs      device, int32 [max_pairs][2], written: the moves (src, dst), then
+ *             (-1, -1) -- run cb_copy_blocks_layers on them before the caches are
+ *             used again.  Moves past max_pairs are left to the next call
+ *             (num_blocks / 2 hold all)
+ *  counts     device, int32 [2], written: live blocks, moves
+ * Tables and refs follow the moves. */
+int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows, int32_t* lens, int32_t* refs,
+                      int num_blocks, int block_size, int32_t* block_map, int32_t* pairs, int max_pairs, int32_t* counts,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* cb_copy_blocks in every layer at once, for either kind of cache.
+ *  pairs      device, int32 [n_pairs][2] (src, dst); src < 0 skips the pair.  The
+ *             dsts are distinct and none is a src of another pair
+ *  caches     host, n_caches device pointers (1 .. CB_MAX_CACHE_BUFFERS), each to
+ *             [n_layers][num_blocks] blocks, 16-byte aligned: K and V, and the
+ *             exponents of an 8-bit cache
+ *  block_bytes host, n_caches: bytes of a block, a multiple of 16
+ * Bit-exact.  A pair with an id out of range is skipped and reported
+ * (CB_EDEVICE).  Errors: CB_EINVAL, CB_ECUDA. */
+int cb_copy_blocks_layers(const int32_t* pairs, int n_pairs, void* const* caches, const size_t* block_bytes, int n_caches,
+                          int n_layers, int num_blocks, void* stream);
+
 /* ---------------------------------------------------------------- no-allocation variant
  * The pages have no counterpart: this exists for callers that cannot allocate
  * device memory when they run a step -- hosts whose device memory is owned by
@@ -343,7 +433,8 @@ int cb_paged_attention_noalloc(const void* q, const int32_t* cu_q_lens, const in
 /* Synchronise `stream`, then read and clear that stream's error word: the bad
  * metadata or timeouts reported by kernels this library launched on `stream`
  * (never another stream's).
- * Returns CB_OK, CB_EDEVICE, CB_ETIMEOUT or CB_ECUDA. */
+ * Returns CB_OK, CB_EDEVICE, CB_ETIMEOUT, CB_ESTATE (a pool ran out of free
+ * blocks, and nothing else is to be reported) or CB_ECUDA. */
 int cb_last_error(void* stream);
 
 /* Static description of an error code (never NULL). */

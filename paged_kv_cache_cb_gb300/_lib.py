@@ -48,6 +48,14 @@ SIGNATURES = [
     ("cb_kv_append_paged_attention_fp8", _c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                                   _c_int, _vp, _vp, _vp, _vp, _c_int, _vp, _c_float, _c_int, _c_int,
                                                   _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    ("cb_block_ops_workspace_size", _c_size, [_c_int] * 4),
+    ("cb_fork_blocks", _c_int, [_vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_size, _vp]),
+    ("cb_grow_blocks", _c_int, [_vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_size,
+                                _vp]),
+    ("cb_compact_blocks", _c_int, [_vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _c_size,
+                                   _vp]),
+    ("cb_copy_blocks_layers", _c_int, [_vp, _c_int, ctypes.POINTER(_vp), ctypes.POINTER(_c_size), _c_int, _c_int,
+                                       _c_int, _vp]),
     ("cb_paged_attention_noalloc", _c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp,
                                             _c_int, _vp, _c_float, _c_int, _c_int, _c_int, _c_int, _vp]),
     ("cb_last_error", _c_int, [_vp]),
@@ -450,6 +458,95 @@ def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_c
         _check(name, lib().cb_kv_append_paged_attention_fp8(pk, pv, ps, *args))
         return
     _check(name, lib().cb_paged_attention_fp8(*args))
+
+
+# ---------------------------------------------------------------- block pool on the device
+_BLOCK = 16
+
+
+def cb_block_ops_workspace_size(n_rows, max_blocks_per_seq, num_blocks, block_size=_BLOCK):
+    _fit_int(n_rows, max_blocks_per_seq, num_blocks, block_size)
+    return int(lib().cb_block_ops_workspace_size(n_rows, max_blocks_per_seq, num_blocks, block_size))
+
+
+def _pool(c, dev, block_tables, lens, refs, workspace):
+    """Pointers of a pool's tables [n_rows, max_blocks], lengths [n_rows], counts [num_blocks] and a workspace, and
+    the sizes."""
+    ptrs = (_on(dev, block_tables, c.i32, "block_tables", 2), _on(dev, lens, c.i32, "lens", 1),
+            _on(dev, refs, c.i32, "refs", 1), _on(dev, workspace, c.u8, "workspace", 1))
+    shape = block_tables.shape
+    if len(shape) != 2 or lens.shape != shape[:1] or refs.dim() != 1 or workspace.dim() != 1:
+        raise ValueError("shape mismatch")
+    return ptrs, shape[0], shape[1], refs.shape[0]
+
+
+def cb_fork_blocks(parents, keep_lens, block_tables, lens, refs, pairs, workspace, stream=None):
+    """Row j of block_tables (int32 [n_rows, max_blocks]) and lens (int32 [n_rows]) becomes the first keep_lens[j]
+    tokens of what row parents[j] was (parents int32 [n_rows], < 0: the row is freed; keep_lens int32 [n_rows] or
+    None, < 0: all).  refs: int32 [num_blocks], every block's holders.  pairs: int32 [n_rows, 2], written: the block
+    copies (src, dst) that the rows need, -1 for none; run cb_copy_blocks_layers on them.  workspace: uint8 CUDA
+    tensor of at least cb_block_ops_workspace_size bytes."""
+    c = _tc()
+    dev = _current_device(c, parents)
+    pp = _on(dev, parents, c.i32, "parents", 1)
+    pk = None if keep_lens is None else _on(dev, keep_lens, c.i32, "keep_lens", 1)
+    px = _on(dev, pairs, c.i32, "pairs", 2)
+    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    if parents.shape != (n,) or (pk is not None and keep_lens.shape != (n,)) or pairs.shape != (n, 2):
+        raise ValueError("shape mismatch")
+    _check("cb_fork_blocks", lib().cb_fork_blocks(pp, pk, pt, width, n, pl, pr, nb, _BLOCK, px, pw, workspace.shape[0],
+                                                  _raw_stream(c, dev, stream)))
+
+
+def cb_grow_blocks(cu_q_lens, block_tables, lens, refs, ctx_lens, slot_mapping, workspace, stream=None):
+    """Row i gets room for cu_q_lens[i + 1] - cu_q_lens[i] new tokens (int32 [n_rows + 1]): its table gets the lowest
+    free blocks, lens grows; ctx_lens (int32 [n_rows]) and slot_mapping (int64 [n_tokens], -1 past the last row's
+    tokens) are written, as the append and attention calls take them.  The pool as for cb_fork_blocks."""
+    c = _tc()
+    dev = _current_device(c, cu_q_lens)
+    pc = _on(dev, cu_q_lens, c.i32, "cu_q_lens", 1)
+    px = _on(dev, ctx_lens, c.i32, "ctx_lens", 1)
+    ps = _on(dev, slot_mapping, c.i64, "slot_mapping", 1)
+    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    if cu_q_lens.shape != (n + 1,) or ctx_lens.shape != (n,) or slot_mapping.dim() != 1:
+        raise ValueError("shape mismatch")
+    _check("cb_grow_blocks", lib().cb_grow_blocks(pc, pt, width, n, pl, pr, nb, _BLOCK, px, ps, slot_mapping.shape[0],
+                                                  pw, workspace.shape[0], _raw_stream(c, dev, stream)))
+
+
+def cb_compact_blocks(block_tables, lens, refs, block_map, pairs, counts, workspace, stream=None):
+    """Live blocks move to the pool's lowest ids; tables and refs follow.  Written: block_map (int32 [num_blocks],
+    each block's new id, -1: free), pairs (int32 [max_pairs, 2], the moves, then -1; run cb_copy_blocks_layers on
+    them), counts (int32 [2]: live blocks, moves).  The pool as for cb_fork_blocks."""
+    c = _tc()
+    dev = _current_device(c, block_tables)
+    pm = _on(dev, block_map, c.i32, "block_map", 1)
+    px = _on(dev, pairs, c.i32, "pairs", 2)
+    pc = _on(dev, counts, c.i32, "counts", 1)
+    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    if block_map.shape != (nb,) or pairs.dim() != 2 or pairs.shape[1] != 2 or counts.shape != (2,):
+        raise ValueError("shape mismatch")
+    _check("cb_compact_blocks", lib().cb_compact_blocks(pt, width, n, pl, pr, nb, _BLOCK, pm, px, pairs.shape[0], pc, pw,
+                                                        workspace.shape[0], _raw_stream(c, dev, stream)))
+
+
+def cb_copy_blocks_layers(pairs, caches, stream=None):
+    """Block dst becomes block src for every (src, dst) of pairs (int32 [n, 2], src < 0: none) in every layer of every
+    tensor of caches: contiguous CUDA tensors [n_layers, num_blocks, ...] of any type, the same two sizes in all."""
+    c = _tc()
+    dev = _current_device(c, pairs)
+    pp = _on(dev, pairs, c.i32, "pairs", 2)
+    n = len(caches)
+    if pairs.dim() != 2 or pairs.shape[1] != 2 or not n:
+        raise ValueError("shape mismatch")
+    ptrs, sizes, first = (_vp * n)(), (_c_size * n)(), caches[0].shape[:2]
+    for i, t in enumerate(caches):
+        ptrs[i] = _on(dev, t, t.dtype, "caches", None)
+        if t.dim() < 3 or t.shape[:2] != first or t.numel() == 0:
+            raise ValueError("caches must be [n_layers, num_blocks, ...] of the same two sizes")
+        sizes[i] = t.numel() // (first[0] * first[1]) * t.element_size()
+    _check("cb_copy_blocks_layers", lib().cb_copy_blocks_layers(pp, pairs.shape[0], ptrs, sizes, n, first[0], first[1],
+                                                                _raw_stream(c, dev, stream)))
 
 
 CB_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024

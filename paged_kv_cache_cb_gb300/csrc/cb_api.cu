@@ -527,7 +527,8 @@ int cb_last_error(void* stream) {
     if (cudaMemcpy(&slot->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return CB_ECUDA;
   }
   if (bits & CB_DEVERR_TIMEOUT) return CB_ETIMEOUT;
-  if (bits) return CB_EDEVICE;
+  if (bits & ~CB_DEVERR_NOBLOCK) return CB_EDEVICE;
+  if (bits) return CB_ESTATE;
   return CB_OK;
 }
 

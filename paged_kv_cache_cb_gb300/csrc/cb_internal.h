@@ -13,6 +13,7 @@ constexpr unsigned CB_DEVERR_TIMEOUT = 1u;   // a bounded mbarrier wait ran out
 constexpr unsigned CB_DEVERR_BADBLOCK = 2u;  // block-table entry outside [0, num_blocks)
 constexpr unsigned CB_DEVERR_BADSLOT = 4u;   // slot outside the cache
 constexpr unsigned CB_DEVERR_BADLEN = 8u;    // lengths inconsistent with the table / launch
+constexpr unsigned CB_DEVERR_NOBLOCK = 16u;  // no free block left in the pool
 
 // Longest a kernel waits on one mbarrier phase before giving up (wall clock).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;

@@ -1,0 +1,140 @@
+"""The block pool without a GPU: the oracle pinned by hand, and what the entry
+points refuse before anything is enqueued."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import blocks as ob
+
+
+def _lib():
+    from paged_kv_cache_cb_gb300 import _lib as L
+    if not os.path.exists(L.LIB_PATH):
+        from paged_kv_cache_cb_gb300 import build
+        build.build()
+    return L
+
+
+# ------------------------------------------------------------------ the oracle
+def _pool(rows, num_blocks, width=6):
+    """Rows as (length, blocks)."""
+    tables = np.full((len(rows), width), -1, np.int64)
+    refs = np.zeros(num_blocks, np.int64)
+    for r, (n, blocks) in enumerate(rows):
+        tables[r, :len(blocks)] = blocks
+        for b in blocks:
+            refs[b] += 1
+    return tables, np.array([n for n, _ in rows], np.int64), refs
+
+
+def test_fork_worked_by_hand():
+    # two beams of one prompt: block 4 shared, 7 and 2 their own partial ones
+    tables, lens, refs = _pool([(20, [4, 7]), (20, [4, 2])], 9)
+    pairs, cut = ob.fork([1, 1], None, tables, lens, refs)
+    assert tables[:, :2].tolist() == [[4, 2], [4, 0]]        # row 0 keeps block 2, row 1 has a copy in the lowest free
+    assert pairs.tolist() == [[-1, -1], [2, 0]] and not cut
+    assert refs[[0, 2, 4, 7]].tolist() == [1, 1, 2, 0]
+    # a prefix of a row that goes on: the row itself keeps what it will write
+    tables, lens, refs = _pool([(40, [1, 2, 3]), (0, [])], 5)
+    pairs, cut = ob.fork([0, 0], [-1, 18], tables, lens, refs)
+    assert tables[1, :2].tolist() == [1, 0] and pairs.tolist() == [[-1, -1], [2, 0]]   # block 2 is whole in row 0
+    # freed, and cut to whole blocks where no block is left for the copy
+    tables, lens, refs = _pool([(20, [0, 1]), (0, [])], 2)
+    pairs, cut = ob.fork([0, 0], None, tables, lens, refs)
+    assert cut == [1] and lens.tolist() == [20, 16] and refs.tolist() == [2, 1]
+    assert tables[1, :2].tolist() == [0, -1]
+    ob.fork([-1, -1], None, tables, lens, refs)
+    assert lens.tolist() == [0, 0] and not refs.any() and (tables == -1).all()
+
+
+def test_grow_worked_by_hand():
+    tables, lens, refs = _pool([(15, [3]), (16, [1]), (0, [])], 6)
+    ctx, slots, stay = ob.grow([1, 1, 17], tables, lens, refs)
+    assert lens.tolist() == [16, 17, 17] and ctx.tolist() == [15, 16, 0] and not stay
+    assert tables[1, 1] == 0 and tables[2, :2].tolist() == [2, 4]
+    assert slots.tolist() == [3 * 16 + 15, 0] + [2 * 16 + i for i in range(16)] + [64]
+    ctx, slots, stay = ob.grow([16, 1, 2], tables, lens, refs)      # one block left: row 0 takes it
+    assert stay == [] and tables[0, 1] == 5
+    ctx, slots, stay = ob.grow([1, 1, 1], tables, lens, refs)       # none left: row 0 stays
+    assert stay == [0] and slots.tolist() == [-1, 2, 4 * 16 + 3]
+
+
+def test_compact_worked_by_hand():
+    tables, lens, refs = _pool([(30, [5, 0]), (20, [5, 6])], 8)
+    block_map, moves, live = ob.compact(tables, lens, refs)
+    assert live == 3 and moves.tolist() == [[5, 1], [6, 2]]
+    assert tables[:, :2].tolist() == [[1, 0], [1, 2]] and refs.tolist() == [1, 2, 1, 0, 0, 0, 0, 0]
+    assert block_map.tolist() == [0, -1, -1, -1, -1, 1, 2, -1]
+
+
+# ------------------------------------------------------------------ refusals of the C ABI
+D = ctypes.c_void_p(4096)
+ODD = ctypes.c_void_p(4098)
+
+
+def test_pool_arguments():
+    L = _lib().lib()
+
+    def fork(pa=D, ke=None, bt=D, w=4, n=2, ln=D, rf=D, nb=8, bs=16, pr=D, ws=D, wsb=1 << 20):
+        return L.cb_fork_blocks(pa, ke, bt, w, n, ln, rf, nb, bs, pr, ws, wsb, None)
+
+    def grow(pa=D, bt=D, w=4, n=2, ln=D, rf=D, nb=8, bs=16, ctx=D, sl=D, nt=3, ws=D, wsb=1 << 20):
+        return L.cb_grow_blocks(pa, bt, w, n, ln, rf, nb, bs, ctx, sl, nt, ws, wsb, None)
+
+    def compact(bt=D, w=4, n=2, ln=D, rf=D, nb=8, bs=16, mp=D, pr=D, m=4, ct=D, ws=D, wsb=1 << 20):
+        return L.cb_compact_blocks(bt, w, n, ln, rf, nb, bs, mp, pr, m, ct, ws, wsb, None)
+
+    for f in (fork, grow):
+        assert f(n=0) == 0
+        assert f(pa=None) == -1 and f(pa=ODD) == -1
+    for f in (fork, grow, compact):
+        for bad in (dict(n=-1), dict(n=2049), dict(w=0), dict(nb=0), dict(bs=32), dict(bt=None), dict(ln=None), dict(rf=None),
+                    dict(bt=ODD), dict(ln=ODD), dict(rf=ODD), dict(ws=None), dict(ws=ctypes.c_void_p(4100)),
+                    dict(w=1 << 30), dict(w=1 << 27, n=1)):
+            assert f(**bad) == -1, (f.__name__, bad)
+    assert fork(pr=None) == -1 and fork(pr=ODD) == -1 and fork(ke=ODD) == -1 and fork(wsb=8) == -3
+    assert grow(ctx=None) == -1 and grow(sl=None) == -1 and grow(sl=ctypes.c_void_p(4100)) == -1 and grow(nt=-1) == -1
+    assert grow(wsb=8) == -3
+    assert compact(mp=None) == -1 and compact(pr=None) == -1 and compact(m=-1) == -1 and compact(ct=None) == -1
+    assert compact(pr=ODD) == -1 and compact(wsb=8) == -3
+
+
+def test_workspace_size():
+    L = _lib()
+    f = L.cb_block_ops_workspace_size
+    assert f(-1, 4, 8) == 0 and f(2049, 4, 8) == 0 and f(4, 0, 8) == 0 and f(4, 4, 0) == 0 and f(4, 4, 8, 32) == 0
+    assert f(0, 4, 8) > 0
+    assert f(2048, 100, 8) >= 2048 * 100 * 4 and f(1, 1, 1 << 20) >= (1 << 20) * 4
+    with pytest.raises(ValueError):
+        f(1 << 33, 4, 8)
+
+
+def test_copy_arguments():
+    L = _lib().lib()
+
+    def copy(p=D, n=1, ptrs=(4096, 8192), sizes=(64, 16), k=None, layers=2, nb=8):
+        a, b = (ctypes.c_void_p * len(ptrs))(*ptrs), (ctypes.c_size_t * len(sizes))(*sizes)
+        return L.cb_copy_blocks_layers(p, n, a, b, len(ptrs) if k is None else k, layers, nb, None)
+
+    assert copy(n=0) == 0
+    for bad in (dict(n=-1), dict(k=0), dict(k=9), dict(layers=0), dict(nb=0), dict(ptrs=(None, 4096)), dict(ptrs=(4100, 8192)),
+                dict(sizes=(24, 16)), dict(sizes=(64, 0)), dict(p=None), dict(p=ODD), dict(sizes=(1 << 30, 16))):
+        assert copy(**bad) == -1, bad
+    assert L.cb_copy_blocks_layers(D, 1, None, None, 1, 1, 1, None) == -1
+
+
+def test_binding_refuses_host_tensors():
+    L = _lib()
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        L.cb_fork_blocks(i(2), None, i(2, 4), i(2), i(8), i(2, 2), ws)
+    with pytest.raises(ValueError):
+        L.cb_grow_blocks(i(3), i(2, 4), i(2), i(8), i(2), torch.zeros(3, dtype=torch.int64), ws)
+    with pytest.raises(ValueError):
+        L.cb_compact_blocks(i(2, 4), i(2), i(8), i(8), i(4, 2), i(2), ws)
+    with pytest.raises(ValueError):
+        L.cb_copy_blocks_layers(i(1, 2), [torch.zeros(1, 8, 16)])
