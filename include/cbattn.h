@@ -42,7 +42,8 @@
  *  - Per-stream state: the library keeps, in its own device memory, one slot
  *    per (device, stream) used -- an error word that the kernels launched on
  *    that stream report bad metadata or timeouts into (read and cleared by
- *    cb_last_error(stream)), and the block-tile launches' work counters.  Slots
+ *    cb_last_error(stream)), and the block-tile and cross attention launches' work
+ *    counters.  Slots
  *    are handed out in order of first use, at most 4096 per device; a call on a
  *    further stream returns CB_ESTATE.  The first call on a device looks up the
  *    slots' device address (cudaGetSymbolAddress): make it before any stream
@@ -217,6 +218,45 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
                                         void* out, float scale, int n_q_heads, int n_kv_heads, int head_dim,
                                         int block_size, int window, void* workspace, size_t workspace_bytes,
                                         void* stream);
+
+/* ---------------------------------------------------------------- cross attention
+ * [CB] Attention with Q [nQ, A] and K, V [nK, A] of another length and no mask:
+ * the new tokens of request r attend to all of its stored keys -- an encoder's
+ * states, written once with cb_kv_append --
+ *     out[t][h] = softmax_j(scale * q[t][h] . K[j]) . V[j],   0 <= j < kv_lens[r],
+ * in the layouts of cb_paged_attention.  A request's tokens see the same keys:
+ * they may be a prompt's, one decoding step's, or one token of each beam.
+ *  q, out     device, bf16 [n_tokens][n_q_heads][head_dim]
+ *  cu_q_lens  device, int32 [n_reqs + 1], as for cb_paged_attention; a request may
+ *             have no token
+ *  kv_lens    device, int32 [n_reqs], >= 0.  Tokens of a request without keys get
+ *             zeros
+ *  block_tables device, int32 [n_reqs][max_blocks_per_seq]; entries past
+ *             ceil(kv_lens[r] / block_size) are never read
+ *  max_q_len, max_kv_len  host int, >= every request's tokens (>= 1) and keys
+ *             (0 .. 2^30)
+ *  workspace  device, cb_paged_cross_attention_workspace_size(...) bytes, 16-byte
+ *             aligned, no initialisation
+ * Shapes: head_dim 64 or 128; n_q_heads / n_kv_heads 1, 2, 4, 8, 16 or 32, with any
+ * number of KV heads.  One cooperative kernel launch (CB_ECUDA if the device
+ * cannot hold one CTA per SM at once); its counters are the stream's (see
+ * "Per-stream state": calls that overlap must come from different streams).  Rows
+ * of out that belong to no request are left as they were.
+ * Precision: scores, softmax statistics and sums are fp32; a weight is rounded to
+ * bf16 before it multiplies v.
+ * Errors: those of cb_paged_attention; steps whose work could pass 2^30 units (2
+ * max_kv_len / 128 + 1 for every KV head and 256 n_kv_heads / n_q_heads tokens) are
+ * refused with CB_EINVAL.  A request whose lengths are out of range is reported
+ * and its rows stay as they were; the rows of a bad block id count as zeros. */
+int cb_paged_cross_attention(const void* q, const int32_t* cu_q_lens, const int32_t* kv_lens, const int32_t* block_tables,
+                             int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len, int max_kv_len,
+                             const void* k_cache, const void* v_cache, int num_blocks, void* out, float scale,
+                             int n_q_heads, int n_kv_heads, int head_dim, int block_size, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace for these sizes (0 on invalid sizes).  Pure host function. */
+size_t cb_paged_cross_attention_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
+                                               int n_kv_heads, int head_dim, int block_size);
 
 /* ---------------------------------------------------------------- 8-bit cache
  * The same step over a cache of half the bytes: K and V rows are quantised as

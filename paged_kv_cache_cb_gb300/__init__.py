@@ -11,7 +11,7 @@ from ._lib import (CB_EDEVICE, CB_EINVAL, CB_ESTATE, CB_ETIMEOUT, CB_EWORKSPACE,
                    cb_kv_append_paged_attention_window, cb_kv_gather_fp8, cb_last_error, cb_last_launch_count,
                    cb_paged_attention, cb_paged_attention_fp8, cb_paged_attention_fp8_workspace_size,
                    cb_paged_attention_noalloc, cb_paged_attention_window, cb_paged_attention_workspace_size,
-                   cb_strerror, lib)
+                   cb_paged_cross_attention, cb_paged_cross_attention_workspace_size, cb_strerror, lib)
 
 __all__ = [
     "CB_OK", "CB_EINVAL", "CB_EWORKSPACE", "CB_EDEVICE", "CB_ESTATE", "CB_ETIMEOUT", "CB_MAX_REQS", "CBError", "Graph",
@@ -20,6 +20,6 @@ __all__ = [
     "cb_kv_append_fp8", "cb_kv_append_paged_attention", "cb_kv_append_paged_attention_fp8",
     "cb_kv_append_paged_attention_window", "cb_kv_gather_fp8", "cb_last_error", "cb_last_launch_count",
     "cb_paged_attention", "cb_paged_attention_fp8", "cb_paged_attention_fp8_workspace_size",
-    "cb_paged_attention_noalloc", "cb_paged_attention_window", "cb_paged_attention_workspace_size", "cb_strerror",
-    "lib",
+    "cb_paged_attention_noalloc", "cb_paged_attention_window", "cb_paged_attention_workspace_size",
+    "cb_paged_cross_attention", "cb_paged_cross_attention_workspace_size", "cb_strerror", "lib",
 ]

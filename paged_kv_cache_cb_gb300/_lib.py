@@ -38,6 +38,9 @@ SIGNATURES = [
     ("cb_kv_append_paged_attention_window", _c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                                      _c_int, _c_int, _vp, _vp, _c_int, _vp, _c_float, _c_int,
                                                      _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    ("cb_paged_cross_attention", _c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_int,
+                                          _vp, _c_float, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    ("cb_paged_cross_attention_workspace_size", _c_size, [_c_int] * 8),
     ("cb_kv_append_fp8", _c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
     ("cb_kv_gather_fp8", _c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _vp]),
     ("cb_copy_blocks_fp8", _c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
@@ -458,6 +461,48 @@ def _attention_fp8(name, new, q, cu_q_lens, ctx_lens, block_tables, k_cache, v_c
         _check(name, lib().cb_kv_append_paged_attention_fp8(pk, pv, ps, *args))
         return
     _check(name, lib().cb_paged_attention_fp8(*args))
+
+
+# ---------------------------------------------------------------- cross attention
+def cb_paged_cross_attention_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim,
+                                            block_size):
+    sizes = (n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads, n_kv_heads, head_dim, block_size)
+    _fit_int(*sizes)
+    return int(lib().cb_paged_cross_attention_workspace_size(*sizes))
+
+
+def cb_paged_cross_attention(q, cu_q_lens, kv_lens, block_tables, k_cache, v_cache, out, scale, workspace, max_q_len,
+                             max_kv_len, stream=None):
+    """Every new token of request r attends to all of its kv_lens[r] stored keys (no causal mask).  q, out: bf16
+    [n_tokens, Hq, A]; cu_q_lens int32 [n_reqs + 1]; kv_lens int32 [n_reqs]; block_tables int32 [n_reqs, max_blocks];
+    caches bf16 [num_blocks, Hkv, block_size, A]; workspace: uint8 CUDA tensor of at least
+    cb_paged_cross_attention_workspace_size bytes."""
+    c = _tc()
+    dev = _current_device(c, q)
+    pq = _on(dev, q, c.bf16, "q", 3)
+    pcu = _on(dev, cu_q_lens, c.i32, "cu_q_lens", 1)
+    pkv = _on(dev, kv_lens, c.i32, "kv_lens", 1)
+    pbt = _on(dev, block_tables, c.i32, "block_tables", 2)
+    ck = _on(dev, k_cache, c.bf16, "k_cache", 4)
+    cv = _on(dev, v_cache, c.bf16, "v_cache", 4)
+    po = _on(dev, out, c.bf16, "out", 3)
+    pw = _on(dev, workspace, c.u8, "workspace", 1)
+    shape, tables, cache = q.shape, block_tables.shape, k_cache.shape
+    if len(shape) != 3 or out.shape != shape or kv_lens.dim() != 1 or len(tables) != 2 or workspace.dim() != 1:
+        raise ValueError("shape mismatch")
+    n_reqs = kv_lens.shape[0]
+    if cu_q_lens.shape != (n_reqs + 1,) or tables[0] != n_reqs:
+        raise ValueError("shape mismatch")
+    if len(cache) != 4 or v_cache.shape != cache or cache[3] != shape[2]:
+        raise ValueError("cache shape mismatch")
+    n_tok, hq, a = shape
+    nb, hk, bs, _ = cache
+    max_q_len, max_kv_len = int(max_q_len), int(max_kv_len)
+    _fit_int(max_q_len, max_kv_len, n_tok)
+    _check("cb_paged_cross_attention",
+           lib().cb_paged_cross_attention(pq, pcu, pkv, pbt, tables[1], n_reqs, n_tok, max_q_len, max_kv_len, ck, cv, nb,
+                                          po, float(scale), hq, hk, a, bs, pw, workspace.shape[0],
+                                          _raw_stream(c, dev, stream)))
 
 
 # ---------------------------------------------------------------- block pool on the device

@@ -27,6 +27,9 @@ struct StreamSlot {
 };
 constexpr int kStreamSlots = 4096;
 __device__ StreamSlot g_stream_slots[kStreamSlots];
+// Cross attention's arrival counters of one (device, stream): zero at load, and
+// every launch leaves them at zero.
+__device__ unsigned g_join_counters[kStreamSlots][kMaxDecodeGrid];
 
 namespace {
 
@@ -57,8 +60,9 @@ bool device_info(DeviceInfo* out) {
 // (create = false: only look it up).  Returns nullptr on a CUDA error, when a
 // device has used up its kStreamSlots slots (*full = true), or, without
 // create, when the stream has none yet.
-StreamSlot* stream_slot(cudaStream_t stream, bool create, bool* full = nullptr) {
+StreamSlot* stream_slot(cudaStream_t stream, bool create, bool* full = nullptr, unsigned** joins = nullptr) {
   static void* base[kMaxDevices] = {};
+  static void* join_base[kMaxDevices] = {};
   static int next[kMaxDevices] = {};
   static std::map<std::pair<int, uintptr_t>, int> slot_of;
   static std::mutex mu;
@@ -67,6 +71,7 @@ StreamSlot* stream_slot(cudaStream_t stream, bool create, bool* full = nullptr) 
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   std::lock_guard<std::mutex> lock(mu);
   if (!base[dev] && cudaGetSymbolAddress(&base[dev], g_stream_slots) != cudaSuccess) return nullptr;
+  if (!join_base[dev] && cudaGetSymbolAddress(&join_base[dev], g_join_counters) != cudaSuccess) return nullptr;
   const auto key = std::make_pair(dev, reinterpret_cast<uintptr_t>(stream));
   auto it = slot_of.find(key);
   if (it == slot_of.end()) {
@@ -77,6 +82,7 @@ StreamSlot* stream_slot(cudaStream_t stream, bool create, bool* full = nullptr) 
     }
     it = slot_of.emplace(key, next[dev]++).first;
   }
+  if (joins) *joins = static_cast<unsigned*>(join_base[dev]) + (size_t)it->second * kMaxDecodeGrid;
   return static_cast<StreamSlot*>(base[dev]) + it->second;
 }
 
@@ -238,6 +244,12 @@ bool shape_ok(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
   const int g = n_q_heads / n_kv_heads;
   if (g == 1 || g == 2 || g == 4 || g == 8) return true;
   return block_tile_shape(n_q_heads, n_kv_heads, head_dim);    // G = 16, 32
+}
+// Cross attention takes every group of 1, 2, 4, .. 32 heads on any number of KV heads.
+bool cross_shape(int n_q_heads, int n_kv_heads, int head_dim, int block_size) {
+  if (n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads) return false;
+  const int g = n_q_heads / n_kv_heads;
+  return g <= 32 && (g & (g - 1)) == 0 && (head_dim == 64 || head_dim == 128) && block_size == kBlockSize;
 }
 
 }  // namespace
@@ -513,6 +525,76 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
   return attention_step(&app, q, cu_q_lens, ctx_lens, block_tables, max_blocks_per_seq, n_reqs, n_tokens, max_q_len,
                         max_kv_len, k_cache, v_cache, num_blocks, out, scale, n_q_heads, n_kv_heads, head_dim,
                         block_size, window, workspace, workspace_bytes, stream);
+}
+
+size_t cb_paged_cross_attention_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
+                                               int n_kv_heads, int head_dim, int block_size) {
+  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 0 ||
+      !cross_shape(n_q_heads, n_kv_heads, head_dim, block_size))
+    return 0;
+  return (size_t)2 * kMaxDecodeGrid * cross_part_rows(max_q_len, n_q_heads / n_kv_heads) * (head_dim + 2) * 4;
+}
+
+int cb_paged_cross_attention(const void* q, const int32_t* cu_q_lens, const int32_t* kv_lens, const int32_t* block_tables,
+                             int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len, int max_kv_len,
+                             const void* k_cache, const void* v_cache, int num_blocks, void* out, float scale,
+                             int n_q_heads, int n_kv_heads, int head_dim, int block_size, void* workspace,
+                             size_t workspace_bytes, void* stream) try {
+  if (!cross_shape(n_q_heads, n_kv_heads, head_dim, block_size)) return CB_EINVAL;
+  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 0 || max_kv_len > 1 << 30 ||
+      max_blocks_per_seq < 1 || num_blocks <= 0 || !(scale > 0.f))
+    return CB_EINVAL;
+  if ((long long)num_blocks * n_kv_heads * kBlockSize >= (1LL << 31) - kBlockSize) return CB_EINVAL;
+  const int group = n_q_heads / n_kv_heads;
+  // the kernel counts a step's work in 32 bits
+  const long long units = cross_units_bound(n_reqs, n_tokens, max_kv_len, n_kv_heads, group);
+  if (units >= 1LL << 30) return CB_EINVAL;
+  if (n_reqs == 0 || n_tokens == 0) {
+    g_last_launches = 0;
+    return CB_OK;
+  }
+  if (!q || !cu_q_lens || !kv_lens || !block_tables || !k_cache || !v_cache || !out || !workspace) return CB_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(workspace))
+    return CB_EINVAL;
+  if (workspace_bytes < cb_paged_cross_attention_workspace_size(n_reqs, n_tokens, max_q_len, max_kv_len, n_q_heads,
+                                                                n_kv_heads, head_dim, block_size))
+    return CB_EWORKSPACE;
+  DeviceInfo di;
+  if (!device_info(&di)) return CB_ECUDA;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CrossParams p{};
+  bool slots_full = false;
+  StreamSlot* slot = stream_slot(s, true, &slots_full, &p.joins);
+  if (!slot) return slots_full ? CB_ESTATE : CB_ECUDA;
+  p.cu_q_lens = cu_q_lens;
+  p.kv_lens = kv_lens;
+  p.block_tables = block_tables;
+  p.out = static_cast<uint16_t*>(out);
+  p.part = static_cast<float*>(workspace);
+  p.err = &slot->err;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.n_reqs = n_reqs;
+  p.n_tokens = n_tokens;
+  p.max_q_len = max_q_len;
+  p.max_kv_len = max_kv_len;
+  p.num_blocks = num_blocks;
+  p.n_q_heads = n_q_heads;
+  p.n_kv_heads = n_kv_heads;
+  while (1 << p.group_log2 < group) ++p.group_log2;
+  p.part_rows = cross_part_rows(max_q_len, group);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const int box_tokens = std::min(kTileM / group, max_q_len);
+  p.q_bytes = (unsigned)(box_tokens * group * head_dim * 2);
+  CUtensorMap maps[3];
+  if (!encode_cache_map(&maps[0], k_cache, num_blocks, n_kv_heads, head_dim) ||
+      !encode_cache_map(&maps[1], v_cache, num_blocks, n_kv_heads, head_dim) ||
+      !encode_q_map(&maps[2], q, n_tokens, n_q_heads, head_dim, group, box_tokens))
+    return CB_ECUDA;
+  if (launch_cross(p, maps, head_dim, cross_grid(units, di.n_sms), s) != cudaSuccess) return CB_ECUDA;
+  g_last_launches = 1;
+  return CB_OK;
+} catch (...) {   // an allocation or a lock of the library's host state
+  return CB_ECUDA;
 }
 
 int cb_last_error(void* stream) {

@@ -1,0 +1,811 @@
+// Cross attention over a paged cache: every new token of a request attends to
+// all of the request's stored keys (an encoder's states: another length, no
+// causal mask),
+//     out[t][h] = softmax_j(scale * q[t][h] . K[j]) . V[j],   0 <= j < kv_len.
+//
+// Work.  A query row is (token, head of the KV head's group); an item is (request,
+// KV head, up to 256 of its rows), its keys in tiles of 128.  An item of more than
+// 128 rows is wide: two row tiles share every key tile, one per softmax group.  An
+// item of at most 128 rows (a decoding step, a few beams) is narrow: one row tile,
+// and the two groups take the key tiles in turn, so that one's softmax runs beside
+// the other's products; their results are joined at the item's end.  All items' key
+// tiles, in order, are cut into equal ranges, one per CTA of a persistent grid:
+// whatever the batch looks like, every SM streams the same share.  An item that a
+// boundary cuts leaves partial results (running max, sum, O), and the CTAs that
+// share it join them, each its part of the rows, after their last tile.  They
+// wait for each other there, so the launch is cooperative.
+//
+// Tensor memory (512 columns): S_A|P_A [0,128), S_B|P_B [128,256), O_A, O_B.  P
+// (bf16) is written over its own S and is the A operand of O += P V.
+//
+// Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
+// and V; warp 9: MMA issue.  Scores, running max (base 2, scale folded in), sums
+// and O are fp32; the weights are rounded to bf16 for the tensor cores (within 2^-8
+// of each, as the output is of itself) and summed before that rounding.
+// Every wait is bounded.
+#include <algorithm>
+
+#include "../../include/cbattn.h"
+#include "cb_common.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kRows = 256;             // of a wide item
+constexpr float kNoKey = -__builtin_huge_valf();
+
+// Cost of a key tile of a narrow and of a wide item, and of an item's start.
+constexpr int kNarrow = 1, kWide = 2, kLead = 1;
+constexpr int kLeast = 4;              // of a CTA's share
+
+template <int A>
+struct Tiles {
+  static constexpr int kHalves = A / 64;
+  static constexpr int kHalfBytes = 128 * 128;
+  static constexpr int kBytes = kHalves * kHalfBytes;     // of 128 rows
+  static constexpr int kStages = A == 128 ? 2 : 4;
+  uint8_t q[2][kHalves][128][128];
+  uint8_t k[kStages][kHalves][128][128];
+  uint8_t v[kStages][kHalves][128][128];
+};
+
+template <int NS>
+struct alignas(16) Ctl {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t ml_full;                    // ml is written
+  uint64_t drain;
+  uint32_t tmem_base;
+  volatile int abort;
+  int any_empty;                       // a request has tokens and no keys
+  int share;                           // units of a CTA's range
+  int total;
+  long long scan[kThreads / 32];
+  float2 ml[128];                      // group B's (max, sum) of a narrow item
+};
+
+// ---------------------------------------------------------------- plan
+struct Request {
+  int q0, q_len, kv;                   // q_len 0: nothing to do
+};
+__device__ __forceinline__ Request load_request(const CrossParams& P, int r, bool report) {
+  const int q0 = __ldg(P.cu_q_lens + r), q1 = __ldg(P.cu_q_lens + r + 1), kv = __ldg(P.kv_lens + r);
+  const bool bad = q0 < 0 || q1 < q0 || q1 > P.n_tokens || q1 - q0 > P.max_q_len || kv < 0 || kv > P.max_kv_len ||
+                   (kv + kBlockSize - 1) / kBlockSize > P.max_blocks_per_seq;
+  if (bad) {
+    if (report) set_error(P.err, CB_DEVERR_BADLEN);
+    return {0, 0, 0};
+  }
+  return {q0, q1 - q0, kv};
+}
+
+// A request's items: per KV head, groups of 256 rows, the last one narrow if it
+// has at most 128.
+struct Shape {
+  int groups, tiles, last;             // last: cost of the last group
+  int full;                            // of the others
+  __device__ __forceinline__ int head() const { return (groups - 1) * full + last; }
+};
+__device__ __forceinline__ Shape shape_of(const CrossParams& P, const Request& q) {
+  const int tok = kRows >> P.group_log2;
+  Shape s;
+  s.groups = (q.q_len + tok - 1) / tok;
+  s.tiles = (q.kv + kTileN - 1) / kTileN;
+  s.full = kLead + s.tiles * kWide;
+  s.last = q.q_len - (s.groups - 1) * tok > tok / 2 ? s.full : kLead + s.tiles * kNarrow;
+  return s;
+}
+
+// pre[r]: units of the requests before r.  All threads; ends with a barrier.
+template <class C>
+__device__ void make_plan(const CrossParams& P, C& c, int* pre) {
+  const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
+  long long mine = 0;
+  for (int r = lo; r < hi; ++r) {
+    const Request q = load_request(P, r, blockIdx.x == 0);
+    if (q.q_len && q.kv) mine += (long long)shape_of(P, q).head() * P.n_kv_heads;
+    if (q.q_len && !q.kv) c.any_empty = 1;
+  }
+  long long x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) c.scan[warp] = x;
+  __syncthreads();
+  long long before = x - mine, all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += c.scan[w];
+    all += c.scan[w];
+  }
+  const bool fits = all < 1LL << 30;   // always, for lengths that the host's bounds allow
+  if (!fits && blockIdx.x == 0 && tid == 0) set_error(P.err, CB_DEVERR_BADLEN);
+  for (int r = lo; r < hi; ++r) {
+    pre[r] = fits ? (int)before : 0;
+    const Request q = load_request(P, r, false);
+    if (q.q_len && q.kv) before += (long long)shape_of(P, q).head() * P.n_kv_heads;
+  }
+  if (tid == 0) {
+    c.total = fits ? (int)all : 0;
+    pre[n] = c.total;
+    c.share = max(kLeast, (c.total + (int)gridDim.x - 1) / (int)gridDim.x);
+  }
+  __syncthreads();
+}
+
+// A CTA's part of an item: key tiles [ta, tb) of [0, tiles).
+struct Piece {
+  Request q;
+  int r, g, tok_lo, tokens, tiles, ta, tb;
+  int at, step;                        // unit of tile 0, units per tile
+  bool wide;
+  __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
+};
+
+// Walks a CTA's pieces in order; every role has its own.
+struct Pieces {
+  const int* pre;
+  int u0, u1, n;
+  int r, g, grp, u;                    // the next item and its first unit
+  Request q;
+  Shape s;
+  template <class C>
+  __device__ Pieces(const CrossParams& P, const C& c, const int* pre_) : pre(pre_), n(P.n_reqs) {
+    u0 = (int)min((long long)c.total, (long long)blockIdx.x * c.share);
+    u1 = (int)min((long long)c.total, (long long)u0 + c.share);
+    r = n;
+    u = u1;
+    if (u0 >= u1) return;
+    int lo = 0, hi = n;                // last r with pre[r] <= u0
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= u0) lo = mid;
+      else hi = mid;
+    }
+    r = lo;
+    open(P);
+    int off = u0 - pre[r];
+    g = off / s.head();
+    off -= g * s.head();
+    grp = min(off / s.full, s.groups - 1);
+    u = pre[r] + g * s.head() + grp * s.full;
+  }
+  __device__ __forceinline__ void open(const CrossParams& P) {
+    q = load_request(P, r, false);
+    s = shape_of(P, q);
+  }
+  __device__ bool next(const CrossParams& P, Piece& p) {
+    while (u < u1) {
+      const int tok = kRows >> P.group_log2;
+      const bool last = grp == s.groups - 1;
+      p.q = q;
+      p.r = r;
+      p.g = g;
+      p.tok_lo = grp * tok;
+      p.tokens = min(tok, q.q_len - p.tok_lo);
+      p.wide = p.tokens > tok / 2;
+      p.tiles = s.tiles;
+      p.step = p.wide ? kWide : kNarrow;
+      p.at = u + kLead;
+      p.ta = min(s.tiles, max(0, u0 - p.at + p.step - 1) / p.step);
+      p.tb = min(s.tiles, max(0, u1 - p.at + p.step - 1) / p.step);
+      u += last ? s.last : s.full;
+      if (!last) {
+        ++grp;
+      } else {
+        grp = 0;
+        if (++g == P.n_kv_heads) {
+          g = 0;
+          do ++r;
+          while (r < n && pre[r + 1] == pre[r]);
+          if (r < n) open(P);
+        }
+      }
+      if (p.ta < p.tb) return true;
+    }
+    return false;
+  }
+};
+
+// ---------------------------------------------------------------- waits
+template <class C>
+__device__ __forceinline__ bool lane_wait(const CrossParams& P, C& c, uint64_t* bar, uint32_t parity) {
+  if (mbar_wait(bar, parity)) return true;
+  set_error(P.err, CB_DEVERR_TIMEOUT);
+  c.abort = 1;
+  return false;
+}
+__device__ __forceinline__ bool warp_wait(const CrossParams& P, uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_wait(bar, parity);
+  if (!ok) set_error(P.err, CB_DEVERR_TIMEOUT);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// ---------------------------------------------------------------- loads (warp 8)
+template <int A, class C>
+__device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUtensorMap* vmap, const CUtensorMap* qmap,
+                       Tiles<A>& T, C& c, const int* pre) {
+  using TT = Tiles<A>;
+  constexpr int H = TT::kHalves, NS = TT::kStages;
+  const unsigned FULL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int none = P.num_blocks * P.n_kv_heads * kBlockSize;      // past the map's rows: zeros
+  const int my_b = (lane / H) & 7, my_h = lane % H;
+  const bool issues = lane < 8 * H;
+  const int tok_tile = kTileM >> P.group_log2, group = 1 << P.group_log2;
+  uint32_t kt = 0, qs = 0;
+  int held = -1;                                                  // V rows of tile kt - 1, not yet asked for
+  bool some = false;
+  Pieces pieces(P, c, pre);
+  Piece p;
+  auto load_v = [&](uint32_t t, int y) -> bool {
+    const uint32_t st = t % NS;
+    int ok = 1;
+    if (lane == 0) {
+      ok = lane_wait(P, c, &c.v_empty[st], ((t / NS) & 1) ^ 1);
+      if (ok) mbar_arrive_expect_tx(&c.v_full[st], TT::kBytes);
+    }
+    if (!__shfl_sync(FULL, ok, 0)) return false;
+    if (issues) tma_load_2d(&T.v[st][my_h][my_b * kBlockSize][0], vmap, my_h * 64, y, &c.v_full[st]);
+    return true;
+  };
+  bool ok = true;
+  while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
+    int fine = 1;
+    if (lane == 0) {
+      for (int side = 0; side < (p.wide ? 2 : 1) && fine; ++side) {
+        const uint32_t x = qs + side, st = x & 1;
+        fine = lane_wait(P, c, &c.q_empty[st], ((x >> 1) & 1) ^ 1);
+        if (fine) {
+          mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes);
+#pragma unroll
+          for (int h = 0; h < H; ++h)
+            tma_load_3d(&T.q[st][h][0][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
+        }
+      }
+    }
+    ok = __shfl_sync(FULL, fine, 0);
+    if (!ok) break;
+    qs += p.wide ? 2 : 1;
+    const int n_blocks = (p.q.kv + kBlockSize - 1) / kBlockSize;
+    int y = none;
+    for (int j = p.ta; j < p.tb; ++j, ++kt) {
+      if (((j - p.ta) & 3) == 0) {     // entries of this tile and the next three
+        const int b = j * 8 + lane;
+        y = none;
+        if (b < n_blocks) {
+          const int e = __ldg(P.block_tables + (size_t)p.r * P.max_blocks_per_seq + b);
+          if (e >= 0 && e < P.num_blocks)
+            y = (e * P.n_kv_heads + p.g) * kBlockSize;
+          else
+            set_error(P.err, CB_DEVERR_BADBLOCK);
+        }
+      }
+      const int yb = __shfl_sync(FULL, y, ((j - p.ta) & 3) * 8 + my_b);
+      const uint32_t st = kt % NS;
+      fine = 1;
+      if (lane == 0) {
+        fine = lane_wait(P, c, &c.k_empty[st], ((kt / NS) & 1) ^ 1);
+        if (fine) mbar_arrive_expect_tx(&c.k_full[st], TT::kBytes);
+      }
+      ok = __shfl_sync(FULL, fine, 0);
+      if (!ok) break;
+      if (issues) tma_load_2d(&T.k[st][my_h][my_b * kBlockSize][0], kmap, my_h * 64, yb, &c.k_full[st]);
+      if (some) ok = load_v(kt - 1, held);                        // K runs a tile ahead of V
+      if (!ok) break;
+      held = yb;
+      some = true;
+    }
+  }
+  if (ok && some) load_v(kt - 1, held);
+  if (c.abort && lane == 0) {          // copies in flight land before shared memory is given back
+    for (int par = 0; par < 2; ++par) {
+      for (int s = 0; s < NS; ++s) {
+        mbar_wait(&c.k_full[s], par, 20000000ull);
+        mbar_wait(&c.v_full[s], par, 20000000ull);
+      }
+      mbar_wait(&c.q_full[0], par, 20000000ull);
+      mbar_wait(&c.q_full[1], par, 20000000ull);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- MMA issue (warp 9, one lane)
+// Group s's tiles run as a chain S(0) PV(0) S(1) PV(1) ...; S(i + 1) goes out right
+// behind PV(i), which reads P from the columns that S(i + 1) overwrites: operations of
+// one thread run in order.  The two chains' turns alternate.
+template <int A, class C>
+__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, uint32_t tmem) {
+  using TT = Tiles<A>;
+  constexpr int NS = TT::kStages;
+  constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, A, 1);
+  const uint64_t q0 = smem_desc_sw128(smem_u32(&T.q[0][0][0][0]), 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(smem_u32(&T.k[0][0][0][0]), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(smem_u32(&T.v[0][0][0][0]), TT::kHalfBytes, 1024);
+  uint32_t kt = 0, qs = 0;
+  uint32_t np[2] = {0, 0}, items[2] = {0, 0};      // P tiles consumed, items begun, per group
+  Pieces pieces(P, c, pre);
+  Piece p;
+  bool ok = true;
+  auto scores = [&](int side, uint32_t t, uint32_t slot) -> bool {
+    const uint32_t st = t % NS;
+    if (!lane_wait(P, c, &c.k_full[st], (t / NS) & 1)) return false;
+    tc_fence_after();
+    const uint64_t q = q0 + slot * (TT::kBytes >> 4), k = k0 + st * (TT::kBytes >> 4);
+#pragma unroll
+    for (int ks = 0; ks < A / 16; ++ks) {
+      const uint64_t off = ((ks >> 2) * TT::kHalfBytes + (ks & 3) * 32) >> 4;
+      tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
+    }
+    tc_commit(&c.s_full[side]);
+    return true;
+  };
+  auto values = [&](int side, uint32_t t, bool first) -> bool {
+    const uint32_t st = t % NS;
+    if (!lane_wait(P, c, &c.v_full[st], (t / NS) & 1)) return false;
+    if (first && !lane_wait(P, c, &c.o_free[side], (items[side]++ & 1) ^ 1)) return false;
+    if (!lane_wait(P, c, &c.p_full[side], np[side]++ & 1)) return false;
+    tc_fence_after();
+    const uint64_t v = v0 + st * (TT::kBytes >> 4);
+#pragma unroll
+    for (int ks = 0; ks < kTileN / 16; ++ks)
+      tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
+                    (!first || ks > 0) ? 1u : 0u);
+    tc_commit(&c.o_done[side]);
+    return true;
+  };
+  while (ok && !c.abort && pieces.next(P, p)) {
+    const int n = p.tb - p.ta;
+    const int na = p.wide ? n : (n + 1) / 2, nb = p.wide ? n : n / 2;
+    const uint32_t sa = qs & 1, sb = p.wide ? sa ^ 1 : sa;
+    ok = lane_wait(P, c, &c.q_full[sa], (qs >> 1) & 1);
+    if (ok && p.wide) ok = lane_wait(P, c, &c.q_full[sb], ((qs + 1) >> 1) & 1);
+    if (!ok) break;
+    // group A's tile i and group B's
+    auto ta = [&](int i) { return kt + (p.wide ? i : 2 * i); };
+    auto tb = [&](int i) { return kt + (p.wide ? i : 2 * i + 1); };
+    auto after_s = [&](int side, uint32_t t, bool last) {
+      if (!p.wide || side) tc_commit(&c.k_empty[t % NS]);
+      if (last) {
+        tc_commit(&c.q_empty[sa]);
+        if (p.wide) tc_commit(&c.q_empty[sb]);
+      }
+    };
+    // the piece's last S: B's if the groups have as many, else A's
+    ok = scores(0, ta(0), sa);
+    if (ok) after_s(0, ta(0), nb == 0);
+    if (ok && nb) {
+      ok = scores(1, tb(0), sb);
+      if (ok) after_s(1, tb(0), nb == 1 && na == 1);
+    }
+    for (int i = 0; ok && i < na; ++i) {
+      ok = values(0, ta(i), i == 0);
+      if (!ok) break;
+      if (!p.wide) tc_commit(&c.v_empty[ta(i) % NS]);
+      if (i + 1 < na) {
+        ok = scores(0, ta(i + 1), sa);
+        if (!ok) break;
+        after_s(0, ta(i + 1), i + 2 == na && nb < na);
+      }
+      if (i < nb) {
+        ok = values(1, tb(i), i == 0);
+        if (!ok) break;
+        tc_commit(&c.v_empty[tb(i) % NS]);
+        if (i + 1 < nb) {
+          ok = scores(1, tb(i + 1), sb);
+          if (!ok) break;
+          after_s(1, tb(i + 1), i + 2 == nb && nb == na);
+        }
+      }
+    }
+    kt += n;
+    qs += p.wide ? 2 : 1;
+  }
+  if (!ok) c.abort = 1;
+  tc_commit(&c.drain);                 // what was issued completes before the TMEM is freed
+  mbar_wait(&c.drain, 0, 20000000ull);
+}
+
+// ---------------------------------------------------------------- softmax (warps 0-7)
+// Scale a row's O by alpha.
+template <int A>
+__device__ __forceinline__ void rescale(uint32_t o, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < A / 32; ++c) {
+    float x[32];
+    tmem_ld32(o + c * 32, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] *= alpha;
+    tmem_st32(o + c * 32, x);
+  }
+}
+
+template <int A, class C>
+__device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, uint32_t tmem, int side) {
+  using TT = Tiles<A>;
+  constexpr int H = TT::kHalves, NS = TT::kStages;
+  const unsigned FULL = 0xffffffffu;
+  const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const uint32_t s_at = tmem + lanes + side * 128, o_at = tmem + lanes + 256 + side * A;
+  const int group = 1 << P.group_log2, tok_tile = kTileM >> P.group_log2;
+  const float sl2 = P.scale_log2;
+  // key tiles before this piece; this group's; group B's (counted by both); pieces that both share
+  uint32_t kt = 0, sc = 0, scb = 0, shared = 0;
+  Pieces pieces(P, c, pre);
+  Piece p;
+  while (!__any_sync(FULL, c.abort) && pieces.next(P, p)) {
+    const int n = p.tb - p.ta;
+    const int mine = p.wide ? n : side ? n / 2 : (n + 1) / 2;
+    const int tok = (p.wide && side ? tok_tile : 0) + (row >> P.group_log2);      // of the item
+    const bool valid = tok < p.tokens;
+    const bool busy = __any_sync(FULL, valid);                                    // this warp has rows
+    float m = kNoKey, l = 0.f;         // running max times scale * log2 e; sum
+    bool ok = true;
+    for (int i = 0; i < mine; ++i, ++sc) {
+      const int j = p.wide ? i : 2 * i + side, key0 = (p.ta + j) * kTileN;
+      ok = warp_wait(P, &c.s_full[side], sc & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (busy) {
+        float s[128];
+        tmem_ld64(s_at, *reinterpret_cast<float(*)[64]>(s));
+        tmem_ld64(s_at + 64, *reinterpret_cast<float(*)[64]>(s + 64));
+        tmem_wait_ld();
+        if (key0 + kTileN > p.q.kv) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = key0 + k < p.q.kv ? s[k] : kNoKey;
+        }
+        float a[4] = {kNoKey, kNoKey, kNoKey, kNoKey};
+#pragma unroll
+        for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
+        const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * sl2;
+        // O keeps the max that it was scaled by until the new one is 2^8 times that: exact all
+        // the same, since the weights, their sum and O refer to one max
+        const float mn = fmaxf(m, mt);
+        const bool need = valid && mn > m + 8.f;
+        float alpha = 1.f;
+        if (need) {
+          alpha = ex2(m - mn);
+          m = mn;
+        }
+        if (i > 0 && __any_sync(FULL, need)) {
+          ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          rescale<A>(o_at, alpha);
+        }
+        const float ms = m == kNoKey ? 0.f : m;                    // no key so far but -inf: weights 0
+        const uint64_t sl2x2 = f2(sl2, sl2), nm2 = f2(-ms, -ms);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float x0, x1;
+            f2split(ffma2(f2(s[h * 32 + 2 * k], s[h * 32 + 2 * k + 1]), sl2x2, nm2), x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            sum[k & 1] = fadd2(sum[k & 1], f2(p0, p1));
+            pk[k] = pack_bf16(p0, p1);
+          }
+          tmem_st16u(s_at + h * 16, pk);
+        }
+        float t[4];
+        f2split(sum[0], t[0], t[1]);
+        f2split(sum[1], t[2], t[3]);
+        l = l * alpha + ((t[0] + t[1]) + (t[2] + t[3]));
+      }
+      // values behind the last key in its block: whatever the cache holds there, and 0 * inf must
+      // not reach O.  In a wide item both groups write the same zeros.
+      if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {
+        const uint32_t t = kt + j, st = t % NS;
+        ok = warp_wait(P, &c.v_full[st], (t / NS) & 1);
+        if (!ok) break;
+        const int r0 = p.q.kv - key0, r1 = ((p.q.kv + kBlockSize - 1) & ~(kBlockSize - 1)) - key0;
+        for (int x = row; x < (r1 - r0) * H * 8; x += 128)
+          *reinterpret_cast<uint4*>(&T.v[st][(x >> 3) % H][r0 + x / (H * 8)][(x & 7) << 4]) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&c.p_full[side]);
+    }
+    kt += n;
+    const bool two = !p.wide && n > 1; // both groups hold parts of the same rows
+    scb += p.wide ? n : n / 2;
+    if (ok && mine) ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
+    if (!ok) {
+      c.abort = 1;
+      break;
+    }
+    tc_fence_after();
+    float alpha = 1.f, beta = 0.f;     // of this group's O and of the other's
+    if (two) {
+      if (side == 1) {
+        c.ml[row] = make_float2(m, l);
+        mbar_arrive(&c.ml_full);
+        continue;                      // group A takes it from here, and frees group B's O
+      }
+      if (!warp_wait(P, &c.o_done[1], (scb - 1) & 1) || !warp_wait(P, &c.ml_full, shared++ & 1)) {
+        c.abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const float2 b = c.ml[row];
+      const float mn = fmaxf(m, b.x), ms = mn == kNoKey ? 0.f : mn;
+      alpha = ex2(m - ms);
+      beta = ex2(b.x - ms);
+      l = l * alpha + b.y * beta;
+      m = mn;
+    } else if (!mine) {
+      continue;                        // a narrow piece of one tile has nothing for group B
+    }
+    const bool whole = p.whole();
+    const float inv = whole ? 1.f / l : 1.f;
+    alpha *= inv;
+    beta *= inv;
+    const int irow = (p.wide && side ? 128 : 0) + row;
+    const int slot = 2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0);
+    float* part = P.part + (size_t)slot * P.part_rows * (A + 2);
+    uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
+    if (busy) {
+#pragma unroll 1
+      for (int ch = 0; ch < A / 32; ++ch) {
+        float o[32];
+        tmem_ld32(o_at + ch * 32, o);
+        if (two) {
+          float b[32];
+          tmem_ld32(o_at + A + ch * 32, b);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = o[k] * alpha + b[k] * beta;
+        } else {
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] *= alpha;
+        }
+        if (valid && whole) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(dst + ch * 32 + k) = make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                                                                      pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+        } else if (valid) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(part + (size_t)irow * A + ch * 32 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+      if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)P.part_rows * A + irow * 2) = make_float2(m, l);
+    }
+    tc_fence_before();
+    mbar_arrive(&c.o_free[side]);
+    if (two) mbar_arrive(&c.o_free[1]);
+  }
+}
+
+// ---------------------------------------------------------------- joining
+// The pieces of an item that CTA boundaries cut are in the CTAs first .. last: the
+// first's slot 2 first + 1, then slot 2 c.  Each of those CTAs joins its part of
+// the rows:
+//     M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Counter `first` of the stream counts the arrivals of n CTAs, then as many
+// departures; the last sets it back to 0.
+template <int A, int LANES>
+__device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n, int lo, int hi) {
+  const int sub = threadIdx.x % LANES, group = 1 << P.group_log2;
+  const size_t slot_floats = (size_t)P.part_rows * (A + 2);
+  // every lane of a warp goes through the same number of rounds: the shuffles need them all
+  for (int base = lo; base < hi; base += kThreads / LANES) {
+    const int task = base + threadIdx.x / LANES;
+    const bool on = task < hi;
+    const int row = on ? task / (A / 4) : 0, col = on ? task % (A / 4) : 0;
+    auto piece = [&](int i) { return P.part + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * slot_floats; };
+    auto ml = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)P.part_rows * A) + row); };
+    float M = kNoKey;
+    if (on) {
+#pragma unroll 4
+      for (int i = sub; i < n; i += LANES) M = fmaxf(M, ml(i).x);
+    }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    float L = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (on) {
+#pragma unroll 4
+      for (int i = sub; i < n; i += LANES) {
+        const float2 x = ml(i);
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(piece(i) + (size_t)row * A) + col);
+        const float w = ex2(x.x - M);
+        L += w * x.y;
+        y.x += w * o.x, y.y += w * o.y, y.z += w * o.z, y.w += w * o.w;
+      }
+    }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) {
+      L += __shfl_xor_sync(0xffffffffu, L, d);
+      y.x += __shfl_xor_sync(0xffffffffu, y.x, d);
+      y.y += __shfl_xor_sync(0xffffffffu, y.y, d);
+      y.z += __shfl_xor_sync(0xffffffffu, y.z, d);
+      y.w += __shfl_xor_sync(0xffffffffu, y.w, d);
+    }
+    if (on && sub == 0) {
+      const float inv = 1.f / L;
+      uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + (row >> P.group_log2)) * P.n_q_heads + (size_t)p.g * group +
+                               (row & (group - 1))) * A + col * 4;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv));
+    }
+  }
+}
+
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// All threads, after the pipeline.
+template <int A, class C>
+__device__ void join(const CrossParams& P, C& c, const int* pre, volatile int* go) {
+  // a CTA's cut items are its first piece's and its last piece's: arrive for both before waiting for either
+  for (int pass = 0; pass < 2; ++pass) {
+    Pieces pieces(P, c, pre);
+    Piece p;
+    while (pieces.next(P, p)) {
+      if (p.whole()) continue;
+      const int first = p.at / c.share, last = (p.at + (p.tiles - 1) * p.step) / c.share, n = last - first + 1;
+      unsigned* count = P.joins + first;
+      if (pass == 0) {
+        if (threadIdx.x == 0) {
+          __threadfence();             // with the barrier before join(): every thread's partial results
+          atomicAdd(count, 1u);
+        }
+        continue;
+      }
+      if (threadIdx.x == 0) {
+        int ok = 1;
+        const uint64_t t0 = globaltimer_ns();
+        while (ld_acquire(count) < (unsigned)n) {
+          if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            set_error(P.err, CB_DEVERR_TIMEOUT);
+            ok = 0;
+            break;
+          }
+        }
+        *go = ok;
+      }
+      __syncthreads();
+      if (*go && !c.abort) {
+        const int rows = p.tokens << P.group_log2, tasks = rows * (A / 4), i = (int)blockIdx.x - first;
+        const int lo = (int)((long long)tasks * i / n), hi = (int)((long long)tasks * (i + 1) / n);
+        if (n <= 6) join_rows<A, 1>(P, p, first, n, lo, hi);
+        else if (n <= 24) join_rows<A, 4>(P, p, first, n, lo, hi);
+        else join_rows<A, 16>(P, p, first, n, lo, hi);
+      }
+      __syncthreads();
+      if (threadIdx.x == 0 && atomicAdd(count, 1u) == 2u * n - 1) *count = 0u;
+    }
+  }
+}
+
+// Rows of requests without keys: zeros.  All threads of the grid.
+template <int A>
+__device__ void zero_rows(const CrossParams& P) {
+  const int lane = threadIdx.x & 31, vecs = P.n_q_heads * (A / 8);
+  for (int r = 0; r < P.n_reqs; ++r) {
+    const Request q = load_request(P, r, false);
+    if (!q.q_len || q.kv) continue;
+    for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < q.q_len; t += gridDim.x * (kThreads / 32)) {
+      uint4* dst = reinterpret_cast<uint4*>(P.out + (size_t)(q.q0 + t) * P.n_q_heads * A);
+      for (int i = lane; i < vecs; i += 32) dst[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+template <int A>
+__global__ void __launch_bounds__(kThreads, 1)
+    cross_kernel(const CrossParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                 const __grid_constant__ CUtensorMap qmap) {
+  using TT = Tiles<A>;
+  constexpr int NS = TT::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  TT& T = *reinterpret_cast<TT*>(base);
+  Ctl<NS>& c = *reinterpret_cast<Ctl<NS>*>(base + sizeof(TT));
+  int* pre = reinterpret_cast<int*>(base + sizeof(TT) + sizeof(Ctl<NS>));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&c.q_full[s], 1);
+      mbar_init(&c.q_empty[s], 1);
+      mbar_init(&c.s_full[s], 1);
+      mbar_init(&c.p_full[s], 128);
+      mbar_init(&c.o_done[s], 1);
+      mbar_init(&c.o_free[s], 128);
+    }
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&c.k_full[s], 1);
+      mbar_init(&c.k_empty[s], 1);
+      mbar_init(&c.v_full[s], 1);
+      mbar_init(&c.v_empty[s], 1);
+    }
+    mbar_init(&c.ml_full, 128);
+    mbar_init(&c.drain, 1);
+    c.abort = 0;
+    c.any_empty = 0;
+    fence_mbar_init();
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    prefetch_tmap(&qmap);
+  }
+  if (warp == 9) {
+    tmem_alloc(&c.tmem_base, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  make_plan(P, c, pre);
+  const uint32_t tmem = c.tmem_base;
+  if (warp == 8) {
+    loader<A>(P, &kmap, &vmap, &qmap, T, c, pre);
+  } else if (warp == 9) {
+    if (lane == 0) issuer<A>(P, T, c, pre, tmem);
+    __syncwarp();
+  } else {
+    softmax<A>(P, T, c, pre, tmem, warp >> 2);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (c.any_empty) zero_rows<A>(P);
+  join<A>(P, c, pre, reinterpret_cast<volatile int*>(&c.ml[0]));
+}
+
+constexpr int kSmemLimit = 232448;
+template <int A>
+constexpr size_t smem_bytes(int n_reqs) {
+  return 1024 + sizeof(Tiles<A>) + sizeof(Ctl<Tiles<A>::kStages>) + (size_t)(n_reqs + 1) * 4;
+}
+static_assert(smem_bytes<128>(kMaxReqs) <= (size_t)kSmemLimit && smem_bytes<64>(kMaxReqs) <= (size_t)kSmemLimit, "shared memory");
+static_assert(sizeof(Tiles<128>) % 16 == 0 && sizeof(Ctl<2>) % 16 == 0 && sizeof(Ctl<4>) % 16 == 0, "control blocks 16-byte aligned");
+
+template <int A>
+cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int grid, cudaStream_t stream) {
+  const void* kernel = reinterpret_cast<const void*>(cross_kernel<A>);
+  const cudaError_t e = opt_in_smem(kernel, kSmemLimit);
+  if (e != cudaSuccess) return e;
+  CrossParams pc = p;
+  void* args[] = {&pc, const_cast<CUtensorMap*>(&maps[0]), const_cast<CUtensorMap*>(&maps[1]),
+                  const_cast<CUtensorMap*>(&maps[2])};
+  return cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, smem_bytes<A>(p.n_reqs), stream);
+}
+
+}  // namespace
+
+long long cross_units_bound(int n_reqs, int n_tokens, int max_kv_len, int n_kv_heads, int group) {
+  const long long groups = (long long)n_tokens / (kRows / group) + n_reqs;
+  const long long tiles = ((long long)max_kv_len + kTileN - 1) / kTileN;
+  return groups * n_kv_heads * (kLead + kWide * tiles);
+}
+int cross_grid(long long units, int sms) {
+  return (int)std::max(1LL, std::min<long long>(std::min(sms, kMaxDecodeGrid), (units + kLeast - 1) / kLeast));
+}
+int cross_part_rows(int max_q_len, int group) {
+  return (int)((std::min<long long>(kRows, (long long)max_q_len * group) + 3) / 4 * 4);
+}
+
+cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream) {
+  return head_dim == 128 ? launch_cross_t<128>(p, maps, grid, stream) : launch_cross_t<64>(p, maps, grid, stream);
+}
+
+}  // namespace cb

@@ -116,6 +116,28 @@ cudaError_t launch_copy_blocks(const int32_t* pairs, int n_pairs, void* k_cache,
                                int n_kv_heads, int head_dim, unsigned int* err, cudaStream_t stream);
 cudaError_t launch_hbm_copy(void* dst, const void* src, size_t bytes, int n_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- cross attention
+struct CrossParams {
+  const int32_t* cu_q_lens;     // [n_reqs + 1]
+  const int32_t* kv_lens;       // [n_reqs]
+  const int32_t* block_tables;  // [n_reqs][max_blocks_per_seq]
+  uint16_t* out;                // bf16 [n_tokens][Hq][A]
+  float* part;                  // [2 * grid] partial results: [part_rows][A] O, then [part_rows][2] (max, sum)
+  unsigned* joins;              // [kMaxDecodeGrid] arrivals at cut items, zero between launches
+  unsigned int* err;            // the launching stream's error word
+  int max_blocks_per_seq, n_reqs, n_tokens, max_q_len, max_kv_len, num_blocks, n_q_heads, n_kv_heads;
+  int group_log2;               // log2(Hq / Hkv)
+  int part_rows;
+  unsigned q_bytes;             // of a query tile's load
+  float scale_log2;             // scale * log2(e)
+};
+// Upper bound of a step's units of work; CTAs of a launch with that many; rows of a partial result.
+long long cross_units_bound(int n_reqs, int n_tokens, int max_kv_len, int n_kv_heads, int group);
+int cross_grid(long long units, int sms);
+int cross_part_rows(int max_q_len, int group);
+// maps: K and V with 16-row boxes, q with boxes of a query tile.  Cooperative.
+cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream);
+
 // ---------------------------------------------------------------- 8-bit cache
 // K and V as e4m3 values [num_blocks][Hkv][16][A] with one exponent byte per row
 // [num_blocks][Hkv][16] (cb_fp8.cuh).

@@ -138,3 +138,33 @@ def test_binding_refuses_host_tensors():
         L.cb_compact_blocks(i(2, 4), i(2), i(8), i(8), i(4, 2), i(2), ws)
     with pytest.raises(ValueError):
         L.cb_copy_blocks_layers(i(1, 2), [torch.zeros(1, 8, 16)])
+
+
+# ------------------------------------------------------------------ cross attention's arguments
+def test_cross_attention_arguments():
+    L = _lib().lib()
+
+    def cross(q=D, cu=D, kv=D, bt=D, w=4, n=2, nt=3, mq=2, mkv=40, k=D, v=D, nb=16, out=D, scale=0.1, hq=8, hk=4, a=128, bs=16,
+              ws=D, wsb=1 << 30):
+        return L.cb_paged_cross_attention(q, cu, kv, bt, w, n, nt, mq, mkv, k, v, nb, out, scale, hq, hk, a, bs, ws, wsb, None)
+
+    assert cross(n=0) == 0 and cross(nt=0) == 0
+    for bad in (dict(hq=6), dict(hq=12), dict(hq=256), dict(hk=0), dict(a=96), dict(bs=32), dict(n=-1), dict(n=2049),
+                dict(nt=-1), dict(mq=0), dict(mkv=-1), dict(w=0), dict(nb=0), dict(nb=1 << 29), dict(scale=0.0),
+                dict(scale=float("nan")), dict(mkv=0x7FFFFFFF, nt=1 << 20), dict(q=None), dict(cu=None), dict(kv=None),
+                dict(bt=None), dict(k=None), dict(v=None), dict(out=None), dict(ws=None), dict(q=ODD), dict(k=ODD), dict(v=ODD),
+                dict(out=ODD), dict(ws=ODD)):
+        assert cross(**bad) == -1, bad
+    assert cross(wsb=16) == -3
+
+
+def test_cross_attention_workspace_size():
+    f = _lib().cb_paged_cross_attention_workspace_size
+    assert f(2, 3, 1, 40, 8, 4, 128, 16) == 320 * 4 * 130 * 4        # two rows of a token, four kept
+    assert f(2, 3, 1 << 20, 40, 8, 4, 64, 16) == 320 * 256 * 66 * 4
+    assert f(2, 3, 1, 0, 32, 1, 128, 16) > 0
+    for bad in ((-1, 3, 1, 40, 8, 4, 128, 16), (2, -1, 1, 40, 8, 4, 128, 16), (2, 3, 0, 40, 8, 4, 128, 16),
+                (2, 3, 1, -1, 8, 4, 128, 16), (2, 3, 1, 40, 24, 8, 128, 16), (2, 3, 1, 40, 8, 4, 80, 16), (2, 3, 1, 40, 8, 4, 128, 8)):
+        assert f(*bad) == 0
+    with pytest.raises(ValueError):
+        f(2, 3, 1 << 40, 40, 8, 4, 128, 16)
