@@ -19,11 +19,13 @@
 // (bf16) is written over its own S and is the A operand of O += P V.
 //
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
-// and V; warp 9: MMA issue.  Scores, running max (base 2, scale folded in), sums
+// and V; warp 9: MMA issue; two more complete the third warpgroup, which gives
+// most of its registers to the other two: a row's 128 scores stay in registers.  Scores, running max (base 2, scale folded in), sums
 // and O are fp32; the weights are rounded to bf16 for the tensor cores (within 2^-8
 // of each, as the output is of itself) and summed before that rounding.
 // Every wait is bounded.
 #include <algorithm>
+#include <cstddef>
 
 #include "../../include/cbattn.h"
 #include "cb_common.cuh"
@@ -32,7 +34,7 @@ namespace cb {
 
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kRows = 256;             // of a wide item
 constexpr float kNoKey = -__builtin_huge_valf();
 
@@ -315,65 +317,88 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
   }
 }
 
-// ---------------------------------------------------------------- MMA issue (warp 9, one lane)
+// ---------------------------------------------------------------- MMA issue (warp 9)
 // Group s's tiles run as a chain S(0) PV(0) S(1) PV(1) ...; S(i + 1) goes out right
 // behind PV(i), which reads P from the columns that S(i + 1) overwrites: operations of
 // one thread run in order.  The two chains' turns alternate.
+//
+// The whole warp waits and computes; one elected lane issues.  Operands of an MMA
+// are read from uniform registers, which the compiler uses for values of a converged
+// warp: issued from a branch of one lane, each MMA moved its descriptors there first
+// and took about 110 cycles instead of the 64 that it runs.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 template <int A, class C>
 __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, uint32_t tmem) {
   using TT = Tiles<A>;
   constexpr int NS = TT::kStages;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, A, 1);
-  const uint64_t q0 = smem_desc_sw128(smem_u32(&T.q[0][0][0][0]), 16, 1024);
-  const uint64_t k0 = smem_desc_sw128(smem_u32(&T.k[0][0][0][0]), 16, 1024);
-  const uint64_t v0 = smem_desc_sw128(smem_u32(&T.v[0][0][0][0]), TT::kHalfBytes, 1024);
+  const unsigned FULL = 0xffffffffu;
+  tmem = __shfl_sync(FULL, tmem, 0);
+  const uint32_t base = __shfl_sync(FULL, smem_u32(&T), 0);
+  const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
+  const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, k), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, v), TT::kHalfBytes, 1024);
   uint32_t kt = 0, qs = 0;
   uint32_t np[2] = {0, 0}, items[2] = {0, 0};      // P tiles consumed, items begun, per group
   Pieces pieces(P, c, pre);
   Piece p;
   bool ok = true;
+  auto arrives = [&](uint64_t* bar) {              // when all that was issued so far is done
+    if (elect_lane()) tc_commit(bar);
+  };
   auto scores = [&](int side, uint32_t t, uint32_t slot) -> bool {
-    const uint32_t st = t % NS;
-    if (!lane_wait(P, c, &c.k_full[st], (t / NS) & 1)) return false;
+    const uint32_t st = __shfl_sync(FULL, t % NS, 0);
+    if (!warp_wait(P, &c.k_full[st], (t / NS) & 1)) return false;
     tc_fence_after();
     const uint64_t q = q0 + slot * (TT::kBytes >> 4), k = k0 + st * (TT::kBytes >> 4);
+    if (elect_lane()) {
 #pragma unroll
-    for (int ks = 0; ks < A / 16; ++ks) {
-      const uint64_t off = ((ks >> 2) * TT::kHalfBytes + (ks & 3) * 32) >> 4;
-      tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
+      for (int ks = 0; ks < A / 16; ++ks) {
+        const uint64_t off = ((ks >> 2) * TT::kHalfBytes + (ks & 3) * 32) >> 4;
+        tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
+      }
+      tc_commit(&c.s_full[side]);
     }
-    tc_commit(&c.s_full[side]);
+    __syncwarp();
     return true;
   };
   auto values = [&](int side, uint32_t t, bool first) -> bool {
-    const uint32_t st = t % NS;
-    if (!lane_wait(P, c, &c.v_full[st], (t / NS) & 1)) return false;
-    if (first && !lane_wait(P, c, &c.o_free[side], (items[side]++ & 1) ^ 1)) return false;
-    if (!lane_wait(P, c, &c.p_full[side], np[side]++ & 1)) return false;
+    const uint32_t st = __shfl_sync(FULL, t % NS, 0);
+    if (!warp_wait(P, &c.v_full[st], (t / NS) & 1)) return false;
+    if (first && !warp_wait(P, &c.o_free[side], (items[side]++ & 1) ^ 1)) return false;
+    if (!warp_wait(P, &c.p_full[side], np[side]++ & 1)) return false;
     tc_fence_after();
     const uint64_t v = v0 + st * (TT::kBytes >> 4);
+    if (elect_lane()) {
 #pragma unroll
-    for (int ks = 0; ks < kTileN / 16; ++ks)
-      tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
-                    (!first || ks > 0) ? 1u : 0u);
-    tc_commit(&c.o_done[side]);
+      for (int ks = 0; ks < kTileN / 16; ++ks)
+        tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
+                      (!first || ks > 0) ? 1u : 0u);
+      tc_commit(&c.o_done[side]);
+    }
+    __syncwarp();
     return true;
   };
-  while (ok && !c.abort && pieces.next(P, p)) {
+  while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
     const int na = p.wide ? n : (n + 1) / 2, nb = p.wide ? n : n / 2;
-    const uint32_t sa = qs & 1, sb = p.wide ? sa ^ 1 : sa;
-    ok = lane_wait(P, c, &c.q_full[sa], (qs >> 1) & 1);
-    if (ok && p.wide) ok = lane_wait(P, c, &c.q_full[sb], ((qs + 1) >> 1) & 1);
+    const uint32_t sa = __shfl_sync(FULL, qs & 1, 0), sb = p.wide ? sa ^ 1 : sa;
+    ok = warp_wait(P, &c.q_full[sa], (qs >> 1) & 1);
+    if (ok && p.wide) ok = warp_wait(P, &c.q_full[sb], ((qs + 1) >> 1) & 1);
     if (!ok) break;
     // group A's tile i and group B's
     auto ta = [&](int i) { return kt + (p.wide ? i : 2 * i); };
     auto tb = [&](int i) { return kt + (p.wide ? i : 2 * i + 1); };
     auto after_s = [&](int side, uint32_t t, bool last) {
-      if (!p.wide || side) tc_commit(&c.k_empty[t % NS]);
+      if (!p.wide || side) arrives(&c.k_empty[t % NS]);
       if (last) {
-        tc_commit(&c.q_empty[sa]);
-        if (p.wide) tc_commit(&c.q_empty[sb]);
+        arrives(&c.q_empty[sa]);
+        if (p.wide) arrives(&c.q_empty[sb]);
       }
     };
     // the piece's last S: B's if the groups have as many, else A's
@@ -386,7 +411,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
     for (int i = 0; ok && i < na; ++i) {
       ok = values(0, ta(i), i == 0);
       if (!ok) break;
-      if (!p.wide) tc_commit(&c.v_empty[ta(i) % NS]);
+      if (!p.wide) arrives(&c.v_empty[ta(i) % NS]);
       if (i + 1 < na) {
         ok = scores(0, ta(i + 1), sa);
         if (!ok) break;
@@ -395,7 +420,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
       if (i < nb) {
         ok = values(1, tb(i), i == 0);
         if (!ok) break;
-        tc_commit(&c.v_empty[tb(i) % NS]);
+        arrives(&c.v_empty[tb(i) % NS]);
         if (i + 1 < nb) {
           ok = scores(1, tb(i + 1), sb);
           if (!ok) break;
@@ -407,7 +432,8 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
     qs += p.wide ? 2 : 1;
   }
   if (!ok) c.abort = 1;
-  tc_commit(&c.drain);                 // what was issued completes before the TMEM is freed
+  arrives(&c.drain);                   // what was issued completes before the TMEM is freed
+  __syncwarp();
   mbar_wait(&c.drain, 0, 20000000ull);
 }
 
@@ -719,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   TT& T = *reinterpret_cast<TT*>(base);
   Ctl<NS>& c = *reinterpret_cast<Ctl<NS>*>(base + sizeof(TT));
   int* pre = reinterpret_cast<int*>(base + sizeof(TT) + sizeof(Ctl<NS>));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.q_full[s], 1);
@@ -753,12 +779,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   make_plan(P, c, pre);
   const uint32_t tmem = c.tmem_base;
-  if (warp == 8) {
-    loader<A>(P, &kmap, &vmap, &qmap, T, c, pre);
-  } else if (warp == 9) {
-    if (lane == 0) issuer<A>(P, T, c, pre, tmem);
-    __syncwarp();
+  // three warpgroups of 168 registers a thread at launch: 2 * 208 + 88 = 3 * 168
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 8) {
+      loader<A>(P, &kmap, &vmap, &qmap, T, c, pre);
+    } else if (warp == 9) {
+      issuer<A>(P, T, c, pre, tmem);
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     softmax<A>(P, T, c, pre, tmem, warp >> 2);
   }
   tc_fence_before();
