@@ -42,37 +42,58 @@ constexpr float kNoKey = -__builtin_huge_valf();
 constexpr int kNarrow = 1, kWide = 2, kLead = 1;
 constexpr int kLeast = 4;              // of a CTA's share
 
+// K and V tiles share one ring of buffers, in the order of their use: a wide item's
+// K(0) V(0) K(1) V(1) .., a narrow one's K(0) K(1) V(0) K(2) V(1) .. V(n - 1), since
+// its two groups begin with a key tile each.
 template <int A>
 struct Tiles {
   static constexpr int kHalves = A / 64;
   static constexpr int kHalfBytes = 128 * 128;
   static constexpr int kBytes = kHalves * kHalfBytes;     // of 128 rows
-  static constexpr int kStages = A == 128 ? 2 : 4;
+  static constexpr int kRing = A == 128 ? 5 : 10;
   uint8_t q[2][kHalves][128][128];
-  uint8_t k[kStages][kHalves][128][128];
-  uint8_t v[kStages][kHalves][128][128];
+  uint8_t kv[kRing][kHalves][128][128];
+};
+// Place of tile i's K and V in the ring's order, for a piece of n tiles that begins at tile kt.
+__device__ __forceinline__ uint32_t place_k(uint32_t kt, int i, bool wide) { return 2 * kt + 2 * i - (!wide && i > 0); }
+__device__ __forceinline__ uint32_t place_v(uint32_t kt, int i, bool wide, int n) {
+  return 2 * kt + 2 * i + (wide || i == n - 1 ? 1 : 2);
+}
+
+// A request's tokens and stored keys; q_len 0: nothing to do.
+struct Request {
+  int q0, q_len, kv;
+};
+
+// A CTA's part of an item: key tiles [ta, tb) of [0, tiles).
+struct Piece {
+  Request q;
+  int r, g, tok_lo, tokens, tiles, ta, tb;
+  int at, step;                        // unit of tile 0, units per tile
+  bool wide;
+  __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
 };
 
 template <int NS>
 struct alignas(16) Ctl {
   uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t full[NS], empty[NS];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];        // per group
   uint64_t ml_full;                    // ml is written
   uint64_t drain;
   uint32_t tmem_base;
   volatile int abort;
   int any_empty;                       // a request has tokens and no keys
-  int share;                           // units of a CTA's range
-  int total;
+  int share, total;                    // units of a CTA's range, of all
+  int start_r, start_u;                // the request that the CTA's range begins in, its first unit
+  int n_cut;                           // pieces of cut items
+  int go;
+  Piece cut[2];
   long long scan[kThreads / 32];
   float2 ml[128];                      // group B's (max, sum) of a narrow item
 };
 
 // ---------------------------------------------------------------- plan
-struct Request {
-  int q0, q_len, kv;                   // q_len 0: nothing to do
-};
 __device__ __forceinline__ Request load_request(const CrossParams& P, int r, bool report) {
   const int q0 = __ldg(P.cu_q_lens + r), q1 = __ldg(P.cu_q_lens + r + 1), kv = __ldg(P.kv_lens + r);
   const bool bad = q0 < 0 || q1 < q0 || q1 > P.n_tokens || q1 - q0 > P.max_q_len || kv < 0 || kv > P.max_kv_len ||
@@ -101,9 +122,9 @@ __device__ __forceinline__ Shape shape_of(const CrossParams& P, const Request& q
   return s;
 }
 
-// pre[r]: units of the requests before r.  All threads; ends with a barrier.
+// Where this CTA's range of the units begins.  All threads; ends with a barrier.
 template <class C>
-__device__ void make_plan(const CrossParams& P, C& c, int* pre) {
+__device__ void make_plan(const CrossParams& P, C& c) {
   const int n = P.n_reqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seg = (n + kThreads - 1) / kThreads, lo = min(n, tid * seg), hi = min(n, lo + seg);
   long long mine = 0;
@@ -121,65 +142,60 @@ __device__ void make_plan(const CrossParams& P, C& c, int* pre) {
   if (lane == 31) c.scan[warp] = x;
   __syncthreads();
   long long before = x - mine, all = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += c.scan[w];
     all += c.scan[w];
   }
-  const bool fits = all < 1LL << 30;   // always, for lengths that the host's bounds allow
-  if (!fits && blockIdx.x == 0 && tid == 0) set_error(P.err, CB_DEVERR_BADLEN);
-  for (int r = lo; r < hi; ++r) {
-    pre[r] = fits ? (int)before : 0;
-    const Request q = load_request(P, r, false);
-    if (q.q_len && q.kv) before += (long long)shape_of(P, q).head() * P.n_kv_heads;
+  if (all >= 1LL << 30) {              // not for lengths that the host's bounds allow
+    if (blockIdx.x == 0 && tid == 0) set_error(P.err, CB_DEVERR_BADLEN);
+    all = 0;
   }
+  const int share = max(kLeast, ((int)all + (int)gridDim.x - 1) / (int)gridDim.x);
+  const long long u0 = (long long)blockIdx.x * share;
   if (tid == 0) {
-    c.total = fits ? (int)all : 0;
-    pre[n] = c.total;
-    c.share = max(kLeast, (c.total + (int)gridDim.x - 1) / (int)gridDim.x);
+    c.total = (int)all;
+    c.share = share;
+  }
+  if (u0 < all && before <= u0 && u0 < before + mine) {
+    for (int r = lo; r < hi; ++r) {
+      const Request q = load_request(P, r, false);
+      if (!q.q_len || !q.kv) continue;
+      const int units = shape_of(P, q).head() * P.n_kv_heads;
+      if (u0 < before + units) {
+        c.start_r = r;
+        c.start_u = (int)before;
+        break;
+      }
+      before += units;
+    }
   }
   __syncthreads();
 }
 
-// A CTA's part of an item: key tiles [ta, tb) of [0, tiles).
-struct Piece {
-  Request q;
-  int r, g, tok_lo, tokens, tiles, ta, tb;
-  int at, step;                        // unit of tile 0, units per tile
-  bool wide;
-  __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
-};
-
 // Walks a CTA's pieces in order; every role has its own.
 struct Pieces {
-  const int* pre;
   int u0, u1, n;
   int r, g, grp, u;                    // the next item and its first unit
   Request q;
   Shape s;
   template <class C>
-  __device__ Pieces(const CrossParams& P, const C& c, const int* pre_) : pre(pre_), n(P.n_reqs) {
+  __device__ Pieces(const CrossParams& P, const C& c) : n(P.n_reqs) {
     u0 = (int)min((long long)c.total, (long long)blockIdx.x * c.share);
     u1 = (int)min((long long)c.total, (long long)u0 + c.share);
-    r = n;
     u = u1;
     if (u0 >= u1) return;
-    int lo = 0, hi = n;                // last r with pre[r] <= u0
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= u0) lo = mid;
-      else hi = mid;
-    }
-    r = lo;
+    r = c.start_r;
     open(P);
-    int off = u0 - pre[r];
+    int off = u0 - c.start_u;
     g = off / s.head();
     off -= g * s.head();
     grp = min(off / s.full, s.groups - 1);
-    u = pre[r] + g * s.head() + grp * s.full;
+    u = c.start_u + g * s.head() + grp * s.full;
   }
   __device__ __forceinline__ void open(const CrossParams& P) {
     q = load_request(P, r, false);
-    s = shape_of(P, q);
+    if (q.q_len && q.kv) s = shape_of(P, q);
   }
   __device__ bool next(const CrossParams& P, Piece& p) {
     while (u < u1) {
@@ -203,9 +219,10 @@ struct Pieces {
         grp = 0;
         if (++g == P.n_kv_heads) {
           g = 0;
-          do ++r;
-          while (r < n && pre[r + 1] == pre[r]);
-          if (r < n) open(P);
+          do {
+            if (++r == n) break;
+            open(P);
+          } while (!q.q_len || !q.kv);
         }
       }
       if (p.ta < p.tb) return true;
@@ -231,33 +248,43 @@ __device__ __forceinline__ bool warp_wait(const CrossParams& P, uint64_t* bar, u
 // ---------------------------------------------------------------- loads (warp 8)
 template <int A, class C>
 __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUtensorMap* vmap, const CUtensorMap* qmap,
-                       Tiles<A>& T, C& c, const int* pre) {
+                       Tiles<A>& T, C& c) {
   using TT = Tiles<A>;
-  constexpr int H = TT::kHalves, NS = TT::kStages;
+  constexpr int H = TT::kHalves, NS = TT::kRing;
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int none = P.num_blocks * P.n_kv_heads * kBlockSize;      // past the map's rows: zeros
   const int my_b = (lane / H) & 7, my_h = lane % H;
   const bool issues = lane < 8 * H;
   const int tok_tile = kTileM >> P.group_log2, group = 1 << P.group_log2;
-  uint32_t kt = 0, qs = 0;
-  int held = -1;                                                  // V rows of tile kt - 1, not yet asked for
-  bool some = false;
-  Pieces pieces(P, c, pre);
+  uint32_t at = 0, qs = 0;                                        // place in the ring's order, query tiles
+  Pieces pieces(P, c);
   Piece p;
-  auto load_v = [&](uint32_t t, int y) -> bool {
-    const uint32_t st = t % NS;
+  auto load = [&](const CUtensorMap* map, int y) -> bool {
+    const uint32_t st = at % NS;
     int ok = 1;
     if (lane == 0) {
-      ok = lane_wait(P, c, &c.v_empty[st], ((t / NS) & 1) ^ 1);
-      if (ok) mbar_arrive_expect_tx(&c.v_full[st], TT::kBytes);
+      ok = lane_wait(P, c, &c.empty[st], ((at / NS) & 1) ^ 1);
+      if (ok) mbar_arrive_expect_tx(&c.full[st], TT::kBytes);
     }
+    ++at;
     if (!__shfl_sync(FULL, ok, 0)) return false;
-    if (issues) tma_load_2d(&T.v[st][my_h][my_b * kBlockSize][0], vmap, my_h * 64, y, &c.v_full[st]);
+    if (issues) tma_load_2d(&T.kv[st][my_h][my_b * kBlockSize][0], map, my_h * 64, y, &c.full[st]);
     return true;
   };
   bool ok = true;
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
+    const int n_blocks = (p.q.kv + kBlockSize - 1) / kBlockSize;
+    const int32_t* table = P.block_tables + (size_t)p.r * P.max_blocks_per_seq;
+    // a lane's entry of the four tiles from j on
+    auto entry = [&](int j) { return j * 8 + lane < n_blocks ? __ldg(table + j * 8 + lane) : -1; };
+    auto row_of = [&](int j, int e) {
+      if (j * 8 + lane >= n_blocks) return none;
+      if (e >= 0 && e < P.num_blocks) return (e * P.n_kv_heads + p.g) * kBlockSize;
+      set_error(P.err, CB_DEVERR_BADBLOCK);
+      return none;
+    };
+    int e = entry(p.ta), y = none, held = none;
     int fine = 1;
     if (lane == 0) {
       for (int side = 0; side < (p.wide ? 2 : 1) && fine; ++side) {
@@ -274,43 +301,25 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
     ok = __shfl_sync(FULL, fine, 0);
     if (!ok) break;
     qs += p.wide ? 2 : 1;
-    const int n_blocks = (p.q.kv + kBlockSize - 1) / kBlockSize;
-    int y = none;
-    for (int j = p.ta; j < p.tb; ++j, ++kt) {
-      if (((j - p.ta) & 3) == 0) {     // entries of this tile and the next three
-        const int b = j * 8 + lane;
-        y = none;
-        if (b < n_blocks) {
-          const int e = __ldg(P.block_tables + (size_t)p.r * P.max_blocks_per_seq + b);
-          if (e >= 0 && e < P.num_blocks)
-            y = (e * P.n_kv_heads + p.g) * kBlockSize;
-          else
-            set_error(P.err, CB_DEVERR_BADBLOCK);
-        }
+    for (int j = p.ta; ok && j < p.tb; ++j) {
+      const int in4 = (j - p.ta) & 3;
+      if (in4 == 0) {                  // the entries asked for four tiles ago; the next ones
+        y = row_of(j, e);
+        e = j + 4 < p.tb ? entry(j + 4) : -1;
       }
-      const int yb = __shfl_sync(FULL, y, ((j - p.ta) & 3) * 8 + my_b);
-      const uint32_t st = kt % NS;
-      fine = 1;
-      if (lane == 0) {
-        fine = lane_wait(P, c, &c.k_empty[st], ((kt / NS) & 1) ^ 1);
-        if (fine) mbar_arrive_expect_tx(&c.k_full[st], TT::kBytes);
-      }
-      ok = __shfl_sync(FULL, fine, 0);
-      if (!ok) break;
-      if (issues) tma_load_2d(&T.k[st][my_h][my_b * kBlockSize][0], kmap, my_h * 64, yb, &c.k_full[st]);
-      if (some) ok = load_v(kt - 1, held);                        // K runs a tile ahead of V
-      if (!ok) break;
+      const int yb = __shfl_sync(FULL, y, in4 * 8 + my_b);
+      ok = load(kmap, yb);
+      if (p.wide)
+        ok = ok && load(vmap, yb);
+      else if (j > p.ta)
+        ok = ok && load(vmap, held);
       held = yb;
-      some = true;
     }
+    if (ok && !p.wide) ok = load(vmap, held);
   }
-  if (ok && some) load_v(kt - 1, held);
   if (c.abort && lane == 0) {          // copies in flight land before shared memory is given back
     for (int par = 0; par < 2; ++par) {
-      for (int s = 0; s < NS; ++s) {
-        mbar_wait(&c.k_full[s], par, 20000000ull);
-        mbar_wait(&c.v_full[s], par, 20000000ull);
-      }
+      for (int s = 0; s < NS; ++s) mbar_wait(&c.full[s], par, 20000000ull);
       mbar_wait(&c.q_full[0], par, 20000000ull);
       mbar_wait(&c.q_full[1], par, 20000000ull);
     }
@@ -333,19 +342,19 @@ __device__ __forceinline__ bool elect_lane() {
 }
 
 template <int A, class C>
-__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, uint32_t tmem) {
+__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem) {
   using TT = Tiles<A>;
-  constexpr int NS = TT::kStages;
+  constexpr int NS = TT::kRing;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, A, 1);
   const unsigned FULL = 0xffffffffu;
   tmem = __shfl_sync(FULL, tmem, 0);
   const uint32_t base = __shfl_sync(FULL, smem_u32(&T), 0);
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
-  const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, k), 16, 1024);
-  const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, v), TT::kHalfBytes, 1024);
+  const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
+  const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
   uint32_t kt = 0, qs = 0;
   uint32_t np[2] = {0, 0}, items[2] = {0, 0};      // P tiles consumed, items begun, per group
-  Pieces pieces(P, c, pre);
+  Pieces pieces(P, c);
   Piece p;
   bool ok = true;
   auto arrives = [&](uint64_t* bar) {              // when all that was issued so far is done
@@ -353,7 +362,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
   };
   auto scores = [&](int side, uint32_t t, uint32_t slot) -> bool {
     const uint32_t st = __shfl_sync(FULL, t % NS, 0);
-    if (!warp_wait(P, &c.k_full[st], (t / NS) & 1)) return false;
+    if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
     tc_fence_after();
     const uint64_t q = q0 + slot * (TT::kBytes >> 4), k = k0 + st * (TT::kBytes >> 4);
     if (elect_lane()) {
@@ -369,7 +378,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
   };
   auto values = [&](int side, uint32_t t, bool first) -> bool {
     const uint32_t st = __shfl_sync(FULL, t % NS, 0);
-    if (!warp_wait(P, &c.v_full[st], (t / NS) & 1)) return false;
+    if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
     if (first && !warp_wait(P, &c.o_free[side], (items[side]++ & 1) ^ 1)) return false;
     if (!warp_wait(P, &c.p_full[side], np[side]++ & 1)) return false;
     tc_fence_after();
@@ -391,40 +400,41 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, 
     ok = warp_wait(P, &c.q_full[sa], (qs >> 1) & 1);
     if (ok && p.wide) ok = warp_wait(P, &c.q_full[sb], ((qs + 1) >> 1) & 1);
     if (!ok) break;
-    // group A's tile i and group B's
-    auto ta = [&](int i) { return kt + (p.wide ? i : 2 * i); };
-    auto tb = [&](int i) { return kt + (p.wide ? i : 2 * i + 1); };
-    auto after_s = [&](int side, uint32_t t, bool last) {
-      if (!p.wide || side) arrives(&c.k_empty[t % NS]);
+    // places of group s's i-th K and V
+    auto ks = [&](int side, int i) { return place_k(kt, p.wide ? i : 2 * i + side, p.wide); };
+    auto vs = [&](int side, int i) { return place_v(kt, p.wide ? i : 2 * i + side, p.wide, n); };
+    // a wide item's tiles are free once group B has them behind it
+    auto after_s = [&](int side, int i, bool last) {
+      if (!p.wide || side) arrives(&c.empty[ks(side, i) % NS]);
       if (last) {
         arrives(&c.q_empty[sa]);
         if (p.wide) arrives(&c.q_empty[sb]);
       }
     };
     // the piece's last S: B's if the groups have as many, else A's
-    ok = scores(0, ta(0), sa);
-    if (ok) after_s(0, ta(0), nb == 0);
+    ok = scores(0, ks(0, 0), sa);
+    if (ok) after_s(0, 0, nb == 0);
     if (ok && nb) {
-      ok = scores(1, tb(0), sb);
-      if (ok) after_s(1, tb(0), nb == 1 && na == 1);
+      ok = scores(1, ks(1, 0), sb);
+      if (ok) after_s(1, 0, nb == 1 && na == 1);
     }
     for (int i = 0; ok && i < na; ++i) {
-      ok = values(0, ta(i), i == 0);
+      ok = values(0, vs(0, i), i == 0);
       if (!ok) break;
-      if (!p.wide) arrives(&c.v_empty[ta(i) % NS]);
+      if (!p.wide) arrives(&c.empty[vs(0, i) % NS]);
       if (i + 1 < na) {
-        ok = scores(0, ta(i + 1), sa);
+        ok = scores(0, ks(0, i + 1), sa);
         if (!ok) break;
-        after_s(0, ta(i + 1), i + 2 == na && nb < na);
+        after_s(0, i + 1, i + 2 == na && nb < na);
       }
       if (i < nb) {
-        ok = values(1, tb(i), i == 0);
+        ok = values(1, vs(1, i), i == 0);
         if (!ok) break;
-        arrives(&c.v_empty[tb(i) % NS]);
+        arrives(&c.empty[vs(1, i) % NS]);
         if (i + 1 < nb) {
-          ok = scores(1, tb(i + 1), sb);
+          ok = scores(1, ks(1, i + 1), sb);
           if (!ok) break;
-          after_s(1, tb(i + 1), i + 2 == nb && nb == na);
+          after_s(1, i + 1, i + 2 == nb && nb == na);
         }
       }
     }
@@ -453,9 +463,9 @@ __device__ __forceinline__ void rescale(uint32_t o, float alpha) {
 }
 
 template <int A, class C>
-__device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, const int* pre, uint32_t tmem, int side) {
+__device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A>;
-  constexpr int H = TT::kHalves, NS = TT::kStages;
+  constexpr int H = TT::kHalves, NS = TT::kRing;
   const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
@@ -464,7 +474,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, const int* pre,
   const float sl2 = P.scale_log2;
   // key tiles before this piece; this group's; group B's (counted by both); pieces that both share
   uint32_t kt = 0, sc = 0, scb = 0, shared = 0;
-  Pieces pieces(P, c, pre);
+  Pieces pieces(P, c);
   Piece p;
   while (!__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
@@ -531,12 +541,12 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, const int* pre,
       // values behind the last key in its block: whatever the cache holds there, and 0 * inf must
       // not reach O.  In a wide item both groups write the same zeros.
       if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {
-        const uint32_t t = kt + j, st = t % NS;
-        ok = warp_wait(P, &c.v_full[st], (t / NS) & 1);
+        const uint32_t t = place_v(kt, j, p.wide, n), st = t % NS;
+        ok = warp_wait(P, &c.full[st], (t / NS) & 1);
         if (!ok) break;
         const int r0 = p.q.kv - key0, r1 = ((p.q.kv + kBlockSize - 1) & ~(kBlockSize - 1)) - key0;
         for (int x = row; x < (r1 - r0) * H * 8; x += 128)
-          *reinterpret_cast<uint4*>(&T.v[st][(x >> 3) % H][r0 + x / (H * 8)][(x & 7) << 4]) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(&T.kv[st][(x >> 3) % H][r0 + x / (H * 8)][(x & 7) << 4]) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       tmem_wait_st();
@@ -574,6 +584,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, const int* pre,
       continue;                        // a narrow piece of one tile has nothing for group B
     }
     const bool whole = p.whole();
+    if (!whole && side == 0 && row == 0) c.cut[c.n_cut++] = p;
     const float inv = whole ? 1.f / l : 1.f;
     alpha *= inv;
     beta *= inv;
@@ -678,45 +689,50 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
 
 // All threads, after the pipeline.
 template <int A, class C>
-__device__ void join(const CrossParams& P, C& c, const int* pre, volatile int* go) {
-  // a CTA's cut items are its first piece's and its last piece's: arrive for both before waiting for either
-  for (int pass = 0; pass < 2; ++pass) {
-    Pieces pieces(P, c, pre);
-    Piece p;
-    while (pieces.next(P, p)) {
-      if (p.whole()) continue;
-      const int first = p.at / c.share, last = (p.at + (p.tiles - 1) * p.step) / c.share, n = last - first + 1;
-      unsigned* count = P.joins + first;
-      if (pass == 0) {
-        if (threadIdx.x == 0) {
-          __threadfence();             // with the barrier before join(): every thread's partial results
-          atomicAdd(count, 1u);
-        }
-        continue;
-      }
-      if (threadIdx.x == 0) {
-        int ok = 1;
-        const uint64_t t0 = globaltimer_ns();
-        while (ld_acquire(count) < (unsigned)n) {
-          if (globaltimer_ns() - t0 > kWaitLimitNs) {
-            set_error(P.err, CB_DEVERR_TIMEOUT);
-            ok = 0;
-            break;
-          }
-        }
-        *go = ok;
-      }
-      __syncthreads();
-      if (*go && !c.abort) {
-        const int rows = p.tokens << P.group_log2, tasks = rows * (A / 4), i = (int)blockIdx.x - first;
-        const int lo = (int)((long long)tasks * i / n), hi = (int)((long long)tasks * (i + 1) / n);
-        if (n <= 6) join_rows<A, 1>(P, p, first, n, lo, hi);
-        else if (n <= 24) join_rows<A, 4>(P, p, first, n, lo, hi);
-        else join_rows<A, 16>(P, p, first, n, lo, hi);
-      }
-      __syncthreads();
-      if (threadIdx.x == 0 && atomicAdd(count, 1u) == 2u * n - 1) *count = 0u;
+__device__ void join(const CrossParams& P, C& c) {
+  if (c.abort) {                       // the others still wait for this CTA's arrivals
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      Pieces pieces(P, c);
+      Piece p;
+      c.n_cut = 0;
+      while (pieces.next(P, p))
+        if (!p.whole()) c.cut[c.n_cut++] = p;
     }
+    __syncthreads();
+  }
+  const int n_cut = c.n_cut;           // its first piece's item, its last piece's, or both
+  auto first_of = [&](const Piece& p) { return p.at / c.share; };
+  if (threadIdx.x == 0 && n_cut) {     // arrive for both before waiting for either
+    __threadfence();                   // with the barrier before join(): every thread's partial results
+    for (int k = 0; k < n_cut; ++k) atomicAdd(P.joins + first_of(c.cut[k]), 1u);
+  }
+  for (int k = 0; k < n_cut; ++k) {
+    const Piece& p = c.cut[k];
+    const int first = first_of(p), n = (p.at + (p.tiles - 1) * p.step) / c.share - first + 1;
+    unsigned* count = P.joins + first;
+    if (threadIdx.x == 0) {
+      int ok = 1;
+      const uint64_t t0 = globaltimer_ns();
+      while (ld_acquire(count) < (unsigned)n) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+          set_error(P.err, CB_DEVERR_TIMEOUT);
+          ok = 0;
+          break;
+        }
+      }
+      c.go = ok;
+    }
+    __syncthreads();
+    if (c.go && !c.abort) {
+      const int rows = p.tokens << P.group_log2, tasks = rows * (A / 4), i = (int)blockIdx.x - first;
+      const int lo = (int)((long long)tasks * i / n), hi = (int)((long long)tasks * (i + 1) / n);
+      if (n <= 6) join_rows<A, 1>(P, p, first, n, lo, hi);
+      else if (n <= 24) join_rows<A, 4>(P, p, first, n, lo, hi);
+      else join_rows<A, 16>(P, p, first, n, lo, hi);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(count, 1u) == 2u * n - 1) *count = 0u;
   }
 }
 
@@ -739,12 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const CrossParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap) {
   using TT = Tiles<A>;
-  constexpr int NS = TT::kStages;
+  constexpr int NS = TT::kRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TT& T = *reinterpret_cast<TT*>(base);
   Ctl<NS>& c = *reinterpret_cast<Ctl<NS>*>(base + sizeof(TT));
-  int* pre = reinterpret_cast<int*>(base + sizeof(TT) + sizeof(Ctl<NS>));
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -756,15 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.o_free[s], 128);
     }
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&c.k_full[s], 1);
-      mbar_init(&c.k_empty[s], 1);
-      mbar_init(&c.v_full[s], 1);
-      mbar_init(&c.v_empty[s], 1);
+      mbar_init(&c.full[s], 1);
+      mbar_init(&c.empty[s], 1);
     }
     mbar_init(&c.ml_full, 128);
     mbar_init(&c.drain, 1);
     c.abort = 0;
     c.any_empty = 0;
+    c.n_cut = 0;
     fence_mbar_init();
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
@@ -777,19 +791,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after();
-  make_plan(P, c, pre);
+  make_plan(P, c);
   const uint32_t tmem = c.tmem_base;
   // three warpgroups of 168 registers a thread at launch: 2 * 208 + 88 = 3 * 168
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      loader<A>(P, &kmap, &vmap, &qmap, T, c, pre);
+      loader<A>(P, &kmap, &vmap, &qmap, T, c);
     } else if (warp == 9) {
-      issuer<A>(P, T, c, pre, tmem);
+      issuer<A>(P, T, c, tmem);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax<A>(P, T, c, pre, tmem, warp >> 2);
+    softmax<A>(P, T, c, tmem, warp >> 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -798,26 +812,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (c.any_empty) zero_rows<A>(P);
-  join<A>(P, c, pre, reinterpret_cast<volatile int*>(&c.ml[0]));
+  join<A>(P, c);
 }
 
-constexpr int kSmemLimit = 232448;
 template <int A>
-constexpr size_t smem_bytes(int n_reqs) {
-  return 1024 + sizeof(Tiles<A>) + sizeof(Ctl<Tiles<A>::kStages>) + (size_t)(n_reqs + 1) * 4;
-}
-static_assert(smem_bytes<128>(kMaxReqs) <= (size_t)kSmemLimit && smem_bytes<64>(kMaxReqs) <= (size_t)kSmemLimit, "shared memory");
-static_assert(sizeof(Tiles<128>) % 16 == 0 && sizeof(Ctl<2>) % 16 == 0 && sizeof(Ctl<4>) % 16 == 0, "control blocks 16-byte aligned");
+constexpr int kSmem = 1024 + (int)sizeof(Tiles<A>) + (int)sizeof(Ctl<Tiles<A>::kRing>);
+static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory");
+static_assert(sizeof(Tiles<128>) % 16 == 0 && sizeof(Tiles<64>) % 16 == 0, "control block 16-byte aligned");
 
 template <int A>
 cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int grid, cudaStream_t stream) {
   const void* kernel = reinterpret_cast<const void*>(cross_kernel<A>);
-  const cudaError_t e = opt_in_smem(kernel, kSmemLimit);
+  const cudaError_t e = opt_in_smem(kernel, kSmem<A>);
   if (e != cudaSuccess) return e;
   CrossParams pc = p;
   void* args[] = {&pc, const_cast<CUtensorMap*>(&maps[0]), const_cast<CUtensorMap*>(&maps[1]),
                   const_cast<CUtensorMap*>(&maps[2])};
-  return cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, smem_bytes<A>(p.n_reqs), stream);
+  return cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, kSmem<A>, stream);
 }
 
 }  // namespace
