@@ -232,20 +232,24 @@ struct Pieces {
 };
 
 // ---------------------------------------------------------------- waits
-template <class C>
-__device__ __forceinline__ bool lane_wait(const CrossParams& P, C& c, uint64_t* bar, uint32_t parity) {
-  if (mbar_wait(bar, parity)) return true;
-  set_error(P.err, CB_DEVERR_TIMEOUT);
-  c.abort = 1;
-  return false;
-}
 __device__ __forceinline__ bool warp_wait(const CrossParams& P, uint64_t* bar, uint32_t parity) {
   const bool ok = mbar_wait(bar, parity);
   if (!ok) set_error(P.err, CB_DEVERR_TIMEOUT);
   return __all_sync(0xffffffffu, ok);
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // ---------------------------------------------------------------- loads (warp 8)
+// A key tile is eight blocks of 16 rows, in boxes of 64 columns: 16 boxes of 2 KB.  One
+// elected lane asks for all of them, from coordinates that are the same in the whole
+// warp: a box per lane took 62 cycles each (1000 a tile, as long as its share of the
+// memory's time), the loads of one lane after the other.
 template <int A, class C>
 __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUtensorMap* vmap, const CUtensorMap* qmap,
                        Tiles<A>& T, C& c) {
@@ -254,22 +258,26 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int none = P.num_blocks * P.n_kv_heads * kBlockSize;      // past the map's rows: zeros
-  const int my_b = (lane / H) & 7, my_h = lane % H;
-  const bool issues = lane < 8 * H;
   const int tok_tile = kTileM >> P.group_log2, group = 1 << P.group_log2;
   uint32_t at = 0, qs = 0;                                        // place in the ring's order, query tiles
   Pieces pieces(P, c);
   Piece p;
-  auto load = [&](const CUtensorMap* map, int y) -> bool {
-    const uint32_t st = at % NS;
-    int ok = 1;
-    if (lane == 0) {
-      ok = lane_wait(P, c, &c.empty[st], ((at / NS) & 1) ^ 1);
-      if (ok) mbar_arrive_expect_tx(&c.full[st], TT::kBytes);
-    }
+  // y: rows of the tile's blocks, in lanes [in4 * 8, in4 * 8 + 8)
+  auto load = [&](const CUtensorMap* map, int y, int in4) -> bool {
+    const uint32_t st = __shfl_sync(FULL, at % NS, 0);
+    if (!warp_wait(P, &c.empty[st], ((at / NS) & 1) ^ 1)) return false;
     ++at;
-    if (!__shfl_sync(FULL, ok, 0)) return false;
-    if (issues) tma_load_2d(&T.kv[st][my_h][my_b * kBlockSize][0], map, my_h * 64, y, &c.full[st]);
+    int rows[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) rows[b] = __shfl_sync(FULL, y, in4 * 8 + b);
+    if (elect_lane()) {
+      mbar_arrive_expect_tx(&c.full[st], TT::kBytes);
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+#pragma unroll
+        for (int h = 0; h < H; ++h) tma_load_2d(&T.kv[st][h][b * kBlockSize][0], map, h * 64, rows[b], &c.full[st]);
+    }
+    __syncwarp();
     return true;
   };
   bool ok = true;
@@ -284,39 +292,34 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
       set_error(P.err, CB_DEVERR_BADBLOCK);
       return none;
     };
-    int e = entry(p.ta), y = none, held = none;
-    int fine = 1;
-    if (lane == 0) {
-      for (int side = 0; side < (p.wide ? 2 : 1) && fine; ++side) {
-        const uint32_t x = qs + side, st = x & 1;
-        fine = lane_wait(P, c, &c.q_empty[st], ((x >> 1) & 1) ^ 1);
-        if (fine) {
-          mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes);
+    int e = entry(p.ta), y = none, before = none;
+    for (int side = 0; ok && side < (p.wide ? 2 : 1); ++side, ++qs) {
+      const uint32_t st = qs & 1;
+      ok = warp_wait(P, &c.q_empty[st], ((qs >> 1) & 1) ^ 1);
+      if (ok && elect_lane()) {
+        mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes);
 #pragma unroll
-          for (int h = 0; h < H; ++h)
-            tma_load_3d(&T.q[st][h][0][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
-        }
+        for (int h = 0; h < H; ++h)
+          tma_load_3d(&T.q[st][h][0][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
       }
+      __syncwarp();
     }
-    ok = __shfl_sync(FULL, fine, 0);
-    if (!ok) break;
-    qs += p.wide ? 2 : 1;
     for (int j = p.ta; ok && j < p.tb; ++j) {
       const int in4 = (j - p.ta) & 3;
       if (in4 == 0) {                  // the entries asked for four tiles ago; the next ones
+        before = y;
         y = row_of(j, e);
         e = j + 4 < p.tb ? entry(j + 4) : -1;
       }
-      const int yb = __shfl_sync(FULL, y, in4 * 8 + my_b);
-      ok = load(kmap, yb);
+      ok = load(kmap, y, in4);
       if (p.wide)
-        ok = ok && load(vmap, yb);
+        ok = ok && load(vmap, y, in4);
       else if (j > p.ta)
-        ok = ok && load(vmap, held);
-      held = yb;
+        ok = ok && load(vmap, in4 ? y : before, (in4 + 3) & 3);
     }
-    if (ok && !p.wide) ok = load(vmap, held);
+    if (ok && !p.wide) ok = load(vmap, y, (p.tb - 1 - p.ta) & 3);
   }
+  if (!ok) c.abort = 1;
   if (c.abort && lane == 0) {          // copies in flight land before shared memory is given back
     for (int par = 0; par < 2; ++par) {
       for (int s = 0; s < NS; ++s) mbar_wait(&c.full[s], par, 20000000ull);
@@ -335,12 +338,6 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
 // are read from uniform registers, which the compiler uses for values of a converged
 // warp: issued from a branch of one lane, each MMA moved its descriptors there first
 // and took about 110 cycles instead of the 64 that it runs.
-__device__ __forceinline__ bool elect_lane() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 template <int A, class C>
 __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem) {
   using TT = Tiles<A>;
