@@ -19,8 +19,8 @@
 // (bf16) is written over its own S and is the A operand of O += P V.
 //
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
-// and V; warp 9: MMA issue; two more complete the third warpgroup, which gives
-// most of its registers to the other two: a row's 128 scores stay in registers.  Scores, running max (base 2, scale folded in), sums
+// and V; warps 9, 10: MMA issue for A, B; one more completes the third warpgroup, which
+// gives most of its registers to the other two: a row's 128 scores stay in registers.  Scores, running max (base 2, scale folded in), sums
 // and O are fp32; the weights are rounded to bf16 for the tensor cores (within 2^-8
 // of each, as the output is of itself) and summed before that rounding.
 // Every wait is bounded.
@@ -54,11 +54,6 @@ struct Tiles {
   uint8_t q[2][kHalves][128][128];
   uint8_t kv[kRing][kHalves][128][128];
 };
-// Place of tile i's K and V in the ring's order, for a piece of n tiles that begins at tile kt.
-__device__ __forceinline__ uint32_t place_k(uint32_t kt, int i, bool wide) { return 2 * kt + 2 * i - (!wide && i > 0); }
-__device__ __forceinline__ uint32_t place_v(uint32_t kt, int i, bool wide, int n) {
-  return 2 * kt + 2 * i + (wide || i == n - 1 ? 1 : 2);
-}
 
 // A request's tokens and stored keys; q_len 0: nothing to do.
 struct Request {
@@ -80,7 +75,7 @@ struct alignas(16) Ctl {
   uint64_t full[NS], empty[NS];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];        // per group
   uint64_t ml_full;                    // ml is written
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem_base;
   volatile int abort;
   int any_empty;                       // a request has tokens and no keys
@@ -329,35 +324,42 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
   }
 }
 
-// ---------------------------------------------------------------- MMA issue (warp 9)
+// ---------------------------------------------------------------- MMA issue (warps 9, 10)
 // Group s's tiles run as a chain S(0) PV(0) S(1) PV(1) ...; S(i + 1) goes out right
 // behind PV(i), which reads P from the columns that S(i + 1) overwrites: operations of
-// one thread run in order.  The two chains' turns alternate.
+// one thread run in order.  A warp issues each group's chain: while one is at its
+// barriers (a few hundred cycles a tile), the tensor core has the other's products.
 //
 // The whole warp waits and computes; one elected lane issues.  Operands of an MMA
 // are read from uniform registers, which the compiler uses for values of a converged
 // warp: issued from a branch of one lane, each MMA moved its descriptors there first
 // and took about 110 cycles instead of the 64 that it runs.
 template <int A, class C>
-__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem) {
+__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A>;
   constexpr int NS = TT::kRing;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, A, 1);
   const unsigned FULL = 0xffffffffu;
   tmem = __shfl_sync(FULL, tmem, 0);
+  side = __shfl_sync(FULL, side, 0);
   const uint32_t base = __shfl_sync(FULL, smem_u32(&T), 0);
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
-  uint32_t kt = 0, qs = 0;
-  uint32_t np[2] = {0, 0}, items[2] = {0, 0};      // P tiles consumed, items begun, per group
+  uint32_t kt = 0, qs = 0, np = 0, items = 0;      // P tiles consumed, items begun
   Pieces pieces(P, c);
-  Piece p;
+  Piece p{};
   bool ok = true;
-  auto arrives = [&](uint64_t* bar) {              // when all that was issued so far is done
-    if (elect_lane()) tc_commit(bar);
+  // Both warps see every buffer, in the loads' order, and give it back: the one that reads it
+  // once its products are done, the other at once.  A wait tells a phase from the one before it
+  // only, so neither may run a ring ahead of a load that the other waits for.
+  auto pass_by = [&](uint64_t* full, uint64_t* empty, uint32_t parity) -> bool {
+    if (!warp_wait(P, full, parity)) return false;
+    if (elect_lane()) mbar_arrive(empty);
+    __syncwarp();
+    return true;
   };
-  auto scores = [&](int side, uint32_t t, uint32_t slot) -> bool {
+  auto scores = [&](uint32_t t, uint32_t slot, bool last) -> bool {
     const uint32_t st = __shfl_sync(FULL, t % NS, 0);
     if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
     tc_fence_after();
@@ -369,15 +371,17 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem) {
         tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
       }
       tc_commit(&c.s_full[side]);
+      tc_commit(&c.empty[st]);
+      if (last) tc_commit(&c.q_empty[slot]);
     }
     __syncwarp();
     return true;
   };
-  auto values = [&](int side, uint32_t t, bool first) -> bool {
+  auto values = [&](uint32_t t, bool first) -> bool {
     const uint32_t st = __shfl_sync(FULL, t % NS, 0);
     if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
-    if (first && !warp_wait(P, &c.o_free[side], (items[side]++ & 1) ^ 1)) return false;
-    if (!warp_wait(P, &c.p_full[side], np[side]++ & 1)) return false;
+    if (first && !warp_wait(P, &c.o_free[side], (items++ & 1) ^ 1)) return false;
+    if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
     tc_fence_after();
     const uint64_t v = v0 + st * (TT::kBytes >> 4);
     if (elect_lane()) {
@@ -386,62 +390,44 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem) {
         tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
                       (!first || ks > 0) ? 1u : 0u);
       tc_commit(&c.o_done[side]);
+      tc_commit(&c.empty[st]);
     }
     __syncwarp();
     return true;
   };
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
-    const int n = p.tb - p.ta;
-    const int na = p.wide ? n : (n + 1) / 2, nb = p.wide ? n : n / 2;
-    const uint32_t sa = __shfl_sync(FULL, qs & 1, 0), sb = p.wide ? sa ^ 1 : sa;
-    ok = warp_wait(P, &c.q_full[sa], (qs >> 1) & 1);
-    if (ok && p.wide) ok = warp_wait(P, &c.q_full[sb], ((qs + 1) >> 1) & 1);
-    if (!ok) break;
-    // places of group s's i-th K and V
-    auto ks = [&](int side, int i) { return place_k(kt, p.wide ? i : 2 * i + side, p.wide); };
-    auto vs = [&](int side, int i) { return place_v(kt, p.wide ? i : 2 * i + side, p.wide, n); };
-    // a wide item's tiles are free once group B has them behind it
-    auto after_s = [&](int side, int i, bool last) {
-      if (!p.wide || side) arrives(&c.empty[ks(side, i) % NS]);
-      if (last) {
-        arrives(&c.q_empty[sa]);
-        if (p.wide) arrives(&c.q_empty[sb]);
-      }
-    };
-    // the piece's last S: B's if the groups have as many, else A's
-    ok = scores(0, ks(0, 0), sa);
-    if (ok) after_s(0, 0, nb == 0);
-    if (ok && nb) {
-      ok = scores(1, ks(1, 0), sb);
-      if (ok) after_s(1, 0, nb == 1 && na == 1);
+    const int n = p.tb - p.ta, mine = p.wide ? n : side ? n / 2 : (n + 1) / 2;
+    const uint32_t x = qs + (p.wide && side), slot = __shfl_sync(FULL, x & 1, 0);
+    if (p.wide) {
+      const uint32_t y = qs + !side;               // the other group's query tile
+      if (side) ok = pass_by(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
+      ok = ok && warp_wait(P, &c.q_full[slot], (x >> 1) & 1);
+      if (!side) ok = ok && pass_by(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
+    } else {
+      ok = mine ? warp_wait(P, &c.q_full[slot], (x >> 1) & 1) : pass_by(&c.q_full[slot], &c.q_empty[slot], (x >> 1) & 1);
     }
-    for (int i = 0; ok && i < na; ++i) {
-      ok = values(0, vs(0, i), i == 0);
-      if (!ok) break;
-      if (!p.wide) arrives(&c.empty[vs(0, i) % NS]);
-      if (i + 1 < na) {
-        ok = scores(0, ks(0, i + 1), sa);
-        if (!ok) break;
-        after_s(0, i + 1, i + 2 == na && nb < na);
+    int ns = 0, nv = 0;
+    auto see = [&](uint32_t t, int tile, bool is_k) -> bool {
+      if (!p.wide && (tile & 1) != side) {
+        const uint32_t st = t % NS;
+        return pass_by(&c.full[st], &c.empty[st], (t / NS) & 1);
       }
-      if (i < nb) {
-        ok = values(1, vs(1, i), i == 0);
-        if (!ok) break;
-        arrives(&c.empty[vs(1, i) % NS]);
-        if (i + 1 < nb) {
-          ok = scores(1, ks(1, i + 1), sb);
-          if (!ok) break;
-          after_s(1, i + 1, i + 2 == nb && nb == na);
-        }
-      }
+      if (is_k) return ++ns, scores(t, slot, ns == mine);
+      return ++nv, values(t, nv == 1);
+    };
+    uint32_t t = 2 * kt;
+    for (int j = 0; ok && j <= n; ++j) {           // as the loader has them
+      if (j < n) ok = see(t++, j, true);
+      if (p.wide && j < n) ok = ok && see(t++, j, false);
+      if (!p.wide && j > 0) ok = ok && see(t++, j - 1, false);
     }
     kt += n;
     qs += p.wide ? 2 : 1;
   }
   if (!ok) c.abort = 1;
-  arrives(&c.drain);                   // what was issued completes before the TMEM is freed
+  if (elect_lane()) tc_commit(&c.drain[side]);     // what was issued completes before the TMEM is freed
   __syncwarp();
-  mbar_wait(&c.drain, 0, 20000000ull);
+  mbar_wait(&c.drain[side], 0, 20000000ull);
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
@@ -538,7 +524,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
       // values behind the last key in its block: whatever the cache holds there, and 0 * inf must
       // not reach O.  In a wide item both groups write the same zeros.
       if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {
-        const uint32_t t = place_v(kt, j, p.wide, n), st = t % NS;
+        const uint32_t t = 2 * (kt + n) - 1, st = t % NS;           // the piece's last buffer
         ok = warp_wait(P, &c.full[st], (t / NS) & 1);
         if (!ok) break;
         const int r0 = p.q.kv - key0, r1 = ((p.q.kv + kBlockSize - 1) & ~(kBlockSize - 1)) - key0;
@@ -761,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&c.q_full[s], 1);
-      mbar_init(&c.q_empty[s], 1);
+      mbar_init(&c.q_empty[s], 2);
+      mbar_init(&c.drain[s], 1);
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 128);
       mbar_init(&c.o_done[s], 1);
@@ -769,10 +756,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 1);
-      mbar_init(&c.empty[s], 1);
+      mbar_init(&c.empty[s], 2);
     }
     mbar_init(&c.ml_full, 128);
-    mbar_init(&c.drain, 1);
     c.abort = 0;
     c.any_empty = 0;
     c.n_cut = 0;
@@ -795,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
       loader<A>(P, &kmap, &vmap, &qmap, T, c);
-    } else if (warp == 9) {
-      issuer<A>(P, T, c, tmem);
+    } else if (warp < 11) {
+      issuer<A>(P, T, c, tmem, warp - 9);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
