@@ -37,6 +37,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kRows = 256;             // of a wide item
 constexpr float kNoKey = -__builtin_huge_valf();
+constexpr float kMostSum = 1024.f;     // of a tile's weights: none of them is over 2^10
 
 // Cost of a key tile of a narrow and of a wide item, and of an item's start.
 constexpr int kNarrow = 1, kWide = 2, kLead = 1;
@@ -481,45 +482,59 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
 #pragma unroll
           for (int k = 0; k < 128; ++k) s[k] = key0 + k < p.q.kv ? s[k] : kNoKey;
         }
-        float a[4] = {kNoKey, kNoKey, kNoKey, kNoKey};
+        // The weights refer to the running max m of an item's first tile, and O and their sum with
+        // them: that is exact whatever m is.  A tile's own max is looked for only if its weights' sum
+        // says that one may be large (or NaN, or m has had no key but -inf yet); then m moves up, O is
+        // scaled and the weights are made again.
+        const uint64_t sl2x2 = f2(sl2, sl2);
+        float alpha = 1.f, add;
+        bool known = i > 0, bad = i == 0;
+#pragma unroll 1
+        while (true) {
+          if (!known) {
+            float a[4] = {kNoKey, kNoKey, kNoKey, kNoKey};
 #pragma unroll
-        for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
-        const float mt = max3(a[0], a[1], fmaxf(a[2], a[3])) * sl2;
-        // O keeps the max that it was scaled by until the new one is 2^8 times that: exact all
-        // the same, since the weights, their sum and O refer to one max
-        const float mn = fmaxf(m, mt);
-        const bool need = valid && mn > m + 8.f;
-        float alpha = 1.f;
-        if (need) {
-          alpha = ex2(m - mn);
-          m = mn;
-        }
-        if (i > 0 && __any_sync(FULL, need)) {
-          ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          rescale<A>(o_at, alpha);
-        }
-        const float ms = m == kNoKey ? 0.f : m;                    // no key so far but -inf: weights 0
-        const uint64_t sl2x2 = f2(sl2, sl2), nm2 = f2(-ms, -ms);
-        uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float x0, x1;
-            f2split(ffma2(f2(s[h * 32 + 2 * k], s[h * 32 + 2 * k + 1]), sl2x2, nm2), x0, x1);
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            sum[k & 1] = fadd2(sum[k & 1], f2(p0, p1));
-            pk[k] = pack_bf16(p0, p1);
+            for (int k = 0; k < 128; k += 2) a[(k >> 1) & 3] = max3(a[(k >> 1) & 3], s[k], s[k + 1]);
+            const float mn = fmaxf(m, max3(a[0], a[1], fmaxf(a[2], a[3])) * sl2);
+            if (bad && mn > m) {           // rows without need keep theirs: no row's result depends on another
+              alpha = ex2(m - mn);
+              m = mn;
+            }
+            if (i > 0) {
+              ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+              rescale<A>(o_at, alpha);
+              tmem_wait_st();            // with the weights that are made again
+            }
           }
-          tmem_st16u(s_at + h * 16, pk);
+          const float ms = m == kNoKey ? 0.f : m;                  // no key so far but -inf: weights 0
+          const uint64_t nm2 = f2(-ms, -ms);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x0, x1;
+              f2split(ffma2(f2(s[h * 32 + 2 * k], s[h * 32 + 2 * k + 1]), sl2x2, nm2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              sum[k & 1] = fadd2(sum[k & 1], f2(p0, p1));
+              pk[k] = pack_bf16(p0, p1);
+            }
+            tmem_st16u(s_at + h * 16, pk);
+          }
+          float t[4];
+          f2split(sum[0], t[0], t[1]);
+          f2split(sum[1], t[2], t[3]);
+          add = (t[0] + t[1]) + (t[2] + t[3]);
+          if (!known) break;
+          bad = valid && !(add <= kMostSum && m > kNoKey);
+          if (!__any_sync(FULL, bad)) break;
+          known = false;
         }
-        float t[4];
-        f2split(sum[0], t[0], t[1]);
-        f2split(sum[1], t[2], t[3]);
-        l = l * alpha + ((t[0] + t[1]) + (t[2] + t[3]));
+        if (!ok) break;
+        l = l * alpha + add;
       }
       // values behind the last key in its block: whatever the cache holds there, and 0 * inf must
       // not reach O.  In a wide item both groups write the same zeros.
