@@ -244,9 +244,9 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  * of out that belong to no request are left as they were.
  * Precision: scores, softmax statistics and sums are fp32; a weight is rounded to
  * bf16 before it multiplies v.
- * Errors: those of cb_paged_attention; steps whose work could pass 2^30 units (2
- * max_kv_len / 128 + 1 for every KV head and 256 n_kv_heads / n_q_heads tokens) are
- * refused with CB_EINVAL.  A request whose lengths are out of range is reported
+ * Errors: those of cb_paged_attention; steps whose work could pass 2^30 units (4
+ * max_kv_len / 128 + 6 for every KV head of every request's 256 n_kv_heads /
+ * n_q_heads tokens) are refused with CB_EINVAL.  A request whose lengths are out of range is reported
  * and its rows stay as they were; the rows of a bad block id count as zeros. */
 int cb_paged_cross_attention(const void* q, const int32_t* cu_q_lens, const int32_t* kv_lens, const int32_t* block_tables,
                              int max_blocks_per_seq, int n_reqs, int n_tokens, int max_q_len, int max_kv_len,

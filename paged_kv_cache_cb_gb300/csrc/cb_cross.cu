@@ -39,9 +39,13 @@ constexpr int kRows = 256;             // of a wide item
 constexpr float kNoKey = -__builtin_huge_valf();
 constexpr float kMostSum = 1024.f;     // of a tile's weights: none of them is over 2^10
 
-// Cost of a key tile of a narrow and of a wide item, and of an item's start.
-constexpr int kNarrow = 1, kWide = 2, kLead = 1;
-constexpr int kLeast = 4;              // of a CTA's share
+// Cost of a key tile of a narrow and of a wide item, and of an item's start and end (its
+// query tile's load, its output), which take as long as one and a half tiles of a wide
+// item.  Four prompts of 5 to 1999 tokens: 360 us with a start counted as half a tile of
+// a wide item, 343 as one, 333 as one and a half, 331 as two; 64 x 4 beams: 386, 384, 383,
+// 388.  A tile of a wide item at 3 or 5 instead of 4: 343 (start 4), 349 (start 6).
+constexpr int kNarrow = 2, kWide = 4, kLead = 6;
+constexpr int kLeast = 8;              // of a CTA's share
 
 // K and V tiles share one ring of buffers, in the order of their use: a wide item's
 // K(0) V(0) K(1) V(1) .., a narrow one's K(0) K(1) V(0) K(2) V(1) .. V(n - 1), since
