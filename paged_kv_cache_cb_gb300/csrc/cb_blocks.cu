@@ -6,9 +6,10 @@
 // ceil(lens[r] / 16) entries of its table row.
 //
 // Each operation is one kernel of one thread-block cluster.  They touch a few
-// ints per row and block, so what they cost is the chain of dependent phases --
-// counts, ranks, then writes that need both -- and a cluster's hardware barrier
-// (under half a microsecond) orders those without a grid-wide wait.  Blocks are
+// ints per row and block, so what they cost is the chain of dependent reads --
+// lengths, entries, counts, ranks -- of 0.3 to 0.7 us each.  A cluster's hardware
+// barrier orders the phases without a grid-wide wait; what is a few ints per row
+// every CTA reads and works out for all rows, instead of waiting for another's.  Blocks are
 // always taken from the lowest free id on, in row order: ranks come from prefix
 // sums, never from the order in which atomics arrive, so a call's result is the
 // same every time.  The atomics on refs are integer sums.
@@ -85,6 +86,7 @@ __device__ __forceinline__ Slice my_slice(int num_blocks) {
 constexpr int kPer = 4;                // blocks per thread and round of a pass over the pool
 
 // Number of blocks of [lo, hi) with pred(refs); a single CTA stops once it has `enough`.
+// (What the first pass has read the second finds in L1: nothing else writes there in between.)
 template <class F>
 __device__ int count_blocks(const int32_t* refs, int lo, int hi, int enough, int* red, F pred) {
   int n = 0;
@@ -93,7 +95,7 @@ __device__ int count_blocks(const int32_t* refs, int lo, int hi, int enough, int
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const long long i = at + k * kThreads + threadIdx.x;
-      if (i < hi) mine += pred(__ldcg(refs + i)) ? 1 : 0;
+      if (i < hi) mine += pred(refs[i]) ? 1 : 0;
     }
     cta_scan(mine, red, &all);
     n += all;
@@ -111,7 +113,7 @@ __device__ void visit_blocks(const int32_t* refs, int lo, int hi, int before, in
     const long long first = at + (long long)threadIdx.x * kPer;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      v[k] = first + k < hi ? __ldcg(refs + first + k) : 0;
+      v[k] = first + k < hi ? refs[first + k] : 0;
       mine += first + k < hi && pred(v[k]) ? 1 : 0;
     }
     int rank = before + cta_scan(mine, red, &all);
@@ -127,11 +129,14 @@ __device__ void visit_blocks(const int32_t* refs, int lo, int hi, int before, in
 
 // Sum of the CTAs' counts and of those before this one.
 __device__ __forceinline__ void sum_counts(const int* counts, int* before, int* all) {
+  int c[kCluster];
+#pragma unroll
+  for (int b = 0; b < kCluster; ++b) c[b] = b < (int)gridDim.x ? __ldcg(counts + b) : 0;
   *before = *all = 0;
-  for (int b = 0; b < (int)gridDim.x; ++b) {
-    const int c = __ldcg(counts + b);
-    *before += b < (int)blockIdx.x ? c : 0;
-    *all += c;
+#pragma unroll
+  for (int b = 0; b < kCluster; ++b) {
+    *before += b < (int)blockIdx.x ? c[b] : 0;
+    *all += c[b];
   }
 }
 
@@ -144,8 +149,7 @@ struct IsLive {
 constexpr int kNoLimit = 0x7fffffff;
 
 // A row's length as far as its table row goes.
-__device__ __forceinline__ int row_len(const Pool& P, int r, bool report) {
-  const int n = __ldcg(P.lens + r);
+__device__ __forceinline__ int fit_len(const Pool& P, int n, bool report) {
   const long long most = (long long)P.width * kBlockSize;
   if (n >= 0 && n <= most) return n;
   if (report) set_error(P.err, CB_DEVERR_BADLEN);
@@ -158,150 +162,179 @@ __device__ __forceinline__ bool names_block(const Pool& P, int e) {
   return e >= 0 && e < P.num_blocks;
 }
 
+constexpr int kUnroll = 4;             // reads of a lane in flight in a row's passes
+
 // ---------------------------------------------------------------- fork
 // Row j becomes the first keep[j] tokens of row parents[j] as it was before the
-// call.  Phases, a barrier after each:
+// call.  Every CTA knows all rows' parents, lengths and partial last blocks, and
+// has the latter in a hash table: how many rows end in each, and the lowest.
 //   A  (warp per row) counts of the blocks that the row lets go of and takes;
-//      equal entries of both rows cancel.  The old row is saved where it changes.
-//   B  free blocks of each CTA's slice; rows whose partial last block is held by
-//      another row too need a copy, but for the lowest of its holders if all of
-//      them have it as their partial last block.
+//      equal entries of both rows cancel.  A row that changes is saved if others
+//      come from it.
+//   B  rows whose partial last block is held elsewhere too need a copy, but for
+//      the lowest of its holders if all of them end in it.
 //   C  the k-th row in need gets the k-th lowest free block; tables are written.
-//   D  the copies' entries, counts, pairs and all lengths.
+//   D  the copies' entries and counts, pairs and lengths.
+// A barrier after A, after C's counting of free blocks and after C; the last two
+// only if a row is in need.
 struct ForkArgs {
   Pool P;
   const int32_t* parents;
   const int32_t* keep;                 // nullptr: all
   int32_t* pairs;                      // [n_rows][2]
+  int hash;                            // entries of the hash table, a power of two > n_rows
   // workspace
   int32_t* old_rows;                   // [n_rows][width]
-  int32_t* has;                        // [n_rows] tokens after the call
-  int32_t* last;                       // [n_rows] partial last block, -1: none
-  int32_t* need;                       // [n_rows]
-  int32_t* rank;                       // [n_rows] among the rows in need, -1: none
   int32_t* fresh;                      // [n_rows] lowest free blocks
   int32_t* counts;                     // [kCluster]
 };
+constexpr int kForkInts = 6;           // shared ints per row, and kHashInts per entry of the table
+constexpr int kHashInts = 3;
 
 struct ForkRow {
   int parent, had, has;                // parent -1: none; tokens before and after
 };
-// Reads lens: not after the phase that writes them has begun.
-__device__ __forceinline__ ForkRow fork_row(const ForkArgs& A, int j, bool report) {
-  ForkRow f;
-  f.parent = __ldg(A.parents + j);
-  if (f.parent >= A.P.n_rows) {
-    if (report) set_error(A.P.err, CB_DEVERR_BADLEN);
-    f.parent = -1;
-  }
-  f.had = row_len(A.P, j, report);
-  f.has = f.parent < 0 ? 0 : f.parent == j ? f.had : row_len(A.P, f.parent, false);
-  const int k = A.keep ? __ldg(A.keep + j) : -1;
-  if (k >= 0) f.has = min(f.has, k);
-  return f;
-}
-__device__ __forceinline__ bool fork_changes(const ForkRow& f, int j) {
-  return f.parent != j || blocks_of(f.has) < blocks_of(f.had);
-}
 
 __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs A) {
   __shared__ int red[kWarps];
+  extern __shared__ int shared_ints[];
   const Pool& P = A.P;
+  const int n = P.n_rows;
+  int* parent = shared_ints;
+  int* had = parent + n;
+  int* has = had + n;
+  int* last = has + n;                 // partial last block, -1: none
+  int* rank = last + n;                // among the rows in need, -1: none
+  int* source = rank + n;              // some other row comes from this one
+  int* key = source + n;               // block, -1: empty
+  int* ends = key + A.hash;            // rows that end in it
+  int* lowest = ends + A.hash;
   const int lane = threadIdx.x & 31;
   const int w0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
+  for (int j = threadIdx.x; j < n; j += kThreads) {
+    const int p = __ldg(A.parents + j), l = __ldcg(P.lens + j);
+    const int k = A.keep ? __ldg(A.keep + j) : -1;
+    if (p >= n && blockIdx.x == 0) set_error(P.err, CB_DEVERR_BADLEN);
+    parent[j] = p >= n ? -1 : p;
+    had[j] = fit_len(P, l, blockIdx.x == 0);
+    has[j] = k;
+    source[j] = 0;
+  }
+  for (int h = threadIdx.x; h < A.hash; h += kThreads) {
+    key[h] = -1;
+    ends[h] = 0;
+    lowest[h] = n;
+  }
+  __syncthreads();
+  auto row = [&](int j) { return ForkRow{parent[j], had[j], has[j]}; };
+  auto changes = [&](const ForkRow& f, int j) { return f.parent != j || blocks_of(f.has) < blocks_of(f.had); };
+  auto place = [&](int e) {            // of block e in the hash table, or of the empty entry for it
+    unsigned h = (unsigned)e * 2654435761u >> 16 & (A.hash - 1);
+    while (key[h] != e && key[h] != -1) h = (h + 1) & (A.hash - 1);
+    return h;
+  };
+  for (int j = threadIdx.x; j < n; j += kThreads) {
+    const int p = parent[j], k = has[j];
+    int m = p < 0 ? 0 : had[p];
+    if (k >= 0) m = min(m, k);
+    has[j] = m;
+    if (p >= 0 && p != j) source[p] = 1;
+    int e = -1;
+    if (m % kBlockSize) {
+      e = __ldcg(P.tables + (size_t)p * P.width + m / kBlockSize);
+      if (!names_block(P, e)) e = -1;
+    }
+    last[j] = e;
+    if (e >= 0) {
+      unsigned h = place(e);
+      for (int got; (got = atomicCAS(key + h, -1, e)) != -1 && got != e;) h = (h + 1) & (A.hash - 1);
+      atomicAdd(ends + h, 1);
+      atomicMin(lowest + h, j);
+    }
+  }
+  __syncthreads();
   // A
-  for (int j = w0; j < P.n_rows; j += nw) {
-    const ForkRow f = fork_row(A, j, lane == 0);
+  for (int j = w0; j < n; j += nw) {
+    const ForkRow f = row(j);
     const int ob = blocks_of(f.had), nb = blocks_of(f.has);
+    if (!changes(f, j)) continue;
     const int32_t* mine = P.tables + (size_t)j * P.width;
     const int32_t* theirs = P.tables + (size_t)max(f.parent, 0) * P.width;
     int32_t* save = A.old_rows + (size_t)j * P.width;
-    const bool changes = fork_changes(f, j);
-    int last = -1;
-    for (int c = lane; c < max(ob, nb); c += 32) {
-      const int a = c < ob ? __ldcg(mine + c) : -1;
-      const int b = c >= nb ? -1 : f.parent == j ? a : __ldcg(theirs + c);
-      if (changes && c < ob) save[c] = a;
-      if (a != b) {
-        if (names_block(P, a)) atomicAdd(P.refs + a, -1);
-        if (names_block(P, b)) atomicAdd(P.refs + b, 1);
-      }
-      if (c == nb - 1 && f.has % kBlockSize && names_block(P, b)) last = b;
-    }
+    const bool saves = source[j];
+    for (int c0 = lane; c0 < max(ob, nb); c0 += 32 * kUnroll) {
+      int a[kUnroll], b[kUnroll];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, d));
-    if (lane == 0) {
-      A.last[j] = last;
-      A.has[j] = f.has;
+      for (int k = 0; k < kUnroll; ++k) {
+        const int c = c0 + 32 * k;
+        a[k] = c < ob ? __ldcg(mine + c) : -1;
+        b[k] = c >= nb ? -1 : f.parent == j ? a[k] : __ldcg(theirs + c);
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const int c = c0 + 32 * k;
+        if (saves && c < ob) save[c] = a[k];
+        if (a[k] == b[k]) continue;
+        if (names_block(P, a[k])) atomicAdd(P.refs + a[k], -1);
+        if (names_block(P, b[k])) atomicAdd(P.refs + b[k], 1);
+      }
     }
   }
   sync_all();
   // B
-  for (int j = w0; j < P.n_rows; j += nw) {
-    const int e = __ldcg(A.last + j);
-    int need = 0;
-    const int held = e >= 0 ? __ldcg(P.refs + e) : 1;
-    if (held != 1) {
-      int n = 0, low = P.n_rows;
-      for (int i = lane; i < P.n_rows; i += 32)
-        if (__ldcg(A.last + i) == e) {
-          ++n;
-          low = min(low, i);
-        }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        n += __shfl_xor_sync(0xffffffffu, n, d);
-        low = min(low, __shfl_xor_sync(0xffffffffu, low, d));
-      }
-      need = !(n == held && low == j);
-    }
-    if (lane == 0) A.need[j] = need;
-  }
-  const Slice s = my_slice(P.num_blocks);
-  if (gridDim.x > 1) {
-    const int n = count_blocks(P.refs, s.lo, s.hi, kNoLimit, red, IsFree());
-    if (threadIdx.x == 0) A.counts[blockIdx.x] = n;
-  }
-  sync_all();
-  // C
   int wanted = 0;
-  for (int at = 0; at < P.n_rows; at += kThreads) {
-    const int j = at + threadIdx.x;
-    const int n = j < P.n_rows ? __ldcg(A.need + j) : 0;
-    int all;
-    const int rank = wanted + cta_scan(n, red, &all);
-    if (blockIdx.x == 0 && j < P.n_rows) A.rank[j] = n ? rank : -1;
-    wanted += all;
+  for (int at = 0; at < n; at += kThreads) {
+    const int j = at + threadIdx.x, e = j < n ? last[j] : -1;
+    int need = 0, all;
+    if (e >= 0) {
+      const int held = __ldcg(P.refs + e);
+      const unsigned h = place(e);
+      need = held != 1 && !(ends[h] == held && lowest[h] == j);
+    }
+    const int k = wanted + cta_scan(need, red, &all);
+    if (j < n) rank[j] = need ? k : -1;
+    wanted += all;                     // the same in every CTA
   }
+  // C
+  const Slice s = my_slice(P.num_blocks);
   int before = 0, found = 0;
-  if (gridDim.x > 1)
-    sum_counts(A.counts, &before, &found);
-  else if (wanted)
-    found = count_blocks(P.refs, s.lo, s.hi, wanted, red, IsFree());
-  visit_blocks(P.refs, s.lo, s.hi, before, wanted, red, IsFree(), [&](int b, int r, int rank) {
-    if (r == 0 && rank < wanted) A.fresh[rank] = b;
-  });
-  for (int j = w0; j < P.n_rows; j += nw) {
-    const ForkRow f = fork_row(A, j, false);
+  if (wanted) {
+    found = count_blocks(P.refs, s.lo, s.hi, gridDim.x > 1 ? kNoLimit : wanted, red, IsFree());
+    if (gridDim.x > 1) {
+      if (threadIdx.x == 0) A.counts[blockIdx.x] = found;
+      sync_all();
+      sum_counts(A.counts, &before, &found);
+    }
+    visit_blocks(P.refs, s.lo, s.hi, before, wanted, red, IsFree(), [&](int b, int r, int k) {
+      if (r == 0 && k < wanted) A.fresh[k] = b;
+    });
+  }
+  for (int j = w0; j < n; j += nw) {
+    const ForkRow f = row(j);
     const int ob = blocks_of(f.had), nb = blocks_of(f.has);
     int32_t* mine = P.tables + (size_t)j * P.width;
     if (f.parent >= 0 && f.parent != j) {
       // the parent's row as it was: saved if it changes too, else untouched so far
-      const bool saved = fork_changes(fork_row(A, f.parent, false), f.parent);
+      const bool saved = changes(row(f.parent), f.parent);
       const int32_t* theirs = (saved ? A.old_rows : P.tables) + (size_t)f.parent * P.width;
-      for (int c = lane; c < nb; c += 32) mine[c] = __ldcg(theirs + c);
+      for (int c0 = lane; c0 < nb; c0 += 32 * kUnroll) {
+        int b[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) b[k] = c0 + 32 * k < nb ? __ldcg(theirs + c0 + 32 * k) : 0;
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k)
+          if (c0 + 32 * k < nb) mine[c0 + 32 * k] = b[k];
+      }
     }
     for (int c = nb + lane; c < ob; c += 32) mine[c] = -1;
   }
-  sync_all();
+  if (wanted) sync_all();
   // D
-  for (int j = blockIdx.x * kThreads + threadIdx.x; j < P.n_rows; j += gridDim.x * kThreads) {
-    int has = __ldcg(A.has + j), src = -1, dst = -1;
-    const int rank = __ldcg(A.rank + j);
-    if (rank >= 0) {
-      const int e = __ldcg(A.last + j);
-      const int b = rank < found ? __ldcg(A.fresh + rank) : -1;
-      P.tables[(size_t)j * P.width + blocks_of(has) - 1] = b;
+  for (int j = blockIdx.x * kThreads + threadIdx.x; j < n; j += gridDim.x * kThreads) {
+    int m = has[j], src = -1, dst = -1;
+    if (rank[j] >= 0) {
+      const int e = last[j], b = rank[j] < found ? __ldcg(A.fresh + rank[j]) : -1;
+      P.tables[(size_t)j * P.width + m / kBlockSize] = b;
       atomicAdd(P.refs + e, -1);
       if (b >= 0) {
         P.refs[b] = 1;
@@ -309,10 +342,10 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs A) {
         dst = b;
       } else {
         set_error(P.err, CB_DEVERR_NOBLOCK);
-        has = has / kBlockSize * kBlockSize;
+        m = m / kBlockSize * kBlockSize;
       }
     }
-    P.lens[j] = has;
+    P.lens[j] = m;
     A.pairs[2 * j] = src;
     A.pairs[2 * j + 1] = dst;
   }
@@ -328,8 +361,18 @@ struct GrowArgs {
   int32_t* ctx;                        // [n_rows]
   int64_t* slots;                      // [n_tokens]
   int n_tokens;
+  int many;                            // slots_kernel follows
   int32_t* counts;                     // workspace: [kCluster]
 };
+
+// Slot of position pos of row i (pos < 0: none).
+__device__ __forceinline__ int64_t slot_of(const Pool& P, int i, int pos) {
+  if (pos < 0) return -1;
+  const int e = __ldcg(P.tables + (size_t)i * P.width + pos / kBlockSize);
+  if (e >= 0 && e < P.num_blocks) return (int64_t)e * kBlockSize + pos % kBlockSize;
+  set_error(P.err, CB_DEVERR_BADBLOCK);
+  return -1;
+}
 
 // The last i of [0, n) with a[i] <= x (a[0] <= x).
 __device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
@@ -355,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const GrowArgs A) {
     int need = 0, all;
     if (i < n) {
       const int q0 = __ldg(A.cu + i), q1 = __ldg(A.cu + i + 1), raw = __ldcg(P.lens + i);
-      const int l = row_len(P, i, blockIdx.x == 0);
+      const int l = fit_len(P, raw, blockIdx.x == 0);
       const bool no = l != raw || q0 < 0 || q1 < q0 || q1 > A.n_tokens ||
                       (long long)l + (q1 - q0) > (long long)P.width * kBlockSize;
       if (no && blockIdx.x == 0) set_error(P.err, CB_DEVERR_BADLEN);
@@ -379,22 +422,30 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const GrowArgs A) {
   sync_all();                          // every CTA has read lens; counts
   if (wanted) {
     if (gridDim.x > 1) sum_counts(A.counts, &before, &found);
+    int i = n;                         // a thread's free blocks go to rows in order
     visit_blocks(P.refs, s.lo, s.hi, before, wanted, red, IsFree(), [&](int b, int r, int rank) {
       if (r != 0 || rank >= wanted) return;
       // the row whose needs reach past rank: the first with ends > rank
-      int lo = 0, hi = n - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (ends[mid] > rank) hi = mid;
-        else lo = mid + 1;
+      if (i == n || ends[i] <= rank) {
+        if (i + 1 < n && ends[i + 1] > rank) {
+          ++i;
+        } else {
+          int lo = 0, hi = n - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (ends[mid] > rank) hi = mid;
+            else lo = mid + 1;
+          }
+          i = lo;
+        }
       }
-      if (ends[lo] > found) return;    // not enough for the whole row: it gets none
-      const int first = lo ? ends[lo - 1] : 0;
-      P.tables[(size_t)lo * P.width + blocks_of(len[lo]) + rank - first] = b;
+      if (ends[i] > found) return;     // not enough for the whole row: it gets none
+      const int first = i ? ends[i - 1] : 0;
+      P.tables[(size_t)i * P.width + blocks_of(len[i]) + rank - first] = b;
       P.refs[b] = 1;
     });
+    sync_all();
   }
-  sync_all();
   auto granted = [&](int i) {
     return !bad[i] && (ends[i] <= found || ends[i] == (i ? ends[i - 1] : 0));
   };
@@ -404,18 +455,46 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const GrowArgs A) {
     A.ctx[i] = len[i];
     if (ok) P.lens[i] = len[i] + cu[i + 1] - cu[i];
   }
+  if (A.many) return;                  // slots_kernel
   for (int t = blockIdx.x * kThreads + threadIdx.x; t < A.n_tokens; t += gridDim.x * kThreads) {
-    int64_t slot = -1;
     const int i = last_at_most(cu, n, t);
-    if (t >= cu[i] && t < cu[i + 1] && granted(i)) {
-      const int pos = len[i] + t - cu[i];
-      const int e = __ldcg(P.tables + (size_t)i * P.width + pos / kBlockSize);
-      if (e >= 0 && e < P.num_blocks)
-        slot = (int64_t)e * kBlockSize + pos % kBlockSize;
-      else
-        set_error(P.err, CB_DEVERR_BADBLOCK);
+    int pos = -1;
+    if (t >= cu[i] && t < cu[i + 1] && granted(i)) pos = len[i] + t - cu[i];
+    A.slots[t] = slot_of(P, i, pos);
+  }
+}
+
+// The slots of many tokens, on the whole device: rows that have grown say so by
+// their lengths.  A warp takes 32 * kRun tokens, whose entries are read together.
+constexpr int kRun = 8, kSlotThreads = 256;
+__global__ void __launch_bounds__(kSlotThreads) slots_kernel(const GrowArgs A) {
+  __shared__ int cu[kMaxReqs + 1], len[kMaxReqs];
+  const Pool& P = A.P;
+  const int n = P.n_rows, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = threadIdx.x; i <= n; i += kSlotThreads) {
+    cu[i] = __ldg(A.cu + i);
+    if (i == n) break;
+    const int was = __ldcg(A.ctx + i), now = __ldcg(P.lens + i);
+    len[i] = (long long)was + __ldg(A.cu + i + 1) - cu[i] == now ? was : -1;
+  }
+  __syncthreads();
+  const int w0 = blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5), nw = gridDim.x * (kSlotThreads / 32);
+  for (long long t0 = (long long)w0 * 32 * kRun; t0 < A.n_tokens; t0 += (long long)nw * 32 * kRun) {
+    int i = last_at_most(cu, n, (int)t0);
+    int64_t slot[kRun];
+#pragma unroll
+    for (int k = 0; k < kRun; ++k) {
+      const long long t = t0 + k * 32 + lane;
+      slot[k] = -1;
+      if (t >= A.n_tokens) continue;
+      if (t >= cu[i + 1]) i = i + 1 < n && t < cu[i + 2] ? i + 1 : last_at_most(cu, n, (int)t);
+      const bool in = t >= cu[i] && t < cu[i + 1] && len[i] >= 0;
+      slot[k] = slot_of(P, i, in ? len[i] + (int)t - cu[i] : -1);
     }
-    A.slots[t] = slot;
+#pragma unroll
+    for (int k = 0; k < kRun; ++k)
+      if (t0 + k * 32 + lane < A.n_tokens) A.slots[t0 + k * 32 + lane] = slot[k];
   }
 }
 
@@ -429,8 +508,8 @@ struct CompactArgs {
   int max_pairs;
   int32_t* result;                     // [2] live blocks, pairs written
   // workspace
+  int2* movers;                        // [num_blocks / 2 + 1] (block, holders)
   int32_t* holes;                      // [num_blocks / 2 + 1]
-  int32_t* movers;                     // the same
   int32_t* counts;                     // [kCluster]
 };
 
@@ -440,17 +519,18 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs A) 
   const int lane = threadIdx.x & 31, nb = P.num_blocks;
   const Slice s = my_slice(nb);
   int before = 0, live = count_blocks(P.refs, s.lo, s.hi, kNoLimit, red, IsLive());
+  int under = 0;                       // live blocks under the line: whole slices, then the one that it cuts
   if (gridDim.x > 1) {
     if (threadIdx.x == 0) A.counts[blockIdx.x] = live;
     sync_all();
     sum_counts(A.counts, &before, &live);
+    const int size = slice_size(nb), cut = live / size;
+#pragma unroll
+    for (int b = 0; b < kCluster; ++b) under += b < cut ? __ldcg(A.counts + b) : 0;
+    under += count_blocks(P.refs, cut * size, live, kNoLimit, red, IsLive());
+  } else {
+    under = count_blocks(P.refs, 0, live, kNoLimit, red, IsLive());
   }
-  // live blocks under the line: whole slices, then the slice that the line cuts
-  const int size = slice_size(nb), cut = live / size;
-  int under = 0;
-  for (int b = 0; b < cut && gridDim.x > 1; ++b) under += __ldcg(A.counts + b);
-  const long long cut_at = gridDim.x > 1 ? (long long)cut * size : 0;
-  under += count_blocks(P.refs, (int)min((long long)live, cut_at), live, kNoLimit, red, IsLive());
   const int moves = live - under, done = min(moves, A.max_pairs);
   visit_blocks(P.refs, s.lo, s.hi, before, kNoLimit, red, IsLive(), [&](int b, int r, int rank) {
     const bool is = r > 0;
@@ -458,18 +538,19 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs A) 
       if (!is) A.holes[b - rank] = b;
       A.map[b] = is ? b : -1;
     } else {
-      if (is) A.movers[rank - under] = b;
+      if (is) A.movers[rank - under] = make_int2(b, r);
       if (!is || rank - under >= done) A.map[b] = is ? b : -1;
     }
   });
-  sync_all();
+  if (moves) sync_all();
   for (int k = blockIdx.x * kThreads + threadIdx.x; k < A.max_pairs; k += gridDim.x * kThreads) {
     int src = -1, dst = -1;
     if (k < done) {
-      src = __ldcg(A.movers + k);
+      const int2 m = __ldcg(A.movers + k);
+      src = m.x;
       dst = __ldcg(A.holes + k);
       A.map[src] = dst;
-      P.refs[dst] = __ldcg(P.refs + src);
+      P.refs[dst] = m.y;
       P.refs[src] = 0;
     }
     A.pairs[2 * k] = src;
@@ -481,12 +562,16 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs A) 
   const int w0 = blockIdx.x * kWarps + (threadIdx.x >> 5), nw = gridDim.x * kWarps;
   for (int j = w0; j < P.n_rows; j += nw) {
     int32_t* row = P.tables + (size_t)j * P.width;
-    const int n = blocks_of(row_len(P, j, lane == 0));
-    for (int c = lane; c < n; c += 32) {
-      const int e = __ldcg(row + c);
-      if (!names_block(P, e)) continue;
-      const int to = __ldcg(A.map + e);
-      if (to >= 0 && to != e) row[c] = to;
+    const int n = blocks_of(fit_len(P, __ldcg(P.lens + j), lane == 0));
+    for (int c0 = lane; c0 < n; c0 += 32 * kUnroll) {
+      int e[kUnroll], to[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) e[k] = c0 + 32 * k < n ? __ldcg(row + c0 + 32 * k) : -1;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) to[k] = names_block(P, e[k]) ? __ldcg(A.map + e[k]) : -1;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        if (to[k] >= 0 && to[k] != e[k]) row[c0 + 32 * k] = to[k];
     }
   }
 }
@@ -581,20 +666,41 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0;
 
 // One cluster of kCluster CTAs, or one CTA where there is little to do.
 template <class Args>
-cudaError_t launch_pool(void (*kernel)(const Args), const Args& a, bool large, cudaStream_t stream) {
+cudaError_t launch_pool(void (*kernel)(const Args), const Args& a, bool large, size_t smem, cudaStream_t stream) {
+  if (!large) {
+    kernel<<<1, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(large ? kCluster : 1);
+  cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = large ? kCluster : 1;
+  attr[0].val.clusterDim.x = kCluster;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
+// A kernel that is placed while the one before it on the stream ends, and waits for it itself.
+template <class Args>
+cudaError_t launch_behind(void (*kernel)(const Args), const Args& a, int ctas, int threads, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+constexpr int kManyTokens = 8192;      // slots that one cluster writes itself
 // A single CTA goes over up to this many blocks and rows.
 constexpr int kSmallPool = 8192, kSmallRows = 64;
 
@@ -619,8 +725,8 @@ int guarded(F call) {
 }
 
 // Ints of workspace: the fork's and the compaction's.
-size_t fork_ints(int n_rows, int width) { return (size_t)n_rows * width + (size_t)n_rows * 5 + kCluster; }
-size_t compact_ints(int num_blocks) { return 2 * ((size_t)num_blocks / 2 + 1) + kCluster; }
+size_t fork_ints(int n_rows, int width) { return (size_t)n_rows * width + (size_t)n_rows + kCluster; }
+size_t compact_ints(int num_blocks) { return 3 * ((size_t)num_blocks / 2 + 1) + kCluster; }
 
 }  // namespace
 }  // namespace cb
@@ -659,14 +765,15 @@ int cb_fork_blocks(const int32_t* parents, const int32_t* keep_lens, int32_t* bl
     a.pairs = pairs;
     int32_t* w = static_cast<int32_t*>(workspace);
     a.old_rows = w;
-    w += (size_t)n_rows * max_blocks_per_seq;
-    a.has = w;
-    a.last = w + n_rows;
-    a.need = w + 2 * (size_t)n_rows;
-    a.rank = w + 3 * (size_t)n_rows;
-    a.fresh = w + 4 * (size_t)n_rows;
-    a.counts = w + 5 * (size_t)n_rows;
-    if (launch_pool(fork_kernel, a, n_rows > kSmallRows || num_blocks > kSmallPool, st) != cudaSuccess) return CB_ECUDA;
+    a.fresh = w + (size_t)n_rows * max_blocks_per_seq;
+    a.counts = a.fresh + n_rows;
+    a.hash = 64;
+    while (a.hash <= n_rows) a.hash *= 2;
+    const size_t smem = ((size_t)kForkInts * n_rows + (size_t)kHashInts * a.hash) * 4;
+    constexpr int kMostSmem = (kForkInts * CB_MAX_REQS + kHashInts * 2 * CB_MAX_REQS) * 4;
+    if (smem > 48 * 1024 - 256 && opt_in_smem(reinterpret_cast<const void*>(fork_kernel), kMostSmem) != cudaSuccess)
+      return CB_ECUDA;
+    if (launch_pool(fork_kernel, a, n_rows > kSmallRows || num_blocks > kSmallPool, smem, st) != cudaSuccess) return CB_ECUDA;
     set_last_launches(1);
     return CB_OK;
   });
@@ -696,8 +803,15 @@ int cb_grow_blocks(const int32_t* cu_q_lens, int32_t* block_tables, int max_bloc
     a.slots = slot_mapping;
     a.n_tokens = n_tokens;
     a.counts = static_cast<int32_t*>(workspace);
-    if (launch_pool(grow_kernel, a, num_blocks > kSmallPool || n_tokens > 8 * kThreads, st) != cudaSuccess) return CB_ECUDA;
-    set_last_launches(1);
+    a.many = n_tokens > kManyTokens;
+    if (launch_pool(grow_kernel, a, num_blocks > kSmallPool, 0, st) != cudaSuccess) return CB_ECUDA;
+    if (a.many) {
+      int sms = 0;
+      if (!device_sms(&sms)) return CB_ECUDA;
+      const int ctas = std::min(2 * sms, (n_tokens + kSlotThreads * kRun - 1) / (kSlotThreads * kRun));
+      if (launch_behind(slots_kernel, a, ctas, kSlotThreads, st) != cudaSuccess) return CB_ECUDA;
+    }
+    set_last_launches(a.many ? 2 : 1);
     return CB_OK;
   });
 }
@@ -723,10 +837,10 @@ int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows,
     a.pairs = pairs;
     a.max_pairs = max_pairs;
     a.result = counts;
-    a.holes = static_cast<int32_t*>(workspace);
-    a.movers = a.holes + num_blocks / 2 + 1;
-    a.counts = a.movers + num_blocks / 2 + 1;
-    if (launch_pool(compact_kernel, a, num_blocks > kSmallPool || n_rows > kSmallRows, st) != cudaSuccess) return CB_ECUDA;
+    a.movers = static_cast<int2*>(workspace);
+    a.holes = reinterpret_cast<int32_t*>(a.movers + num_blocks / 2 + 1);
+    a.counts = a.holes + num_blocks / 2 + 1;
+    if (launch_pool(compact_kernel, a, num_blocks > kSmallPool || n_rows > kSmallRows, 0, st) != cudaSuccess) return CB_ECUDA;
     set_last_launches(1);
     return CB_OK;
   });
