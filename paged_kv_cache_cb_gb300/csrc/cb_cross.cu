@@ -80,6 +80,7 @@ struct alignas(16) Ctl {
   uint64_t full[NS], empty[NS];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];        // per group
   uint64_t ml_full;                    // ml is written
+  uint64_t turn[2];                    // a wide item's products, group by group
   uint64_t drain[2];
   uint32_t tmem_base;
   volatile int abort;
@@ -351,7 +352,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
-  uint32_t kt = 0, qs = 0, np = 0, items = 0;      // P tiles consumed, items begun
+  uint32_t kt = 0, qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   Pieces pieces(P, c);
   Piece p{};
   bool ok = true;
@@ -387,6 +388,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
     if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
     if (first && !warp_wait(P, &c.o_free[side], (items++ & 1) ^ 1)) return false;
     if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
+    if (p.wide && !warp_wait(P, &c.turn[side], (turns++ & 1) ^ !side)) return false;
     tc_fence_after();
     const uint64_t v = v0 + st * (TT::kBytes >> 4);
     if (elect_lane()) {
@@ -417,8 +419,13 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
         const uint32_t st = t % NS;
         return pass_by(&c.full[st], &c.empty[st], (t / NS) & 1);
       }
-      if (is_k) return ++ns, scores(t, slot, ns == mine);
-      return ++nv, values(t, nv == 1);
+      auto pass_on = [&]() {                       // the other group's turn
+        if (p.wide && elect_lane()) mbar_arrive(&c.turn[side ^ 1]);
+        __syncwarp();
+        return true;
+      };
+      if (is_k) return ++ns, scores(t, slot, ns == mine) && (ns == 1 || pass_on());
+      return ++nv, values(t, nv == 1) && (nv < mine || pass_on());
     };
     uint32_t t = 2 * kt;
     for (int j = 0; ok && j <= n; ++j) {           // as the loader has them
@@ -768,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.q_full[s], 1);
       mbar_init(&c.q_empty[s], 2);
       mbar_init(&c.drain[s], 1);
+      mbar_init(&c.turn[s], 1);
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 128);
       mbar_init(&c.o_done[s], 1);
