@@ -352,88 +352,105 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
-  uint32_t kt = 0, qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
+  uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
+  uint32_t st = 0, ph = 0;                         // the ring's next buffer
   Pieces pieces(P, c);
   Piece p{};
   bool ok = true;
   // Both warps see every buffer, in the loads' order, and give it back: the one that reads it
   // once its products are done, the other at once.  A wait tells a phase from the one before it
   // only, so neither may run a ring ahead of a load that the other waits for.
-  auto pass_by = [&](uint64_t* full, uint64_t* empty, uint32_t parity) -> bool {
+  auto step = [&]() {
+    if (++st == NS) {
+      st = 0;
+      ph ^= 1;
+    }
+  };
+  auto give_back = [&](uint64_t* full, uint64_t* empty, uint32_t parity) -> bool {
     if (!warp_wait(P, full, parity)) return false;
     if (elect_lane()) mbar_arrive(empty);
     __syncwarp();
     return true;
   };
-  auto scores = [&](uint32_t t, uint32_t slot, bool last) -> bool {
-    const uint32_t st = __shfl_sync(FULL, t % NS, 0);
-    if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
-    tc_fence_after();
-    const uint64_t q = q0 + slot * (TT::kBytes >> 4), k = k0 + st * (TT::kBytes >> 4);
-    if (elect_lane()) {
+  auto other = [&]() -> bool {                     // the other group's tile
+    const bool fine = give_back(&c.full[st], &c.empty[st], ph);
+    step();
+    return fine;
+  };
+  auto issue_s = [&](uint32_t slot, uint32_t kst, bool last) {
+    const uint64_t q = q0 + slot * (TT::kBytes >> 4), k = k0 + kst * (TT::kBytes >> 4);
 #pragma unroll
-      for (int ks = 0; ks < A / 16; ++ks) {
-        const uint64_t off = ((ks >> 2) * TT::kHalfBytes + (ks & 3) * 32) >> 4;
-        tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
-      }
-      tc_commit(&c.s_full[side]);
-      tc_commit(&c.empty[st]);
-      if (last) tc_commit(&c.q_empty[slot]);
+    for (int ks = 0; ks < A / 16; ++ks) {
+      const uint64_t off = ((ks >> 2) * TT::kHalfBytes + (ks & 3) * 32) >> 4;
+      tc_mma_f16(tmem + side * 128, q + off, k + off, kIdescS, ks > 0);
     }
+    tc_commit(&c.s_full[side]);
+    tc_commit(&c.empty[kst]);
+    if (last) tc_commit(&c.q_empty[slot]);
+  };
+  auto scores = [&](uint32_t slot, bool last) -> bool {       // S of the next buffer
+    if (!warp_wait(P, &c.full[st], ph)) return false;
+    tc_fence_after();
+    const uint32_t kst = __shfl_sync(FULL, st, 0);
+    if (elect_lane()) issue_s(slot, kst, last);
     __syncwarp();
+    step();
     return true;
   };
-  auto values = [&](uint32_t t, bool first) -> bool {
-    const uint32_t st = __shfl_sync(FULL, t % NS, 0);
-    if (!warp_wait(P, &c.full[st], (t / NS) & 1)) return false;
+  // PV of the next buffer and, if there is one, S of the group's next tile, in the buffer behind
+  // it: 16 products without a pause.
+  auto values = [&](bool first, uint32_t slot, bool more, bool last) -> bool {
+    const uint32_t vst = __shfl_sync(FULL, st, 0), vph = ph;
+    step();
+    const uint32_t kst = __shfl_sync(FULL, st, 0);
+    if (!warp_wait(P, &c.full[vst], vph)) return false;
+    if (more) {
+      if (!warp_wait(P, &c.full[kst], ph)) return false;
+      step();
+    }
     if (first && !warp_wait(P, &c.o_free[side], (items++ & 1) ^ 1)) return false;
     if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
     if (p.wide && !warp_wait(P, &c.turn[side], (turns++ & 1) ^ !side)) return false;
     tc_fence_after();
-    const uint64_t v = v0 + st * (TT::kBytes >> 4);
+    const uint64_t v = v0 + vst * (TT::kBytes >> 4);
     if (elect_lane()) {
 #pragma unroll
       for (int ks = 0; ks < kTileN / 16; ++ks)
         tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
                       (!first || ks > 0) ? 1u : 0u);
       tc_commit(&c.o_done[side]);
-      tc_commit(&c.empty[st]);
+      tc_commit(&c.empty[vst]);
+      if (more) issue_s(slot, kst, last);
+      if (p.wide) mbar_arrive(&c.turn[side ^ 1]);
     }
     __syncwarp();
     return true;
   };
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
-    const int n = p.tb - p.ta, mine = p.wide ? n : side ? n / 2 : (n + 1) / 2;
+    const int n = p.tb - p.ta;
     const uint32_t x = qs + (p.wide && side), slot = __shfl_sync(FULL, x & 1, 0);
+    const bool mine = p.wide || n > side;          // this group has a tile
     if (p.wide) {
       const uint32_t y = qs + !side;               // the other group's query tile
-      if (side) ok = pass_by(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
+      if (side) ok = give_back(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
       ok = ok && warp_wait(P, &c.q_full[slot], (x >> 1) & 1);
-      if (!side) ok = ok && pass_by(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
+      if (!side) ok = ok && give_back(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
+      ok = ok && scores(slot, n == 1);
+      for (int j = 0; ok && j < n; ++j) ok = values(j == 0, slot, j + 1 < n, j + 2 == n);
     } else {
-      ok = mine ? warp_wait(P, &c.q_full[slot], (x >> 1) & 1) : pass_by(&c.q_full[slot], &c.q_empty[slot], (x >> 1) & 1);
-    }
-    int ns = 0, nv = 0;
-    auto see = [&](uint32_t t, int tile, bool is_k) -> bool {
-      if (!p.wide && (tile & 1) != side) {
-        const uint32_t st = t % NS;
-        return pass_by(&c.full[st], &c.empty[st], (t / NS) & 1);
+      ok = mine ? warp_wait(P, &c.q_full[slot], (x >> 1) & 1) : give_back(&c.q_full[slot], &c.q_empty[slot], (x >> 1) & 1);
+      // K(0) K(1) V(0) K(2) V(1) .. V(n - 1): up to V(side)
+      if (side) ok = ok && other();
+      if (mine) ok = ok && scores(slot, side + 2 >= n);
+      if (n > 1 && !side) ok = ok && other();
+      if (side) ok = ok && other();
+      if (n > 2 && side) ok = ok && other();
+      for (int j = side; ok && j < n; j += 2) {
+        ok = values(j == side, slot, j + 2 < n, j + 4 >= n);
+        if (j + 1 < n) ok = ok && other();         // V(j + 1)
+        if (j + 3 < n) ok = ok && other();         // K(j + 3)
       }
-      auto pass_on = [&]() {                       // the other group's turn
-        if (p.wide && elect_lane()) mbar_arrive(&c.turn[side ^ 1]);
-        __syncwarp();
-        return true;
-      };
-      if (is_k) return ++ns, scores(t, slot, ns == mine) && (ns == 1 || pass_on());
-      return ++nv, values(t, nv == 1) && (nv < mine || pass_on());
-    };
-    uint32_t t = 2 * kt;
-    for (int j = 0; ok && j <= n; ++j) {           // as the loader has them
-      if (j < n) ok = see(t++, j, true);
-      if (p.wide && j < n) ok = ok && see(t++, j, false);
-      if (!p.wide && j > 0) ok = ok && see(t++, j - 1, false);
     }
-    kt += n;
     qs += p.wide ? 2 : 1;
   }
   if (!ok) c.abort = 1;
