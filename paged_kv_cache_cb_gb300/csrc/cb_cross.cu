@@ -409,8 +409,8 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
       step();
     }
     if (first && !warp_wait(P, &c.o_free[side], (items++ & 1) ^ 1)) return false;
-    if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
     if (p.wide && !warp_wait(P, &c.turn[side], (turns++ & 1) ^ !side)) return false;
+    if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
     tc_fence_after();
     const uint64_t v = v0 + vst * (TT::kBytes >> 4);
     if (elect_lane()) {
