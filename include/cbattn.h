@@ -36,6 +36,7 @@
  *  - Supported shapes: head_dim 64 or 128; block_size 16;
  *    n_q_heads / n_kv_heads in {1, 2, 4, 8}; with head_dim 128 also 32 query
  *    heads on 2 KV heads (16 per group) or on 1 (MQA); n_reqs <= CB_MAX_REQS.
+ *    Cross attention takes more (see there).
  *  - Return value: CB_OK (0) on success, a negative CB_E* code otherwise.  Size
  *    and pointer checks happen on the host before anything is enqueued; a
  *    rejected call enqueues nothing.
@@ -66,7 +67,7 @@ extern "C" {
 #define CB_EWORKSPACE (-3) /* workspace too small (see cb_paged_attention_workspace_size) */
 #define CB_EDEVICE (-4)    /* a kernel found bad metadata (block id or slot out of range) */
 #define CB_ETIMEOUT (-5)   /* a kernel's bounded wait ran out; its outputs are undefined */
-#define CB_ESTATE (-6)     /* scheduler: bad request id / state, or capacity exceeded */
+#define CB_ESTATE (-6)     /* scheduler: bad request id / state; capacity exceeded (scheduler, block pool) */
 
 #define CB_MAX_REQS 2048
 #define CB_MAX_CACHE_BUFFERS 8

@@ -23,7 +23,7 @@ namespace cb {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kCluster = 8;            // CTAs of a large call (the portable limit)
+constexpr int kCluster = 16;           // most CTAs of a call
 
 struct Pool {
   int32_t* tables;
@@ -664,21 +664,25 @@ __global__ void __launch_bounds__(kCopyThreads) copy_layers_kernel(const CopyArg
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-// One cluster of kCluster CTAs, or one CTA where there is little to do.
+// One cluster of `ctas` CTAs (1, 8 or 16).
 template <class Args>
-cudaError_t launch_pool(void (*kernel)(const Args), const Args& a, bool large, size_t smem, cudaStream_t stream) {
-  if (!large) {
+cudaError_t launch_pool(void (*kernel)(const Args), const Args& a, int ctas, size_t smem, cudaStream_t stream) {
+  if (ctas == 1) {
     kernel<<<1, kThreads, smem, stream>>>(a);
     return cudaGetLastError();
   }
+  if (ctas > 8) {                      // past the portable size
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -701,8 +705,12 @@ cudaError_t launch_behind(void (*kernel)(const Args), const Args& a, int ctas, i
 }
 
 constexpr int kManyTokens = 8192;      // slots that one cluster writes itself
-// A single CTA goes over up to this many blocks and rows.
-constexpr int kSmallPool = 8192, kSmallRows = 64;
+// What a single CTA goes over alone.  Times of the call and what goes with it (us), one CTA against
+// eight: 48 rows grown in a pool of 14,000 blocks 8.3 against 10.3 (it stops at the last block that it
+// needs); compaction of 333 blocks with its copies 10.2 against 13.6, of 28,610 324 against 292; fork of
+// 128 rows in 6000 blocks 38.4 against 37.4.  512 rows that take 32,000 of 100,000 blocks: 55.8 with
+// one, 31.3 with eight, 24.0 with sixteen, which the others lose 1 to 2 by.
+constexpr int kSmallPool = 8192, kSmallRows = 64, kSmallGrowth = 16384;
 
 // The pool arguments that the calls share; false: CB_EINVAL.
 bool pool_of(Pool* P, int32_t* tables, int width, int n_rows, int32_t* lens, int32_t* refs, int num_blocks, int block_size) {
@@ -773,7 +781,7 @@ int cb_fork_blocks(const int32_t* parents, const int32_t* keep_lens, int32_t* bl
     constexpr int kMostSmem = (kForkInts * CB_MAX_REQS + kHashInts * 2 * CB_MAX_REQS) * 4;
     if (smem > 48 * 1024 - 256 && opt_in_smem(reinterpret_cast<const void*>(fork_kernel), kMostSmem) != cudaSuccess)
       return CB_ECUDA;
-    if (launch_pool(fork_kernel, a, n_rows > kSmallRows || num_blocks > kSmallPool, smem, st) != cudaSuccess) return CB_ECUDA;
+    if (launch_pool(fork_kernel, a, n_rows > kSmallRows || num_blocks > kSmallPool ? 8 : 1, smem, st) != cudaSuccess) return CB_ECUDA;
     set_last_launches(1);
     return CB_OK;
   });
@@ -804,7 +812,7 @@ int cb_grow_blocks(const int32_t* cu_q_lens, int32_t* block_tables, int max_bloc
     a.n_tokens = n_tokens;
     a.counts = static_cast<int32_t*>(workspace);
     a.many = n_tokens > kManyTokens;
-    if (launch_pool(grow_kernel, a, num_blocks > kSmallPool, 0, st) != cudaSuccess) return CB_ECUDA;
+    if (launch_pool(grow_kernel, a, a.many ? 16 : num_blocks > kSmallGrowth ? 8 : 1, 0, st) != cudaSuccess) return CB_ECUDA;
     if (a.many) {
       int sms = 0;
       if (!device_sms(&sms)) return CB_ECUDA;
@@ -840,7 +848,7 @@ int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows,
     a.movers = static_cast<int2*>(workspace);
     a.holes = reinterpret_cast<int32_t*>(a.movers + num_blocks / 2 + 1);
     a.counts = a.holes + num_blocks / 2 + 1;
-    if (launch_pool(compact_kernel, a, num_blocks > kSmallPool || n_rows > kSmallRows, 0, st) != cudaSuccess) return CB_ECUDA;
+    if (launch_pool(compact_kernel, a, num_blocks > kSmallPool || n_rows > kSmallRows ? 8 : 1, 0, st) != cudaSuccess) return CB_ECUDA;
     set_last_launches(1);
     return CB_OK;
   });
