@@ -487,22 +487,22 @@ def cb_paged_cross_attention(q, cu_q_lens, kv_lens, block_tables, k_cache, v_cac
     cv = _on(dev, v_cache, c.bf16, "v_cache", 4)
     po = _on(dev, out, c.bf16, "out", 3)
     pw = _on(dev, workspace, c.u8, "workspace", 1)
-    shape, tables, cache = q.shape, block_tables.shape, k_cache.shape
-    if len(shape) != 3 or out.shape != shape or kv_lens.dim() != 1 or len(tables) != 2 or workspace.dim() != 1:
+    shape = q.shape
+    try:
+        (n_tok, hq, a), (rows, width), (nb, hk, bs, a2) = shape, block_tables.shape, k_cache.shape
+        (n_reqs,), (size,) = kv_lens.shape, workspace.shape
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    if out.shape != shape or cu_q_lens.shape != (n_reqs + 1,) or rows != n_reqs:
         raise ValueError("shape mismatch")
-    n_reqs = kv_lens.shape[0]
-    if cu_q_lens.shape != (n_reqs + 1,) or tables[0] != n_reqs:
-        raise ValueError("shape mismatch")
-    if len(cache) != 4 or v_cache.shape != cache or cache[3] != shape[2]:
+    if v_cache.shape != (nb, hk, bs, a) or a2 != a:
         raise ValueError("cache shape mismatch")
-    n_tok, hq, a = shape
-    nb, hk, bs, _ = cache
     max_q_len, max_kv_len = int(max_q_len), int(max_kv_len)
     _fit_int(max_q_len, max_kv_len, n_tok)
-    _check("cb_paged_cross_attention",
-           lib().cb_paged_cross_attention(pq, pcu, pkv, pbt, tables[1], n_reqs, n_tok, max_q_len, max_kv_len, ck, cv, nb,
-                                          po, float(scale), hq, hk, a, bs, pw, workspace.shape[0],
-                                          _raw_stream(c, dev, stream)))
+    rc = lib().cb_paged_cross_attention(pq, pcu, pkv, pbt, width, n_reqs, n_tok, max_q_len, max_kv_len, ck, cv, nb, po,
+                                        float(scale), hq, hk, a, bs, pw, size, _raw_stream(c, dev, stream))
+    if rc:
+        _check("cb_paged_cross_attention", rc)
 
 
 # ---------------------------------------------------------------- block pool on the device
@@ -517,12 +517,15 @@ def cb_block_ops_workspace_size(n_rows, max_blocks_per_seq, num_blocks, block_si
 def _pool(c, dev, block_tables, lens, refs, workspace):
     """Pointers of a pool's tables [n_rows, max_blocks], lengths [n_rows], counts [num_blocks] and a workspace, and
     the sizes."""
-    ptrs = (_on(dev, block_tables, c.i32, "block_tables", 2), _on(dev, lens, c.i32, "lens", 1),
-            _on(dev, refs, c.i32, "refs", 1), _on(dev, workspace, c.u8, "workspace", 1))
-    shape = block_tables.shape
-    if len(shape) != 2 or lens.shape != shape[:1] or refs.dim() != 1 or workspace.dim() != 1:
+    pt, pl = _on(dev, block_tables, c.i32, "block_tables", 2), _on(dev, lens, c.i32, "lens", 1)
+    pr, pw = _on(dev, refs, c.i32, "refs", 1), _on(dev, workspace, c.u8, "workspace", 1)
+    try:
+        (n, width), (nb,), (size,) = block_tables.shape, refs.shape, workspace.shape
+    except ValueError:
+        raise ValueError("shape mismatch") from None
+    if lens.shape != (n,):
         raise ValueError("shape mismatch")
-    return ptrs, shape[0], shape[1], refs.shape[0]
+    return pt, pl, pr, pw, size, n, width, nb
 
 
 def cb_fork_blocks(parents, keep_lens, block_tables, lens, refs, pairs, workspace, stream=None):
@@ -536,11 +539,12 @@ def cb_fork_blocks(parents, keep_lens, block_tables, lens, refs, pairs, workspac
     pp = _on(dev, parents, c.i32, "parents", 1)
     pk = None if keep_lens is None else _on(dev, keep_lens, c.i32, "keep_lens", 1)
     px = _on(dev, pairs, c.i32, "pairs", 2)
-    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
-    if parents.shape != (n,) or (pk is not None and keep_lens.shape != (n,)) or pairs.shape != (n, 2):
+    pt, pl, pr, pw, size, n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    if parents.shape != (n,) or pairs.shape != (n, 2) or (pk is not None and keep_lens.shape != (n,)):
         raise ValueError("shape mismatch")
-    _check("cb_fork_blocks", lib().cb_fork_blocks(pp, pk, pt, width, n, pl, pr, nb, _BLOCK, px, pw, workspace.shape[0],
-                                                  _raw_stream(c, dev, stream)))
+    rc = lib().cb_fork_blocks(pp, pk, pt, width, n, pl, pr, nb, _BLOCK, px, pw, size, _raw_stream(c, dev, stream))
+    if rc:
+        _check("cb_fork_blocks", rc)
 
 
 def cb_grow_blocks(cu_q_lens, block_tables, lens, refs, ctx_lens, slot_mapping, workspace, stream=None):
@@ -552,11 +556,14 @@ def cb_grow_blocks(cu_q_lens, block_tables, lens, refs, ctx_lens, slot_mapping, 
     pc = _on(dev, cu_q_lens, c.i32, "cu_q_lens", 1)
     px = _on(dev, ctx_lens, c.i32, "ctx_lens", 1)
     ps = _on(dev, slot_mapping, c.i64, "slot_mapping", 1)
-    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
-    if cu_q_lens.shape != (n + 1,) or ctx_lens.shape != (n,) or slot_mapping.dim() != 1:
+    pt, pl, pr, pw, size, n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    slots = slot_mapping.shape
+    if cu_q_lens.shape != (n + 1,) or ctx_lens.shape != (n,) or len(slots) != 1:
         raise ValueError("shape mismatch")
-    _check("cb_grow_blocks", lib().cb_grow_blocks(pc, pt, width, n, pl, pr, nb, _BLOCK, px, ps, slot_mapping.shape[0],
-                                                  pw, workspace.shape[0], _raw_stream(c, dev, stream)))
+    rc = lib().cb_grow_blocks(pc, pt, width, n, pl, pr, nb, _BLOCK, px, ps, slots[0], pw, size,
+                              _raw_stream(c, dev, stream))
+    if rc:
+        _check("cb_grow_blocks", rc)
 
 
 def cb_compact_blocks(block_tables, lens, refs, block_map, pairs, counts, workspace, stream=None):
@@ -568,30 +575,44 @@ def cb_compact_blocks(block_tables, lens, refs, block_map, pairs, counts, worksp
     pm = _on(dev, block_map, c.i32, "block_map", 1)
     px = _on(dev, pairs, c.i32, "pairs", 2)
     pc = _on(dev, counts, c.i32, "counts", 1)
-    (pt, pl, pr, pw), n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
-    if block_map.shape != (nb,) or pairs.dim() != 2 or pairs.shape[1] != 2 or counts.shape != (2,):
+    pt, pl, pr, pw, size, n, width, nb = _pool(c, dev, block_tables, lens, refs, workspace)
+    shape = pairs.shape
+    if block_map.shape != (nb,) or len(shape) != 2 or shape[1] != 2 or counts.shape != (2,):
         raise ValueError("shape mismatch")
-    _check("cb_compact_blocks", lib().cb_compact_blocks(pt, width, n, pl, pr, nb, _BLOCK, pm, px, pairs.shape[0], pc, pw,
-                                                        workspace.shape[0], _raw_stream(c, dev, stream)))
+    rc = lib().cb_compact_blocks(pt, width, n, pl, pr, nb, _BLOCK, pm, px, shape[0], pc, pw, size,
+                                 _raw_stream(c, dev, stream))
+    if rc:
+        _check("cb_compact_blocks", rc)
+
+
+# the C arrays of 1 .. CB_MAX_CACHE_BUFFERS pointers and sizes (making an array type takes longer than an array)
+_ARRAYS = {n: (_vp * n, _c_size * n) for n in range(1, 9)}
 
 
 def cb_copy_blocks_layers(pairs, caches, stream=None):
     """Block dst becomes block src for every (src, dst) of pairs (int32 [n, 2], src < 0: none) in every layer of every
-    tensor of caches: contiguous CUDA tensors [n_layers, num_blocks, ...] of any type, the same two sizes in all."""
+    tensor of caches: up to 8 contiguous CUDA tensors [n_layers, num_blocks, ...] of any type, the same two sizes in
+    all."""
     c = _tc()
     dev = _current_device(c, pairs)
     pp = _on(dev, pairs, c.i32, "pairs", 2)
-    n = len(caches)
-    if pairs.dim() != 2 or pairs.shape[1] != 2 or not n:
+    shape, n = pairs.shape, len(caches)
+    if len(shape) != 2 or shape[1] != 2 or n not in _ARRAYS:
         raise ValueError("shape mismatch")
-    ptrs, sizes, first = (_vp * n)(), (_c_size * n)(), caches[0].shape[:2]
-    for i, t in enumerate(caches):
-        ptrs[i] = _on(dev, t, t.dtype, "caches", None)
-        if t.dim() < 3 or t.shape[:2] != first or t.numel() == 0:
+    if hasattr(caches, "shape"):                   # its first dimension is not one of buffers
+        raise ValueError("caches must be a sequence of tensors")
+    ptrs, sizes, first = [], [], caches[0].shape[:2]
+    for t in caches:
+        ptrs.append(_on(dev, t, t.dtype, "caches", None))
+        size = t.shape
+        if len(size) < 3 or size[:2] != first or t.numel() == 0:
             raise ValueError("caches must be [n_layers, num_blocks, ...] of the same two sizes")
-        sizes[i] = t.numel() // (first[0] * first[1]) * t.element_size()
-    _check("cb_copy_blocks_layers", lib().cb_copy_blocks_layers(pp, pairs.shape[0], ptrs, sizes, n, first[0], first[1],
-                                                                _raw_stream(c, dev, stream)))
+        sizes.append(t.nbytes // (size[0] * size[1]))
+    pointers, counts = _ARRAYS[n]
+    rc = lib().cb_copy_blocks_layers(pp, shape[0], pointers(*ptrs), counts(*sizes), n, first[0], first[1],
+                                     _raw_stream(c, dev, stream))
+    if rc:
+        _check("cb_copy_blocks_layers", rc)
 
 
 CB_NOALLOC_SCRATCH_BYTES = 64 * 1024 * 1024

@@ -150,19 +150,32 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Smallest decode split the launcher may choose; the workspace is sized for it.
 constexpr int kMinSplitBlocks = 8;
 
-// The dynamic shared-memory opt-in of a kernel, once per (device, kernel): the
-// attribute belongs to the current device's context.
+namespace {
+// An attribute of a kernel, set once per (device, kernel): it belongs to the
+// current device's context.  `done`: the ones set.
+struct SetOnce {
+  std::set<std::pair<int, const void*>> done;
+  std::mutex mu;
+  cudaError_t operator()(const void* kernel, cudaFuncAttribute attribute, int value) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({dev, kernel})) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, attribute, value);
+    if (e == cudaSuccess) done.insert({dev, kernel});
+    return e;
+  }
+};
+}  // namespace
+
 cudaError_t opt_in_smem(const void* kernel, int bytes) {
-  static std::set<std::pair<int, const void*>> done;
-  static std::mutex mu;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(mu);
-  if (done.count({dev, kernel})) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) done.insert({dev, kernel});
-  return e;
+  static SetOnce set;
+  return set(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+cudaError_t allow_large_clusters(const void* kernel) {
+  static SetOnce set;
+  return set(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 namespace {

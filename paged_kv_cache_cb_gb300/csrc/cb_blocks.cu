@@ -365,9 +365,9 @@ struct GrowArgs {
   int32_t* counts;                     // workspace: [kCluster]
 };
 
-// Slot of position pos of row i (pos < 0: none).
+// Slot of position pos of row i (pos < 0, or past the table row: none).
 __device__ __forceinline__ int64_t slot_of(const Pool& P, int i, int pos) {
-  if (pos < 0) return -1;
+  if (pos < 0 || pos / kBlockSize >= P.width) return -1;
   const int e = __ldcg(P.tables + (size_t)i * P.width + pos / kBlockSize);
   if (e >= 0 && e < P.num_blocks) return (int64_t)e * kBlockSize + pos % kBlockSize;
   set_error(P.err, CB_DEVERR_BADBLOCK);
@@ -672,7 +672,7 @@ cudaError_t launch_pool(void (*kernel)(const Args), const Args& a, int ctas, siz
     return cudaGetLastError();
   }
   if (ctas > 8) {                      // past the portable size
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = allow_large_clusters(reinterpret_cast<const void*>(kernel));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -92,6 +92,8 @@ int choose_split_blocks(int n_reqs, int max_kv_len, int n_kv_heads, int n_sms);
 // Dynamic shared-memory opt-in of `kernel` on the current device (set once per
 // device and kernel).
 cudaError_t opt_in_smem(const void* kernel, int bytes);
+// The same for clusters of more than the portable 8 CTAs.
+cudaError_t allow_large_clusters(const void* kernel);
 
 // Kernel launchers (defined in the .cu files); return a cudaError_t.
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, const int64_t* slots, int n_tokens,

@@ -259,6 +259,46 @@ def test_bad_metadata_is_reported_and_harmless():
     assert lib.cb_last_error() == lib.CB_EDEVICE and not caches[0].any()
 
 
+def test_slots_of_a_row_whose_length_is_out_of_range():
+    """Many tokens, and a length past the table that is just its nearest length plus the new tokens: the row has not
+    grown, and nothing behind its table row is read."""
+    lib = L()
+    p = Pool([20, 0], 700, 3, width=600)
+    p.d_lens[1] = 600 * BS + 9000
+    cu = torch.tensor([0, 3, 9003], dtype=torch.int32, device="cuda")
+    slots = torch.zeros(9003, dtype=torch.int64, device="cuda")
+    ctx = torch.zeros(2, dtype=torch.int32, device="cuda")
+    lib.cb_grow_blocks(cu, p.d_tables, p.d_lens, p.d_refs, ctx, slots, p.ws)
+    assert lib.cb_last_error() == lib.CB_EDEVICE
+    assert (slots[:3] >= 0).all() and (slots[3:] == -1).all() and p.d_lens.tolist() == [23, 600 * BS + 9000]
+
+
+def test_many_tokens_recorded():
+    """Growth by more tokens than one cluster gives slots to, recorded and replayed."""
+    lib = L()
+    p = Pool([0, 5, 100], 3000, 4, width=900)
+    q = np.array([4000, 3000, 3500])
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(q)]).astype(np.int32)).cuda()
+    slots = torch.zeros(10500 + 7, dtype=torch.int64, device="cuda")
+    ctx = torch.zeros(3, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        call = lambda: lib.cb_grow_blocks(cu, p.d_tables, p.d_lens, p.d_refs, ctx, slots, p.ws)  # noqa: E731
+        call()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call()
+        graph.replay()
+        assert lib.cb_last_error(s) == 0
+    for _ in range(2):
+        want_ctx, want, _ = ob.grow(q, p.tables, p.lens, p.refs)
+    assert np.array_equal(slots.cpu().numpy(), np.concatenate([want, [-1] * 7]))
+    assert np.array_equal(ctx.cpu().numpy(), want_ctx)
+    p.same()
+
+
 @pytest.mark.parametrize("layers,blocks,shapes,n", [
     (1, 5, [(2, 16, 64)], 2),
     (3, 40, [(1, 16, 128), (1, 16, 128), (1, 16), (1, 16)], 17),
@@ -383,6 +423,8 @@ def test_binding_refusals():
             lambda: lib.cb_compact_blocks(*pool, i(8), i(4, 2), i(2), p.ws),
             lambda: lib.cb_compact_blocks(*pool, i(9), i(4, 2), i(3), p.ws),
             lambda: lib.cb_copy_blocks_layers(i(1, 2), []),
+            lambda: lib.cb_copy_blocks_layers(i(1, 2), torch.zeros(2, 8, 4, 16, device="cuda")),
+            lambda: lib.cb_copy_blocks_layers(i(1, 2), [torch.zeros(2, 8, 16, device="cuda")] * 9),
             lambda: lib.cb_copy_blocks_layers(i(1, 2), [torch.zeros(2, 8, device="cuda")]),
             lambda: lib.cb_copy_blocks_layers(i(1, 2), [torch.zeros(2, 8, 16, device="cuda"), torch.zeros(2, 9, 16, device="cuda")]),
     ):
