@@ -660,6 +660,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
 //     M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // Counter `first` of the stream counts the arrivals of n CTAs, then as many
 // departures; the last sets it back to 0.
+// LANES lanes take a row's four columns, at most kHold pieces each, which are read at once.
+constexpr int kHold = 5;
 template <int A, int LANES>
 __device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n, int lo, int hi) {
   const int sub = threadIdx.x % LANES, group = 1 << P.group_log2;
@@ -669,26 +671,31 @@ __device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n
     const int task = base + threadIdx.x / LANES;
     const bool on = task < hi;
     const int row = on ? task / (A / 4) : 0, col = on ? task % (A / 4) : 0;
-    auto piece = [&](int i) { return P.part + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * slot_floats; };
-    auto ml = [&](int i) { return __ldcg(reinterpret_cast<const float2*>(piece(i) + (size_t)P.part_rows * A) + row); };
-    float M = kNoKey;
-    if (on) {
-#pragma unroll 4
-      for (int i = sub; i < n; i += LANES) M = fmaxf(M, ml(i).x);
+    float2 ml[kHold];
+    float4 o[kHold];
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      const int i = sub + k * LANES;
+      ml[k] = make_float2(kNoKey, 0.f);
+      o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!on || i >= n) continue;
+      const float* piece = P.part + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * slot_floats;
+      ml[k] = __ldcg(reinterpret_cast<const float2*>(piece + (size_t)P.part_rows * A) + row);
+      o[k] = __ldcg(reinterpret_cast<const float4*>(piece + (size_t)row * A) + col);
     }
+    float M = kNoKey;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float L = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (on) {
-#pragma unroll 4
-      for (int i = sub; i < n; i += LANES) {
-        const float2 x = ml(i);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(piece(i) + (size_t)row * A) + col);
-        const float w = ex2(x.x - M);
-        L += w * x.y;
-        y.x += w * o.x, y.y += w * o.y, y.z += w * o.z, y.w += w * o.w;
-      }
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) {
+      if (sub + k * LANES >= n) continue;
+      const float w = ex2(ml[k].x - M);
+      L += w * ml[k].y;
+      y.x += w * o[k].x, y.y += w * o[k].y, y.z += w * o[k].z, y.w += w * o[k].w;
     }
 #pragma unroll
     for (int d = LANES / 2; d > 0; d >>= 1) {
@@ -706,6 +713,7 @@ __device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n
     }
   }
 }
+static_assert(kHold * 32 >= kMaxDecodeGrid, "an item's pieces fit a warp");
 
 __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
   unsigned v;
@@ -753,9 +761,10 @@ __device__ void join(const CrossParams& P, C& c) {
     if (c.go && !c.abort) {
       const int rows = p.tokens << P.group_log2, tasks = rows * (A / 4), i = (int)blockIdx.x - first;
       const int lo = (int)((long long)tasks * i / n), hi = (int)((long long)tasks * (i + 1) / n);
-      if (n <= 6) join_rows<A, 1>(P, p, first, n, lo, hi);
-      else if (n <= 24) join_rows<A, 4>(P, p, first, n, lo, hi);
-      else join_rows<A, 16>(P, p, first, n, lo, hi);
+      if (n <= kHold) join_rows<A, 1>(P, p, first, n, lo, hi);
+      else if (n <= 4 * kHold) join_rows<A, 4>(P, p, first, n, lo, hi);
+      else if (n <= 16 * kHold) join_rows<A, 16>(P, p, first, n, lo, hi);
+      else join_rows<A, 32>(P, p, first, n, lo, hi);
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(count, 1u) == 2u * n - 1) *count = 0u;
