@@ -20,10 +20,18 @@
 //
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
 // and V; warps 9, 10: MMA issue for A, B; one more completes the third warpgroup, which
-// gives most of its registers to the other two: a row's 128 scores stay in registers.  Scores, running max (base 2, scale folded in), sums
-// and O are fp32; the weights are rounded to bf16 for the tensor cores (within 2^-8
-// of each, as the output is of itself) and summed before that rounding.
-// Every wait is bounded.
+// gives most of its registers to the other two: a row's 128 scores stay in registers.
+// Scores, running max (base 2, scale folded in), sums and O are fp32; the weights are
+// rounded to bf16 for the tensor cores (within 2^-8 of each, as the output is of itself)
+// and summed before that rounding.  Every wait is bounded.
+//
+// Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
+// head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 145 us = 0.93 of the copy
+// rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 384 us = 0.99: HBM bounds both.
+// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 262 us = 1.34
+// PFLOP/s: the chain scores - weights - product of each group bounds them.  Head dimension
+// 64 has half the bytes per score: 100 single tokens over 100-3000 keys, 32/8 heads, 78.5 us
+// = 0.6 of the copy rate, bound by the softmax's chain.
 #include <algorithm>
 #include <cstddef>
 
@@ -66,12 +74,20 @@ struct Request {
 };
 
 // A CTA's part of an item: key tiles [ta, tb) of [0, tiles).
-struct Piece {
+struct Part {
   Request q;
   int r, g, tok_lo, tokens, tiles, ta, tb;
   int at, step;                        // unit of tile 0, units per tile
-  bool wide;
+  bool two_row_tiles;
   __device__ __forceinline__ bool whole() const { return ta == 0 && tb == tiles; }
+};
+
+// Whether a launch can have wide items (W) is known to the compiler.  Where it cannot, the
+// softmax's code is shorter (100 requests of one token and up to 3000 keys of dimension 64:
+// 83 us without that, 78.5 with it); and partial results have another order: see join_rows.
+template <bool W>
+struct Piece : Part {
+  __device__ __forceinline__ bool wide() const { return W && two_row_tiles; }
 };
 
 template <int NS>
@@ -89,7 +105,7 @@ struct alignas(16) Ctl {
   int start_r, start_u;                // the request that the CTA's range begins in, its first unit
   int n_cut;                           // pieces of cut items
   int go;
-  Piece cut[2];
+  Part cut[2];
   long long scan[kThreads / 32];
   float2 ml[128];                      // group B's (max, sum) of a narrow item
 };
@@ -175,6 +191,7 @@ __device__ void make_plan(const CrossParams& P, C& c) {
 }
 
 // Walks a CTA's pieces in order; every role has its own.
+template <bool W>
 struct Pieces {
   int u0, u1, n;
   int r, g, grp, u;                    // the next item and its first unit
@@ -198,7 +215,7 @@ struct Pieces {
     q = load_request(P, r, false);
     if (q.q_len && q.kv) s = shape_of(P, q);
   }
-  __device__ bool next(const CrossParams& P, Piece& p) {
+  __device__ bool next(const CrossParams& P, Piece<W>& p) {
     while (u < u1) {
       const int tok = kRows >> P.group_log2;
       const bool last = grp == s.groups - 1;
@@ -207,9 +224,9 @@ struct Pieces {
       p.g = g;
       p.tok_lo = grp * tok;
       p.tokens = min(tok, q.q_len - p.tok_lo);
-      p.wide = p.tokens > tok / 2;
+      p.two_row_tiles = p.tokens > tok / 2;
       p.tiles = s.tiles;
-      p.step = p.wide ? kWide : kNarrow;
+      p.step = p.wide() ? kWide : kNarrow;
       p.at = u + kLead;
       p.ta = min(s.tiles, max(0, u0 - p.at + p.step - 1) / p.step);
       p.tb = min(s.tiles, max(0, u1 - p.at + p.step - 1) / p.step);
@@ -251,7 +268,7 @@ __device__ __forceinline__ bool elect_lane() {
 // elected lane asks for all of them, from coordinates that are the same in the whole
 // warp: a box per lane took 62 cycles each (1000 a tile, as long as its share of the
 // memory's time), the loads of one lane after the other.
-template <int A, class C>
+template <int A, bool W, class C>
 __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUtensorMap* vmap, const CUtensorMap* qmap,
                        Tiles<A>& T, C& c) {
   using TT = Tiles<A>;
@@ -261,8 +278,8 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
   const int none = P.num_blocks * P.n_kv_heads * kBlockSize;      // past the map's rows: zeros
   const int tok_tile = kTileM >> P.group_log2, group = 1 << P.group_log2;
   uint32_t at = 0, qs = 0;                                        // place in the ring's order, query tiles
-  Pieces pieces(P, c);
-  Piece p;
+  Pieces<W> pieces(P, c);
+  Piece<W> p;
   // y: rows of the tile's blocks, in lanes [in4 * 8, in4 * 8 + 8)
   auto load = [&](const CUtensorMap* map, int y, int in4) -> bool {
     const uint32_t st = __shfl_sync(FULL, at % NS, 0);
@@ -294,7 +311,7 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
       return none;
     };
     int e = entry(p.ta), y = none, before = none;
-    for (int side = 0; ok && side < (p.wide ? 2 : 1); ++side, ++qs) {
+    for (int side = 0; ok && side < (p.wide() ? 2 : 1); ++side, ++qs) {
       const uint32_t st = qs & 1;
       ok = warp_wait(P, &c.q_empty[st], ((qs >> 1) & 1) ^ 1);
       if (ok && elect_lane()) {
@@ -313,12 +330,12 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
         e = j + 4 < p.tb ? entry(j + 4) : -1;
       }
       ok = load(kmap, y, in4);
-      if (p.wide)
+      if (p.wide())
         ok = ok && load(vmap, y, in4);
       else if (j > p.ta)
         ok = ok && load(vmap, in4 ? y : before, (in4 + 3) & 3);
     }
-    if (ok && !p.wide) ok = load(vmap, y, (p.tb - 1 - p.ta) & 3);
+    if (ok && !p.wide()) ok = load(vmap, y, (p.tb - 1 - p.ta) & 3);
   }
   if (!ok) c.abort = 1;
   if (c.abort && lane == 0) {          // copies in flight land before shared memory is given back
@@ -340,7 +357,7 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
 // are read from uniform registers, which the compiler uses for values of a converged
 // warp: issued from a branch of one lane, each MMA moved its descriptors there first
 // and took about 110 cycles instead of the 64 that it runs.
-template <int A, class C>
+template <int A, bool W, class C>
 __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A>;
   constexpr int NS = TT::kRing;
@@ -354,8 +371,8 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
   uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   uint32_t st = 0, ph = 0;                         // the ring's next buffer
-  Pieces pieces(P, c);
-  Piece p{};
+  Pieces<W> pieces(P, c);
+  Piece<W> p{};
   bool ok = true;
   // Both warps see every buffer, in the loads' order, and give it back: the one that reads it
   // once its products are done, the other at once.  A wait tells a phase from the one before it
@@ -409,7 +426,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
       step();
     }
     if (first && !warp_wait(P, &c.o_free[side], (items++ & 1) ^ 1)) return false;
-    if (p.wide && !warp_wait(P, &c.turn[side], (turns++ & 1) ^ !side)) return false;
+    if (p.wide() && !warp_wait(P, &c.turn[side], (turns++ & 1) ^ !side)) return false;
     if (!warp_wait(P, &c.p_full[side], np++ & 1)) return false;
     tc_fence_after();
     const uint64_t v = v0 + vst * (TT::kBytes >> 4);
@@ -421,16 +438,16 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
       tc_commit(&c.o_done[side]);
       tc_commit(&c.empty[vst]);
       if (more) issue_s(slot, kst, last);
-      if (p.wide) mbar_arrive(&c.turn[side ^ 1]);
+      if (p.wide()) mbar_arrive(&c.turn[side ^ 1]);
     }
     __syncwarp();
     return true;
   };
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
-    const uint32_t x = qs + (p.wide && side), slot = __shfl_sync(FULL, x & 1, 0);
-    const bool mine = p.wide || n > side;          // this group has a tile
-    if (p.wide) {
+    const uint32_t x = qs + (p.wide() && side), slot = __shfl_sync(FULL, x & 1, 0);
+    const bool mine = p.wide() || n > side;          // this group has a tile
+    if (p.wide()) {
       const uint32_t y = qs + !side;               // the other group's query tile
       if (side) ok = give_back(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
       ok = ok && warp_wait(P, &c.q_full[slot], (x >> 1) & 1);
@@ -451,7 +468,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
         if (j + 3 < n) ok = ok && other();         // K(j + 3)
       }
     }
-    qs += p.wide ? 2 : 1;
+    qs += p.wide() ? 2 : 1;
   }
   if (!ok) c.abort = 1;
   if (elect_lane()) tc_commit(&c.drain[side]);     // what was issued completes before the TMEM is freed
@@ -474,7 +491,7 @@ __device__ __forceinline__ void rescale(uint32_t o, float alpha) {
   }
 }
 
-template <int A, class C>
+template <int A, bool W, class C>
 __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A>;
   constexpr int H = TT::kHalves, NS = TT::kRing;
@@ -486,18 +503,18 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
   const float sl2 = P.scale_log2;
   // key tiles before this piece; this group's; group B's (counted by both); pieces that both share
   uint32_t kt = 0, sc = 0, scb = 0, shared = 0;
-  Pieces pieces(P, c);
-  Piece p;
+  Pieces<W> pieces(P, c);
+  Piece<W> p;
   while (!__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
-    const int mine = p.wide ? n : side ? n / 2 : (n + 1) / 2;
-    const int tok = (p.wide && side ? tok_tile : 0) + (row >> P.group_log2);      // of the item
+    const int mine = p.wide() ? n : side ? n / 2 : (n + 1) / 2;
+    const int tok = (p.wide() && side ? tok_tile : 0) + (row >> P.group_log2);      // of the item
     const bool valid = tok < p.tokens;
     const bool busy = __any_sync(FULL, valid);                                    // this warp has rows
     float m = kNoKey, l = 0.f;         // running max times scale * log2 e; sum
     bool ok = true;
     for (int i = 0; i < mine; ++i, ++sc) {
-      const int j = p.wide ? i : 2 * i + side, key0 = (p.ta + j) * kTileN;
+      const int j = p.wide() ? i : 2 * i + side, key0 = (p.ta + j) * kTileN;
       ok = warp_wait(P, &c.s_full[side], sc & 1);
       if (!ok) break;
       tc_fence_after();
@@ -580,8 +597,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
       mbar_arrive(&c.p_full[side]);
     }
     kt += n;
-    const bool two = !p.wide && n > 1; // both groups hold parts of the same rows
-    scb += p.wide ? n : n / 2;
+    const bool two = !p.wide() && n > 1; // both groups hold parts of the same rows
+    scb += p.wide() ? n : n / 2;
     if (ok && mine) ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
     if (!ok) {
       c.abort = 1;
@@ -614,7 +631,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
     const float inv = whole ? 1.f / l : 1.f;
     alpha *= inv;
     beta *= inv;
-    const int irow = (p.wide && side ? 128 : 0) + row;
+    const int irow = (p.wide() && side ? 128 : 0) + row;
     const int slot = 2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0);
     float* part = P.part + (size_t)slot * P.part_rows * (A + 2);
     uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
@@ -642,7 +659,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
         } else if (valid) {
 #pragma unroll
           for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(part + (size_t)irow * A + ch * 32 + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            reinterpret_cast<float4*>(part)[W ? (size_t)(ch * 8 + k / 4) * P.part_rows + irow : (size_t)irow * (A / 4) + ch * 8 + k / 4] =
+                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         }
       }
       if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)P.part_rows * A + irow * 2) = make_float2(m, l);
@@ -661,16 +679,20 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
 // Counter `first` of the stream counts the arrivals of n CTAs, then as many
 // departures; the last sets it back to 0.
 // LANES lanes take a row's four columns, at most kHold pieces each, which are read at once.
+// Where items are wide, four columns of all rows lie together, so that a warp of the softmax
+// (thread = row) writes whole lines, and a warp here takes 32 rows: prompts of up to 2000
+// tokens 267 us with rows together, 262.5 so.  The few rows of narrow items are better
+// kept whole (one token a request, dimension 64: 83.2 and 84.8 us).
 constexpr int kHold = 5;
-template <int A, int LANES>
-__device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n, int lo, int hi) {
-  const int sub = threadIdx.x % LANES, group = 1 << P.group_log2;
+template <int A, bool W, int LANES>
+__device__ void join_rows(const CrossParams& P, const Part& p, int first, int n, int lo, int hi) {
+  const int sub = threadIdx.x % LANES, group = 1 << P.group_log2, rows = p.tokens << P.group_log2;
   const size_t slot_floats = (size_t)P.part_rows * (A + 2);
   // every lane of a warp goes through the same number of rounds: the shuffles need them all
   for (int base = lo; base < hi; base += kThreads / LANES) {
     const int task = base + threadIdx.x / LANES;
     const bool on = task < hi;
-    const int row = on ? task / (A / 4) : 0, col = on ? task % (A / 4) : 0;
+    const int row = !on ? 0 : W ? task % rows : task / (A / 4), col = !on ? 0 : W ? task / rows : task % (A / 4);
     float2 ml[kHold];
     float4 o[kHold];
 #pragma unroll
@@ -681,7 +703,7 @@ __device__ void join_rows(const CrossParams& P, const Piece& p, int first, int n
       if (!on || i >= n) continue;
       const float* piece = P.part + (size_t)(2 * (first + i) + (i == 0 ? 1 : 0)) * slot_floats;
       ml[k] = __ldcg(reinterpret_cast<const float2*>(piece + (size_t)P.part_rows * A) + row);
-      o[k] = __ldcg(reinterpret_cast<const float4*>(piece + (size_t)row * A) + col);
+      o[k] = __ldcg(reinterpret_cast<const float4*>(piece) + (W ? (size_t)col * P.part_rows + row : (size_t)row * (A / 4) + col));
     }
     float M = kNoKey;
 #pragma unroll
@@ -722,13 +744,13 @@ __device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
 }
 
 // All threads, after the pipeline.
-template <int A, class C>
+template <int A, bool W, class C>
 __device__ void join(const CrossParams& P, C& c) {
   if (c.abort) {                       // the others still wait for this CTA's arrivals
     __syncthreads();
     if (threadIdx.x == 0) {
-      Pieces pieces(P, c);
-      Piece p;
+      Pieces<W> pieces(P, c);
+      Piece<W> p;
       c.n_cut = 0;
       while (pieces.next(P, p))
         if (!p.whole()) c.cut[c.n_cut++] = p;
@@ -736,13 +758,13 @@ __device__ void join(const CrossParams& P, C& c) {
     __syncthreads();
   }
   const int n_cut = c.n_cut;           // its first piece's item, its last piece's, or both
-  auto first_of = [&](const Piece& p) { return p.at / c.share; };
+  auto first_of = [&](const Part& p) { return p.at / c.share; };
   if (threadIdx.x == 0 && n_cut) {     // arrive for both before waiting for either
     __threadfence();                   // with the barrier before join(): every thread's partial results
     for (int k = 0; k < n_cut; ++k) atomicAdd(P.joins + first_of(c.cut[k]), 1u);
   }
   for (int k = 0; k < n_cut; ++k) {
-    const Piece& p = c.cut[k];
+    const Part& p = c.cut[k];
     const int first = first_of(p), n = (p.at + (p.tiles - 1) * p.step) / c.share - first + 1;
     unsigned* count = P.joins + first;
     if (threadIdx.x == 0) {
@@ -761,10 +783,10 @@ __device__ void join(const CrossParams& P, C& c) {
     if (c.go && !c.abort) {
       const int rows = p.tokens << P.group_log2, tasks = rows * (A / 4), i = (int)blockIdx.x - first;
       const int lo = (int)((long long)tasks * i / n), hi = (int)((long long)tasks * (i + 1) / n);
-      if (n <= kHold) join_rows<A, 1>(P, p, first, n, lo, hi);
-      else if (n <= 4 * kHold) join_rows<A, 4>(P, p, first, n, lo, hi);
-      else if (n <= 16 * kHold) join_rows<A, 16>(P, p, first, n, lo, hi);
-      else join_rows<A, 32>(P, p, first, n, lo, hi);
+      if (n <= kHold) join_rows<A, W, 1>(P, p, first, n, lo, hi);
+      else if (n <= 4 * kHold) join_rows<A, W, 4>(P, p, first, n, lo, hi);
+      else if (n <= 16 * kHold) join_rows<A, W, 16>(P, p, first, n, lo, hi);
+      else join_rows<A, W, 32>(P, p, first, n, lo, hi);
     }
     __syncthreads();
     if (threadIdx.x == 0 && atomicAdd(count, 1u) == 2u * n - 1) *count = 0u;
@@ -785,7 +807,7 @@ __device__ void zero_rows(const CrossParams& P) {
   }
 }
 
-template <int A>
+template <int A, bool W>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const CrossParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap) {
@@ -833,13 +855,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      loader<A>(P, &kmap, &vmap, &qmap, T, c);
+      loader<A, W>(P, &kmap, &vmap, &qmap, T, c);
     } else if (warp < 11) {
-      issuer<A>(P, T, c, tmem, warp - 9);
+      issuer<A, W>(P, T, c, tmem, warp - 9);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax<A>(P, T, c, tmem, warp >> 2);
+    softmax<A, W>(P, T, c, tmem, warp >> 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -848,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (c.any_empty) zero_rows<A>(P);
-  join<A>(P, c);
+  join<A, W>(P, c);
 }
 
 template <int A>
@@ -856,9 +878,9 @@ constexpr int kSmem = 1024 + (int)sizeof(Tiles<A>) + (int)sizeof(Ctl<Tiles<A>::k
 static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory");
 static_assert(sizeof(Tiles<128>) % 16 == 0 && sizeof(Tiles<64>) % 16 == 0, "control block 16-byte aligned");
 
-template <int A>
+template <int A, bool W>
 cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int grid, cudaStream_t stream) {
-  const void* kernel = reinterpret_cast<const void*>(cross_kernel<A>);
+  const void* kernel = reinterpret_cast<const void*>(cross_kernel<A, W>);
   const cudaError_t e = opt_in_smem(kernel, kSmem<A>);
   if (e != cudaSuccess) return e;
   CrossParams pc = p;
@@ -882,7 +904,10 @@ int cross_part_rows(int max_q_len, int group) {
 }
 
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream) {
-  return head_dim == 128 ? launch_cross_t<128>(p, maps, grid, stream) : launch_cross_t<64>(p, maps, grid, stream);
+  const bool wide = ((long long)p.max_q_len << p.group_log2) > kRows / 2;      // an item can be
+  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true> : launch_cross_t<128, false>)
+                                      : (wide ? launch_cross_t<64, true> : launch_cross_t<64, false>);
+  return launch(p, maps, grid, stream);
 }
 
 }  // namespace cb

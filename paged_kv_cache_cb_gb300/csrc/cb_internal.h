@@ -125,6 +125,7 @@ struct CrossParams {
   const int32_t* block_tables;  // [n_reqs][max_blocks_per_seq]
   uint16_t* out;                // bf16 [n_tokens][Hq][A]
   float* part;                  // [2 * grid] partial results: [part_rows][A] O, then [part_rows][2] (max, sum)
+                                // (a launch with wide items: O as [A / 4][part_rows][4])
   unsigned* joins;              // [kMaxDecodeGrid] arrivals at cut items, zero between launches
   unsigned int* err;            // the launching stream's error word
   int max_blocks_per_seq, n_reqs, n_tokens, max_q_len, max_kv_len, num_blocks, n_q_heads, n_kv_heads;
