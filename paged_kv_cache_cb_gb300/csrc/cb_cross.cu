@@ -103,11 +103,10 @@ struct alignas(16) Ctl {
   int any_empty;                       // a request has tokens and no keys
   int share, total;                    // units of a CTA's range, of all
   int start_r, start_u;                // the request that the CTA's range begins in, its first unit
-  int n_cut;                           // pieces of cut items
   int go;
-  Part cut[2];
+  Part cut[2];                         // pieces of cut items: begun before the CTA, by it; tiles 0: none
   long long scan[kThreads / 32];
-  float2 ml[128];                      // group B's (max, sum) of a narrow item
+  float2 ml[128];                      // (max, sum) of a narrow item's second group
 };
 
 // ---------------------------------------------------------------- plan
@@ -371,6 +370,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
   uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   uint32_t st = 0, ph = 0;                         // the ring's next buffer
+  int second = side;                               // see softmax
   Pieces<W> pieces(P, c);
   Piece<W> p{};
   bool ok = true;
@@ -446,7 +446,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
     const uint32_t x = qs + (p.wide() && side), slot = __shfl_sync(FULL, x & 1, 0);
-    const bool mine = p.wide() || n > side;          // this group has a tile
+    const bool mine = p.wide() || n > second;        // this group has a tile
     if (p.wide()) {
       const uint32_t y = qs + !side;               // the other group's query tile
       if (side) ok = give_back(&c.q_full[y & 1], &c.q_empty[y & 1], (y >> 1) & 1);
@@ -456,18 +456,19 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
       for (int j = 0; ok && j < n; ++j) ok = values(j == 0, slot, j + 1 < n, j + 2 == n);
     } else {
       ok = mine ? warp_wait(P, &c.q_full[slot], (x >> 1) & 1) : give_back(&c.q_full[slot], &c.q_empty[slot], (x >> 1) & 1);
-      // K(0) K(1) V(0) K(2) V(1) .. V(n - 1): up to V(side)
-      if (side) ok = ok && other();
-      if (mine) ok = ok && scores(slot, side + 2 >= n);
-      if (n > 1 && !side) ok = ok && other();
-      if (side) ok = ok && other();
-      if (n > 2 && side) ok = ok && other();
-      for (int j = side; ok && j < n; j += 2) {
-        ok = values(j == side, slot, j + 2 < n, j + 4 >= n);
+      // K(0) K(1) V(0) K(2) V(1) .. V(n - 1): up to V(second)
+      if (second) ok = ok && other();
+      if (mine) ok = ok && scores(slot, second + 2 >= n);
+      if (n > 1 && !second) ok = ok && other();
+      if (second) ok = ok && other();
+      if (n > 2 && second) ok = ok && other();
+      for (int j = second; ok && j < n; j += 2) {
+        ok = values(j == second, slot, j + 2 < n, j + 4 >= n);
         if (j + 1 < n) ok = ok && other();         // V(j + 1)
         if (j + 3 < n) ok = ok && other();         // K(j + 3)
       }
     }
+    if (!W) second ^= 1;
     qs += p.wide() ? 2 : 1;
   }
   if (!ok) c.abort = 1;
@@ -498,23 +499,29 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
   const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  const uint32_t s_at = tmem + lanes + side * 128, o_at = tmem + lanes + 256 + side * A;
+  const uint32_t s_at = tmem + lanes + side * 128, o_at = tmem + lanes + 256 + side * A, other_o = tmem + lanes + 256 + (side ^ 1) * A;
   const int group = 1 << P.group_log2, tok_tile = kTileM >> P.group_log2;
   const float sl2 = P.scale_log2;
-  // key tiles before this piece; this group's; group B's (counted by both); pieces that both share
-  uint32_t kt = 0, sc = 0, scb = 0, shared = 0;
+  // key tiles before this piece; this group's; the other group's; pieces that both share
+  uint32_t kt = 0, sc = 0, oc = 0, shared = 0;
+  // Of a narrow piece, the group that has key tiles 1, 3, ..: the groups in turn, so that pieces of
+  // one tile run beside each other and those of an odd number fill both groups (32 heads of
+  // dimension 64, 100 tokens over 128 keys: 43.5 us, 68.5 with B always; 1408 keys: 203 and 218).
+  // Where some items are wide, that cost these more than it gave (prompts 266 us, 263 without).
+  int second = W ? side : side ^ 1;
   Pieces<W> pieces(P, c);
   Piece<W> p;
   while (!__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
-    const int mine = p.wide() ? n : side ? n / 2 : (n + 1) / 2;
+    if (!W) second ^= 1;
+    const int mine = p.wide() ? n : (n + !second) / 2;
     const int tok = (p.wide() && side ? tok_tile : 0) + (row >> P.group_log2);      // of the item
     const bool valid = tok < p.tokens;
     const bool busy = __any_sync(FULL, valid);                                    // this warp has rows
     float m = kNoKey, l = 0.f;         // running max times scale * log2 e; sum
     bool ok = true;
     for (int i = 0; i < mine; ++i, ++sc) {
-      const int j = p.wide() ? i : 2 * i + side, key0 = (p.ta + j) * kTileN;
+      const int j = p.wide() ? i : 2 * i + second, key0 = (p.ta + j) * kTileN;
       ok = warp_wait(P, &c.s_full[side], sc & 1);
       if (!ok) break;
       tc_fence_after();
@@ -598,7 +605,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
     }
     kt += n;
     const bool two = !p.wide() && n > 1; // both groups hold parts of the same rows
-    scb += p.wide() ? n : n / 2;
+    oc += p.wide() ? n : n - mine;
+    shared += two;
     if (ok && mine) ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
     if (!ok) {
       c.abort = 1;
@@ -607,12 +615,12 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
     tc_fence_after();
     float alpha = 1.f, beta = 0.f;     // of this group's O and of the other's
     if (two) {
-      if (side == 1) {
+      if (second) {
         c.ml[row] = make_float2(m, l);
         mbar_arrive(&c.ml_full);
-        continue;                      // group A takes it from here, and frees group B's O
+        continue;                      // the first group takes it from here, and frees both O
       }
-      if (!warp_wait(P, &c.o_done[1], (scb - 1) & 1) || !warp_wait(P, &c.ml_full, shared++ & 1)) {
+      if (!warp_wait(P, &c.ml_full, (shared - 1) & 1) || !warp_wait(P, &c.o_done[side ^ 1], (oc - 1) & 1)) {
         c.abort = 1;
         break;
       }
@@ -624,15 +632,16 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
       l = l * alpha + b.y * beta;
       m = mn;
     } else if (!mine) {
-      continue;                        // a narrow piece of one tile has nothing for group B
+      continue;                        // a narrow piece of one tile has nothing for the second group
     }
     const bool whole = p.whole();
-    if (!whole && side == 0 && row == 0) c.cut[c.n_cut++] = p;
+    const int which = p.ta == 0;       // of cut pieces and partial results
+    if (!whole && row == 0 && !(p.wide() && side)) c.cut[which] = p;
     const float inv = whole ? 1.f / l : 1.f;
     alpha *= inv;
     beta *= inv;
     const int irow = (p.wide() && side ? 128 : 0) + row;
-    const int slot = 2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0);
+    const int slot = 2 * (int)blockIdx.x + which;
     float* part = P.part + (size_t)slot * P.part_rows * (A + 2);
     uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
     if (busy) {
@@ -642,7 +651,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
         tmem_ld32(o_at + ch * 32, o);
         if (two) {
           float b[32];
-          tmem_ld32(o_at + A + ch * 32, b);
+          tmem_ld32(other_o + ch * 32, b);
           tmem_wait_ld();
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = o[k] * alpha + b[k] * beta;
@@ -667,7 +676,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
     }
     tc_fence_before();
     mbar_arrive(&c.o_free[side]);
-    if (two) mbar_arrive(&c.o_free[1]);
+    if (two) mbar_arrive(&c.o_free[side ^ 1]);
   }
 }
 
@@ -751,20 +760,20 @@ __device__ void join(const CrossParams& P, C& c) {
     if (threadIdx.x == 0) {
       Pieces<W> pieces(P, c);
       Piece<W> p;
-      c.n_cut = 0;
       while (pieces.next(P, p))
-        if (!p.whole()) c.cut[c.n_cut++] = p;
+        if (!p.whole()) c.cut[p.ta == 0] = p;
     }
     __syncthreads();
   }
-  const int n_cut = c.n_cut;           // its first piece's item, its last piece's, or both
   auto first_of = [&](const Part& p) { return p.at / c.share; };
-  if (threadIdx.x == 0 && n_cut) {     // arrive for both before waiting for either
+  if (threadIdx.x == 0) {              // arrive for both before waiting for either
     __threadfence();                   // with the barrier before join(): every thread's partial results
-    for (int k = 0; k < n_cut; ++k) atomicAdd(P.joins + first_of(c.cut[k]), 1u);
+    for (int k = 0; k < 2; ++k)
+      if (c.cut[k].tiles) atomicAdd(P.joins + first_of(c.cut[k]), 1u);
   }
-  for (int k = 0; k < n_cut; ++k) {
+  for (int k = 0; k < 2; ++k) {
     const Part& p = c.cut[k];
+    if (!p.tiles) continue;
     const int first = first_of(p), n = (p.at + (p.tiles - 1) * p.step) / c.share - first + 1;
     unsigned* count = P.joins + first;
     if (threadIdx.x == 0) {
@@ -836,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&c.ml_full, 128);
     c.abort = 0;
     c.any_empty = 0;
-    c.n_cut = 0;
+    c.cut[0].tiles = c.cut[1].tiles = 0;
     fence_mbar_init();
     prefetch_tmap(&kmap);
     prefetch_tmap(&vmap);
