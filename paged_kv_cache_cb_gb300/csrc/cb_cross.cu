@@ -58,13 +58,15 @@ constexpr int kLeast = 8;              // of a CTA's share
 // K and V tiles share one ring of buffers, in the order of their use: a wide item's
 // K(0) V(0) K(1) V(1) .., a narrow one's K(0) K(1) V(0) K(2) V(1) .. V(n - 1), since
 // its two groups begin with a key tile each.
-template <int A>
+// F: a launch whose items have at most 32 rows; see softmax_few.
+template <int A, bool F>
 struct Tiles {
   static constexpr int kHalves = A / 64;
   static constexpr int kHalfBytes = 128 * 128;
   static constexpr int kBytes = kHalves * kHalfBytes;     // of 128 rows
   static constexpr int kRing = A == 128 ? 5 : 10;
   uint8_t q[2][kHalves][128][128];
+  uint8_t p[F ? 2 : 0][2][32][128];    // a group's weights; the products read 128 rows, that is, into kv
   uint8_t kv[kRing][kHalves][128][128];
 };
 
@@ -90,7 +92,7 @@ struct Piece : Part {
   __device__ __forceinline__ bool wide() const { return W && two_row_tiles; }
 };
 
-template <int NS>
+template <int NS, bool F>
 struct alignas(16) Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[NS], empty[NS];
@@ -106,6 +108,8 @@ struct alignas(16) Ctl {
   int go;
   Part cut[2];                         // pieces of cut items: begun before the CTA, by it; tiles 0: none
   long long scan[kThreads / 32];
+  float2 top[F ? 2 : 0][4][32];        // per group and warp: a row's maximum, and whether m must move up
+  float sum[F ? 2 : 0][4][32];         // a row's weights
   float2 ml[128];                      // (max, sum) of a narrow item's second group
 };
 
@@ -267,10 +271,10 @@ __device__ __forceinline__ bool elect_lane() {
 // elected lane asks for all of them, from coordinates that are the same in the whole
 // warp: a box per lane took 62 cycles each (1000 a tile, as long as its share of the
 // memory's time), the loads of one lane after the other.
-template <int A, bool W, class C>
+template <int A, bool W, bool F, class C>
 __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUtensorMap* vmap, const CUtensorMap* qmap,
-                       Tiles<A>& T, C& c) {
-  using TT = Tiles<A>;
+                       Tiles<A, F>& T, C& c) {
+  using TT = Tiles<A, F>;
   constexpr int H = TT::kHalves, NS = TT::kRing;
   const unsigned FULL = 0xffffffffu;
   const int lane = threadIdx.x & 31;
@@ -314,10 +318,12 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
       const uint32_t st = qs & 1;
       ok = warp_wait(P, &c.q_empty[st], ((qs >> 1) & 1) ^ 1);
       if (ok && elect_lane()) {
-        mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes);
+        mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes * (F ? 4 : 1));
 #pragma unroll
         for (int h = 0; h < H; ++h)
-          tma_load_3d(&T.q[st][h][0][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
+#pragma unroll
+          for (int w = 0; w < (F ? 4 : 1); ++w)
+            tma_load_3d(&T.q[st][h][w * 32][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
       }
       __syncwarp();
     }
@@ -356,9 +362,9 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
 // are read from uniform registers, which the compiler uses for values of a converged
 // warp: issued from a branch of one lane, each MMA moved its descriptors there first
 // and took about 110 cycles instead of the 64 that it runs.
-template <int A, bool W, class C>
-__device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
-  using TT = Tiles<A>;
+template <int A, bool W, bool F, class C>
+__device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem, int side) {
+  using TT = Tiles<A, F>;
   constexpr int NS = TT::kRing;
   constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, 0), kIdescPV = idesc_bf16_f32(128, A, 1);
   const unsigned FULL = 0xffffffffu;
@@ -368,6 +374,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
+  const uint64_t p0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, p) + side * (uint32_t)sizeof(T.p[0]), 16, 1024);
   uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   uint32_t st = 0, ph = 0;                         // the ring's next buffer
   int second = side;                               // see softmax
@@ -433,8 +440,12 @@ __device__ void issuer(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, i
     if (elect_lane()) {
 #pragma unroll
       for (int ks = 0; ks < kTileN / 16; ++ks)
-        tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
-                      (!first || ks > 0) ? 1u : 0u);
+        if constexpr (F)
+          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * (uint32_t)sizeof(T.p[0][0]) + (ks & 3) * 32) >> 4),
+                     v + ((ks * 16 * 128) >> 4), kIdescPV, (!first || ks > 0) ? 1u : 0u);
+        else
+          tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
+                        (!first || ks > 0) ? 1u : 0u);
       tc_commit(&c.o_done[side]);
       tc_commit(&c.empty[vst]);
       if (more) issue_s(slot, kst, last);
@@ -492,15 +503,59 @@ __device__ __forceinline__ void rescale(uint32_t o, float alpha) {
   }
 }
 
+// A row's result: its output if the piece is its whole item, else its part of the join.  O and
+// the other group's O (two) are scaled by alpha and beta; busy: some row of the warp is valid.
+template <int A, bool W>
+__device__ __forceinline__ void write_rows(const CrossParams& P, const Part& p, int row, int irow, bool busy, bool valid,
+                                           bool two, uint32_t o_at, uint32_t other_o, float alpha, float beta, float m, float l) {
+  if (!busy) return;
+  const bool whole = p.whole();
+  const int group = 1 << P.group_log2;
+  const float inv = whole ? 1.f / l : 1.f;
+  alpha *= inv;
+  beta *= inv;
+  float* part = P.part + (size_t)(2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0)) * P.part_rows * (A + 2);
+  const int tok = irow >> P.group_log2;
+  uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
+#pragma unroll 1
+  for (int ch = 0; ch < A / 32; ++ch) {
+    float o[32];
+    tmem_ld32(o_at + ch * 32, o);
+    if (two) {
+      float b[32];
+      tmem_ld32(other_o + ch * 32, b);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = o[k] * alpha + b[k] * beta;
+    } else {
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] *= alpha;
+    }
+    if (valid && whole) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        *reinterpret_cast<uint4*>(dst + ch * 32 + k) = make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                                                                  pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+    } else if (valid) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 4)
+        reinterpret_cast<float4*>(part)[W ? (size_t)(ch * 8 + k / 4) * P.part_rows + irow : (size_t)irow * (A / 4) + ch * 8 + k / 4] =
+            make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+    }
+  }
+  if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)P.part_rows * A + irow * 2) = make_float2(m, l);
+}
+
 template <int A, bool W, class C>
-__device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, int side) {
-  using TT = Tiles<A>;
+__device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t tmem, int side) {
+  using TT = Tiles<A, false>;
   constexpr int H = TT::kHalves, NS = TT::kRing;
   const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const uint32_t s_at = tmem + lanes + side * 128, o_at = tmem + lanes + 256 + side * A, other_o = tmem + lanes + 256 + (side ^ 1) * A;
-  const int group = 1 << P.group_log2, tok_tile = kTileM >> P.group_log2;
+  const int tok_tile = kTileM >> P.group_log2;
   const float sl2 = P.scale_log2;
   // key tiles before this piece; this group's; the other group's; pieces that both share
   uint32_t kt = 0, sc = 0, oc = 0, shared = 0;
@@ -634,50 +689,169 @@ __device__ void softmax(const CrossParams& P, Tiles<A>& T, C& c, uint32_t tmem, 
     } else if (!mine) {
       continue;                        // a narrow piece of one tile has nothing for the second group
     }
-    const bool whole = p.whole();
-    const int which = p.ta == 0;       // of cut pieces and partial results
-    if (!whole && row == 0 && !(p.wide() && side)) c.cut[which] = p;
-    const float inv = whole ? 1.f / l : 1.f;
-    alpha *= inv;
-    beta *= inv;
-    const int irow = (p.wide() && side ? 128 : 0) + row;
-    const int slot = 2 * (int)blockIdx.x + which;
-    float* part = P.part + (size_t)slot * P.part_rows * (A + 2);
-    uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
-    if (busy) {
-#pragma unroll 1
-      for (int ch = 0; ch < A / 32; ++ch) {
-        float o[32];
-        tmem_ld32(o_at + ch * 32, o);
-        if (two) {
-          float b[32];
-          tmem_ld32(other_o + ch * 32, b);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = o[k] * alpha + b[k] * beta;
-        } else {
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= alpha;
-        }
-        if (valid && whole) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(dst + ch * 32 + k) = make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
-                                                                      pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
-        } else if (valid) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            reinterpret_cast<float4*>(part)[W ? (size_t)(ch * 8 + k / 4) * P.part_rows + irow : (size_t)irow * (A / 4) + ch * 8 + k / 4] =
-                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
-      }
-      if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)P.part_rows * A + irow * 2) = make_float2(m, l);
-    }
+    if (row == 0 && !p.whole() && !(p.wide() && side)) c.cut[p.ta == 0] = p;
+    write_rows<A, W>(P, p, row, (p.wide() && side ? 128 : 0) + row, busy, valid, two, o_at, other_o, alpha, beta, m, l);
     tc_fence_before();
     mbar_arrive(&c.o_free[side]);
     if (two) mbar_arrive(&c.o_free[side ^ 1]);
   }
+}
+
+// Items of at most 32 rows: thread = row leaves three of a group's warps idle, while one
+// takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
+// one copy for each warp's lanes, and so have the scores: warp w makes the weights of keys
+// 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
+// lanes.  m is the same in the four warps, which tell each other their maxima when it may move;
+// sums stay apart until the item's end.  Every exit is taken by the four warps together:
+// they meet at named barriers.
+template <int A, class C>
+__device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint32_t tmem, int side) {
+  using TT = Tiles<A, true>;
+  constexpr int H = TT::kHalves, NS = TT::kRing;
+  const int thread = threadIdx.x & 127, warp = thread >> 5, row = thread & 31, bar = 1 + side;
+  const uint32_t s_at = tmem + ((uint32_t)(warp * 32) << 16) + side * 128 + warp * 32;
+  const uint32_t o_at = tmem + 256 + side * A, other_o = tmem + 256 + (side ^ 1) * A;     // warp 0
+  const float sl2 = P.scale_log2;
+  uint8_t* const weights = T.p[side][warp >> 1][row];
+  uint32_t kt = 0, sc = 0, oc = 0, shared = 0;          // as in softmax
+  int second = side ^ 1;
+  bool ok = true;
+  Pieces<false> pieces(P, c);
+  Piece<false> p;
+  while (pieces.next(P, p)) {
+    if (named_bar_or(bar, 128, !ok || c.abort)) break;
+    const int n = p.tb - p.ta;
+    second ^= 1;
+    const int mine = (n + !second) / 2;
+    const int tok = row >> P.group_log2;
+    const bool valid = tok < p.tokens;
+    float m = kNoKey, l = 0.f;
+    for (int i = 0; i < mine; ++i, ++sc) {
+      const int key0 = (p.ta + 2 * i + second) * kTileN, key = key0 + warp * 32;
+      ok = ok && warp_wait(P, &c.s_full[side], sc & 1);
+      tc_fence_after();
+      float s[32];
+      tmem_ld32(s_at, s);
+      tmem_wait_ld();
+      if (key + 32 > p.q.kv) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = key + k < p.q.kv ? s[k] : kNoKey;
+      }
+      const uint64_t sl2x2 = f2(sl2, sl2);
+      float alpha = 1.f, add;
+      uint32_t pk[16];
+      bool known = i > 0, bad = i == 0, met = true;
+#pragma unroll 1
+      while (true) {
+        if (!known) {
+          float a[2] = {kNoKey, kNoKey};
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) a[(k >> 1) & 1] = max3(a[(k >> 1) & 1], s[k], s[k + 1]);
+          c.top[side][warp][row] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
+          if (named_bar_or(bar, 128, !ok)) {
+            met = false;
+            break;
+          }
+          float mn = m, need = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 x = c.top[side][w][row];
+            mn = fmaxf(mn, x.x);
+            need += x.y;
+          }
+          if (need > 0.f && mn > m) {
+            alpha = ex2(m - mn);
+            m = mn;
+          }
+          if (i > 0 && warp == 0) {
+            ok = warp_wait(P, &c.o_done[side], (sc - 1) & 1);
+            if (ok) {
+              tc_fence_after();
+              rescale<A>(o_at, alpha);
+              tmem_wait_st();
+            }
+          }
+        }
+        const float ms = m == kNoKey ? 0.f : m;
+        const uint64_t nm2 = f2(-ms, -ms);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          float x0, x1;
+          f2split(ffma2(f2(s[2 * k], s[2 * k + 1]), sl2x2, nm2), x0, x1);
+          const float p0 = ex2(x0), p1 = ex2(x1);
+          sum[k & 1] = fadd2(sum[k & 1], f2(p0, p1));
+          pk[k] = pack_bf16(p0, p1);
+        }
+        float t[4];
+        f2split(sum[0], t[0], t[1]);
+        f2split(sum[1], t[2], t[3]);
+        add = (t[0] + t[1]) + (t[2] + t[3]);
+        if (!known) break;
+        bad = valid && !(add <= kMostSum && m > kNoKey);
+        if (!named_bar_or(bar, 128, bad || !ok)) break;
+        known = false;
+      }
+      if (!met) {
+        ok = false;
+        break;
+      }
+      l = l * alpha + add;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<uint4*>(weights + ((((warp & 1) * 4 + u) ^ (row & 7)) << 4)) =
+            make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+      if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {       // as in softmax
+        const uint32_t t = 2 * (kt + n) - 1, st = t % NS;
+        ok = ok && warp_wait(P, &c.full[st], (t / NS) & 1);
+        const int r0 = p.q.kv - key0, r1 = ((p.q.kv + kBlockSize - 1) & ~(kBlockSize - 1)) - key0;
+        if (ok)
+          for (int x = thread; x < (r1 - r0) * H * 8; x += 128)
+            *reinterpret_cast<uint4*>(&T.kv[st][(x >> 3) % H][r0 + x / (H * 8)][(x & 7) << 4]) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      if (ok) mbar_arrive(&c.p_full[side]);
+    }
+    kt += n;
+    const bool two = n > 1;
+    oc += n - mine;
+    shared += two;
+    if (!mine) continue;
+    ok = ok && warp_wait(P, &c.o_done[side], (sc - 1) & 1);
+    tc_fence_after();
+    c.sum[side][warp][row] = l;
+    if (two && second) {
+      if (warp == 0) c.ml[row].x = m;
+      if (ok) mbar_arrive(&c.ml_full);
+      continue;
+    }
+    if (named_bar_or(bar, 128, !ok)) {
+      ok = false;
+      break;
+    }
+    if (warp > 0) continue;            // their sums are read before any of them comes here again
+    l = (c.sum[side][0][row] + c.sum[side][1][row]) + (c.sum[side][2][row] + c.sum[side][3][row]);
+    float alpha = 1.f, beta = 0.f;
+    if (two) {
+      ok = warp_wait(P, &c.ml_full, (shared - 1) & 1) && warp_wait(P, &c.o_done[side ^ 1], (oc - 1) & 1);
+      if (!ok) continue;
+      tc_fence_after();
+      const int o = side ^ 1;
+      const float bm = c.ml[row].x, bl = (c.sum[o][0][row] + c.sum[o][1][row]) + (c.sum[o][2][row] + c.sum[o][3][row]);
+      const float mn = fmaxf(m, bm), ms = mn == kNoKey ? 0.f : mn;
+      alpha = ex2(m - ms);
+      beta = ex2(bm - ms);
+      l = l * alpha + bl * beta;
+      m = mn;
+    }
+    if (row == 0 && !p.whole()) c.cut[p.ta == 0] = p;
+    write_rows<A, false>(P, p, row, row, true, valid, two, o_at, other_o, alpha, beta, m, l);
+    tc_fence_before();
+    mbar_arrive(&c.o_free[side]);
+    if (two) mbar_arrive(&c.o_free[side ^ 1]);
+  }
+  if (!ok) c.abort = 1;
 }
 
 // ---------------------------------------------------------------- joining
@@ -816,16 +990,16 @@ __device__ void zero_rows(const CrossParams& P) {
   }
 }
 
-template <int A, bool W>
+template <int A, bool W, bool F>
 __global__ void __launch_bounds__(kThreads, 1)
     cross_kernel(const CrossParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                  const __grid_constant__ CUtensorMap qmap) {
-  using TT = Tiles<A>;
+  using TT = Tiles<A, F>;
   constexpr int NS = TT::kRing;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TT& T = *reinterpret_cast<TT*>(base);
-  Ctl<NS>& c = *reinterpret_cast<Ctl<NS>*>(base + sizeof(TT));
+  Ctl<NS, F>& c = *reinterpret_cast<Ctl<NS, F>*>(base + sizeof(TT));
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -836,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.s_full[s], 1);
       mbar_init(&c.p_full[s], 128);
       mbar_init(&c.o_done[s], 1);
-      mbar_init(&c.o_free[s], 128);
+      mbar_init(&c.o_free[s], F ? 32 : 128);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(&c.full[s], 1);
@@ -864,13 +1038,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 8) {
-      loader<A, W>(P, &kmap, &vmap, &qmap, T, c);
+      loader<A, W, F>(P, &kmap, &vmap, &qmap, T, c);
     } else if (warp < 11) {
-      issuer<A, W>(P, T, c, tmem, warp - 9);
+      issuer<A, W, F>(P, T, c, tmem, warp - 9);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    softmax<A, W>(P, T, c, tmem, warp >> 2);
+    if constexpr (F)
+      softmax_few<A>(P, T, c, tmem, warp >> 2);
+    else
+      softmax<A, W>(P, T, c, tmem, warp >> 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -882,20 +1059,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   join<A, W>(P, c);
 }
 
-template <int A>
-constexpr int kSmem = 1024 + (int)sizeof(Tiles<A>) + (int)sizeof(Ctl<Tiles<A>::kRing>);
-static_assert(kSmem<128> <= 232448 && kSmem<64> <= 232448, "shared memory");
-static_assert(sizeof(Tiles<128>) % 16 == 0 && sizeof(Tiles<64>) % 16 == 0, "control block 16-byte aligned");
+template <int A, bool F>
+constexpr int kSmem = 1024 + (int)sizeof(Tiles<A, F>) + (int)sizeof(Ctl<Tiles<A, F>::kRing, F>);
+static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem<64, true> <= 232448, "shared memory");
+static_assert(sizeof(Tiles<128, false>) % 16 == 0 && sizeof(Tiles<64, false>) % 16 == 0 && sizeof(Tiles<64, true>) % 16 == 0,
+              "control block 16-byte aligned");
 
-template <int A, bool W>
+template <int A, bool W, bool F>
 cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int grid, cudaStream_t stream) {
-  const void* kernel = reinterpret_cast<const void*>(cross_kernel<A, W>);
-  const cudaError_t e = opt_in_smem(kernel, kSmem<A>);
+  const void* kernel = reinterpret_cast<const void*>(cross_kernel<A, W, F>);
+  const cudaError_t e = opt_in_smem(kernel, kSmem<A, F>);
   if (e != cudaSuccess) return e;
   CrossParams pc = p;
   void* args[] = {&pc, const_cast<CUtensorMap*>(&maps[0]), const_cast<CUtensorMap*>(&maps[1]),
                   const_cast<CUtensorMap*>(&maps[2])};
-  return cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, kSmem<A>, stream);
+  return cudaLaunchCooperativeKernel(kernel, dim3(grid), dim3(kThreads), args, kSmem<A, F>, stream);
 }
 
 }  // namespace
@@ -913,9 +1091,12 @@ int cross_part_rows(int max_q_len, int group) {
 }
 
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream) {
-  const bool wide = ((long long)p.max_q_len << p.group_log2) > kRows / 2;      // an item can be
-  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true> : launch_cross_t<128, false>)
-                                      : (wide ? launch_cross_t<64, true> : launch_cross_t<64, false>);
+  const long long rows = (long long)p.max_q_len << p.group_log2;      // that an item can have
+  const bool wide = rows > kRows / 2;
+  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true, false> : launch_cross_t<128, false, false>)
+                      : wide          ? launch_cross_t<64, true, false>
+                      : rows <= 32    ? launch_cross_t<64, false, true>
+                                      : launch_cross_t<64, false, false>;
   return launch(p, maps, grid, stream);
 }
 
