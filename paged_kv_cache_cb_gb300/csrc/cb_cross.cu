@@ -66,8 +66,18 @@ struct Tiles {
   static constexpr int kBytes = kHalves * kHalfBytes;     // of 128 rows
   static constexpr int kRing = A == 128 ? 5 : 10;
   uint8_t q[2][kHalves][128][128];
-  uint8_t p[F ? 2 : 0][2][32][128];    // a group's weights; the products read 128 rows, that is, into kv
+  // The weights of two groups, two halves of the keys, kFewRows rows (the products read 128, that
+  // is, into what follows); per group, warp and row its maximum, and whether m must move up; its
+  // weights' sum.  Dimension 128 leaves no room for them: they take the half of the query tiles
+  // that items of 16 rows do not use.
+  uint8_t few[F && A == 64 ? 2 * 2 * 32 * 128 + 2 * 4 * 32 * 12 : 0];
   uint8_t kv[kRing][kHalves][128][128];
+  static constexpr int kFewRows = A == 64 ? 32 : 16;
+  [[maybe_unused]] static constexpr int kQBytes = 2 * kBytes, kRowsBytes = kFewRows * 128;
+  static constexpr int weights_at(int group) { return A == 64 ? kQBytes + group * 2 * kRowsBytes : 16 * 128 + group * 32 * 128; }
+  [[maybe_unused]] static constexpr int kWeightsHalf = A == 64 ? kRowsBytes : kHalfBytes;
+  [[maybe_unused]] static constexpr int kTopAt = A == 64 ? kQBytes + 4 * kRowsBytes : kBytes + 16 * 128;
+  [[maybe_unused]] static constexpr int kSumAt = A == 64 ? kTopAt + 2 * 4 * kFewRows * 8 : kBytes + 24 * 128;
 };
 
 // A request's tokens and stored keys; q_len 0: nothing to do.
@@ -92,7 +102,7 @@ struct Piece : Part {
   __device__ __forceinline__ bool wide() const { return W && two_row_tiles; }
 };
 
-template <int NS, bool F>
+template <int NS>
 struct alignas(16) Ctl {
   uint64_t q_full[2], q_empty[2];
   uint64_t full[NS], empty[NS];
@@ -108,8 +118,6 @@ struct alignas(16) Ctl {
   int go;
   Part cut[2];                         // pieces of cut items: begun before the CTA, by it; tiles 0: none
   long long scan[kThreads / 32];
-  float2 top[F ? 2 : 0][4][32];        // per group and warp: a row's maximum, and whether m must move up
-  float sum[F ? 2 : 0][4][32];         // a row's weights
   float2 ml[128];                      // (max, sum) of a narrow item's second group
 };
 
@@ -374,7 +382,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
-  const uint64_t p0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, p) + side * (uint32_t)sizeof(T.p[0]), 16, 1024);
+  const uint64_t p0 = smem_desc_sw128(base + TT::weights_at(side), 16, 1024);
   uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   uint32_t st = 0, ph = 0;                         // the ring's next buffer
   int second = side;                               // see softmax
@@ -441,7 +449,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
 #pragma unroll
       for (int ks = 0; ks < kTileN / 16; ++ks)
         if constexpr (F)
-          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * (uint32_t)sizeof(T.p[0][0]) + (ks & 3) * 32) >> 4),
+          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * TT::kWeightsHalf + (ks & 3) * 32) >> 4),
                      v + ((ks * 16 * 128) >> 4), kIdescPV, (!first || ks > 0) ? 1u : 0u);
         else
           tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
@@ -697,7 +705,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   }
 }
 
-// Items of at most 32 rows: thread = row leaves three of a group's warps idle, while one
+// Items of at most 32 rows (dimension 128: 16): thread = row leaves three of a group's warps idle, while one
 // takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
 // one copy for each warp's lanes, and so have the scores: warp w makes the weights of keys
 // 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
@@ -712,7 +720,13 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
   const uint32_t s_at = tmem + ((uint32_t)(warp * 32) << 16) + side * 128 + warp * 32;
   const uint32_t o_at = tmem + 256 + side * A, other_o = tmem + 256 + (side ^ 1) * A;     // warp 0
   const float sl2 = P.scale_log2;
-  uint8_t* const weights = T.p[side][warp >> 1][row];
+  constexpr int R = TT::kFewRows;
+  uint8_t* const base = reinterpret_cast<uint8_t*>(&T);
+  uint8_t* const weights = base + TT::weights_at(side) + (warp >> 1) * TT::kWeightsHalf + row * 128;
+  // [group][warp][row]
+  float2* const tops = reinterpret_cast<float2*>(base + TT::kTopAt) + side * 4 * R + row;
+  float* const sums = reinterpret_cast<float*>(base + TT::kSumAt) + row;
+  const bool has = row < R;
   uint32_t kt = 0, sc = 0, oc = 0, shared = 0;          // as in softmax
   int second = side ^ 1;
   bool ok = true;
@@ -747,7 +761,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
           float a[2] = {kNoKey, kNoKey};
 #pragma unroll
           for (int k = 0; k < 32; k += 2) a[(k >> 1) & 1] = max3(a[(k >> 1) & 1], s[k], s[k + 1]);
-          c.top[side][warp][row] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
+          if (has) tops[warp * R] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
           if (named_bar_or(bar, 128, !ok)) {
             met = false;
             break;
@@ -755,7 +769,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
           float mn = m, need = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const float2 x = c.top[side][w][row];
+            const float2 x = has ? tops[w * R] : make_float2(kNoKey, 0.f);
             mn = fmaxf(mn, x.x);
             need += x.y;
           }
@@ -799,7 +813,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
       l = l * alpha + add;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<uint4*>(weights + ((((warp & 1) * 4 + u) ^ (row & 7)) << 4)) =
+        if (has) *reinterpret_cast<uint4*>(weights + ((((warp & 1) * 4 + u) ^ (row & 7)) << 4)) =
             make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
       if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {       // as in softmax
         const uint32_t t = 2 * (kt + n) - 1, st = t % NS;
@@ -820,7 +834,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
     if (!mine) continue;
     ok = ok && warp_wait(P, &c.o_done[side], (sc - 1) & 1);
     tc_fence_after();
-    c.sum[side][warp][row] = l;
+    if (has) sums[(side * 4 + warp) * R] = l;
     if (two && second) {
       if (warp == 0) c.ml[row].x = m;
       if (ok) mbar_arrive(&c.ml_full);
@@ -831,14 +845,17 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
       break;
     }
     if (warp > 0) continue;            // their sums are read before any of them comes here again
-    l = (c.sum[side][0][row] + c.sum[side][1][row]) + (c.sum[side][2][row] + c.sum[side][3][row]);
+    auto total = [&](int g) {
+      const float* x = sums + g * 4 * R;
+      return has ? (x[0] + x[R]) + (x[2 * R] + x[3 * R]) : 0.f;
+    };
+    l = total(side);
     float alpha = 1.f, beta = 0.f;
     if (two) {
       ok = warp_wait(P, &c.ml_full, (shared - 1) & 1) && warp_wait(P, &c.o_done[side ^ 1], (oc - 1) & 1);
       if (!ok) continue;
       tc_fence_after();
-      const int o = side ^ 1;
-      const float bm = c.ml[row].x, bl = (c.sum[o][0][row] + c.sum[o][1][row]) + (c.sum[o][2][row] + c.sum[o][3][row]);
+      const float bm = c.ml[row].x, bl = total(side ^ 1);
       const float mn = fmaxf(m, bm), ms = mn == kNoKey ? 0.f : mn;
       alpha = ex2(m - ms);
       beta = ex2(bm - ms);
@@ -999,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TT& T = *reinterpret_cast<TT*>(base);
-  Ctl<NS, F>& c = *reinterpret_cast<Ctl<NS, F>*>(base + sizeof(TT));
+  Ctl<NS>& c = *reinterpret_cast<Ctl<NS>*>(base + sizeof(TT));
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -1060,8 +1077,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int A, bool F>
-constexpr int kSmem = 1024 + (int)sizeof(Tiles<A, F>) + (int)sizeof(Ctl<Tiles<A, F>::kRing, F>);
+constexpr int kSmem = 1024 + (int)sizeof(Tiles<A, F>) + (int)sizeof(Ctl<Tiles<A, F>::kRing>);
 static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem<64, true> <= 232448, "shared memory");
+static_assert(sizeof(Tiles<128, true>) == sizeof(Tiles<128, false>), "no room of its own");
+using Few64 = Tiles<64, true>;
+static_assert(offsetof(Few64, few) == Few64::kQBytes && offsetof(Few64, kv) % 1024 == 0 &&
+              Few64::kSumAt + 2 * 4 * 32 * 4 <= offsetof(Few64, kv), "layout of few rows");
 static_assert(sizeof(Tiles<128, false>) % 16 == 0 && sizeof(Tiles<64, false>) % 16 == 0 && sizeof(Tiles<64, true>) % 16 == 0,
               "control block 16-byte aligned");
 
@@ -1093,10 +1114,12 @@ int cross_part_rows(int max_q_len, int group) {
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream) {
   const long long rows = (long long)p.max_q_len << p.group_log2;      // that an item can have
   const bool wide = rows > kRows / 2;
-  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true, false> : launch_cross_t<128, false, false>)
-                      : wide          ? launch_cross_t<64, true, false>
-                      : rows <= 32    ? launch_cross_t<64, false, true>
-                                      : launch_cross_t<64, false, false>;
+  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true, false>
+                                         : rows <= Tiles<128, true>::kFewRows ? launch_cross_t<128, false, true>
+                                                                              : launch_cross_t<128, false, false>)
+                      : wide ? launch_cross_t<64, true, false>
+                      : rows <= Tiles<64, true>::kFewRows ? launch_cross_t<64, false, true>
+                                                          : launch_cross_t<64, false, false>;
   return launch(p, maps, grid, stream);
 }
 

@@ -238,3 +238,56 @@ def test_refusals():
     assert lib.cb_last_error() == 0
     e = torch.zeros(0, 8, 128, device="cuda", dtype=torch.bfloat16)
     call(q=e, out=e.clone(), cu=b.d_cu * 0)         # no tokens: nothing to do
+
+
+@pytest.mark.parametrize("hq,hk,a,q", [(4, 4, 64, 2), (32, 1, 64, 1), (8, 4, 64, 16), (4, 4, 128, 2), (16, 1, 128, 1), (4, 2, 128, 8),
+                                       (17 * 4, 17, 128, 4), (17, 17, 64, 32)])
+def test_few_rows(hq, hk, a, q):
+    """Items of up to 32 rows (16 of dimension 128), whose keys four warps share: lengths around a
+    warp's 32 keys and a tile's 128, maxima that grow from tile to tile, and keys of score -inf."""
+    lens = [1, 15, 16, 17, 31, 32, 33, 64, 65, 95, 97, 127, 128, 129, 255, 256, 257, 383, 385, 640, 1500]
+    b = Batch([(1 + (r % q), n) for r, n in enumerate(lens)] + [(0, 70), (q, 0), (q, 900)], hq, hk, a, seed=hq + a)
+    b.compare(b.run())
+    for r, n in enumerate(b.kv):                    # scores that grow with the key
+        for i in range(-(-n // BS)):
+            rows = min(BS, n - i * BS)
+            b.k[int(b.tables[r, i]), :, :rows] = torch.linspace(i, i + 1, BS, device="cuda")[:rows, None].to(torch.bfloat16)
+    b.q.copy_(torch.rand_like(b.q) * 0.2)
+    out = b.run()
+    b.compare(out)
+    b.q[0, 0] = math.nan                            # a row that is not finite stays alone
+    bad = b.run()
+    assert bad[0, 0].isnan().all()
+    assert torch.equal(bad.flatten(0, 1)[1:], out.flatten(0, 1)[1:])
+
+
+@pytest.mark.parametrize("a", [64, 128])
+def test_few_rows_of_infinite_scores(a):
+    b = Batch([(2, 200)], 2, 2, a, seed=20)
+    b.q.copy_(b.q.abs() + 0.5)
+    blk = [int(x) for x in b.tables[0, :13]]
+    gone = (0, 1, 5, 8, 9, 10, 11, 12)              # a warp's whole share of the first tile, and the second tile
+    for i in range(13):
+        rows = min(BS, 200 - i * BS)
+        if i in gone:
+            b.k[blk[i], 0, :rows] = -math.inf
+        b.k[blk[i], 1, :rows] = -math.inf
+    out = b.run()
+    assert out[:, 1].isnan().all()                  # softmax of nothing but -inf
+    keep = [i for i in range(200) if i // BS not in gone]
+    k, v = b.request(0)
+    s = torch.einsum("qd,nd->qn", b.q[:, 0].double(), k[0][keep]) * b.scale
+    p = torch.softmax(s, -1)
+    ref, size = p @ v[0][keep], p @ v[0][keep].abs()
+    e = a * 2.0 ** -23 * b.scale * (b.q[:, 0].double().abs() @ k[0][keep].abs().T).amax(-1, keepdim=True)      # as Batch.compare
+    e = e + (1 + s.abs().amax(-1, keepdim=True)) * 2.0 ** -20
+    bound = 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2 * torch.expm1(e) + 200 * 2.0 ** -23) * size
+    assert ((out[:, 0].double() - ref).abs() <= bound * (1 + 2.0 ** -8)).all()
+
+
+def test_few_rows_cut_between_ctas():
+    for hq, hk, a in ((32, 8, 64), (32, 8, 128), (4, 4, 64), (4, 4, 128)):
+        b = Batch([(1, 40000), (1, 3), (2, 5001), (1, 128 * 9)], hq, hk, a, seed=a)
+        out = b.run()
+        b.compare(out)
+        assert torch.equal(out, b.run())
