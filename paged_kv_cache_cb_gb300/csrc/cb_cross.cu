@@ -73,11 +73,11 @@ struct Tiles {
   uint8_t few[F && A == 64 ? 2 * 2 * 32 * 128 + 2 * 4 * 32 * 12 : 0];
   uint8_t kv[kRing][kHalves][128][128];
   static constexpr int kFewRows = A == 64 ? 32 : 16;
-  [[maybe_unused]] static constexpr int kQBytes = 2 * kBytes, kRowsBytes = kFewRows * 128;
+  static constexpr int kQBytes = 2 * kBytes, kRowsBytes = kFewRows * 128;
   static constexpr int weights_at(int group) { return A == 64 ? kQBytes + group * 2 * kRowsBytes : 16 * 128 + group * 32 * 128; }
-  [[maybe_unused]] static constexpr int kWeightsHalf = A == 64 ? kRowsBytes : kHalfBytes;
-  [[maybe_unused]] static constexpr int kTopAt = A == 64 ? kQBytes + 4 * kRowsBytes : kBytes + 16 * 128;
-  [[maybe_unused]] static constexpr int kSumAt = A == 64 ? kTopAt + 2 * 4 * kFewRows * 8 : kBytes + 24 * 128;
+  static constexpr int weights_half() { return A == 64 ? kRowsBytes : kHalfBytes; }
+  static constexpr int top_at() { return A == 64 ? kQBytes + 4 * kRowsBytes : kBytes + 16 * 128; }
+  static constexpr int sum_at() { return A == 64 ? top_at() + 2 * 4 * kFewRows * 8 : kBytes + 24 * 128; }
 };
 
 // A request's tokens and stored keys; q_len 0: nothing to do.
@@ -449,7 +449,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
 #pragma unroll
       for (int ks = 0; ks < kTileN / 16; ++ks)
         if constexpr (F)
-          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * TT::kWeightsHalf + (ks & 3) * 32) >> 4),
+          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * TT::weights_half() + (ks & 3) * 32) >> 4),
                      v + ((ks * 16 * 128) >> 4), kIdescPV, (!first || ks > 0) ? 1u : 0u);
         else
           tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
@@ -722,10 +722,10 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
   const float sl2 = P.scale_log2;
   constexpr int R = TT::kFewRows;
   uint8_t* const base = reinterpret_cast<uint8_t*>(&T);
-  uint8_t* const weights = base + TT::weights_at(side) + (warp >> 1) * TT::kWeightsHalf + row * 128;
+  uint8_t* const weights = base + TT::weights_at(side) + (warp >> 1) * TT::weights_half() + row * 128;
   // [group][warp][row]
-  float2* const tops = reinterpret_cast<float2*>(base + TT::kTopAt) + side * 4 * R + row;
-  float* const sums = reinterpret_cast<float*>(base + TT::kSumAt) + row;
+  float2* const tops = reinterpret_cast<float2*>(base + TT::top_at()) + side * 4 * R + row;
+  float* const sums = reinterpret_cast<float*>(base + TT::sum_at()) + row;
   const bool has = row < R;
   uint32_t kt = 0, sc = 0, oc = 0, shared = 0;          // as in softmax
   int second = side ^ 1;
@@ -1082,7 +1082,7 @@ static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem
 static_assert(sizeof(Tiles<128, true>) == sizeof(Tiles<128, false>), "no room of its own");
 using Few64 = Tiles<64, true>;
 static_assert(offsetof(Few64, few) == Few64::kQBytes && offsetof(Few64, kv) % 1024 == 0 &&
-              Few64::kSumAt + 2 * 4 * 32 * 4 <= offsetof(Few64, kv), "layout of few rows");
+              Few64::sum_at() + 2 * 4 * 32 * 4 <= offsetof(Few64, kv), "layout of few rows");
 static_assert(sizeof(Tiles<128, false>) % 16 == 0 && sizeof(Tiles<64, false>) % 16 == 0 && sizeof(Tiles<64, true>) % 16 == 0,
               "control block 16-byte aligned");
 
