@@ -177,6 +177,8 @@ constexpr int kUnroll = 4;             // reads of a lane in flight in a row's p
 //   D  the copies' entries and counts, pairs and lengths.
 // A barrier after A, after C's counting of free blocks and after C; the last two
 // only if a row is in need.
+// 4 beams of up to 400 tokens: 8.3 us with their copies; 128 beams of 1000 to 1700 tokens: 15
+// (cold) before the copies.  Five dependent reads bound it.
 struct ForkArgs {
   Pool P;
   const int32_t* parents;
@@ -354,7 +356,9 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const ForkArgs A) {
 // ---------------------------------------------------------------- grow
 // Row i gets room for its cu[i + 1] - cu[i] new tokens.  Every CTA knows what
 // each row needs (a prefix sum over the rows); the CTA that finds the k-th
-// lowest free block in its slice hands it to the row that k falls to.
+// lowest free block in its slice hands it to the row that k falls to.  48 rows by up to 8 tokens:
+// 8.4 us with the caller's reset of the pool; 512 rows by up to 2000 tokens: 24 (cold: 19.6 and
+// 11.1 for the slots).  A pass over the pool's counts, twice, and the barriers bound it.
 struct GrowArgs {
   Pool P;
   const int32_t* cu;                   // [n_rows + 1]
@@ -500,7 +504,9 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const GrowArgs A) {
 
 // ---------------------------------------------------------------- compact
 // With L live blocks, the k-th lowest live block of id >= L moves to the k-th
-// lowest free id < L (there are as many of the one as of the other).
+// lowest free id < L (there are as many of the one as of the other).  8 rows and 333 blocks:
+// 10.5 us with the moves' copies; 256 rows and 28,610 blocks: 17 before the copies.  Seven
+// dependent reads and the cluster's barriers bound it.
 struct CompactArgs {
   Pool P;
   int32_t* map;                        // [num_blocks]
@@ -580,7 +586,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs A) 
 // Block dst becomes block src in every layer of every buffer.  Memory-bound: a
 // warp copies 4 KB at a time, eight 16-byte loads in flight per lane.  Pairs are
 // taken kTile at a time; each CTA packs the tile's valid ones in shared memory,
-// and the 4 KB pieces of all of them are dealt over all warps of the grid.
+// and the 4 KB pieces of all of them are dealt over all warps of the grid.  1024 blocks of 32
+// layers, 4.3 GB read and written: 660 to 676 us, 0.94 to 0.96 of a plain copy's rate.
 struct CopyArgs {
   const int32_t* pairs;
   int n_pairs, n_layers, num_blocks, n_buffers;

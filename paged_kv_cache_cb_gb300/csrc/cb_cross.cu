@@ -18,6 +18,9 @@
 // Tensor memory (512 columns): S_A|P_A [0,128), S_B|P_B [128,256), O_A, O_B.  P
 // (bf16) is written over its own S and is the A operand of O += P V.
 //
+// A batch whose items have few rows (at most 32, 16 of dimension 128: a decoding step) takes
+// another form of the softmax, in which four warps share each row's keys: softmax_few.
+//
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
 // and V; warps 9, 10: MMA issue for A, B; one more completes the third warpgroup, which
 // gives most of its registers to the other two: a row's 128 scores stay in registers.
@@ -26,12 +29,12 @@
 // and summed before that rounding.  Every wait is bounded.
 //
 // Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
-// head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 145 us = 0.93 of the copy
-// rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 384 us = 0.99: HBM bounds both.
-// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 262 us = 1.34
+// head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 144 us = 0.94 of the copy
+// rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 382 us = 0.99: HBM bounds both.
+// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 265 us = 1.32
 // PFLOP/s: the chain scores - weights - product of each group bounds them.  Head dimension
-// 64 has half the bytes per score: 100 single tokens over 100-3000 keys, 32/8 heads, 78.5 us
-// = 0.6 of the copy rate, bound by the softmax's chain.
+// 64, 100 single tokens over 100-3000 keys: 32/32 heads 190 us = 0.92 of the copy rate,
+// 32/8 heads 59.5 us = 0.74, of which the launch's start and the joins at its end are 8.
 #include <algorithm>
 #include <cstddef>
 
@@ -49,9 +52,9 @@ constexpr float kMostSum = 1024.f;     // of a tile's weights: none of them is o
 
 // Cost of a key tile of a narrow and of a wide item, and of an item's start and end (its
 // query tile's load, its output), which take as long as one and a half tiles of a wide
-// item.  Four prompts of 5 to 1999 tokens: 360 us with a start counted as half a tile of
-// a wide item, 343 as one, 333 as one and a half, 331 as two; 64 x 4 beams: 386, 384, 383,
-// 388.  A tile of a wide item at 3 or 5 instead of 4: 343 (start 4), 349 (start 6).
+// item.  Four prompts of 5 to 1999 tokens: 310 us with a start counted as half a tile of
+// a wide item, 298 as one, 265 as one and a half, 272 as two; 64 x 4 beams: 380, 380, 382,
+// 385; 100 tokens over 100 to 3000 keys of dimension 64, 32 heads: 198, 187, 190, 195.
 constexpr int kNarrow = 2, kWide = 4, kLead = 6;
 constexpr int kLeast = 8;              // of a CTA's share
 
@@ -570,7 +573,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   // Of a narrow piece, the group that has key tiles 1, 3, ..: the groups in turn, so that pieces of
   // one tile run beside each other and those of an odd number fill both groups (32 heads of
   // dimension 64, 100 tokens over 128 keys: 43.5 us, 68.5 with B always; 1408 keys: 203 and 218).
-  // Where some items are wide, that cost these more than it gave (prompts 266 us, 263 without).
+  // Where some items are wide, that cost these more than it gave (prompts 267 us, 263 without).
   int second = W ? side : side ^ 1;
   Pieces<W> pieces(P, c);
   Piece<W> p;
@@ -705,13 +708,14 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   }
 }
 
-// Items of at most 32 rows (dimension 128: 16): thread = row leaves three of a group's warps idle, while one
-// takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
+// Items of at most 32 rows (dimension 128: 16): thread = row leaves three of a group's warps
+// idle, while one takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
 // one copy for each warp's lanes, and so have the scores: warp w makes the weights of keys
 // 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
 // lanes.  m is the same in the four warps, which tell each other their maxima when it may move;
 // sums stay apart until the item's end.  Every exit is taken by the four warps together:
-// they meet at named barriers.
+// they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 190 us
+// (thread = row: 257), over 128 keys 35.5 (43.4); dimension 128 over 257 keys 112 (162).
 template <int A, class C>
 __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A, true>;
