@@ -31,7 +31,7 @@
 // Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
 // head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 144 us = 0.94 of the copy
 // rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 382 us = 0.99: HBM bounds both.
-// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 265 us = 1.32
+// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 262 us = 1.34
 // PFLOP/s: the chain scores - weights - product of each group bounds them.  Head dimension
 // 64, 100 single tokens over 100-3000 keys: 32/32 heads 190 us = 0.92 of the copy rate,
 // 32/8 heads 59.5 us = 0.74, of which the launch's start and the joins at its end are 8.
@@ -53,7 +53,7 @@ constexpr float kMostSum = 1024.f;     // of a tile's weights: none of them is o
 // Cost of a key tile of a narrow and of a wide item, and of an item's start and end (its
 // query tile's load, its output), which take as long as one and a half tiles of a wide
 // item.  Four prompts of 5 to 1999 tokens: 310 us with a start counted as half a tile of
-// a wide item, 298 as one, 265 as one and a half, 272 as two; 64 x 4 beams: 380, 380, 382,
+// a wide item, 298 as one, 262 as one and a half, 270 as two; 64 x 4 beams: 380, 380, 382,
 // 385; 100 tokens over 100 to 3000 keys of dimension 64, 32 heads: 198, 187, 190, 195.
 constexpr int kNarrow = 2, kWide = 4, kLead = 6;
 constexpr int kLeast = 8;              // of a CTA's share
@@ -515,19 +515,12 @@ __device__ __forceinline__ void rescale(uint32_t o, float alpha) {
 }
 
 // A row's result: its output if the piece is its whole item, else its part of the join.  O and
-// the other group's O (two) are scaled by alpha and beta; busy: some row of the warp is valid.
+// the other group's O (two) are scaled by alpha and beta.  (Where they lie is worked out by the
+// caller: prompts of up to 2000 tokens took 265 us with that in here, 262 without.)
 template <int A, bool W>
-__device__ __forceinline__ void write_rows(const CrossParams& P, const Part& p, int row, int irow, bool busy, bool valid,
-                                           bool two, uint32_t o_at, uint32_t other_o, float alpha, float beta, float m, float l) {
-  if (!busy) return;
-  const bool whole = p.whole();
-  const int group = 1 << P.group_log2;
-  const float inv = whole ? 1.f / l : 1.f;
-  alpha *= inv;
-  beta *= inv;
-  float* part = P.part + (size_t)(2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0)) * P.part_rows * (A + 2);
-  const int tok = irow >> P.group_log2;
-  uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
+__device__ __forceinline__ void write_rows(int part_rows, int irow, bool whole, bool valid, bool two, uint32_t o_at,
+                                           uint32_t other_o, float alpha, float beta, float m, float l, uint16_t* dst,
+                                           float* part) {
 #pragma unroll 1
   for (int ch = 0; ch < A / 32; ++ch) {
     float o[32];
@@ -551,11 +544,11 @@ __device__ __forceinline__ void write_rows(const CrossParams& P, const Part& p, 
     } else if (valid) {
 #pragma unroll
       for (int k = 0; k < 32; k += 4)
-        reinterpret_cast<float4*>(part)[W ? (size_t)(ch * 8 + k / 4) * P.part_rows + irow : (size_t)irow * (A / 4) + ch * 8 + k / 4] =
+        reinterpret_cast<float4*>(part)[W ? (size_t)(ch * 8 + k / 4) * part_rows + irow : (size_t)irow * (A / 4) + ch * 8 + k / 4] =
             make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
     }
   }
-  if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)P.part_rows * A + irow * 2) = make_float2(m, l);
+  if (valid && !whole) *reinterpret_cast<float2*>(part + (size_t)part_rows * A + irow * 2) = make_float2(m, l);
 }
 
 template <int A, bool W, class C>
@@ -565,7 +558,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   const unsigned FULL = 0xffffffffu;
   const int row = threadIdx.x & 127, warp = (threadIdx.x >> 5) & 3;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  const uint32_t s_at = tmem + lanes + side * 128, o_at = tmem + lanes + 256 + side * A, other_o = tmem + lanes + 256 + (side ^ 1) * A;
+  const uint32_t s_at = tmem + lanes + side * 128;
+  const uint32_t o_at = tmem + lanes + 256 + side * A, other_o = tmem + lanes + 256 + (side ^ 1) * A;
   const int tok_tile = kTileM >> P.group_log2;
   const float sl2 = P.scale_log2;
   // key tiles before this piece; this group's; the other group's; pieces that both share
@@ -700,8 +694,15 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
     } else if (!mine) {
       continue;                        // a narrow piece of one tile has nothing for the second group
     }
-    if (row == 0 && !p.whole() && !(p.wide() && side)) c.cut[p.ta == 0] = p;
-    write_rows<A, W>(P, p, row, (p.wide() && side ? 128 : 0) + row, busy, valid, two, o_at, other_o, alpha, beta, m, l);
+    const bool whole = p.whole();
+    if (!whole && row == 0 && !(p.wide() && side)) c.cut[p.ta == 0] = p;
+    const float inv = whole ? 1.f / l : 1.f;
+    alpha *= inv;
+    beta *= inv;
+    const int group = 1 << P.group_log2, irow = (p.wide() && side ? 128 : 0) + row;
+    float* part = P.part + (size_t)(2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0)) * P.part_rows * (A + 2);
+    uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
+    if (busy) write_rows<A, W>(P.part_rows, irow, whole, valid, two, o_at, other_o, alpha, beta, m, l, dst, part);
     tc_fence_before();
     mbar_arrive(&c.o_free[side]);
     if (two) mbar_arrive(&c.o_free[side ^ 1]);
@@ -866,8 +867,15 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
       l = l * alpha + bl * beta;
       m = mn;
     }
-    if (row == 0 && !p.whole()) c.cut[p.ta == 0] = p;
-    write_rows<A, false>(P, p, row, row, true, valid, two, o_at, other_o, alpha, beta, m, l);
+    const bool whole = p.whole();
+    if (!whole && row == 0) c.cut[p.ta == 0] = p;
+    const float inv = whole ? 1.f / l : 1.f;
+    alpha *= inv;
+    beta *= inv;
+    const int group = 1 << P.group_log2, irow = row;
+    float* part = P.part + (size_t)(2 * (int)blockIdx.x + (p.ta == 0 ? 1 : 0)) * P.part_rows * (A + 2);
+    uint16_t* dst = P.out + ((size_t)(p.q.q0 + p.tok_lo + tok) * P.n_q_heads + (size_t)p.g * group + (row & (group - 1))) * A;
+    write_rows<A, false>(P.part_rows, irow, whole, valid, two, o_at, other_o, alpha, beta, m, l, dst, part);
     tc_fence_before();
     mbar_arrive(&c.o_free[side]);
     if (two) mbar_arrive(&c.o_free[side ^ 1]);
