@@ -18,8 +18,7 @@
 // Tensor memory (512 columns): S_A|P_A [0,128), S_B|P_B [128,256), O_A, O_B.  P
 // (bf16) is written over its own S and is the A operand of O += P V.
 //
-// A batch whose items have few rows (at most 32, 16 of dimension 128: a decoding step) takes
-// another form of the softmax, in which four warps share each row's keys: softmax_few.
+// A batch whose items have few rows (at most 32: a decoding step, a few beams) takes another form of the softmax, in which four warps share each row's keys: softmax_few.
 //
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
 // and V; warps 9, 10: MMA issue for A, B; one more completes the third warpgroup, which
@@ -61,26 +60,24 @@ constexpr int kLeast = 8;              // of a CTA's share
 // K and V tiles share one ring of buffers, in the order of their use: a wide item's
 // K(0) V(0) K(1) V(1) .., a narrow one's K(0) K(1) V(0) K(2) V(1) .. V(n - 1), since
 // its two groups begin with a key tile each.
-// F: a launch whose items have at most 32 rows; see softmax_few.
+// F: a launch whose items have at most kFewRows rows; see softmax_few.
+constexpr int kFewRows = 32;
 template <int A, bool F>
 struct Tiles {
   static constexpr int kHalves = A / 64;
   static constexpr int kHalfBytes = 128 * 128;
   static constexpr int kBytes = kHalves * kHalfBytes;     // of 128 rows
   static constexpr int kRing = A == 128 ? 5 : 10;
-  uint8_t q[2][kHalves][128][128];
-  // The weights of two groups, two halves of the keys, kFewRows rows (the products read 128, that
-  // is, into what follows); per group, warp and row its maximum, and whether m must move up; its
-  // weights' sum.  Dimension 128 leaves no room for them: they take the half of the query tiles
-  // that items of 16 rows do not use.
-  uint8_t few[F && A == 64 ? 2 * 2 * 32 * 128 + 2 * 4 * 32 * 12 : 0];
+  // With few rows of dimension 128 there is room for one query tile beside the ring.  Four buffers
+  // and two query tiles: 48 tokens over 256-8192 keys 146.8 us, 143.7 so, and 64 x 4 beams 391
+  // and 382.
+  static constexpr int kQ = A == 128 && F ? 1 : 2;
+  static constexpr int kFewHalf = kFewRows * 128, kFewGroup = 2 * kFewHalf;
+  uint8_t q[kQ][kHalves][128][128];
+  uint8_t weights[F ? 2 : 0][2][kFewRows][128];           // the products read 128 rows, that is, into kv
+  float2 top[F ? 2 : 0][4][kFewRows];  // per group, warp and row: the maximum, and whether m must move up
+  float sum[F ? 2 : 0][4][kFewRows];   // of a row's weights
   uint8_t kv[kRing][kHalves][128][128];
-  static constexpr int kFewRows = A == 64 ? 32 : 16;
-  static constexpr int kQBytes = 2 * kBytes, kRowsBytes = kFewRows * 128;
-  static constexpr int weights_at(int group) { return A == 64 ? kQBytes + group * 2 * kRowsBytes : 16 * 128 + group * 32 * 128; }
-  static constexpr int weights_half() { return A == 64 ? kRowsBytes : kHalfBytes; }
-  static constexpr int top_at() { return A == 64 ? kQBytes + 4 * kRowsBytes : kBytes + 16 * 128; }
-  static constexpr int sum_at() { return A == 64 ? top_at() + 2 * 4 * kFewRows * 8 : kBytes + 24 * 128; }
 };
 
 // A request's tokens and stored keys; q_len 0: nothing to do.
@@ -325,19 +322,22 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
       return none;
     };
     int e = entry(p.ta), y = none, before = none;
-    for (int side = 0; ok && side < (p.wide() ? 2 : 1); ++side, ++qs) {
-      const uint32_t st = qs & 1;
-      ok = warp_wait(P, &c.q_empty[st], ((qs >> 1) & 1) ^ 1);
-      if (ok && elect_lane()) {
-        mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes * (F ? 4 : 1));
+    auto load_q = [&]() {
+      for (int side = 0; ok && side < (p.wide() ? 2 : 1); ++side, ++qs) {
+        const uint32_t st = qs % TT::kQ;
+        ok = warp_wait(P, &c.q_empty[st], ((qs / TT::kQ) & 1) ^ 1);
+        if (ok && elect_lane()) {
+          mbar_arrive_expect_tx(&c.q_full[st], P.q_bytes * (F ? 4 : 1));
 #pragma unroll
-        for (int h = 0; h < H; ++h)
+          for (int h = 0; h < H; ++h)
 #pragma unroll
-          for (int w = 0; w < (F ? 4 : 1); ++w)
-            tma_load_3d(&T.q[st][h][w * 32][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
+            for (int w = 0; w < (F ? 4 : 1); ++w)
+              tma_load_3d(&T.q[st][h][w * 32][0], qmap, h * 64, p.g * group, p.q.q0 + p.tok_lo + side * tok_tile, &c.q_full[st]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-    }
+    };
+    if (TT::kQ == 2) load_q();
     for (int j = p.ta; ok && j < p.tb; ++j) {
       const int in4 = (j - p.ta) & 3;
       if (in4 == 0) {                  // the entries asked for four tiles ago; the next ones
@@ -346,6 +346,8 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
         e = j + 4 < p.tb ? entry(j + 4) : -1;
       }
       ok = load(kmap, y, in4);
+      // one query tile waits for the last item's scores: the first keys go ahead of it
+      if (TT::kQ == 1 && j == p.ta) load_q();
       if (p.wide())
         ok = ok && load(vmap, y, in4);
       else if (j > p.ta)
@@ -358,7 +360,7 @@ __device__ void loader(const CrossParams& P, const CUtensorMap* kmap, const CUte
     for (int par = 0; par < 2; ++par) {
       for (int s = 0; s < NS; ++s) mbar_wait(&c.full[s], par, 20000000ull);
       mbar_wait(&c.q_full[0], par, 20000000ull);
-      mbar_wait(&c.q_full[1], par, 20000000ull);
+      if (TT::kQ == 2) mbar_wait(&c.q_full[1], par, 20000000ull);
     }
   }
 }
@@ -385,7 +387,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
   const uint64_t q0 = smem_desc_sw128(base, 16, 1024);
   const uint64_t k0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), 16, 1024);
   const uint64_t v0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, kv), TT::kHalfBytes, 1024);
-  const uint64_t p0 = smem_desc_sw128(base + TT::weights_at(side), 16, 1024);
+  const uint64_t p0 = smem_desc_sw128(base + (uint32_t)offsetof(TT, weights) + side * TT::kFewGroup, 16, 1024);
   uint32_t qs = 0, np = 0, items = 0, turns = 0;   // P tiles consumed, items begun, turns taken
   uint32_t st = 0, ph = 0;                         // the ring's next buffer
   int second = side;                               // see softmax
@@ -452,7 +454,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
 #pragma unroll
       for (int ks = 0; ks < kTileN / 16; ++ks)
         if constexpr (F)
-          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * TT::weights_half() + (ks & 3) * 32) >> 4),
+          tc_mma_f16(tmem + 256 + side * A, p0 + (((ks >> 2) * TT::kFewHalf + (ks & 3) * 32) >> 4),
                      v + ((ks * 16 * 128) >> 4), kIdescPV, (!first || ks > 0) ? 1u : 0u);
         else
           tc_mma_f16_ts(tmem + 256 + side * A, tmem + side * 128 + ks * 8, v + ((ks * 16 * 128) >> 4), kIdescPV,
@@ -467,7 +469,7 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
   };
   while (ok && !__any_sync(FULL, c.abort) && pieces.next(P, p)) {
     const int n = p.tb - p.ta;
-    const uint32_t x = qs + (p.wide() && side), slot = __shfl_sync(FULL, x & 1, 0);
+    const uint32_t x = qs + (p.wide() && side), slot = __shfl_sync(FULL, x % TT::kQ, 0);
     const bool mine = p.wide() || n > second;        // this group has a tile
     if (p.wide()) {
       const uint32_t y = qs + !side;               // the other group's query tile
@@ -477,7 +479,8 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
       ok = ok && scores(slot, n == 1);
       for (int j = 0; ok && j < n; ++j) ok = values(j == 0, slot, j + 1 < n, j + 2 == n);
     } else {
-      ok = mine ? warp_wait(P, &c.q_full[slot], (x >> 1) & 1) : give_back(&c.q_full[slot], &c.q_empty[slot], (x >> 1) & 1);
+      const uint32_t qp = (x / TT::kQ) & 1;
+      ok = mine ? warp_wait(P, &c.q_full[slot], qp) : give_back(&c.q_full[slot], &c.q_empty[slot], qp);
       // K(0) K(1) V(0) K(2) V(1) .. V(n - 1): up to V(second)
       if (second) ok = ok && other();
       if (mine) ok = ok && scores(slot, second + 2 >= n);
@@ -709,14 +712,14 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   }
 }
 
-// Items of at most 32 rows (dimension 128: 16): thread = row leaves three of a group's warps
-// idle, while one takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
+// Items of at most 32 rows: thread = row leaves three of a group's warps idle, while one takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
 // one copy for each warp's lanes, and so have the scores: warp w makes the weights of keys
 // 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
 // lanes.  m is the same in the four warps, which tell each other their maxima when it may move;
 // sums stay apart until the item's end.  Every exit is taken by the four warps together:
 // they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 190 us
-// (thread = row: 257), over 128 keys 35.5 (43.4); dimension 128 over 257 keys 112 (162).
+// (thread = row: 257), over 128 keys 35.5 (43.4); dimension 128 over 257 keys 104 (162); 8
+// tokens each over 257 keys, 32/8 heads of 128, 39.8 (55.8).
 template <int A, class C>
 __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A, true>;
@@ -725,13 +728,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
   const uint32_t s_at = tmem + ((uint32_t)(warp * 32) << 16) + side * 128 + warp * 32;
   const uint32_t o_at = tmem + 256 + side * A, other_o = tmem + 256 + (side ^ 1) * A;     // warp 0
   const float sl2 = P.scale_log2;
-  constexpr int R = TT::kFewRows;
-  uint8_t* const base = reinterpret_cast<uint8_t*>(&T);
-  uint8_t* const weights = base + TT::weights_at(side) + (warp >> 1) * TT::weights_half() + row * 128;
-  // [group][warp][row]
-  float2* const tops = reinterpret_cast<float2*>(base + TT::top_at()) + side * 4 * R + row;
-  float* const sums = reinterpret_cast<float*>(base + TT::sum_at()) + row;
-  const bool has = row < R;
+  uint8_t* const weights = T.weights[side][warp >> 1][row];
   uint32_t kt = 0, sc = 0, oc = 0, shared = 0;          // as in softmax
   int second = side ^ 1;
   bool ok = true;
@@ -766,7 +763,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
           float a[2] = {kNoKey, kNoKey};
 #pragma unroll
           for (int k = 0; k < 32; k += 2) a[(k >> 1) & 1] = max3(a[(k >> 1) & 1], s[k], s[k + 1]);
-          if (has) tops[warp * R] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
+          T.top[side][warp][row] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
           if (named_bar_or(bar, 128, !ok)) {
             met = false;
             break;
@@ -774,7 +771,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
           float mn = m, need = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const float2 x = has ? tops[w * R] : make_float2(kNoKey, 0.f);
+            const float2 x = T.top[side][w][row];
             mn = fmaxf(mn, x.x);
             need += x.y;
           }
@@ -818,7 +815,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
       l = l * alpha + add;
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (has) *reinterpret_cast<uint4*>(weights + ((((warp & 1) * 4 + u) ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(weights + ((((warp & 1) * 4 + u) ^ (row & 7)) << 4)) =
             make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
       if (key0 + kTileN > p.q.kv && (p.q.kv & (kBlockSize - 1))) {       // as in softmax
         const uint32_t t = 2 * (kt + n) - 1, st = t % NS;
@@ -839,7 +836,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
     if (!mine) continue;
     ok = ok && warp_wait(P, &c.o_done[side], (sc - 1) & 1);
     tc_fence_after();
-    if (has) sums[(side * 4 + warp) * R] = l;
+    T.sum[side][warp][row] = l;
     if (two && second) {
       if (warp == 0) c.ml[row].x = m;
       if (ok) mbar_arrive(&c.ml_full);
@@ -851,8 +848,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
     }
     if (warp > 0) continue;            // their sums are read before any of them comes here again
     auto total = [&](int g) {
-      const float* x = sums + g * 4 * R;
-      return has ? (x[0] + x[R]) + (x[2 * R] + x[3 * R]) : 0.f;
+      return (T.sum[g][0][row] + T.sum[g][1][row]) + (T.sum[g][2][row] + T.sum[g][3][row]);
     };
     l = total(side);
     float alpha = 1.f, beta = 0.f;
@@ -1090,13 +1086,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int A, bool F>
 constexpr int kSmem = 1024 + (int)sizeof(Tiles<A, F>) + (int)sizeof(Ctl<Tiles<A, F>::kRing>);
-static_assert(kSmem<128, false> <= 232448 && kSmem<64, false> <= 232448 && kSmem<64, true> <= 232448, "shared memory");
-static_assert(sizeof(Tiles<128, true>) == sizeof(Tiles<128, false>), "no room of its own");
-using Few64 = Tiles<64, true>;
-static_assert(offsetof(Few64, few) == Few64::kQBytes && offsetof(Few64, kv) % 1024 == 0 &&
-              Few64::sum_at() + 2 * 4 * 32 * 4 <= offsetof(Few64, kv), "layout of few rows");
-static_assert(sizeof(Tiles<128, false>) % 16 == 0 && sizeof(Tiles<64, false>) % 16 == 0 && sizeof(Tiles<64, true>) % 16 == 0,
-              "control block 16-byte aligned");
+template <int A, bool F>
+constexpr bool fits() {
+  using TT = Tiles<A, F>;
+  return kSmem<A, F> <= 232448 && sizeof(TT) % 16 == 0 && offsetof(TT, weights) % 1024 == 0 && offsetof(TT, kv) % 1024 == 0;
+}
+static_assert(fits<128, false>() && fits<128, true>() && fits<64, false>() && fits<64, true>(), "shared memory");
 
 template <int A, bool W, bool F>
 cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int grid, cudaStream_t stream) {
@@ -1126,12 +1121,13 @@ int cross_part_rows(int max_q_len, int group) {
 cudaError_t launch_cross(const CrossParams& p, const CUtensorMap* maps, int head_dim, int grid, cudaStream_t stream) {
   const long long rows = (long long)p.max_q_len << p.group_log2;      // that an item can have
   const bool wide = rows > kRows / 2;
-  const auto launch = head_dim == 128 ? (wide ? launch_cross_t<128, true, false>
-                                         : rows <= Tiles<128, true>::kFewRows ? launch_cross_t<128, false, true>
-                                                                              : launch_cross_t<128, false, false>)
-                      : wide ? launch_cross_t<64, true, false>
-                      : rows <= Tiles<64, true>::kFewRows ? launch_cross_t<64, false, true>
-                                                          : launch_cross_t<64, false, false>;
+  const bool few = rows <= kFewRows;
+  const auto launch = head_dim == 128 ? (wide  ? launch_cross_t<128, true, false>
+                                         : few ? launch_cross_t<128, false, true>
+                                               : launch_cross_t<128, false, false>)
+                                      : (wide  ? launch_cross_t<64, true, false>
+                                         : few ? launch_cross_t<64, false, true>
+                                               : launch_cross_t<64, false, false>);
   return launch(p, maps, grid, stream);
 }
 

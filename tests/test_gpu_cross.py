@@ -241,9 +241,10 @@ def test_refusals():
 
 
 @pytest.mark.parametrize("hq,hk,a,q", [(4, 4, 64, 2), (32, 1, 64, 1), (8, 4, 64, 16), (4, 4, 128, 2), (16, 1, 128, 1), (4, 2, 128, 8),
-                                       (17 * 4, 17, 128, 4), (17, 17, 64, 32)])
+                                       (17 * 4, 17, 128, 4), (17, 17, 64, 32), (32, 1, 128, 1), (16, 2, 128, 4), (4, 4, 128, 32),
+                                       (8, 8, 128, 33)])
 def test_few_rows(hq, hk, a, q):
-    """Items of up to 32 rows (16 of dimension 128), whose keys four warps share: lengths around a
+    """Items of up to 32 rows (and of 33), whose keys four warps share: lengths around a
     warp's 32 keys and a tile's 128, maxima that grow from tile to tile, and keys of score -inf."""
     lens = [1, 15, 16, 17, 31, 32, 33, 64, 65, 95, 97, 127, 128, 129, 255, 256, 257, 383, 385, 640, 1500]
     b = Batch([(1 + (r % q), n) for r, n in enumerate(lens)] + [(0, 70), (q, 0), (q, 900)], hq, hk, a, seed=hq + a)
