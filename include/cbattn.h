@@ -235,7 +235,9 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  *  block_tables device, int32 [n_reqs][max_blocks_per_seq]; entries past
  *             ceil(kv_lens[r] / block_size) are never read
  *  max_q_len, max_kv_len  host int, >= every request's tokens (>= 1) and keys
- *             (0 .. 2^30)
+ *             (0 .. 2^30).  A tight max_q_len pays: up to 32 rows of a KV head
+ *             (max_q_len * n_q_heads / n_kv_heads) take a form of the kernel made
+ *             for them
  *  workspace  device, cb_paged_cross_attention_workspace_size(...) bytes, 16-byte
  *             aligned, no initialisation
  * Shapes: head_dim 64 or 128; n_q_heads / n_kv_heads 1, 2, 4, 8, 16 or 32, with any

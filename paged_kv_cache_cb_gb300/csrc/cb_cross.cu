@@ -18,14 +18,16 @@
 // Tensor memory (512 columns): S_A|P_A [0,128), S_B|P_B [128,256), O_A, O_B.  P
 // (bf16) is written over its own S and is the A operand of O += P V.
 //
-// A batch whose items have few rows (at most 32: a decoding step, a few beams) takes another form of the softmax, in which four warps share each row's keys: softmax_few.
+// A batch whose items have few rows (at most 32: a decoding step, a few beams) takes another
+// form of the softmax, in which four warps share each row's keys: softmax_few.
 //
 // Warps 0-3, 4-7: softmax of group A, B (thread = row); warp 8: TMA loads of Q, K
 // and V; warps 9, 10: MMA issue for A, B; one more completes the third warpgroup, which
 // gives most of its registers to the other two: a row's 128 scores stay in registers.
 // Scores, running max (base 2, scale folded in), sums and O are fp32; the weights are
 // rounded to bf16 for the tensor cores (within 2^-8 of each, as the output is of itself)
-// and summed before that rounding.  Every wait is bounded.
+// and summed before that rounding.  Every wait is bounded; the four warps that meet at a named
+// barrier agree there on whether one of them has given up.
 //
 // Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
 // head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 144 us = 0.94 of the copy
