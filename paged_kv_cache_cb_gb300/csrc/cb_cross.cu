@@ -1109,9 +1109,11 @@ cudaError_t launch_cross_t(const CrossParams& p, const CUtensorMap* maps, int gr
 }  // namespace
 
 long long cross_units_bound(int n_reqs, int n_tokens, int max_kv_len, int n_kv_heads, int group) {
+  constexpr long long kMost = 1LL << 30;                      // what the caller refuses
   const long long groups = (long long)n_tokens / (kRows / group) + n_reqs;
   const long long tiles = ((long long)max_kv_len + kTileN - 1) / kTileN;
-  return groups * n_kv_heads * (kLead + kWide * tiles);
+  const long long items = groups * n_kv_heads;                // at most 2^59
+  return items >= kMost ? kMost : items * (kLead + kWide * tiles);
 }
 int cross_grid(long long units, int sms) {
   return (int)std::max(1LL, std::min<long long>(std::min(sms, kMaxDecodeGrid), (units + kLeast - 1) / kLeast));

@@ -134,7 +134,8 @@ struct CrossParams {
   unsigned q_bytes;             // of a query tile's load
   float scale_log2;             // scale * log2(e)
 };
-// Upper bound of a step's units of work; CTAs of a launch with that many; rows of a partial result.
+// Upper bound of a step's units of work (2^30 from that many items on); CTAs of a launch with that many; rows of a
+// partial result.
 long long cross_units_bound(int n_reqs, int n_tokens, int max_kv_len, int n_kv_heads, int group);
 int cross_grid(long long units, int sms);
 int cross_part_rows(int max_q_len, int group);

@@ -168,3 +168,16 @@ def test_cross_attention_workspace_size():
         assert f(*bad) == 0
     with pytest.raises(ValueError):
         f(2, 3, 1 << 40, 40, 8, 4, 128, 16)
+
+
+@pytest.mark.parametrize("n,nt,hk,mkv,want", [
+    (1, 0x7FFFFFFF, 1 << 26, 524288, -1),           # the product of groups, KV heads and key tiles passes 63 bits
+    (1, 0x7FFFFFFF, 1 << 26, 1 << 30, -1),
+    (2048, 0x7FFFFFFF, 1 << 26, 0, -1),
+    (2, 1 << 20, 4, 1 << 30, -1),
+    (2, 256 * 2046, 1 << 12, 3841, -1),             # 2^23 items of 6 + 4 * 31 units
+    (2, 256 * 2046, 1 << 12, 3840, -3),             # of 126: fewer than 2^30 in all; the workspace is too small
+])
+def test_cross_attention_work_is_bounded(n, nt, hk, mkv, want):
+    L = _lib().lib()
+    assert L.cb_paged_cross_attention(D, D, D, D, 4, n, nt, 1, mkv, D, D, 1, D, 0.1, hk, hk, 64, 16, D, 16, None) == want
