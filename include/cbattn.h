@@ -415,7 +415,7 @@ int cb_grow_blocks(const int32_t* cu_q_lens, int32_t* block_tables, int max_bloc
  *  pairs      device, int32 [max_pairs][2], written: the moves (src, dst), then
  *             (-1, -1) -- run cb_copy_blocks_layers on them before the caches are
  *             used again.  Moves past max_pairs are left to the next call
- *             (num_blocks / 2 hold all)
+ *             (num_blocks / 2 hold all; at most 2^30)
  *  counts     device, int32 [2], written: live blocks, moves
  * Tables and refs follow the moves. */
 int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows, int32_t* lens, int32_t* refs,
@@ -424,7 +424,7 @@ int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows,
 
 /* cb_copy_blocks in every layer at once, for either kind of cache.
  *  pairs      device, int32 [n_pairs][2] (src, dst); src < 0 skips the pair.  The
- *             dsts are distinct and none is a src of another pair
+ *             dsts are distinct and none is a src of another pair.  n_pairs 0 .. 2^30
  *  caches     host, n_caches device pointers (1 .. CB_MAX_CACHE_BUFFERS), each to
  *             [n_layers][num_blocks] blocks, 16-byte aligned: K and V, and the
  *             exponents of an 8-bit cache

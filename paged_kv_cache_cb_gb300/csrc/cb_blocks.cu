@@ -719,6 +719,8 @@ constexpr int kManyTokens = 8192;      // slots that one cluster writes itself
 // one, 31.3 with eight, 24.0 with sixteen, which the others lose 1 to 2 by.
 constexpr int kSmallPool = 8192, kSmallRows = 64, kSmallGrowth = 16384;
 
+constexpr int kMostPairs = 1 << 30;    // their ints are counted in 32 bits
+
 // The pool arguments that the calls share; false: CB_EINVAL.
 bool pool_of(Pool* P, int32_t* tables, int width, int n_rows, int32_t* lens, int32_t* refs, int num_blocks, int block_size) {
   if (n_rows < 0 || n_rows > CB_MAX_REQS || width < 1 || num_blocks < 1 || block_size != kBlockSize) return false;
@@ -838,7 +840,7 @@ int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows,
     CompactArgs a{};
     int32_t any = 0;                   // without rows there is still a pool
     if (!pool_of(&a.P, n_rows ? block_tables : &any, max_blocks_per_seq, n_rows, n_rows ? lens : &any, refs, num_blocks,
-                 block_size) || max_pairs < 0)
+                 block_size) || max_pairs < 0 || max_pairs > kMostPairs)
       return CB_EINVAL;
     if (!refs || !aligned4(refs) || !block_map || !counts || !workspace || !aligned4(block_map) || !aligned4(counts) ||
         !aligned16(workspace) || (max_pairs && (!pairs || !aligned4(pairs))))
@@ -864,8 +866,8 @@ int cb_compact_blocks(int32_t* block_tables, int max_blocks_per_seq, int n_rows,
 int cb_copy_blocks_layers(const int32_t* pairs, int n_pairs, void* const* caches, const size_t* block_bytes, int n_caches,
                           int n_layers, int num_blocks, void* stream) {
   return guarded([&]() -> int {
-    if (n_pairs < 0 || n_caches < 1 || n_caches > CB_MAX_CACHE_BUFFERS || n_layers < 1 || num_blocks < 1 || !caches ||
-        !block_bytes)
+    if (n_pairs < 0 || n_pairs > kMostPairs || n_caches < 1 || n_caches > CB_MAX_CACHE_BUFFERS || n_layers < 1 ||
+        num_blocks < 1 || !caches || !block_bytes)
       return CB_EINVAL;
     CopyArgs a{};
     long long pieces = 0;

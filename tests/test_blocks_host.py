@@ -181,3 +181,12 @@ def test_cross_attention_workspace_size():
 def test_cross_attention_work_is_bounded(n, nt, hk, mkv, want):
     L = _lib().lib()
     assert L.cb_paged_cross_attention(D, D, D, D, 4, n, nt, 1, mkv, D, D, 1, D, 0.1, hk, hk, 64, 16, D, 16, None) == want
+
+
+def test_pairs_that_32_bits_cannot_index():
+    """The kernels count the ints of pairs in 32 bits: 2^30 pairs are the most."""
+    L = _lib().lib()
+    a, b = (ctypes.c_void_p * 1)(4096), (ctypes.c_size_t * 1)(64)
+    for n in ((1 << 30) + 1, 0x7FFFFFFF):
+        assert L.cb_copy_blocks_layers(D, n, a, b, 1, 1, 8, None) == -1
+        assert L.cb_compact_blocks(D, 4, 2, D, D, 8, 16, D, D, n, D, D, 1 << 20, None) == -1
