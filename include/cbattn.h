@@ -362,8 +362,8 @@ int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const
  *             it, and whoever else holds it (a kept prefix: the caller adds 1
  *             for it).  0: free
  * Free blocks are taken from the lowest id on, in row order: the result of a
- * call depends on nothing else.  n_rows <= CB_MAX_REQS, block_size 16, fewer than
- * 2^31 table entries; n_rows 0 does nothing (cb_compact_blocks still compacts).
+ * call depends on nothing else.  n_rows <= CB_MAX_REQS, num_blocks <= 2^30, block_size
+ * 16, fewer than 2^31 table entries; n_rows 0 does nothing (cb_compact_blocks still compacts).
  * workspace: device, cb_block_ops_workspace_size(...) bytes, 16-byte aligned, no
  * initialisation; calls that may overlap need their own.  The arguments do not
  * overlap in memory.

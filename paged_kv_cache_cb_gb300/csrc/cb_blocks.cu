@@ -720,10 +720,13 @@ constexpr int kManyTokens = 8192;      // slots that one cluster writes itself
 constexpr int kSmallPool = 8192, kSmallRows = 64, kSmallGrowth = 16384;
 
 constexpr int kMostPairs = 1 << 30;    // their ints are counted in 32 bits
+constexpr int kMostBlocks = 1 << 30;   // a CTA's share is rounded up in 32 bits
 
 // The pool arguments that the calls share; false: CB_EINVAL.
 bool pool_of(Pool* P, int32_t* tables, int width, int n_rows, int32_t* lens, int32_t* refs, int num_blocks, int block_size) {
-  if (n_rows < 0 || n_rows > CB_MAX_REQS || width < 1 || num_blocks < 1 || block_size != kBlockSize) return false;
+  if (n_rows < 0 || n_rows > CB_MAX_REQS || width < 1 || num_blocks < 1 || num_blocks > kMostBlocks ||
+      block_size != kBlockSize)
+    return false;
   if ((long long)n_rows * width >= 1LL << 31 || (long long)width * kBlockSize >= 1LL << 31) return false;
   if (n_rows == 0) return true;
   if (!tables || !lens || !refs || !aligned4(tables) || !aligned4(lens) || !aligned4(refs)) return false;

@@ -190,3 +190,14 @@ def test_pairs_that_32_bits_cannot_index():
     for n in ((1 << 30) + 1, 0x7FFFFFFF):
         assert L.cb_copy_blocks_layers(D, n, a, b, 1, 1, 8, None) == -1
         assert L.cb_compact_blocks(D, 4, 2, D, D, 8, 16, D, D, n, D, D, 1 << 20, None) == -1
+
+
+def test_pools_that_32_bits_cannot_cut():
+    """A CTA's share of the pool is counted in 32 bits: 2^30 blocks are the most."""
+    L = _lib()
+    for nb in ((1 << 30) + 1, 0x7FFFFFFF):
+        assert L.lib().cb_fork_blocks(D, None, D, 4, 2, D, D, nb, 16, D, D, 1 << 40, None) == -1
+        assert L.lib().cb_grow_blocks(D, D, 4, 2, D, D, nb, 16, D, D, 3, D, 1 << 40, None) == -1
+        assert L.lib().cb_compact_blocks(D, 4, 2, D, D, nb, 16, D, D, 4, D, D, 1 << 40, None) == -1
+        assert L.cb_block_ops_workspace_size(2, 4, nb) == 0
+    assert L.cb_block_ops_workspace_size(2, 4, 1 << 30) >= 12 << 29
