@@ -828,7 +828,7 @@ int cb_grow_blocks(const int32_t* cu_q_lens, int32_t* block_tables, int max_bloc
     if (a.many) {
       int sms = 0;
       if (!device_sms(&sms)) return CB_ECUDA;
-      const int ctas = std::min(2 * sms, (n_tokens + kSlotThreads * kRun - 1) / (kSlotThreads * kRun));
+      const int ctas = std::min(2 * sms, (n_tokens - 1) / (kSlotThreads * kRun) + 1);
       if (launch_behind(slots_kernel, a, ctas, kSlotThreads, st) != cudaSuccess) return CB_ECUDA;
     }
     set_last_launches(a.many ? 2 : 1);
