@@ -334,8 +334,9 @@ def _current_device(c, t):
 
 def _fit_int(*sizes):
     """Refuses what a C int cannot hold (ctypes would pass the low 32 bits)."""
-    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
-        raise ValueError(f"sizes must fit a C int, got {sizes}")
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"sizes must fit a C int, got {sizes}")
 
 
 def _raw_stream(c, dev, stream):
@@ -498,7 +499,7 @@ def cb_paged_cross_attention(q, cu_q_lens, kv_lens, block_tables, k_cache, v_cac
     if v_cache.shape != (nb, hk, bs, a) or a2 != a:
         raise ValueError("cache shape mismatch")
     max_q_len, max_kv_len = int(max_q_len), int(max_kv_len)
-    _fit_int(max_q_len, max_kv_len, n_tok)
+    _fit_int(n_reqs, n_tok, max_q_len, max_kv_len, width, nb, hq, hk, a, bs)
     rc = lib().cb_paged_cross_attention(pq, pcu, pkv, pbt, width, n_reqs, n_tok, max_q_len, max_kv_len, ck, cv, nb, po,
                                         float(scale), hq, hk, a, bs, pw, size, _raw_stream(c, dev, stream))
     if rc:
@@ -525,6 +526,7 @@ def _pool(c, dev, block_tables, lens, refs, workspace):
         raise ValueError("shape mismatch") from None
     if lens.shape != (n,):
         raise ValueError("shape mismatch")
+    _fit_int(n, width, nb)
     return pt, pl, pr, pw, size, n, width, nb
 
 
@@ -560,6 +562,7 @@ def cb_grow_blocks(cu_q_lens, block_tables, lens, refs, ctx_lens, slot_mapping, 
     slots = slot_mapping.shape
     if cu_q_lens.shape != (n + 1,) or ctx_lens.shape != (n,) or len(slots) != 1:
         raise ValueError("shape mismatch")
+    _fit_int(slots[0])
     rc = lib().cb_grow_blocks(pc, pt, width, n, pl, pr, nb, _BLOCK, px, ps, slots[0], pw, size,
                               _raw_stream(c, dev, stream))
     if rc:
@@ -579,6 +582,7 @@ def cb_compact_blocks(block_tables, lens, refs, block_map, pairs, counts, worksp
     shape = pairs.shape
     if block_map.shape != (nb,) or len(shape) != 2 or shape[1] != 2 or counts.shape != (2,):
         raise ValueError("shape mismatch")
+    _fit_int(shape[0])
     rc = lib().cb_compact_blocks(pt, width, n, pl, pr, nb, _BLOCK, pm, px, shape[0], pc, pw, size,
                                  _raw_stream(c, dev, stream))
     if rc:
@@ -608,6 +612,7 @@ def cb_copy_blocks_layers(pairs, caches, stream=None):
         if len(size) < 3 or size[:2] != first or t.numel() == 0:
             raise ValueError("caches must be [n_layers, num_blocks, ...] of the same two sizes")
         sizes.append(t.nbytes // (size[0] * size[1]))
+    _fit_int(shape[0], *first)
     pointers, counts = _ARRAYS[n]
     rc = lib().cb_copy_blocks_layers(pp, shape[0], pointers(*ptrs), counts(*sizes), n, first[0], first[1],
                                      _raw_stream(c, dev, stream))

@@ -1,6 +1,7 @@
 """The block pool without a GPU: the oracle pinned by hand, and what the entry
 points refuse before anything is enqueued."""
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -8,6 +9,7 @@ import pytest
 import torch
 
 from oracle import blocks as ob
+from test_fp8_host import _Fake
 
 
 def _lib():
@@ -201,3 +203,69 @@ def test_pools_that_32_bits_cannot_cut():
         assert L.lib().cb_compact_blocks(D, 4, 2, D, D, nb, 16, D, D, 4, D, D, 1 << 40, None) == -1
         assert L.cb_block_ops_workspace_size(2, 4, nb) == 0
     assert L.cb_block_ops_workspace_size(2, 4, 1 << 30) >= 12 << 29
+
+
+# ------------------------------------------------------------------ sizes beyond 32 bits in the binding
+class _Tensor(_Fake):
+    def numel(self):
+        return math.prod(self.shape)
+
+    @property
+    def nbytes(self):
+        return self.numel() * self.dtype.itemsize
+
+
+def _made(**kw):
+    i, u8, bf = torch.int32, torch.uint8, torch.bfloat16
+    made = dict(pa=(i, 3), ke=(i, 3), bt=(i, 3, 4), ln=(i, 3), rf=(i, 8), pr=(i, 3, 2), cu=(i, 4), ctx=(i, 3),
+                sl=(torch.int64, 5), mp=(i, 8), ct=(i, 2), ws=(u8, 1 << 20), c1=(u8, 2, 8, 64), c2=(u8, 2, 8, 16),
+                q=(bf, 5, 4, 64), kv=(i, 3), k=(bf, 8, 2, 16, 64), v=(bf, 8, 2, 16, 64), out=(bf, 5, 4, 64))
+    made.update(kw)
+    return {name: _Tensor(*x) for name, x in made.items()}
+
+
+def _step(L, f):
+    pool = (f["bt"], f["ln"], f["rf"])
+    return {"fork": lambda: L.cb_fork_blocks(f["pa"], f["ke"], *pool, f["pr"], f["ws"], stream=1),
+            "grow": lambda: L.cb_grow_blocks(f["cu"], *pool, f["ctx"], f["sl"], f["ws"], stream=1),
+            "compact": lambda: L.cb_compact_blocks(*pool, f["mp"], f["pr"], f["ct"], f["ws"], stream=1),
+            "copy": lambda: L.cb_copy_blocks_layers(f["pr"], [f["c1"], f["c2"]], stream=1),
+            "cross": lambda: L.cb_paged_cross_attention(f["q"], f["cu"], f["kv"], f["bt"], f["k"], f["v"], f["out"], 0.1,
+                                                        f["ws"], 3, 60, stream=1)}
+
+
+BIG = 1 << 32
+INT, BYTE, BF = torch.int32, torch.uint8, torch.bfloat16
+
+
+@pytest.mark.parametrize("calls,kw", [
+    ("fork grow compact cross", dict(bt=(INT, 3, 4 + BIG))),
+    ("fork grow compact", dict(rf=(INT, 8 + BIG), mp=(INT, 8 + BIG))),
+    ("fork", dict(pa=(INT, 3 + BIG), ke=(INT, 3 + BIG), bt=(INT, 3 + BIG, 4), ln=(INT, 3 + BIG), pr=(INT, 3 + BIG, 2))),
+    ("grow", dict(sl=(torch.int64, 5 + BIG))),
+    ("grow", dict(sl=(torch.int64, 1 << 31))),
+    ("compact copy", dict(pr=(INT, 3 + BIG, 2))),
+    ("copy", dict(c1=(BYTE, 2 + BIG, 8, 64), c2=(BYTE, 2 + BIG, 8, 16))),
+    ("copy", dict(c1=(BYTE, 2, 8 + BIG, 64), c2=(BYTE, 2, 8 + BIG, 16))),
+    ("cross", dict(kv=(INT, 3 + BIG), cu=(INT, 4 + BIG), bt=(INT, 3 + BIG, 4))),
+    ("cross", dict(q=(BF, 5 + BIG, 4, 64), out=(BF, 5 + BIG, 4, 64))),
+    ("cross", dict(q=(BF, 5, 4 + BIG, 64), out=(BF, 5, 4 + BIG, 64))),
+    ("cross", dict(k=(BF, 8 + BIG, 2, 16, 64), v=(BF, 8 + BIG, 2, 16, 64))),
+    ("cross", dict(k=(BF, 8, 2 + BIG, 16, 64), v=(BF, 8, 2 + BIG, 16, 64))),
+    ("cross", dict(k=(BF, 8, 2, 16 + BIG, 64), v=(BF, 8, 2, 16 + BIG, 64))),
+])
+def test_binding_refuses_sizes_beyond_32_bits(calls, kw, monkeypatch):
+    """A pool of 2^32 + 8 blocks is not one of 8."""
+    L = _lib()
+    monkeypatch.setattr(L._tc(), "device", lambda: 0)
+    monkeypatch.setattr(torch, "Tensor", (torch.Tensor, _Fake))
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(L, "lib", Lib)
+    for name in calls.split():
+        _step(L, _made())[name]()
+        with pytest.raises(ValueError):
+            _step(L, _made(**kw))[name]()
