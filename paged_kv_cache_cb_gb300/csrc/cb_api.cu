@@ -542,7 +542,7 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
 
 size_t cb_paged_cross_attention_workspace_size(int n_reqs, int n_tokens, int max_q_len, int max_kv_len, int n_q_heads,
                                                int n_kv_heads, int head_dim, int block_size) {
-  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 0 ||
+  if (n_reqs < 0 || n_reqs > CB_MAX_REQS || n_tokens < 0 || max_q_len < 1 || max_kv_len < 0 || max_kv_len > 1 << 30 ||
       !cross_shape(n_q_heads, n_kv_heads, head_dim, block_size))
     return 0;
   return (size_t)2 * kMaxDecodeGrid * cross_part_rows(max_q_len, n_q_heads / n_kv_heads) * (head_dim + 2) * 4;

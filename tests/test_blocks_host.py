@@ -205,6 +205,15 @@ def test_pools_that_32_bits_cannot_cut():
     assert L.cb_block_ops_workspace_size(2, 4, 1 << 30) >= 12 << 29
 
 
+def test_cross_attention_workspace_of_refused_lengths():
+    """No workspace for more keys than the call takes."""
+    L = _lib()
+    f = L.cb_paged_cross_attention_workspace_size
+    assert f(2, 3, 1, 1 << 30, 8, 4, 128, 16) > 0
+    for keys in ((1 << 30) + 1, 0x7FFFFFFF):
+        assert f(2, 3, 1, keys, 8, 4, 128, 16) == 0
+
+
 # ------------------------------------------------------------------ sizes beyond 32 bits in the binding
 class _Tensor(_Fake):
     def numel(self):
