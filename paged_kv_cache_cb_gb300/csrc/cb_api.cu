@@ -596,6 +596,7 @@ int cb_paged_cross_attention(const void* q, const int32_t* cu_q_lens, const int3
   while (1 << p.group_log2 < group) ++p.group_log2;
   p.part_rows = cross_part_rows(max_q_len, group);
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.per_scale_log2 = 1.f / p.scale_log2;
   const int box_tokens = std::min(kTileM / group, max_q_len);
   p.q_bytes = (unsigned)(box_tokens * group * head_dim * 2);
   CUtensorMap maps[3];

@@ -50,6 +50,10 @@ constexpr int kThreads = 384;
 constexpr int kRows = 256;             // of a wide item
 constexpr float kNoKey = -__builtin_huge_valf();
 constexpr float kMostSum = 1024.f;     // of a tile's weights: none of them is over 2^10
+// A weight's exponent is s sl2 - m with one rounding, and m the rounded s sl2 of the largest score: there the
+// exponent is what that rounding took, at most 8 for m below this.  Farther out it could be any power of two, and
+// every weight or none would pass fp32; see centre.
+constexpr float kFar = 268435456.f;    // 2^28
 
 // Cost of a key tile of a narrow and of a wide item, and of an item's start and end (its
 // query tile's load, its output), which take as long as one and a half tiles of a wide
@@ -505,6 +509,31 @@ __device__ void issuer(const CrossParams& P, Tiles<A, F>& T, C& c, uint32_t tmem
 }
 
 // ---------------------------------------------------------------- softmax (warps 0-7)
+// The scores of a row whose m lies far out become what is left of them beside it: s sl2 is rounded as m was, so
+// that the largest is 0, and divided by sl2 (back: 1 / sl2), by which the weights multiply.  The warp's other rows
+// keep theirs.  Rarely done, and a loop over the scores' own columns: the softmax goes round a short block for it.
+// (Every exponent with two roundings: prompts of up to 2000 tokens 276 to 281 us; this in registers 267; this 265.5;
+// without it 262.5.)
+__device__ __forceinline__ void centre(float (&s)[128], uint32_t s_at, bool far, float sl2, float back, float m) {
+  const float by = far ? sl2 : 1.f, top = far && m != kNoKey ? m : 0.f, per = far ? back : 1.f;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) tmem_st32(s_at + h * 32, *reinterpret_cast<float(*)[32]>(s + h * 32));
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < 128; c += 8) {
+    float x[8];
+    tmem_ld8(s_at + c, x);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = (__fmul_rn(x[k], by) - top) * per;
+    tmem_st8(s_at + c, x);
+  }
+  tmem_wait_st();
+  tmem_ld64(s_at, *reinterpret_cast<float(*)[64]>(s));
+  tmem_ld64(s_at + 64, *reinterpret_cast<float(*)[64]>(s + 64));
+  tmem_wait_ld();
+}
+
 // Scale a row's O by alpha.
 template <int A>
 __device__ __forceinline__ void rescale(uint32_t o, float alpha) {
@@ -601,8 +630,8 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
         }
         // The weights refer to the running max m of an item's first tile, and O and their sum with
         // them: that is exact whatever m is.  A tile's own max is looked for only if its weights' sum
-        // says that one may be large (or NaN, or m has had no key but -inf yet); then m moves up, O is
-        // scaled and the weights are made again.
+        // says that one may be large (or NaN), or if m lies far out (or has had no key but -inf yet): then m
+        // moves up, O is scaled and the weights are made again.
         const uint64_t sl2x2 = f2(sl2, sl2);
         float alpha = 1.f, add;
         bool known = i > 0, bad = i == 0;
@@ -624,8 +653,10 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
               rescale<A>(o_at, alpha);
               tmem_wait_st();            // with the weights that are made again
             }
+            const bool far = valid && fabsf(m) >= kFar;
+            if (__any_sync(FULL, far)) centre(s, s_at, far, sl2, P.per_scale_log2, m);
           }
-          const float ms = m == kNoKey ? 0.f : m;                  // no key so far but -inf: weights 0
+          const float ms = fabsf(m) >= kFar ? 0.f : m;             // no key so far but -inf: weights 0
           const uint64_t nm2 = f2(-ms, -ms);
           uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
@@ -646,7 +677,7 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
           f2split(sum[1], t[2], t[3]);
           add = (t[0] + t[1]) + (t[2] + t[3]);
           if (!known) break;
-          bad = valid && !(add <= kMostSum && m > kNoKey);
+          bad = valid && !(add <= kMostSum && fabsf(m) < kFar);
           if (!__any_sync(FULL, bad)) break;
           known = false;
         }
@@ -755,7 +786,12 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
 #pragma unroll
         for (int k = 0; k < 32; ++k) s[k] = key + k < p.q.kv ? s[k] : kNoKey;
       }
+      // scaled and rounded before m, a maximum of such products, is taken off: the largest has exponent 0 however
+      // far from 0 it lies (see kFar; in here the product costs next to nothing: 100 tokens over 77 keys 18.2 and
+      // 18.8 us, over 257 keys 104.5 and 106.5)
       const uint64_t sl2x2 = f2(sl2, sl2);
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) f2split(fmul2(f2(s[k], s[k + 1]), sl2x2), s[k], s[k + 1]);
       float alpha = 1.f, add;
       uint32_t pk[16];
       bool known = i > 0, bad = i == 0, met = true;
@@ -765,7 +801,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
           float a[2] = {kNoKey, kNoKey};
 #pragma unroll
           for (int k = 0; k < 32; k += 2) a[(k >> 1) & 1] = max3(a[(k >> 1) & 1], s[k], s[k + 1]);
-          T.top[side][warp][row] = make_float2(fmaxf(a[0], a[1]) * sl2, bad ? 1.f : 0.f);
+          T.top[side][warp][row] = make_float2(fmaxf(a[0], a[1]), bad ? 1.f : 0.f);
           if (named_bar_or(bar, 128, !ok)) {
             met = false;
             break;
@@ -796,7 +832,7 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           float x0, x1;
-          f2split(ffma2(f2(s[2 * k], s[2 * k + 1]), sl2x2, nm2), x0, x1);
+          f2split(fadd2(f2(s[2 * k], s[2 * k + 1]), nm2), x0, x1);
           const float p0 = ex2(x0), p1 = ex2(x1);
           sum[k & 1] = fadd2(sum[k & 1], f2(p0, p1));
           pk[k] = pack_bf16(p0, p1);

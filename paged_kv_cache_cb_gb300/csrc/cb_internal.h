@@ -133,6 +133,7 @@ struct CrossParams {
   int part_rows;
   unsigned q_bytes;             // of a query tile's load
   float scale_log2;             // scale * log2(e)
+  float per_scale_log2;         // 1 / scale_log2
 };
 // Upper bound of a step's units of work (2^30 from that many items on); CTAs of a launch with that many; rows of a
 // partial result.
