@@ -46,7 +46,10 @@
  *    cb_last_error(stream)), and the block-tile and cross attention launches' work
  *    counters.  Slots
  *    are handed out in order of first use, at most 4096 per device; a call on a
- *    further stream returns CB_ESTATE.  The first call on a device looks up the
+ *    further stream returns CB_ESTATE.  A recorded call keeps the slot of the
+ *    stream that it was recorded on, whichever stream its graph is launched on:
+ *    graphs recorded on one stream, and calls on that stream, are not to overlap
+ *    where the call keeps counters there.  The first call on a device looks up the
  *    slots' device address (cudaGetSymbolAddress): make it before any stream
  *    capture.  Addresses are cached per device, so cudaDeviceReset is not
  *    supported while the library is in use.
@@ -243,7 +246,8 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  * Shapes: head_dim 64 or 128; n_q_heads / n_kv_heads 1, 2, 4, 8, 16 or 32, with any
  * number of KV heads.  One cooperative kernel launch (CB_ECUDA if the device
  * cannot hold one CTA per SM at once); its counters are the stream's (see
- * "Per-stream state": calls that overlap must come from different streams).  Rows
+ * "Per-stream state": calls that overlap must come from different streams, recorded
+ * ones from streams that they were recorded on).  Rows
  * of out that belong to no request are left as they were.
  * Precision: scores, softmax statistics and sums are fp32; a weight is rounded to
  * bf16 before it multiplies v.
@@ -366,7 +370,9 @@ int cb_kv_append_paged_attention_fp8(const void* k_new, const void* v_new, const
  * 16, fewer than 2^31 table entries; n_rows 0 does nothing (cb_compact_blocks still compacts).
  * workspace: device, cb_block_ops_workspace_size(...) bytes, 16-byte aligned, no
  * initialisation; calls that may overlap need their own.  The arguments do not
- * overlap in memory.
+ * overlap in memory.  A call is one CTA or a cluster of 8, and growth by more than
+ * 8192 tokens a cluster of 16 CTAs of 1024 threads: CB_ECUDA where the device cannot
+ * hold one (a partition of it).
  * Errors: CB_EINVAL, CB_EWORKSPACE, CB_ECUDA; found by the kernels, and
  * reported by cb_last_error: CB_EDEVICE for lengths and block ids out of range
  * (lengths count as the nearest one in range, ids name no block), CB_ESTATE for

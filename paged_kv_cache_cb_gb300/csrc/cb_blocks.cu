@@ -5,12 +5,14 @@
 // refs [num_blocks] (holders of each block; 0: free).  Row r holds the first
 // ceil(lens[r] / 16) entries of its table row.
 //
-// Each operation is one kernel of one thread-block cluster.  They touch a few
-// ints per row and block, so what they cost is the chain of dependent reads --
-// lengths, entries, counts, ranks -- of 0.3 to 0.7 us each.  A cluster's hardware
-// barrier orders the phases without a grid-wide wait; what is a few ints per row
-// every CTA reads and works out for all rows, instead of waiting for another's.  Blocks are
-// always taken from the lowest free id on, in row order: ranks come from prefix
+// Fork, grow and compact are one kernel each, of one CTA (sync_all is then a block's
+// barrier) or of one cluster of 8 or 16.  They touch a few ints per row and block, so
+// what they cost is the chain of dependent reads -- lengths, entries, counts, ranks --
+// of 0.3 to 0.7 us each.  A cluster's hardware barrier orders the phases without a
+// grid-wide wait; what is a few ints per row every CTA reads and works out for all
+// rows, instead of waiting for another's.  Two kernels are ordinary grids without
+// barriers between their CTAs: slots_kernel, which a growth by many tokens puts
+// behind its own, and the copies.  Blocks are always taken from the lowest free id on, in row order: ranks come from prefix
 // sums, never from the order in which atomics arrive, so a call's result is the
 // same every time.  The atomics on refs are integer sums.
 #include <algorithm>
@@ -711,12 +713,19 @@ cudaError_t launch_behind(void (*kernel)(const Args), const Args& a, int ctas, i
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-constexpr int kManyTokens = 8192;      // slots that one cluster writes itself
-// What a single CTA goes over alone.  Times of the call and what goes with it (us), one CTA against
-// eight: 48 rows grown in a pool of 14,000 blocks 8.3 against 10.3 (it stops at the last block that it
-// needs); compaction of 333 blocks with its copies 10.2 against 13.6, of 28,610 324 against 292; fork of
-// 128 rows in 6000 blocks 38.4 against 37.4.  512 rows that take 32,000 of 100,000 blocks: 55.8 with
-// one, 31.3 with eight, 24.0 with sixteen, which the others lose 1 to 2 by.
+// Slots that one cluster writes itself.  GPU time (us) so and with slots_kernel, a pool of 100,000 blocks: 8000
+// tokens 10.5 and 15.0, 16,000 11.1 and 15.0, 64,000 16.7 to 22.8 and 15.9 to 20.8, 512,000 81 and 21: up to some
+// 50,000 tokens the second kernel costs 4, past that it gives all but itself.
+constexpr int kManyTokens = 8192;
+// What a single CTA goes over alone.  GPU time of the call (us) with 1, 8 and 16 CTAs:
+//  growth of 48 rows by up to 8 tokens, in pools of 2000 to 65,536 blocks whose first free ones lie low (one CTA
+//    stops at the last block that it needs): 6.1-8.0, 8.4-11.1, 10.4-11.5; where the first 95 % are taken: 8000
+//    blocks 8.3, 8.8, 10.6; 14,000 11.5, 8.9, 11.2; 32,768 18.6, 9.4, 11.3; 65,536 33.8, 10.9, 10.8.  How full a
+//    pool is the host does not know: kSmallGrowth is a size at which neither loses more than 3.
+//  growth of 512 rows that take 32,000 of 100,000 blocks, with their slots: 55.8, 31.3, 24.0
+//  compaction of 32 rows: 2000 blocks 5.8, 9.5, 11.1; 4000 7.8, 11.1, 13.0; 8192 14.0, 12.7, 15.8; 16,384 23.8,
+//    16.0, 18.8; of 64 rows and 1920 blocks 6.6, 9.5, 13.1; of 256 and 7680 16.0, 10.3, 14.0
+//  fork without copies, in pools of any size: 8 rows 4.3-4.6, 4.7-5.1, 4.7-5.1; 64 7.6, 6.2, 6.2; 128 10.7, 6.2, 6.3
 constexpr int kSmallPool = 8192, kSmallRows = 64, kSmallGrowth = 16384;
 
 constexpr int kMostPairs = 1 << 30;    // their ints are counted in 32 bits

@@ -30,12 +30,12 @@
 // barrier agree there on whether one of them has given up.
 //
 // Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
-// head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 144 us = 0.94 of the copy
-// rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 382 us = 0.99: HBM bounds both.
-// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 262 us = 1.34
+// head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 142 to 144 us = 0.94 of the
+// copy rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 376 to 382 us = 0.99: HBM bounds both.
+// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 265 us = 1.32
 // PFLOP/s: the chain scores - weights - product of each group bounds them.  Head dimension
-// 64, 100 single tokens over 100-3000 keys: 32/32 heads 190 us = 0.92 of the copy rate,
-// 32/8 heads 59.5 us = 0.74, of which the launch's start and the joins at its end are 8.
+// 64, 100 single tokens over 100-3000 keys: 32/32 heads 189 us = 0.92 of the copy rate,
+// 32/8 heads 59 us = 0.74, of which the launch's start and the joins at its end are 8.
 #include <algorithm>
 #include <cstddef>
 
@@ -57,9 +57,9 @@ constexpr float kFar = 268435456.f;    // 2^28
 
 // Cost of a key tile of a narrow and of a wide item, and of an item's start and end (its
 // query tile's load, its output), which take as long as one and a half tiles of a wide
-// item.  Four prompts of 5 to 1999 tokens: 310 us with a start counted as half a tile of
-// a wide item, 298 as one, 262 as one and a half, 270 as two; 64 x 4 beams: 380, 380, 382,
-// 385; 100 tokens over 100 to 3000 keys of dimension 64, 32 heads: 198, 187, 190, 195.
+// item.  Four prompts of 5 to 1999 tokens: 307 us with a start counted as half a tile of
+// a wide item, 295 as one, 265 as one and a half, 270 as two; 64 x 4 beams: 374, 375, 376,
+// 379; 100 tokens over 100 to 3000 keys of dimension 64, 32 heads: 198, 186, 189, 194.
 constexpr int kNarrow = 2, kWide = 4, kLead = 6;
 constexpr int kLeast = 8;              // of a CTA's share
 
@@ -745,14 +745,15 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
   }
 }
 
-// Items of at most 32 rows: thread = row leaves three of a group's warps idle, while one takes 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times,
-// one copy for each warp's lanes, and so have the scores: warp w makes the weights of keys
+// Items of at most 32 rows: thread = row leaves three of a group's warps idle, while one takes
+// 1750 cycles for a row's 128 weights.  Here the query tile has its rows four times, one copy
+// for each warp's lanes, and so have the scores: warp w makes the weights of keys
 // 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
 // lanes.  m is the same in the four warps, which tell each other their maxima when it may move;
 // sums stay apart until the item's end.  Every exit is taken by the four warps together:
-// they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 190 us
-// (thread = row: 257), over 128 keys 35.5 (43.4); dimension 128 over 257 keys 104 (162); 8
-// tokens each over 257 keys, 32/8 heads of 128, 39.8 (55.8).
+// they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 189 us
+// (thread = row: 257), over 128 keys 35.6 (43.4); dimension 128 over 257 keys 107 (162); 8
+// tokens each over 257 keys, 32/8 heads of 128, 40.5 (55.8).
 template <int A, class C>
 __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A, true>;
