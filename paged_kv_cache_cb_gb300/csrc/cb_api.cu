@@ -8,6 +8,7 @@
 #include <mutex>
 #include <new>
 #include <set>
+#include <vector>
 
 #include "../../include/cbattn.h"
 #include "cb_internal.h"
@@ -656,7 +657,36 @@ int cb_last_launch_count(void) { return g_last_launches; }
 struct cb_graph {
   cudaGraphExec_t exec = nullptr;
   int device = -1;
+  bool clusters_known = false;
+  std::vector<unsigned> clusters;      // of exec, as cluster_sizes has them
+  std::vector<unsigned> recorded;      // of the recording at hand
+  std::vector<cudaGraphNode_t> nodes;
 };
+
+// The cluster of every node of g's recording, in its order (0: none).  An update in place takes over a node's
+// kernel, grid and arguments, but leaves it the cluster that it was instantiated with: a kernel of clusters
+// would run without the barrier between its CTAs, one without clusters not at all where the old size does not
+// divide its grid.  (Cooperative launches and programmatic edges make the update fail, as they should.)
+// false: not known.
+static bool cluster_sizes(cb_graph* g, cudaGraph_t graph) try {
+  size_t n = 0;
+  if (cudaGraphGetNodes(graph, nullptr, &n) != cudaSuccess) return false;
+  g->nodes.resize(n);
+  g->recorded.assign(n, 0u);
+  if (n && cudaGraphGetNodes(graph, g->nodes.data(), &n) != cudaSuccess) return false;
+  for (size_t i = 0; i < n; ++i) {
+    cudaGraphNodeType type;
+    if (cudaGraphNodeGetType(g->nodes[i], &type) != cudaSuccess) return false;
+    if (type != cudaGraphNodeTypeKernel) continue;
+    cudaLaunchAttributeValue v = {};
+    if (cudaGraphKernelNodeGetAttribute(g->nodes[i], cudaLaunchAttributeClusterDimension, &v) != cudaSuccess) return false;
+    const unsigned x = v.clusterDim.x, y = v.clusterDim.y, z = v.clusterDim.z;
+    g->recorded[i] = x * y * z > 1 ? x << 20 | y << 10 | z : 0u;      // at most 16 CTAs
+  }
+  return true;
+} catch (...) {
+  return false;
+}
 
 cb_graph* cb_graph_create(void) { return new (std::nothrow) cb_graph(); }
 
@@ -689,17 +719,17 @@ int cb_graph_end(cb_graph* g, void* stream) {
     (void)cudaGraphDestroy(graph);
     return CB_ECUDA;
   }
-  if (g->exec && g->device == dev) {
+  const bool known = cluster_sizes(g, graph);
+  if (!known) (void)cudaGetLastError();
+  if (g->exec) {
     // the same kernels in the same order: new parameters in place, no instantiation
     cudaGraphExecUpdateResultInfo info;
-    if (cudaGraphExecUpdate(g->exec, graph, &info) != cudaSuccess) {
+    const bool same = g->device == dev && known && g->clusters_known && g->recorded == g->clusters;
+    if (!same || cudaGraphExecUpdate(g->exec, graph, &info) != cudaSuccess) {
       (void)cudaGetLastError();
       (void)cudaGraphExecDestroy(g->exec);
       g->exec = nullptr;
     }
-  } else if (g->exec) {
-    (void)cudaGraphExecDestroy(g->exec);
-    g->exec = nullptr;
   }
   if (!g->exec) {
     if (cudaGraphInstantiate(&g->exec, graph, 0) != cudaSuccess) {
@@ -709,6 +739,8 @@ int cb_graph_end(cb_graph* g, void* stream) {
       return CB_ECUDA;
     }
     g->device = dev;
+    g->clusters_known = known;
+    g->clusters.swap(g->recorded);
   }
   (void)cudaGraphDestroy(graph);
   if (cudaGraphLaunch(g->exec, s) != cudaSuccess) {
