@@ -242,7 +242,7 @@ int cb_kv_append_paged_attention_window(const void* k_new, const void* v_new, co
  *             (max_q_len * n_q_heads / n_kv_heads) take a form of the kernel made
  *             for them
  *  workspace  device, cb_paged_cross_attention_workspace_size(...) bytes, 16-byte
- *             aligned, no initialisation
+ *             aligned, no initialisation; calls that may overlap need their own
  * Shapes: head_dim 64 or 128; n_q_heads / n_kv_heads 1, 2, 4, 8, 16 or 32, with any
  * number of KV heads.  One cooperative kernel launch (CB_ECUDA if the device
  * cannot hold one CTA per SM at once); its counters are the stream's (see
@@ -513,8 +513,9 @@ int cb_last_launch_count(void);
  *                              work on `stream`.  The graph object keeps one
  *                              instantiated graph: it is updated in place when
  *                              the new recording has the same shape of work
- *                              (the same kernels in the same order, parameters
- *                              free to change), otherwise instantiated anew.
+ *                              (the same kernels and clusters in the same order,
+ *                              parameters free to change), otherwise
+ *                              instantiated anew.
  * Arguments are captured by value; the buffers they point to are read when the
  * graph runs.  A shape's first call on a device must run outside a capture
  * (it sets up the library's per-device state); cb_last_error synchronises and
