@@ -146,3 +146,24 @@ def test_a_step_of_several_calls(recorder):
                 before[:, dst] = before[:, src]
         assert torch.equal(cache[0], before)
         t.grown()
+
+
+def test_recorded_while_the_last_one_runs(recorder):
+    """Small and large pools in turn, all launched before one synchronisation."""
+    small, large = Steps(8, 200, 60, 1), Steps(100, 20000, 60, 3)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for t in (small, large):
+            recorder.g.begin(recorder.s)
+            with torch.cuda.stream(recorder.s):
+                t.fork()
+                t.compact()
+            recorder.g.end(recorder.s)
+    assert L().cb_last_error(recorder.s) == 0
+    for t in (small, large):
+        for _ in range(5):
+            pairs, cut = ob.fork(t.parents, None, t.p.tables, t.p.lens, t.p.refs)
+            assert not cut
+            block_map, _, _ = ob.compact(t.p.tables, t.p.lens, t.p.refs)
+        assert np.array_equal(t.pairs.cpu().numpy(), pairs) and np.array_equal(t.map.cpu().numpy(), block_map)
+        t.p.same()
