@@ -12,9 +12,10 @@
 // grid-wide wait; what is a few ints per row every CTA reads and works out for all
 // rows, instead of waiting for another's.  Two kernels are ordinary grids without
 // barriers between their CTAs: slots_kernel, which a growth by many tokens puts
-// behind its own, and the copies.  Blocks are always taken from the lowest free id on, in row order: ranks come from prefix
-// sums, never from the order in which atomics arrive, so a call's result is the
-// same every time.  The atomics on refs are integer sums.
+// behind its own, and the copies.  Blocks are always taken from the lowest free id on,
+// in row order: ranks come from prefix sums, never from the order in which atomics
+// arrive, so a call's result is the same every time.  The atomics on refs are integer
+// sums.
 #include <algorithm>
 
 #include "../../include/cbattn.h"

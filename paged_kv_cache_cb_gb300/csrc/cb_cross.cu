@@ -32,10 +32,10 @@
 // Measured (a recorded graph, 6788 GB/s copy rate, 1899 TFLOP/s of a library's product),
 // head dimension 128: 48 tokens over 256-8192 keys, 32/8 heads, 142 to 144 us = 0.94 of the
 // copy rate; 64 x 4 beams over 512-4096 keys, 32/32 heads, 376 to 382 us = 0.99: HBM bounds both.
-// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 265 us = 1.32
+// Prompts of 1999, 1203, 515 tokens over 9001, 2500, 777 keys, 32/8 heads, 266 us = 1.32
 // PFLOP/s: the chain scores - weights - product of each group bounds them.  Head dimension
-// 64, 100 single tokens over 100-3000 keys: 32/32 heads 189 us = 0.92 of the copy rate,
-// 32/8 heads 59 us = 0.74, of which the launch's start and the joins at its end are 8.
+// 64, 100 single tokens over 100-3000 keys: 32/32 heads 189 to 192 us = 0.91 to 0.92,
+// 32/8 heads 59.5 us = 0.73, of which the launch's start and the joins at its end are 8.
 #include <algorithm>
 #include <cstddef>
 
@@ -751,9 +751,9 @@ __device__ void softmax(const CrossParams& P, Tiles<A, false>& T, C& c, uint32_t
 // 32 w .. 32 w + 31.  They go to shared memory, one row for all four; O is in warp 0's
 // lanes.  m is the same in the four warps, which tell each other their maxima when it may move;
 // sums stay apart until the item's end.  Every exit is taken by the four warps together:
-// they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 189 us
-// (thread = row: 257), over 128 keys 35.6 (43.4); dimension 128 over 257 keys 107 (162); 8
-// tokens each over 257 keys, 32/8 heads of 128, 40.5 (55.8).
+// they meet at named barriers.  100 tokens, 32 heads: dimension 64 over 100 to 3000 keys 192 us
+// (thread = row: 257), over 128 keys 35.6 (43.4); dimension 128 over 257 keys 108 (162); 8
+// tokens each over 257 keys, 32/8 heads of 128, 41 (55.8).
 template <int A, class C>
 __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint32_t tmem, int side) {
   using TT = Tiles<A, true>;
@@ -789,10 +789,9 @@ __device__ void softmax_few(const CrossParams& P, Tiles<A, true>& T, C& c, uint3
       }
       // scaled and rounded before m, a maximum of such products, is taken off: the largest has exponent 0 however
       // far from 0 it lies (see kFar; in here the product costs next to nothing: 100 tokens over 77 keys 18.2 and
-      // 18.8 us, over 257 keys 104.5 and 106.5)
-      const uint64_t sl2x2 = f2(sl2, sl2);
+      // 18.9 us, over 257 keys 104.8 and 108)
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) f2split(fmul2(f2(s[k], s[k + 1]), sl2x2), s[k], s[k + 1]);
+      for (int k = 0; k < 32; ++k) s[k] = __fmul_rn(s[k], sl2);      // never fused with the sum, as packed products can be
       float alpha = 1.f, add;
       uint32_t pk[16];
       bool known = i > 0, bad = i == 0, met = true;
